@@ -357,6 +357,101 @@ NVFP4_API int32_t nvfp4_mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scal
                          void* stream);
 
 /*
+ * Paged key/value cache in NVFP4, for the full-attention layers of the hybrid model
+ * ("Why Gated DeltaNet Survives 4-Bit Quantization" review page: a hybrid GDN/attention
+ * model served with a quantized cache; the format is the layer's own).
+ *
+ * The cache is n_pages pages of nvfp4_kv_page_bytes(...) bytes; a page holds page_size
+ * token slots of every kv head, keys and values: 9/16 byte per element (codes and E4M3
+ * block scales; 16-element blocks along the head).  Slot s is place s % page_size of page
+ * s / page_size.  Its inner order is the library's (heads, then granules of 16 tokens in
+ * the order the matrix instructions read them); nvfp4_kv_gather gives rows back as
+ * values.  One fp32 global scale per kv head for keys and one for values (device arrays
+ * k_gscale, v_gscale [n_kv_heads], calibrated: > 0, amax / 2688 covers a head's values),
+ * the same ones in every call over a cache.  New memory needs no clearing: bytes of
+ * slots that were never written are never part of a result.
+ *   head_dim 64, 128 or 256; page_size a power of two in [16, 4096]
+ *   (NVFP4_ERR_UNSUPPORTED otherwise).
+ */
+
+/* Bytes of one page (host only). */
+NVFP4_API int32_t nvfp4_kv_page_bytes(int32_t n_kv_heads, int32_t page_size, int32_t head_dim, int64_t* bytes_out);
+
+/*
+ * New tokens: rotate q and k by position, quantize k and v, write them to their slots.
+ * A head row x at position p is rotated with c = cos[p], s = sin[p] over its first
+ * R = rot_dim elements (the rest is unchanged):
+ *   interleaved == 0: y_i = x_i c_i - x_{i+R/2} s_i, y_{i+R/2} = x_{i+R/2} c_i + x_i s_i
+ *   interleaved != 0: the same on the pairs (x_{2i}, x_{2i+1})
+ * in fp32, both products and their sum rounded separately.  Keys are quantized from the
+ * fp32 result, by the numerics above.
+ *   q, k, v   device, [T][ldq], [T][ldk], [T][ldv] of dtype (F32 or BF16), e.g. column slices
+ *             of one projection's output: head h at columns h*head_dim ..
+ *   n_q_heads 0: no q (q and q_out NULL)
+ *   cos, sin  device fp32 [n_pos][rot_dim/2]; rot_dim a multiple of 32 (0: no rotation,
+ *             cos and sin unused)
+ *   positions device int32 [T]; positions outside [0, n_pos) are clamped into it
+ *   slots     device int64 [T]; a token whose slot is outside the cache (-1: padding) is not
+ *             appended (its q is rotated all the same).  No two tokens of a call may have
+ *             the same slot.
+ *   cache     device, n_pages pages, 16-byte aligned
+ *   q_out     device [T][ldqo] of dtype: the rotated q; may be q itself (same ld)
+ */
+NVFP4_API int32_t nvfp4_rope_append_kv(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                             int32_t dtype, int64_t T, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                             const float* cos, const float* sin, int64_t n_pos, int32_t rot_dim, int32_t interleaved,
+                             const int32_t* positions, const int64_t* slots, uint8_t* cache, int64_t n_pages,
+                             int32_t page_size, const float* k_gscale, const float* v_gscale, void* q_out,
+                             int64_t ldqo, void* stream);
+
+/*
+ * Rows of the cache as values e2m1 * s * g (the product rounded once to fp32, then once
+ * to out_dtype): k_out, v_out device [T][ld] of out_dtype, head h at columns h*head_dim ...
+ * A slot outside the cache gives a row of zeros.
+ */
+NVFP4_API int32_t nvfp4_kv_gather(const uint8_t* cache, int64_t n_pages, int32_t page_size, int32_t n_kv_heads,
+                        int32_t head_dim, const float* k_gscale, const float* v_gscale, const int64_t* slots,
+                        int64_t T, void* k_out, int64_t ldk, void* v_out, int64_t ldv, int32_t out_dtype,
+                        void* stream);
+
+/*
+ * Attention over the cache.  Sequence b has n = kv_len[b] tokens in the pages
+ * page_table[b][0 ..] and m query tokens, the last m of the n (their keys and values
+ * appended already): rows cu_q[b] .. cu_q[b+1] of q.  Query token i, at position
+ * p = n - m + i, attends to the tokens max(0, p - window + 1) <= t <= p:
+ *   o = sum_t softmax_t(scale * <q, k_t>) v_t
+ * per query head h over kv head h / (n_q_heads / n_kv_heads).  Softmax statistics and sums
+ * are fp32; bf16 queries enter exactly and the weights are rounded to f16 for the second
+ * product, fp32 queries and their weights go as two f16 terms each.  A row that attends to
+ * nothing (kv_len 0, or p < 0) gives o = 0 and lse = -inf.
+ *   q, o      device [T][ldq], [T][ldo] of dtype (F32 or BF16); o must not overlap q
+ *   cu_q      device int32 [batch + 1], non-decreasing, from 0 to T, or NULL: one query
+ *             token per sequence (T == batch)
+ *   kv_len    device int32 [batch]
+ *   page_table device int32 [batch][ld_table], max_pages entries a row; entries past a
+ *             sequence's last page are not used
+ *   max_q_len, max_kv_len  host: bounds on the sequences' lengths, from which the launch is
+ *             chosen; a longer sequence is still computed in full, more slowly
+ *   scale     the scores' factor (1/sqrt(head_dim) as a rule)
+ *   window    0: none
+ *   lse       device fp32 [T][n_q_heads] or NULL: log of the softmax's denominator
+ *   workspace device, at least nvfp4_kv_attention_workspace(...) bytes, 16-byte aligned (NULL
+ *             where that is 0).  Calls that overlap on the GPU need one each.
+ * Lengths and table entries outside their range are clamped into it (results are then
+ * meaningless, accesses stay inside the buffers).
+ */
+NVFP4_API int32_t nvfp4_kv_attention(const void* q, int32_t dtype, int64_t ldq, int64_t T, int32_t n_q_heads,
+                           int32_t n_kv_heads, int32_t head_dim, int32_t batch, const int32_t* cu_q,
+                           int64_t max_q_len, const int32_t* kv_len, int64_t max_kv_len, const int32_t* page_table,
+                           int64_t max_pages, int64_t ld_table, const uint8_t* cache, int64_t n_pages, int32_t page_size,
+                           const float* k_gscale, const float* v_gscale, float scale, int32_t window, void* o,
+                           int64_t ldo, float* lse, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes of such a call (host only; 0 where it needs none). */
+NVFP4_API int32_t nvfp4_kv_attention_workspace(int32_t dtype, int64_t T, int32_t batch, int32_t n_q_heads, int32_t n_kv_heads,
+                                     int32_t head_dim, int64_t max_q_len, int64_t max_kv_len, int64_t* bytes_out);
+
+/*
  * Measurement helper, not part of the layer: a kernel that only issues f16 MFMA
  * 32x32x16 instructions (n_blocks workgroups of 4 waves, each wave 4 x iters of
  * them, 32768 FLOP each), so that a benchmark can report the matrix rate the chip

@@ -30,7 +30,9 @@ NVFP4_MAX_SEGMENTS = 64
 EXPORTED = ["nvfp4_abi_version", "nvfp4_last_error", "nvfp4_quantize_act", "nvfp4_pack_weight",
             "nvfp4_w4a4_gemm", "nvfp4_w4a4_linear", "nvfp4_w4a4_linear_noalloc", "nvfp4_requantize_weight", "nvfp4_segment_mismatch_factor",
             "nvfp4_require_single_scale", "nvfp4_rotate_quantize", "nvfp4_w4a4_gemm_rowcol",
-            "nvfp4_gdn_gated_delta", "nvfp4_mxfp4_quantize", "nvfp4_mxfp4_gemm", "nvfp4_bench_mfma_peak"]
+            "nvfp4_gdn_gated_delta", "nvfp4_mxfp4_quantize", "nvfp4_mxfp4_gemm", "nvfp4_bench_mfma_peak",
+            "nvfp4_kv_page_bytes", "nvfp4_rope_append_kv", "nvfp4_kv_gather", "nvfp4_kv_attention",
+            "nvfp4_kv_attention_workspace"]
 
 
 class Nvfp4Error(RuntimeError):
@@ -81,6 +83,18 @@ def _load() -> ctypes.CDLL:
     lib.nvfp4_mxfp4_quantize.argtypes = [P, I32, I64, I64, I64, P, P, P]
     lib.nvfp4_mxfp4_gemm.restype = I32
     lib.nvfp4_mxfp4_gemm.argtypes = [P, P, I64, I64, I64, P, P, P, I32, I64, P]
+    lib.nvfp4_kv_page_bytes.restype = I32
+    lib.nvfp4_kv_page_bytes.argtypes = [I32, I32, I32, P]
+    lib.nvfp4_rope_append_kv.restype = I32
+    lib.nvfp4_rope_append_kv.argtypes = [P, I64, P, I64, P, I64, I32, I64, I32, I32, I32, P, P, I64, I32, I32, P, P, P,
+                                         I64, I32, P, P, P, I64, P]
+    lib.nvfp4_kv_gather.restype = I32
+    lib.nvfp4_kv_gather.argtypes = [P, I64, I32, I32, I32, P, P, P, I64, P, I64, P, I64, I32, P]
+    lib.nvfp4_kv_attention.restype = I32
+    lib.nvfp4_kv_attention.argtypes = [P, I32, I64, I64, I32, I32, I32, I32, P, I64, P, I64, P, I64, I64, P, I64, I32, P, P,
+                                       ctypes.c_float, I32, P, I64, P, P, I64, P]
+    lib.nvfp4_kv_attention_workspace.restype = I32
+    lib.nvfp4_kv_attention_workspace.argtypes = [I32, I64, I32, I32, I32, I32, I64, I64, P]
     return lib
 
 
@@ -319,6 +333,164 @@ def nvfp4_mxfp4_gemm(a_codes, a_scales, w_codes, w_scales, y, stream=None) -> No
     _, _, ldy = _rows(y, "y")
     _check(lib.nvfp4_mxfp4_gemm(a_codes.data_ptr(), a_scales.data_ptr(), M, N, 2 * half_k, w_codes.data_ptr(),
                                 w_scales.data_ptr(), y.data_ptr(), _dtype_code(y), ldy, _stream(stream)))
+
+
+# ----------------------------------------------------------------------------- key/value cache
+
+def nvfp4_kv_page_bytes(n_kv_heads: int, page_size: int, head_dim: int) -> int:
+    """Bytes of one page of the NVFP4 key/value cache."""
+    n = ctypes.c_int64(0)
+    _check(lib.nvfp4_kv_page_bytes(n_kv_heads, page_size, head_dim, ctypes.byref(n)))
+    return n.value
+
+
+def empty_kv_cache(n_pages: int, n_kv_heads: int, page_size: int, head_dim: int, device="cuda"):
+    """Device buffer uint8 [n_pages, page bytes] for a key/value cache."""
+    torch = _torch()
+    return torch.empty((n_pages, nvfp4_kv_page_bytes(n_kv_heads, page_size, head_dim)), dtype=torch.uint8,
+                       device=device)
+
+
+def _kv_cache(cache, k_gscale, v_gscale, page_size, head_dim=None):
+    """(n_kv_heads, head_dim, n_pages) of a cache buffer; the head dimension follows from
+    the page's bytes (9/8 byte per token, head and element)."""
+    torch = _torch()
+    if cache.dtype != torch.uint8 or cache.dim() != 2 or not cache.is_contiguous():
+        raise Nvfp4Error(NVFP4_ERR_INVALID_ARG, "cache must be contiguous uint8 [n_pages, page bytes]")
+    for t, name in ((k_gscale, "k_gscale"), (v_gscale, "v_gscale")):
+        if t.dtype != torch.float32 or t.dim() != 1 or not t.is_contiguous():
+            raise Nvfp4Error(NVFP4_ERR_INVALID_ARG, f"{name} must be contiguous float32 [n_kv_heads]")
+    n_pages, page_bytes = cache.shape
+    n_kv_heads = k_gscale.shape[0]
+    if head_dim is None:
+        head_dim = page_bytes * 8 // (9 * max(n_kv_heads * page_size, 1))
+    if v_gscale.shape[0] != n_kv_heads or n_kv_heads * page_size * head_dim * 9 != page_bytes * 8:
+        raise Nvfp4Error(NVFP4_ERR_INVALID_ARG,
+                         f"cache pages of {page_bytes} bytes do not hold {page_size} tokens of {n_kv_heads} heads")
+    return n_kv_heads, head_dim, n_pages
+
+
+def _on_gpu(**named):
+    for name, t in named.items():
+        if t is not None and not t.is_cuda:
+            raise Nvfp4Error(NVFP4_ERR_INVALID_ARG, f"{name} must be in device memory")
+
+
+def _indices(t, name, dtype, n):
+    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or t.stride(0) != 1 and n > 1:
+        raise Nvfp4Error(NVFP4_ERR_INVALID_ARG, f"{name} must be contiguous {dtype} [{n}]")
+    return t.data_ptr()
+
+
+def _same_dtype(dtype, *named):
+    for t, name in named:
+        if t.dtype != dtype:
+            raise Nvfp4Error(NVFP4_ERR_UNSUPPORTED, f"{name} must be {dtype} like the others")
+
+
+def nvfp4_rope_append_kv(q, k, v, cos, sin, positions, slots, cache, k_gscale, v_gscale, page_size, q_out,
+                         interleaved=False, stream=None) -> None:
+    """Rotate q [T, n_q_heads * d] and k [T, n_kv_heads * d] by position (cos, sin fp32
+    [n_pos, rot_dim / 2], or both None: no rotation; positions int32 [T]), write the
+    rotated q to q_out (may be q; both None: no queries), and append k and v to the cache
+    at slots (int64 [T]; outside the cache, e.g. -1: not appended)."""
+    torch = _torch()
+    _on_gpu(q=q, k=k, v=v, cos=cos, sin=sin, positions=positions, slots=slots, cache=cache, k_gscale=k_gscale,
+            v_gscale=v_gscale, q_out=q_out)
+    T, kv_cols, ldk = _rows(k, "k")
+    n_kv_heads, d, n_pages = _kv_cache(cache, k_gscale, v_gscale, page_size, kv_cols // max(k_gscale.shape[0], 1))
+    Tv, v_cols, ldv = _rows(v, "v")
+    if (Tv, v_cols) != (T, kv_cols) or n_kv_heads * d != kv_cols:
+        raise Nvfp4Error(NVFP4_ERR_INVALID_ARG, f"k and v must both be [T, {n_kv_heads} heads * head_dim]")
+    _same_dtype(k.dtype, (v, "v"))
+    n_q_heads = ldq = ldqo = 0
+    if (q is None) != (q_out is None):
+        raise Nvfp4Error(NVFP4_ERR_INVALID_ARG, "q and q_out must both be given or both be None")
+    if q is not None:
+        Tq, q_cols, ldq = _rows(q, "q")
+        To, o_cols, ldqo = _rows(q_out, "q_out")
+        if Tq != T or To != T or o_cols != q_cols or q_cols % d:
+            raise Nvfp4Error(NVFP4_ERR_INVALID_ARG, f"q and q_out must be [{T}, n_q_heads * {d}]")
+        _same_dtype(k.dtype, (q, "q"), (q_out, "q_out"))
+        n_q_heads = q_cols // d
+    rot_dim = n_pos = 0
+    if (cos is None) != (sin is None):
+        raise Nvfp4Error(NVFP4_ERR_INVALID_ARG, "cos and sin must both be given or both be None")
+    if cos is not None:
+        if cos.dtype != torch.float32 or sin.dtype != torch.float32 or cos.dim() != 2 or cos.shape != sin.shape \
+                or not cos.is_contiguous() or not sin.is_contiguous():
+            raise Nvfp4Error(NVFP4_ERR_INVALID_ARG, "cos and sin must be contiguous float32 [n_pos, rot_dim / 2]")
+        n_pos, rot_dim = cos.shape[0], 2 * cos.shape[1]
+    _check(lib.nvfp4_rope_append_kv(_ptr(q), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, _dtype_code(k), T, n_q_heads,
+                                    n_kv_heads, d, _ptr(cos), _ptr(sin), n_pos, rot_dim, 1 if interleaved else 0,
+                                    _indices(positions, "positions", torch.int32, T),
+                                    _indices(slots, "slots", torch.int64, T), cache.data_ptr(), n_pages, page_size,
+                                    k_gscale.data_ptr(), v_gscale.data_ptr(), _ptr(q_out), ldqo, _stream(stream)))
+
+
+def nvfp4_kv_gather(cache, slots, k_gscale, v_gscale, page_size, k_out, v_out, stream=None) -> None:
+    """The values of cache rows (slots int64 [T]; outside the cache: zeros) into k_out
+    and v_out [T, n_kv_heads * d]."""
+    torch = _torch()
+    _on_gpu(cache=cache, slots=slots, k_gscale=k_gscale, v_gscale=v_gscale, k_out=k_out, v_out=v_out)
+    n_kv_heads, d, n_pages = _kv_cache(cache, k_gscale, v_gscale, page_size)
+    T, k_cols, ldk = _rows(k_out, "k_out")
+    Tv, v_cols, ldv = _rows(v_out, "v_out")
+    if Tv != T or k_cols != n_kv_heads * d or v_cols != k_cols:
+        raise Nvfp4Error(NVFP4_ERR_INVALID_ARG, f"k_out and v_out must both be [T, {n_kv_heads * d}]")
+    _same_dtype(k_out.dtype, (v_out, "v_out"))
+    _check(lib.nvfp4_kv_gather(cache.data_ptr(), n_pages, page_size, n_kv_heads, d, k_gscale.data_ptr(),
+                               v_gscale.data_ptr(), _indices(slots, "slots", torch.int64, T), T, k_out.data_ptr(), ldk,
+                               v_out.data_ptr(), ldv, _dtype_code(k_out), _stream(stream)))
+
+
+def nvfp4_kv_attention_workspace(n_tokens: int, batch: int, n_q_heads: int, n_kv_heads: int, head_dim: int,
+                                 max_q_len: int, max_kv_len: int, dtype=None) -> int:
+    """Workspace bytes of an nvfp4_kv_attention call of these sizes and q dtype (None:
+    enough for either)."""
+    torch = _torch()
+    codes = {None: (NVFP4_DTYPE_F32, NVFP4_DTYPE_BF16), torch.float32: (NVFP4_DTYPE_F32,),
+             torch.bfloat16: (NVFP4_DTYPE_BF16,)}
+    if dtype not in codes:
+        raise Nvfp4Error(NVFP4_ERR_UNSUPPORTED, f"dtype {dtype} is not float32 or bfloat16")
+    need = 0
+    for code in codes[dtype]:
+        n = ctypes.c_int64(0)
+        _check(lib.nvfp4_kv_attention_workspace(code, n_tokens, batch, n_q_heads, n_kv_heads, head_dim, max_q_len,
+                                                max_kv_len, ctypes.byref(n)))
+        need = max(need, n.value)
+    return need
+
+
+def nvfp4_kv_attention(q, cache, page_table, kv_len, k_gscale, v_gscale, page_size, o, max_kv_len, workspace=None,
+                       cu_q=None, max_q_len=1, scale=None, window=0, lse=None, stream=None) -> None:
+    """Causal attention of q [T, n_q_heads * d] over the cache into o: sequence b has
+    kv_len[b] tokens in pages page_table[b] and the query rows cu_q[b] .. cu_q[b + 1] (None:
+    row b alone), the last of its tokens.  max_q_len and max_kv_len bound the lengths;
+    workspace: uint8 buffer of nvfp4_kv_attention_workspace bytes; lse fp32 [T, n_q_heads]."""
+    torch = _torch()
+    _on_gpu(q=q, cache=cache, page_table=page_table, kv_len=kv_len, k_gscale=k_gscale, v_gscale=v_gscale, o=o,
+            workspace=workspace, cu_q=cu_q, lse=lse)
+    n_kv_heads, d, n_pages = _kv_cache(cache, k_gscale, v_gscale, page_size)
+    T, q_cols, ldq = _rows(q, "q")
+    To, o_cols, ldo = _rows(o, "o")
+    if To != T or o_cols != q_cols or q_cols % max(d, 1):
+        raise Nvfp4Error(NVFP4_ERR_INVALID_ARG, f"q and o must both be [T, n_q_heads * {d}]")
+    _same_dtype(q.dtype, (o, "o"))
+    n_q_heads = q_cols // max(d, 1)
+    if page_table.dtype != torch.int32:
+        raise Nvfp4Error(NVFP4_ERR_UNSUPPORTED, "page_table must be int32")
+    batch, max_pages, ld_table = _rows(page_table, "page_table")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, n_q_heads) or not lse.is_contiguous()):
+        raise Nvfp4Error(NVFP4_ERR_INVALID_ARG, f"lse must be contiguous float32 [{T}, {n_q_heads}]")
+    _check(lib.nvfp4_kv_attention(q.data_ptr(), _dtype_code(q), ldq, T, n_q_heads, n_kv_heads, d, batch,
+                                  None if cu_q is None else _indices(cu_q, "cu_q", torch.int32, batch + 1), max_q_len,
+                                  _indices(kv_len, "kv_len", torch.int32, batch), max_kv_len, page_table.data_ptr(),
+                                  max_pages, ld_table, cache.data_ptr(), n_pages, page_size, k_gscale.data_ptr(),
+                                  v_gscale.data_ptr(), d ** -0.5 if scale is None else scale, window, o.data_ptr(),
+                                  ldo, _ptr(lse), _ptr(workspace),
+                                  0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                  _stream(stream)))
 
 
 def nvfp4_bench_mfma_peak(iters: int, n_blocks: int, out, stream=None) -> None:

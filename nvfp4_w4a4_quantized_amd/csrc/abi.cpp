@@ -241,6 +241,53 @@ int32_t linear_impl(const void* x, int32_t x_dtype, int64_t M, int64_t K, int64_
 int64_t noalloc_scales_offset(int64_t M, int64_t K) { return ((M * (K / 2)) + 255) / 256 * 256; }
 int64_t noalloc_bytes(int64_t M, int64_t K) { return noalloc_scales_offset(M, K) + M * (K / 16); }
 
+// The paged key/value cache: its shape, the rows of a call, its buffers.
+int32_t check_kv_shape(int32_t n_kv_heads, int32_t page_size, int32_t head_dim, int64_t n_pages, nvfp4::KvGeom* g) {
+  if (n_kv_heads <= 0 || n_kv_heads > 65536)
+    return fail(NVFP4_ERR_INVALID_ARG, "n_kv_heads=%d outside [1, 65536]", n_kv_heads);
+  if (!nvfp4::kv_shape_ok(head_dim, page_size))
+    return fail(NVFP4_ERR_UNSUPPORTED,
+                "head_dim=%d, page_size=%d: head_dim must be 64, 128 or 256, page_size a power of two in [16, 4096]",
+                head_dim, page_size);
+  if (n_pages <= 0 || n_pages > 0x7FFFFFFFll)
+    return fail(NVFP4_ERR_INVALID_ARG, "n_pages=%lld outside [1, 2^31 - 1]", (long long)n_pages);
+  g->n_kv_heads = n_kv_heads;
+  g->page_shift = __builtin_ctz((unsigned)page_size);
+  g->page_bytes = nvfp4::kv_page_bytes(n_kv_heads, page_size, head_dim);
+  g->n_pages = n_pages;
+  return NVFP4_OK;
+}
+
+int32_t check_kv_rows(int64_t T, int64_t heads) {
+  if (T * heads > 0x7FFFFFFFll)
+    return fail(NVFP4_ERR_UNSUPPORTED, "%lld tokens of %lld heads: at most 2^31 - 1 rows", (long long)T,
+                (long long)heads);
+  return NVFP4_OK;
+}
+
+int32_t check_kv_cache(const uint8_t* cache, const float* k_gscale, const float* v_gscale) {
+  if (!cache) return fail(NVFP4_ERR_INVALID_ARG, "cache is NULL");
+  if (!aligned16(cache)) return fail(NVFP4_ERR_UNSUPPORTED, "cache must be 16-byte aligned");
+  if (!k_gscale || !v_gscale) return fail(NVFP4_ERR_INVALID_ARG, "k_gscale/v_gscale is NULL");
+  return NVFP4_OK;
+}
+
+int32_t check_kv_attn_sizes(int64_t T, int32_t batch, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                            int64_t max_q_len, int64_t max_kv_len) {
+  if (T <= 0 || T > (1ll << 30) || batch <= 0 || n_q_heads <= 0 || n_kv_heads <= 0)
+    return fail(NVFP4_ERR_INVALID_ARG, "T (up to 2^30), batch and head counts must be positive (T=%lld batch=%d heads %d/%d)",
+                (long long)T, batch, n_q_heads, n_kv_heads);
+  if (n_q_heads % n_kv_heads)
+    return fail(NVFP4_ERR_INVALID_ARG, "n_q_heads=%d is not a multiple of n_kv_heads=%d", n_q_heads, n_kv_heads);
+  if (!nvfp4::kv_shape_ok(head_dim, 16)) return fail(NVFP4_ERR_UNSUPPORTED, "head_dim=%d is not 64, 128 or 256", head_dim);
+  if (max_q_len <= 0 || max_q_len > 0x7FFFFFFFll || max_kv_len < 0 || max_kv_len > 0x7FFFFFFFll)
+    return fail(NVFP4_ERR_INVALID_ARG, "max_q_len=%lld and max_kv_len=%lld must be in [1, 2^31) and [0, 2^31)",
+                (long long)max_q_len, (long long)max_kv_len);
+  if ((int64_t)batch * n_kv_heads > (1 << 22))
+    return fail(NVFP4_ERR_UNSUPPORTED, "batch * n_kv_heads = %lld exceeds 2^22", (long long)batch * n_kv_heads);
+  return check_kv_rows(T, n_q_heads);
+}
+
 }  // namespace
 
 extern "C" {
@@ -524,6 +571,167 @@ int32_t nvfp4_bench_mfma_peak(int64_t iters, int32_t n_blocks, float* out, void*
   if (st) return st;
   return hip_status(nvfp4::launch_mfma_peak(iters, n_blocks, out, static_cast<hipStream_t>(stream)),
                     "nvfp4_bench_mfma_peak launch");
+}
+
+int32_t nvfp4_kv_page_bytes(int32_t n_kv_heads, int32_t page_size, int32_t head_dim, int64_t* bytes_out) {
+  if (!bytes_out) return fail(NVFP4_ERR_INVALID_ARG, "bytes_out is NULL");
+  nvfp4::KvGeom g;
+  const int32_t st = check_kv_shape(n_kv_heads, page_size, head_dim, 1, &g);
+  if (st) return st;
+  *bytes_out = g.page_bytes;
+  return ok();
+}
+
+int32_t nvfp4_rope_append_kv(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                             int32_t dtype, int64_t T, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                             const float* cos, const float* sin, int64_t n_pos, int32_t rot_dim, int32_t interleaved,
+                             const int32_t* positions, const int64_t* slots, uint8_t* cache, int64_t n_pages,
+                             int32_t page_size, const float* k_gscale, const float* v_gscale, void* q_out,
+                             int64_t ldqo, void* stream) {
+  nvfp4::KvAppendArgs a{};
+  int32_t st = check_kv_shape(n_kv_heads, page_size, head_dim, n_pages, &a.geom);
+  if (st) return st;
+  if (n_q_heads < 0) return fail(NVFP4_ERR_INVALID_ARG, "n_q_heads must not be negative");
+  if ((n_q_heads > 0) != (q != nullptr) || (n_q_heads > 0) != (q_out != nullptr))
+    return fail(NVFP4_ERR_INVALID_ARG, "q and q_out go with n_q_heads > 0 (all three, or none)");
+  if (n_q_heads > 0) {
+    st = check_x(q, dtype, T, (int64_t)n_q_heads * head_dim, ldq, "q");
+    if (!st) st = check_x(q_out, dtype, T, (int64_t)n_q_heads * head_dim, ldqo, "q_out");
+    if (st) return st;
+  }
+  st = check_x(k, dtype, T, (int64_t)n_kv_heads * head_dim, ldk, "k");
+  if (!st) st = check_x(v, dtype, T, (int64_t)n_kv_heads * head_dim, ldv, "v");
+  if (!st) st = check_kv_rows(T, (int64_t)n_q_heads + 2 * (int64_t)n_kv_heads);
+  if (!st) st = check_kv_cache(cache, k_gscale, v_gscale);
+  if (st) return st;
+  if (!positions || !slots) return fail(NVFP4_ERR_INVALID_ARG, "positions/slots is NULL");
+  if (rot_dim < 0 || rot_dim > head_dim)
+    return fail(NVFP4_ERR_INVALID_ARG, "rot_dim=%d outside [0, head_dim=%d]", rot_dim, head_dim);
+  if (rot_dim % 32) return fail(NVFP4_ERR_UNSUPPORTED, "rot_dim=%d is not a multiple of 32", rot_dim);
+  if (rot_dim > 0) {
+    if (!cos || !sin) return fail(NVFP4_ERR_INVALID_ARG, "cos/sin is NULL");
+    if (n_pos <= 0) return fail(NVFP4_ERR_INVALID_ARG, "n_pos must be positive");
+    if (!aligned16(cos) || !aligned16(sin)) return fail(NVFP4_ERR_UNSUPPORTED, "cos/sin must be 16-byte aligned");
+  }
+  st = check_device();
+  if (st) return st;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.ldq = ldq;
+  a.ldk = ldk;
+  a.ldv = ldv;
+  a.ldqo = ldqo;
+  a.T = T;
+  a.n_q_heads = n_q_heads;
+  a.cos = cos;
+  a.sin = sin;
+  a.n_pos = n_pos;
+  a.rot_dim = rot_dim;
+  a.interleaved = interleaved != 0;
+  a.positions = positions;
+  a.slots = slots;
+  a.cache = cache;
+  a.k_gscale = k_gscale;
+  a.v_gscale = v_gscale;
+  a.q_out = q_out;
+  return hip_status(nvfp4::launch_rope_append(a, in_type(dtype), head_dim, static_cast<hipStream_t>(stream)),
+                    "nvfp4_rope_append_kv launch");
+}
+
+int32_t nvfp4_kv_gather(const uint8_t* cache, int64_t n_pages, int32_t page_size, int32_t n_kv_heads,
+                        int32_t head_dim, const float* k_gscale, const float* v_gscale, const int64_t* slots,
+                        int64_t T, void* k_out, int64_t ldk, void* v_out, int64_t ldv, int32_t out_dtype,
+                        void* stream) {
+  nvfp4::KvGatherArgs a{};
+  int32_t st = check_kv_shape(n_kv_heads, page_size, head_dim, n_pages, &a.geom);
+  if (!st) st = check_x(k_out, out_dtype, T, (int64_t)n_kv_heads * head_dim, ldk, "k_out");
+  if (!st) st = check_x(v_out, out_dtype, T, (int64_t)n_kv_heads * head_dim, ldv, "v_out");
+  if (!st) st = check_kv_rows(T, 2 * (int64_t)n_kv_heads);
+  if (!st) st = check_kv_cache(cache, k_gscale, v_gscale);
+  if (st) return st;
+  if (!slots) return fail(NVFP4_ERR_INVALID_ARG, "slots is NULL");
+  st = check_device();
+  if (st) return st;
+  a.cache = cache;
+  a.slots = slots;
+  a.T = T;
+  a.k_gscale = k_gscale;
+  a.v_gscale = v_gscale;
+  a.k_out = k_out;
+  a.v_out = v_out;
+  a.ldk = ldk;
+  a.ldv = ldv;
+  return hip_status(nvfp4::launch_kv_gather(a, in_type(out_dtype), head_dim, static_cast<hipStream_t>(stream)),
+                    "nvfp4_kv_gather launch");
+}
+
+int32_t nvfp4_kv_attention_workspace(int32_t dtype, int64_t T, int32_t batch, int32_t n_q_heads, int32_t n_kv_heads,
+                                     int32_t head_dim, int64_t max_q_len, int64_t max_kv_len, int64_t* bytes_out) {
+  if (!bytes_out) return fail(NVFP4_ERR_INVALID_ARG, "bytes_out is NULL");
+  if (!valid_dtype(dtype)) return fail(NVFP4_ERR_UNSUPPORTED, "dtype %d is not F32 or BF16", dtype);
+  const int32_t st = check_kv_attn_sizes(T, batch, n_q_heads, n_kv_heads, head_dim, max_q_len, max_kv_len);
+  if (st) return st;
+  *bytes_out = nvfp4::kv_attn_plan(in_type(dtype), T, batch, n_q_heads, n_kv_heads, head_dim, max_q_len, max_kv_len)
+                   .workspace;
+  return ok();
+}
+
+int32_t nvfp4_kv_attention(const void* q, int32_t dtype, int64_t ldq, int64_t T, int32_t n_q_heads,
+                           int32_t n_kv_heads, int32_t head_dim, int32_t batch, const int32_t* cu_q,
+                           int64_t max_q_len, const int32_t* kv_len, int64_t max_kv_len, const int32_t* page_table,
+                           int64_t max_pages, int64_t ld_table, const uint8_t* cache, int64_t n_pages, int32_t page_size,
+                           const float* k_gscale, const float* v_gscale, float scale, int32_t window, void* o,
+                           int64_t ldo, float* lse, void* workspace, int64_t workspace_bytes, void* stream) {
+  nvfp4::KvAttnArgs a{};
+  int32_t st = check_kv_attn_sizes(T, batch, n_q_heads, n_kv_heads, head_dim, max_q_len, max_kv_len);
+  if (!st) st = check_kv_shape(n_kv_heads, page_size, head_dim, n_pages, &a.geom);
+  if (!st) st = check_x(q, dtype, T, (int64_t)n_q_heads * head_dim, ldq, "q");
+  if (!st) st = check_x(o, dtype, T, (int64_t)n_q_heads * head_dim, ldo, "o");
+  if (!st) st = check_kv_cache(cache, k_gscale, v_gscale);
+  if (st) return st;
+  if (!cu_q && T != batch)
+    return fail(NVFP4_ERR_INVALID_ARG, "without cu_q every sequence has one token: T=%lld must equal batch=%d",
+                (long long)T, batch);
+  if (!kv_len || !page_table) return fail(NVFP4_ERR_INVALID_ARG, "kv_len/page_table is NULL");
+  if (max_pages <= 0 || max_pages > (1ll << 30) / page_size)
+    return fail(NVFP4_ERR_INVALID_ARG, "max_pages=%lld of %d tokens: 1 to 2^30 tokens are supported",
+                (long long)max_pages, page_size);
+  if (ld_table < max_pages)
+    return fail(NVFP4_ERR_INVALID_ARG, "ld_table=%lld < max_pages=%lld", (long long)ld_table, (long long)max_pages);
+  if (!std::isfinite(scale)) return fail(NVFP4_ERR_INVALID_ARG, "scale is not finite");
+  if (window < 0) return fail(NVFP4_ERR_INVALID_ARG, "window=%d must not be negative (0 = none)", window);
+  const nvfp4::KvAttnPlan plan =
+      nvfp4::kv_attn_plan(in_type(dtype), T, batch, n_q_heads, n_kv_heads, head_dim, max_q_len, max_kv_len);
+  if (plan.workspace > 0) {
+    if (!workspace || workspace_bytes < plan.workspace)
+      return fail(NVFP4_ERR_INVALID_ARG, "workspace of %lld bytes is too small: %lld needed",
+                  (long long)(workspace ? workspace_bytes : 0), (long long)plan.workspace);
+    if (!aligned16(workspace)) return fail(NVFP4_ERR_UNSUPPORTED, "workspace must be 16-byte aligned");
+  }
+  st = check_device();
+  if (st) return st;
+  a.q = q;
+  a.ldq = ldq;
+  a.T = T;
+  a.n_q_heads = n_q_heads;
+  a.batch = batch;
+  a.cu_q = cu_q;
+  a.kv_len = kv_len;
+  a.table = page_table;
+  a.max_pages = max_pages;
+  a.ld_table = ld_table;
+  a.cache = cache;
+  a.k_gscale = k_gscale;
+  a.v_gscale = v_gscale;
+  a.scale = scale;
+  a.window = window < (1 << 30) ? window : (1 << 30);   // no sequence is longer
+  a.o = o;
+  a.ldo = ldo;
+  a.lse = lse;
+  a.part = static_cast<float*>(workspace);
+  return hip_status(nvfp4::launch_kv_attn(a, plan, in_type(dtype), head_dim, static_cast<hipStream_t>(stream)),
+                    "nvfp4_kv_attention launch");
 }
 
 int32_t nvfp4_mxfp4_quantize(const void* x, int32_t x_dtype, int64_t M, int64_t K, int64_t ldx, uint8_t* codes,

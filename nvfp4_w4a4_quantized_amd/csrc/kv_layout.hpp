@@ -1,0 +1,41 @@
+// Layout of the paged NVFP4 key/value cache, shared by the kernels that write and
+// read it.
+//
+// A page holds page_size tokens (a power of two, at least 16) of every kv head as
+// [head][page_size / 16] granules of 16 tokens; a granule is 18 D bytes:
+//   K codes   [16 tokens][D/2]              at 0
+//   K scales  [16 tokens][D/16]             at 8 D
+//   V codes   [4 quads][16][4 tokens][D/32] at 9 D   (a token's D/2 bytes in 16 parts)
+//   V scales  [4 quads][D/16][4 tokens]     at 17 D
+// The order is the one in which the matrix instructions take their operands, so that
+// every load of the attention kernels is a whole contiguous piece of a granule: lane
+// (g = lane / 16, r = lane % 16) of a 16-row MFMA reads key row r at its g-th quarter
+// of the elements, and for the values (transposed: rows are elements, the K axis is
+// tokens) part r of the four tokens of quad g, 16 bytes at D = 128.  Each code byte
+// holds two elements of ONE token, and each token has its own scale bytes, so that
+// appending a token writes whole bytes and never touches its neighbours'.
+#pragma once
+
+#include <stdint.h>
+
+namespace nvfp4 {
+
+constexpr int kv_granule_bytes(int D) { return 18 * D; }
+
+struct KvGeom {
+  int32_t n_kv_heads;
+  int32_t page_shift;      // log2(page_size)
+  int64_t page_bytes;      // n_kv_heads * page_size * D * 9 / 8
+  int64_t n_pages;
+};
+
+inline bool kv_shape_ok(int32_t D, int32_t page_size) {
+  return (D == 64 || D == 128 || D == 256) && page_size >= 16 && page_size <= 4096 &&
+         (page_size & (page_size - 1)) == 0;
+}
+
+inline int64_t kv_page_bytes(int32_t n_kv_heads, int32_t page_size, int32_t D) {
+  return (int64_t)n_kv_heads * page_size * D * 9 / 8;
+}
+
+}  // namespace nvfp4
