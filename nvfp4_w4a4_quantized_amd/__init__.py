@@ -351,41 +351,36 @@ def empty_kv_cache(n_pages: int, n_kv_heads: int, page_size: int, head_dim: int,
                        device=device)
 
 
-def _kv_cache(cache, k_gscale, v_gscale, page_size, head_dim=None):
-    """(n_kv_heads, head_dim, n_pages) of a cache buffer; the head dimension follows from
-    the page's bytes (9/8 byte per token, head and element)."""
+def _kv_call(name, stream, *args):
+    """One of the calls of csrc/torch_binding.cpp, which reads and checks the tensors (in
+    Python that took longer than the smaller kernels) on the current device and stream."""
     torch = _torch()
-    if cache.dtype != torch.uint8 or cache.dim() != 2 or not cache.is_contiguous():
-        raise Nvfp4Error(NVFP4_ERR_INVALID_ARG, "cache must be contiguous uint8 [n_pages, page bytes]")
-    for t, name in ((k_gscale, "k_gscale"), (v_gscale, "v_gscale")):
-        if t.dtype != torch.float32 or t.dim() != 1 or not t.is_contiguous():
-            raise Nvfp4Error(NVFP4_ERR_INVALID_ARG, f"{name} must be contiguous float32 [n_kv_heads]")
-    n_pages, page_bytes = cache.shape
-    n_kv_heads = k_gscale.shape[0]
-    if head_dim is None:
-        head_dim = page_bytes * 8 // (9 * max(n_kv_heads * page_size, 1))
-    if v_gscale.shape[0] != n_kv_heads or n_kv_heads * page_size * head_dim * 9 != page_bytes * 8:
-        raise Nvfp4Error(NVFP4_ERR_INVALID_ARG,
-                         f"cache pages of {page_bytes} bytes do not hold {page_size} tokens of {n_kv_heads} heads")
-    return n_kv_heads, head_dim, n_pages
+    if _kv_binding is None:
+        _load_kv_binding()
+    try:
+        device = torch._C._cuda_getDevice()
+        raw = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    except RuntimeError:                      # no GPU: no tensor can be on it
+        device, raw = -1, 0
+    refused = getattr(_kv_binding, name)(device, raw, *args)
+    if refused is not None:
+        raise Nvfp4Error(*refused)
 
 
-def _on_gpu(**named):
-    for name, t in named.items():
-        if t is not None and not t.is_cuda:
-            raise Nvfp4Error(NVFP4_ERR_INVALID_ARG, f"{name} must be in device memory")
+_kv_binding = None
 
 
-def _indices(t, name, dtype, n):
-    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or t.stride(0) != 1 and n > 1:
-        raise Nvfp4Error(NVFP4_ERR_INVALID_ARG, f"{name} must be contiguous {dtype} [{n}]")
-    return t.data_ptr()
-
-
-def _same_dtype(dtype, *named):
-    for t, name in named:
-        if t.dtype != dtype:
-            raise Nvfp4Error(NVFP4_ERR_UNSUPPORTED, f"{name} must be {dtype} like the others")
+def _load_kv_binding():
+    global _kv_binding
+    import importlib.machinery
+    import importlib.util
+    path = os.path.join(_HERE, "_torch_binding.so")
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is not built: run `python nvfp4_w4a4_quantized_amd/build.py`")
+    loader = importlib.machinery.ExtensionFileLoader("_torch_binding", path)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_torch_binding", loader))
+    loader.exec_module(module)
+    _kv_binding = module
 
 
 def nvfp4_rope_append_kv(q, k, v, cos, sin, positions, slots, cache, k_gscale, v_gscale, page_size, q_out,
@@ -394,54 +389,14 @@ def nvfp4_rope_append_kv(q, k, v, cos, sin, positions, slots, cache, k_gscale, v
     [n_pos, rot_dim / 2], or both None: no rotation; positions int32 [T]), write the
     rotated q to q_out (may be q; both None: no queries), and append k and v to the cache
     at slots (int64 [T]; outside the cache, e.g. -1: not appended)."""
-    torch = _torch()
-    _on_gpu(q=q, k=k, v=v, cos=cos, sin=sin, positions=positions, slots=slots, cache=cache, k_gscale=k_gscale,
-            v_gscale=v_gscale, q_out=q_out)
-    T, kv_cols, ldk = _rows(k, "k")
-    n_kv_heads, d, n_pages = _kv_cache(cache, k_gscale, v_gscale, page_size, kv_cols // max(k_gscale.shape[0], 1))
-    Tv, v_cols, ldv = _rows(v, "v")
-    if (Tv, v_cols) != (T, kv_cols) or n_kv_heads * d != kv_cols:
-        raise Nvfp4Error(NVFP4_ERR_INVALID_ARG, f"k and v must both be [T, {n_kv_heads} heads * head_dim]")
-    _same_dtype(k.dtype, (v, "v"))
-    n_q_heads = ldq = ldqo = 0
-    if (q is None) != (q_out is None):
-        raise Nvfp4Error(NVFP4_ERR_INVALID_ARG, "q and q_out must both be given or both be None")
-    if q is not None:
-        Tq, q_cols, ldq = _rows(q, "q")
-        To, o_cols, ldqo = _rows(q_out, "q_out")
-        if Tq != T or To != T or o_cols != q_cols or q_cols % d:
-            raise Nvfp4Error(NVFP4_ERR_INVALID_ARG, f"q and q_out must be [{T}, n_q_heads * {d}]")
-        _same_dtype(k.dtype, (q, "q"), (q_out, "q_out"))
-        n_q_heads = q_cols // d
-    rot_dim = n_pos = 0
-    if (cos is None) != (sin is None):
-        raise Nvfp4Error(NVFP4_ERR_INVALID_ARG, "cos and sin must both be given or both be None")
-    if cos is not None:
-        if cos.dtype != torch.float32 or sin.dtype != torch.float32 or cos.dim() != 2 or cos.shape != sin.shape \
-                or not cos.is_contiguous() or not sin.is_contiguous():
-            raise Nvfp4Error(NVFP4_ERR_INVALID_ARG, "cos and sin must be contiguous float32 [n_pos, rot_dim / 2]")
-        n_pos, rot_dim = cos.shape[0], 2 * cos.shape[1]
-    _check(lib.nvfp4_rope_append_kv(_ptr(q), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, _dtype_code(k), T, n_q_heads,
-                                    n_kv_heads, d, _ptr(cos), _ptr(sin), n_pos, rot_dim, 1 if interleaved else 0,
-                                    _indices(positions, "positions", torch.int32, T),
-                                    _indices(slots, "slots", torch.int64, T), cache.data_ptr(), n_pages, page_size,
-                                    k_gscale.data_ptr(), v_gscale.data_ptr(), _ptr(q_out), ldqo, _stream(stream)))
+    _kv_call("rope_append_kv", stream, cache, k_gscale, v_gscale, page_size, q, k, v, cos, sin, positions, slots, q_out,
+             interleaved)
 
 
 def nvfp4_kv_gather(cache, slots, k_gscale, v_gscale, page_size, k_out, v_out, stream=None) -> None:
     """The values of cache rows (slots int64 [T]; outside the cache: zeros) into k_out
     and v_out [T, n_kv_heads * d]."""
-    torch = _torch()
-    _on_gpu(cache=cache, slots=slots, k_gscale=k_gscale, v_gscale=v_gscale, k_out=k_out, v_out=v_out)
-    n_kv_heads, d, n_pages = _kv_cache(cache, k_gscale, v_gscale, page_size)
-    T, k_cols, ldk = _rows(k_out, "k_out")
-    Tv, v_cols, ldv = _rows(v_out, "v_out")
-    if Tv != T or k_cols != n_kv_heads * d or v_cols != k_cols:
-        raise Nvfp4Error(NVFP4_ERR_INVALID_ARG, f"k_out and v_out must both be [T, {n_kv_heads * d}]")
-    _same_dtype(k_out.dtype, (v_out, "v_out"))
-    _check(lib.nvfp4_kv_gather(cache.data_ptr(), n_pages, page_size, n_kv_heads, d, k_gscale.data_ptr(),
-                               v_gscale.data_ptr(), _indices(slots, "slots", torch.int64, T), T, k_out.data_ptr(), ldk,
-                               v_out.data_ptr(), ldv, _dtype_code(k_out), _stream(stream)))
+    _kv_call("kv_gather", stream, cache, k_gscale, v_gscale, page_size, slots, k_out, v_out)
 
 
 def nvfp4_kv_attention_workspace(n_tokens: int, batch: int, n_q_heads: int, n_kv_heads: int, head_dim: int,
@@ -468,29 +423,8 @@ def nvfp4_kv_attention(q, cache, page_table, kv_len, k_gscale, v_gscale, page_si
     kv_len[b] tokens in pages page_table[b] and the query rows cu_q[b] .. cu_q[b + 1] (None:
     row b alone), the last of its tokens.  max_q_len and max_kv_len bound the lengths;
     workspace: uint8 buffer of nvfp4_kv_attention_workspace bytes; lse fp32 [T, n_q_heads]."""
-    torch = _torch()
-    _on_gpu(q=q, cache=cache, page_table=page_table, kv_len=kv_len, k_gscale=k_gscale, v_gscale=v_gscale, o=o,
-            workspace=workspace, cu_q=cu_q, lse=lse)
-    n_kv_heads, d, n_pages = _kv_cache(cache, k_gscale, v_gscale, page_size)
-    T, q_cols, ldq = _rows(q, "q")
-    To, o_cols, ldo = _rows(o, "o")
-    if To != T or o_cols != q_cols or q_cols % max(d, 1):
-        raise Nvfp4Error(NVFP4_ERR_INVALID_ARG, f"q and o must both be [T, n_q_heads * {d}]")
-    _same_dtype(q.dtype, (o, "o"))
-    n_q_heads = q_cols // max(d, 1)
-    if page_table.dtype != torch.int32:
-        raise Nvfp4Error(NVFP4_ERR_UNSUPPORTED, "page_table must be int32")
-    batch, max_pages, ld_table = _rows(page_table, "page_table")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, n_q_heads) or not lse.is_contiguous()):
-        raise Nvfp4Error(NVFP4_ERR_INVALID_ARG, f"lse must be contiguous float32 [{T}, {n_q_heads}]")
-    _check(lib.nvfp4_kv_attention(q.data_ptr(), _dtype_code(q), ldq, T, n_q_heads, n_kv_heads, d, batch,
-                                  None if cu_q is None else _indices(cu_q, "cu_q", torch.int32, batch + 1), max_q_len,
-                                  _indices(kv_len, "kv_len", torch.int32, batch), max_kv_len, page_table.data_ptr(),
-                                  max_pages, ld_table, cache.data_ptr(), n_pages, page_size, k_gscale.data_ptr(),
-                                  v_gscale.data_ptr(), d ** -0.5 if scale is None else scale, window, o.data_ptr(),
-                                  ldo, _ptr(lse), _ptr(workspace),
-                                  0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                  _stream(stream)))
+    _kv_call("kv_attention", stream, cache, k_gscale, v_gscale, page_size, q, page_table, kv_len, o, max_kv_len,
+             workspace, cu_q, max_q_len, scale, window, lse)
 
 
 def nvfp4_bench_mfma_peak(iters: int, n_blocks: int, out, stream=None) -> None:

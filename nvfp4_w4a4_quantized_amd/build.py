@@ -1,22 +1,26 @@
-"""Build libnvfp4.so (the C ABI + HIP kernels) for gfx950 with hipcc, in-tree.
+"""Build libnvfp4.so (the C ABI + HIP kernels) for gfx950 with hipcc, in-tree, and
+_torch_binding.so (host code: torch tensors to the C ABI) against it.
 
 Each source is compiled to an object in its own process (in parallel), then the
-objects are linked into the shared library.  Every call rebuilds everything.
+objects are linked into the shared libraries.  Every call rebuilds everything.
 
     python nvfp4_w4a4_quantized_amd/build.py
 
 It imports nothing from the package, whose import needs the built library.
 """
 
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libnvfp4.so")
+BINDING = os.path.join(HERE, "_torch_binding.so")
 OBJDIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["abi.cpp", "quant.hip", "gemm.hip", "gemv.hip", "skinny.hip", "requant.hip", "mx.hip", "noalloc.hip", "gdn.hip", "probe.hip", "soloq.hip", "kvcache.hip",
@@ -35,6 +39,7 @@ COMPILE_FLAGS = [
     "-I", os.path.join(ROOT, "include"),
 ]
 LINK_FLAGS = ["--offload-arch=gfx950", "-shared", "-fPIC"]
+BINDING_SOURCE = "torch_binding.cpp"
 
 
 def _run(cmd, verbose):
@@ -45,17 +50,34 @@ def _run(cmd, verbose):
         raise RuntimeError("hipcc failed:\n" + " ".join(cmd) + "\n" + res.stdout + res.stderr)
 
 
+def _binding_commands():
+    """Compile and link of the host-only binding.  torch is found, not imported; its
+    libraries are loaded by the time the binding is."""
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    obj = os.path.join(OBJDIR, "torch_binding.o")
+    compile_ = ["g++", "-O2", "-std=c++20", "-fPIC", "-fvisibility=hidden", "-w", "-isystem",
+                os.path.join(torch, "include"), "-I", sysconfig.get_paths()["include"], "-c", "-o", obj,
+                os.path.join(CSRC, BINDING_SOURCE)]
+    link = ["g++", "-shared", "-o", BINDING + ".tmp", obj, "-L" + HERE, "-lnvfp4", "-Wl,-rpath,$ORIGIN",
+            "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    return compile_, link
+
+
 def build(verbose: bool = False) -> str:
     hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
     os.makedirs(OBJDIR, exist_ok=True)
     objs = [os.path.join(OBJDIR, os.path.splitext(s)[0] + ".o") for s in SOURCES]
     cmds = [[hipcc] + COMPILE_FLAGS + ["-c", "-o", o, os.path.join(CSRC, s)] for s, o in zip(SOURCES, objs)]
+    compile_binding, link_binding = _binding_commands()
+    cmds.insert(0, compile_binding)
     with ThreadPoolExecutor(max_workers=len(cmds)) as ex:
         for f in [ex.submit(_run, c, verbose) for c in cmds]:
             f.result()
     tmp = LIB + ".tmp"
     _run([hipcc] + LINK_FLAGS + ["-o", tmp] + objs, verbose)
     os.replace(tmp, LIB)
+    _run(link_binding, verbose)
+    os.replace(BINDING + ".tmp", BINDING)
     return LIB
 
 

@@ -114,6 +114,49 @@ def test_positions_outside_the_table_are_clamped(nv):
     assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
 
 
+def test_binding_refusals(nv):
+    cuda = dict(device="cuda")
+    cache = nv.empty_kv_cache(4, 2, 16, 64)
+    g, x = torch.ones(2, **cuda), torch.zeros(3, 128, **cuda)
+    i32, slots = torch.zeros(3, dtype=torch.int32, **cuda), torch.zeros(3, dtype=torch.int64, **cuda)
+    half = torch.rand(5, 32, **cuda)
+    cu = torch.arange(4, dtype=torch.int32, **cuda)
+
+    def append(q=x, k=x, v=x, cos=half, sin=half, pos=i32, slots=slots, cache=cache, kg=g, vg=g, page=16, out=x):
+        nv.nvfp4_rope_append_kv(q, k, v, cos, sin, pos, slots, cache, kg, vg, page, out)
+
+    def gather(cache=cache, slots=slots, kg=g, vg=g, page=16, k=x, v=x):
+        nv.nvfp4_kv_gather(cache, slots, kg, vg, page, k, v)
+
+    def attend(q=x, cache=cache, table=i32[:, None], kv_len=i32, kg=g, page=16, o=x, most=10, ws=None, **kw):
+        nv.nvfp4_kv_attention(q, cache, table, kv_len, kg, g, page, o, most, ws, **kw)
+
+    inv, uns = nv.NVFP4_ERR_INVALID_ARG, nv.NVFP4_ERR_UNSUPPORTED
+    for call, bad, status in (
+            (append, dict(k=x[:, :64]), inv), (append, dict(v=x[:2]), inv), (append, dict(v=x.bfloat16()), uns),
+            (append, dict(k=x.half(), v=x.half()), uns), (append, dict(q=x.t()), inv), (append, dict(q=None), inv),
+            (append, dict(out=None), inv), (append, dict(q=x[:, :100], out=x[:, :100]), inv), (append, dict(out=x.bfloat16()), uns),
+            (append, dict(pos=slots), inv), (append, dict(slots=i32), inv), (append, dict(slots=slots[:2]), inv),
+            (append, dict(cos=None), inv), (append, dict(cos=half.double()), inv), (append, dict(sin=half[:4]), inv),
+            (append, dict(cos=torch.rand(5, 64, **cuda), sin=torch.rand(5, 64, **cuda)), inv), (append, dict(kg=g[:1]), inv),
+            (append, dict(vg=g.double()), inv), (append, dict(page=32), inv), (append, dict(page=0), inv),
+            (append, dict(cache=cache[:, :-1]), inv), (append, dict(cache=cache.view(-1)), inv), (append, dict(slots=None), inv),
+            (append, dict(slots=[1, 2, 3]), inv), (append, dict(page="16"), inv), (append, dict(k=x.cpu()), inv),
+            (gather, dict(k=x[:, :64]), inv), (gather, dict(v=x.bfloat16()), uns), (gather, dict(slots=slots[:1]), inv),
+            (gather, dict(k=x[:2], v=x[:2]), inv), (gather, dict(cache=cache.float()), inv),
+            (attend, dict(o=x[:2]), inv), (attend, dict(o=x.bfloat16()), uns), (attend, dict(table=slots[:, None]), uns),
+            (attend, dict(table=i32), inv), (attend, dict(kv_len=i32[:2]), inv), (attend, dict(kv_len=slots), inv),
+            (attend, dict(table=i32[:2, None], kv_len=i32[:2]), inv), (attend, dict(cu_q=i32), inv),
+            (attend, dict(cu_q=cu.long()), inv), (attend, dict(lse=torch.zeros(3, 3, **cuda)), inv),
+            (attend, dict(lse=torch.zeros(3, 2, dtype=torch.float64, **cuda)), inv), (attend, dict(scale=float("nan")), inv),
+            (attend, dict(scale="big"), inv), (attend, dict(window=-1), inv), (attend, dict(window=1 << 40), inv),
+            (attend, dict(most=-1), inv), (attend, dict(max_q_len=0), inv), (attend, dict(most=100000), inv),
+            (attend, dict(most=100000, ws=torch.empty(16, dtype=torch.uint8, **cuda)), inv)):
+        with pytest.raises(nv.Nvfp4Error) as e:
+            call(**bad)
+        assert e.value.status == status, (bad, str(e.value))
+
+
 # ----------------------------------------------------------------------------- attention
 
 class Problem:

@@ -99,18 +99,13 @@ def test_workspace_covers_both_types(nv):
         nv.nvfp4_kv_attention_workspace(1, 1, 8, 1, 128, 1, 1, dtype=torch.float16)
 
 
-def test_binding_refuses_what_the_library_cannot_see(nv):
+def test_binding_refuses_host_memory(nv):
     cache = torch.empty(4, nv.nvfp4_kv_page_bytes(2, 16, 64), dtype=torch.uint8)
-    g = torch.ones(2)
-    x = torch.zeros(3, 128)
-    with pytest.raises(nv.Nvfp4Error, match="device memory"):
-        nv.nvfp4_kv_gather(cache, torch.zeros(3, dtype=torch.int64), g, g, 16, x, x.clone())
-    with pytest.raises(nv.Nvfp4Error, match="do not hold"):
-        nv._kv_cache(cache, g, g, 16, 128)
-    with pytest.raises(nv.Nvfp4Error, match="k_gscale"):
-        nv._kv_cache(cache, g.double(), g, 16)
-    with pytest.raises(nv.Nvfp4Error, match="uint8"):
-        nv._kv_cache(cache.float(), g, g, 16)
-    assert nv._kv_cache(cache, g, g, 16) == (2, 64, 4)
-    with pytest.raises(nv.Nvfp4Error, match="slots"):
-        nv._indices(torch.zeros(3, dtype=torch.int32), "slots", torch.int64, 3)
+    g, x, i32 = torch.ones(2), torch.zeros(3, 128), torch.zeros(3, dtype=torch.int32)
+    slots = torch.zeros(3, dtype=torch.int64)
+    for call in (lambda: nv.nvfp4_kv_gather(cache, slots, g, g, 16, x, x.clone()),
+                 lambda: nv.nvfp4_rope_append_kv(None, x, x, None, None, i32, slots, cache, g, g, 16, None),
+                 lambda: nv.nvfp4_kv_attention(x, cache, i32[:, None], i32, g, g, 16, x.clone(), 10)):
+        with pytest.raises(nv.Nvfp4Error, match="device memory") as e:
+            call()
+        assert e.value.status == nv.NVFP4_ERR_INVALID_ARG
