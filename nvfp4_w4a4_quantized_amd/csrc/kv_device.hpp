@@ -1,0 +1,145 @@
+// Device helpers of the attention kernels over the NVFP4 key/value cache.
+#pragma once
+
+#include "kernel_common.hpp"
+#include "kv_layout.hpp"
+
+namespace nvfp4 {
+namespace {
+
+constexpr float kNegBig = -1.0e30f;      // reference M of a row that has seen nothing
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float xor16(float x) { return __shfl_xor(x, 16); }
+__device__ __forceinline__ float xor32(float x) { return __shfl_xor(x, 32); }
+
+// Query rows enter the f16 product scaled by 2^(14 - e), amax of the row in [2^e, 2^(e+1)), and
+// their scores are scaled back; rows below 2^-100 stay near zero.
+__device__ __forceinline__ int query_exponent(float amax) {
+  const int e = (int)((__float_as_uint(amax) >> 23) & 255u) - 127;
+  return e < -100 ? -100 : e;
+}
+__device__ __forceinline__ float query_up(float amax) {
+  return __uint_as_float((uint32_t)(14 - query_exponent(amax) + 127) << 23);
+}
+__device__ __forceinline__ float query_down(float amax) {
+  return __uint_as_float((uint32_t)(query_exponent(amax) - 14 + 127) << 23);
+}
+
+// What a workgroup needs of its sequence
+struct SeqInfo {
+  int64_t q0;              // first query token (row of q)
+  int32_t m;               // query tokens
+  int32_t n;               // cached tokens
+};
+
+__device__ __forceinline__ SeqInfo seq_info(const KvAttnArgs& a, int b) {
+  SeqInfo s;
+  int64_t q0 = b, q1 = b + 1;
+  if (a.cu_q) {
+    q0 = a.cu_q[b];
+    q1 = a.cu_q[b + 1];
+  }
+  q0 = q0 < 0 ? 0 : (q0 > a.T ? a.T : q0);
+  q1 = q1 < q0 ? q0 : (q1 > a.T ? a.T : q1);
+  s.q0 = q0;
+  s.m = (int32_t)(q1 - q0);
+  const int64_t most = a.max_pages << a.geom.page_shift;
+  const int64_t n = a.kv_len[b];
+  s.n = (int32_t)(n < 0 ? 0 : (n > most ? most : n));
+  return s;
+}
+
+// The tokens that query columns [col0, col1) of a sequence attend to, as one range
+struct Span {
+  int32_t lo, hi;          // [lo, hi)
+  int32_t all_lo, all_hi;  // tokens that every one of these columns attends to
+};
+
+__device__ __forceinline__ Span span_of(const SeqInfo& s, int32_t col0, int32_t col1, int group, int window) {
+  const int32_t first = s.n - s.m + col0 / group, last = s.n - s.m + (col1 - 1) / group;
+  Span r;
+  r.hi = last + 1 > 0 ? last + 1 : 0;
+  r.all_hi = first + 1 > 0 ? first + 1 : 0;
+  r.lo = window && first - window + 1 > 0 ? first - window + 1 : 0;
+  r.all_lo = window && last - window + 1 > 0 ? last - window + 1 : 0;
+  return r;
+}
+
+template <int N>
+__device__ __forceinline__ void load_dwords(const uint8_t* p, uint32_t* d) {
+  if constexpr (N == 2) {
+    const u32x2 x = *reinterpret_cast<const u32x2*>(p);
+    d[0] = x[0];
+    d[1] = x[1];
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const u32x4 x = *reinterpret_cast<const u32x4*>(p + 4 * i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) d[i + e] = x[e];
+    }
+  }
+}
+
+// Nibbles of four tokens' code bytes re-paired by token: byte i of lo[0] holds element 2 i
+// of tokens (0, 1), of hi[0] element 2 i + 1, and lo[1], hi[1] those of tokens (2, 3); w = the
+// dword (4 bytes) of each token.
+__device__ __forceinline__ void pair_tokens(const uint32_t w[4], uint32_t lo[2], uint32_t hi[2]) {
+  constexpr uint32_t M = 0x0F0F0F0Fu;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t x = w[2 * i], y = w[2 * i + 1];
+    lo[i] = (x & M) | ((y << 4) & ~M);
+    hi[i] = ((x >> 4) & M) | (y & ~M);
+  }
+}
+
+template <int SEL>
+__device__ __forceinline__ f16x2 cvt_fp4(uint32_t w) {
+  return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, SEL);
+}
+
+// The four tokens' code bytes of dword `part` (8 elements) of a value granule
+template <int D>
+__device__ __forceinline__ void value_words(const uint32_t v[D / 32], int part, uint32_t w[4]) {
+  if constexpr (D == 64) {               // 2 bytes per token
+    w[0] = v[0];
+    w[1] = v[0] >> 16;
+    w[2] = v[1];
+    w[3] = v[1] >> 16;
+  } else if constexpr (D == 128) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = v[e];
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = v[2 * e + part];
+  }
+}
+
+template <bool F32>
+__device__ __forceinline__ void load8(const void* base, int64_t off, float v[8]) {
+  if constexpr (F32) {
+    const f32x4* p = reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(base) + off);
+    const f32x4 a = p[0], b = p[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = a[i];
+      v[4 + i] = b[i];
+    }
+  } else {
+    const u32x4 a = *reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(base) + off);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(a[i] << 16);
+      v[2 * i + 1] = __uint_as_float(a[i] & 0xFFFF0000u);
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  return f32_to_bf16_bits(a) | (f32_to_bf16_bits(b) << 16);
+}
+
+}  // namespace
+}  // namespace nvfp4

@@ -24,57 +24,17 @@
 // and the scores of two 16-token granules are, in place, the B operand of O^T = V^T P^T
 // (the K axis, tokens, in the order quads g of both granules; V^T is read in the same
 // order).  Codes go from HBM to registers in whole 16-byte pieces and are decoded there.
-#include "kernel_common.hpp"
-#include "kv_layout.hpp"
+#include "kv_device.hpp"
 
 namespace nvfp4 {
 
 namespace {
 
-constexpr float kNegBig = -1.0e30f;      // reference M of a row that has seen nothing
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kMaxWorkers = 512;         // two workgroups per compute unit
 
-__device__ __forceinline__ float xor16(float x) { return __shfl_xor(x, 16); }
-__device__ __forceinline__ float xor32(float x) { return __shfl_xor(x, 32); }
-
-// What a workgroup needs of its sequence
-struct SeqInfo {
-  int64_t q0;              // first query token (row of q)
-  int32_t m;               // query tokens
-  int32_t n;               // cached tokens
-};
-
-__device__ __forceinline__ SeqInfo seq_info(const KvAttnArgs& a, int b) {
-  SeqInfo s;
-  int64_t q0 = b, q1 = b + 1;
-  if (a.cu_q) {
-    q0 = a.cu_q[b];
-    q1 = a.cu_q[b + 1];
-  }
-  q0 = q0 < 0 ? 0 : (q0 > a.T ? a.T : q0);
-  q1 = q1 < q0 ? q0 : (q1 > a.T ? a.T : q1);
-  s.q0 = q0;
-  s.m = (int32_t)(q1 - q0);
-  const int64_t most = a.max_pages << a.geom.page_shift;
-  const int64_t n = a.kv_len[b];
-  s.n = (int32_t)(n < 0 ? 0 : (n > most ? most : n));
-  return s;
-}
-
-// The tokens that query columns [col0, col1) of a sequence attend to, as one range
-struct Span {
-  int32_t lo, hi;          // [lo, hi)
-  int32_t all_lo, all_hi;  // tokens that every one of these columns attends to
-};
-
-__device__ __forceinline__ Span span_of(const SeqInfo& s, int64_t col0, int64_t col1, int group, int window) {
-  const int32_t first = s.n - s.m + (int32_t)col0 / group, last = s.n - s.m + ((int32_t)col1 - 1) / group;
-  Span r;
-  r.hi = last + 1 > 0 ? last + 1 : 0;
-  r.all_hi = first + 1 > 0 ? first + 1 : 0;
-  r.lo = window && first - window + 1 > 0 ? first - window + 1 : 0;
-  r.all_lo = window && last - window + 1 > 0 ? last - window + 1 : 0;
-  return r;
+__device__ __forceinline__ int64_t uniform64(int64_t x) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)x), hi = __builtin_amdgcn_readfirstlane((uint32_t)(x >> 32));
+  return (int64_t)(((uint64_t)hi << 32) | lo);
 }
 
 // One granule as a lane of the 16-row MFMAs holds it.
@@ -84,22 +44,6 @@ struct Granule {
   static constexpr int KS = D == 256 ? 2 : 1;
   uint32_t k[KD], ks[KS], v[KD], vs;
 };
-
-template <int N>
-__device__ __forceinline__ void load_dwords(const uint8_t* p, uint32_t* d) {
-  if constexpr (N == 2) {
-    const u32x2 x = *reinterpret_cast<const u32x2*>(p);
-    d[0] = x[0];
-    d[1] = x[1];
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; i += 4) {
-      const u32x4 x = *reinterpret_cast<const u32x4*>(p + 4 * i);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) d[i + e] = x[e];
-    }
-  }
-}
 
 // Keys: lane (g, r) holds token r, elements 32 g + 8 m + j (D = 128), 128 c + 32 g + 8 m + j
 // (D = 256), 16 g + 8 m + j (D = 64); values: tokens 4 g + e, elements (D / 16) r + j.
@@ -132,41 +76,6 @@ __device__ __forceinline__ f16x8 key_frag(const Granule<D>& x, int i) {
   }
 }
 
-// Nibbles of four tokens' code bytes re-paired by token: byte i of lo[0] holds element 2 i
-// of tokens (0, 1), of hi[0] element 2 i + 1, and lo[1], hi[1] those of tokens (2, 3); w = the
-// dword (4 bytes) of each token.
-__device__ __forceinline__ void pair_tokens(const uint32_t w[4], uint32_t lo[2], uint32_t hi[2]) {
-  constexpr uint32_t M = 0x0F0F0F0Fu;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t x = w[2 * i], y = w[2 * i + 1];
-    lo[i] = (x & M) | ((y << 4) & ~M);
-    hi[i] = ((x >> 4) & M) | (y & ~M);
-  }
-}
-
-template <int SEL>
-__device__ __forceinline__ f16x2 cvt_fp4(uint32_t w) {
-  return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, SEL);
-}
-
-// The four tokens' code bytes of dword `part` (8 elements) of a value granule
-template <int D>
-__device__ __forceinline__ void value_words(const Granule<D>& x, int part, uint32_t w[4]) {
-  if constexpr (D == 64) {               // 2 bytes per token
-    w[0] = x.v[0];
-    w[1] = x.v[0] >> 16;
-    w[2] = x.v[1];
-    w[3] = x.v[1] >> 16;
-  } else if constexpr (D == 128) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) w[e] = x.v[e];
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) w[e] = x.v[2 * e + part];
-  }
-}
-
 __device__ __forceinline__ f32x4 mfma16(f16x8 a, f16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
@@ -178,39 +87,44 @@ __device__ __forceinline__ f16x8 join(f16x2 a, f16x2 b, f16x2 c, f16x2 d) {
 // Two fp32 -> two f16, round to nearest even
 __device__ __forceinline__ f16x2 to_f16(float a, float b) { return f16x2{(_Float16)a, (_Float16)b}; }
 
-template <bool F32>
-__device__ __forceinline__ void load8(const void* base, int64_t off, float v[8]) {
-  if constexpr (F32) {
-    const f32x4* p = reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(base) + off);
-    const f32x4 a = p[0], b = p[1];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] = a[i];
-      v[4 + i] = b[i];
-    }
-  } else {
-    const u32x4 a = *reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(base) + off);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(a[i] << 16);
-      v[2 * i + 1] = __uint_as_float(a[i] & 0xFFFF0000u);
-    }
-  }
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  return f32_to_bf16_bits(a) | (f32_to_bf16_bits(b) << 16);
-}
-
-// One workgroup = W waves = (sequence, kv head, 16 NQ query columns, split of the key
-// axis); each wave takes a contiguous piece of the split's tokens, NG granules at a time,
-// with the next ones' loads in flight; the waves' (maximum, sum, output) are joined in
-// LDS.  With one split the result goes out, else it goes to the partials for k_kv_join.
+// Work of a call: items (sequence, kv head, tile of tile_cols query columns), each a run of
+// steps of NG granules along its keys.  With whole items (n_workers == 0) a workgroup takes
+// one.  Otherwise all steps of the call, in item order, are cut into n_workers equal runs, one
+// per workgroup, whatever the sequences' lengths: a run takes the end of one item, perhaps
+// whole ones, and the start of another.  Items that fell into several runs leave partial results
+// (slot 1: an item's first piece, slot 0: a later one) for k_kv_join.
+//
+// Inside a workgroup, waves are CW groups of 16 NQ columns by W / CW pieces of the run's
+// tokens; the pieces are joined in LDS.
 constexpr int kAttnWaves = 4;
 
-template <int D, int NQ, bool F32>
+// Steps of one item of sequence b, and its items
+struct SeqWork {
+  SeqInfo seq;
+  int32_t cols, tiles, begin, steps;    // begin: first token, granule-aligned
+};
+
+template <int TOK>
+__device__ __forceinline__ SeqWork seq_work(const KvAttnArgs& a, int b, int group) {
+  SeqWork w;
+  w.seq = seq_info(a, b);
+  w.cols = w.seq.m * group;
+  w.tiles = 0;
+  w.begin = w.steps = 0;
+  if (w.cols > 0) {
+    const Span sp = span_of(w.seq, 0, w.cols, group, a.window);
+    const int32_t tiles = (w.cols + a.tile_cols - 1) / a.tile_cols;
+    w.tiles = tiles < a.col_tiles ? tiles : a.col_tiles;   // further ones go with the first tiles' items
+    w.begin = sp.lo & ~15;
+    w.steps = (sp.hi - w.begin + TOK - 1) / TOK;
+    w.steps = w.steps < 1 ? 1 : w.steps;                   // an empty item still writes its zeros
+  }
+  return w;
+}
+
+template <int D, int NQ, int CW, bool F32>
 __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
-  constexpr int W = kAttnWaves;
+  constexpr int W = kAttnWaves, TW = W / CW;
   constexpr int NG = D == 256 ? 2 : 4;             // granules per step
   constexpr int TOK = 16 * NG;
   constexpr int KC = D / 32;                       // 32-element chunks of the first product
@@ -222,33 +136,109 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int cg = wave % CW, tg = wave / CW;
   const int g = lane >> 4, r = lane & 15;
   const int hkv = a.geom.n_kv_heads, group = a.n_q_heads / hkv;
-  int bid = blockIdx.x;
-  const int split = bid % a.n_splits;
-  bid /= a.n_splits;
-  const int tile = bid % a.col_tiles;
-  bid /= a.col_tiles;
-  const int kh = bid % hkv, b = bid / hkv;
-  const SeqInfo seq = seq_info(a, b);
-  const int64_t cols = (int64_t)seq.m * group;
-  const float kg = a.k_gscale[kh], vg = a.v_gscale[kh];
-  const int32_t last_page = (seq.n - 1) >> a.geom.page_shift;
   const int per_head = 1 << (a.geom.page_shift - 4);
 
-  for (int64_t col0 = (int64_t)tile * 16 * NQ; col0 < cols; col0 += (int64_t)a.col_tiles * 16 * NQ) {
-    const int64_t col1 = col0 + 16 * NQ < cols ? col0 + 16 * NQ : cols;
-    const Span sp = span_of(seq, col0, col1, group, a.window);
-    // this split's tokens, in whole steps from a granule-aligned start; the split
-    // length is the plan's, or longer where the plan's bound was too low
-    const int32_t begin = sp.lo & ~15;
-    const int32_t steps = (sp.hi - begin + TOK - 1) / TOK;
-    int32_t per = (steps + a.n_splits - 1) / a.n_splits;
-    const int32_t planned = a.split_tokens / TOK;
-    per = per > planned ? per : planned;
-    const int32_t s0 = split * per, s1 = s0 + per < steps ? s0 + per : steps;
-    const int32_t pw = s1 > s0 ? (s1 - s0 + W - 1) / W : 0;
-    const int32_t w0 = s0 + wave * pw, w1 = w0 + pw < s1 ? w0 + pw : s1;
+  // this workgroup's run of steps: [u, u_end) of the sequences from b on, whose first
+  // step is u_seq
+  int b;
+  int64_t u = 0, u_end = 1, u_seq = 0;
+  SeqWork sw;
+  if (a.n_workers == 0) {
+    const int item = blockIdx.x / a.col_tiles;
+    b = item / hkv;
+    sw = seq_work<TOK>(a, b, group);
+    if ((int)(blockIdx.x % a.col_tiles) >= sw.tiles) return;
+  } else {
+    // each lane counts the steps of `each` consecutive sequences
+    const int each = (a.batch + 63) / 64;
+    int64_t own = 0;
+    for (int i = 0; i < each; ++i) {
+      const int bb = lane * each + i;
+      if (bb < a.batch) {
+        const SeqWork x = seq_work<TOK>(a, bb, group);
+        own += (int64_t)x.tiles * hkv * x.steps;
+      }
+    }
+    int64_t upto = own;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int64_t x = __shfl_up(upto, off);
+      if (lane >= off) upto += x;
+    }
+    const int64_t total = __shfl(upto, 63);
+    const int64_t workers = total < a.n_workers ? total : a.n_workers;   // none without a step
+    if (blockIdx.x >= workers) return;
+    u = total * blockIdx.x / workers;
+    u_end = total * (blockIdx.x + 1) / workers;
+    const int first = __builtin_ctzll(__builtin_amdgcn_ballot_w64(upto > u));
+    u_seq = __shfl(upto - own, first);
+    b = first * each;
+    // wave-uniform from here on
+    u = uniform64(u);
+    u_end = uniform64(u_end);
+    u_seq = uniform64(u_seq);
+    b = __builtin_amdgcn_readfirstlane(b);
+    for (;; ++b) {
+      sw = seq_work<TOK>(a, b, group);
+      const int64_t n = (int64_t)sw.tiles * hkv * sw.steps;
+      if (u < u_seq + n) break;
+      u_seq += n;
+    }
+  }
+
+  while (u < u_end) {
+    int kh, tile0;
+    int32_t s_first, s_last;                       // the item's steps in this run
+    if (a.n_workers == 0) {
+      tile0 = blockIdx.x % a.col_tiles;
+      kh = (blockIdx.x / a.col_tiles) % hkv;
+      s_first = 0;
+      s_last = sw.steps;
+      u = u_end;
+    } else {
+      while (u >= u_seq + (int64_t)sw.tiles * hkv * sw.steps) {
+        u_seq += (int64_t)sw.tiles * hkv * sw.steps;
+        sw = seq_work<TOK>(a, ++b, group);
+      }
+      const int32_t item = (int32_t)((u - u_seq) / sw.steps);
+      tile0 = item % sw.tiles;
+      kh = item / sw.tiles;
+      s_first = (int32_t)(u - u_seq - (int64_t)item * sw.steps);
+      const int64_t left = u_end - u;
+      s_last = left < sw.steps - s_first ? s_first + (int32_t)left : sw.steps;
+      u += s_last - s_first;
+      // where the pieces of the item are
+      if (threadIdx.x == 0) {
+        int32_t* where = a.pieces + 2 * (((int64_t)b * hkv + kh) * a.col_tiles + tile0);
+        if (s_first == 0) where[0] = s_last == sw.steps ? -1 : (int32_t)blockIdx.x;
+        if (s_last == sw.steps && s_first > 0) where[1] = (int32_t)blockIdx.x;
+      }
+    }
+    const SeqInfo& seq = sw.seq;
+    const float kg = a.k_gscale[kh], vg = a.v_gscale[kh];
+    const int32_t last_page = (seq.n - 1) >> a.geom.page_shift;
+
+    // tiles past the planned ones are done whole, with the item's first piece
+    for (int32_t tile = tile0; (int64_t)tile * a.tile_cols < sw.cols; tile += a.col_tiles) {
+    if (tile != tile0 && s_first > 0) break;
+    const int32_t col_first = tile * a.tile_cols;
+    const int32_t cols = col_first + a.tile_cols < sw.cols ? col_first + a.tile_cols : sw.cols;   // end of the tile
+    Span sp = span_of(seq, col_first, cols, group, a.window);
+    int32_t begin = sw.begin, s0 = s_first, s1 = s_last;
+    bool whole = s0 == 0 && s1 == sw.steps;
+    if (a.n_workers == 0 || tile != tile0) {       // the tile's own keys
+      begin = sp.lo & ~15;
+      s0 = 0;
+      s1 = (sp.hi - begin + TOK - 1) / TOK;
+      whole = true;
+    }
+    if (seq.n <= 0) s1 = s0;
+    const int32_t col0 = col_first + cg * 16 * NQ;
+    const int32_t pw = s1 > s0 && col0 < cols ? (s1 - s0 + TW - 1) / TW : 0;
+    const int32_t w0 = s0 + tg * pw, w1 = w0 + pw < s1 ? w0 + pw : s1;
 
     // query columns: lane (g, r) holds column r of every block, the chunks' elements
     f16x8 qf[TERMS][NQ][KC];
@@ -257,10 +247,10 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
     f32x4 acc[NQ][NJ];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-      int64_t col = col0 + 16 * n + r;
+      int32_t col = col0 + 16 * n + r;
       if (col >= cols) col = cols - 1;             // computed, never written
-      const int32_t qi = (int32_t)col / group;
-      const int head = kh * group + ((int32_t)col - qi * group);
+      const int32_t qi = col / group;
+      const int head = kh * group + (col - qi * group);
       const int64_t off = (seq.q0 + qi) * a.ldq + (int64_t)head * D;
       float v[KC][8];
       float amax = 0.0f;
@@ -273,11 +263,8 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
       }
       amax = __builtin_fmaxf(amax, xor16(amax));
       amax = __builtin_fmaxf(amax, xor32(amax));
-      // 2^(14 - e) for amax in [2^e, 2^(e+1)); zero and tiny rows are left near zero
-      int e = (int)((__float_as_uint(amax) >> 23) & 255u) - 127;
-      e = e < -100 ? -100 : e;
-      const float up = __uint_as_float((uint32_t)(14 - e + 127) << 23);
-      csc[n] = a.scale * kLog2e * kg * __uint_as_float((uint32_t)(e - 14 + 127) << 23);
+      const float up = query_up(amax);
+      csc[n] = a.scale * kLog2e * kg * query_down(amax);
 #pragma unroll
       for (int c = 0; c < KC; ++c)
 #pragma unroll
@@ -423,7 +410,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
               uint32_t w[4];
-              value_words<D>(cur[2 * k + u], part, w);
+              value_words<D>(cur[2 * k + u].v, part, w);
               pair_tokens(w, lo[u], hi[u]);
             }
             auto rows = [&](int j, f16x2 (&x)[2][2]) {
@@ -455,7 +442,8 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
       }
     }
 
-    // join the waves
+    // join the waves of each column group
+    __syncthreads();                               // s_m, s_l, s_o of the work before are read
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
       l[n] += xor16(l[n]);
@@ -468,10 +456,11 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
     __syncthreads();
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-      float top = s_m[0][16 * n + r];
+      float top = s_m[cg][16 * n + r];
 #pragma unroll
-      for (int w = 1; w < W; ++w) top = __builtin_fmaxf(top, s_m[w][16 * n + r]);
+      for (int w = 1; w < TW; ++w) top = __builtin_fmaxf(top, s_m[cg + w * CW][16 * n + r]);
       const float f = __builtin_amdgcn_exp2f(m[n] - top);
+      if (n) __syncthreads();
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float* dst = &s_o[wave][r * LDO + NJ * (4 * g + i)];
@@ -481,28 +470,30 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
               f32x4{acc[n][j][i] * f, acc[n][j + 1][i] * f, acc[n][j + 2][i] * f, acc[n][j + 3][i] * f};
       }
       __syncthreads();
-      // thread = (column, D / 16 elements)
+      // thread = (column, D / 16 elements) of each column group in turn
       const int c = threadIdx.x >> 4, part = threadIdx.x & 15;
-      const int64_t col = col0 + 16 * n + c;
-      if (col < cols) {
-        float top_c = s_m[0][16 * n + c], sum = 0.0f;
 #pragma unroll
-        for (int w = 1; w < W; ++w) top_c = __builtin_fmaxf(top_c, s_m[w][16 * n + c]);
+      for (int h = 0; h < CW; ++h) {
+        const int32_t col = col_first + h * 16 * NQ + 16 * n + c;
+        if (col >= cols) break;
+        float top_c = s_m[h][16 * n + c], sum = 0.0f;
 #pragma unroll
-        for (int w = 0; w < W; ++w) sum += s_l[w][16 * n + c] * __builtin_amdgcn_exp2f(s_m[w][16 * n + c] - top_c);
+        for (int w = 1; w < TW; ++w) top_c = __builtin_fmaxf(top_c, s_m[h + w * CW][16 * n + c]);
+#pragma unroll
+        for (int w = 0; w < TW; ++w)
+          sum += s_l[h + w * CW][16 * n + c] * __builtin_amdgcn_exp2f(s_m[h + w * CW][16 * n + c] - top_c);
         float out[NJ];
 #pragma unroll
         for (int j = 0; j < NJ; j += 4) {
-          f32x4 x = *reinterpret_cast<const f32x4*>(&s_o[0][c * LDO + part * NJ + j]);
+          f32x4 x = *reinterpret_cast<const f32x4*>(&s_o[h][c * LDO + part * NJ + j]);
 #pragma unroll
-          for (int w = 1; w < W; ++w) x += *reinterpret_cast<const f32x4*>(&s_o[w][c * LDO + part * NJ + j]);
+          for (int w = 1; w < TW; ++w) x += *reinterpret_cast<const f32x4*>(&s_o[h + w * CW][c * LDO + part * NJ + j]);
 #pragma unroll
           for (int e = 0; e < 4; ++e) out[j + e] = x[e];
         }
-        const int32_t qi = (int32_t)col / group;
-        const int head = kh * group + ((int32_t)col - qi * group);
-        const int64_t row = (seq.q0 + qi) * a.n_q_heads + head;
-        if (a.n_splits == 1) {
+        if (whole) {
+          const int32_t qi = col / group;
+          const int head = kh * group + (col - qi * group);
           const float f = sum > 0.0f ? vg / sum : 0.0f;
           const int64_t off = (seq.q0 + qi) * a.ldo + (int64_t)head * D + part * NJ;
           if constexpr (F32) {
@@ -517,9 +508,10 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
                   u32x2{pack_bf16(out[j] * f, out[j + 1] * f), pack_bf16(out[j + 2] * f, out[j + 3] * f)};
           }
           if (a.lse && part == 0)
-            a.lse[row] = sum > 0.0f ? (top_c + __builtin_log2f(sum)) * kLn2 : -__builtin_inff();
+            a.lse[(seq.q0 + qi) * a.n_q_heads + head] =
+                sum > 0.0f ? (top_c + __builtin_log2f(sum)) * kLn2 : -__builtin_inff();
         } else {
-          float* dst = a.part + (row * a.n_splits + split) * (D + 4);
+          float* dst = a.part + ((2 * (int64_t)blockIdx.x + (s_first == 0)) * a.tile_cols + col - col_first) * (D + 4);
 #pragma unroll
           for (int j = 0; j < NJ; j += 4)
             *reinterpret_cast<f32x4*>(dst + 4 + part * NJ + j) = f32x4{out[j], out[j + 1], out[j + 2], out[j + 3]};
@@ -529,53 +521,102 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
           }
         }
       }
-      __syncthreads();
+    }
     }
   }
 }
 
-// Join the splits of an output row: one wave per row, lane = D / 64 elements.
+// Join the pieces of an item: one workgroup per query column.  The pieces' factors go to
+// LDS first, then D / 4 threads take four elements of a piece each, 1024 / D pieces at a
+// time, with no load depending on another.
 template <int D, bool F32>
 __global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs a) {
-  constexpr int E = D / 64;
-  const int lane = threadIdx.x & 63;
-  const int64_t row = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (row >= a.T * a.n_q_heads) return;
-  const float* src = a.part + row * a.n_splits * (D + 4);
-  float top = kNegBig;
-  for (int s = 0; s < a.n_splits; ++s) top = __builtin_fmaxf(top, src[s * (D + 4)]);
-  float sum = 0.0f, out[E];
+  constexpr int TPS = D / 4, LANES = 256 / TPS;      // threads per piece, pieces side by side
+  __shared__ float s_f[kMaxWorkers], s_red[4], s_sum[4];
+  __shared__ f32x4 s_x[LANES][TPS];
+  const int tid = threadIdx.x;
+  const int group = a.n_q_heads / a.geom.n_kv_heads;
+  const int c = blockIdx.x % a.tile_cols;
+  const int item = blockIdx.x / a.tile_cols;
+  const int tile = item % a.col_tiles, kh = (item / a.col_tiles) % a.geom.n_kv_heads;
+  const SeqInfo seq = seq_info(a, item / a.col_tiles / a.geom.n_kv_heads);
+  const int32_t col = tile * a.tile_cols + c;
+  if (col >= seq.m * group) return;
+  const int32_t first = a.pieces[2 * (int64_t)item];
+  if (first < 0) return;                             // done whole
+  const int32_t n = a.pieces[2 * (int64_t)item + 1] - first + 1;
+  auto piece = [&](int i) {
+    return a.part + ((2 * (int64_t)(first + i) + (i == 0)) * a.tile_cols + c) * (D + 4);
+  };
+  float m[kMaxWorkers / 256], l[kMaxWorkers / 256], top = kNegBig;
 #pragma unroll
-  for (int e = 0; e < E; ++e) out[e] = 0.0f;
-  for (int s = 0; s < a.n_splits; ++s) {
-    const float* p = src + s * (D + 4);
-    const float f = __builtin_amdgcn_exp2f(p[0] - top);
-    sum += p[1] * f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) out[e] += p[4 + lane * E + e] * f;
+  for (int i = 0; i < kMaxWorkers / 256; ++i) {
+    m[i] = kNegBig;
+    l[i] = 0.0f;
+    if (tid + 256 * i < n) {
+      const f32x4 ml = *reinterpret_cast<const f32x4*>(piece(tid + 256 * i));
+      m[i] = ml[0];
+      l[i] = ml[1];
+    }
+    top = __builtin_fmaxf(top, m[i]);
   }
-  const int64_t tok = row / a.n_q_heads;
-  const int head = (int)(row - tok * a.n_q_heads);
-  const float f = sum > 0.0f ? a.v_gscale[head / (a.n_q_heads / a.geom.n_kv_heads)] / sum : 0.0f;
-  const int64_t off = tok * a.ldo + (int64_t)head * D + lane * E;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    if constexpr (F32) reinterpret_cast<float*>(a.o)[off + e] = out[e] * f;
-    else reinterpret_cast<uint16_t*>(a.o)[off + e] = (uint16_t)f32_to_bf16_bits(out[e] * f);
+  for (int off = 32; off >= 1; off >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, off));
+  if ((tid & 63) == 0) s_red[tid >> 6] = top;
+  __syncthreads();
+  top = __builtin_fmaxf(__builtin_fmaxf(s_red[0], s_red[1]), __builtin_fmaxf(s_red[2], s_red[3]));
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kMaxWorkers / 256; ++i) {
+    const float f = __builtin_amdgcn_exp2f(m[i] - top);
+    s_f[tid + 256 * i] = f;
+    sum += l[i] * f;
   }
-  if (a.lse && lane == 0) a.lse[row] = sum > 0.0f ? (top + __builtin_log2f(sum)) * kLn2 : -__builtin_inff();
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off);
+  if ((tid & 63) == 0) s_sum[tid >> 6] = sum;
+  __syncthreads();
+  sum = (s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]);
+  const int part = tid % TPS, lane = tid / TPS;
+  f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+  for (int i = lane; i < n; i += LANES) x += *reinterpret_cast<const f32x4*>(piece(i) + 4 + 4 * part) * s_f[i];
+  s_x[lane][part] = x;
+  __syncthreads();
+  if (tid >= TPS) return;
+#pragma unroll
+  for (int i = 1; i < LANES; ++i) x += s_x[i][part];
+  const int64_t tok = seq.q0 + col / group;
+  const int head = kh * group + col % group;
+  const float g = sum > 0.0f ? a.v_gscale[kh] / sum : 0.0f;
+  const int64_t off = tok * a.ldo + (int64_t)head * D + 4 * part;
+  if constexpr (F32) {
+    *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.o) + off) = x * g;
+  } else {
+    *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(a.o) + off) =
+        u32x2{pack_bf16(x[0] * g, x[1] * g), pack_bf16(x[2] * g, x[3] * g)};
+  }
+  if (a.lse && tid == 0) a.lse[tok * a.n_q_heads + head] = sum > 0.0f ? (top + __builtin_log2f(sum)) * kLn2 : -__builtin_inff();
 }
 
-template <int D, int NQ, bool F32>
+template <int D, int NQ, int CW, bool F32>
 hipError_t launch(const KvAttnArgs& a, hipStream_t s) {
-  const int64_t blocks = (int64_t)a.batch * a.geom.n_kv_heads * a.col_tiles * a.n_splits;
-  hipLaunchKernelGGL((k_kv_attn<D, NQ, F32>), dim3((unsigned)blocks), dim3(64 * kAttnWaves), 0, s, a);
+  const int64_t items = (int64_t)a.batch * a.geom.n_kv_heads * a.col_tiles;
+  const int64_t blocks = a.n_workers ? a.n_workers : items;
+  hipLaunchKernelGGL((k_kv_attn<D, NQ, CW, F32>), dim3((unsigned)blocks), dim3(64 * kAttnWaves), 0, s, a);
   hipError_t e = hipGetLastError();
-  if (e == hipSuccess && a.n_splits > 1) {
-    hipLaunchKernelGGL((k_kv_join<D, F32>), dim3((unsigned)((a.T * a.n_q_heads + 3) / 4)), dim3(256), 0, s, a);
+  if (e == hipSuccess && a.n_workers) {
+    hipLaunchKernelGGL((k_kv_join<D, F32>), dim3((unsigned)(items * a.tile_cols)), dim3(256), 0, s, a);
     e = hipGetLastError();
   }
   return e;
+}
+
+template <int D, int NQ, bool F32>
+hipError_t launch_cw(const KvAttnArgs& a, int cw, hipStream_t s) {
+  if (cw == 1) return launch<D, NQ, 1, F32>(a, s);
+  if (cw == 2) return launch<D, NQ, 2, F32>(a, s);
+  return launch<D, NQ, 4, F32>(a, s);
 }
 
 }  // namespace
@@ -583,42 +624,54 @@ hipError_t launch(const KvAttnArgs& a, hipStream_t s) {
 KvAttnPlan kv_attn_plan(InType t, int64_t T, int32_t batch, int32_t n_q_heads, int32_t n_kv_heads, int32_t D,
                         int64_t max_q_len, int64_t max_kv_len) {
   KvAttnPlan p{};
-  const int64_t cols = max_q_len * (n_q_heads / n_kv_heads);
+  const int64_t cols = (max_q_len < T ? max_q_len : T) * (n_q_heads / n_kv_heads);
+  if (t == InType::BF16 && cols >= kv_prefill_cols()) {
+    p.prefill = true;
+    p.tile_cols = kv_prefill_cols();
+    const int64_t tiles = (cols + p.tile_cols - 1) / p.tile_cols, most = ((int64_t)1 << 30) / ((int64_t)batch * n_kv_heads);
+    p.col_tiles = (int32_t)(tiles < most ? tiles : most);
+    return p;
+  }
   // two column blocks share a decoded granule where their registers fit
   p.nq = cols > 16 && (D == 64 || (D == 128 && t == InType::BF16)) ? 2 : 1;
-  int64_t tiles = (cols + 16 * p.nq - 1) / (16 * p.nq);
-  // the kernel walks the tiles with the grid's stride: any number of them is right
-  const int64_t most_tiles = ((int64_t)1 << 30) / ((int64_t)batch * n_kv_heads * 64);
+  const int64_t blk = 16 * p.nq;
+  p.cw = cols <= blk ? 1 : (cols <= 2 * blk ? 2 : 4);
+  p.tile_cols = (int32_t)(cols < blk * p.cw ? cols : blk * p.cw);
+  int64_t tiles = (cols + p.tile_cols - 1) / p.tile_cols;
+  const int64_t pairs = (int64_t)batch * n_kv_heads;
+  // any number of planned tiles is right: the kernel takes further ones with the first
+  const int64_t most_tiles = ((int64_t)1 << 30) / (pairs * p.tile_cols);
   if (tiles > most_tiles) tiles = most_tiles < 1 ? 1 : most_tiles;
   p.col_tiles = (int32_t)tiles;
-  const int64_t wgs = (int64_t)batch * n_kv_heads * tiles;
-  const int64_t chunk = 256;                            // fewest tokens of a split
-  int64_t splits = (512 + wgs - 1) / wgs;
-  const int64_t most = (max_kv_len + chunk - 1) / chunk;
-  if (splits > most) splits = most;
-  if (splits > 64) splits = 64;
-  if (splits < 1) splits = 1;
-  p.n_splits = (int32_t)splits;
-  const int64_t per = (max_kv_len + splits - 1) / splits;
-  p.split_tokens = (int32_t)((per + 255) / 256 * 256);
-  p.workspace = splits > 1 ? T * n_q_heads * splits * (D + 4) * (int64_t)sizeof(float) : 0;
+  const int64_t items = pairs * tiles;
+  const int64_t tok = D == 256 ? 32 : 64, waves = kAttnWaves / p.cw;
+  const int64_t steps = (max_kv_len + tok - 1) / tok;
+  if (items >= 1024 || steps <= 3 * waves) return p;    // whole items
+  int64_t n = items * steps / (2 * waves);
+  if (n > kMaxWorkers) n = kMaxWorkers;
+  if (n < 1) n = 1;
+  p.n_workers = (int32_t)n;
+  p.pieces_at = n * 2 * p.tile_cols * (D + 4) * (int64_t)sizeof(float);
+  p.workspace = p.pieces_at + items * 2 * (int64_t)sizeof(int32_t);
   return p;
 }
 
 hipError_t launch_kv_attn(KvAttnArgs a, const KvAttnPlan& p, InType t, int32_t D, hipStream_t s) {
-  a.n_splits = p.n_splits;
-  a.split_tokens = p.split_tokens;
+  a.n_workers = p.n_workers;
+  a.tile_cols = p.tile_cols;
   a.col_tiles = p.col_tiles;
+  if (p.prefill) return launch_kv_prefill(a, D, s);
+  a.pieces = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(a.part) + p.pieces_at);
   const bool f32 = t == InType::F32;
   if (D == 64) {
-    if (p.nq == 2) return f32 ? launch<64, 2, true>(a, s) : launch<64, 2, false>(a, s);
-    return f32 ? launch<64, 1, true>(a, s) : launch<64, 1, false>(a, s);
+    if (p.nq == 2) return f32 ? launch_cw<64, 2, true>(a, p.cw, s) : launch_cw<64, 2, false>(a, p.cw, s);
+    return f32 ? launch_cw<64, 1, true>(a, p.cw, s) : launch_cw<64, 1, false>(a, p.cw, s);
   }
   if (D == 128) {
-    if (p.nq == 2) return launch<128, 2, false>(a, s);
-    return f32 ? launch<128, 1, true>(a, s) : launch<128, 1, false>(a, s);
+    if (p.nq == 2) return launch_cw<128, 2, false>(a, p.cw, s);
+    return f32 ? launch_cw<128, 1, true>(a, p.cw, s) : launch_cw<128, 1, false>(a, p.cw, s);
   }
-  return f32 ? launch<256, 1, true>(a, s) : launch<256, 1, false>(a, s);
+  return f32 ? launch_cw<256, 1, true>(a, p.cw, s) : launch_cw<256, 1, false>(a, p.cw, s);
 }
 
 }  // namespace nvfp4

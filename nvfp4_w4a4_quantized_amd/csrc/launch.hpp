@@ -178,19 +178,27 @@ struct KvAttnArgs {
   void* o;
   int64_t ldo;
   float* lse;                  // optional
-  float* part;                 // split partials (NULL when n_splits == 1)
+  float* part;                 // partial results (workspace)
   // the plan
-  int32_t n_splits;
-  int32_t split_tokens;        // tokens of a split, unless a sequence needs more
-  int32_t col_tiles;           // tiles of query columns per kv head in the grid
+  int32_t* pieces;             // [items][first, last] workgroups of an item done in pieces
+  int32_t n_workers;           // 0: one workgroup per item; else equal runs of all steps
+  int32_t tile_cols;           // query columns of an item
+  int32_t col_tiles;           // items per sequence and kv head
 };
 struct KvAttnPlan {
-  int32_t n_splits, split_tokens, col_tiles, nq;
+  int32_t n_workers, tile_cols, col_tiles, nq, cw;
+  bool prefill;                // kvprefill.hip
+  int64_t pieces_at;           // byte offset in the workspace
   int64_t workspace;           // bytes
 };
 KvAttnPlan kv_attn_plan(InType t, int64_t T, int32_t batch, int32_t n_q_heads, int32_t n_kv_heads, int32_t D,
                         int64_t max_q_len, int64_t max_kv_len);
 hipError_t launch_kv_attn(KvAttnArgs a, const KvAttnPlan& p, InType t, int32_t D, hipStream_t s);
+
+// kvprefill.hip: bf16, whole items of kv_prefill_cols() query columns (a.col_tiles per
+// sequence and kv head in the grid; any number is right).
+int32_t kv_prefill_cols();
+hipError_t launch_kv_prefill(const KvAttnArgs& a, int32_t D, hipStream_t s);
 
 // noalloc.hip: this device's copy of the fixed workspace (kNoallocScratchBytes),
 // looked up once per device with that device current.
