@@ -13,6 +13,9 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 __device__ __forceinline__ float xor16(float x) { return __shfl_xor(x, 16); }
 __device__ __forceinline__ float xor32(float x) { return __shfl_xor(x, 32); }
 
+// Two fp32 -> two f16, round to nearest even
+__device__ __forceinline__ f16x2 to_f16(float a, float b) { return f16x2{(_Float16)a, (_Float16)b}; }
+
 // Query rows enter the f16 product scaled by 2^(14 - e), amax of the row in [2^e, 2^(e+1)), and
 // their scores are scaled back; rows below 2^-100 stay near zero.
 __device__ __forceinline__ int query_exponent(float amax) {

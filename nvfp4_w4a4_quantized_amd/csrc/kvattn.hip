@@ -84,9 +84,6 @@ __device__ __forceinline__ f16x8 join(f16x2 a, f16x2 b, f16x2 c, f16x2 d) {
   return f16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// Two fp32 -> two f16, round to nearest even
-__device__ __forceinline__ f16x2 to_f16(float a, float b) { return f16x2{(_Float16)a, (_Float16)b}; }
-
 // Work of a call: items (sequence, kv head, tile of tile_cols query columns), each a run of
 // steps of NG granules along its keys.  With whole items (n_workers == 0) a workgroup takes
 // one.  Otherwise all steps of the call, in item order, are cut into n_workers equal runs, one

@@ -2,18 +2,25 @@
 // The mathematics and numerics are those of kvattn.hip; what differs is the work split.
 //
 // Here the two matrix products bound the kernel, so keys and values are decoded once per
-// workgroup: eight waves share a tile of 64 tokens, decoded to f16 (exactly) into LDS, and
-// each wave takes 32 query columns through it with MFMA 32x32x16.  S^T = K q^T leaves a
-// lane with scores of one column, 16 of every 32 tokens (tokens 8 (i / 4) + 4 h + i % 4, h =
-// lane / 32), which are in place the B operand of O^T = V^T P^T when its K axis takes the
-// tokens of a granule in the order quads 0, 2, 1, 3; V^T is written to LDS in that order, so
-// the weights never leave the registers.
+// workgroup: eight waves share tiles of tokens, decoded to f16 (exactly) into LDS, and each
+// wave takes 32 query columns through them with MFMA 32x32x16.  S^T = K q^T leaves a lane with
+// scores of one column, 16 of every 32 tokens (tokens 8 (i / 4) + 4 h + i % 4, h = lane / 32), which
+// are in place the B operand of O^T = V^T P^T when its K axis takes the tokens of a granule in
+// the order quads 0, 2, 1, 3; V^T is written to LDS in that order, so the weights never leave
+// the registers.
 //
-// LDS, twice (a tile is decoded while the one before is used, one barrier per tile):
-//   K   [64 tokens][D]: 16-byte chunk c of row t at place c ^ (t mod 16)
-//   V^T [D][64 slots]:  16-byte chunk c of row d at place c ^ ((d ^ d/8 ^ d/64) mod 8)
+// Where the registers allow (D <= 128) a wave works on three blocks of 32 tokens at once: the
+// scores of block j + 1 and the output of block j - 1 on the matrix unit beside the softmax of
+// block j on the vector unit, neither waiting for the other.
+//
+// LDS, two decoded tiles of each (a tile is decoded while the one before is used; one barrier
+// per tile):
+//   K   [tokens][D], V^T [D][tokens], the 16-byte chunks of a row swizzled by the row
 // so that a wave's 16-byte reads of 32 rows, and the decoder's writes, spread over the banks.
-// Wave w loads granule w % 4 of the next tile but one, keys (w < 4) or values.
+// D <= 128: tiles of 128 tokens, wave w loads and decodes granule w.  D = 256: 64 tokens (what LDS
+// holds), wave w granule w % 4, keys (w < 4) or values.
+#include <type_traits>
+
 #include "kv_device.hpp"
 
 namespace nvfp4 {
@@ -22,28 +29,69 @@ namespace {
 
 constexpr int kPrefillWaves = 8;
 constexpr int kPrefillCols = 32 * kPrefillWaves;
-constexpr int kTok = 64;
+template <int D>
+constexpr int kTok = D == 256 ? 64 : 128;          // tokens of a tile
 
 __device__ __forceinline__ f32x16 mfma32(f16x8 a, f16x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
 
+// Places in a decoded tile.  The swizzles are exclusive ors on the chunk number (the bits of
+// the address from 4 on, below the row's), so that the places of a lane's chunks follow from
+// one base by a constant exclusive or, and those of further rows by a constant offset.  16
+// consecutive rows (a 16-byte read) use every 16-byte place of 256 bytes once, and so do the
+// decoder's writes, D / 16 rows apart, as far as there are places.
+template <int D>
+constexpr int kKMask = D == 64 ? 7 : 15;
 template <int D>
 __device__ __forceinline__ int k_place(int t, int c) {
-  constexpr int M = D == 64 ? 7 : 15;
-  return t * 2 * D + ((c ^ (t & M)) << 4);
+  return t * 2 * D + ((c ^ ((D == 64 ? t >> 1 : t) & kKMask<D>)) << 4);
 }
 
-__device__ __forceinline__ int v_place(int d, int c) { return d * 2 * kTok + ((c ^ ((d ^ (d >> 3) ^ (d >> 6)) & 7)) << 4); }
+template <int D>
+constexpr int kVMask = D == 256 ? 7 : 15;
+template <int D>
+constexpr int v_swizzle(int d) { return (D == 256 ? (d >> 1) ^ (d >> 4) : d ^ (d >> 3)) & kVMask<D>; }
+template <int D>
+__device__ __forceinline__ int v_place(int d, int c) { return d * 2 * kTok<D> + ((c ^ v_swizzle<D>(d)) << 4); }
+
+template <typename T>
+__device__ __forceinline__ __attribute__((address_space(3))) T& lds_at(uint32_t at) {
+  return *reinterpret_cast<__attribute__((address_space(3))) T*>(at);
+}
+
+// x of the other half of the wave joined to this lane's by f
+__device__ __forceinline__ float max_halves(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __builtin_fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+__device__ __forceinline__ f32x16 zeros16() {
+  f32x16 x;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) x[e] = 0.0f;
+  return x;
+}
+
+__device__ __forceinline__ float max16(const f32x16& x) {
+  float m;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(m) : "v"(x[0]), "v"(x[1]), "v"(x[2]));
+#pragma unroll
+  for (int i = 3; i + 1 < 16; i += 2) asm("v_max3_f32 %0, %0, %1, %2" : "+v"(m) : "v"(x[i]), "v"(x[i + 1]));
+  asm("v_max_f32 %0, %0, %1" : "+v"(m) : "v"(x[15]));
+  return m;
+}
 
 template <int D>
 __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs a) {
-  constexpr int KD = D / 32;                       // dwords of codes a lane decodes
+  constexpr bool PIPE = D <= 128;
+  constexpr int TOK = kTok<D>, TILE = TOK * D * 2;               // bytes of one decoded tile, keys or values
+  constexpr int KD = D / 32;                       // dwords of codes a lane decodes, keys and values each
   constexpr int NB = D / 32;                       // 32-row blocks of O^T
   constexpr int KS = D / 16;                       // K steps of the first product
-  constexpr int SB = D == 256 ? 1 : 2;             // 32-token blocks of scores at a time: what registers hold
-  constexpr int KBYTES = kTok * D * 2, BUF = 2 * KBYTES;
-  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  extern __shared__ __attribute__((aligned(256))) uint8_t shared[];
+  // LDS addresses as numbers: one register each, offsets in the instruction
+  const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)shared;
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -54,212 +102,330 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
   const SeqInfo seq = seq_info(a, pair / hkv);
   const int32_t cols = seq.m * group;
   const int32_t tiles = (cols + kPrefillCols - 1) / kPrefillCols;
-  const int32_t last_page = (seq.n - 1) >> a.geom.page_shift;
+  const int32_t last_page = (seq.n - 1) >> a.geom.page_shift, last_granule = (seq.n - 1) >> 4;
   const int per_head = 1 << (a.geom.page_shift - 4);
   const float kg = a.k_gscale[kh], vg = a.v_gscale[kh];
-  const int u = wave & 3, h = lane >> 5, c32 = lane & 31;
-  const bool values = wave >= 4;
+  const int h = lane >> 5, c32 = lane & 31;
+  const int gran = D == 256 ? wave & 3 : wave;      // this wave's granule of a tile
 
   for (int32_t tile = tiles - 1 - (int32_t)(blockIdx.x / pairs); tile >= 0; tile -= a.col_tiles) {
     const int32_t col_first = tile * kPrefillCols;
     const int32_t col_end = col_first + kPrefillCols < cols ? col_first + kPrefillCols : cols;
     const Span all = span_of(seq, col_first, col_end, group, a.window);
     const int32_t begin = all.lo & ~15;
-    const int32_t steps = seq.n > 0 ? (all.hi - begin + kTok - 1) / kTok : 0;
+    const int32_t steps = seq.n > 0 ? (all.hi - begin + TOK - 1) / TOK : 0;
 
-    // this wave's columns
+    // this wave's columns (past the tile's end: its last one again, never written)
     const int32_t col0 = col_first + 32 * wave;
-    const bool live = col0 < col_end;
-    const int32_t col1 = col0 + 32 < col_end ? col0 + 32 : col_end;
-    Span sp{0, 0, 0, 0};
-    if (live) sp = span_of(seq, col0, col1, group, a.window);
-    int32_t col = col0 + c32;
-    if (col >= col_end) col = col_end - 1;
-    const int32_t qi = col / group;
-    const int head = kh * group + (col - qi * group);
+    const int32_t w0 = col0 < col_end ? col0 : col_end - 1;
+    const int32_t w1 = col0 + 32 < col_end ? col0 + 32 : col_end;
+    const Span sp = span_of(seq, w0, w1, group, a.window);
 
     // loads of tile s: this wave's granule, its page id known one tile ahead
     auto page_of = [&](int32_t s) -> int32_t {
-      int32_t pg = (begin + s * kTok + 16 * u) >> a.geom.page_shift;
+      int32_t pg = (begin + s * TOK + 16 * gran) >> a.geom.page_shift;
       pg = pg < last_page ? pg : last_page;
       const int32_t id = a.table[(int64_t)(pair / hkv) * a.ld_table + pg];
       return id < 0 ? 0 : (id >= a.geom.n_pages ? (int32_t)a.geom.n_pages - 1 : id);
     };
-    uint32_t raw[KD], rs = 0;
-    auto load = [&](int32_t s, int32_t id) {
-      int32_t gr = (begin + s * kTok) / 16 + u;
-      const int32_t last = (seq.n - 1) >> 4;
-      gr = gr < last ? gr : last;
-      const uint8_t* p = a.cache + (int64_t)id * a.geom.page_bytes +
-                         (int64_t)(kh * per_head + (gr & (per_head - 1))) * kv_granule_bytes(D);
-      if (!values) {
-        load_dwords<KD>(p + lane * (D / 8), raw);
-        const uint8_t* ps = p + 8 * D + lane * (D / 64);
-        if constexpr (D == 64) rs = *ps;
-        else if constexpr (D == 128) rs = *reinterpret_cast<const uint16_t*>(ps);
-        else rs = *reinterpret_cast<const uint32_t*>(ps);
-      } else {
-        load_dwords<KD>(p + 9 * D + lane * (D / 8), raw);
-        rs = *reinterpret_cast<const uint32_t*>(p + 17 * D + ((lane >> 4) * (D / 16) + (lane & 15) * D / 256) * 4);
-      }
+    auto granule = [&](int32_t s, int32_t id) {
+      int32_t gr = (begin + s * TOK) / 16 + gran;
+      gr = gr < last_granule ? gr : last_granule;
+      return a.cache + (int64_t)id * a.geom.page_bytes +
+             (int64_t)(kh * per_head + (gr & (per_head - 1))) * kv_granule_bytes(D);
     };
-    // decode the loaded granule of tile s into its buffer
-    auto decode = [&](int32_t s) {
-      uint8_t* buf = lds + (s & 1) * BUF;
-      if (!values) {
-        const int t = 16 * u + lane / 4, part = lane % 4;
-#pragma unroll
-        for (int i = 0; i < KD; ++i) {
-          const f16x2 sc = bcast(scale_pair_f16(D == 256 ? rs >> (16 * (i / 4)) : rs), D == 64 ? 0 : (i >> 1) & 1);
-          *reinterpret_cast<f16x8*>(buf + k_place<D>(t, part * KD + i)) = decode8_f16(raw[i], sc);
-        }
-      } else {
-        const int g = lane >> 4, r = lane & 15;
-        const int32_t left = seq.n - (begin + s * kTok + 16 * u + 4 * g);
-        const uint32_t sb = left >= 4 ? rs : (left <= 0 ? 0u : rs & ((1u << (8 * left)) - 1u));
-        f16x2 sc[2];
-        sc[0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(sb, 1.0f, false);
-        sc[1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(sb, 1.0f, true);
-        const int chunk = 2 * u + (g & 1);
-        uint8_t* base = buf + KBYTES + (g >> 1) * 8;
-#pragma unroll
-        for (int part = 0; part < (KD + 3) / 4; ++part) {
-          uint32_t w[4], lo[2], hi[2];
-          value_words<D>(raw, part, w);
-          pair_tokens(w, lo, hi);
-          auto put = [&](int j, f16x2 x, f16x2 y) {
-            const int d = r * (D / 16) + 8 * part + j;
-            typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
-            *reinterpret_cast<f16x4*>(base + v_place(d, chunk)) = f16x4{x[0], x[1], y[0], y[1]};
-          };
-#define NVFP4_VROWS(SEL)                                                     \
-  if constexpr (2 * (SEL) < D / 16) {                                        \
-    put(2 * (SEL), cvt_fp4<SEL>(lo[0]) * sc[0], cvt_fp4<SEL>(lo[1]) * sc[1]); \
-    put(2 * (SEL) + 1, cvt_fp4<SEL>(hi[0]) * sc[0], cvt_fp4<SEL>(hi[1]) * sc[1]); \
-  }
-          NVFP4_VROWS(0)
-          NVFP4_VROWS(1)
-          NVFP4_VROWS(2)
-          NVFP4_VROWS(3)
-#undef NVFP4_VROWS
-        }
-      }
+    uint32_t rk[KD] = {}, rv[KD] = {}, ksc = 0, vsc = 0;
+    auto load_k = [&](int32_t s, int32_t id) {
+      const uint8_t* p = granule(s, id);
+      load_dwords<KD>(p + lane * (D / 8), rk);
+      p += 8 * D + lane * (D / 64);
+      if constexpr (D == 64) ksc = *p;
+      else if constexpr (D == 128) ksc = *reinterpret_cast<const uint16_t*>(p);
+      else ksc = *reinterpret_cast<const uint32_t*>(p);
     };
+    auto load_v = [&](int32_t s, int32_t id) {
+      const uint8_t* p = granule(s, id);
+      load_dwords<KD>(p + 9 * D + lane * (D / 8), rv);
+      vsc = *reinterpret_cast<const uint32_t*>(p + 17 * D + ((lane >> 4) * (D / 16) + (lane & 15) * D / 256) * 4);
+      // scales of tokens past the end are cleared: their bytes may be NaN
+      const int32_t left = seq.n - (begin + s * TOK + 16 * gran + 4 * (lane >> 4));
+      if (left < 4) vsc = left <= 0 ? 0u : vsc & ((1u << (8 * left)) - 1u);
+    };
+    // decode dword i of the loaded keys: a 16-byte chunk of a token's row
+    auto decode_k = [&](uint32_t kb, int i) {               // kb: the lane's first chunk in the tile
+      const f16x2 sc = bcast(scale_pair_f16(D == 256 ? ksc >> (16 * (i / 4)) : ksc), D == 64 ? 0 : (i >> 1) & 1);
+      lds_at<f16x8>(kb ^ (i << 4)) = decode8_f16(rk[i], sc);
+    };
+    // decode byte i of the four tokens' words of the loaded values: elements 2 i and 2 i + 1
+    auto decode_v = [&](uint32_t vb, int i) {               // vb: the lane's first element in the tile
+      f16x2 sc[2];
+      sc[0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(vsc, 1.0f, false);
+      sc[1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(vsc, 1.0f, true);
+      uint32_t w[4], lo[2], hi[2];
+      value_words<D>(rv, i / 4, w);
+      pair_tokens(w, lo, hi);
+      typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+      auto put = [&](int j, f16x2 x, f16x2 y) {
+        lds_at<f16x4>((vb ^ ((D == 256 ? j >> 1 : j) << 4)) + j * 2 * TOK) = f16x4{x[0], x[1], y[0], y[1]};
+      };
+      auto two = [&](auto sel) {
+        constexpr int SEL = decltype(sel)::value;
+        put(2 * i, cvt_fp4<SEL>(lo[0]) * sc[0], cvt_fp4<SEL>(lo[1]) * sc[1]);
+        put(2 * i + 1, cvt_fp4<SEL>(hi[0]) * sc[0], cvt_fp4<SEL>(hi[1]) * sc[1]);
+      };
+      if (i % 4 == 0) two(std::integral_constant<int, 0>{});
+      else if (i % 4 == 1) two(std::integral_constant<int, 1>{});
+      else if (i % 4 == 2) two(std::integral_constant<int, 2>{});
+      else two(std::integral_constant<int, 3>{});
+    };
+    const int kwbase = k_place<D>(16 * gran + lane / 4, (lane % 4) * KD);
+    const int vwbase = v_place<D>((lane & 15) * (D / 16), 2 * gran + ((lane >> 4) & 1)) + (lane >> 5) * 8;
 
     int32_t id_next = 0;
     __syncthreads();                               // the tile before is done with LDS
     if (steps > 0) {
-      load(0, page_of(0));
+      const int32_t id = page_of(0);
+      load_k(0, id);
+      load_v(0, id);
       id_next = page_of(1);
     }
 
     // query columns: B operand of K step k: elements 16 k + 8 h + j of column c32
     f16x8 qf[KS];
+    int32_t col = col0 + c32;
+    col = col < col_end ? col : col_end - 1;
+    const int32_t qi = col / group;
+    const int head = kh * group + (col - qi * group);
     float amax = 0.0f;
     {
-      float v[KS][8];
-      const int64_t off = (seq.q0 + qi) * a.ldq + (int64_t)head * D + 8 * h;
+      u32x4 raw[KS];
+      const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + (seq.q0 + qi) * a.ldq + (int64_t)head * D + 8 * h;
 #pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        load8<false>(a.q, off + 16 * k, v[k]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) amax = __builtin_fmaxf(amax, __builtin_fabsf(v[k][e]));
-      }
-      amax = __builtin_fmaxf(amax, xor32(amax));
-      const float up = query_up(amax);
+      for (int k = 0; k < KS; ++k) raw[k] = *reinterpret_cast<const u32x4*>(src + 16 * k);
 #pragma unroll
       for (int k = 0; k < KS; ++k)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) qf[k][e] = (_Float16)(v[k][e] * up);
+        for (int e = 0; e < 4; ++e) {
+          amax = __builtin_fmaxf(amax, __builtin_fabsf(__uint_as_float(raw[k][e] << 16)));
+          amax = __builtin_fmaxf(amax, __builtin_fabsf(__uint_as_float(raw[k][e] & 0xFFFF0000u)));
+        }
+      amax = max_halves(amax);
+      const float up = a.scale < 0.0f ? -query_up(amax) : query_up(amax);
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const f16x2 x = to_f16(__uint_as_float(raw[k][e] << 16) * up, __uint_as_float(raw[k][e] & 0xFFFF0000u) * up);
+          qf[k][2 * e] = x[0];
+          qf[k][2 * e + 1] = x[1];
+        }
     }
-    const float csc = a.scale * kLog2e * kg * query_down(amax);
+    // positive, so that a mask of -inf stays one and the largest product is the largest score
+    const float csc = __builtin_fmaxf(__builtin_fabsf(a.scale) * kLog2e * kg * query_down(amax), 0x1p-120f);
     const int32_t pos = seq.n - seq.m + qi;
     const int32_t limit = pos + 1, floor_ = a.window ? pos - a.window + 1 : 0;
     float m = kNegBig, l = 0.0f;
     f32x16 acc[NB];
 #pragma unroll
-    for (int i = 0; i < NB; ++i)
+    for (int i = 0; i < NB; ++i) acc[i] = zeros16();
+
+    // The parts of a block of 32 tokens, cut into KS pieces that the pipeline deals out: piece
+    // i of the scores is K step i, piece i of the output one value operand, both read from LDS
+    // PF pieces ahead.
+    constexpr int PF = D == 256 ? 1 : 3;
+    f16x8 kf[PF + 1], vf[PF + 1];
+    const int kbase = k_place<D>(c32, h), vbase = v_place<D>(c32, h);
+    auto read_k = [&](uint32_t kb, int b, int i) {          // kb: kbase in the tile
+      constexpr int M = kKMask<D>;
+      kf[i % (PF + 1)] = lds_at<f16x8>((kb ^ ((2 * i & M) << 4)) + 64 * D * b + ((2 * i & ~M) << 4));
+    };
+    auto read_v = [&](uint32_t vb, int b, int i) {
+      const int blk = i % NB, c = 2 * (2 * b + i / NB);
+      vf[i % (PF + 1)] = lds_at<f16x8>((vb ^ ((c ^ v_swizzle<D>(32 * blk)) << 4)) + 64 * TOK * blk);
+    };
+    auto score_piece = [&](f32x16& sc, int i) { sc = mfma32(kf[i % (PF + 1)], qf[i], sc); };
+    auto output_piece = [&](const f16x8 p[2], int i) { acc[i % NB] = mfma32(vf[i % (PF + 1)], p[i / NB], acc[i % NB]); };
+    // moves the reference M for the block from token t0 on; returns what the earlier sums are
+    // scaled by
+    auto reference = [&](int32_t t0, f32x16& sc) {
+      if (t0 < sp.all_lo || t0 + 32 > sp.all_hi) {
+        const int32_t upto = limit - t0 - 4 * h, from = floor_ - t0 - 4 * h;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][e] = 0.0f;
+        for (int e = 0; e < 16; ++e) {
+          const int32_t t = 8 * (e / 4) + e % 4;
+          if (t >= upto || t < from) sc[e] = -__builtin_inff();
+        }
+      }
+      const float top = max_halves(max16(sc)) * csc;
+      const float m1 = top > m + 15.0f ? __builtin_fmaxf(m, top - 7.0f) : m;
+      const float f = __builtin_amdgcn_exp2f(m - m1);
+      l *= f;
+      m = m1;
+      return f;
+    };
+    // weights of scores 2 i and 2 i + 1
+    auto weight_pair = [&](const f32x16& sc, f16x8 p[2], int i) {
+      const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[2 * i], csc, -m));
+      const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[2 * i + 1], csc, -m));
+      l += x + y;
+      const f16x2 w = to_f16(x, y);
+      p[i / 4][2 * (i % 4)] = w[0];
+      p[i / 4][2 * (i % 4) + 1] = w[1];
+    };
+    auto rescale = [&](float f) {
+      if (__builtin_amdgcn_ballot_w64(f != 1.0f)) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i) acc[i] *= f;
+      }
+    };
+    auto k_tile = [&](int32_t s) { return lds + (uint32_t)((s & 1) * TILE); };
+    auto v_tile = [&](int32_t s) { return lds + (uint32_t)(2 * TILE + (s & 1) * TILE); };
+    // an address that the compiler does not take out of the loop: with every chunk's address
+    // in a register of its own the kernel spills
+    auto fresh = [](uint32_t x) {
+      asm volatile("" : "+v"(x));
+      return x;
+    };
 
     if (steps > 0) {
-      decode(0);
+      if (D != 256 || wave < 4) {
+#pragma unroll
+        for (int i = 0; i < KD; ++i) decode_k(k_tile(0) + kwbase, i);
+      }
+      if (D != 256 || wave >= 4) {
+#pragma unroll
+        for (int i = 0; i < KS / 2; ++i) decode_v(v_tile(0) + vwbase, i);
+      }
       if (steps > 1) {
-        load(1, id_next);
+        load_k(1, id_next);
+        load_v(1, id_next);
         id_next = page_of(2);
       }
-      __syncthreads();
-    }
-    for (int32_t s = 0; s < steps; ++s) {
-      if (s + 1 < steps) {
-        decode(s + 1);
-        if (s + 2 < steps) {
-          load(s + 2, id_next);
-          id_next = page_of(s + 3);
-        }
+      if constexpr (PIPE) {
+        // the values "before" tile 0 meet weights of zero: they must not be NaN
+#pragma unroll
+        for (int i = 0; i < TILE / (16 * 64 * kPrefillWaves); ++i)
+          lds_at<u32x4>(v_tile(1) + (i * 64 * kPrefillWaves + threadIdx.x) * 16) = u32x4{0, 0, 0, 0};
       }
-      const int32_t t0 = begin + s * kTok;
-      if (live && t0 < sp.hi && t0 + kTok > sp.lo) {
-        const uint8_t* kb = lds + (s & 1) * BUF;
-        const uint8_t* vb = kb + KBYTES;
+      __syncthreads();
+      if constexpr (PIPE) {
+        // one stage: scores of a block (kb, bk) into `next`, the weights of the block before it
+        // (scores `now`, from token t0 on) into `w`, the output of the one before that (vb, bv;
+        // weights `old`); pieces of the next tile's decoding in between
+        auto stage = [&](uint32_t kt, int bk, uint32_t vt, int bv, int32_t t0, f32x16& next, f32x16& now,
+                         f16x8 (&w)[2], const f16x8 (&old)[2], auto decode_piece) {
+          float f = 1.0f;
+          const uint32_t kb = fresh(kbase + kt), vb = fresh(vbase + vt);
+          next = zeros16();
 #pragma unroll
-        for (int pass = 0; pass < 2 / SB; ++pass) {
-        f32x16 sc[SB];
-#pragma unroll
-        for (int i = 0; i < SB; ++i)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) sc[i][e] = 0.0f;
-#pragma unroll
-        for (int k = 0; k < KS; ++k)
-#pragma unroll
-          for (int i = 0; i < SB; ++i) {
-            const f16x8 kf = *reinterpret_cast<const f16x8*>(kb + k_place<D>(32 * (SB * pass + i) + c32, 2 * k + h));
-            sc[i] = mfma32(kf, qf[k], sc[i]);
+          for (int i = 0; i < PF; ++i) {
+            read_k(kb, bk, i);
+            read_v(vb, bv, i);
           }
 #pragma unroll
-        for (int i = 0; i < SB; ++i) sc[i] *= csc;
-        if (t0 < sp.all_lo || t0 + kTok > sp.all_hi) {
-#pragma unroll
-          for (int i = 0; i < SB; ++i)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int32_t t = t0 + 32 * (SB * pass + i) + 8 * (e / 4) + 4 * h + e % 4;
-              if (t >= limit || t < floor_) sc[i][e] = -__builtin_inff();
+          for (int i = 0; i < KS; ++i) {
+            __builtin_amdgcn_sched_barrier(0);
+            if (i + PF < KS) {
+              read_k(kb, bk, i + PF);
+              read_v(vb, bv, i + PF);
             }
+            score_piece(next, i);
+            output_piece(old, i);
+            if (i == 0) f = reference(t0, now);
+            // 8 pairs over the pieces after the first
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              if (x >= (i - 1) * 8 / (KS - 1) && x < i * 8 / (KS - 1)) weight_pair(now, w, x);
+            decode_piece(i);
+          }
+          // the weights and their sum are due here, not where they are used
+          asm volatile("" : "+v"(w[0]), "+v"(w[1]), "+v"(l));
+          __builtin_amdgcn_sched_barrier(0);
+          rescale(f);
+        };
+        auto nothing = [](int) {};
+        f32x16 sa = zeros16(), sb;
+        f16x8 pa[2], pb[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) pb[k][e] = (_Float16)0.0f;
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+          read_k(k_tile(0) + kbase, 0, i);
+          score_piece(sa, i);
         }
-        float top = -__builtin_inff();
-#pragma unroll
-        for (int i = 0; i < SB; ++i)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) top = __builtin_fmaxf(top, sc[i][e]);
-        top = __builtin_fmaxf(top, xor32(top));
-        if (__builtin_amdgcn_ballot_w64(top > m + 15.0f)) {
-          const float m1 = __builtin_fmaxf(m, top - 7.0f);
-          const float f = __builtin_amdgcn_exp2f(m - m1);
-          m = m1;
-          l *= f;
-#pragma unroll
-          for (int i = 0; i < NB; ++i) acc[i] *= f;
+        // Past the last tile the decoder writes, from stale registers, what nothing reads unmasked.
+        // The next keys are written after the reads of the tile before them and are due after the
+        // second barrier, the next values after the second and due after the first.
+        for (int32_t s = 0; s < steps; ++s) {
+          const int32_t t0 = begin + s * TOK;
+          stage(k_tile(s), 1, v_tile(s + 1), 3, t0, sb, sa, pa, pb, nothing);
+          __syncthreads();
+          const uint32_t kw = fresh(k_tile(s + 1) + kwbase);
+          stage(k_tile(s), 2, v_tile(s), 0, t0 + 32, sa, sb, pb, pa, [&](int i) {
+            if (i < KD) decode_k(kw, i);
+          });
+          if (s + 2 < steps) load_k(s + 2, id_next);
+          stage(k_tile(s), 3, v_tile(s), 1, t0 + 64, sb, sa, pa, pb, nothing);
+          __syncthreads();
+          const uint32_t vw = fresh(v_tile(s + 1) + vwbase);
+          stage(k_tile(s + 1), 0, v_tile(s), 2, t0 + 96, sa, sb, pb, pa, [&](int i) {
+            if (i < KS / 2) decode_v(vw, i);
+          });
+          if (s + 2 < steps) {
+            load_v(s + 2, id_next);
+            id_next = page_of(s + 3);
+          }
         }
-        f16x8 pf[2 * SB];
 #pragma unroll
-        for (int i = 0; i < SB; ++i)
+        for (int i = 0; i < KS; ++i) {
+          read_v(v_tile(steps - 1) + vbase, 3, i);
+          output_piece(pb, i);
+        }
+      } else {
+        for (int32_t s = 0; s < steps; ++s) {
+          const uint32_t kw = fresh(k_tile(s + 1) + kwbase), vw = fresh(v_tile(s + 1) + vwbase);
+          if (wave < 4) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float p = __builtin_amdgcn_exp2f(sc[i][e] - m);
-            l += p;
-            pf[2 * i + e / 8][e % 8] = (_Float16)p;
+            for (int i = 0; i < KD; ++i) decode_k(kw, i);
+          } else {
+#pragma unroll
+            for (int i = 0; i < KS / 2; ++i) decode_v(vw, i);
+          }
+          if (s + 2 < steps) {
+            if (wave < 4) load_k(s + 2, id_next);
+            else load_v(s + 2, id_next);
+            id_next = page_of(s + 3);
           }
 #pragma unroll
-        for (int k = 0; k < 2 * SB; ++k)
+          for (int b = 0; b < 2; ++b) {
+            f32x16 sc = zeros16();
+            f16x8 w[2];
+            const uint32_t kb = fresh(k_tile(s) + kbase), vb = fresh(v_tile(s) + vbase);
+            read_k(kb, b, 0);
 #pragma unroll
-          for (int i = 0; i < NB; ++i) {
-            const f16x8 vf = *reinterpret_cast<const f16x8*>(vb + v_place(32 * i + c32, 2 * (2 * SB * pass + k) + h));
-            acc[i] = mfma32(vf, pf[k], acc[i]);
+            for (int i = 0; i < KS; ++i) {
+              if (i + 1 < KS) read_k(kb, b, i + 1);
+              score_piece(sc, i);
+              __builtin_amdgcn_sched_barrier(0);
+            }
+            rescale(reference(begin + s * TOK + 32 * b, sc));
+            read_v(vb, b, 0);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) weight_pair(sc, w, x);
+            asm volatile("" : "+v"(w[0]), "+v"(w[1]), "+v"(l));
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < KS; ++i) {
+              if (i + 1 < KS) read_v(vb, b, i + 1);
+              output_piece(w, i);
+              __builtin_amdgcn_sched_barrier(0);
+            }
           }
+          __syncthreads();
         }
       }
-      __syncthreads();
     }
 
     l += xor32(l);
@@ -280,7 +446,7 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
 
 template <int D>
 hipError_t launch(const KvAttnArgs& a, hipStream_t s) {
-  constexpr int bytes = 2 * 2 * kTok * D * 2;
+  constexpr int bytes = 4 * kTok<D> * D * 2;          // two tiles of keys, two of values
   const hipError_t e = lds_limit_once<k_kv_prefill<D>>(bytes);
   if (e != hipSuccess) return e;
   const int64_t blocks = (int64_t)a.batch * a.geom.n_kv_heads * a.col_tiles;
