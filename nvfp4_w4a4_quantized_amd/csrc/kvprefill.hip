@@ -134,7 +134,10 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
       return a.cache + (int64_t)id * a.geom.page_bytes +
              (int64_t)(kh * per_head + (gr & (per_head - 1))) * kv_granule_bytes(D);
     };
-    uint32_t rk[KD] = {}, rv[KD] = {}, ksc = 0, vsc = 0;
+    // (D = 256: a wave holds either)
+    uint32_t rk[KD] = {}, rv_[D == 256 ? 1 : KD] = {}, ksc = 0, vsc_ = 0;
+    uint32_t* const rv = D == 256 ? rk : rv_;
+    uint32_t& vsc = D == 256 ? ksc : vsc_;
     auto load_k = [&](int32_t s, int32_t id) {
       const uint8_t* p = granule(s, id);
       load_dwords<KD>(p + lane * (D / 8), rk);
@@ -185,8 +188,8 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
     __syncthreads();                               // the tile before is done with LDS
     if (steps > 0) {
       const int32_t id = page_of(0);
-      load_k(0, id);
-      load_v(0, id);
+      if (D != 256 || wave < 4) load_k(0, id);
+      if (D != 256 || wave >= 4) load_v(0, id);
       id_next = page_of(1);
     }
 
@@ -232,8 +235,9 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
     // The parts of a block of 32 tokens, cut into KS pieces that the pipeline deals out: piece
     // i of the scores is K step i, piece i of the output one value operand, both read from LDS
     // PF pieces ahead.
-    constexpr int PF = D == 256 ? 1 : 3;
-    f16x8 kf[PF + 1], vf[PF + 1];
+    constexpr int PF = D == 256 ? 2 : 3;
+    f16x8 kf[PF + 1], vf_[D == 256 ? 1 : PF + 1];
+    f16x8* const vf = D == 256 ? kf : vf_;           // one at a time there
     const int kbase = k_place<D>(c32, h), vbase = v_place<D>(c32, h);
     auto read_k = [&](uint32_t kb, int b, int i) {          // kb: kbase in the tile
       constexpr int M = kKMask<D>;
@@ -297,8 +301,8 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
         for (int i = 0; i < KS / 2; ++i) decode_v(v_tile(0) + vwbase, i);
       }
       if (steps > 1) {
-        load_k(1, id_next);
-        load_v(1, id_next);
+        if (D != 256 || wave < 4) load_k(1, id_next);
+        if (D != 256 || wave >= 4) load_v(1, id_next);
         id_next = page_of(2);
       }
       if constexpr (PIPE) {
@@ -403,25 +407,30 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
             f32x16 sc = zeros16();
             f16x8 w[2];
             const uint32_t kb = fresh(k_tile(s) + kbase), vb = fresh(v_tile(s) + vbase);
-            read_k(kb, b, 0);
+#pragma unroll
+            for (int i = 0; i < PF; ++i) read_k(kb, b, i);
 #pragma unroll
             for (int i = 0; i < KS; ++i) {
-              if (i + 1 < KS) read_k(kb, b, i + 1);
-              score_piece(sc, i);
               __builtin_amdgcn_sched_barrier(0);
+              if (i + PF < KS) read_k(kb, b, i + PF);
+              score_piece(sc, i);
             }
-            rescale(reference(begin + s * TOK + 32 * b, sc));
-            read_v(vb, b, 0);
+            __builtin_amdgcn_sched_barrier(0);
+            const float f = reference(begin + s * TOK + 32 * b, sc);
 #pragma unroll
             for (int x = 0; x < 8; ++x) weight_pair(sc, w, x);
             asm volatile("" : "+v"(w[0]), "+v"(w[1]), "+v"(l));
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
+            for (int i = 0; i < PF; ++i) read_v(vb, b, i);
+            rescale(f);
+#pragma unroll
             for (int i = 0; i < KS; ++i) {
-              if (i + 1 < KS) read_v(vb, b, i + 1);
-              output_piece(w, i);
               __builtin_amdgcn_sched_barrier(0);
+              if (i + PF < KS) read_v(vb, b, i + PF);
+              output_piece(w, i);
             }
+            __builtin_amdgcn_sched_barrier(0);
           }
           __syncthreads();
         }
