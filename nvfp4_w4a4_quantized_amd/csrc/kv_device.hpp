@@ -10,8 +10,36 @@ namespace {
 constexpr float kNegBig = -1.0e30f;      // reference M of a row that has seen nothing
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-__device__ __forceinline__ float xor16(float x) { return __shfl_xor(x, 16); }
-__device__ __forceinline__ float xor32(float x) { return __shfl_xor(x, 32); }
+// Joined with the lane 32 (16) away, by a swap of the halves (of the rows of 16) with itself
+__device__ __forceinline__ float max_xor32(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __builtin_fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float max_xor16(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __builtin_fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float sum_xor32(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float sum_xor16(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// Largest of N MFMA results (N even), by v_max3_f32 (fmaxf gets a canonicalizing max per
+// value).  The compiler does not count the wait states between an MFMA and an asm that reads
+// its result, so an ordinary max of the first and the last value comes first: when the last
+// MFMA's result may be read, those of the ones before it may.
+template <int N>
+__device__ __forceinline__ float max_of(const float* x) {
+  static_assert(N % 2 == 0, "pairs");
+  float m = __builtin_fmaxf(x[0], x[N - 1]);
+#pragma unroll
+  for (int i = 1; i + 1 < N; i += 2) asm("v_max3_f32 %0, %0, %1, %2" : "+v"(m) : "v"(x[i]), "v"(x[i + 1]));
+  return m;
+}
 
 // Two fp32 -> two f16, round to nearest even
 __device__ __forceinline__ f16x2 to_f16(float a, float b) { return f16x2{(_Float16)a, (_Float16)b}; }
@@ -25,8 +53,12 @@ __device__ __forceinline__ int query_exponent(float amax) {
 __device__ __forceinline__ float query_up(float amax) {
   return __uint_as_float((uint32_t)(14 - query_exponent(amax) + 127) << 23);
 }
-__device__ __forceinline__ float query_down(float amax) {
-  return __uint_as_float((uint32_t)(query_exponent(amax) - 14 + 127) << 23);
+// What a product of the scaled query (negated where the scale is negative) and a stored key
+// counts in a base-2 exponent: positive, so that the largest product is the largest score and
+// a product masked with -inf stays masked.
+__device__ __forceinline__ float score_factor(float scale, float kg, float amax) {
+  const float down = __uint_as_float((uint32_t)(query_exponent(amax) - 14 + 127) << 23);
+  return __builtin_fmaxf(__builtin_fabsf(scale) * kLog2e * kg * down, 0x1p-120f);
 }
 
 // What a workgroup needs of its sequence
@@ -69,16 +101,29 @@ __device__ __forceinline__ Span span_of(const SeqInfo& s, int32_t col0, int32_t 
   return r;
 }
 
+__device__ __forceinline__ int64_t uniform64(int64_t x) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)x), hi = __builtin_amdgcn_readfirstlane((uint32_t)(x >> 32));
+  return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+
+// A granule as a buffer: its address in scalar registers, the lanes' 32-bit offsets in one
+// register each for all granules.
+template <int D>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t granule_buffer(const KvAttnArgs& a, int32_t page, int32_t in_page) {
+  const uint8_t* p = a.cache + uniform64((int64_t)page * a.geom.page_bytes + (int64_t)in_page * kv_granule_bytes(D));
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), (short)0, kv_granule_bytes(D), 0x00020000);
+}
+
 template <int N>
-__device__ __forceinline__ void load_dwords(const uint8_t* p, uint32_t* d) {
+__device__ __forceinline__ void load_dwords(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t* d) {
   if constexpr (N == 2) {
-    const u32x2 x = *reinterpret_cast<const u32x2*>(p);
+    const auto x = __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0);
     d[0] = x[0];
     d[1] = x[1];
   } else {
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
-      const u32x4 x = *reinterpret_cast<const u32x4*>(p + 4 * i);
+      const auto x = __builtin_amdgcn_raw_buffer_load_b128(r, off + 4 * i, 0, 0);
 #pragma unroll
       for (int e = 0; e < 4; ++e) d[i + e] = x[e];
     }

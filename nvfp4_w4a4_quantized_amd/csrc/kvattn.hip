@@ -32,11 +32,6 @@ namespace {
 
 constexpr int kMaxWorkers = 512;         // two workgroups per compute unit
 
-__device__ __forceinline__ int64_t uniform64(int64_t x) {
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)x), hi = __builtin_amdgcn_readfirstlane((uint32_t)(x >> 32));
-  return (int64_t)(((uint64_t)hi << 32) | lo);
-}
-
 // One granule as a lane of the 16-row MFMAs holds it.
 template <int D>
 struct Granule {
@@ -48,22 +43,22 @@ struct Granule {
 // Keys: lane (g, r) holds token r, elements 32 g + 8 m + j (D = 128), 128 c + 32 g + 8 m + j
 // (D = 256), 16 g + 8 m + j (D = 64); values: tokens 4 g + e, elements (D / 16) r + j.
 template <int D>
-__device__ __forceinline__ void load_granule(const uint8_t* p, int lane, Granule<D>& x) {
-  const int g = lane >> 4, r = lane & 15;
+__device__ __forceinline__ void load_granule(__amdgpu_buffer_rsrc_t p, uint32_t lane, Granule<D>& x) {
+  const uint32_t g = lane >> 4, r = lane & 15;
   if constexpr (D == 64) {
-    load_dwords<2>(p + r * 32 + g * 8, x.k);
-    x.ks[0] = p[8 * D + r * 4 + g];
+    load_dwords<2>(p, r * 32 + g * 8, x.k);
+    x.ks[0] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(p, r * 4 + g, 8 * D, 0);
   } else if constexpr (D == 128) {
-    load_dwords<4>(p + r * 64 + g * 16, x.k);
-    x.ks[0] = *reinterpret_cast<const uint16_t*>(p + 8 * D + r * 8 + 2 * g);
+    load_dwords<4>(p, r * 64 + g * 16, x.k);
+    x.ks[0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(p, r * 8 + 2 * g, 8 * D, 0);
   } else {
-    load_dwords<4>(p + r * 128 + g * 16, x.k);
-    load_dwords<4>(p + r * 128 + 64 + g * 16, x.k + 4);
-    x.ks[0] = *reinterpret_cast<const uint16_t*>(p + 8 * D + r * 16 + 2 * g);
-    x.ks[1] = *reinterpret_cast<const uint16_t*>(p + 8 * D + r * 16 + 8 + 2 * g);
+    load_dwords<4>(p, r * 128 + g * 16, x.k);
+    load_dwords<4>(p, r * 128 + g * 16 + 64, x.k + 4);
+    x.ks[0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(p, r * 16 + 2 * g, 8 * D, 0);
+    x.ks[1] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(p, r * 16 + 2 * g + 8, 8 * D, 0);
   }
-  load_dwords<D / 32>(p + 9 * D + (g * 16 + r) * (D / 8), x.v);
-  x.vs = *reinterpret_cast<const uint32_t*>(p + 17 * D + (g * (D / 16) + r * D / 256) * 4);
+  load_dwords<D / 32>(p, lane * (D / 8) + 9 * D, x.v);
+  x.vs = __builtin_amdgcn_raw_buffer_load_b32(p, (g * (D / 16) + r * D / 256) * 4, 17 * D, 0);
 }
 
 // A operand of key chunk i (8 elements of token r): codes k[i] under their block's scale
@@ -258,10 +253,9 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) amax = __builtin_fmaxf(amax, __builtin_fabsf(v[c][e]));
       }
-      amax = __builtin_fmaxf(amax, xor16(amax));
-      amax = __builtin_fmaxf(amax, xor32(amax));
-      const float up = query_up(amax);
-      csc[n] = a.scale * kLog2e * kg * query_down(amax);
+      amax = max_xor32(max_xor16(amax));
+      const float up = a.scale < 0.0f ? -query_up(amax) : query_up(amax);
+      csc[n] = score_factor(a.scale, kg, amax);
 #pragma unroll
       for (int c = 0; c < KC; ++c)
 #pragma unroll
@@ -298,9 +292,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
           const int32_t id = __builtin_amdgcn_readlane(pages, i * NG + u);
           int32_t gr = (begin + s * TOK) / 16 + u;
           gr = gr < last_granule ? gr : last_granule;   // past the end: the last granule again
-          const uint8_t* p = a.cache + (int64_t)id * a.geom.page_bytes +
-                             (int64_t)(kh * per_head + (gr & (per_head - 1))) * kv_granule_bytes(D);
-          load_granule<D>(p, lane, x[u]);
+          load_granule<D>(granule_buffer<D>(a, id, kh * per_head + (gr & (per_head - 1))), lane, x[u]);
         }
         if (i == SPB - 1) {
           pages = pages_next;
@@ -337,26 +329,15 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
         f16x8 pf[TERMS][NQ][NG / 2];
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
-          float x[NG][4], top = -__builtin_inff();
-#pragma unroll
-          for (int u = 0; u < NG; ++u)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[u][i] = sc[n][u][i] * csc[n];
           if (edge) {
+            const int32_t upto = limit[n] - t0 - 4 * g, from = floor_[n] - t0 - 4 * g;
 #pragma unroll
             for (int u = 0; u < NG; ++u)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int32_t t = t0 + 16 * u + 4 * g + i;
-                if (t >= limit[n] || t < floor_[n]) x[u][i] = -__builtin_inff();
-              }
+              for (int i = 0; i < 4; ++i)
+                if (16 * u + i >= upto || 16 * u + i < from) sc[n][u][i] = -__builtin_inff();
           }
-#pragma unroll
-          for (int u = 0; u < NG; ++u)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) top = __builtin_fmaxf(top, x[u][i]);
-          top = __builtin_fmaxf(top, xor16(top));
-          top = __builtin_fmaxf(top, xor32(top));
+          const float top = max_xor32(max_xor16(max_of<4 * NG>(reinterpret_cast<const float*>(&sc[n][0])))) * csc[n];
           if (__builtin_amdgcn_ballot_w64(top > m[n] + 15.0f)) {
             const float m1 = __builtin_fmaxf(m[n], top - 7.0f);
             const float f = __builtin_amdgcn_exp2f(m[n] - m1);
@@ -365,22 +346,21 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
 #pragma unroll
             for (int j = 0; j < NJ; ++j) acc[n][j] *= f;
           }
-          float p[NG][4];
-#pragma unroll
-          for (int u = 0; u < NG; ++u)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              p[u][i] = __builtin_amdgcn_exp2f(x[u][i] - m[n]);
-              l[n] += p[u][i];
-            }
 #pragma unroll
           for (int k = 0; k < NG / 2; ++k)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float v = p[2 * k + i / 4][i % 4];
-              const _Float16 hi = (_Float16)v;
-              pf[0][n][k][i] = hi;
-              if constexpr (F32) pf[TERMS - 1][n][k][i] = (_Float16)(v - (float)hi);
+            for (int i = 0; i < 8; i += 2) {
+              const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[n][2 * k + i / 4][i % 4], csc[n], -m[n]));
+              const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[n][2 * k + i / 4][i % 4 + 1], csc[n], -m[n]));
+              l[n] += x + y;
+              const f16x2 hi = to_f16(x, y);
+              pf[0][n][k][i] = hi[0];
+              pf[0][n][k][i + 1] = hi[1];
+              if constexpr (F32) {
+                const f16x2 lo = to_f16(x - (float)hi[0], y - (float)hi[1]);
+                pf[TERMS - 1][n][k][i] = lo[0];
+                pf[TERMS - 1][n][k][i + 1] = lo[1];
+              }
             }
         }
 
@@ -443,8 +423,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
     __syncthreads();                               // s_m, s_l, s_o of the work before are read
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-      l[n] += xor16(l[n]);
-      l[n] += xor32(l[n]);
+      l[n] = sum_xor32(sum_xor16(l[n]));
       if (g == 0) {
         s_m[wave][16 * n + r] = m[n];
         s_l[wave][16 * n + r] = l[n];

@@ -60,26 +60,11 @@ __device__ __forceinline__ __attribute__((address_space(3))) T& lds_at(uint32_t 
   return *reinterpret_cast<__attribute__((address_space(3))) T*>(at);
 }
 
-// x of the other half of the wave joined to this lane's by f
-__device__ __forceinline__ float max_halves(float x) {
-  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return __builtin_fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
-}
-
 __device__ __forceinline__ f32x16 zeros16() {
   f32x16 x;
 #pragma unroll
   for (int e = 0; e < 16; ++e) x[e] = 0.0f;
   return x;
-}
-
-__device__ __forceinline__ float max16(const f32x16& x) {
-  float m;
-  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(m) : "v"(x[0]), "v"(x[1]), "v"(x[2]));
-#pragma unroll
-  for (int i = 3; i + 1 < 16; i += 2) asm("v_max3_f32 %0, %0, %1, %2" : "+v"(m) : "v"(x[i]), "v"(x[i + 1]));
-  asm("v_max_f32 %0, %0, %1" : "+v"(m) : "v"(x[15]));
-  return m;
 }
 
 template <int D>
@@ -131,25 +116,23 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
     auto granule = [&](int32_t s, int32_t id) {
       int32_t gr = (begin + s * TOK) / 16 + gran;
       gr = gr < last_granule ? gr : last_granule;
-      return a.cache + (int64_t)id * a.geom.page_bytes +
-             (int64_t)(kh * per_head + (gr & (per_head - 1))) * kv_granule_bytes(D);
+      return granule_buffer<D>(a, id, kh * per_head + (gr & (per_head - 1)));
     };
     // (D = 256: a wave holds either)
     uint32_t rk[KD] = {}, rv_[D == 256 ? 1 : KD] = {}, ksc = 0, vsc_ = 0;
     uint32_t* const rv = D == 256 ? rk : rv_;
     uint32_t& vsc = D == 256 ? ksc : vsc_;
     auto load_k = [&](int32_t s, int32_t id) {
-      const uint8_t* p = granule(s, id);
-      load_dwords<KD>(p + lane * (D / 8), rk);
-      p += 8 * D + lane * (D / 64);
-      if constexpr (D == 64) ksc = *p;
-      else if constexpr (D == 128) ksc = *reinterpret_cast<const uint16_t*>(p);
-      else ksc = *reinterpret_cast<const uint32_t*>(p);
+      const __amdgpu_buffer_rsrc_t p = granule(s, id);
+      load_dwords<KD>(p, lane * (D / 8), rk);
+      if constexpr (D == 64) ksc = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(p, lane, 8 * D, 0);
+      else if constexpr (D == 128) ksc = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(p, lane * 2, 8 * D, 0);
+      else ksc = __builtin_amdgcn_raw_buffer_load_b32(p, lane * 4, 8 * D, 0);
     };
     auto load_v = [&](int32_t s, int32_t id) {
-      const uint8_t* p = granule(s, id);
-      load_dwords<KD>(p + 9 * D + lane * (D / 8), rv);
-      vsc = *reinterpret_cast<const uint32_t*>(p + 17 * D + ((lane >> 4) * (D / 16) + (lane & 15) * D / 256) * 4);
+      const __amdgpu_buffer_rsrc_t p = granule(s, id);
+      load_dwords<KD>(p, lane * (D / 8) + 9 * D, rv);
+      vsc = __builtin_amdgcn_raw_buffer_load_b32(p, ((lane >> 4) * (D / 16) + (lane & 15) * D / 256) * 4, 17 * D, 0);
       // scales of tokens past the end are cleared: their bytes may be NaN
       const int32_t left = seq.n - (begin + s * TOK + 16 * gran + 4 * (lane >> 4));
       if (left < 4) vsc = left <= 0 ? 0u : vsc & ((1u << (8 * left)) - 1u);
@@ -212,7 +195,7 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
           amax = __builtin_fmaxf(amax, __builtin_fabsf(__uint_as_float(raw[k][e] << 16)));
           amax = __builtin_fmaxf(amax, __builtin_fabsf(__uint_as_float(raw[k][e] & 0xFFFF0000u)));
         }
-      amax = max_halves(amax);
+      amax = max_xor32(amax);
       const float up = a.scale < 0.0f ? -query_up(amax) : query_up(amax);
 #pragma unroll
       for (int k = 0; k < KS; ++k)
@@ -223,8 +206,7 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
           qf[k][2 * e + 1] = x[1];
         }
     }
-    // positive, so that a mask of -inf stays one and the largest product is the largest score
-    const float csc = __builtin_fmaxf(__builtin_fabsf(a.scale) * kLog2e * kg * query_down(amax), 0x1p-120f);
+    const float csc = score_factor(a.scale, kg, amax);
     const int32_t pos = seq.n - seq.m + qi;
     const int32_t limit = pos + 1, floor_ = a.window ? pos - a.window + 1 : 0;
     float m = kNegBig, l = 0.0f;
@@ -260,7 +242,7 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
           if (t >= upto || t < from) sc[e] = -__builtin_inff();
         }
       }
-      const float top = max_halves(max16(sc)) * csc;
+      const float top = max_xor32(max_of<16>(reinterpret_cast<const float*>(&sc))) * csc;
       const float m1 = top > m + 15.0f ? __builtin_fmaxf(m, top - 7.0f) : m;
       const float f = __builtin_amdgcn_exp2f(m - m1);
       l *= f;
@@ -437,7 +419,7 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
       }
     }
 
-    l += xor32(l);
+    l = sum_xor32(l);
     if (col0 + c32 < col_end) {
       const float f = l > 0.0f ? vg / l : 0.0f;
       uint16_t* dst = reinterpret_cast<uint16_t*>(a.o) + (seq.q0 + qi) * a.ldo + (int64_t)head * D + 4 * h;
