@@ -672,7 +672,8 @@ int32_t nvfp4_kv_attention_workspace(int32_t dtype, int64_t T, int32_t batch, in
   if (!valid_dtype(dtype)) return fail(NVFP4_ERR_UNSUPPORTED, "dtype %d is not F32 or BF16", dtype);
   const int32_t st = check_kv_attn_sizes(T, batch, n_q_heads, n_kv_heads, head_dim, max_q_len, max_kv_len);
   if (st) return st;
-  *bytes_out = nvfp4::kv_attn_plan(in_type(dtype), T, batch, n_q_heads, n_kv_heads, head_dim, max_q_len, max_kv_len)
+  // a window never needs more
+  *bytes_out = nvfp4::kv_attn_plan(in_type(dtype), T, batch, n_q_heads, n_kv_heads, head_dim, max_q_len, max_kv_len, 0)
                    .workspace;
   return ok();
 }
@@ -702,7 +703,7 @@ int32_t nvfp4_kv_attention(const void* q, int32_t dtype, int64_t ldq, int64_t T,
   if (!std::isfinite(scale)) return fail(NVFP4_ERR_INVALID_ARG, "scale is not finite");
   if (window < 0) return fail(NVFP4_ERR_INVALID_ARG, "window=%d must not be negative (0 = none)", window);
   const nvfp4::KvAttnPlan plan =
-      nvfp4::kv_attn_plan(in_type(dtype), T, batch, n_q_heads, n_kv_heads, head_dim, max_q_len, max_kv_len);
+      nvfp4::kv_attn_plan(in_type(dtype), T, batch, n_q_heads, n_kv_heads, head_dim, max_q_len, max_kv_len, window);
   if (plan.workspace > 0) {
     if (!workspace || workspace_bytes < plan.workspace)
       return fail(NVFP4_ERR_INVALID_ARG, "workspace of %lld bytes is too small: %lld needed",

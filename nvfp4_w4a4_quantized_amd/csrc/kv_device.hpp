@@ -28,16 +28,22 @@ __device__ __forceinline__ float sum_xor16(float x) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-// Largest of N MFMA results (N even), by v_max3_f32 (fmaxf gets a canonicalizing max per
-// value).  The compiler does not count the wait states between an MFMA and an asm that reads
-// its result, so an ordinary max of the first and the last value comes first: when the last
+// Largest of 16 or 8 MFMA results, by v_max3_f32 (fmaxf gets a canonicalizing max per value).
+// The compiler does not count the wait states between an MFMA and an asm that reads its
+// result, so an ordinary max of the first and the last value comes first: when the last
 // MFMA's result may be read, those of the ones before it may.
-template <int N>
-__device__ __forceinline__ float max_of(const float* x) {
-  static_assert(N % 2 == 0, "pairs");
-  float m = __builtin_fmaxf(x[0], x[N - 1]);
+__device__ __forceinline__ float max_of(const f32x16& x) {
+  float m = __builtin_fmaxf(x[0], x[15]);
 #pragma unroll
-  for (int i = 1; i + 1 < N; i += 2) asm("v_max3_f32 %0, %0, %1, %2" : "+v"(m) : "v"(x[i]), "v"(x[i + 1]));
+  for (int i = 1; i + 1 < 16; i += 2) asm("v_max3_f32 %0, %0, %1, %2" : "+v"(m) : "v"(x[i]), "v"(x[i + 1]));
+  return m;
+}
+template <int N>
+__device__ __forceinline__ float max_of(const f32x4 (&x)[N]) {
+  float m = __builtin_fmaxf(x[0][0], x[N - 1][3]);
+#pragma unroll
+  for (int i = 1; i + 1 < 4 * N; i += 2)
+    asm("v_max3_f32 %0, %0, %1, %2" : "+v"(m) : "v"(x[i / 4][i % 4]), "v"(x[(i + 1) / 4][(i + 1) % 4]));
   return m;
 }
 
@@ -63,7 +69,7 @@ __device__ __forceinline__ float score_factor(float scale, float kg, float amax)
 
 // What a workgroup needs of its sequence
 struct SeqInfo {
-  int64_t q0;              // first query token (row of q)
+  int32_t q0;              // first query token (row of q)
   int32_t m;               // query tokens
   int32_t n;               // cached tokens
 };
@@ -77,7 +83,7 @@ __device__ __forceinline__ SeqInfo seq_info(const KvAttnArgs& a, int b) {
   }
   q0 = q0 < 0 ? 0 : (q0 > a.T ? a.T : q0);
   q1 = q1 < q0 ? q0 : (q1 > a.T ? a.T : q1);
-  s.q0 = q0;
+  s.q0 = (int32_t)q0;
   s.m = (int32_t)(q1 - q0);
   const int64_t most = a.max_pages << a.geom.page_shift;
   const int64_t n = a.kv_len[b];
@@ -104,6 +110,57 @@ __device__ __forceinline__ Span span_of(const SeqInfo& s, int32_t col0, int32_t 
 __device__ __forceinline__ int64_t uniform64(int64_t x) {
   const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)x), hi = __builtin_amdgcn_readfirstlane((uint32_t)(x >> 32));
   return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+
+// The sequences of a call, one per lane where there are at most 64.
+struct SeqTable {
+  SeqInfo mine;
+  bool held;
+
+  __device__ __forceinline__ SeqTable(const KvAttnArgs& a, int lane) : mine{0, 0, 0}, held(a.batch <= 64) {
+    if (held && lane < a.batch) mine = seq_info(a, lane);
+  }
+  // sequence b (wave-uniform)
+  __device__ __forceinline__ SeqInfo at(const KvAttnArgs& a, int b) const {
+    if (!held) return seq_info(a, b);
+    SeqInfo s;
+    s.q0 = __builtin_amdgcn_readlane(mine.q0, b);
+    s.m = __builtin_amdgcn_readlane(mine.m, b);
+    s.n = __builtin_amdgcn_readlane(mine.n, b);
+    return s;
+  }
+};
+
+// `total` units dealt out to workers: each gets the same number, the first `rest` one more.
+struct Deal {
+  int64_t each, rest;
+
+  __device__ __forceinline__ Deal(int64_t total, int64_t workers) {
+    each = total >> 31 ? total / workers : (int64_t)((uint32_t)total / (uint32_t)workers);
+    rest = total - each * workers;
+  }
+  __device__ __forceinline__ int64_t first_of(int64_t w) const { return w * each + (w < rest ? w : rest); }
+  __device__ __forceinline__ int32_t worker_of(int64_t unit) const {
+    const int64_t longer = rest * (each + 1);
+    const int64_t x = unit < longer ? unit : unit - longer, y = unit < longer ? each + 1 : each;
+    const int32_t w = x >> 31 || y >> 31 ? (int32_t)(x / y) : (int32_t)((uint32_t)x / (uint32_t)y);
+    return unit < longer ? w : (int32_t)rest + w;
+  }
+};
+
+// What the first worker of an item done in pieces leaves for the join: the item's query
+// columns and who has the other pieces.  The pieces are in slot 1 of that worker and slot 0 of
+// those after it, up to `last`.
+struct alignas(16) ItemPieces {
+  int32_t cols;            // columns of the item; 0: this worker left none
+  int32_t last;
+  int32_t q0, first_col, kh, pad[3];
+};
+static_assert(sizeof(ItemPieces) == kItemPiecesBytes, "launch.hpp");
+
+// Partial results of column c: [maximum, sum, -, -, output D] floats
+__device__ __forceinline__ float* piece_at(const KvAttnArgs& a, int D, int32_t worker, int slot, int32_t c) {
+  return a.part + ((2 * (int64_t)worker + slot) * a.tile_cols + c) * (D + 4);
 }
 
 // A granule as a buffer: its address in scalar registers, the lanes' 32-bit offsets in one

@@ -97,9 +97,9 @@ struct SeqWork {
 };
 
 template <int TOK>
-__device__ __forceinline__ SeqWork seq_work(const KvAttnArgs& a, int b, int group) {
+__device__ __forceinline__ SeqWork seq_work(const KvAttnArgs& a, const SeqInfo& seq, int group) {
   SeqWork w;
-  w.seq = seq_info(a, b);
+  w.seq = seq;
   w.cols = w.seq.m * group;
   w.tiles = 0;
   w.begin = w.steps = 0;
@@ -138,10 +138,12 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
   int b;
   int64_t u = 0, u_end = 1, u_seq = 0;
   SeqWork sw;
+  Deal deal(1, 1);
+  const SeqTable seqs(a, lane);
   if (a.n_workers == 0) {
     const int item = blockIdx.x / a.col_tiles;
     b = item / hkv;
-    sw = seq_work<TOK>(a, b, group);
+    sw = seq_work<TOK>(a, seq_info(a, b), group);
     if ((int)(blockIdx.x % a.col_tiles) >= sw.tiles) return;
   } else {
     // each lane counts the steps of `each` consecutive sequences
@@ -150,7 +152,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
     for (int i = 0; i < each; ++i) {
       const int bb = lane * each + i;
       if (bb < a.batch) {
-        const SeqWork x = seq_work<TOK>(a, bb, group);
+        const SeqWork x = seq_work<TOK>(a, seqs.held ? seqs.mine : seq_info(a, bb), group);
         own += (int64_t)x.tiles * hkv * x.steps;
       }
     }
@@ -160,21 +162,20 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
       const int64_t x = __shfl_up(upto, off);
       if (lane >= off) upto += x;
     }
-    const int64_t total = __shfl(upto, 63);
+    const int64_t total = uniform64(__shfl(upto, 63));
     const int64_t workers = total < a.n_workers ? total : a.n_workers;   // none without a step
-    if (blockIdx.x >= workers) return;
-    u = total * blockIdx.x / workers;
-    u_end = total * (blockIdx.x + 1) / workers;
+    if (blockIdx.x >= workers) {
+      if (threadIdx.x == 0) static_cast<ItemPieces*>(a.pieces)[blockIdx.x].cols = 0;
+      return;
+    }
+    deal = Deal(total, workers);
+    u = deal.first_of(blockIdx.x);
+    u_end = deal.first_of(blockIdx.x + 1);
     const int first = __builtin_ctzll(__builtin_amdgcn_ballot_w64(upto > u));
-    u_seq = __shfl(upto - own, first);
+    u_seq = uniform64(__shfl(upto - own, first));
     b = first * each;
-    // wave-uniform from here on
-    u = uniform64(u);
-    u_end = uniform64(u_end);
-    u_seq = uniform64(u_seq);
-    b = __builtin_amdgcn_readfirstlane(b);
     for (;; ++b) {
-      sw = seq_work<TOK>(a, b, group);
+      sw = seq_work<TOK>(a, seqs.at(a, b), group);
       const int64_t n = (int64_t)sw.tiles * hkv * sw.steps;
       if (u < u_seq + n) break;
       u_seq += n;
@@ -193,21 +194,27 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
     } else {
       while (u >= u_seq + (int64_t)sw.tiles * hkv * sw.steps) {
         u_seq += (int64_t)sw.tiles * hkv * sw.steps;
-        sw = seq_work<TOK>(a, ++b, group);
+        sw = seq_work<TOK>(a, seqs.at(a, ++b), group);
       }
-      const int32_t item = (int32_t)((u - u_seq) / sw.steps);
+      const int64_t in_seq = u - u_seq;
+      const int32_t item =
+          in_seq >> 31 ? (int32_t)(in_seq / sw.steps) : (int32_t)((uint32_t)in_seq / (uint32_t)sw.steps);
       tile0 = item % sw.tiles;
       kh = item / sw.tiles;
-      s_first = (int32_t)(u - u_seq - (int64_t)item * sw.steps);
+      s_first = (int32_t)(in_seq - (int64_t)item * sw.steps);
       const int64_t left = u_end - u;
       s_last = left < sw.steps - s_first ? s_first + (int32_t)left : sw.steps;
-      u += s_last - s_first;
-      // where the pieces of the item are
-      if (threadIdx.x == 0) {
-        int32_t* where = a.pieces + 2 * (((int64_t)b * hkv + kh) * a.col_tiles + tile0);
-        if (s_first == 0) where[0] = s_last == sw.steps ? -1 : (int32_t)blockIdx.x;
-        if (s_last == sw.steps && s_first > 0) where[1] = (int32_t)blockIdx.x;
+      const bool begun = s_first == 0 && s_last < sw.steps;
+      if (threadIdx.x == 0 && (begun || u + (s_last - s_first) >= u_end)) {
+        const int32_t fc = tile0 * a.tile_cols, rest = sw.cols - fc;
+        ItemPieces* const p = static_cast<ItemPieces*>(a.pieces) + blockIdx.x;
+        p->cols = begun ? (rest < a.tile_cols ? rest : a.tile_cols) : 0;
+        p->last = deal.worker_of(u - s_first + sw.steps - 1);
+        p->q0 = sw.seq.q0;
+        p->first_col = fc;
+        p->kh = kh;
       }
+      u += s_last - s_first;
     }
     const SeqInfo& seq = sw.seq;
     const float kg = a.k_gscale[kh], vg = a.v_gscale[kh];
@@ -231,6 +238,35 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
     const int32_t col0 = col_first + cg * 16 * NQ;
     const int32_t pw = s1 > s0 && col0 < cols ? (s1 - s0 + TW - 1) / TW : 0;
     const int32_t w0 = s0 + tg * pw, w1 = w0 + pw < s1 ? w0 + pw : s1;
+
+    // page of token tb + 16 lane, held by the lane, for 1024 tokens and the 1024 after
+    auto load_pages = [&](int32_t t) -> int32_t {
+      int32_t pg = (t + 16 * lane) >> a.geom.page_shift;
+      pg = pg < last_page ? pg : last_page;
+      const int32_t id = a.table[(int64_t)b * a.ld_table + pg];
+      return id < 0 ? 0 : (id >= a.geom.n_pages ? (int32_t)a.geom.n_pages - 1 : id);
+    };
+    constexpr int SPB = 64 / NG;                   // steps per 64 granules
+    const int32_t last_granule = (seq.n - 1) >> 4;
+    int32_t pages = 0, pages_next = 0;
+    auto issue = [&](int32_t s, Granule<D> x[NG]) {
+      const int32_t i = (s - w0) % SPB;
+#pragma unroll
+      for (int u = 0; u < NG; ++u) {
+        const int32_t id = __builtin_amdgcn_readlane(pages, i * NG + u);
+        int32_t gr = (begin + s * TOK) / 16 + u;
+        gr = gr < last_granule ? gr : last_granule;     // past the end: the last granule again
+        load_granule<D>(granule_buffer<D>(a, id, kh * per_head + (gr & (per_head - 1))), lane, x[u]);
+      }
+      if (i == SPB - 1) {
+        pages = pages_next;
+        pages_next = load_pages(begin + (s + 1 + SPB) * TOK);
+      }
+    };
+    if (w0 < w1) {
+      pages = load_pages(begin + w0 * TOK);
+      pages_next = load_pages(begin + (w0 + SPB) * TOK);
+    }
 
     // query columns: lane (g, r) holds column r of every block, the chunks' elements
     f16x8 qf[TERMS][NQ][KC];
@@ -275,31 +311,6 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
     }
 
     if (w0 < w1) {
-      // page of token tb + 16 lane, held by the lane, for 1024 tokens and the 1024 after
-      auto load_pages = [&](int32_t t) -> int32_t {
-        int32_t pg = (t + 16 * lane) >> a.geom.page_shift;
-        pg = pg < last_page ? pg : last_page;
-        int32_t id = a.table[(int64_t)b * a.ld_table + pg];
-        return id < 0 ? 0 : (id >= a.geom.n_pages ? (int32_t)a.geom.n_pages - 1 : id);
-      };
-      constexpr int SPB = 64 / NG;                 // steps per 64 granules
-      int32_t pages = load_pages(begin + w0 * TOK), pages_next = load_pages(begin + (w0 + SPB) * TOK);
-      const int32_t last_granule = (seq.n - 1) >> 4;
-      auto issue = [&](int32_t s, Granule<D> x[NG]) {
-        const int32_t i = (s - w0) % SPB;
-#pragma unroll
-        for (int u = 0; u < NG; ++u) {
-          const int32_t id = __builtin_amdgcn_readlane(pages, i * NG + u);
-          int32_t gr = (begin + s * TOK) / 16 + u;
-          gr = gr < last_granule ? gr : last_granule;   // past the end: the last granule again
-          load_granule<D>(granule_buffer<D>(a, id, kh * per_head + (gr & (per_head - 1))), lane, x[u]);
-        }
-        if (i == SPB - 1) {
-          pages = pages_next;
-          pages_next = load_pages(begin + (s + 1 + SPB) * TOK);
-        }
-      };
-
       Granule<D> cur[NG], nxt[NG];
       issue(w0, nxt);
       for (int32_t s = w0; s < w1; ++s) {
@@ -337,7 +348,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
               for (int i = 0; i < 4; ++i)
                 if (16 * u + i >= upto || 16 * u + i < from) sc[n][u][i] = -__builtin_inff();
           }
-          const float top = max_xor32(max_xor16(max_of<4 * NG>(reinterpret_cast<const float*>(&sc[n][0])))) * csc[n];
+          const float top = max_xor32(max_xor16(max_of(sc[n]))) * csc[n];
           if (__builtin_amdgcn_ballot_w64(top > m[n] + 15.0f)) {
             const float m1 = __builtin_fmaxf(m[n], top - 7.0f);
             const float f = __builtin_amdgcn_exp2f(m[n] - m1);
@@ -487,7 +498,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
             a.lse[(seq.q0 + qi) * a.n_q_heads + head] =
                 sum > 0.0f ? (top_c + __builtin_log2f(sum)) * kLn2 : -__builtin_inff();
         } else {
-          float* dst = a.part + ((2 * (int64_t)blockIdx.x + (s_first == 0)) * a.tile_cols + col - col_first) * (D + 4);
+          float* dst = piece_at(a, D, blockIdx.x, s_first == 0, col - col_first);
 #pragma unroll
           for (int j = 0; j < NJ; j += 4)
             *reinterpret_cast<f32x4*>(dst + 4 + part * NJ + j) = f32x4{out[j], out[j + 1], out[j + 2], out[j + 3]};
@@ -502,28 +513,21 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
   }
 }
 
-// Join the pieces of an item: one workgroup per query column.  The pieces' factors go to
-// LDS first, then D / 4 threads take four elements of a piece each, 1024 / D pieces at a
-// time, with no load depending on another.
+// Join the pieces of an item: one workgroup per worker that began one, and query column.
+// The pieces' factors go to LDS first, then D / 4 threads take four elements of a piece
+// each, 1024 / D pieces at a time, with no load depending on another.
 template <int D, bool F32>
 __global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs a) {
   constexpr int TPS = D / 4, LANES = 256 / TPS;      // threads per piece, pieces side by side
   __shared__ float s_f[kMaxWorkers], s_red[4], s_sum[4];
   __shared__ f32x4 s_x[LANES][TPS];
   const int tid = threadIdx.x;
+  const int32_t worker = blockIdx.x / a.tile_cols, c = blockIdx.x % a.tile_cols;
+  const ItemPieces item = static_cast<const ItemPieces*>(a.pieces)[worker];
+  if (c >= item.cols) return;
   const int group = a.n_q_heads / a.geom.n_kv_heads;
-  const int c = blockIdx.x % a.tile_cols;
-  const int item = blockIdx.x / a.tile_cols;
-  const int tile = item % a.col_tiles, kh = (item / a.col_tiles) % a.geom.n_kv_heads;
-  const SeqInfo seq = seq_info(a, item / a.col_tiles / a.geom.n_kv_heads);
-  const int32_t col = tile * a.tile_cols + c;
-  if (col >= seq.m * group) return;
-  const int32_t first = a.pieces[2 * (int64_t)item];
-  if (first < 0) return;                             // done whole
-  const int32_t n = a.pieces[2 * (int64_t)item + 1] - first + 1;
-  auto piece = [&](int i) {
-    return a.part + ((2 * (int64_t)(first + i) + (i == 0)) * a.tile_cols + c) * (D + 4);
-  };
+  const int32_t col = item.first_col + c, n = item.last - worker + 1;
+  auto piece = [&](int i) { return piece_at(a, D, worker + i, i == 0, c); };
   float m[kMaxWorkers / 256], l[kMaxWorkers / 256], top = kNegBig;
 #pragma unroll
   for (int i = 0; i < kMaxWorkers / 256; ++i) {
@@ -562,9 +566,9 @@ __global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs a) {
   if (tid >= TPS) return;
 #pragma unroll
   for (int i = 1; i < LANES; ++i) x += s_x[i][part];
-  const int64_t tok = seq.q0 + col / group;
-  const int head = kh * group + col % group;
-  const float g = sum > 0.0f ? a.v_gscale[kh] / sum : 0.0f;
+  const int64_t tok = item.q0 + col / group;
+  const int head = item.kh * group + col % group;
+  const float g = sum > 0.0f ? a.v_gscale[item.kh] / sum : 0.0f;
   const int64_t off = tok * a.ldo + (int64_t)head * D + 4 * part;
   if constexpr (F32) {
     *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.o) + off) = x * g;
@@ -582,7 +586,7 @@ hipError_t launch(const KvAttnArgs& a, hipStream_t s) {
   hipLaunchKernelGGL((k_kv_attn<D, NQ, CW, F32>), dim3((unsigned)blocks), dim3(64 * kAttnWaves), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e == hipSuccess && a.n_workers) {
-    hipLaunchKernelGGL((k_kv_join<D, F32>), dim3((unsigned)(items * a.tile_cols)), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((k_kv_join<D, F32>), dim3((unsigned)a.n_workers * a.tile_cols), dim3(256), 0, s, a);
     e = hipGetLastError();
   }
   return e;
@@ -598,7 +602,7 @@ hipError_t launch_cw(const KvAttnArgs& a, int cw, hipStream_t s) {
 }  // namespace
 
 KvAttnPlan kv_attn_plan(InType t, int64_t T, int32_t batch, int32_t n_q_heads, int32_t n_kv_heads, int32_t D,
-                        int64_t max_q_len, int64_t max_kv_len) {
+                        int64_t max_q_len, int64_t max_kv_len, int64_t window) {
   KvAttnPlan p{};
   const int64_t cols = (max_q_len < T ? max_q_len : T) * (n_q_heads / n_kv_heads);
   if (t == InType::BF16 && cols >= kv_prefill_cols()) {
@@ -621,14 +625,16 @@ KvAttnPlan kv_attn_plan(InType t, int64_t T, int32_t batch, int32_t n_q_heads, i
   p.col_tiles = (int32_t)tiles;
   const int64_t items = pairs * tiles;
   const int64_t tok = D == 256 ? 32 : 64, waves = kAttnWaves / p.cw;
-  const int64_t steps = (max_kv_len + tok - 1) / tok;
+  // keys that a tile attends to, at most
+  const int64_t span = window > 0 && window + max_q_len < max_kv_len ? window + max_q_len : max_kv_len;
+  const int64_t steps = (span + tok - 1) / tok;
   if (items >= 1024 || steps <= 3 * waves) return p;    // whole items
-  int64_t n = items * steps / (2 * waves);
+  int64_t n = items * steps / waves;                      // at least a step for each wave
   if (n > kMaxWorkers) n = kMaxWorkers;
   if (n < 1) n = 1;
   p.n_workers = (int32_t)n;
   p.pieces_at = n * 2 * p.tile_cols * (D + 4) * (int64_t)sizeof(float);
-  p.workspace = p.pieces_at + items * 2 * (int64_t)sizeof(int32_t);
+  p.workspace = p.pieces_at + n * kItemPiecesBytes;
   return p;
 }
 
@@ -637,7 +643,7 @@ hipError_t launch_kv_attn(KvAttnArgs a, const KvAttnPlan& p, InType t, int32_t D
   a.tile_cols = p.tile_cols;
   a.col_tiles = p.col_tiles;
   if (p.prefill) return launch_kv_prefill(a, D, s);
-  a.pieces = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(a.part) + p.pieces_at);
+  a.pieces = reinterpret_cast<uint8_t*>(a.part) + p.pieces_at;
   const bool f32 = t == InType::F32;
   if (D == 64) {
     if (p.nq == 2) return f32 ? launch_cw<64, 2, true>(a, p.cw, s) : launch_cw<64, 2, false>(a, p.cw, s);

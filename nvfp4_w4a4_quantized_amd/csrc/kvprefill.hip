@@ -242,7 +242,7 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
           if (t >= upto || t < from) sc[e] = -__builtin_inff();
         }
       }
-      const float top = max_xor32(max_of<16>(reinterpret_cast<const float*>(&sc))) * csc;
+      const float top = max_xor32(max_of(sc)) * csc;
       const float m1 = top > m + 15.0f ? __builtin_fmaxf(m, top - 7.0f) : m;
       const float f = __builtin_amdgcn_exp2f(m - m1);
       l *= f;

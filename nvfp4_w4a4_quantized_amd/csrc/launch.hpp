@@ -180,11 +180,12 @@ struct KvAttnArgs {
   float* lse;                  // optional
   float* part;                 // partial results (workspace)
   // the plan
-  int32_t* pieces;             // [items][first, last] workgroups of an item done in pieces
+  void* pieces;                // [n_workers] items done in pieces
   int32_t n_workers;           // 0: one workgroup per item; else equal runs of all steps
   int32_t tile_cols;           // query columns of an item
   int32_t col_tiles;           // items per sequence and kv head
 };
+constexpr int kItemPiecesBytes = 32;
 struct KvAttnPlan {
   int32_t n_workers, tile_cols, col_tiles, nq, cw;
   bool prefill;                // kvprefill.hip
@@ -192,7 +193,7 @@ struct KvAttnPlan {
   int64_t workspace;           // bytes
 };
 KvAttnPlan kv_attn_plan(InType t, int64_t T, int32_t batch, int32_t n_q_heads, int32_t n_kv_heads, int32_t D,
-                        int64_t max_q_len, int64_t max_kv_len);
+                        int64_t max_q_len, int64_t max_kv_len, int64_t window);
 hipError_t launch_kv_attn(KvAttnArgs a, const KvAttnPlan& p, InType t, int32_t D, hipStream_t s);
 
 // kvprefill.hip: bf16, whole items of kv_prefill_cols() query columns (a.col_tiles per
