@@ -171,16 +171,18 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t granule_buffer(const KvAttnArg
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), (short)0, kv_granule_bytes(D), 0x00020000);
 }
 
-template <int N>
+constexpr int kStream = 2;         // cache policy of loads: non-temporal
+
+template <int N, int POLICY = 0>
 __device__ __forceinline__ void load_dwords(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t* d) {
   if constexpr (N == 2) {
-    const auto x = __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0);
+    const auto x = __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, POLICY);
     d[0] = x[0];
     d[1] = x[1];
   } else {
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
-      const auto x = __builtin_amdgcn_raw_buffer_load_b128(r, off + 4 * i, 0, 0);
+      const auto x = __builtin_amdgcn_raw_buffer_load_b128(r, off + 4 * i, 0, POLICY);
 #pragma unroll
       for (int e = 0; e < 4; ++e) d[i + e] = x[e];
     }
