@@ -97,7 +97,7 @@ struct Span {
   int32_t all_lo, all_hi;  // tokens that every one of these columns attends to
 };
 
-__device__ __forceinline__ Span span_of(const SeqInfo& s, int32_t col0, int32_t col1, int group, int window) {
+__device__ __forceinline__ Span span_of(const SeqInfo& s, int32_t col0, int32_t col1, const FastDiv& group, int window) {
   const int32_t first = s.n - s.m + col0 / group, last = s.n - s.m + (col1 - 1) / group;
   Span r;
   r.hi = last + 1 > 0 ? last + 1 : 0;

@@ -22,6 +22,27 @@ namespace nvfp4 {
 
 constexpr int kv_granule_bytes(int D) { return 18 * D; }
 
+// Division of n in [0, 2^31) by a divisor known on the host: n m >> (31 + L) with L =
+// ceil(log2 d), m = floor(2^(31+L) / d) + 1 (the product exceeds n / d by less than 2^-L <= 1 / d).
+// On the device a division costs some 30 dependent instructions, and a single-token call
+// makes ten before its first load.
+struct FastDiv {
+  uint32_t d, m, s;
+};
+
+inline FastDiv fast_div(uint32_t d) {
+  uint32_t l = 0;
+  while ((1ull << l) < d) ++l;
+  return FastDiv{d, (uint32_t)((1ull << (31 + l)) / d + 1), 31 + l};
+}
+
+#ifdef __HIPCC__
+__host__ __device__
+#endif
+inline int32_t operator/(int32_t n, const FastDiv& f) {
+  return (int32_t)(((uint64_t)(uint32_t)n * f.m) >> f.s);
+}
+
 struct KvGeom {
   int32_t n_kv_heads;
   int32_t page_shift;      // log2(page_size)

@@ -88,8 +88,8 @@ __device__ __forceinline__ f16x8 join(f16x2 a, f16x2 b, f16x2 c, f16x2 d) {
 // whole ones, and the start of another.  Items that fell into several runs leave partial results
 // (slot 1: an item's first piece, slot 0: a later one) for k_kv_join.
 //
-// Inside a workgroup, waves are CW groups of 16 NQ columns by W / CW pieces of the run's
-// tokens; the pieces are joined in LDS.
+// Inside a workgroup, waves are groups of 16 NQ columns (1, 2 or 4, what the item has) by pieces
+// of the run's tokens; the pieces are joined in LDS.
 constexpr int kAttnWaves = 4;
 
 // Steps of one item of sequence b, and its items
@@ -99,15 +99,15 @@ struct SeqWork {
 };
 
 template <int TOK>
-__device__ __forceinline__ SeqWork seq_work(const KvAttnArgs& a, const SeqInfo& seq, int group) {
+__device__ __forceinline__ SeqWork seq_work(const KvAttnArgs& a, const SeqInfo& seq) {
   SeqWork w;
   w.seq = seq;
-  w.cols = w.seq.m * group;
+  w.cols = w.seq.m * (int32_t)a.by_group.d;
   w.tiles = 0;
   w.begin = w.steps = 0;
   if (w.cols > 0) {
-    const Span sp = span_of(w.seq, 0, w.cols, group, a.window);
-    const int32_t tiles = (w.cols + a.tile_cols - 1) / a.tile_cols;
+    const Span sp = span_of(w.seq, 0, w.cols, a.by_group, a.window);
+    const int32_t tiles = (w.cols + a.tile_cols - 1) / a.by_tile_cols;
     w.tiles = tiles < a.col_tiles ? tiles : a.col_tiles;   // further ones go with the first tiles' items
     w.begin = sp.lo & ~15;
     w.steps = (sp.hi - w.begin + TOK - 1) / TOK;
@@ -116,9 +116,9 @@ __device__ __forceinline__ SeqWork seq_work(const KvAttnArgs& a, const SeqInfo& 
   return w;
 }
 
-template <int D, int NQ, int CW, bool F32>
+template <int D, int NQ, bool GROUPS, bool F32>
 __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
-  constexpr int W = kAttnWaves, TW = W / CW;
+  constexpr int W = kAttnWaves;
   constexpr int NG = D == 256 ? 2 : 4;             // granules per step
   constexpr int TOK = 16 * NG;
   constexpr int KC = D / 32;                       // 32-element chunks of the first product
@@ -130,9 +130,8 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int cg = wave % CW, tg = wave / CW;
   const int g = lane >> 4, r = lane & 15;
-  const int hkv = a.geom.n_kv_heads, group = a.n_q_heads / hkv;
+  const int hkv = a.geom.n_kv_heads, group = (int)a.by_group.d;
   const int per_head = 1 << (a.geom.page_shift - 4);
 
   // this workgroup's run of steps: [u, u_end) of the sequences from b on, whose first
@@ -143,10 +142,10 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
   Deal deal(1, 1);
   const SeqTable seqs(a, lane);
   if (a.n_workers == 0) {
-    const int item = blockIdx.x / a.col_tiles;
-    b = item / hkv;
-    sw = seq_work<TOK>(a, seq_info(a, b), group);
-    if ((int)(blockIdx.x % a.col_tiles) >= sw.tiles) return;
+    const int item = (int)blockIdx.x / a.by_col_tiles;
+    b = item / a.by_heads;
+    sw = seq_work<TOK>(a, seq_info(a, b));
+    if ((int)blockIdx.x - item * a.col_tiles >= sw.tiles) return;
   } else {
     // each lane counts the steps of `each` consecutive sequences
     const int each = (a.batch + 63) / 64;
@@ -154,7 +153,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
     for (int i = 0; i < each; ++i) {
       const int bb = lane * each + i;
       if (bb < a.batch) {
-        const SeqWork x = seq_work<TOK>(a, seqs.held ? seqs.mine : seq_info(a, bb), group);
+        const SeqWork x = seq_work<TOK>(a, seqs.held ? seqs.mine : seq_info(a, bb));
         own += (int64_t)x.tiles * hkv * x.steps;
       }
     }
@@ -177,7 +176,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
     u_seq = uniform64(__shfl(upto - own, first));
     b = first * each;
     for (;; ++b) {
-      sw = seq_work<TOK>(a, seqs.at(a, b), group);
+      sw = seq_work<TOK>(a, seqs.at(a, b));
       const int64_t n = (int64_t)sw.tiles * hkv * sw.steps;
       if (u < u_seq + n) break;
       u_seq += n;
@@ -188,21 +187,22 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
     int kh, tile0;
     int32_t s_first, s_last;                       // the item's steps in this run
     if (a.n_workers == 0) {
-      tile0 = blockIdx.x % a.col_tiles;
-      kh = (blockIdx.x / a.col_tiles) % hkv;
+      const int item = (int)blockIdx.x / a.by_col_tiles;
+      tile0 = (int)blockIdx.x - item * a.col_tiles;
+      kh = item - b * hkv;
       s_first = 0;
       s_last = sw.steps;
       u = u_end;
     } else {
       while (u >= u_seq + (int64_t)sw.tiles * hkv * sw.steps) {
         u_seq += (int64_t)sw.tiles * hkv * sw.steps;
-        sw = seq_work<TOK>(a, seqs.at(a, ++b), group);
+        sw = seq_work<TOK>(a, seqs.at(a, ++b));
       }
       const int64_t in_seq = u - u_seq;
       const int32_t item =
           in_seq >> 31 ? (int32_t)(in_seq / sw.steps) : (int32_t)((uint32_t)in_seq / (uint32_t)sw.steps);
-      tile0 = item % sw.tiles;
-      kh = item / sw.tiles;
+      kh = sw.tiles == 1 ? item : item / sw.tiles;
+      tile0 = item - kh * sw.tiles;
       s_first = (int32_t)(in_seq - (int64_t)item * sw.steps);
       const int64_t left = u_end - u;
       s_last = left < sw.steps - s_first ? s_first + (int32_t)left : sw.steps;
@@ -227,7 +227,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
     if (tile != tile0 && s_first > 0) break;
     const int32_t col_first = tile * a.tile_cols;
     const int32_t cols = col_first + a.tile_cols < sw.cols ? col_first + a.tile_cols : sw.cols;   // end of the tile
-    Span sp = span_of(seq, col_first, cols, group, a.window);
+    Span sp = span_of(seq, col_first, cols, a.by_group, a.window);
     int32_t begin = sw.begin, s0 = s_first, s1 = s_last;
     bool whole = s0 == 0 && s1 == sw.steps;
     if (a.n_workers == 0 || tile != tile0) {       // the tile's own keys
@@ -237,8 +237,11 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
       whole = true;
     }
     if (seq.n <= 0) s1 = s0;
+    // column groups of this item: 2^cs of them, by W >> cs pieces of tokens
+    const int cs = !GROUPS || cols - col_first <= 16 * NQ ? 0 : (cols - col_first <= 32 * NQ ? 1 : 2);
+    const int cg = wave & ((1 << cs) - 1), tg = wave >> cs, tw = W >> cs;
     const int32_t col0 = col_first + cg * 16 * NQ;
-    const int32_t pw = s1 > s0 && col0 < cols ? (s1 - s0 + TW - 1) / TW : 0;
+    const int32_t pw = s1 > s0 && col0 < cols ? (s1 - s0 + tw - 1) >> (2 - cs) : 0;
     const int32_t w0 = s0 + tg * pw, w1 = w0 + pw < s1 ? w0 + pw : s1;
 
     // page of token tb + 16 lane, held by the lane, for 1024 tokens and the 1024 after
@@ -277,11 +280,9 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
     f32x4 acc[NQ][NJ];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-      int32_t col = col0 + 16 * n + r;
-      if (col >= cols) col = cols - 1;             // computed, never written
-      const int32_t qi = col / group;
-      const int head = kh * group + (col - qi * group);
-      const int64_t off = (seq.q0 + qi) * a.ldq + (int64_t)head * D;
+      const int32_t col = col0 + 16 * n + r < cols ? col0 + 16 * n + r : cols - 1;   // past the end: never written
+      const int32_t qi = col / a.by_group, pos = seq.n - seq.m + qi;
+      const int64_t off = (seq.q0 + qi) * a.ldq + (int64_t)(kh * group + (col - qi * group)) * D;
       float v[KC][8];
       float amax = 0.0f;
 #pragma unroll
@@ -303,7 +304,6 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
           qf[0][n][c][i] = hi;
           if constexpr (F32) qf[TERMS - 1][n][c][i] = (_Float16)(x - (float)hi);
         }
-      const int32_t pos = seq.n - seq.m + qi;
       limit[n] = pos + 1;
       floor_[n] = a.window ? pos - a.window + 1 : 0;
       m[n] = kNegBig;
@@ -445,9 +445,12 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
     __syncthreads();
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-      float top = s_m[cg][16 * n + r];
+      float top = m[n];
 #pragma unroll
-      for (int w = 1; w < TW; ++w) top = __builtin_fmaxf(top, s_m[cg + w * CW][16 * n + r]);
+      for (int w = 0; w < W; ++w) {
+        const float x = s_m[w][16 * n + r];
+        if ((w & ((1 << cs) - 1)) == cg) top = __builtin_fmaxf(top, x);
+      }
       const float f = __builtin_amdgcn_exp2f(m[n] - top);
       if (n) __syncthreads();
 #pragma unroll
@@ -461,27 +464,30 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
       __syncthreads();
       // thread = (column, D / 16 elements) of each column group in turn
       const int c = threadIdx.x >> 4, part = threadIdx.x & 15;
-#pragma unroll
-      for (int h = 0; h < CW; ++h) {
+      for (int h = 0; h < 1 << cs; ++h) {
         const int32_t col = col_first + h * 16 * NQ + 16 * n + c;
         if (col >= cols) break;
-        float top_c = s_m[h][16 * n + c], sum = 0.0f;
+        float top_c = kNegBig, sum = 0.0f, out[NJ] = {};
+        auto add = [&](int w) {
+          sum += s_l[w][16 * n + c] * __builtin_amdgcn_exp2f(s_m[w][16 * n + c] - top_c);
 #pragma unroll
-        for (int w = 1; w < TW; ++w) top_c = __builtin_fmaxf(top_c, s_m[h + w * CW][16 * n + c]);
+          for (int j = 0; j < NJ; j += 4) {
+            const f32x4 x = *reinterpret_cast<const f32x4*>(&s_o[w][c * LDO + part * NJ + j]);
 #pragma unroll
-        for (int w = 0; w < TW; ++w)
-          sum += s_l[h + w * CW][16 * n + c] * __builtin_amdgcn_exp2f(s_m[h + w * CW][16 * n + c] - top_c);
-        float out[NJ];
+            for (int e = 0; e < 4; ++e) out[j + e] += x[e];
+          }
+        };
+        if (cs == 0) {                             // the usual case, its reads side by side
 #pragma unroll
-        for (int j = 0; j < NJ; j += 4) {
-          f32x4 x = *reinterpret_cast<const f32x4*>(&s_o[h][c * LDO + part * NJ + j]);
+          for (int w = 0; w < W; ++w) top_c = __builtin_fmaxf(top_c, s_m[w][16 * n + c]);
 #pragma unroll
-          for (int w = 1; w < TW; ++w) x += *reinterpret_cast<const f32x4*>(&s_o[h + w * CW][c * LDO + part * NJ + j]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) out[j + e] = x[e];
+          for (int w = 0; w < W; ++w) add(w);
+        } else {
+          for (int w = h; w < W; w += 1 << cs) top_c = __builtin_fmaxf(top_c, s_m[w][16 * n + c]);
+          for (int w = h; w < W; w += 1 << cs) add(w);
         }
         if (whole) {
-          const int32_t qi = col / group;
+          const int32_t qi = col / a.by_group;
           const int head = kh * group + (col - qi * group);
           const float f = sum > 0.0f ? vg / sum : 0.0f;
           const int64_t off = (seq.q0 + qi) * a.ldo + (int64_t)head * D + part * NJ;
@@ -519,9 +525,8 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
 template <int D, bool F32, int E>
 __device__ __forceinline__ void store_joined(const KvAttnArgs& a, const ItemPieces& item, int32_t c, int first,
                                              const float (&x)[E], float top, float sum) {
-  const int group = a.n_q_heads / a.geom.n_kv_heads;
-  const int32_t col = item.first_col + c, tok = item.q0 + col / group;
-  const int head = item.kh * group + col % group;
+  const int32_t col = item.first_col + c, qi = col / a.by_group, tok = item.q0 + qi;
+  const int head = item.kh * (int)a.by_group.d + col - qi * (int)a.by_group.d;
   const float g = sum > 0.0f ? a.v_gscale[item.kh] / sum : 0.0f;
   const int64_t off = (int64_t)tok * a.ldo + (int64_t)head * D + first;
   if constexpr (F32) {
@@ -544,8 +549,8 @@ template <int D, bool F32>
 __global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs a) {
   constexpr int E = D / 64;
   const int lane = threadIdx.x & 63;
-  const int64_t id = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int32_t worker = (int32_t)(id / a.tile_cols), c = (int32_t)(id % a.tile_cols);
+  const int32_t id = (int32_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int32_t worker = id / a.by_tile_cols, c = id - worker * a.tile_cols;
   if (worker >= a.n_workers) return;
   const ItemPieces item = static_cast<const ItemPieces*>(a.pieces)[worker];
   if (c >= item.cols) return;
@@ -585,7 +590,7 @@ __global__ __launch_bounds__(256) void k_kv_join_many(KvAttnArgs a) {
   __shared__ float s_f[kMaxWorkers], s_red[4], s_sum[4];
   __shared__ f32x4 s_x[LANES][TPS];
   const int tid = threadIdx.x;
-  const int32_t worker = blockIdx.x / a.tile_cols, c = blockIdx.x % a.tile_cols;
+  const int32_t worker = (int32_t)blockIdx.x / a.by_tile_cols, c = (int32_t)blockIdx.x - worker * a.tile_cols;
   const ItemPieces item = static_cast<const ItemPieces*>(a.pieces)[worker];
   if (c >= item.cols) return;
   const int32_t n = item.last - worker + 1;
@@ -632,11 +637,14 @@ __global__ __launch_bounds__(256) void k_kv_join_many(KvAttnArgs a) {
   store_joined<D, F32>(a, item, c, 4 * part, out, top, sum);
 }
 
-template <int D, int NQ, int CW, bool F32>
+template <int D, int NQ, bool F32>
 hipError_t launch(const KvAttnArgs& a, hipStream_t s) {
   const int64_t items = (int64_t)a.batch * a.geom.n_kv_heads * a.col_tiles;
   const int64_t blocks = a.n_workers ? a.n_workers : items;
-  hipLaunchKernelGGL((k_kv_attn<D, NQ, CW, F32>), dim3((unsigned)blocks), dim3(64 * kAttnWaves), 0, s, a);
+  if (a.tile_cols > 16 * NQ)
+    hipLaunchKernelGGL((k_kv_attn<D, NQ, true, F32>), dim3((unsigned)blocks), dim3(64 * kAttnWaves), 0, s, a);
+  else
+    hipLaunchKernelGGL((k_kv_attn<D, NQ, false, F32>), dim3((unsigned)blocks), dim3(64 * kAttnWaves), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e == hipSuccess && a.n_workers) {
     const unsigned columns = (unsigned)a.n_workers * a.tile_cols;
@@ -647,13 +655,6 @@ hipError_t launch(const KvAttnArgs& a, hipStream_t s) {
     e = hipGetLastError();
   }
   return e;
-}
-
-template <int D, int NQ, bool F32>
-hipError_t launch_cw(const KvAttnArgs& a, int cw, hipStream_t s) {
-  if (cw == 1) return launch<D, NQ, 1, F32>(a, s);
-  if (cw == 2) return launch<D, NQ, 2, F32>(a, s);
-  return launch<D, NQ, 4, F32>(a, s);
 }
 
 }  // namespace
@@ -672,8 +673,7 @@ KvAttnPlan kv_attn_plan(InType t, int64_t T, int32_t batch, int32_t n_q_heads, i
   // two column blocks share a decoded granule where their registers fit
   p.nq = cols > 16 && (D == 64 || (D == 128 && t == InType::BF16)) ? 2 : 1;
   const int64_t blk = 16 * p.nq;
-  p.cw = cols <= blk ? 1 : (cols <= 2 * blk ? 2 : 4);
-  p.tile_cols = (int32_t)(cols < blk * p.cw ? cols : blk * p.cw);
+  p.tile_cols = (int32_t)(cols < blk * kAttnWaves ? cols : blk * kAttnWaves);
   int64_t tiles = (cols + p.tile_cols - 1) / p.tile_cols;
   const int64_t pairs = (int64_t)batch * n_kv_heads;
   // any number of planned tiles is right: the kernel takes further ones with the first
@@ -681,7 +681,7 @@ KvAttnPlan kv_attn_plan(InType t, int64_t T, int32_t batch, int32_t n_q_heads, i
   if (tiles > most_tiles) tiles = most_tiles < 1 ? 1 : most_tiles;
   p.col_tiles = (int32_t)tiles;
   const int64_t items = pairs * tiles;
-  const int64_t tok = D == 256 ? 32 : 64, waves = kAttnWaves / p.cw;
+  const int64_t tok = D == 256 ? 32 : 64, waves = cols <= blk ? 4 : (cols <= 2 * blk ? 2 : 1);
   // keys that a tile attends to, at most
   const int64_t span = window > 0 && window + max_q_len < max_kv_len ? window + max_q_len : max_kv_len;
   const int64_t steps = (span + tok - 1) / tok;
@@ -699,18 +699,23 @@ hipError_t launch_kv_attn(KvAttnArgs a, const KvAttnPlan& p, InType t, int32_t D
   a.n_workers = p.n_workers;
   a.tile_cols = p.tile_cols;
   a.col_tiles = p.col_tiles;
+  a.by_group = fast_div((uint32_t)(a.n_q_heads / a.geom.n_kv_heads));
+  a.by_heads = fast_div((uint32_t)a.geom.n_kv_heads);
+  a.by_tile_cols = fast_div((uint32_t)a.tile_cols);
+  a.by_col_tiles = fast_div((uint32_t)a.col_tiles);
+  a.by_pairs = fast_div((uint32_t)a.batch * (uint32_t)a.geom.n_kv_heads);
   if (p.prefill) return launch_kv_prefill(a, D, s);
   a.pieces = reinterpret_cast<uint8_t*>(a.part) + p.pieces_at;
   const bool f32 = t == InType::F32;
   if (D == 64) {
-    if (p.nq == 2) return f32 ? launch_cw<64, 2, true>(a, p.cw, s) : launch_cw<64, 2, false>(a, p.cw, s);
-    return f32 ? launch_cw<64, 1, true>(a, p.cw, s) : launch_cw<64, 1, false>(a, p.cw, s);
+    if (p.nq == 2) return f32 ? launch<64, 2, true>(a, s) : launch<64, 2, false>(a, s);
+    return f32 ? launch<64, 1, true>(a, s) : launch<64, 1, false>(a, s);
   }
   if (D == 128) {
-    if (p.nq == 2) return launch_cw<128, 2, false>(a, p.cw, s);
-    return f32 ? launch_cw<128, 1, true>(a, p.cw, s) : launch_cw<128, 1, false>(a, p.cw, s);
+    if (p.nq == 2) return launch<128, 2, false>(a, s);
+    return f32 ? launch<128, 1, true>(a, s) : launch<128, 1, false>(a, s);
   }
-  return f32 ? launch_cw<256, 1, true>(a, p.cw, s) : launch_cw<256, 1, false>(a, p.cw, s);
+  return f32 ? launch<256, 1, true>(a, s) : launch<256, 1, false>(a, s);
 }
 
 }  // namespace nvfp4

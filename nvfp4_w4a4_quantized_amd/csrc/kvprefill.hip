@@ -80,11 +80,12 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int hkv = a.geom.n_kv_heads, group = a.n_q_heads / hkv;
+  const int hkv = a.geom.n_kv_heads, group = (int)a.by_group.d;
   const int pairs = a.batch * hkv;
   // the longest spans (last tiles) start first; workgroups side by side differ in the head
-  const int pair = blockIdx.x % pairs, kh = pair % hkv;
-  const SeqInfo seq = seq_info(a, pair / hkv);
+  const int turn = (int)blockIdx.x / a.by_pairs, pair = (int)blockIdx.x - turn * pairs;
+  const int b = pair / a.by_heads, kh = pair - b * hkv;
+  const SeqInfo seq = seq_info(a, b);
   const int32_t cols = seq.m * group;
   const int32_t tiles = (cols + kPrefillCols - 1) / kPrefillCols;
   const int32_t last_page = (seq.n - 1) >> a.geom.page_shift, last_granule = (seq.n - 1) >> 4;
@@ -93,10 +94,10 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
   const int h = lane >> 5, c32 = lane & 31;
   const int gran = D == 256 ? wave & 3 : wave;      // this wave's granule of a tile
 
-  for (int32_t tile = tiles - 1 - (int32_t)(blockIdx.x / pairs); tile >= 0; tile -= a.col_tiles) {
+  for (int32_t tile = tiles - 1 - turn; tile >= 0; tile -= a.col_tiles) {
     const int32_t col_first = tile * kPrefillCols;
     const int32_t col_end = col_first + kPrefillCols < cols ? col_first + kPrefillCols : cols;
-    const Span all = span_of(seq, col_first, col_end, group, a.window);
+    const Span all = span_of(seq, col_first, col_end, a.by_group, a.window);
     const int32_t begin = all.lo & ~15;
     const int32_t steps = seq.n > 0 ? (all.hi - begin + TOK - 1) / TOK : 0;
 
@@ -104,13 +105,13 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
     const int32_t col0 = col_first + 32 * wave;
     const int32_t w0 = col0 < col_end ? col0 : col_end - 1;
     const int32_t w1 = col0 + 32 < col_end ? col0 + 32 : col_end;
-    const Span sp = span_of(seq, w0, w1, group, a.window);
+    const Span sp = span_of(seq, w0, w1, a.by_group, a.window);
 
     // loads of tile s: this wave's granule, its page id known one tile ahead
     auto page_of = [&](int32_t s) -> int32_t {
       int32_t pg = (begin + s * TOK + 16 * gran) >> a.geom.page_shift;
       pg = pg < last_page ? pg : last_page;
-      const int32_t id = a.table[(int64_t)(pair / hkv) * a.ld_table + pg];
+      const int32_t id = a.table[(int64_t)b * a.ld_table + pg];
       return id < 0 ? 0 : (id >= a.geom.n_pages ? (int32_t)a.geom.n_pages - 1 : id);
     };
     auto granule = [&](int32_t s, int32_t id) {
@@ -180,7 +181,7 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
     f16x8 qf[KS];
     int32_t col = col0 + c32;
     col = col < col_end ? col : col_end - 1;
-    const int32_t qi = col / group;
+    const int32_t qi = col / a.by_group;
     const int head = kh * group + (col - qi * group);
     float amax = 0.0f;
     {

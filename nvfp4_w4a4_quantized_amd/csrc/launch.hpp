@@ -184,10 +184,11 @@ struct KvAttnArgs {
   int32_t n_workers;           // 0: one workgroup per item; else equal runs of all steps
   int32_t tile_cols;           // query columns of an item
   int32_t col_tiles;           // items per sequence and kv head
+  FastDiv by_group, by_heads, by_tile_cols, by_col_tiles, by_pairs;   // pairs: sequence, kv head
 };
 constexpr int kItemPiecesBytes = 32;
 struct KvAttnPlan {
-  int32_t n_workers, tile_cols, col_tiles, nq, cw;
+  int32_t n_workers, tile_cols, col_tiles, nq;
   bool prefill;                // kvprefill.hip
   int64_t pieces_at;           // byte offset in the workspace
   int64_t workspace;           // bytes
