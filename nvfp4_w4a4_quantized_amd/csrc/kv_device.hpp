@@ -131,36 +131,18 @@ struct SeqTable {
   }
 };
 
-// `total` units dealt out to workers: each gets the same number, the first `rest` one more.
-struct Deal {
-  int64_t each, rest;
-
-  __device__ __forceinline__ Deal(int64_t total, int64_t workers) {
-    each = total >> 31 ? total / workers : (int64_t)((uint32_t)total / (uint32_t)workers);
-    rest = total - each * workers;
-  }
-  __device__ __forceinline__ int64_t first_of(int64_t w) const { return w * each + (w < rest ? w : rest); }
-  __device__ __forceinline__ int32_t worker_of(int64_t unit) const {
-    const int64_t longer = rest * (each + 1);
-    const int64_t x = unit < longer ? unit : unit - longer, y = unit < longer ? each + 1 : each;
-    const int32_t w = x >> 31 || y >> 31 ? (int32_t)(x / y) : (int32_t)((uint32_t)x / (uint32_t)y);
-    return unit < longer ? w : (int32_t)rest + w;
-  }
-};
-
 // What the first worker of an item done in pieces leaves for the join: the item's query
-// columns and who has the other pieces.  The pieces are in slot 1 of that worker and slot 0 of
-// those after it, up to `last`.
+// columns.  The other pieces are those of the workers after it.
 struct alignas(16) ItemPieces {
-  int32_t cols;            // columns of the item; 0: this worker left none
-  int32_t last;
+  int32_t cols;            // columns of the item; 0: this worker began none
+  int32_t pieces;
   int32_t q0, first_col, kh, pad[3];
 };
 static_assert(sizeof(ItemPieces) == kItemPiecesBytes, "launch.hpp");
 
 // Partial results of column c: [maximum, sum, -, -, output D] floats
-__device__ __forceinline__ float* piece_at(const KvAttnArgs& a, int D, int32_t worker, int slot, int32_t c) {
-  return a.part + ((2 * (int64_t)worker + slot) * a.tile_cols + c) * (D + 4);
+__device__ __forceinline__ float* piece_at(const KvAttnArgs& a, int D, int32_t worker, int32_t c) {
+  return a.part + ((int64_t)worker * a.tile_cols + c) * (D + 4);
 }
 
 // A granule as a buffer: its address in scalar registers, the lanes' 32-bit offsets in one

@@ -31,6 +31,7 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kMaxWorkers = 512;         // two workgroups per compute unit
+constexpr int kMostPieces = kMaxWorkers; // of one item (S is at least its share of all steps)
 
 // One granule as a lane of the 16-row MFMAs holds it.
 template <int D>
@@ -83,13 +84,14 @@ __device__ __forceinline__ f16x8 join(f16x2 a, f16x2 b, f16x2 c, f16x2 d) {
 
 // Work of a call: items (sequence, kv head, tile of tile_cols query columns), each a run of
 // steps of NG granules along its keys.  With whole items (n_workers == 0) a workgroup takes
-// one.  Otherwise all steps of the call, in item order, are cut into n_workers equal runs, one
-// per workgroup, whatever the sequences' lengths: a run takes the end of one item, perhaps
-// whole ones, and the start of another.  Items that fell into several runs leave partial results
-// (slot 1: an item's first piece, slot 0: a later one) for k_kv_join.
+// one.  Otherwise an item is cut into the fewest equal pieces of at most S steps, a workgroup
+// each, where S is all steps of the call by n_workers; there are at most n_workers + items
+// pieces, and as many workgroups.  Pieces of one item leave partial results for k_kv_join.
+// (Equal runs of all steps, one per workgroup whatever items they cross, were slower: the
+// second item of a workgroup costs 5 us of latency, more than the better balance gives.)
 //
 // Inside a workgroup, waves are groups of 16 NQ columns (1, 2 or 4, what the item has) by pieces
-// of the run's tokens; the pieces are joined in LDS.
+// of the piece's tokens, joined in LDS.
 constexpr int kAttnWaves = 4;
 
 // Steps of one item of sequence b, and its items
@@ -134,90 +136,87 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
   const int hkv = a.geom.n_kv_heads, group = (int)a.by_group.d;
   const int per_head = 1 << (a.geom.page_shift - 4);
 
-  // this workgroup's run of steps: [u, u_end) of the sequences from b on, whose first
-  // step is u_seq
-  int b;
-  int64_t u = 0, u_end = 1, u_seq = 0;
+  // this workgroup's item and its steps [s_first, s_last) of it
+  int b, kh, tile0;
+  int32_t s_first, s_last;
   SeqWork sw;
-  Deal deal(1, 1);
-  const SeqTable seqs(a, lane);
   if (a.n_workers == 0) {
     const int item = (int)blockIdx.x / a.by_col_tiles;
     b = item / a.by_heads;
+    kh = item - b * hkv;
+    tile0 = (int)blockIdx.x - item * a.col_tiles;
     sw = seq_work<TOK>(a, seq_info(a, b));
-    if ((int)blockIdx.x - item * a.col_tiles >= sw.tiles) return;
+    if (tile0 >= sw.tiles) return;
+    s_first = 0;
+    s_last = sw.steps;
   } else {
-    // each lane counts the steps of `each` consecutive sequences
+    // each lane counts the steps, then the pieces, of `each` consecutive sequences
+    const SeqTable seqs(a, lane);
     const int each = (a.batch + 63) / 64;
-    int64_t own = 0;
-    for (int i = 0; i < each; ++i) {
+    auto steps_of = [&](int i, int32_t& items) {
       const int bb = lane * each + i;
-      if (bb < a.batch) {
-        const SeqWork x = seq_work<TOK>(a, seqs.held ? seqs.mine : seq_info(a, bb));
-        own += (int64_t)x.tiles * hkv * x.steps;
-      }
+      items = 0;
+      if (bb >= a.batch) return 0;
+      const SeqWork x = seq_work<TOK>(a, seqs.held ? seqs.mine : seq_info(a, bb));
+      items = x.tiles * hkv;
+      return x.steps;
+    };
+    float total = 0.0f;
+    for (int i = 0; i < each; ++i) {
+      int32_t items;
+      const int32_t steps = steps_of(i, items);
+      total += (float)items * (float)steps;
     }
-    int64_t upto = own;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) total += __shfl_xor(total, off);
+    // rounded up, past the rounding of the sum
+    int32_t S = (int32_t)(total * 1.0001f / (float)a.n_workers) + 1;
+    S = S < a.min_steps ? a.min_steps : S;
+    int32_t own = 0;
+    for (int i = 0; i < each; ++i) {
+      int32_t items;
+      const int32_t steps = steps_of(i, items);
+      if (items) own += items * (int32_t)((uint32_t)(steps + S - 1) / (uint32_t)S);
+    }
+    int32_t upto = own;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
-      const int64_t x = __shfl_up(upto, off);
+      const int32_t x = __shfl_up(upto, off);
       if (lane >= off) upto += x;
     }
-    const int64_t total = uniform64(__shfl(upto, 63));
-    const int64_t workers = total < a.n_workers ? total : a.n_workers;   // none without a step
-    if (blockIdx.x >= workers) {
+    const uint64_t past = __builtin_amdgcn_ballot_w64(upto > (int32_t)blockIdx.x);
+    if (past == 0) {
       if (threadIdx.x == 0) static_cast<ItemPieces*>(a.pieces)[blockIdx.x].cols = 0;
       return;
     }
-    deal = Deal(total, workers);
-    u = deal.first_of(blockIdx.x);
-    u_end = deal.first_of(blockIdx.x + 1);
-    const int first = __builtin_ctzll(__builtin_amdgcn_ballot_w64(upto > u));
-    u_seq = uniform64(__shfl(upto - own, first));
-    b = first * each;
-    for (;; ++b) {
+    const int first = __builtin_ctzll(past);
+    int32_t in_seq = (int32_t)blockIdx.x - __builtin_amdgcn_readlane(upto - own, first), pieces;
+    for (b = first * each;; ++b) {
       sw = seq_work<TOK>(a, seqs.at(a, b));
-      const int64_t n = (int64_t)sw.tiles * hkv * sw.steps;
-      if (u < u_seq + n) break;
-      u_seq += n;
+      pieces = (int32_t)((uint32_t)(sw.steps + S - 1) / (uint32_t)S);
+      if (in_seq < sw.tiles * hkv * pieces) break;
+      in_seq -= sw.tiles * hkv * pieces;
+    }
+    const int32_t item = pieces == 1 ? in_seq : (int32_t)((uint32_t)in_seq / (uint32_t)pieces);
+    const int32_t piece = in_seq - item * pieces;
+    kh = sw.tiles == 1 ? item : (int32_t)((uint32_t)item / (uint32_t)sw.tiles);
+    tile0 = item - kh * sw.tiles;
+    const int32_t q = pieces == 1 ? sw.steps : (int32_t)((uint32_t)sw.steps / (uint32_t)pieces);
+    const int32_t rest = sw.steps - q * pieces;
+    s_first = piece * q + (piece < rest ? piece : rest);
+    s_last = s_first + q + (piece < rest);
+    if (threadIdx.x == 0) {
+      const int32_t fc = tile0 * a.tile_cols, left = sw.cols - fc;
+      ItemPieces* const p = static_cast<ItemPieces*>(a.pieces) + blockIdx.x;
+      p->cols = piece == 0 && pieces > 1 ? (left < a.tile_cols ? left : a.tile_cols) : 0;
+      p->pieces = pieces;
+      p->q0 = sw.seq.q0;
+      p->first_col = fc;
+      p->kh = kh;
     }
   }
 
-  while (u < u_end) {
-    int kh, tile0;
-    int32_t s_first, s_last;                       // the item's steps in this run
-    if (a.n_workers == 0) {
-      const int item = (int)blockIdx.x / a.by_col_tiles;
-      tile0 = (int)blockIdx.x - item * a.col_tiles;
-      kh = item - b * hkv;
-      s_first = 0;
-      s_last = sw.steps;
-      u = u_end;
-    } else {
-      while (u >= u_seq + (int64_t)sw.tiles * hkv * sw.steps) {
-        u_seq += (int64_t)sw.tiles * hkv * sw.steps;
-        sw = seq_work<TOK>(a, seqs.at(a, ++b));
-      }
-      const int64_t in_seq = u - u_seq;
-      const int32_t item =
-          in_seq >> 31 ? (int32_t)(in_seq / sw.steps) : (int32_t)((uint32_t)in_seq / (uint32_t)sw.steps);
-      kh = sw.tiles == 1 ? item : item / sw.tiles;
-      tile0 = item - kh * sw.tiles;
-      s_first = (int32_t)(in_seq - (int64_t)item * sw.steps);
-      const int64_t left = u_end - u;
-      s_last = left < sw.steps - s_first ? s_first + (int32_t)left : sw.steps;
-      const bool begun = s_first == 0 && s_last < sw.steps;
-      if (threadIdx.x == 0 && (begun || u + (s_last - s_first) >= u_end)) {
-        const int32_t fc = tile0 * a.tile_cols, rest = sw.cols - fc;
-        ItemPieces* const p = static_cast<ItemPieces*>(a.pieces) + blockIdx.x;
-        p->cols = begun ? (rest < a.tile_cols ? rest : a.tile_cols) : 0;
-        p->last = deal.worker_of(u - s_first + sw.steps - 1);
-        p->q0 = sw.seq.q0;
-        p->first_col = fc;
-        p->kh = kh;
-      }
-      u += s_last - s_first;
-    }
+  {
     const SeqInfo& seq = sw.seq;
     const float kg = a.k_gscale[kh], vg = a.v_gscale[kh];
     const int32_t last_page = (seq.n - 1) >> a.geom.page_shift;
@@ -506,7 +505,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
             a.lse[(seq.q0 + qi) * a.n_q_heads + head] =
                 sum > 0.0f ? (top_c + __builtin_log2f(sum)) * kLn2 : -__builtin_inff();
         } else {
-          float* dst = piece_at(a, D, blockIdx.x, s_first == 0, col - col_first);
+          float* dst = piece_at(a, D, blockIdx.x, col - col_first);
 #pragma unroll
           for (int j = 0; j < NJ; j += 4)
             *reinterpret_cast<f32x4*>(dst + 4 + part * NJ + j) = f32x4{out[j], out[j + 1], out[j + 2], out[j + 3]};
@@ -551,17 +550,17 @@ __global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs a) {
   const int lane = threadIdx.x & 63;
   const int32_t id = (int32_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int32_t worker = id / a.by_tile_cols, c = id - worker * a.tile_cols;
-  if (worker >= a.n_workers) return;
+  if (worker >= a.blocks) return;
   const ItemPieces item = static_cast<const ItemPieces*>(a.pieces)[worker];
   if (c >= item.cols) return;
-  const int32_t n = item.last - worker + 1;
+  const int32_t n = item.pieces;
   float top = kNegBig, sum = 0.0f, x[E] = {};
   for (int32_t i0 = 0; i0 < n; i0 += 4) {
     float m[4], l[4], v[4][E];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int32_t k = i0 + i < n ? i0 + i : n - 1;
-      const float* p = piece_at(a, D, worker + k, k == 0, c);
+      const float* p = piece_at(a, D, worker + k, c);
       m[i] = p[0];
       l[i] = p[1];
 #pragma unroll
@@ -587,17 +586,17 @@ __global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs a) {
 template <int D, bool F32>
 __global__ __launch_bounds__(256) void k_kv_join_many(KvAttnArgs a) {
   constexpr int TPS = D / 4, LANES = 256 / TPS;      // threads per piece, pieces side by side
-  __shared__ float s_f[kMaxWorkers], s_red[4], s_sum[4];
+  __shared__ float s_f[kMostPieces], s_red[4], s_sum[4];
   __shared__ f32x4 s_x[LANES][TPS];
   const int tid = threadIdx.x;
   const int32_t worker = (int32_t)blockIdx.x / a.by_tile_cols, c = (int32_t)blockIdx.x - worker * a.tile_cols;
   const ItemPieces item = static_cast<const ItemPieces*>(a.pieces)[worker];
   if (c >= item.cols) return;
-  const int32_t n = item.last - worker + 1;
-  auto piece = [&](int i) { return piece_at(a, D, worker + i, i == 0, c); };
-  float m[kMaxWorkers / 256], l[kMaxWorkers / 256], top = kNegBig;
+  const int32_t n = item.pieces;
+  auto piece = [&](int i) { return piece_at(a, D, worker + i, c); };
+  float m[kMostPieces / 256], l[kMostPieces / 256], top = kNegBig;
 #pragma unroll
-  for (int i = 0; i < kMaxWorkers / 256; ++i) {
+  for (int i = 0; i < kMostPieces / 256; ++i) {
     m[i] = kNegBig;
     l[i] = 0.0f;
     if (tid + 256 * i < n) {
@@ -614,7 +613,7 @@ __global__ __launch_bounds__(256) void k_kv_join_many(KvAttnArgs a) {
   top = __builtin_fmaxf(__builtin_fmaxf(s_red[0], s_red[1]), __builtin_fmaxf(s_red[2], s_red[3]));
   float sum = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kMaxWorkers / 256; ++i) {
+  for (int i = 0; i < kMostPieces / 256; ++i) {
     const float f = __builtin_amdgcn_exp2f(m[i] - top);
     s_f[tid + 256 * i] = f;
     sum += l[i] * f;
@@ -639,16 +638,15 @@ __global__ __launch_bounds__(256) void k_kv_join_many(KvAttnArgs a) {
 
 template <int D, int NQ, bool F32>
 hipError_t launch(const KvAttnArgs& a, hipStream_t s) {
-  const int64_t items = (int64_t)a.batch * a.geom.n_kv_heads * a.col_tiles;
-  const int64_t blocks = a.n_workers ? a.n_workers : items;
+  const int64_t blocks = a.blocks;
   if (a.tile_cols > 16 * NQ)
     hipLaunchKernelGGL((k_kv_attn<D, NQ, true, F32>), dim3((unsigned)blocks), dim3(64 * kAttnWaves), 0, s, a);
   else
     hipLaunchKernelGGL((k_kv_attn<D, NQ, false, F32>), dim3((unsigned)blocks), dim3(64 * kAttnWaves), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e == hipSuccess && a.n_workers) {
-    const unsigned columns = (unsigned)a.n_workers * a.tile_cols;
-    if (a.n_workers > 8 * items)
+    const unsigned columns = (unsigned)a.blocks * a.tile_cols;
+    if (a.n_workers > 8 * (a.blocks - a.n_workers))             // more than 8 pieces an item
       hipLaunchKernelGGL((k_kv_join_many<D, F32>), dim3(columns), dim3(256), 0, s, a);
     else
       hipLaunchKernelGGL((k_kv_join<D, F32>), dim3((columns + 3) / 4), dim3(256), 0, s, a);
@@ -681,22 +679,30 @@ KvAttnPlan kv_attn_plan(InType t, int64_t T, int32_t batch, int32_t n_q_heads, i
   if (tiles > most_tiles) tiles = most_tiles < 1 ? 1 : most_tiles;
   p.col_tiles = (int32_t)tiles;
   const int64_t items = pairs * tiles;
+  p.blocks = (int32_t)items;
   const int64_t tok = D == 256 ? 32 : 64, waves = cols <= blk ? 4 : (cols <= 2 * blk ? 2 : 1);
   // keys that a tile attends to, at most
   const int64_t span = window > 0 && window + max_q_len < max_kv_len ? window + max_q_len : max_kv_len;
   const int64_t steps = (span + tok - 1) / tok;
-  if (items >= 1024 || steps <= 3 * waves) return p;    // whole items
-  int64_t n = items * steps / waves;                      // at least a step for each wave
-  if (n > kMaxWorkers) n = kMaxWorkers;
-  if (n < 1) n = 1;
-  p.n_workers = (int32_t)n;
-  p.pieces_at = n * 2 * p.tile_cols * (D + 4) * (int64_t)sizeof(float);
-  p.workspace = p.pieces_at + n * kItemPiecesBytes;
+  // Whole items where a wave's part of one is short: cutting costs the join's launch and
+  // latency (4.5 us) and pays where it brings idle compute units to work.  Measured, whole
+  // / cut: 256 items of up to 64 steps 29.7 / 32.8 us, 128 of 32 15.8 / 20.2 and of 64 26.7 / 22.0,
+  // 64 of 32 15.1 / 18.8, 32 of 32 15.5 / 11.3.
+  const int64_t alone = items >= 256 ? 16 : (items >= 64 ? 8 : 4);
+  if (items >= 1024 || steps <= alone * waves) return p;
+  p.min_steps = (int32_t)waves;                           // a step for each wave
+  // about as many pieces as run at once: rounding up adds half a piece to an item
+  p.n_workers = (int32_t)(items > kMaxWorkers ? kMaxWorkers / 2 : kMaxWorkers - items / 2);
+  p.blocks = (int32_t)(p.n_workers + items);
+  p.pieces_at = (int64_t)p.blocks * p.tile_cols * (D + 4) * (int64_t)sizeof(float);
+  p.workspace = p.pieces_at + (int64_t)p.blocks * kItemPiecesBytes;
   return p;
 }
 
 hipError_t launch_kv_attn(KvAttnArgs a, const KvAttnPlan& p, InType t, int32_t D, hipStream_t s) {
   a.n_workers = p.n_workers;
+  a.blocks = p.blocks;
+  a.min_steps = p.min_steps;
   a.tile_cols = p.tile_cols;
   a.col_tiles = p.col_tiles;
   a.by_group = fast_div((uint32_t)(a.n_q_heads / a.geom.n_kv_heads));

@@ -180,15 +180,17 @@ struct KvAttnArgs {
   float* lse;                  // optional
   float* part;                 // partial results (workspace)
   // the plan
-  void* pieces;                // [n_workers] items done in pieces
-  int32_t n_workers;           // 0: one workgroup per item; else equal runs of all steps
+  void* pieces;                // [blocks] items done in pieces
+  int32_t n_workers;           // 0: one workgroup per item; else items are cut into pieces
+  int32_t blocks;              // workgroups
+  int32_t min_steps;           // of a piece
   int32_t tile_cols;           // query columns of an item
   int32_t col_tiles;           // items per sequence and kv head
   FastDiv by_group, by_heads, by_tile_cols, by_col_tiles, by_pairs;   // pairs: sequence, kv head
 };
 constexpr int kItemPiecesBytes = 32;
 struct KvAttnPlan {
-  int32_t n_workers, tile_cols, col_tiles, nq;
+  int32_t n_workers, blocks, min_steps, tile_cols, col_tiles, nq;
   bool prefill;                // kvprefill.hip
   int64_t pieces_at;           // byte offset in the workspace
   int64_t workspace;           // bytes
