@@ -155,7 +155,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t granule_buffer(const KvAttnArg
 
 constexpr int kStream = 2;         // cache policy of loads: non-temporal
 
-template <int N, int POLICY = 0>
+template <int N, int POLICY>
 __device__ __forceinline__ void load_dwords(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t* d) {
   if constexpr (N == 2) {
     const auto x = __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, POLICY);

@@ -67,6 +67,24 @@ __device__ __forceinline__ f32x16 zeros16() {
   return x;
 }
 
+// Plain loads of a granule's pieces (buffer loads, whose descriptors take scalar registers, were
+// slower here: head dimension 256 1376 us against 1322 us)
+template <int N>
+__device__ __forceinline__ void read_dwords(const uint8_t* p, uint32_t* d) {
+  if constexpr (N == 2) {
+    const u32x2 x = *reinterpret_cast<const u32x2*>(p);
+    d[0] = x[0];
+    d[1] = x[1];
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const u32x4 x = *reinterpret_cast<const u32x4*>(p + 4 * i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) d[i + e] = x[e];
+    }
+  }
+}
+
 template <int D>
 __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs a) {
   constexpr bool PIPE = D <= 128;
@@ -117,23 +135,24 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
     auto granule = [&](int32_t s, int32_t id) {
       int32_t gr = (begin + s * TOK) / 16 + gran;
       gr = gr < last_granule ? gr : last_granule;
-      return granule_buffer<D>(a, id, kh * per_head + (gr & (per_head - 1)));
+      return a.cache + (int64_t)id * a.geom.page_bytes +
+             (int64_t)(kh * per_head + (gr & (per_head - 1))) * kv_granule_bytes(D);
     };
     // (D = 256: a wave holds either)
     uint32_t rk[KD] = {}, rv_[D == 256 ? 1 : KD] = {}, ksc = 0, vsc_ = 0;
     uint32_t* const rv = D == 256 ? rk : rv_;
     uint32_t& vsc = D == 256 ? ksc : vsc_;
     auto load_k = [&](int32_t s, int32_t id) {
-      const __amdgpu_buffer_rsrc_t p = granule(s, id);
-      load_dwords<KD>(p, lane * (D / 8), rk);
-      if constexpr (D == 64) ksc = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(p, lane, 8 * D, 0);
-      else if constexpr (D == 128) ksc = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(p, lane * 2, 8 * D, 0);
-      else ksc = __builtin_amdgcn_raw_buffer_load_b32(p, lane * 4, 8 * D, 0);
+      const uint8_t* p = granule(s, id);
+      read_dwords<KD>(p + lane * (D / 8), rk);
+      if constexpr (D == 64) ksc = p[8 * D + lane];
+      else if constexpr (D == 128) ksc = *reinterpret_cast<const uint16_t*>(p + 8 * D + 2 * lane);
+      else ksc = *reinterpret_cast<const uint32_t*>(p + 8 * D + 4 * lane);
     };
     auto load_v = [&](int32_t s, int32_t id) {
-      const __amdgpu_buffer_rsrc_t p = granule(s, id);
-      load_dwords<KD>(p, lane * (D / 8) + 9 * D, rv);
-      vsc = __builtin_amdgcn_raw_buffer_load_b32(p, ((lane >> 4) * (D / 16) + (lane & 15) * D / 256) * 4, 17 * D, 0);
+      const uint8_t* p = granule(s, id);
+      read_dwords<KD>(p + 9 * D + lane * (D / 8), rv);
+      vsc = *reinterpret_cast<const uint32_t*>(p + 17 * D + ((lane >> 4) * (D / 16) + (lane & 15) * D / 256) * 4);
       // scales of tokens past the end are cleared: their bytes may be NaN
       const int32_t left = seq.n - (begin + s * TOK + 16 * gran + 4 * (lane >> 4));
       if (left < 4) vsc = left <= 0 ? 0u : vsc & ((1u << (8 * left)) - 1u);
