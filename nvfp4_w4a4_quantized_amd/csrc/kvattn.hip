@@ -643,29 +643,55 @@ hipError_t launch(const KvAttnArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((k_kv_attn<D, NQ, true, F32>), dim3((unsigned)blocks), dim3(64 * kAttnWaves), 0, s, a);
   else
     hipLaunchKernelGGL((k_kv_attn<D, NQ, false, F32>), dim3((unsigned)blocks), dim3(64 * kAttnWaves), 0, s, a);
-  hipError_t e = hipGetLastError();
-  if (e == hipSuccess && a.n_workers) {
-    const unsigned columns = (unsigned)a.blocks * a.tile_cols;
-    if (a.n_workers > 8 * (a.blocks - a.n_workers))             // more than 8 pieces an item
-      hipLaunchKernelGGL((k_kv_join_many<D, F32>), dim3(columns), dim3(256), 0, s, a);
-    else
-      hipLaunchKernelGGL((k_kv_join<D, F32>), dim3((columns + 3) / 4), dim3(256), 0, s, a);
-    e = hipGetLastError();
-  }
-  return e;
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess && a.n_workers ? launch_kv_join(a, F32 ? InType::F32 : InType::BF16, D, s) : e;
+}
+
+template <int D, bool F32>
+hipError_t join(const KvAttnArgs& a, hipStream_t s) {
+  const unsigned columns = (unsigned)a.blocks * a.tile_cols;
+  if (a.n_workers > 8 * (a.blocks - a.n_workers))             // more than 8 pieces an item
+    hipLaunchKernelGGL((k_kv_join_many<D, F32>), dim3(columns), dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((k_kv_join<D, F32>), dim3((columns + 3) / 4), dim3(256), 0, s, a);
+  return hipGetLastError();
 }
 
 }  // namespace
+
+hipError_t launch_kv_join(const KvAttnArgs& a, InType t, int32_t D, hipStream_t s) {
+  const bool f32 = t == InType::F32;
+  if (D == 64) return f32 ? join<64, true>(a, s) : join<64, false>(a, s);
+  if (D == 128) return f32 ? join<128, true>(a, s) : join<128, false>(a, s);
+  return f32 ? join<256, true>(a, s) : join<256, false>(a, s);
+}
 
 KvAttnPlan kv_attn_plan(InType t, int64_t T, int32_t batch, int32_t n_q_heads, int32_t n_kv_heads, int32_t D,
                         int64_t max_q_len, int64_t max_kv_len, int64_t window) {
   KvAttnPlan p{};
   const int64_t cols = (max_q_len < T ? max_q_len : T) * (n_q_heads / n_kv_heads);
+  // From one full tile of query columns on, decoding a key once for all of them pays.  This
+  // kernel / kvprefill.hip, us: 1 x 16384 keys and 256 columns 64 / 53, 1024 columns 123 / 93; 8 x
+  // 4096 and 256 columns 81 / 66, but 128 columns 56 / 58; 32 x 4096 and 256 columns 245 / 175, but 128
+  // columns 127 / 146; head dimension 256, 1 x 16384, 512 columns 81 / 61; 64, 2 x 4096, 512 columns 44 / 35.
   if (t == InType::BF16 && cols >= kv_prefill_cols()) {
     p.prefill = true;
     p.tile_cols = kv_prefill_cols();
-    const int64_t tiles = (cols + p.tile_cols - 1) / p.tile_cols, most = ((int64_t)1 << 30) / ((int64_t)batch * n_kv_heads);
+    const int64_t pairs = (int64_t)batch * n_kv_heads, tiles = (cols + p.tile_cols - 1) / p.tile_cols;
+    const int64_t most = ((int64_t)1 << 30) / pairs;
     p.col_tiles = (int32_t)(tiles < most ? tiles : most);
+    const int64_t items = pairs * p.col_tiles;
+    p.blocks = (int32_t)items;
+    // Fewer items than compute units: cut along the keys, one workgroup a compute unit.
+    // Whole / cut: 8 items of 16384 keys 452 / 53 us, 128 items of 4096 keys
+    // 123 / 101.  (A lane of the kernel looks up a sequence: at most 64.)
+    if (items <= 160 && batch <= 64) {
+      p.n_workers = (int32_t)(256 - items / 2);
+      p.blocks = (int32_t)(p.n_workers + items);
+      p.min_steps = 2;
+      p.pieces_at = (int64_t)p.blocks * p.tile_cols * (D + 4) * (int64_t)sizeof(float);
+      p.workspace = p.pieces_at + (int64_t)p.blocks * kItemPiecesBytes;
+    }
     return p;
   }
   // two column blocks share a decoded granule where their registers fit
@@ -710,8 +736,8 @@ hipError_t launch_kv_attn(KvAttnArgs a, const KvAttnPlan& p, InType t, int32_t D
   a.by_tile_cols = fast_div((uint32_t)a.tile_cols);
   a.by_col_tiles = fast_div((uint32_t)a.col_tiles);
   a.by_pairs = fast_div((uint32_t)a.batch * (uint32_t)a.geom.n_kv_heads);
-  if (p.prefill) return launch_kv_prefill(a, D, s);
   a.pieces = reinterpret_cast<uint8_t*>(a.part) + p.pieces_at;
+  if (p.prefill) return launch_kv_prefill(a, D, s);
   const bool f32 = t == InType::F32;
   if (D == 64) {
     if (p.nq == 2) return f32 ? launch<64, 2, true>(a, s) : launch<64, 2, false>(a, s);

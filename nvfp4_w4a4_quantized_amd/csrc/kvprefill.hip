@@ -19,6 +19,11 @@
 // so that a wave's 16-byte reads of 32 rows, and the decoder's writes, spread over the banks.
 // D <= 128: tiles of 128 tokens, wave w loads and decodes granule w.  D = 256: 64 tokens (what LDS
 // holds), wave w granule w % 4, keys (w < 4) or values.
+//
+// A workgroup has one item (256 query columns of a kv head and sequence).  Where these are
+// fewer than the compute units, items are cut along the keys into equal pieces, one per
+// workgroup, which k_kv_join puts together, as in kvattn.hip: 256 columns of 16384 keys in 53 us
+// instead of 452.
 #include <type_traits>
 
 #include "kv_device.hpp"
@@ -85,7 +90,30 @@ __device__ __forceinline__ void read_dwords(const uint8_t* p, uint32_t* d) {
   }
 }
 
+// A tile of query columns: the keys it attends to, from granule-aligned `begin` on
+struct TileSpan {
+  int32_t begin, steps;
+};
 template <int D>
+__device__ __forceinline__ TileSpan tile_span(const KvAttnArgs& a, const SeqInfo& seq, int32_t tile, int group) {
+  const int32_t cols = seq.m * group, first = tile * kPrefillCols;
+  const Span s = span_of(seq, first, first + kPrefillCols < cols ? first + kPrefillCols : cols, a.by_group, a.window);
+  TileSpan t;
+  t.begin = s.lo & ~15;
+  t.steps = seq.n > 0 ? (s.hi - t.begin + kTok<D> - 1) / kTok<D> : 0;
+  return t;
+}
+__device__ __forceinline__ int32_t tiles_of(const SeqInfo& seq, int group) {
+  return (seq.m * group + kPrefillCols - 1) / kPrefillCols;
+}
+__device__ __forceinline__ int32_t planned_tiles(const KvAttnArgs& a, const SeqInfo& seq, int group) {
+  const int32_t t = tiles_of(seq, group);
+  return t < a.col_tiles ? t : a.col_tiles;
+}
+
+// SPLIT: workgroups have pieces of items instead of items (a template parameter: its
+// registers cost the other form 2 to 5 %)
+template <int D, bool SPLIT>
 __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs a) {
   constexpr bool PIPE = D <= 128;
   constexpr int TOK = kTok<D>, TILE = TOK * D * 2;               // bytes of one decoded tile, keys or values
@@ -99,25 +127,105 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int hkv = a.geom.n_kv_heads, group = (int)a.by_group.d;
-  const int pairs = a.batch * hkv;
-  // the longest spans (last tiles) start first; workgroups side by side differ in the head
-  const int turn = (int)blockIdx.x / a.by_pairs, pair = (int)blockIdx.x - turn * pairs;
-  const int b = pair / a.by_heads, kh = pair - b * hkv;
-  const SeqInfo seq = seq_info(a, b);
+  // this workgroup's item, and its steps [s_first, s_last) of it (s_last < 0: all)
+  int b, kh, tile0;
+  int32_t s_first = 0, s_last = -1;
+  SeqInfo seq;
+  if constexpr (!SPLIT) {
+    // the longest spans (last tiles) start first; workgroups side by side differ in the head
+    const int turn = (int)blockIdx.x / a.by_pairs, pair = (int)blockIdx.x - turn * (int)a.by_pairs.d;
+    b = pair / a.by_heads;
+    kh = pair - b * hkv;
+    seq = seq_info(a, b);
+    const int32_t tiles = tiles_of(seq, group);
+    tile0 = (tiles < a.col_tiles ? tiles : a.col_tiles) - 1 - turn;
+    if (tile0 < 0) return;
+  } else {
+    // Few items: each is cut into equal pieces of at most S steps (tokens of a tile), S all
+    // steps of the call by n_workers, as in kvattn.hip; a lane counts every 64th tile.
+    const SeqTable seqs(a, lane);
+    float total = 0.0f;
+    for (b = 0; b < a.batch; ++b) {
+      seq = seqs.at(a, b);
+      const int32_t tiles = planned_tiles(a, seq, group);
+      for (int32_t t = lane; t < tiles; t += 64) total += (float)tile_span<D>(a, seq, t, group).steps;
+    }
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) total += __shfl_xor(total, off);
+    int32_t S = (int32_t)(total * (float)hkv * 1.0001f / (float)a.n_workers) + 1;
+    S = S < a.min_steps ? a.min_steps : S;
+    auto pieces_of = [&](int32_t steps) {
+      return steps <= S ? 1 : (int32_t)((uint32_t)(steps + S - 1) / (uint32_t)S);
+    };
+    int32_t rest = (int32_t)blockIdx.x, tiles = 0, of_head = 0;
+    for (b = 0; b < a.batch; ++b) {
+      seq = seqs.at(a, b);
+      tiles = planned_tiles(a, seq, group);
+      of_head = 0;
+      for (int32_t t = lane; t < tiles; t += 64) of_head += pieces_of(tile_span<D>(a, seq, t, group).steps);
+#pragma unroll
+      for (int off = 1; off < 64; off <<= 1) of_head += __shfl_xor(of_head, off);
+      of_head = __builtin_amdgcn_readfirstlane(of_head);
+      if (rest < of_head * hkv) break;
+      rest -= of_head * hkv;
+    }
+    if (b == a.batch) {
+      if (threadIdx.x == 0) static_cast<ItemPieces*>(a.pieces)[blockIdx.x].cols = 0;
+      return;
+    }
+    kh = (int32_t)((uint32_t)rest / (uint32_t)of_head);
+    rest -= kh * of_head;
+    int32_t pieces = 1;
+    for (int32_t t0 = 0;; t0 += 64) {
+      const int32_t own = t0 + lane < tiles ? pieces_of(tile_span<D>(a, seq, t0 + lane, group).steps) : 0;
+      int32_t upto = own;
+#pragma unroll
+      for (int off = 1; off < 64; off <<= 1) {
+        const int32_t x = __shfl_up(upto, off);
+        if (lane >= off) upto += x;
+      }
+      const uint64_t past = __builtin_amdgcn_ballot_w64(upto > rest);
+      if (past) {
+        const int first = __builtin_ctzll(past);
+        tile0 = t0 + first;
+        pieces = __builtin_amdgcn_readlane(own, first);
+        rest -= __builtin_amdgcn_readlane(upto - own, first);
+        break;
+      }
+      rest -= __builtin_amdgcn_readlane(upto, 63);
+    }
+    const int32_t steps = tile_span<D>(a, seq, tile0, group).steps;
+    if (pieces > 1) {
+      const int32_t q = (int32_t)((uint32_t)steps / (uint32_t)pieces), more = steps - q * pieces;
+      s_first = rest * q + (rest < more ? rest : more);
+      s_last = s_first + q + (rest < more);
+    }
+    if (threadIdx.x == 0) {
+      const int32_t fc = tile0 * kPrefillCols, left = seq.m * group - fc;
+      ItemPieces* const p = static_cast<ItemPieces*>(a.pieces) + blockIdx.x;
+      p->cols = pieces > 1 && rest == 0 ? (left < kPrefillCols ? left : kPrefillCols) : 0;
+      p->pieces = pieces;
+      p->q0 = seq.q0;
+      p->first_col = fc;
+      p->kh = kh;
+    }
+  }
   const int32_t cols = seq.m * group;
-  const int32_t tiles = (cols + kPrefillCols - 1) / kPrefillCols;
   const int32_t last_page = (seq.n - 1) >> a.geom.page_shift, last_granule = (seq.n - 1) >> 4;
   const int per_head = 1 << (a.geom.page_shift - 4);
   const float kg = a.k_gscale[kh], vg = a.v_gscale[kh];
   const int h = lane >> 5, c32 = lane & 31;
   const int gran = D == 256 ? wave & 3 : wave;      // this wave's granule of a tile
 
-  for (int32_t tile = tiles - 1 - turn; tile >= 0; tile -= a.col_tiles) {
+  // tiles past the planned ones are done whole, with the first piece of one of those
+  for (int32_t tile = tile0; (int64_t)tile * kPrefillCols < cols; tile += a.col_tiles) {
+    const bool whole = !SPLIT || s_last < 0 || tile != tile0;
+    if (SPLIT && tile != tile0 && s_first > 0) break;
     const int32_t col_first = tile * kPrefillCols;
     const int32_t col_end = col_first + kPrefillCols < cols ? col_first + kPrefillCols : cols;
-    const Span all = span_of(seq, col_first, col_end, a.by_group, a.window);
-    const int32_t begin = all.lo & ~15;
-    const int32_t steps = seq.n > 0 ? (all.hi - begin + TOK - 1) / TOK : 0;
+    const TileSpan span = tile_span<D>(a, seq, tile, group);
+    const int32_t begin = whole ? span.begin : span.begin + s_first * TOK;
+    const int32_t steps = whole ? span.steps : s_last - s_first;
 
     // this wave's columns (past the tile's end: its last one again, never written)
     const int32_t col0 = col_first + 32 * wave;
@@ -441,28 +549,47 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
 
     l = sum_xor32(l);
     if (col0 + c32 < col_end) {
-      const float f = l > 0.0f ? vg / l : 0.0f;
-      uint16_t* dst = reinterpret_cast<uint16_t*>(a.o) + (seq.q0 + qi) * a.ldo + (int64_t)head * D + 4 * h;
+      if (whole) {
+        const float f = l > 0.0f ? vg / l : 0.0f;
+        uint16_t* dst = reinterpret_cast<uint16_t*>(a.o) + (seq.q0 + qi) * a.ldo + (int64_t)head * D + 4 * h;
 #pragma unroll
-      for (int i = 0; i < NB; ++i)
+        for (int i = 0; i < NB; ++i)
 #pragma unroll
-        for (int e = 0; e < 16; e += 4)
-          *reinterpret_cast<u32x2*>(dst + 32 * i + 2 * e) =
-              u32x2{pack_bf16(acc[i][e] * f, acc[i][e + 1] * f), pack_bf16(acc[i][e + 2] * f, acc[i][e + 3] * f)};
-      if (a.lse && h == 0)
-        a.lse[(seq.q0 + qi) * a.n_q_heads + head] = l > 0.0f ? (m + __builtin_log2f(l)) * kLn2 : -__builtin_inff();
+          for (int e = 0; e < 16; e += 4)
+            *reinterpret_cast<u32x2*>(dst + 32 * i + 2 * e) =
+                u32x2{pack_bf16(acc[i][e] * f, acc[i][e + 1] * f), pack_bf16(acc[i][e + 2] * f, acc[i][e + 3] * f)};
+        if (a.lse && h == 0)
+          a.lse[(seq.q0 + qi) * a.n_q_heads + head] = l > 0.0f ? (m + __builtin_log2f(l)) * kLn2 : -__builtin_inff();
+      } else {
+        float* dst = piece_at(a, D, blockIdx.x, col0 + c32 - col_first);
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+          for (int e = 0; e < 16; e += 4)
+            *reinterpret_cast<f32x4*>(dst + 4 + 32 * i + 2 * e + 4 * h) =
+                f32x4{acc[i][e], acc[i][e + 1], acc[i][e + 2], acc[i][e + 3]};
+        if (h == 0) {
+          dst[0] = m;
+          dst[1] = l;
+        }
+      }
     }
   }
 }
 
-template <int D>
+template <int D, bool SPLIT>
 hipError_t launch(const KvAttnArgs& a, hipStream_t s) {
   constexpr int bytes = 4 * kTok<D> * D * 2;          // two tiles of keys, two of values
-  const hipError_t e = lds_limit_once<k_kv_prefill<D>>(bytes);
+  const hipError_t e = lds_limit_once<k_kv_prefill<D, SPLIT>>(bytes);
   if (e != hipSuccess) return e;
-  const int64_t blocks = (int64_t)a.batch * a.geom.n_kv_heads * a.col_tiles;
-  hipLaunchKernelGGL((k_kv_prefill<D>), dim3((unsigned)blocks), dim3(64 * kPrefillWaves), bytes, s, a);
-  return hipGetLastError();
+  hipLaunchKernelGGL((k_kv_prefill<D, SPLIT>), dim3((unsigned)a.blocks), dim3(64 * kPrefillWaves), bytes, s, a);
+  const hipError_t launched = hipGetLastError();
+  return SPLIT && launched == hipSuccess ? launch_kv_join(a, InType::BF16, D, s) : launched;
+}
+
+template <int D>
+hipError_t launch(const KvAttnArgs& a, hipStream_t s) {
+  return a.n_workers ? launch<D, true>(a, s) : launch<D, false>(a, s);
 }
 
 }  // namespace

@@ -199,8 +199,10 @@ KvAttnPlan kv_attn_plan(InType t, int64_t T, int32_t batch, int32_t n_q_heads, i
                         int64_t max_q_len, int64_t max_kv_len, int64_t window);
 hipError_t launch_kv_attn(KvAttnArgs a, const KvAttnPlan& p, InType t, int32_t D, hipStream_t s);
 
-// kvprefill.hip: bf16, whole items of kv_prefill_cols() query columns (a.col_tiles per
-// sequence and kv head in the grid; any number is right).
+// joins the pieces that either kernel left
+hipError_t launch_kv_join(const KvAttnArgs& a, InType t, int32_t D, hipStream_t s);
+
+// kvprefill.hip: bf16, items of kv_prefill_cols() query columns.
 int32_t kv_prefill_cols();
 hipError_t launch_kv_prefill(const KvAttnArgs& a, int32_t D, hipStream_t s);
 

@@ -282,6 +282,24 @@ def test_long_queries(nv, dtype, D, Hq, Hkv, n, m, window):
     p.check(p.run(nv, window), window, rows=rows)
 
 
+@pytest.mark.parametrize("D,Hq,Hkv,kv,m", [
+    (64, 56, 56, [400, 65, 0], [300, 65, 7]), (128, 64, 32, [333, 150, 1], [140, 150, 1]),
+    (256, 56, 28, [290, 129, 40], [150, 3, 0]), (128, 4, 2, [300] + [5] * 89, [129] + [1] * 89)])
+@pytest.mark.parametrize("window", [0, 70])
+def test_prompts_of_many_items(nv, D, Hq, Hkv, kv, m, window):
+    # more (sequence, head, 256 query columns) than are cut along the keys
+    p = Problem(nv, kv, m, Hq, Hkv, D, 16, "bf16", seed=D + len(kv))
+    rows = sorted({0, 1, 31, 32, 127, 128, m[0] - 1, m[0], m[0] + 1})
+    p.check(p.run(nv, window), window, rows=rows)
+
+
+def test_prompt_hints_that_are_too_low(nv):
+    # the tiles of columns that were not planned for, whole and cut along the keys
+    for kv, m, Hq, Hkv, hint in (([900, 4, 300], [600, 1, 9], 4, 1, 64), ([300, 290], [280, 290], 192, 96, 128)):
+        p = Problem(nv, kv, m, Hq, Hkv, 64, 16, "bf16", seed=8)
+        p.check(p.run(nv, hints=(hint, 10)), rows=[0, 1, 63, 64, 129, 255, 256, 279, 280, 281])
+
+
 def test_hints_that_are_too_low(nv):
     p = Problem(nv, [900, 4, 300], [40, 1, 9], 4, 2, 128, 16, "bf16", seed=5)
     for hints in ((1, 1), (3, 500), (1, 5000), (40, 0)):
