@@ -15,8 +15,11 @@
 //
 // LDS, two decoded tiles of each (a tile is decoded while the one before is used; one barrier
 // per tile):
-//   K   [tokens][D], V^T [D][tokens], the 16-byte chunks of a row swizzled by the row
-// so that a wave's 16-byte reads of 32 rows, and the decoder's writes, spread over the banks.
+//   K   [tokens][D], V^T [D][tokens], each row one 16-byte chunk longer than its data
+// so that a wave's 16-byte reads of 16 rows meet every bank once, and every address is one base
+// plus a constant (with exclusive-or swizzles instead: 14 more vector instructions on the 100 of a
+// block of 32 tokens, prompts of 8192 tokens 572 us against 543).  Row 16 i + p of V^T is dimension
+// p D/16 + i, so that the 16 parts of a quad are decoded into 16 neighbouring rows.
 // D <= 128: tiles of 128 tokens, wave w loads and decodes granule w.  D = 256: 64 tokens (what LDS
 // holds), wave w granule w % 4, keys (w < 4) or values.
 //
@@ -41,24 +44,15 @@ __device__ __forceinline__ f32x16 mfma32(f16x8 a, f16x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
 
-// Places in a decoded tile.  The swizzles are exclusive ors on the chunk number (the bits of
-// the address from 4 on, below the row's), so that the places of a lane's chunks follow from
-// one base by a constant exclusive or, and those of further rows by a constant offset.  16
-// consecutive rows (a 16-byte read) use every 16-byte place of 256 bytes once, and so do the
-// decoder's writes, D / 16 rows apart, as far as there are places.
+// Places in the decoded tiles: rows of 16-byte chunks, one chunk longer than their data.
 template <int D>
-constexpr int kKMask = D == 64 ? 7 : 15;
+constexpr int kKRow = 2 * D + 16;
 template <int D>
-__device__ __forceinline__ int k_place(int t, int c) {
-  return t * 2 * D + ((c ^ ((D == 64 ? t >> 1 : t) & kKMask<D>)) << 4);
-}
-
+constexpr int kVRow = 2 * kTok<D> + 16;
 template <int D>
-constexpr int kVMask = D == 256 ? 7 : 15;
+constexpr int kKTile = kTok<D> * kKRow<D>;
 template <int D>
-constexpr int v_swizzle(int d) { return (D == 256 ? (d >> 1) ^ (d >> 4) : d ^ (d >> 3)) & kVMask<D>; }
-template <int D>
-__device__ __forceinline__ int v_place(int d, int c) { return d * 2 * kTok<D> + ((c ^ v_swizzle<D>(d)) << 4); }
+constexpr int kVTile = D * kVRow<D>;
 
 template <typename T>
 __device__ __forceinline__ __attribute__((address_space(3))) T& lds_at(uint32_t at) {
@@ -116,7 +110,7 @@ __device__ __forceinline__ int32_t planned_tiles(const KvAttnArgs& a, const SeqI
 template <int D, bool SPLIT>
 __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs a) {
   constexpr bool PIPE = D <= 128;
-  constexpr int TOK = kTok<D>, TILE = TOK * D * 2;               // bytes of one decoded tile, keys or values
+  constexpr int TOK = kTok<D>;
   constexpr int KD = D / 32;                       // dwords of codes a lane decodes, keys and values each
   constexpr int NB = D / 32;                       // 32-row blocks of O^T
   constexpr int KS = D / 16;                       // K steps of the first product
@@ -246,29 +240,36 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
       return a.cache + (int64_t)id * a.geom.page_bytes +
              (int64_t)(kh * per_head + (gr & (per_head - 1))) * kv_granule_bytes(D);
     };
+    // the quad of tokens and part of a granule's values that this lane decodes
+    const int quad = lane >> 4, part = lane & 15;
     // (D = 256: a wave holds either)
     uint32_t rk[KD] = {}, rv_[D == 256 ? 1 : KD] = {}, ksc = 0, vsc_ = 0;
     uint32_t* const rv = D == 256 ? rk : rv_;
     uint32_t& vsc = D == 256 ? ksc : vsc_;
     auto load_k = [&](int32_t s, int32_t id) {
       const uint8_t* p = granule(s, id);
-      read_dwords<KD>(p + lane * (D / 8), rk);
-      if constexpr (D == 64) ksc = p[8 * D + lane];
-      else if constexpr (D == 128) ksc = *reinterpret_cast<const uint16_t*>(p + 8 * D + 2 * lane);
-      else ksc = *reinterpret_cast<const uint32_t*>(p + 8 * D + 4 * lane);
+      if constexpr (D == 256) {          // a quarter of either half of a token's row
+        const uint8_t *c = p + (lane >> 2) * 128 + (lane & 3) * 16, *f = p + 8 * D + (lane >> 2) * 16 + (lane & 3) * 2;
+        read_dwords<4>(c, rk);
+        read_dwords<4>(c + 64, rk + 4);
+        ksc = *reinterpret_cast<const uint16_t*>(f) | (uint32_t)*reinterpret_cast<const uint16_t*>(f + 8) << 16;
+      } else {                           // a quarter of a token's row
+        read_dwords<KD>(p + lane * (D / 8), rk);
+        ksc = D == 64 ? p[8 * D + lane] : *reinterpret_cast<const uint16_t*>(p + 8 * D + 2 * lane);
+      }
     };
     auto load_v = [&](int32_t s, int32_t id) {
       const uint8_t* p = granule(s, id);
-      read_dwords<KD>(p + 9 * D + lane * (D / 8), rv);
-      vsc = *reinterpret_cast<const uint32_t*>(p + 17 * D + ((lane >> 4) * (D / 16) + (lane & 15) * D / 256) * 4);
+      read_dwords<KD>(p + 9 * D + (16 * quad + part) * (D / 8), rv);
+      vsc = *reinterpret_cast<const uint32_t*>(p + 17 * D + (quad * (D / 16) + part * D / 256) * 4);
       // scales of tokens past the end are cleared: their bytes may be NaN
-      const int32_t left = seq.n - (begin + s * TOK + 16 * gran + 4 * (lane >> 4));
+      const int32_t left = seq.n - (begin + s * TOK + 16 * gran + 4 * quad);
       if (left < 4) vsc = left <= 0 ? 0u : vsc & ((1u << (8 * left)) - 1u);
     };
     // decode dword i of the loaded keys: a 16-byte chunk of a token's row
     auto decode_k = [&](uint32_t kb, int i) {               // kb: the lane's first chunk in the tile
       const f16x2 sc = bcast(scale_pair_f16(D == 256 ? ksc >> (16 * (i / 4)) : ksc), D == 64 ? 0 : (i >> 1) & 1);
-      lds_at<f16x8>(kb ^ (i << 4)) = decode8_f16(rk[i], sc);
+      lds_at<f16x8>(kb + 16 * i + (i < 4 ? 0 : 192)) = decode8_f16(rk[i], sc);
     };
     // decode byte i of the four tokens' words of the loaded values: elements 2 i and 2 i + 1
     auto decode_v = [&](uint32_t vb, int i) {               // vb: the lane's first element in the tile
@@ -280,7 +281,7 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
       pair_tokens(w, lo, hi);
       typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
       auto put = [&](int j, f16x2 x, f16x2 y) {
-        lds_at<f16x4>((vb ^ ((D == 256 ? j >> 1 : j) << 4)) + j * 2 * TOK) = f16x4{x[0], x[1], y[0], y[1]};
+        lds_at<f16x4>(vb + j * 16 * kVRow<D>) = f16x4{x[0], x[1], y[0], y[1]};
       };
       auto two = [&](auto sel) {
         constexpr int SEL = decltype(sel)::value;
@@ -292,8 +293,8 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
       else if (i % 4 == 2) two(std::integral_constant<int, 2>{});
       else two(std::integral_constant<int, 3>{});
     };
-    const int kwbase = k_place<D>(16 * gran + lane / 4, (lane % 4) * KD);
-    const int vwbase = v_place<D>((lane & 15) * (D / 16), 2 * gran + ((lane >> 4) & 1)) + (lane >> 5) * 8;
+    const int kwbase = (16 * gran + lane / 4) * kKRow<D> + (lane % 4) * (D == 256 ? 4 : KD) * 16;
+    const int vwbase = part * kVRow<D> + 32 * gran + 16 * (quad & 1) + 8 * (quad >> 1);
 
     int32_t id_next = 0;
     __syncthreads();                               // the tile before is done with LDS
@@ -348,14 +349,12 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
     constexpr int PF = D == 256 ? 2 : 3;
     f16x8 kf[PF + 1], vf_[D == 256 ? 1 : PF + 1];
     f16x8* const vf = D == 256 ? kf : vf_;           // one at a time there
-    const int kbase = k_place<D>(c32, h), vbase = v_place<D>(c32, h);
+    const int kbase = c32 * kKRow<D> + 16 * h, vbase = c32 * kVRow<D> + 16 * h;
     auto read_k = [&](uint32_t kb, int b, int i) {          // kb: kbase in the tile
-      constexpr int M = kKMask<D>;
-      kf[i % (PF + 1)] = lds_at<f16x8>((kb ^ ((2 * i & M) << 4)) + 64 * D * b + ((2 * i & ~M) << 4));
+      kf[i % (PF + 1)] = lds_at<f16x8>(kb + 32 * kKRow<D> * b + 32 * i);
     };
     auto read_v = [&](uint32_t vb, int b, int i) {
-      const int blk = i % NB, c = 2 * (2 * b + i / NB);
-      vf[i % (PF + 1)] = lds_at<f16x8>((vb ^ ((c ^ v_swizzle<D>(32 * blk)) << 4)) + 64 * TOK * blk);
+      vf[i % (PF + 1)] = lds_at<f16x8>(vb + 32 * kVRow<D> * (i % NB) + 32 * (2 * b + i / NB));
     };
     auto score_piece = [&](f32x16& sc, int i) { sc = mfma32(kf[i % (PF + 1)], qf[i], sc); };
     auto output_piece = [&](const f16x8 p[2], int i) { acc[i % NB] = mfma32(vf[i % (PF + 1)], p[i / NB], acc[i % NB]); };
@@ -369,6 +368,8 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
           const int32_t t = 8 * (e / 4) + e % 4;
           if (t >= upto || t < from) sc[e] = -__builtin_inff();
         }
+        // masked in place (as two versions, the scores were copied in every block)
+        asm volatile("" : "+v"(sc));
       }
       const float top = max_xor32(max_of(sc)) * csc;
       const float m1 = top > m + 15.0f ? __builtin_fmaxf(m, top - 7.0f) : m;
@@ -392,8 +393,8 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
         for (int i = 0; i < NB; ++i) acc[i] *= f;
       }
     };
-    auto k_tile = [&](int32_t s) { return lds + (uint32_t)((s & 1) * TILE); };
-    auto v_tile = [&](int32_t s) { return lds + (uint32_t)(2 * TILE + (s & 1) * TILE); };
+    auto k_tile = [&](int32_t s) { return lds + (uint32_t)((s & 1) * kKTile<D>); };
+    auto v_tile = [&](int32_t s) { return lds + (uint32_t)(2 * kKTile<D> + (s & 1) * kVTile<D>); };
     // an address that the compiler does not take out of the loop: with every chunk's address
     // in a register of its own the kernel spills
     auto fresh = [](uint32_t x) {
@@ -418,8 +419,8 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
       if constexpr (PIPE) {
         // the values "before" tile 0 meet weights of zero: they must not be NaN
 #pragma unroll
-        for (int i = 0; i < TILE / (16 * 64 * kPrefillWaves); ++i)
-          lds_at<u32x4>(v_tile(1) + (i * 64 * kPrefillWaves + threadIdx.x) * 16) = u32x4{0, 0, 0, 0};
+        for (int at = 16 * threadIdx.x; at < kVTile<D>; at += 16 * 64 * kPrefillWaves)
+          lds_at<u32x4>(v_tile(1) + at) = u32x4{0, 0, 0, 0};
       }
       __syncthreads();
       if constexpr (PIPE) {
@@ -547,27 +548,29 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
       }
     }
 
+    // elements g and g + 8 of the blocks: consecutive dimensions, those of a part of the granule
     l = sum_xor32(l);
     if (col0 + c32 < col_end) {
+      auto first_of = [&](int g) { return ((g & 4) * 2 + 4 * h + (g & 3)) * (D / 16); };
       if (whole) {
         const float f = l > 0.0f ? vg / l : 0.0f;
-        uint16_t* dst = reinterpret_cast<uint16_t*>(a.o) + (seq.q0 + qi) * a.ldo + (int64_t)head * D + 4 * h;
+        uint16_t* dst = reinterpret_cast<uint16_t*>(a.o) + (seq.q0 + qi) * a.ldo + (int64_t)head * D;
 #pragma unroll
-        for (int i = 0; i < NB; ++i)
+        for (int g = 0; g < 8; ++g)
 #pragma unroll
-          for (int e = 0; e < 16; e += 4)
-            *reinterpret_cast<u32x2*>(dst + 32 * i + 2 * e) =
-                u32x2{pack_bf16(acc[i][e] * f, acc[i][e + 1] * f), pack_bf16(acc[i][e + 2] * f, acc[i][e + 3] * f)};
+          for (int i = 0; i < NB; i += 2)
+            *reinterpret_cast<u32x2*>(dst + first_of(g) + 2 * i) =
+                u32x2{pack_bf16(acc[i][g] * f, acc[i][g + 8] * f), pack_bf16(acc[i + 1][g] * f, acc[i + 1][g + 8] * f)};
         if (a.lse && h == 0)
           a.lse[(seq.q0 + qi) * a.n_q_heads + head] = l > 0.0f ? (m + __builtin_log2f(l)) * kLn2 : -__builtin_inff();
       } else {
         float* dst = piece_at(a, D, blockIdx.x, col0 + c32 - col_first);
 #pragma unroll
-        for (int i = 0; i < NB; ++i)
+        for (int g = 0; g < 8; ++g)
 #pragma unroll
-          for (int e = 0; e < 16; e += 4)
-            *reinterpret_cast<f32x4*>(dst + 4 + 32 * i + 2 * e + 4 * h) =
-                f32x4{acc[i][e], acc[i][e + 1], acc[i][e + 2], acc[i][e + 3]};
+          for (int i = 0; i < NB; i += 2)
+            *reinterpret_cast<f32x4*>(dst + 4 + first_of(g) + 2 * i) =
+                f32x4{acc[i][g], acc[i][g + 8], acc[i + 1][g], acc[i + 1][g + 8]};
         if (h == 0) {
           dst[0] = m;
           dst[1] = l;
@@ -579,7 +582,7 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
 
 template <int D, bool SPLIT>
 hipError_t launch(const KvAttnArgs& a, hipStream_t s) {
-  constexpr int bytes = 4 * kTok<D> * D * 2;          // two tiles of keys, two of values
+  constexpr int bytes = 2 * (kKTile<D> + kVTile<D>);
   const hipError_t e = lds_limit_once<k_kv_prefill<D, SPLIT>>(bytes);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((k_kv_prefill<D, SPLIT>), dim3((unsigned)a.blocks), dim3(64 * kPrefillWaves), bytes, s, a);
