@@ -447,7 +447,8 @@ NVFP4_API int32_t nvfp4_kv_attention(const void* q, int32_t dtype, int64_t ldq, 
                            const float* k_gscale, const float* v_gscale, float scale, int32_t window, void* o,
                            int64_t ldo, float* lse, void* workspace, int64_t workspace_bytes, void* stream);
 
-/* Workspace bytes of such a call (host only; 0 where it needs none). */
+/* Workspace bytes of a call of just these sizes (host only; 0 where it needs none).  A call of
+ * smaller ones may need more: the largest of all calls to come is what a program keeps. */
 NVFP4_API int32_t nvfp4_kv_attention_workspace(int32_t dtype, int64_t T, int32_t batch, int32_t n_q_heads, int32_t n_kv_heads,
                                      int32_t head_dim, int64_t max_q_len, int64_t max_kv_len, int64_t* bytes_out);
 

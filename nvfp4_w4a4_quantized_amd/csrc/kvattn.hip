@@ -685,8 +685,14 @@ KvAttnPlan kv_attn_plan(InType t, int64_t T, int32_t batch, int32_t n_q_heads, i
     // Fewer items than compute units: cut along the keys, one workgroup a compute unit.
     // Whole / cut: 8 items of 16384 keys 452 / 53 us, 128 items of 4096 keys
     // 123 / 101.  (A lane of the kernel looks up a sequence: at most 64.)
-    if (items <= 160 && batch <= 64) {
-      p.n_workers = (int32_t)(256 - items / 2);
+    const bool few = items <= 160;
+    // So are the items of sequences of unlike lengths, which n_tokens shows, where the longest
+    // run far longer than the others: 3 x up to 2048 new tokens of up to 16384 (head dimension
+    // 256) 1337 / 903 us, 4 x 1024 of 16384 814 / 587, 2 x 2048 of 8192 387 / 312.  Equal lengths lose by it, 4 x
+    // 1024 of 16384 974 / 1004 us, 1 x 2048 of 8192 245 / 286, and short ones, 16 x 1024 of 4096 (64) 131 / 148.
+    const bool unlike = 8 * T <= 7 * (int64_t)batch * max_q_len && items <= 512 && max_kv_len >= 64 * (D == 256 ? 64 : 128);
+    if ((few || unlike) && batch <= 64) {
+      p.n_workers = (int32_t)(few ? 256 - items / 2 : 384);
       p.blocks = (int32_t)(p.n_workers + items);
       p.min_steps = 2;
       p.pieces_at = (int64_t)p.blocks * p.tile_cols * (D + 4) * (int64_t)sizeof(float);

@@ -293,6 +293,19 @@ def test_prompts_of_many_items(nv, D, Hq, Hkv, kv, m, window):
     p.check(p.run(nv, window), window, rows=rows)
 
 
+@pytest.mark.parametrize("D,Hq,Hkv,kv,m", [
+    (64, 56, 56, [400, 65, 0], [300, 65, 7]), (128, 64, 32, [1333, 150, 1], [140, 150, 1]),
+    (256, 56, 28, [290, 129, 40], [150, 3, 0])])
+def test_prompts_of_unlike_lengths(nv, D, Hq, Hkv, kv, m):
+    # as many items, cut all the same: new tokens of unlike numbers under a bound of many keys
+    p = Problem(nv, kv, m, Hq, Hkv, D, 16, "bf16", seed=D + 1)
+    assert nv.nvfp4_kv_attention_workspace(p.T, 3, Hq, Hkv, D, max(m), 20000, p.q.dtype) > 0
+    assert nv.nvfp4_kv_attention_workspace(p.T, 3, Hq, Hkv, D, max(m), max(kv), p.q.dtype) == 0
+    rows = sorted({0, 1, 31, 32, 127, 128, m[0] - 1, m[1] - 1})
+    p.check(p.run(nv, hints=(max(m), 20000)), rows=rows)
+    p.check(p.run(nv, 70, hints=(max(m), 20000)), 70, rows=rows)
+
+
 def test_prompt_hints_that_are_too_low(nv):
     # the tiles of columns that were not planned for, whole and cut along the keys
     for kv, m, Hq, Hkv, hint in (([900, 4, 300], [600, 1, 9], 4, 1, 64), ([300, 290], [280, 290], 192, 96, 128)):
