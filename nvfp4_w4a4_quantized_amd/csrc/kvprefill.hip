@@ -24,9 +24,16 @@
 // holds), wave w granule w % 4, keys (w < 4) or values.
 //
 // A workgroup has one item (256 query columns of a kv head and sequence).  Where these are
-// fewer than the compute units, items are cut along the keys into equal pieces, one per
+// fewer than the compute units, or of unlike lengths, items are cut along the keys into equal pieces, one per
 // workgroup, which k_kv_join puts together, as in kvattn.hip: 256 columns of 16384 keys in 53 us
 // instead of 452.
+//
+// What bounds it: matrix and vector instructions of two waves per SIMD that only partly overlap.  8192
+// tokens, 32 / 8 heads of 128: 543 us, 1013 TFLOP/s (a large f16 matrix product reaches 1193 at the
+// clock that its power leaves); the matrix unit is busy 48 % of the cycles, the vector unit 55 %,
+// LDS 36 %, and waves wait 32 %.  Head dimension 256, whose accumulators leave no registers for the
+// pipeline: 3 sequences of 300 to 2048 new tokens of up to 16384 902 us, 927 TFLOP/s.  64 columns a
+// wave at one wave per SIMD (512 registers) took 845 us where this took 606.
 #include <type_traits>
 
 #include "kv_device.hpp"
