@@ -11,6 +11,7 @@
 #include <mutex>
 #include <string>
 
+#include "kv_launch.hpp"
 #include "launch.hpp"
 
 namespace {

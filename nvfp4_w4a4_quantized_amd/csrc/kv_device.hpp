@@ -2,7 +2,7 @@
 #pragma once
 
 #include "kernel_common.hpp"
-#include "kv_layout.hpp"
+#include "kv_launch.hpp"
 
 namespace nvfp4 {
 namespace {

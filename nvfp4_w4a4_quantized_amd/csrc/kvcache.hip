@@ -10,7 +10,7 @@
 // (the rotated key is not rounded to the input type first) by the layer's exact
 // block-scale and code routines under one calibrated global scale per kv head.
 #include "kernel_common.hpp"
-#include "kv_layout.hpp"
+#include "kv_launch.hpp"
 
 namespace nvfp4 {
 
