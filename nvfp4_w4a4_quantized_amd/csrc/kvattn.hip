@@ -498,7 +498,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
         if (whole) {
           const int32_t qi = col / a.by_group;
           const int head = kh * group + (col - qi * group);
-          const float f = sum > 0.0f ? vg / sum : 0.0f;
+          const float f = sum == 0.0f ? 0.0f : vg / sum;
           const int64_t off = (seq.q0 + qi) * a.ldo + (int64_t)head * D + part * NJ;
           if constexpr (F32) {
 #pragma unroll
@@ -513,7 +513,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
           }
           if (a.lse && part == 0)
             a.lse[(seq.q0 + qi) * a.n_q_heads + head] =
-                sum > 0.0f ? (top_c + __builtin_log2f(sum)) * kLn2 : -__builtin_inff();
+                sum == 0.0f ? -__builtin_inff() : (top_c + __builtin_log2f(sum)) * kLn2;
         } else {
           float* dst = piece_at(a, D, blockIdx.x, col - col_first);
 #pragma unroll
@@ -536,7 +536,7 @@ __device__ __forceinline__ void store_joined(const KvAttnArgs& a, const ItemPiec
                                              const float (&x)[E], float top, float sum) {
   const int32_t col = item.first_col + c, qi = col / a.by_group, tok = item.q0 + qi;
   const int head = item.kh * (int)a.by_group.d + col - qi * (int)a.by_group.d;
-  const float g = sum > 0.0f ? a.v_gscale[item.kh] / sum : 0.0f;
+  const float g = sum == 0.0f ? 0.0f : a.v_gscale[item.kh] / sum;
   const int64_t off = (int64_t)tok * a.ldo + (int64_t)head * D + first;
   if constexpr (F32) {
 #pragma unroll
@@ -549,7 +549,7 @@ __device__ __forceinline__ void store_joined(const KvAttnArgs& a, const ItemPiec
       *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(a.o) + off + e) = pack_bf16(x[e] * g, x[e + 1] * g);
   }
   if (a.lse && first == 0)
-    a.lse[(int64_t)tok * a.n_q_heads + head] = sum > 0.0f ? (top + __builtin_log2f(sum)) * kLn2 : -__builtin_inff();
+    a.lse[(int64_t)tok * a.n_q_heads + head] = sum == 0.0f ? -__builtin_inff() : (top + __builtin_log2f(sum)) * kLn2;
 }
 
 // Join the pieces of the item that a worker began, few pieces: a wave per query column, a

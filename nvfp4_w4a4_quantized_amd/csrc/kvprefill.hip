@@ -560,7 +560,7 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
     if (col0 + c32 < col_end) {
       auto first_of = [&](int g) { return ((g & 4) * 2 + 4 * h + (g & 3)) * (D / 16); };
       if (whole) {
-        const float f = l > 0.0f ? vg / l : 0.0f;
+        const float f = l == 0.0f ? 0.0f : vg / l;
         uint16_t* dst = reinterpret_cast<uint16_t*>(a.o) + (seq.q0 + qi) * a.ldo + (int64_t)head * D;
 #pragma unroll
         for (int g = 0; g < 8; ++g)
@@ -569,7 +569,7 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
             *reinterpret_cast<u32x2*>(dst + first_of(g) + 2 * i) =
                 u32x2{pack_bf16(acc[i][g] * f, acc[i][g + 8] * f), pack_bf16(acc[i + 1][g] * f, acc[i + 1][g + 8] * f)};
         if (a.lse && h == 0)
-          a.lse[(seq.q0 + qi) * a.n_q_heads + head] = l > 0.0f ? (m + __builtin_log2f(l)) * kLn2 : -__builtin_inff();
+          a.lse[(seq.q0 + qi) * a.n_q_heads + head] = l == 0.0f ? -__builtin_inff() : (m + __builtin_log2f(l)) * kLn2;
       } else {
         float* dst = piece_at(a, D, blockIdx.x, col0 + c32 - col_first);
 #pragma unroll

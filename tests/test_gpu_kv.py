@@ -335,6 +335,25 @@ def test_query_magnitudes(nv, dtype, gain):
     p.check(p.run(nv))
 
 
+@pytest.mark.parametrize("dtype,D,Hq,Hkv,kv,m,hint", [
+    ("bf16", 64, 6, 2, [70, 33], [1, 1], 70),                      # whole items
+    ("f32", 128, 4, 2, [3000, 40], [2, 1], 3000),                  # joined pieces, many and few
+    ("bf16", 128, 8, 4, [2500] * 6, [3] * 6, 2500),
+    ("bf16", 128, 4, 1, [400, 100], [200, 70], 400),               # prompts, joined pieces
+    ("bf16", 64, 56, 56, [300, 65, 7], [290, 65, 7], 300)])        # and whole items
+def test_a_nan_stays_in_its_row(nv, dtype, D, Hq, Hkv, kv, m, hint):
+    p = Problem(nv, kv, m, Hq, Hkv, D, 16, dtype, seed=11)
+    clean = p.run(nv, hints=(max(m), hint))
+    at, q = (m[0] // 2, Hq - 1), p.q
+    p.q = q.clone()
+    p.q[at[0], at[1], 5] = float("nan")
+    o, lse = p.run(nv, hints=(max(m), hint))
+    p.q = q
+    assert np.all(np.isnan(o[at])) and np.isnan(lse[at])
+    o[at], lse[at] = clean[0][at], clean[1][at]
+    p.check((o, lse), rows=sorted({0, m[0] // 2, m[0] - 1, max(0, m[0] // 2 - 1)}))
+
+
 def test_rising_scores_move_the_reference(nv):
     # keys that grow along the sequence: the maximum keeps rising, tile after tile
     D, n = 64, 1024
