@@ -107,6 +107,16 @@ __device__ __forceinline__ Span span_of(const SeqInfo& s, int32_t col0, int32_t 
   return r;
 }
 
+// The scales (a byte each) of four tokens from `first` on, those outside [lo, hi) cleared:
+// nothing attends to these tokens, but their bytes may never have been written, and a weight of
+// zero times a NaN would reach the sums.
+__device__ __forceinline__ uint32_t live_scales(uint32_t x, int32_t first, int32_t lo, int32_t hi) {
+  const int32_t skip = lo - first, left = hi - first;
+  const uint32_t from = skip <= 0 ? ~0u : (skip >= 4 ? 0u : ~0u << (8 * skip));
+  const uint32_t upto = left >= 4 ? ~0u : (left <= 0 ? 0u : (1u << (8 * left)) - 1u);
+  return x & from & upto;
+}
+
 __device__ __forceinline__ int64_t uniform64(int64_t x) {
   const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)x), hi = __builtin_amdgcn_readfirstlane((uint32_t)(x >> 32));
   return (int64_t)(((uint64_t)hi << 32) | lo);

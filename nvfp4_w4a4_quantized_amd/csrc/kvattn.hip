@@ -386,14 +386,10 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
             }
         }
 
-        // O^T += V^T P^T: rows = elements NJ r + j.  The scales of tokens past the end
-        // are cleared: their bytes may hold anything, and 0 * NaN would reach the sums.
-        if (t0 + TOK > seq.n) {
+        // O^T += V^T P^T: rows = elements NJ r + j
+        if (t0 < sp.lo || t0 + TOK > seq.n) {
 #pragma unroll
-          for (int u = 0; u < NG; ++u) {
-            const int32_t left = seq.n - (t0 + 16 * u + 4 * g);    // live tokens from this quad's first on
-            cur[u].vs = left <= 0 ? 0u : (left >= 4 ? cur[u].vs : cur[u].vs & ((1u << (8 * left)) - 1u));
-          }
+          for (int u = 0; u < NG; ++u) cur[u].vs = live_scales(cur[u].vs, t0 + 16 * u + 4 * g, sp.lo, seq.n);
         }
 #pragma unroll
         for (int k = 0; k < NG / 2; ++k) {

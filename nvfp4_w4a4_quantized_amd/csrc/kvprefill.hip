@@ -91,15 +91,17 @@ __device__ __forceinline__ void read_dwords(const uint8_t* p, uint32_t* d) {
   }
 }
 
-// A tile of query columns: the keys it attends to, from granule-aligned `begin` on
+// A tile of query columns: the keys it attends to, the first of them, and `steps` tiles of tokens
+// from granule-aligned `begin` on
 struct TileSpan {
-  int32_t begin, steps;
+  int32_t lo, begin, steps;
 };
 template <int D>
 __device__ __forceinline__ TileSpan tile_span(const KvAttnArgs& a, const SeqInfo& seq, int32_t tile, int group) {
   const int32_t cols = seq.m * group, first = tile * kPrefillCols;
   const Span s = span_of(seq, first, first + kPrefillCols < cols ? first + kPrefillCols : cols, a.by_group, a.window);
   TileSpan t;
+  t.lo = s.lo;
   t.begin = s.lo & ~15;
   t.steps = seq.n > 0 ? (s.hi - t.begin + kTok<D> - 1) / kTok<D> : 0;
   return t;
@@ -269,9 +271,8 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
       const uint8_t* p = granule(s, id);
       read_dwords<KD>(p + 9 * D + (16 * quad + part) * (D / 8), rv);
       vsc = *reinterpret_cast<const uint32_t*>(p + 17 * D + (quad * (D / 16) + part * D / 256) * 4);
-      // scales of tokens past the end are cleared: their bytes may be NaN
-      const int32_t left = seq.n - (begin + s * TOK + 16 * gran + 4 * quad);
-      if (left < 4) vsc = left <= 0 ? 0u : vsc & ((1u << (8 * left)) - 1u);
+      const int32_t first = begin + s * TOK + 16 * gran + 4 * quad;
+      if (first < span.lo || first + 4 > seq.n) vsc = live_scales(vsc, first, span.lo, seq.n);
     };
     // decode dword i of the loaded keys: a 16-byte chunk of a token's row
     auto decode_k = [&](uint32_t kb, int i) {               // kb: the lane's first chunk in the tile

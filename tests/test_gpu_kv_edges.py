@@ -1,0 +1,93 @@
+"""Cache and attention at the edges of their ranges: bytes that were never written, scores
+of any size, scales of either sign, bounds far above the lengths, many sequences, rows
+beyond the caches.  Tolerances as in test_gpu_kv.py."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import kv as KV
+from oracle import nvfp4 as O
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="module")
+def nv():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import nvfp4_w4a4_quantized_amd as nvmod
+    return nvmod
+
+
+def _dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def _held(x, g):
+    """The values that the cache holds for x [n, H, D] under g [H], float64."""
+    n, H, D = x.shape
+    codes, scales = KV.quantize_heads(x, g)
+    return O.dequantize_rows(codes.reshape(n * H, -1), scales.reshape(n * H, -1), np.tile(g, n)).reshape(n, H, D)
+
+
+def _cache(nv, k, v, g, page, written=None):
+    """(cache, table) of one sequence k, v fp32 [n, H, D] in pages in reverse order, with bytes
+    that decode to NaN where nothing (or not `written`) is."""
+    n, H, D = k.shape
+    pages = -(-n // page)
+    table = np.arange(pages, dtype=np.int32)[::-1].copy()
+    slots = table[np.arange(n) // page].astype(np.int64) * page + np.arange(n) % page
+    if written is not None:
+        slots[~written] = -1
+    cache = nv.empty_kv_cache(pages, H, page, D).fill_(0x7F)
+    nv.nvfp4_rope_append_kv(None, _dev(k.reshape(n, -1)), _dev(v.reshape(n, -1)), None, None,
+                            torch.zeros(n, dtype=torch.int32, device="cuda"), _dev(slots), cache, _dev(g), _dev(g), page, None)
+    return cache, _dev(table)[None]
+
+
+def _attend(nv, q, cache, table, n, g, page, Hkv, most=None, window=0, scale=None):
+    """q [m, Hq, D] of the dtype on the CPU -> (o, lse) float64."""
+    m, Hq, D = q.shape
+    x = q.reshape(m, -1).cuda()
+    o, lse = torch.full_like(x, 3.0), torch.full((m, Hq), 3.0, device="cuda")
+    most = most or n
+    ws = torch.empty(nv.nvfp4_kv_attention_workspace(m, 1, Hq, Hkv, D, m, most, q.dtype), dtype=torch.uint8, device="cuda")
+    cu = torch.tensor([0, m], dtype=torch.int32, device="cuda")
+    nv.nvfp4_kv_attention(x, cache, table, torch.tensor([n], dtype=torch.int32, device="cuda"), _dev(g), _dev(g), page, o, most,
+                          ws, cu_q=cu, max_q_len=m, scale=scale, window=window, lse=lse)
+    torch.cuda.synchronize()
+    return o.double().cpu().numpy().reshape(m, Hq, D), lse.double().cpu().numpy()
+
+
+def _check(q, k, v, got, scale, window, dtype):
+    o, lse = got
+    wo, wl, w = KV.attention(q.float().numpy(), k, v, scale, window)
+    bo, bl = KV.attention_bounds(q.float().numpy(), k, v, w, scale, dtype)
+    assert np.all(np.abs(o - wo) <= bo + O.ulp(wo, dtype)), np.max(np.abs(o - wo))
+    assert np.all(np.abs(lse - wl) <= bl + 4 * 2.0 ** -24 * np.abs(wl))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D,m,n,window,most", [
+    (64, 1, 300, 33, 0), (128, 1, 301, 34, 0), (256, 1, 302, 35, 0), (128, 3, 300, 36, 0),
+    (128, 1, 4096, 3001, 8192),                     # cut along the keys
+    (64, 70, 300, 33, 0), (128, 70, 301, 34, 0), (256, 71, 300, 36, 0),   # prompts (bf16), cut
+    (64, 70, 300, 33, -1), (128, 70, 301, 34, -1), (256, 71, 300, 36, -1)])   # and whole items
+def test_slots_before_every_window_may_be_unwritten(nv, dtype, D, m, n, window, most):
+    rng = np.random.default_rng(n + m + D)
+    Hkv, Hq = (1, 4) if most >= 0 else (192, 768)
+    most = max(most, n)
+    k, v = rng.standard_normal((2, n, Hkv, D)).astype(np.float32)
+    g = np.full(Hkv, 5 / 2688, dtype=np.float32)
+    first = n - m - window + 1                      # of the first query's window
+    assert first % 4 and first > 0
+    cache, table = _cache(nv, k, v, g, 16, np.arange(n) >= first)
+    q = torch.from_numpy(rng.standard_normal((m, Hq, D)).astype(np.float32)).to(DT[dtype])
+    o, lse = _attend(nv, q, cache, table, n, g, 16, Hkv, most, window)
+    assert np.all(np.isfinite(o)) and np.all(np.isfinite(lse))
+    kh = min(Hkv, 2)                                # heads whose values are checked
+    _check(q[:, :4 * kh], _held(k[:, :kh], g[:kh]), _held(v[:, :kh], g[:kh]), (o[:, :4 * kh], lse[:, :4 * kh]), D ** -0.5,
+           window, dtype)
