@@ -111,6 +111,7 @@ __device__ __forceinline__ Span span_of(const SeqInfo& s, int32_t col0, int32_t 
 // nothing attends to these tokens, but their bytes may never have been written, and a weight of
 // zero times a NaN would reach the sums.
 __device__ __forceinline__ uint32_t live_scales(uint32_t x, int32_t first, int32_t lo, int32_t hi) {
+  asm volatile("" : "+v"(first));          // rare: nothing of it is kept in registers through a loop
   const int32_t skip = lo - first, left = hi - first;
   const uint32_t from = skip <= 0 ? ~0u : (skip >= 4 ? 0u : ~0u << (8 * skip));
   const uint32_t upto = left >= 4 ? ~0u : (left <= 0 ? 0u : (1u << (8 * left)) - 1u);

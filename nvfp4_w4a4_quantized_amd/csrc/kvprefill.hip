@@ -271,8 +271,8 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
       const uint8_t* p = granule(s, id);
       read_dwords<KD>(p + 9 * D + (16 * quad + part) * (D / 8), rv);
       vsc = *reinterpret_cast<const uint32_t*>(p + 17 * D + (quad * (D / 16) + part * D / 256) * 4);
-      const int32_t first = begin + s * TOK + 16 * gran + 4 * quad;
-      if (first < span.lo || first + 4 > seq.n) vsc = live_scales(vsc, first, span.lo, seq.n);
+      const int32_t first = begin + s * TOK + 16 * gran;
+      if (first < span.lo || first + 16 > seq.n) vsc = live_scales(vsc, first + 4 * quad, span.lo, seq.n);
     };
     // decode dword i of the loaded keys: a 16-byte chunk of a token's row
     auto decode_k = [&](uint32_t kb, int i) {               // kb: the lane's first chunk in the tile
