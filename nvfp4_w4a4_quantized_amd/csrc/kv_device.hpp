@@ -7,7 +7,7 @@
 namespace nvfp4 {
 namespace {
 
-constexpr float kNegBig = -1.0e30f;      // reference M of a row that has seen nothing
+constexpr float kNegBig = -3.402823466e38f;   // reference M of a row that has seen nothing: the lowest fp32
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Joined with the lane 32 (16) away, by a swap of the halves (of the rows of 16) with itself
@@ -66,6 +66,13 @@ __device__ __forceinline__ float score_factor(float scale, float kg, float amax)
   const float down = __uint_as_float((uint32_t)(query_exponent(amax) - 14 + 127) << 23);
   return __builtin_fmaxf(__builtin_fabsf(scale) * kLog2e * kg * down, 0x1p-120f);
 }
+
+// The exponent fma(product, factor, -M) is exact but for M, which is the largest score, rounded:
+// off by 1 where scores reach 2^24 (then weights pass f16's range), by anything beyond.  Products
+// stay below 2^15 * 2688 * 256 < 2^35, so columns whose factor is at most this one have scores
+// below 2^23; a wave that holds another ("wide") multiplies its products by their factors first
+// and goes on with a factor of 1, so that scores and M round alike.
+constexpr float kWideFactor = 0x1p-12f;
 
 // What a workgroup needs of its sequence
 struct SeqInfo {

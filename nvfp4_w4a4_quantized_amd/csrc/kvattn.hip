@@ -16,7 +16,8 @@
 // terms where it is fp32; their sum is taken of the unrounded fp32 values.  Weights are
 // 2^(s - M) with M 7 below the running maximum when it was last moved, and M moves only when a
 // tile's largest weight would pass 2^15: f16 has that range, most tiles leave the output
-// accumulators alone, and weights 2^-21 below the largest are still normal f16 numbers.
+// accumulators alone, and weights 2^-21 below the largest are still normal f16 numbers.  Scores
+// may be of any size that fp32 holds (kWideFactor).
 //
 // One pass over the cache.  S^T = K q^T: keys are the A operand's rows (tokens), query
 // columns (query token x head of the group, 16 per block) the B operand's; a lane's
@@ -138,7 +139,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
   constexpr int TERMS = F32 ? 2 : 1;
   constexpr int LDO = D + 4;                       // LDS row of a column's output: 16-byte aligned, banks spread
   __shared__ float s_o[W][16 * LDO];
-  __shared__ float s_m[W][16 * NQ], s_l[W][16 * NQ];
+  __shared__ float s_m[W][16 * NQ], s_l[W][16 * NQ], s_c[W][16 * NQ];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -321,6 +322,18 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
       for (int j = 0; j < NJ; ++j) acc[n][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
 
+    bool wide = false;
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) wide |= __builtin_amdgcn_ballot_w64(csc[n] > kWideFactor) != 0;
+    if (wide) {
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        s_c[wave][16 * n + r] = csc[n];            // each lane reads what it wrote
+        csc[n] = 1.0f;
+      }
+    }
+    const int32_t all_lo = wide ? INT32_MAX : sp.all_lo;   // wide: every step takes the slower way
+
     if (w0 < w1) {
       Granule<D> cur[NG], nxt[NG];
       issue(w0, nxt);
@@ -329,7 +342,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
         for (int u = 0; u < NG; ++u) cur[u] = nxt[u];
         if (s + 1 < w1) issue(s + 1, nxt);
         const int32_t t0 = begin + s * TOK;
-        const bool edge = t0 < sp.all_lo || t0 + TOK > sp.all_hi;
+        const bool edge = t0 < all_lo || t0 + TOK > sp.all_hi;
 
         // S^T: rows = tokens 16 u + 4 g + i
         f32x4 sc[NQ][NG];
@@ -358,9 +371,14 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
 #pragma unroll
               for (int i = 0; i < 4; ++i)
                 if (16 * u + i >= upto || 16 * u + i < from) sc[n][u][i] = -__builtin_inff();
+            if (wide) {
+              const float factor = s_c[wave][16 * n + r];
+#pragma unroll
+              for (int u = 0; u < NG; ++u) sc[n][u] *= factor;
+            }
           }
           const float top = max_xor32(max_xor16(max_of(sc[n]))) * csc[n];
-          if (__builtin_amdgcn_ballot_w64(top > m[n] + 15.0f)) {
+          if (__builtin_amdgcn_ballot_w64(top - m[n] > 15.0f)) {
             const float m1 = __builtin_fmaxf(m[n], top - 7.0f);
             const float f = __builtin_amdgcn_exp2f(m[n] - m1);
             m[n] = m1;

@@ -60,6 +60,9 @@ template <int D>
 constexpr int kKTile = kTok<D> * kKRow<D>;
 template <int D>
 constexpr int kVTile = D * kVRow<D>;
+// after the tiles: the columns' score factors where a wave's are wide
+template <int D>
+constexpr int kFactors = 2 * (kKTile<D> + kVTile<D>);
 
 template <typename T>
 __device__ __forceinline__ __attribute__((address_space(3))) T& lds_at(uint32_t at) {
@@ -343,7 +346,13 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
           qf[k][2 * e + 1] = x[1];
         }
     }
-    const float csc = score_factor(a.scale, kg, amax);
+    float csc = score_factor(a.scale, kg, amax);
+    const bool wide = __builtin_amdgcn_ballot_w64(csc > kWideFactor) != 0;
+    if (wide) {
+      lds_at<float>(lds + kFactors<D> + 4 * (32 * wave + c32)) = csc;   // each lane reads what it wrote
+      csc = 1.0f;
+    }
+    const int32_t all_lo = wide ? INT32_MAX : sp.all_lo;   // wide: every block takes the slower way
     const int32_t pos = seq.n - seq.m + qi;
     const int32_t limit = pos + 1, floor_ = a.window ? pos - a.window + 1 : 0;
     float m = kNegBig, l = 0.0f;
@@ -369,18 +378,23 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
     // moves the reference M for the block from token t0 on; returns what the earlier sums are
     // scaled by
     auto reference = [&](int32_t t0, f32x16& sc) {
-      if (t0 < sp.all_lo || t0 + 32 > sp.all_hi) {
+      if (t0 < all_lo || t0 + 32 > sp.all_hi) {
         const int32_t upto = limit - t0 - 4 * h, from = floor_ - t0 - 4 * h;
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const int32_t t = 8 * (e / 4) + e % 4;
           if (t >= upto || t < from) sc[e] = -__builtin_inff();
         }
+        if (wide) {
+          const float factor = lds_at<float>(lds + kFactors<D> + 4 * (32 * wave + c32));
+#pragma unroll
+          for (int e = 0; e < 16; ++e) sc[e] *= factor;
+        }
         // masked in place (as two versions, the scores were copied in every block)
         asm volatile("" : "+v"(sc));
       }
       const float top = max_xor32(max_of(sc)) * csc;
-      const float m1 = top > m + 15.0f ? __builtin_fmaxf(m, top - 7.0f) : m;
+      const float m1 = top - m > 15.0f ? __builtin_fmaxf(m, top - 7.0f) : m;
       const float f = __builtin_amdgcn_exp2f(m - m1);
       l *= f;
       m = m1;
@@ -590,7 +604,7 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
 
 template <int D, bool SPLIT>
 hipError_t launch(const KvAttnArgs& a, hipStream_t s) {
-  constexpr int bytes = 2 * (kKTile<D> + kVTile<D>);
+  constexpr int bytes = kFactors<D> + 4 * kPrefillCols;
   const hipError_t e = lds_limit_once<k_kv_prefill<D, SPLIT>>(bytes);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((k_kv_prefill<D, SPLIT>), dim3((unsigned)a.blocks), dim3(64 * kPrefillWaves), bytes, s, a);

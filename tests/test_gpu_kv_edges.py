@@ -91,3 +91,47 @@ def test_slots_before_every_window_may_be_unwritten(nv, dtype, D, m, n, window, 
     kh = min(Hkv, 2)                                # heads whose values are checked
     _check(q[:, :4 * kh], _held(k[:, :kh], g[:kh]), _held(v[:, :kh], g[:kh]), (o[:, :4 * kh], lse[:, :4 * kh]), D ** -0.5,
            window, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D,m,n,most", [
+    (64, 1, 300, 0), (128, 1, 301, 0), (256, 2, 302, 0), (128, 9, 300, 0),
+    (128, 1, 3000, 8192),                           # cut along the keys
+    (64, 70, 300, 0), (128, 70, 301, 0), (256, 71, 300, 0), (128, 300, 333, 8192)])   # prompts (bf16)
+@pytest.mark.parametrize("gain", [1e6, 1e8, 1e10, 1e20, 3e33, -1e8, -1e20, -3e33])
+def test_scores_of_any_size(nv, dtype, D, m, n, most, gain):
+    """Queries so long that a key stands out, or several are alike within the scores' rounding;
+    gain < 0: all scores negative, the lowest near -1e35."""
+    rng = np.random.default_rng(n + m + D)
+    k, v = rng.standard_normal((2, n, 2, D)).astype(np.float32)
+    x = rng.standard_normal((m, 6, D))
+    if gain < 0:
+        k, x = np.abs(k) + 0.25, np.abs(x)
+    x[m // 2, 0] /= gain                            # a row of ordinary scores beside them
+    g = np.full(2, 5 / 2688, dtype=np.float32)
+    q = torch.from_numpy((x * gain).astype(np.float32)).to(DT[dtype])
+    cache, table = _cache(nv, k, v, g, 16)
+    o, lse = _attend(nv, q, cache, table, n, g, 16, 2, max(most, n))
+    assert np.all(np.isfinite(o)) and np.all(np.isfinite(lse))
+    kk, vv, scale = _held(k, g), _held(v, g), D ** -0.5
+    qn = q.double().numpy()
+    wo, wl, w = KV.attention(qn, kk, vv, scale)
+    bo, bl = KV.attention_bounds(qn, kk, vv, w, scale, dtype)
+    # the score's error with every key's magnitudes, not those of positive weights alone
+    mag = scale * np.einsum("mhd,nhd->mhn", np.abs(qn), np.abs(np.repeat(kk, 3, 1))).max(-1)
+    ds = ((D + 16) * 2.0 ** -24 + (2.0 ** -21 if dtype == "f32" else 0)) * mag + 16 * 2.0 ** -24
+    assert np.all(np.abs(lse - wl) <= ds + np.log(n) + 1e-6 * np.abs(wl))
+    ordinary = (m // 2, 0)
+    assert np.all(np.abs(o[ordinary] - wo[ordinary]) <= bo[ordinary] + O.ulp(wo[ordinary], dtype))
+    most_v = np.abs(vv).max()
+    alone = 0
+    for i in range(m):
+        for h in range(6):
+            s = scale * (kk[:n - m + i + 1, h // 3] @ qn[i, h])
+            values = vv[:len(s), h // 3]
+            # keys that the scores' error may make the largest: a mean of their values
+            near = values[s >= s.max() - 4 * ds[i, h] - 40]
+            alone += len(near) == 1
+            slack = 2.0 ** -8 * most_v if dtype == "bf16" else 2.0 ** -19 * most_v
+            assert np.all(o[i, h] <= near.max(0) + slack) and np.all(o[i, h] >= near.min(0) - slack)
+    assert alone >= m                               # most rows have one such key
