@@ -84,8 +84,10 @@ hipError_t launch_kv_attn(KvAttnArgs a, const KvAttnPlan& p, InType t, int32_t D
 // joins the pieces that either kernel left
 hipError_t launch_kv_join(const KvAttnArgs& a, InType t, int32_t D, hipStream_t s);
 
-// kvprefill.hip: bf16, items of kv_prefill_cols() query columns.
+// kvprefill.hip: bf16, items of kv_prefill_cols() query columns, a workgroup of
+// kv_prefill_threads() each.
 int32_t kv_prefill_cols();
+int32_t kv_prefill_threads();
 hipError_t launch_kv_prefill(const KvAttnArgs& a, int32_t D, hipStream_t s);
 
 }  // namespace nvfp4

@@ -59,4 +59,16 @@ inline int64_t kv_page_bytes(int32_t n_kv_heads, int32_t page_size, int32_t D) {
   return (int64_t)n_kv_heads * page_size * D * 9 / 8;
 }
 
+// Workgroups of `threads` that one launch may have: HIP counts a grid's threads in 32 bits and
+// refuses more.
+inline int64_t kv_most_blocks(int32_t threads) { return 0xFFFFFFFFll / threads; }
+
+// Column tiles that the attention's grid has for each of `pairs` (sequence, kv head), at most
+// 2^22 of them, where the bounds on the lengths ask for `tiles`.  Any number is right (the kernels
+// take further tiles with the planned ones), and bounds far above the lengths ask for too many.
+inline int32_t kv_planned_tiles(int64_t tiles, int64_t pairs, int32_t threads) {
+  const int64_t most = kv_most_blocks(threads) / pairs;
+  return (int32_t)(tiles < most ? tiles : most);
+}
+
 }  // namespace nvfp4

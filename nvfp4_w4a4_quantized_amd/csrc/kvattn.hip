@@ -702,8 +702,7 @@ KvAttnPlan kv_attn_plan(InType t, int64_t T, int32_t batch, int32_t n_q_heads, i
     p.prefill = true;
     p.tile_cols = kv_prefill_cols();
     const int64_t pairs = (int64_t)batch * n_kv_heads, tiles = (cols + p.tile_cols - 1) / p.tile_cols;
-    const int64_t most = ((int64_t)1 << 30) / pairs;
-    p.col_tiles = (int32_t)(tiles < most ? tiles : most);
+    p.col_tiles = kv_planned_tiles(tiles, pairs, kv_prefill_threads());
     const int64_t items = pairs * p.col_tiles;
     p.blocks = (int32_t)items;
     // Fewer items than compute units: cut along the keys, one workgroup a compute unit.
@@ -728,13 +727,9 @@ KvAttnPlan kv_attn_plan(InType t, int64_t T, int32_t batch, int32_t n_q_heads, i
   p.nq = cols > 16 && (D == 64 || (D == 128 && t == InType::BF16)) ? 2 : 1;
   const int64_t blk = 16 * p.nq;
   p.tile_cols = (int32_t)(cols < blk * kAttnWaves ? cols : blk * kAttnWaves);
-  int64_t tiles = (cols + p.tile_cols - 1) / p.tile_cols;
   const int64_t pairs = (int64_t)batch * n_kv_heads;
-  // any number of planned tiles is right: the kernel takes further ones with the first
-  const int64_t most_tiles = ((int64_t)1 << 30) / (pairs * p.tile_cols);
-  if (tiles > most_tiles) tiles = most_tiles < 1 ? 1 : most_tiles;
-  p.col_tiles = (int32_t)tiles;
-  const int64_t items = pairs * tiles;
+  p.col_tiles = kv_planned_tiles((cols + p.tile_cols - 1) / p.tile_cols, pairs, 64 * kAttnWaves);
+  const int64_t items = pairs * p.col_tiles;
   p.blocks = (int32_t)items;
   const int64_t tok = D == 256 ? 32 : 64, waves = cols <= blk ? 4 : (cols <= 2 * blk ? 2 : 1);
   // keys that a tile attends to, at most

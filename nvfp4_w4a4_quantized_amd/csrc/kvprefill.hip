@@ -620,6 +620,7 @@ hipError_t launch(const KvAttnArgs& a, hipStream_t s) {
 }  // namespace
 
 int32_t kv_prefill_cols() { return kPrefillCols; }
+int32_t kv_prefill_threads() { return 64 * kPrefillWaves; }
 
 hipError_t launch_kv_prefill(const KvAttnArgs& a, int32_t D, hipStream_t s) {
   if (D == 64) return launch<64>(a, s);

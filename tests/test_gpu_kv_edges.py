@@ -135,3 +135,35 @@ def test_scores_of_any_size(nv, dtype, D, m, n, most, gain):
             slack = 2.0 ** -8 * most_v if dtype == "bf16" else 2.0 ** -19 * most_v
             assert np.all(o[i, h] <= near.max(0) + slack) and np.all(o[i, h] >= near.min(0) - slack)
     assert alone >= m                               # most rows have one such key
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 64), ("f32", 128)])
+def test_bounds_far_above_the_lengths(nv, dtype, D):
+    """65536 sequences, one of them with all 32768 queries: planned for what the bounds allow, the
+    grid would have 2^23 workgroups of 512 threads (2^25 of 256), more than a launch takes."""
+    rng = np.random.default_rng(D)
+    batch, m, n, page = 1 << 16, 1 << 15, 600, 16
+    k, v = rng.standard_normal((2, n, 1, D)).astype(np.float32)
+    g = np.full(1, 5 / 2688, dtype=np.float32)
+    cache, one = _cache(nv, k, v, g, page)
+    q = torch.from_numpy(rng.standard_normal((m, D)).astype(np.float32)).to(DT[dtype])
+    x = q.cuda()
+    o, lse = torch.full_like(x, 3.0), torch.full((m, 1), 3.0, device="cuda")
+    at = batch // 3
+    table = torch.zeros(batch, one.shape[1], dtype=torch.int32, device="cuda")
+    table[at] = one[0]
+    kv_len = torch.full((batch,), 5, dtype=torch.int32, device="cuda")
+    kv_len[at] = n
+    cu = torch.zeros(batch + 1, dtype=torch.int32, device="cuda")
+    cu[at + 1:] = m
+    need = nv.nvfp4_kv_attention_workspace(m, batch, 1, 1, D, m, n, q.dtype)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    nv.nvfp4_kv_attention(x, cache, table, kv_len, _dev(g), _dev(g), page, o, n, ws, cu_q=cu, max_q_len=m, lse=lse)
+    torch.cuda.synchronize()
+    o, lse = o.double().cpu().numpy()[:, None], lse.double().cpu().numpy()
+    seen = m - n                                    # rows before it have no key
+    assert np.all(o[:seen] == 0) and np.all(np.isneginf(lse[:seen]))
+    kk, vv = _held(k, g), _held(v, g)
+    for i in [seen, seen + 1, m - 257, m - 256, m - 255, m - 64, m - 2, m - 1]:
+        end = i - seen + 1
+        _check(q[i:i + 1, None], kk[:end], vv[:end], (o[i:i + 1], lse[i:i + 1]), D ** -0.5, 0, dtype)
