@@ -370,8 +370,9 @@ NVFP4_API int32_t nvfp4_mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scal
  * k_gscale, v_gscale [n_kv_heads], calibrated: > 0, amax / 2688 covers a head's values),
  * the same ones in every call over a cache.  New memory needs no clearing: bytes of
  * slots that were never written are never part of a result.
- *   head_dim 64, 128 or 256; page_size a power of two in [16, 4096]
- *   (NVFP4_ERR_UNSUPPORTED otherwise).
+ *   head_dim 64, 128 or 256; page_size a power of two in [16, 4096]; a call takes fewer than
+ *   2^31 rows (tokens x heads) and appends or reads fewer than 2^36 elements, q, k and v
+ *   together (NVFP4_ERR_UNSUPPORTED otherwise).
  */
 
 /* Bytes of one page (host only). */

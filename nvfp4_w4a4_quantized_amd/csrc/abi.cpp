@@ -266,6 +266,15 @@ int32_t check_kv_rows(int64_t T, int64_t heads) {
   return NVFP4_OK;
 }
 
+// Appending or reading `heads` rows of T tokens is one launch
+int32_t check_kv_launch(int64_t T, int64_t heads, int32_t head_dim) {
+  const int32_t st = check_kv_rows(T, heads);
+  if (!st && nvfp4::kv_row_blocks(T, heads, head_dim) > nvfp4::kv_most_blocks(nvfp4::kKvRowThreads))
+    return fail(NVFP4_ERR_UNSUPPORTED, "%lld tokens of %lld heads of %d: at most 2^36 elements a call", (long long)T,
+                (long long)heads, head_dim);
+  return st;
+}
+
 int32_t check_kv_cache(const uint8_t* cache, const float* k_gscale, const float* v_gscale) {
   if (!cache) return fail(NVFP4_ERR_INVALID_ARG, "cache is NULL");
   if (!aligned16(cache)) return fail(NVFP4_ERR_UNSUPPORTED, "cache must be 16-byte aligned");
@@ -602,7 +611,7 @@ int32_t nvfp4_rope_append_kv(const void* q, int64_t ldq, const void* k, int64_t 
   }
   st = check_x(k, dtype, T, (int64_t)n_kv_heads * head_dim, ldk, "k");
   if (!st) st = check_x(v, dtype, T, (int64_t)n_kv_heads * head_dim, ldv, "v");
-  if (!st) st = check_kv_rows(T, (int64_t)n_q_heads + 2 * (int64_t)n_kv_heads);
+  if (!st) st = check_kv_launch(T, (int64_t)n_q_heads + 2 * (int64_t)n_kv_heads, head_dim);
   if (!st) st = check_kv_cache(cache, k_gscale, v_gscale);
   if (st) return st;
   if (!positions || !slots) return fail(NVFP4_ERR_INVALID_ARG, "positions/slots is NULL");
@@ -648,7 +657,7 @@ int32_t nvfp4_kv_gather(const uint8_t* cache, int64_t n_pages, int32_t page_size
   int32_t st = check_kv_shape(n_kv_heads, page_size, head_dim, n_pages, &a.geom);
   if (!st) st = check_x(k_out, out_dtype, T, (int64_t)n_kv_heads * head_dim, ldk, "k_out");
   if (!st) st = check_x(v_out, out_dtype, T, (int64_t)n_kv_heads * head_dim, ldv, "v_out");
-  if (!st) st = check_kv_rows(T, 2 * (int64_t)n_kv_heads);
+  if (!st) st = check_kv_launch(T, 2 * (int64_t)n_kv_heads, head_dim);
   if (!st) st = check_kv_cache(cache, k_gscale, v_gscale);
   if (st) return st;
   if (!slots) return fail(NVFP4_ERR_INVALID_ARG, "slots is NULL");

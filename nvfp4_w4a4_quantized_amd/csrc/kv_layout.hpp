@@ -63,6 +63,14 @@ inline int64_t kv_page_bytes(int32_t n_kv_heads, int32_t page_size, int32_t D) {
 // refuses more.
 inline int64_t kv_most_blocks(int32_t threads) { return 0xFFFFFFFFll / threads; }
 
+// Workgroups (256 threads) that append or read `heads` rows of each of T tokens: a wave takes
+// 64 / (D / 16) tokens of one head.
+constexpr int kKvRowThreads = 256;
+inline int64_t kv_row_blocks(int64_t T, int64_t heads, int32_t D) {
+  const int64_t per_wave = 64 / (D / 16), per_block = kKvRowThreads / 64;
+  return ((T + per_wave - 1) / per_wave * heads + per_block - 1) / per_block;
+}
+
 // Column tiles that the attention's grid has for each of `pairs` (sequence, kv head), at most
 // 2^22 of them, where the bounds on the lengths ask for `tiles`.  Any number is right (the kernels
 // take further tiles with the planned ones), and bounds far above the lengths ask for too many.

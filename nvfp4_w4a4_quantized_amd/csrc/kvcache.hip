@@ -16,7 +16,7 @@ namespace nvfp4 {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = kKvRowThreads;
 constexpr int kWaves = kThreads / 64;
 
 // 16 consecutive elements of a row as fp32
@@ -324,16 +324,10 @@ __global__ __launch_bounds__(kThreads) void k_kv_gather(KvGatherArgs a) {
   store16<T>(values ? a.v_out : a.k_out, t * (values ? a.ldv : a.ldk) + (int64_t)kh * D + 16 * b, v);
 }
 
-unsigned waves_grid(int64_t T, int32_t D, int32_t heads) {
-  const int64_t tpw = 64 / (D / 16);
-  const int64_t waves = (T + tpw - 1) / tpw * heads;
-  return (unsigned)((waves + kWaves - 1) / kWaves);
-}
-
 }  // namespace
 
 hipError_t launch_rope_append(const KvAppendArgs& a, InType t, int32_t D, hipStream_t s) {
-  const dim3 grid(waves_grid(a.T, D, a.n_q_heads + 2 * a.geom.n_kv_heads)), block(kThreads);
+  const dim3 grid((unsigned)kv_row_blocks(a.T, a.n_q_heads + 2 * (int64_t)a.geom.n_kv_heads, D)), block(kThreads);
   // queries beyond the L2s (32 MiB): 8192 tokens of 32 heads of 128 in bf16 54.3 us with ordinary
   // loads and stores, 50.1 us with non-temporal ones; 1543 fp32 tokens of 15 heads of 64 the other way
   // round, 10.9 and 12.4 us (with the read-back of the rows in both)
@@ -353,7 +347,7 @@ hipError_t launch_rope_append(const KvAppendArgs& a, InType t, int32_t D, hipStr
 }
 
 hipError_t launch_kv_gather(const KvGatherArgs& a, InType t, int32_t D, hipStream_t s) {
-  const dim3 grid(waves_grid(a.T, D, 2 * a.geom.n_kv_heads)), block(kThreads);
+  const dim3 grid((unsigned)kv_row_blocks(a.T, 2 * (int64_t)a.geom.n_kv_heads, D)), block(kThreads);
 #define NVFP4_GATHER(DD)                                                                            \
   if (t == InType::BF16) hipLaunchKernelGGL((k_kv_gather<InType::BF16, DD>), grid, block, 0, s, a); \
   else hipLaunchKernelGGL((k_kv_gather<InType::F32, DD>), grid, block, 0, s, a)
