@@ -28,10 +28,10 @@ __device__ __forceinline__ float sum_xor16(float x) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-// Largest of 16 or 8 MFMA results, by v_max3_f32 (fmaxf gets a canonicalizing max per value).
-// The compiler does not count the wait states between an MFMA and an asm that reads its
-// result, so an ordinary max of the first and the last value comes first: when the last
-// MFMA's result may be read, those of the ones before it may.
+// Largest of the results of one MFMA, or of N of them, by v_max3_f32 (fmaxf gets a canonicalizing
+// max per value).  The compiler does not count the wait states between an MFMA and an asm that
+// reads its result, so the asm takes its first operand from ordinary maxima that read a result of
+// every one of the MFMAs: those wait, and what an MFMA writes is all there when any of it is.
 __device__ __forceinline__ float max_of(const f32x16& x) {
   float m = __builtin_fmaxf(x[0], x[15]);
 #pragma unroll
@@ -40,10 +40,14 @@ __device__ __forceinline__ float max_of(const f32x16& x) {
 }
 template <int N>
 __device__ __forceinline__ float max_of(const f32x4 (&x)[N]) {
-  float m = __builtin_fmaxf(x[0][0], x[N - 1][3]);
+  static_assert(N % 2 == 0, "pairs");
+  float m = __builtin_fmaxf(x[0][0], x[1][0]);
 #pragma unroll
-  for (int i = 1; i + 1 < 4 * N; i += 2)
-    asm("v_max3_f32 %0, %0, %1, %2" : "+v"(m) : "v"(x[i / 4][i % 4]), "v"(x[(i + 1) / 4][(i + 1) % 4]));
+  for (int u = 2; u < N; ++u) m = __builtin_fmaxf(m, x[u][0]);
+#pragma unroll
+  for (int u = 0; u < N; u += 2)
+#pragma unroll
+    for (int i = 1; i < 4; ++i) asm("v_max3_f32 %0, %0, %1, %2" : "+v"(m) : "v"(x[u][i]), "v"(x[u + 1][i]));
   return m;
 }
 
