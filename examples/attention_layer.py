@@ -60,16 +60,23 @@ class AttentionLayer:
         self.kv_len = torch.zeros(batch, dtype=torch.int32, device=device)
         self.qkv_rows = torch.empty(max_tokens, ends[-1], dtype=torch.bfloat16, device=device)
         self.o_rows = torch.empty(max_tokens, n_q * d, dtype=torch.bfloat16, device=device)
+        # A generated token's calls are all of one size.  Graphs hold the address of their
+        # workspace, so it is never replaced, as the prompts' is when a longer one comes.
+        self.decode_workspace = torch.empty(self._workspace_bytes(batch, 1), dtype=torch.uint8, device=device)
         self.workspace = torch.empty(0, dtype=torch.uint8, device=device)
 
-    def reserve(self, tokens, max_q_len):
-        """Before the first call (or a capture) of a size: the attention's workspace."""
-        need = nv.nvfp4_kv_attention_workspace(tokens, self.batch, self.n_q, self.n_kv, self.d, max_q_len, self.max_len,
+    def _workspace_bytes(self, tokens, max_q_len):
+        return nv.nvfp4_kv_attention_workspace(tokens, self.batch, self.n_q, self.n_kv, self.d, max_q_len, self.max_len,
                                                torch.bfloat16)
+
+    def reserve(self, tokens, max_q_len):
+        """Before a call of a size: the attention's workspace (not for calls in graphs, which
+        would hold the address of one that a later call replaces)."""
+        need = self._workspace_bytes(tokens, max_q_len)
         if need > self.workspace.numel():
             self.workspace = torch.empty(need, dtype=torch.uint8, device=self.cache.device)
 
-    def __call__(self, x, y, seq, positions, cu_q=None, max_q_len=1):
+    def __call__(self, x, y, seq, positions, cu_q=None, max_q_len=1, workspace=None):
         """x [T, hidden]: new tokens of sequences seq [T] at positions [T], those of one
         sequence in rows cu_q[b] .. cu_q[b + 1]; self.kv_len counts them already."""
         tokens = x.shape[0]
@@ -80,7 +87,8 @@ class AttentionLayer:
         nv.nvfp4_rope_append_kv(q, k, v, self.cos, self.sin, positions, slots, self.cache, self.k_gscale, self.v_gscale,
                                 self.page, q)                      # queries rotated in place
         nv.nvfp4_kv_attention(q, self.cache, self.table, self.kv_len, self.k_gscale, self.v_gscale, self.page, o,
-                              self.max_len, self.workspace, cu_q=cu_q, max_q_len=max_q_len)
+                              self.max_len, self.workspace if workspace is None else workspace, cu_q=cu_q,
+                              max_q_len=max_q_len)
         return self.out(o, y)
 
     def prompt(self, x, lens, y):
@@ -95,10 +103,10 @@ class AttentionLayer:
         return self(x, y, seq, positions, cu, max(lens))
 
     def decode(self, x, y):
-        """One more token of every sequence."""
+        """One more token of every sequence; may be captured in a graph."""
         positions = self.kv_len.clone()
         self.kv_len += 1
-        return self(x, y, torch.arange(self.batch, device=x.device), positions)
+        return self(x, y, torch.arange(self.batch, device=x.device), positions, workspace=self.decode_workspace)
 
 
 def elapsed(fn, reps):
@@ -129,7 +137,6 @@ def main():
 
     x1 = torch.randn(args.batch, hidden, device="cuda").bfloat16()
     y1 = torch.empty_like(x1)
-    layer.reserve(args.batch, 1)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):

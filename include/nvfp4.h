@@ -437,7 +437,8 @@ NVFP4_API int32_t nvfp4_kv_gather(const uint8_t* cache, int64_t n_pages, int32_t
  *   window    0: none
  *   lse       device fp32 [T][n_q_heads] or NULL: log of the softmax's denominator
  *   workspace device, at least nvfp4_kv_attention_workspace(...) bytes, 16-byte aligned (NULL
- *             where that is 0).  Calls that overlap on the GPU need one each.
+ *             where that is 0).  Calls that overlap on the GPU need one each, and a recorded
+ *             graph needs the one that it was recorded with for as long as it is replayed.
  * Lengths and table entries outside their range are clamped into it (results are then
  * meaningless, accesses stay inside the buffers).
  */

@@ -2,6 +2,9 @@
 of any size, scales of either sign, bounds far above the lengths, many sequences, rows
 beyond the caches.  Tolerances as in test_gpu_kv.py."""
 
+import importlib.util
+import os
+
 import numpy as np
 import pytest
 import torch
@@ -167,3 +170,46 @@ def test_bounds_far_above_the_lengths(nv, dtype, D):
     for i in [seen, seen + 1, m - 257, m - 256, m - 255, m - 64, m - 2, m - 1]:
         end = i - seen + 1
         _check(q[i:i + 1, None], kk[:end], vv[:end], (o[i:i + 1], lse[i:i + 1]), D ** -0.5, 0, dtype)
+
+
+def test_prompts_between_replays_of_a_captured_step(nv):
+    """examples/attention_layer.py: prompt, capture, prompts that need more workspace, replay; the
+    replays equal eager steps and write nowhere else."""
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "attention_layer.py")
+    spec = importlib.util.spec_from_file_location("attention_layer", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    gen = torch.Generator("cuda").manual_seed(5)
+
+    def rows(n):
+        return torch.randn(n, 256, generator=gen, device="cuda").bfloat16()
+    layer = example.AttentionLayer(256, 8, 2, 64, 3, 5000, 3000, page=16, seed=3)
+    layer.cache.zero_()
+    x, y = rows(33), torch.empty(3000, 256, dtype=torch.bfloat16, device="cuda")
+    layer.prompt(x, [30, 2, 1], y[:33])
+    x1, y1 = rows(3), torch.empty(3, 256, dtype=torch.bfloat16, device="cuda")
+    layer.decode(x1, y1)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer.decode(x1, y1)
+    held = layer.workspace.numel()
+    for lens in ([100, 200, 300], [2000, 10, 900]):
+        x = rows(sum(lens))
+        layer.prompt(x, lens, y[:sum(lens)])
+        torch.cuda.synchronize()
+        guards = [torch.full((max(held, 1 << 20),), 0x5A, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        steps = [rows(3) for _ in range(4)]
+        got = []
+        for s in steps:
+            x1.copy_(s)
+            graph.replay()
+            torch.cuda.synchronize()
+            got.append(y1.clone())
+        assert all(bool((t == 0x5A).all()) for t in guards)
+        layer.prompt(x, lens, y[:sum(lens)])                      # again, then the same steps eagerly
+        for s, want in zip(steps, got):
+            x1.copy_(s)
+            layer.decode(x1, y1)
+            assert torch.equal(y1, want)
+    assert layer.workspace.numel() > held

@@ -1,10 +1,12 @@
 """Host-side rules of the key/value cache at the edges of their ranges.  CPU only."""
 
 import ctypes
+import importlib.util
 import os
 import subprocess
 
 import pytest
+import torch
 
 from tests.test_kv_abi_cpu import _append, _gather, nv  # noqa: F401  (the fixture)
 
@@ -49,3 +51,28 @@ def test_rows_beyond_a_launch_are_refused(nv):   # noqa: F811
         assert _append(nv, T=tokens - 64, **q, **heads) == inv and "slots" in nv.nvfp4_last_error()
         assert _gather(nv, T=2 * tokens, **heads) == uns and "2^36" in nv.nvfp4_last_error(), d
         assert _gather(nv, T=2 * tokens - 64, **heads) == inv and "slots" in nv.nvfp4_last_error()
+
+
+def test_prompts_leave_the_workspace_of_captured_steps_alone(nv, monkeypatch):   # noqa: F811
+    """examples/attention_layer.py with the device's calls left out: the workspace that a captured
+    step got is still the layer's after prompts that need more than any call before them."""
+    spec = importlib.util.spec_from_file_location("attention_layer", os.path.join(ROOT, "examples", "attention_layer.py"))
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    used = []
+    for name in ("nvfp4_pack_weight", "nvfp4_w4a4_linear", "nvfp4_rope_append_kv"):
+        monkeypatch.setattr(example.nv, name, lambda *a, **k: None)
+    monkeypatch.setattr(example.nv, "nvfp4_kv_attention", lambda *a, **k: used.append(a[9]))
+    layer = example.AttentionLayer(256, 8, 2, 64, 3, 5000, 3000, page=16, device="cpu")
+    x, y = torch.zeros(3000, 256, dtype=torch.bfloat16), torch.zeros(3000, 256, dtype=torch.bfloat16)
+    layer.prompt(x[:33], [30, 2, 1], y[:33])
+    layer.decode(x[:3], y[:3])
+    need = nv.nvfp4_kv_attention_workspace(3, 3, 8, 2, 64, 1, 5000, torch.bfloat16)
+    captured = used[-1].data_ptr()
+    assert need > 0 and used[-1].numel() >= need
+    for lens in ([100, 200, 300], [2000, 10, 900], [1, 1, 1]):
+        layer.prompt(x[:sum(lens)], lens, y[:sum(lens)])
+        now = nv.nvfp4_kv_attention_workspace(sum(lens), 3, 8, 2, 64, max(lens), 5000, torch.bfloat16)
+        assert used[-1].numel() >= now and used[-1].data_ptr() != captured
+        layer.decode(x[:3], y[:3])
+        assert used[-1].data_ptr() == captured
