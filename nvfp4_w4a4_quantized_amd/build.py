@@ -2,7 +2,9 @@
 _torch_binding.so (host code: torch tensors to the C ABI) against it.
 
 Each source is compiled to an object in its own process (in parallel), then the
-objects are linked into the shared libraries.  Every call rebuilds everything.
+objects are linked into the shared libraries.  Every call rebuilds everything.  The
+library needs hipcc alone; the binding needs g++, Python's headers and torch, and without
+torch it is left out.
 
     python nvfp4_w4a4_quantized_amd/build.py
 
@@ -47,13 +49,16 @@ def _run(cmd, verbose):
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
-        raise RuntimeError("hipcc failed:\n" + " ".join(cmd) + "\n" + res.stdout + res.stderr)
+        raise RuntimeError(os.path.basename(cmd[0]) + " failed:\n" + " ".join(cmd) + "\n" + res.stdout + res.stderr)
 
 
 def _binding_commands():
-    """Compile and link of the host-only binding.  torch is found, not imported; its
-    libraries are loaded by the time the binding is."""
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    """Compile and link of the host-only binding (None without torch).  torch is found, not
+    imported; its libraries are loaded by the time the binding is."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or spec.origin is None:
+        return None
+    torch = os.path.dirname(spec.origin)
     obj = os.path.join(OBJDIR, "torch_binding.o")
     compile_ = ["g++", "-O2", "-std=c++20", "-fPIC", "-fvisibility=hidden", "-w", "-isystem",
                 os.path.join(torch, "include"), "-I", sysconfig.get_paths()["include"], "-c", "-o", obj,
@@ -68,15 +73,20 @@ def build(verbose: bool = False) -> str:
     os.makedirs(OBJDIR, exist_ok=True)
     objs = [os.path.join(OBJDIR, os.path.splitext(s)[0] + ".o") for s in SOURCES]
     cmds = [[hipcc] + COMPILE_FLAGS + ["-c", "-o", o, os.path.join(CSRC, s)] for s, o in zip(SOURCES, objs)]
-    compile_binding, link_binding = _binding_commands()
-    cmds.insert(0, compile_binding)
-    with ThreadPoolExecutor(max_workers=len(cmds)) as ex:
+    binding = _binding_commands()
+    with ThreadPoolExecutor(max_workers=len(cmds) + 1) as ex:
+        compiled = ex.submit(_run, binding[0], verbose) if binding else None
         for f in [ex.submit(_run, c, verbose) for c in cmds]:
             f.result()
     tmp = LIB + ".tmp"
     _run([hipcc] + LINK_FLAGS + ["-o", tmp] + objs, verbose)
     os.replace(tmp, LIB)
-    _run(link_binding, verbose)
+    # the library stands by itself: it is there whatever becomes of the binding
+    if binding is None:
+        print("torch is not installed: _torch_binding.so is not built", file=sys.stderr)
+        return LIB
+    compiled.result()
+    _run(binding[1], verbose)
     os.replace(BINDING + ".tmp", BINDING)
     return LIB
 

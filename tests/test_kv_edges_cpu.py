@@ -76,3 +76,40 @@ def test_prompts_leave_the_workspace_of_captured_steps_alone(nv, monkeypatch):  
         assert used[-1].numel() >= now and used[-1].data_ptr() != captured
         layer.decode(x[:3], y[:3])
         assert used[-1].data_ptr() == captured
+
+
+@pytest.fixture
+def build(tmp_path, monkeypatch):
+    """build.py with its results under tmp_path and its commands recorded instead of run."""
+    spec = importlib.util.spec_from_file_location("nvfp4_build", os.path.join(ROOT, "nvfp4_w4a4_quantized_amd", "build.py"))
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    for name, at in (("OBJDIR", "objects"), ("LIB", "libnvfp4.so"), ("BINDING", "_torch_binding.so")):
+        monkeypatch.setattr(mod, name, str(tmp_path / at))
+    mod.refuse = ()
+
+    def run(cmd, verbose):
+        if os.path.basename(cmd[0]) in mod.refuse:
+            raise FileNotFoundError(cmd[0])
+        with open(cmd[cmd.index("-o") + 1], "w") as f:
+            f.write(" ".join(cmd))
+    monkeypatch.setattr(mod, "_run", run)
+    return mod
+
+
+def test_the_library_is_built_without_torch_and_without_a_host_compiler(build, tmp_path, monkeypatch, capsys):
+    library, binding = tmp_path / "libnvfp4.so", tmp_path / "_torch_binding.so"
+    build.build()
+    assert library.exists() and binding.exists()
+    library.unlink()
+    binding.unlink()
+    build.refuse = ("g++",)
+    with pytest.raises(FileNotFoundError):            # said, with the library in place
+        build.build()
+    assert library.exists() and not binding.exists()
+    library.unlink()
+    build.refuse = ()
+    find = importlib.util.find_spec
+    monkeypatch.setattr(importlib.util, "find_spec", lambda name, *a: None if name == "torch" else find(name, *a))
+    assert build.build() == str(library) and library.exists() and not binding.exists()
+    assert "torch" in capsys.readouterr().err
