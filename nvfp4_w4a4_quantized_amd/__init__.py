@@ -360,8 +360,10 @@ def _kv_call(name, stream, *args):
     try:
         device = torch._C._cuda_getDevice()
         raw = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
-    except RuntimeError:                      # no GPU: no tensor can be on it
-        device, raw = -1, 0
+    except RuntimeError as e:
+        if torch.cuda.is_initialized():       # an earlier failure that the runtime reports now
+            raise Nvfp4Error(NVFP4_ERR_HIP, str(e)) from e
+        device, raw = -1, 0                   # no GPU in use: no tensor can be on it
     refused = getattr(_kv_binding, name)(device, raw, *args)
     if refused is not None:
         raise Nvfp4Error(*refused)

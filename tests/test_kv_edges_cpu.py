@@ -113,3 +113,23 @@ def test_the_library_is_built_without_torch_and_without_a_host_compiler(build, t
     monkeypatch.setattr(importlib.util, "find_spec", lambda name, *a: None if name == "torch" else find(name, *a))
     assert build.build() == str(library) and library.exists() and not binding.exists()
     assert "torch" in capsys.readouterr().err
+
+
+def test_a_failed_runtime_is_reported_as_such(nv, monkeypatch):   # noqa: F811
+    cache = torch.empty(4, nv.nvfp4_kv_page_bytes(2, 16, 64), dtype=torch.uint8)
+    g, x, slots = torch.ones(2), torch.zeros(3, 128), torch.zeros(3, dtype=torch.int64)
+
+    def call():
+        with pytest.raises(nv.Nvfp4Error) as e:
+            nv.nvfp4_kv_gather(cache, slots, g, g, 16, x, x.clone())
+        return e.value
+
+    def failed():
+        raise RuntimeError("HIP error: an earlier launch failed")
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", failed)
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    got = call()
+    assert got.status == nv.NVFP4_ERR_HIP and "an earlier launch failed" in str(got)
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: False)   # no GPU
+    got = call()
+    assert got.status == nv.NVFP4_ERR_INVALID_ARG and "device memory" in str(got)
