@@ -104,11 +104,12 @@ struct Rows {
   int64_t rows = 0, cols = 0, ld = 0;
 };
 
+// The stride of a dimension of one element means nothing (torch gives it any value).
 Rows rows_of(const at::Tensor* t, const char* name) {
   if (!t) return {};
-  if (t->dim() != 2 || t->stride(1) != 1)
+  if (t->dim() != 2 || (t->size(1) > 1 && t->stride(1) != 1))
     refuse(NVFP4_ERR_INVALID_ARG, "%s must be 2-D with unit column stride", name);
-  return {t->data_ptr(), t->size(0), t->size(1), t->stride(0)};
+  return {t->data_ptr(), t->size(0), t->size(1), t->size(0) == 1 ? t->size(1) : t->stride(0)};
 }
 
 int dtype_of(const at::Tensor* t, const char* name) {

@@ -213,3 +213,35 @@ def test_prompts_between_replays_of_a_captured_step(nv):
             layer.decode(x1, y1)
             assert torch.equal(y1, want)
     assert layer.workspace.numel() > held
+
+
+def test_strides_of_single_rows_and_columns_mean_nothing(nv):
+    rng = np.random.default_rng(3)
+    D, page, n = 64, 16, 16
+    x = _dev(rng.standard_normal((1, 2 * D)).astype(np.float32))
+    g = torch.full((2,), 0.002, device="cuda")
+    i32 = torch.zeros(1, dtype=torch.int32, device="cuda")
+    slots = torch.zeros(1, dtype=torch.int64, device="cuda")
+
+    def step(odd):
+        one = (lambda t: t.as_strided(t.shape, (odd, 1))) if odd is not None else (lambda t: t)
+        cache = nv.empty_kv_cache(1, 2, page, D).zero_()
+        table = i32[:, None] if odd is None else i32.as_strided((1, 1), (odd, odd))
+        outs = [torch.empty_like(x) for _ in range(4)]
+        nv.nvfp4_rope_append_kv(one(x), one(x), one(x), None, None, i32, slots, cache, g, g, page, one(outs[0]))
+        nv.nvfp4_kv_gather(cache, slots, g, g, page, one(outs[1]), one(outs[2]))
+        nv.nvfp4_kv_attention(one(outs[0]), cache, table, i32 + 1, g, g, page, one(outs[3]), n)
+        return outs + [cache]
+    plain = step(None)
+    for odd in (0, 1, 7, 1000):
+        assert all(torch.equal(a, b) for a, b in zip(step(odd), plain))
+    # several rows keep theirs: a table of one column, and rows that overlap are refused
+    many = torch.zeros(3, dtype=torch.int32, device="cuda")
+    q = x.expand(3, -1).contiguous()
+    o = [torch.empty_like(q) for _ in range(2)]
+    for out, table in zip(o, (many[:, None], many.as_strided((3, 1), (1, 0)))):
+        nv.nvfp4_kv_attention(q, plain[-1], table, many + 1, g, g, page, out, n)
+    assert torch.equal(*o)
+    for bad in (many.as_strided((3, 1), (0, 1)), many.as_strided((2, 2), (1, 1))):
+        with pytest.raises(nv.Nvfp4Error):
+            nv.nvfp4_kv_attention(q[:bad.shape[0]], plain[-1], bad, many[:bad.shape[0]], g, g, page, o[0][:bad.shape[0]], n)
