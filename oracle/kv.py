@@ -119,7 +119,7 @@ def attention_bounds(q, k, v, weights, scale, out_dtype):
     m, Hq, D = q.shape
     n, Hkv, _ = k.shape
     kr, vr = np.repeat(k, Hq // Hkv, 1), np.repeat(v, Hq // Hkv, 1)
-    mag = scale * np.einsum("mhd,nhd->mhn", np.abs(np.asarray(q, dtype=np.float64)), np.abs(kr))
+    mag = abs(scale) * np.einsum("mhd,nhd->mhn", np.abs(np.asarray(q, dtype=np.float64)), np.abs(kr))
     mag = np.where(weights > 0, mag, 0).max(-1) if n else np.zeros((m, Hq))
     ds = ((D + 16) * u + (2.0 ** -21 if out_dtype == "f32" else 0)) * mag + 16 * u
     f16 = 2.0 ** -11 if out_dtype == "bf16" else 2.0 ** -21

@@ -11,6 +11,7 @@ import torch
 
 from oracle import kv as KV
 from oracle import nvfp4 as O
+from tests.test_gpu_kv import Problem
 
 pytestmark = pytest.mark.gpu
 
@@ -245,3 +246,13 @@ def test_strides_of_single_rows_and_columns_mean_nothing(nv):
     for bad in (many.as_strided((3, 1), (0, 1)), many.as_strided((2, 2), (1, 1))):
         with pytest.raises(nv.Nvfp4Error):
             nv.nvfp4_kv_attention(q[:bad.shape[0]], plain[-1], bad, many[:bad.shape[0]], g, g, page, o[0][:bad.shape[0]], n)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [-0.2, 0.0, -0.0])
+@pytest.mark.parametrize("D,Hq,Hkv,kv,m", [
+    (128, 4, 2, [130, 40], [1, 3]), (64, 4, 1, [3000, 70], [1, 1]), (256, 2, 1, [2500, 20], [2, 1]),
+    (128, 4, 1, [300, 100], [90, 70]), (256, 4, 1, [200], [130]), (64, 56, 56, [300, 65, 7], [290, 65, 7])])
+def test_scales_that_are_not_positive(nv, dtype, scale, D, Hq, Hkv, kv, m):
+    p = Problem(nv, kv, m, Hq, Hkv, D, 16, dtype, seed=sum(kv))
+    p.check(p.run(nv, scale=scale), scale=scale, rows=sorted({0, 1, 63, 64, 89, 129, 289}))

@@ -5,9 +5,11 @@ import importlib.util
 import os
 import subprocess
 
+import numpy as np
 import pytest
 import torch
 
+from oracle import kv as KV
 from tests.test_kv_abi_cpu import _append, _gather, nv  # noqa: F401  (the fixture)
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -133,3 +135,15 @@ def test_a_failed_runtime_is_reported_as_such(nv, monkeypatch):   # noqa: F811
     monkeypatch.setattr(torch.cuda, "is_initialized", lambda: False)   # no GPU
     got = call()
     assert got.status == nv.NVFP4_ERR_INVALID_ARG and "device memory" in str(got)
+
+
+def test_bounds_of_negative_scales():
+    """A negative scale's bounds are those of the negated queries under the positive one."""
+    rng = np.random.default_rng(2)
+    q, k, v = rng.standard_normal((3, 4, 64)), rng.standard_normal((50, 2, 64)), rng.standard_normal((50, 2, 64))
+    for dtype in ("bf16", "f32"):
+        o, lse, w = KV.attention(q, k, v, -0.2)
+        o2, lse2, w2 = KV.attention(-q, k, v, 0.2)
+        assert np.allclose(o, o2, atol=1e-12) and np.allclose(lse, lse2)
+        for a, b in zip(KV.attention_bounds(q, k, v, w, -0.2, dtype), KV.attention_bounds(-q, k, v, w2, 0.2, dtype)):
+            assert np.all(a > 0) and np.allclose(a, b, rtol=1e-9)
