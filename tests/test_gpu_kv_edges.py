@@ -256,3 +256,25 @@ def test_strides_of_single_rows_and_columns_mean_nothing(nv):
 def test_scales_that_are_not_positive(nv, dtype, scale, D, Hq, Hkv, kv, m):
     p = Problem(nv, kv, m, Hq, Hkv, D, 16, dtype, seed=sum(kv))
     p.check(p.run(nv, scale=scale), scale=scale, rows=sorted({0, 1, 63, 64, 89, 129, 289}))
+
+
+@pytest.mark.parametrize("batch,Hq,Hkv,D,dtype,most_m", [
+    (65, 4, 1, 128, "bf16", 1), (100, 2, 2, 64, "bf16", 3), (130, 3, 1, 64, "f32", 1), (130, 4, 2, 128, "bf16", 2),
+    (129, 20, 1, 64, "f32", 4), (66, 2, 1, 256, "bf16", 1)])
+def test_many_sequences_cut_along_the_keys(nv, batch, Hq, Hkv, D, dtype, most_m):
+    # more sequences than a wave's lanes: each lane counts the steps of several
+    rng = np.random.default_rng(batch + D)
+    kv = [int(n) for n in rng.integers(1, 400, batch)]
+    m = [int(x) for x in rng.integers(0, most_m + 1, batch)] if most_m > 1 else [1] * batch
+    for b in range(0, batch, 7):
+        kv[b] = int(rng.integers(900, 1500))
+    for b in (3, batch // 2 + 1, batch - 2):
+        kv[b] = 0
+    kv[-1] = 1400
+    p = Problem(nv, kv, m, Hq, Hkv, D, 16, dtype, seed=batch)
+    hints = (most_m, 9000)
+    assert nv.nvfp4_kv_attention_workspace(p.T, batch, Hq, Hkv, D, *hints, p.q.dtype) > 0
+    p.check(p.run(nv, hints=hints))
+    p.check(p.run(nv, window=700, hints=hints), window=700)
+    if most_m == 1:
+        p.check(p.run(nv, hints=hints, use_cu=False))
