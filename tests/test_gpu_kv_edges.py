@@ -278,3 +278,42 @@ def test_many_sequences_cut_along_the_keys(nv, batch, Hq, Hkv, D, dtype, most_m)
     p.check(p.run(nv, window=700, hints=hints), window=700)
     if most_m == 1:
         p.check(p.run(nv, hints=hints, use_cu=False))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D,Hq,Hkv,rot,inter", [(64, 33, 2, 64, False), (128, 17, 1, 96, True), (256, 9, 1, 64, False),
+                                                (256, 8, 2, 256, True), (64, 32, 1, 0, False)])
+def test_append_beyond_the_caches(nv, dtype, D, Hq, Hkv, rot, inter):
+    """Queries of more than 32 MiB, which are read and written past the caches."""
+    size = 2 if dtype == "bf16" else 4
+    T = (32 << 20) // (Hq * D * size) + 5
+    rng = np.random.default_rng(T)
+    x = rng.standard_normal((T, Hq + 2 * Hkv, D), dtype=np.float32)
+    x = torch.from_numpy(x).to(DT[dtype]).float().numpy()
+    g = np.full(Hkv, 5 / 2688, dtype=np.float32)
+    pad, page, n_pos = 8, 64, 300
+    buf = torch.full((T, (Hq + 2 * Hkv) * D + pad), float("nan"), dtype=DT[dtype], device="cuda")
+    buf[:, :-pad] = _dev(x.reshape(T, -1))
+    q, k, v = buf[:, :-pad].split([Hq * D, Hkv * D, Hkv * D], 1)
+    n_pages = -(-T // page) + 1
+    slots = rng.permutation(n_pages * page)[:T].astype(np.int64)
+    slots[7] = -1
+    pos = rng.integers(0, n_pos, T).astype(np.int32)
+    ang = rng.uniform(0, 50, (n_pos, max(rot // 2, 1)))
+    cos, sin = np.cos(ang).astype(np.float32), np.sin(ang).astype(np.float32)
+    c, s = (_dev(cos), _dev(sin)) if rot else (None, None)
+    rotate = (lambda a: KV.rotate_f32(a, cos[pos], sin[pos], inter)) if rot else (lambda a: a)
+    want = torch.from_numpy(rotate(x[:, :Hq])).to(DT[dtype]).reshape(T, -1)
+    wk, wv = _held(rotate(x[:, Hq:Hq + Hkv]), g), _held(x[:, Hq + Hkv:], g)
+    wk[7], wv[7] = 0, 0
+    out = torch.full((T, Hq * D + pad), 3.0, dtype=DT[dtype], device="cuda")
+    for q_out in (out[:, :-pad], q):                # apart, then in place
+        cache = nv.empty_kv_cache(n_pages, Hkv, page, D).fill_(0x7F)
+        nv.nvfp4_rope_append_kv(q, k, v, c, s, _dev(pos), _dev(slots), cache, _dev(g), _dev(g), page, q_out, interleaved=inter)
+        assert torch.equal(q_out.cpu().view(torch.int16 if size == 2 else torch.int32),
+                           want.view(torch.int16 if size == 2 else torch.int32))
+        k_out, v_out = torch.empty(2, T, Hkv * D, device="cuda")
+        nv.nvfp4_kv_gather(cache, _dev(slots), _dev(g), _dev(g), page, k_out, v_out)
+        for got, w in ((k_out, wk), (v_out, wv)):
+            assert np.array_equal(got.cpu().numpy(), w.astype(np.float32).reshape(T, -1))
+    assert bool((out[:, -pad:] == 3.0).all()) and bool(buf[:, -pad:].isnan().all())
