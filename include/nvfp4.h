@@ -422,8 +422,9 @@ NVFP4_API int32_t nvfp4_kv_gather(const uint8_t* cache, int64_t n_pages, int32_t
  * p = n - m + i, attends to the tokens max(0, p - window + 1) <= t <= p:
  *   o = sum_t softmax_t(scale * <q, k_t>) v_t
  * per query head h over kv head h / (n_q_heads / n_kv_heads).  Softmax statistics and sums
- * are fp32; bf16 queries enter exactly and the weights are rounded to f16 for the second
- * product, fp32 queries and their weights go as two f16 terms each.  A row that attends to
+ * are fp32; bf16 queries enter exactly (but elements below 2^-28 of their row's largest) and
+ * the weights are rounded to f16 for the second product, fp32 queries and their weights go as
+ * two f16 terms each.  A row that attends to
  * nothing (kv_len 0, or p < 0) gives o = 0 and lse = -inf.
  *   q, o      device [T][ldq], [T][ldo] of dtype (F32 or BF16); o must not overlap q
  *   cu_q      device int32 [batch + 1], non-decreasing, from 0 to T, or NULL: one query

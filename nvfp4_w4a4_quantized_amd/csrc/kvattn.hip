@@ -9,8 +9,8 @@
 // Numerics.  Cached values e2m1 * s are exact in f16, so both products run on the f16
 // MFMA with fp32 accumulation; the global scales multiply the score and the output.
 // Query rows are scaled by a power of two so that their largest element is in
-// [2^14, 2^15): bf16 queries are then exact in f16 (elements 2^-29 below the row's
-// largest lose bits), and fp32 queries go as two f16 terms q = hi + lo.  The weights
+// [2^14, 2^15): bf16 queries are then exact in f16 (elements below 2^-28 of the row's
+// largest may lose bits), and fp32 queries go as two f16 terms q = hi + lo.  The weights
 // p = 2^(s - M) (base 2, log2 e folded into the scale) are rounded to f16 for the second
 // product where the output is bf16 (11 bits against the output's 8), and go as two f16
 // terms where it is fp32; their sum is taken of the unrounded fp32 values.  Weights are
@@ -30,11 +30,15 @@
 // in 39 us and 4.6 us for the join, 4.4 TB/s (a kernel of these loads alone 44 us before they were
 // non-temporal; a 1 GiB copy moves 5.2); 2 of 131072: 266 MB in 49 us, 5.4 TB/s, and 4.7 us; head
 // dimension 256, 16 of 32768: 226 MB in 49 us, 4.6 TB/s, and 5 us.  One sequence of 257 tokens takes
-// 6.1 us, latency.  From about 16 query columns on the vector unit binds, 450 instructions per 64
-// tokens of a wave, most of them decoding: 24 sequences of 1 to 6 drafted tokens 44 us, 2.2 TB/s.
-// Two blocks of 16 columns share a decoded granule there; three spill 180 registers.  Granules two
-// steps ahead (62 us instead of 49 then) and two steps a turn without the register copies between
-// them (no change; drafts 57 us instead of 47) did not pay.
+// 6.4 us, latency.  Drafted tokens are bound by no unit: 24 sequences of 1 to 6 tokens of 48 / 8 heads
+// take 44 us, 97 MB at 2.2 TB/s with the vector unit 34 % busy, the matrix unit 9 %, and 35 % of the
+// waves' time waiting; of a wave's 4043 vector instructions some 1500 are a piece's own, around
+// about five steps of 450 (64 tokens each, most of it decoding), and 36 columns take a second column
+// group that decodes every key again.  Two blocks of 16 columns share a decoded granule (9 or 14
+// registers spilled, one access of them in the loop over the steps; fp32 at head dimension 256
+// spills 20 or 23); three spilled 180.  Granules two steps ahead (62 us instead of 49 then) and two
+// steps a turn without the register copies between them (no change; drafts 57 us instead of 47) did
+// not pay.
 #include "kv_device.hpp"
 
 namespace nvfp4 {
@@ -710,8 +714,8 @@ KvAttnPlan kv_attn_plan(InType t, int64_t T, int32_t batch, int32_t n_q_heads, i
     // 123 / 101.  (A lane of the kernel looks up a sequence: at most 64.)
     const bool few = items <= 160;
     // So are the items of sequences of unlike lengths, which n_tokens shows, where the longest
-    // run far longer than the others: 3 x up to 2048 new tokens of up to 16384 (head dimension
-    // 256) 1337 / 903 us, 4 x 1024 of 16384 814 / 587, 2 x 2048 of 8192 387 / 312.  Equal lengths lose by it, 4 x
+    // run far longer than the others (all timed before later steps): 3 x up to 2048 new tokens of up
+    // to 16384 (head dimension 256) 1337 / 903 us, 4 x 1024 of 16384 814 / 587, 2 x 2048 of 8192 387 / 312.  Equal lengths lose by it, 4 x
     // 1024 of 16384 974 / 1004 us, 1 x 2048 of 8192 245 / 286, and short ones, 16 x 1024 of 4096 (64) 131 / 148.
     const bool unlike = 8 * T <= 7 * (int64_t)batch * max_q_len && items <= 512 && max_kv_len >= 64 * (D == 256 ? 64 : 128);
     if ((few || unlike) && batch <= 64) {
@@ -723,7 +727,8 @@ KvAttnPlan kv_attn_plan(InType t, int64_t T, int32_t batch, int32_t n_q_heads, i
     }
     return p;
   }
-  // two column blocks share a decoded granule where their registers fit
+  // two column blocks share a decoded granule where their registers fit, or nearly (head dimension
+  // 128: 9 to 14 spill)
   p.nq = cols > 16 && (D == 64 || (D == 128 && t == InType::BF16)) ? 2 : 1;
   const int64_t blk = 16 * p.nq;
   p.tile_cols = (int32_t)(cols < blk * kAttnWaves ? cols : blk * kAttnWaves);

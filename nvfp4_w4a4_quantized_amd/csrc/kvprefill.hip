@@ -29,11 +29,13 @@
 // instead of 452.
 //
 // What bounds it: matrix and vector instructions of two waves per SIMD that only partly overlap.  8192
-// tokens, 32 / 8 heads of 128: 543 us, 1013 TFLOP/s (a large f16 matrix product reaches 1193 at the
-// clock that its power leaves); the matrix unit is busy 48 % of the cycles, the vector unit 55 %,
-// LDS 36 %, and waves wait 32 %.  Head dimension 256, whose accumulators leave no registers for the
-// pipeline: 3 sequences of 300 to 2048 new tokens of up to 16384 902 us, 927 TFLOP/s.  64 columns a
-// wave at one wave per SIMD (512 registers) took 845 us where this took 606.
+// tokens, 32 / 8 heads of 128: 527 to 617 us by card, 890 to 1043 TFLOP/s (a large f16 matrix product
+// reaches 1095 to 1193 there, at the clock that its power leaves); the matrix unit is busy 47 % of the
+// cycles, the vector unit 54 %, LDS 36 %, and waves wait 32 %.  Head dimension 256, whose accumulators leave no
+// registers for the pipeline (20 or 26 spill, four or five accesses of them in the loop over the
+// tiles): 3 sequences of 300 to 2048 new tokens of up to 16384 862 to 952 us, 879 to 971 TFLOP/s, the
+// matrix unit 42 % busy, waves waiting 45 %.  64 columns a wave at one wave per SIMD (512 registers)
+// took 845 us where this took 606.
 #include <type_traits>
 
 #include "kv_device.hpp"
