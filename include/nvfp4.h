@@ -451,7 +451,8 @@ NVFP4_API int32_t nvfp4_kv_attention(const void* q, int32_t dtype, int64_t ldq, 
                            int64_t ldo, float* lse, void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Workspace bytes of a call of just these sizes (host only; 0 where it needs none).  A call of
- * smaller ones may need more: the largest of all calls to come is what a program keeps. */
+ * smaller ones may need more (fewer items are cut into more pieces): a program asks for the
+ * sizes of each call that it makes, which is arithmetic alone, and keeps the largest answer. */
 NVFP4_API int32_t nvfp4_kv_attention_workspace(int32_t dtype, int64_t T, int32_t batch, int32_t n_q_heads, int32_t n_kv_heads,
                                      int32_t head_dim, int64_t max_q_len, int64_t max_kv_len, int64_t* bytes_out);
 
