@@ -450,6 +450,30 @@ NVFP4_API int32_t nvfp4_kv_attention(const void* q, int32_t dtype, int64_t ldq, 
                            const float* k_gscale, const float* v_gscale, float scale, int32_t window, void* o,
                            int64_t ldo, float* lse, void* workspace, int64_t workspace_bytes, void* stream);
 
+/*
+ * Attention of drafted trees over the cache: as nvfp4_kv_attention, but for which tokens a
+ * query token attends to.  The m query tokens of a sequence are the nodes of a tree (or any other
+ * draft), the last m of its n cached tokens, c = n - m.  Query token i attends to every token
+ * t < c, and to token c + j where bit j of its row of tree_mask is set: the nodes on its
+ * path from the root, its own bit among them.
+ *   tree_mask  device uint64 [T][ld_mask], mask_words (1 to 64) a row: bit j is bit j % 64 of word
+ *              j / 64; 8-byte aligned.  64 * mask_words must cover max_q_len; bits from m on, and
+ *              those of tokens before the cache's first, are not looked at
+ *   window     0: none; else a query token attends to the last `window` of its tokens in
+ *              the order of their places: its path's nodes (the last in number first), then the
+ *              tokens before the tree
+ * A row that attends to nothing (no bits, and no token before the tree) gives o = 0 and lse = -inf.
+ * Positions are those that q and k were rotated by (a node's depth, as a rule), wherever the
+ * nodes stand.  The workspace is that of nvfp4_kv_attention for the same sizes.
+ */
+NVFP4_API int32_t nvfp4_kv_tree_attention(const void* q, int32_t dtype, int64_t ldq, int64_t T, int32_t n_q_heads,
+                                int32_t n_kv_heads, int32_t head_dim, int32_t batch, const int32_t* cu_q,
+                                int64_t max_q_len, const int32_t* kv_len, int64_t max_kv_len, const int32_t* page_table,
+                                int64_t max_pages, int64_t ld_table, const uint8_t* cache, int64_t n_pages,
+                                int32_t page_size, const float* k_gscale, const float* v_gscale, float scale,
+                                int32_t window, const uint64_t* tree_mask, int64_t mask_words, int64_t ld_mask, void* o,
+                                int64_t ldo, float* lse, void* workspace, int64_t workspace_bytes, void* stream);
+
 /* Workspace bytes of a call of just these sizes (host only; 0 where it needs none).  A call of
  * smaller ones may need more (fewer items are cut into more pieces): a program asks for the
  * sizes of each call that it makes, which is arithmetic alone, and keeps the largest answer. */

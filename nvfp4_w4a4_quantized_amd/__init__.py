@@ -32,7 +32,7 @@ EXPORTED = ["nvfp4_abi_version", "nvfp4_last_error", "nvfp4_quantize_act", "nvfp
             "nvfp4_require_single_scale", "nvfp4_rotate_quantize", "nvfp4_w4a4_gemm_rowcol",
             "nvfp4_gdn_gated_delta", "nvfp4_mxfp4_quantize", "nvfp4_mxfp4_gemm", "nvfp4_bench_mfma_peak",
             "nvfp4_kv_page_bytes", "nvfp4_rope_append_kv", "nvfp4_kv_gather", "nvfp4_kv_attention",
-            "nvfp4_kv_attention_workspace"]
+            "nvfp4_kv_attention_workspace", "nvfp4_kv_tree_attention"]
 
 
 class Nvfp4Error(RuntimeError):
@@ -427,6 +427,17 @@ def nvfp4_kv_attention(q, cache, page_table, kv_len, k_gscale, v_gscale, page_si
     workspace: uint8 buffer of nvfp4_kv_attention_workspace bytes; lse fp32 [T, n_q_heads]."""
     _kv_call("kv_attention", stream, cache, k_gscale, v_gscale, page_size, q, page_table, kv_len, o, max_kv_len,
              workspace, cu_q, max_q_len, scale, window, lse)
+
+
+def nvfp4_kv_tree_attention(q, cache, page_table, kv_len, k_gscale, v_gscale, page_size, o, max_kv_len, tree_mask,
+                            workspace=None, cu_q=None, max_q_len=1, scale=None, window=0, lse=None, stream=None) -> None:
+    """Attention of drafted trees: as nvfp4_kv_attention, with the sequences' query tokens
+    attending to every token before them and, of the query tokens, to those whose bit is
+    set in their row of tree_mask (int64 [T, words]: bit j of the row, the sequence's query
+    token j; the path from the root, the token itself among it).  The workspace is that of
+    nvfp4_kv_attention."""
+    _kv_call("kv_tree_attention", stream, cache, k_gscale, v_gscale, page_size, q, page_table, kv_len, o, max_kv_len,
+             workspace, cu_q, max_q_len, scale, window, lse, tree_mask)
 
 
 def nvfp4_bench_mfma_peak(iters: int, n_blocks: int, out, stream=None) -> None:

@@ -298,6 +298,86 @@ int32_t check_kv_attn_sizes(int64_t T, int32_t batch, int32_t n_q_heads, int32_t
   return check_kv_rows(T, n_q_heads);
 }
 
+// A drafted tree's bits: rows of `words` words, `ld` apart
+struct TreeMask {
+  const uint64_t* mask;
+  int64_t words, ld;
+};
+
+// tree NULL: causal
+int32_t kv_attention_call(const void* q, int32_t dtype, int64_t ldq, int64_t T, int32_t n_q_heads, int32_t n_kv_heads,
+                          int32_t head_dim, int32_t batch, const int32_t* cu_q, int64_t max_q_len, const int32_t* kv_len,
+                          int64_t max_kv_len, const int32_t* page_table, int64_t max_pages, int64_t ld_table,
+                          const uint8_t* cache, int64_t n_pages, int32_t page_size, const float* k_gscale,
+                          const float* v_gscale, float scale, int32_t window, const TreeMask* tree, void* o, int64_t ldo,
+                          float* lse, void* workspace, int64_t workspace_bytes, void* stream) {
+  nvfp4::KvAttnArgs a{};
+  int32_t st = check_kv_attn_sizes(T, batch, n_q_heads, n_kv_heads, head_dim, max_q_len, max_kv_len);
+  if (!st) st = check_kv_shape(n_kv_heads, page_size, head_dim, n_pages, &a.geom);
+  if (!st) st = check_x(q, dtype, T, (int64_t)n_q_heads * head_dim, ldq, "q");
+  if (!st) st = check_x(o, dtype, T, (int64_t)n_q_heads * head_dim, ldo, "o");
+  if (!st) st = check_kv_cache(cache, k_gscale, v_gscale);
+  if (st) return st;
+  if (!cu_q && T != batch)
+    return fail(NVFP4_ERR_INVALID_ARG, "without cu_q every sequence has one token: T=%lld must equal batch=%d",
+                (long long)T, batch);
+  if (!kv_len || !page_table) return fail(NVFP4_ERR_INVALID_ARG, "kv_len/page_table is NULL");
+  if (max_pages <= 0 || max_pages > (1ll << 30) / page_size)
+    return fail(NVFP4_ERR_INVALID_ARG, "max_pages=%lld of %d tokens: 1 to 2^30 tokens are supported",
+                (long long)max_pages, page_size);
+  if (ld_table < max_pages)
+    return fail(NVFP4_ERR_INVALID_ARG, "ld_table=%lld < max_pages=%lld", (long long)ld_table, (long long)max_pages);
+  if (!std::isfinite(scale)) return fail(NVFP4_ERR_INVALID_ARG, "scale is not finite");
+  if (window < 0) return fail(NVFP4_ERR_INVALID_ARG, "window=%d must not be negative (0 = none)", window);
+  if (tree) {
+    if (!tree->mask) return fail(NVFP4_ERR_INVALID_ARG, "tree_mask is NULL");
+    if (tree->words < 1 || tree->words > nvfp4::kMaxTreeWords)
+      return fail(tree->words < 1 ? NVFP4_ERR_INVALID_ARG : NVFP4_ERR_UNSUPPORTED, "mask_words=%lld outside [1, %d]",
+                  (long long)tree->words, nvfp4::kMaxTreeWords);
+    if (max_q_len > 64 * tree->words)
+      return fail(NVFP4_ERR_INVALID_ARG, "max_q_len=%lld exceeds the %lld bits of a row of tree_mask",
+                  (long long)max_q_len, (long long)(64 * tree->words));
+    if (tree->ld < tree->words)
+      return fail(NVFP4_ERR_INVALID_ARG, "ld_mask=%lld < mask_words=%lld", (long long)tree->ld, (long long)tree->words);
+    if (reinterpret_cast<uintptr_t>(tree->mask) & 7u)
+      return fail(NVFP4_ERR_UNSUPPORTED, "tree_mask must be 8-byte aligned");
+    a.tree = tree->mask;
+    a.ld_tree = tree->ld;
+    a.tree_words = (int32_t)tree->words;
+  }
+  const nvfp4::KvAttnPlan plan =
+      nvfp4::kv_attn_plan(in_type(dtype), T, batch, n_q_heads, n_kv_heads, head_dim, max_q_len, max_kv_len, window);
+  if (plan.workspace > 0) {
+    if (!workspace || workspace_bytes < plan.workspace)
+      return fail(NVFP4_ERR_INVALID_ARG, "workspace of %lld bytes is too small: %lld needed",
+                  (long long)(workspace ? workspace_bytes : 0), (long long)plan.workspace);
+    if (!aligned16(workspace)) return fail(NVFP4_ERR_UNSUPPORTED, "workspace must be 16-byte aligned");
+  }
+  st = check_device();
+  if (st) return st;
+  a.q = q;
+  a.ldq = ldq;
+  a.T = T;
+  a.n_q_heads = n_q_heads;
+  a.batch = batch;
+  a.cu_q = cu_q;
+  a.kv_len = kv_len;
+  a.table = page_table;
+  a.max_pages = max_pages;
+  a.ld_table = ld_table;
+  a.cache = cache;
+  a.k_gscale = k_gscale;
+  a.v_gscale = v_gscale;
+  a.scale = scale;
+  a.window = window < (1 << 30) ? window : (1 << 30);   // no sequence is longer
+  a.o = o;
+  a.ldo = ldo;
+  a.lse = lse;
+  a.part = static_cast<float*>(workspace);
+  return hip_status(nvfp4::launch_kv_attn(a, plan, in_type(dtype), head_dim, static_cast<hipStream_t>(stream)),
+                    tree ? "nvfp4_kv_tree_attention launch" : "nvfp4_kv_attention launch");
+}
+
 }  // namespace
 
 extern "C" {
@@ -694,55 +774,22 @@ int32_t nvfp4_kv_attention(const void* q, int32_t dtype, int64_t ldq, int64_t T,
                            int64_t max_pages, int64_t ld_table, const uint8_t* cache, int64_t n_pages, int32_t page_size,
                            const float* k_gscale, const float* v_gscale, float scale, int32_t window, void* o,
                            int64_t ldo, float* lse, void* workspace, int64_t workspace_bytes, void* stream) {
-  nvfp4::KvAttnArgs a{};
-  int32_t st = check_kv_attn_sizes(T, batch, n_q_heads, n_kv_heads, head_dim, max_q_len, max_kv_len);
-  if (!st) st = check_kv_shape(n_kv_heads, page_size, head_dim, n_pages, &a.geom);
-  if (!st) st = check_x(q, dtype, T, (int64_t)n_q_heads * head_dim, ldq, "q");
-  if (!st) st = check_x(o, dtype, T, (int64_t)n_q_heads * head_dim, ldo, "o");
-  if (!st) st = check_kv_cache(cache, k_gscale, v_gscale);
-  if (st) return st;
-  if (!cu_q && T != batch)
-    return fail(NVFP4_ERR_INVALID_ARG, "without cu_q every sequence has one token: T=%lld must equal batch=%d",
-                (long long)T, batch);
-  if (!kv_len || !page_table) return fail(NVFP4_ERR_INVALID_ARG, "kv_len/page_table is NULL");
-  if (max_pages <= 0 || max_pages > (1ll << 30) / page_size)
-    return fail(NVFP4_ERR_INVALID_ARG, "max_pages=%lld of %d tokens: 1 to 2^30 tokens are supported",
-                (long long)max_pages, page_size);
-  if (ld_table < max_pages)
-    return fail(NVFP4_ERR_INVALID_ARG, "ld_table=%lld < max_pages=%lld", (long long)ld_table, (long long)max_pages);
-  if (!std::isfinite(scale)) return fail(NVFP4_ERR_INVALID_ARG, "scale is not finite");
-  if (window < 0) return fail(NVFP4_ERR_INVALID_ARG, "window=%d must not be negative (0 = none)", window);
-  const nvfp4::KvAttnPlan plan =
-      nvfp4::kv_attn_plan(in_type(dtype), T, batch, n_q_heads, n_kv_heads, head_dim, max_q_len, max_kv_len, window);
-  if (plan.workspace > 0) {
-    if (!workspace || workspace_bytes < plan.workspace)
-      return fail(NVFP4_ERR_INVALID_ARG, "workspace of %lld bytes is too small: %lld needed",
-                  (long long)(workspace ? workspace_bytes : 0), (long long)plan.workspace);
-    if (!aligned16(workspace)) return fail(NVFP4_ERR_UNSUPPORTED, "workspace must be 16-byte aligned");
-  }
-  st = check_device();
-  if (st) return st;
-  a.q = q;
-  a.ldq = ldq;
-  a.T = T;
-  a.n_q_heads = n_q_heads;
-  a.batch = batch;
-  a.cu_q = cu_q;
-  a.kv_len = kv_len;
-  a.table = page_table;
-  a.max_pages = max_pages;
-  a.ld_table = ld_table;
-  a.cache = cache;
-  a.k_gscale = k_gscale;
-  a.v_gscale = v_gscale;
-  a.scale = scale;
-  a.window = window < (1 << 30) ? window : (1 << 30);   // no sequence is longer
-  a.o = o;
-  a.ldo = ldo;
-  a.lse = lse;
-  a.part = static_cast<float*>(workspace);
-  return hip_status(nvfp4::launch_kv_attn(a, plan, in_type(dtype), head_dim, static_cast<hipStream_t>(stream)),
-                    "nvfp4_kv_attention launch");
+  return kv_attention_call(q, dtype, ldq, T, n_q_heads, n_kv_heads, head_dim, batch, cu_q, max_q_len, kv_len, max_kv_len,
+                           page_table, max_pages, ld_table, cache, n_pages, page_size, k_gscale, v_gscale, scale, window,
+                           nullptr, o, ldo, lse, workspace, workspace_bytes, stream);
+}
+
+int32_t nvfp4_kv_tree_attention(const void* q, int32_t dtype, int64_t ldq, int64_t T, int32_t n_q_heads,
+                                int32_t n_kv_heads, int32_t head_dim, int32_t batch, const int32_t* cu_q,
+                                int64_t max_q_len, const int32_t* kv_len, int64_t max_kv_len, const int32_t* page_table,
+                                int64_t max_pages, int64_t ld_table, const uint8_t* cache, int64_t n_pages,
+                                int32_t page_size, const float* k_gscale, const float* v_gscale, float scale,
+                                int32_t window, const uint64_t* tree_mask, int64_t mask_words, int64_t ld_mask, void* o,
+                                int64_t ldo, float* lse, void* workspace, int64_t workspace_bytes, void* stream) {
+  const TreeMask tree{tree_mask, mask_words, ld_mask};
+  return kv_attention_call(q, dtype, ldq, T, n_q_heads, n_kv_heads, head_dim, batch, cu_q, max_q_len, kv_len, max_kv_len,
+                           page_table, max_pages, ld_table, cache, n_pages, page_size, k_gscale, v_gscale, scale, window,
+                           &tree, o, ldo, lse, workspace, workspace_bytes, stream);
 }
 
 int32_t nvfp4_mxfp4_quantize(const void* x, int32_t x_dtype, int64_t M, int64_t K, int64_t ldx, uint8_t* codes,

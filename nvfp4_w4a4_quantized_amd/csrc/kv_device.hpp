@@ -108,7 +108,19 @@ struct Span {
   int32_t all_lo, all_hi;  // tokens that every one of these columns attends to
 };
 
+// TREE: the bits decide among the query tokens, every earlier token is attended to, and a window
+// counts a row's own bits, of which it has at most m: the range is the largest that it can be.
+template <bool TREE = false>
 __device__ __forceinline__ Span span_of(const SeqInfo& s, int32_t col0, int32_t col1, const FastDiv& group, int window) {
+  if constexpr (TREE) {
+    const int32_t c0 = s.n - s.m;
+    Span r;
+    r.hi = s.n;
+    r.all_hi = c0 > 0 ? c0 : 0;
+    r.lo = window && c0 - window > 0 ? c0 - window : 0;
+    r.all_lo = window && s.n - window > 0 ? s.n - window : 0;
+    return r;
+  }
   const int32_t first = s.n - s.m + col0 / group, last = s.n - s.m + (col1 - 1) / group;
   Span r;
   r.hi = last + 1 > 0 ? last + 1 : 0;
@@ -116,6 +128,61 @@ __device__ __forceinline__ Span span_of(const SeqInfo& s, int32_t col0, int32_t 
   r.lo = window && first - window + 1 > 0 ? first - window + 1 : 0;
   r.all_lo = window && last - window + 1 > 0 ? last - window + 1 : 0;
   return r;
+}
+
+// Drafted trees.  Row `row` of q has a bit for each of its sequence's m query tokens, which stand
+// behind the first c0 = n - m tokens: bit j for token c0 + j.
+
+// Word w of a row's bits, those of tokens that the sequence does not have cleared
+__device__ __forceinline__ uint64_t tree_word(const KvAttnArgs& a, const SeqInfo& s, int64_t row, int32_t w) {
+  if (w < 0 || w >= a.tree_words) return 0;
+  uint64_t x = a.tree[row * a.ld_tree + w];
+  const int32_t past = s.m - 64 * w, before = s.m - s.n - 64 * w;    // bits [before, past) are tokens 0 <= t < n
+  if (past < 64) x = past <= 0 ? 0 : x & ((1ull << past) - 1);
+  if (before > 0) x = before >= 64 ? 0 : x & (~0ull << before);
+  return x;
+}
+
+// First token of a row's window: it attends to the last `window` of the tokens before c0 and its
+// own ones behind them, in order.
+__device__ __forceinline__ int32_t tree_floor(const KvAttnArgs& a, const SeqInfo& s, int64_t row) {
+  if (!a.window) return 0;
+  const int32_t c0 = s.n - s.m, words = (s.m + 63) >> 6 < a.tree_words ? (s.m + 63) >> 6 : a.tree_words;
+  int32_t own = 0;
+  for (int32_t w = 0; w < words; ++w) own += __builtin_popcountll(tree_word(a, s, row, w));
+  int32_t skip = own - a.window;
+  if (skip <= 0) return c0 + skip;                         // -skip tokens before c0
+  for (int32_t w = 0; w < words; ++w) {
+    uint64_t x = tree_word(a, s, row, w);
+    const int32_t bits = __builtin_popcountll(x);
+    if (skip >= bits) {
+      skip -= bits;
+      continue;
+    }
+    for (; skip > 0; --skip) x &= x - 1;
+    return c0 + 64 * w + __builtin_ctzll(x);
+  }
+  return s.n;
+}
+
+// Which of the 64 tokens from t0 on a row whose window begins at token `from` attends to
+__device__ __forceinline__ uint64_t tree_sees(const KvAttnArgs& a, const SeqInfo& s, int64_t row, int32_t from, int32_t t0) {
+  const int32_t j0 = t0 - (s.n - s.m);
+  uint64_t x = 0;
+  if (j0 > -64) {
+    const int32_t w = j0 >> 6, shift = j0 & 63;
+    x = tree_word(a, s, row, w) >> shift;
+    if (shift) x |= tree_word(a, s, row, w + 1) << (64 - shift);
+  }
+  if (j0 < 0) x |= j0 <= -64 ? ~0ull : (1ull << -j0) - 1;  // tokens before the tree
+  const int32_t skip = from - t0;
+  if (skip > 0) x &= skip >= 64 ? 0 : ~0ull << skip;
+  return x;
+}
+
+// The bytes (0xFF) that four bits stand for
+__device__ __forceinline__ uint32_t bytes_of_bits(uint32_t x) {
+  return (((x & 15u) * 0x00204081u) & 0x01010101u) * 0xFFu;
 }
 
 // The scales (a byte each) of four tokens from `first` on, those outside [lo, hi) cleared:

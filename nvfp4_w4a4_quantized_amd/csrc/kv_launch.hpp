@@ -57,6 +57,9 @@ struct KvAttnArgs {
   const float* v_gscale;
   float scale;
   int32_t window;              // 0 = none
+  const uint64_t* tree;        // NULL: causal; else the query rows' bits over their sequence's query tokens
+  int64_t ld_tree;             // words from row to row
+  int32_t tree_words;
   void* o;
   int64_t ldo;
   float* lse;                  // optional
@@ -71,6 +74,7 @@ struct KvAttnArgs {
   FastDiv by_group, by_heads, by_tile_cols, by_col_tiles, by_pairs;   // pairs: sequence, kv head
 };
 constexpr int kItemPiecesBytes = 32;
+constexpr int kMaxTreeWords = 64;
 struct KvAttnPlan {
   int32_t n_workers, blocks, min_steps, tile_cols, col_tiles, nq;
   bool prefill;                // kvprefill.hip

@@ -115,7 +115,7 @@ struct SeqWork {
   int32_t cols, tiles, begin, steps;    // begin: first token, granule-aligned
 };
 
-template <int TOK>
+template <int TOK, bool TREE>
 __device__ __forceinline__ SeqWork seq_work(const KvAttnArgs& a, const SeqInfo& seq) {
   SeqWork w;
   w.seq = seq;
@@ -123,7 +123,7 @@ __device__ __forceinline__ SeqWork seq_work(const KvAttnArgs& a, const SeqInfo& 
   w.tiles = 0;
   w.begin = w.steps = 0;
   if (w.cols > 0) {
-    const Span sp = span_of(w.seq, 0, w.cols, a.by_group, a.window);
+    const Span sp = span_of<TREE>(w.seq, 0, w.cols, a.by_group, a.window);
     const int32_t tiles = (w.cols + a.tile_cols - 1) / a.by_tile_cols;
     w.tiles = tiles < a.col_tiles ? tiles : a.col_tiles;   // further ones go with the first tiles' items
     w.begin = sp.lo & ~15;
@@ -133,7 +133,7 @@ __device__ __forceinline__ SeqWork seq_work(const KvAttnArgs& a, const SeqInfo& 
   return w;
 }
 
-template <int D, int NQ, bool GROUPS, bool F32>
+template <int D, int NQ, bool GROUPS, bool F32, bool TREE>
 __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
   constexpr int W = kAttnWaves;
   constexpr int NG = D == 256 ? 2 : 4;             // granules per step
@@ -160,7 +160,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
     b = item / a.by_heads;
     kh = item - b * hkv;
     tile0 = (int)blockIdx.x - item * a.col_tiles;
-    sw = seq_work<TOK>(a, seq_info(a, b));
+    sw = seq_work<TOK, TREE>(a, seq_info(a, b));
     if (tile0 >= sw.tiles) return;
     s_first = 0;
     s_last = sw.steps;
@@ -172,7 +172,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
       const int bb = lane * each + i;
       items = 0;
       if (bb >= a.batch) return 0;
-      const SeqWork x = seq_work<TOK>(a, seqs.held ? seqs.mine : seq_info(a, bb));
+      const SeqWork x = seq_work<TOK, TREE>(a, seqs.held ? seqs.mine : seq_info(a, bb));
       items = x.tiles * hkv;
       return x.steps;
     };
@@ -207,7 +207,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
     const int first = __builtin_ctzll(past);
     int32_t in_seq = (int32_t)blockIdx.x - __builtin_amdgcn_readlane(upto - own, first), pieces;
     for (b = first * each;; ++b) {
-      sw = seq_work<TOK>(a, seqs.at(a, b));
+      sw = seq_work<TOK, TREE>(a, seqs.at(a, b));
       pieces = (int32_t)((uint32_t)(sw.steps + S - 1) / (uint32_t)S);
       if (in_seq < sw.tiles * hkv * pieces) break;
       in_seq -= sw.tiles * hkv * pieces;
@@ -241,7 +241,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
     if (tile != tile0 && s_first > 0) break;
     const int32_t col_first = tile * a.tile_cols;
     const int32_t cols = col_first + a.tile_cols < sw.cols ? col_first + a.tile_cols : sw.cols;   // end of the tile
-    Span sp = span_of(seq, col_first, cols, a.by_group, a.window);
+    Span sp = span_of<TREE>(seq, col_first, cols, a.by_group, a.window);
     int32_t begin = sw.begin, s0 = s_first, s1 = s_last;
     bool whole = s0 == 0 && s1 == sw.steps;
     if (a.n_workers == 0 || tile != tile0) {       // the tile's own keys
@@ -290,7 +290,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
     // query columns: lane (g, r) holds column r of every block, the chunks' elements
     f16x8 qf[TERMS][NQ][KC];
     float csc[NQ], m[NQ], l[NQ];
-    int32_t limit[NQ], floor_[NQ];                 // the column attends to floor_ <= t < limit
+    int32_t limit[NQ], floor_[NQ];                 // the column attends to floor_ <= t < limit (TREE: limit is its row of q)
     f32x4 acc[NQ][NJ];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
@@ -318,8 +318,8 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
           qf[0][n][c][i] = hi;
           if constexpr (F32) qf[TERMS - 1][n][c][i] = (_Float16)(x - (float)hi);
         }
-      limit[n] = pos + 1;
-      floor_[n] = a.window ? pos - a.window + 1 : 0;
+      limit[n] = TREE ? seq.q0 + qi : pos + 1;
+      floor_[n] = TREE ? tree_floor(a, seq, seq.q0 + qi) : (a.window ? pos - a.window + 1 : 0);
       m[n] = kNegBig;
       l[n] = 0.0f;
 #pragma unroll
@@ -366,15 +366,27 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
 
         // weights, in the layout of the second product's B operand
         f16x8 pf[TERMS][NQ][NG / 2];
+        uint64_t seen = 0;                         // TREE: tokens of this step that any column attends to
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
           if (edge) {
-            const int32_t upto = limit[n] - t0 - 4 * g, from = floor_[n] - t0 - 4 * g;
+            if constexpr (TREE) {
+              uint64_t sees = tree_sees(a, seq, limit[n], floor_[n], t0);
+              seen |= sees;
+              sees >>= 4 * g;
 #pragma unroll
-            for (int u = 0; u < NG; ++u)
+              for (int u = 0; u < NG; ++u)
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (16 * u + i >= upto || 16 * u + i < from) sc[n][u][i] = -__builtin_inff();
+                for (int i = 0; i < 4; ++i)
+                  if (!((sees >> (16 * u + i)) & 1)) sc[n][u][i] = -__builtin_inff();
+            } else {
+              const int32_t upto = limit[n] - t0 - 4 * g, from = floor_[n] - t0 - 4 * g;
+#pragma unroll
+              for (int u = 0; u < NG; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  if (16 * u + i >= upto || 16 * u + i < from) sc[n][u][i] = -__builtin_inff();
+            }
             if (wide) {
               const float factor = s_c[wave][16 * n + r];
 #pragma unroll
@@ -409,9 +421,16 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
         }
 
         // O^T += V^T P^T: rows = elements NJ r + j
-        if (t0 < sp.lo || t0 + TOK > seq.n) {
+        if (TREE ? edge : t0 < sp.lo || t0 + TOK > seq.n) {
+          if constexpr (TREE) {
 #pragma unroll
-          for (int u = 0; u < NG; ++u) cur[u].vs = live_scales(cur[u].vs, t0 + 16 * u + 4 * g, sp.lo, seq.n);
+            for (int off = 1; off < 16; off <<= 1) seen |= __shfl_xor(seen, off);
+#pragma unroll
+            for (int u = 0; u < NG; ++u) cur[u].vs &= bytes_of_bits((uint32_t)(seen >> (16 * u + 4 * g)));
+          } else {
+#pragma unroll
+            for (int u = 0; u < NG; ++u) cur[u].vs = live_scales(cur[u].vs, t0 + 16 * u + 4 * g, sp.lo, seq.n);
+          }
         }
 #pragma unroll
         for (int k = 0; k < NG / 2; ++k) {
@@ -664,13 +683,17 @@ __global__ __launch_bounds__(256) void k_kv_join_many(KvAttnArgs a) {
   store_joined<D, F32>(a, item, c, 4 * part, out, top, sum);
 }
 
+template <int D, int NQ, bool F32, bool TREE>
+void launch_items(const KvAttnArgs& a, hipStream_t s) {
+  const dim3 blocks((unsigned)a.blocks), threads(64 * kAttnWaves);
+  if (a.tile_cols > 16 * NQ) hipLaunchKernelGGL((k_kv_attn<D, NQ, true, F32, TREE>), blocks, threads, 0, s, a);
+  else hipLaunchKernelGGL((k_kv_attn<D, NQ, false, F32, TREE>), blocks, threads, 0, s, a);
+}
+
 template <int D, int NQ, bool F32>
 hipError_t launch(const KvAttnArgs& a, hipStream_t s) {
-  const int64_t blocks = a.blocks;
-  if (a.tile_cols > 16 * NQ)
-    hipLaunchKernelGGL((k_kv_attn<D, NQ, true, F32>), dim3((unsigned)blocks), dim3(64 * kAttnWaves), 0, s, a);
-  else
-    hipLaunchKernelGGL((k_kv_attn<D, NQ, false, F32>), dim3((unsigned)blocks), dim3(64 * kAttnWaves), 0, s, a);
+  if (a.tree) launch_items<D, NQ, F32, true>(a, s);
+  else launch_items<D, NQ, F32, false>(a, s);
   const hipError_t e = hipGetLastError();
   return e == hipSuccess && a.n_workers ? launch_kv_join(a, F32 ? InType::F32 : InType::BF16, D, s) : e;
 }

@@ -65,6 +65,14 @@ constexpr int kVTile = D * kVRow<D>;
 // after the tiles: the columns' score factors where a wave's are wide
 template <int D>
 constexpr int kFactors = 2 * (kKTile<D> + kVTile<D>);
+// after those, of a tree's tile: the first token that any column attends to, and the bits of the
+// tree's tokens that any column attends to
+template <int D>
+constexpr int kTreeFirst = kFactors<D> + 4 * kPrefillCols;
+template <int D>
+constexpr int kTreeAny = kTreeFirst<D> + 16;
+template <int D, bool TREE>
+constexpr int kLdsBytes = TREE ? kTreeAny<D> + 8 * kMaxTreeWords : kTreeFirst<D>;
 
 template <typename T>
 __device__ __forceinline__ __attribute__((address_space(3))) T& lds_at(uint32_t at) {
@@ -101,10 +109,10 @@ __device__ __forceinline__ void read_dwords(const uint8_t* p, uint32_t* d) {
 struct TileSpan {
   int32_t lo, begin, steps;
 };
-template <int D>
+template <int D, bool TREE>
 __device__ __forceinline__ TileSpan tile_span(const KvAttnArgs& a, const SeqInfo& seq, int32_t tile, int group) {
   const int32_t cols = seq.m * group, first = tile * kPrefillCols;
-  const Span s = span_of(seq, first, first + kPrefillCols < cols ? first + kPrefillCols : cols, a.by_group, a.window);
+  const Span s = span_of<TREE>(seq, first, first + kPrefillCols < cols ? first + kPrefillCols : cols, a.by_group, a.window);
   TileSpan t;
   t.lo = s.lo;
   t.begin = s.lo & ~15;
@@ -121,7 +129,7 @@ __device__ __forceinline__ int32_t planned_tiles(const KvAttnArgs& a, const SeqI
 
 // SPLIT: workgroups have pieces of items instead of items (a template parameter: its
 // registers cost the other form 2 to 5 %)
-template <int D, bool SPLIT>
+template <int D, bool SPLIT, bool TREE>
 __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs a) {
   constexpr bool PIPE = D <= 128;
   constexpr int TOK = kTok<D>;
@@ -156,7 +164,7 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
     for (b = 0; b < a.batch; ++b) {
       seq = seqs.at(a, b);
       const int32_t tiles = planned_tiles(a, seq, group);
-      for (int32_t t = lane; t < tiles; t += 64) total += (float)tile_span<D>(a, seq, t, group).steps;
+      for (int32_t t = lane; t < tiles; t += 64) total += (float)tile_span<D, TREE>(a, seq, t, group).steps;
     }
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) total += __shfl_xor(total, off);
@@ -170,7 +178,7 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
       seq = seqs.at(a, b);
       tiles = planned_tiles(a, seq, group);
       of_head = 0;
-      for (int32_t t = lane; t < tiles; t += 64) of_head += pieces_of(tile_span<D>(a, seq, t, group).steps);
+      for (int32_t t = lane; t < tiles; t += 64) of_head += pieces_of(tile_span<D, TREE>(a, seq, t, group).steps);
 #pragma unroll
       for (int off = 1; off < 64; off <<= 1) of_head += __shfl_xor(of_head, off);
       of_head = __builtin_amdgcn_readfirstlane(of_head);
@@ -185,7 +193,7 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
     rest -= kh * of_head;
     int32_t pieces = 1;
     for (int32_t t0 = 0;; t0 += 64) {
-      const int32_t own = t0 + lane < tiles ? pieces_of(tile_span<D>(a, seq, t0 + lane, group).steps) : 0;
+      const int32_t own = t0 + lane < tiles ? pieces_of(tile_span<D, TREE>(a, seq, t0 + lane, group).steps) : 0;
       int32_t upto = own;
 #pragma unroll
       for (int off = 1; off < 64; off <<= 1) {
@@ -202,7 +210,7 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
       }
       rest -= __builtin_amdgcn_readlane(upto, 63);
     }
-    const int32_t steps = tile_span<D>(a, seq, tile0, group).steps;
+    const int32_t steps = tile_span<D, TREE>(a, seq, tile0, group).steps;
     if (pieces > 1) {
       const int32_t q = (int32_t)((uint32_t)steps / (uint32_t)pieces), more = steps - q * pieces;
       s_first = rest * q + (rest < more ? rest : more);
@@ -231,7 +239,7 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
     if (SPLIT && tile != tile0 && s_first > 0) break;
     const int32_t col_first = tile * kPrefillCols;
     const int32_t col_end = col_first + kPrefillCols < cols ? col_first + kPrefillCols : cols;
-    const TileSpan span = tile_span<D>(a, seq, tile, group);
+    const TileSpan span = tile_span<D, TREE>(a, seq, tile, group);
     const int32_t begin = whole ? span.begin : span.begin + s_first * TOK;
     const int32_t steps = whole ? span.steps : s_last - s_first;
 
@@ -239,7 +247,7 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
     const int32_t col0 = col_first + 32 * wave;
     const int32_t w0 = col0 < col_end ? col0 : col_end - 1;
     const int32_t w1 = col0 + 32 < col_end ? col0 + 32 : col_end;
-    const Span sp = span_of(seq, w0, w1, a.by_group, a.window);
+    const Span sp = span_of<TREE>(seq, w0, w1, a.by_group, a.window);
 
     // loads of tile s: this wave's granule, its page id known one tile ahead
     auto page_of = [&](int32_t s) -> int32_t {
@@ -277,7 +285,20 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
       read_dwords<KD>(p + 9 * D + (16 * quad + part) * (D / 8), rv);
       vsc = *reinterpret_cast<const uint32_t*>(p + 17 * D + (quad * (D / 16) + part * D / 256) * 4);
       const int32_t first = begin + s * TOK + 16 * gran;
-      if (first < span.lo || first + 16 > seq.n) vsc = live_scales(vsc, first + 4 * quad, span.lo, seq.n);
+      if constexpr (TREE) {
+        const int32_t c0 = seq.n - seq.m, from = lds_at<int32_t>(lds + kTreeFirst<D>);
+        if (first < from || first + 16 > c0) {
+          uint32_t any = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int32_t t = first + 4 * quad + e, j = t - c0;
+            const bool node = j >= 0 && j < seq.m && j < 64 * a.tree_words;
+            const bool sees = node ? (lds_at<uint32_t>(lds + kTreeAny<D> + 4 * (j >> 5)) >> (j & 31)) & 1 : j < 0 && t >= from;
+            any |= (uint32_t)sees << e;
+          }
+          vsc &= bytes_of_bits(any);
+        }
+      } else if (first < span.lo || first + 16 > seq.n) vsc = live_scales(vsc, first + 4 * quad, span.lo, seq.n);
     };
     // decode dword i of the loaded keys: a 16-byte chunk of a token's row
     auto decode_k = [&](uint32_t kb, int i) {               // kb: the lane's first chunk in the tile
@@ -311,6 +332,26 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
 
     int32_t id_next = 0;
     __syncthreads();                               // the tile before is done with LDS
+    if constexpr (TREE) {
+      const int32_t rows = (col_end - 1) / a.by_group - col_first / a.by_group + 1;
+      const int32_t words = (seq.m + 63) >> 6 < a.tree_words ? (seq.m + 63) >> 6 : a.tree_words;
+      if (threadIdx.x < 2 * kMaxTreeWords) lds_at<uint32_t>(lds + kTreeAny<D> + 4 * threadIdx.x) = 0;
+      if (threadIdx.x == 0) lds_at<int32_t>(lds + kTreeFirst<D>) = INT32_MAX;
+      __syncthreads();
+      for (int32_t i = threadIdx.x; i < rows; i += 64 * kPrefillWaves) {
+        const int64_t row = seq.q0 + col_first / a.by_group + i;
+        const int32_t from = tree_floor(a, seq, row);
+        atomicMin((int32_t*)(shared + kTreeFirst<D>), from);
+        for (int32_t w = 0; w < words; ++w) {
+          uint64_t x = tree_word(a, seq, row, w);
+          const int32_t skip = from - (seq.n - seq.m) - 64 * w;
+          if (skip > 0) x &= skip >= 64 ? 0 : ~0ull << skip;
+          atomicOr((uint32_t*)(shared + kTreeAny<D>) + 2 * w, (uint32_t)x);
+          atomicOr((uint32_t*)(shared + kTreeAny<D>) + 2 * w + 1, (uint32_t)(x >> 32));
+        }
+      }
+      __syncthreads();
+    }
     if (steps > 0) {
       const int32_t id = page_of(0);
       if (D != 256 || wave < 4) load_k(0, id);
@@ -356,7 +397,8 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
     }
     const int32_t all_lo = wide ? INT32_MAX : sp.all_lo;   // wide: every block takes the slower way
     const int32_t pos = seq.n - seq.m + qi;
-    const int32_t limit = pos + 1, floor_ = a.window ? pos - a.window + 1 : 0;
+    const int32_t limit = pos + 1;
+    const int32_t floor_ = TREE ? tree_floor(a, seq, seq.q0 + qi) : (a.window ? pos - a.window + 1 : 0);
     float m = kNegBig, l = 0.0f;
     f32x16 acc[NB];
 #pragma unroll
@@ -381,11 +423,18 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
     // scaled by
     auto reference = [&](int32_t t0, f32x16& sc) {
       if (t0 < all_lo || t0 + 32 > sp.all_hi) {
-        const int32_t upto = limit - t0 - 4 * h, from = floor_ - t0 - 4 * h;
+        if constexpr (TREE) {
+          const uint32_t sees = (uint32_t)tree_sees(a, seq, seq.q0 + qi, floor_, t0) >> (4 * h);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int32_t t = 8 * (e / 4) + e % 4;
-          if (t >= upto || t < from) sc[e] = -__builtin_inff();
+          for (int e = 0; e < 16; ++e)
+            if (!((sees >> (8 * (e / 4) + e % 4)) & 1)) sc[e] = -__builtin_inff();
+        } else {
+          const int32_t upto = limit - t0 - 4 * h, from = floor_ - t0 - 4 * h;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int32_t t = 8 * (e / 4) + e % 4;
+            if (t >= upto || t < from) sc[e] = -__builtin_inff();
+          }
         }
         if (wide) {
           const float factor = lds_at<float>(lds + kFactors<D> + 4 * (32 * wave + c32));
@@ -604,19 +653,20 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
   }
 }
 
-template <int D, bool SPLIT>
+template <int D, bool SPLIT, bool TREE>
 hipError_t launch(const KvAttnArgs& a, hipStream_t s) {
-  constexpr int bytes = kFactors<D> + 4 * kPrefillCols;
-  const hipError_t e = lds_limit_once<k_kv_prefill<D, SPLIT>>(bytes);
+  constexpr int bytes = kLdsBytes<D, TREE>;
+  const hipError_t e = lds_limit_once<k_kv_prefill<D, SPLIT, TREE>>(bytes);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((k_kv_prefill<D, SPLIT>), dim3((unsigned)a.blocks), dim3(64 * kPrefillWaves), bytes, s, a);
+  hipLaunchKernelGGL((k_kv_prefill<D, SPLIT, TREE>), dim3((unsigned)a.blocks), dim3(64 * kPrefillWaves), bytes, s, a);
   const hipError_t launched = hipGetLastError();
   return SPLIT && launched == hipSuccess ? launch_kv_join(a, InType::BF16, D, s) : launched;
 }
 
 template <int D>
 hipError_t launch(const KvAttnArgs& a, hipStream_t s) {
-  return a.n_workers ? launch<D, true>(a, s) : launch<D, false>(a, s);
+  if (a.tree) return a.n_workers ? launch<D, true, true>(a, s) : launch<D, false, true>(a, s);
+  return a.n_workers ? launch<D, true, false>(a, s) : launch<D, false, false>(a, s);
 }
 
 }  // namespace

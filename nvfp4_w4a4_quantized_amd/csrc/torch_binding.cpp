@@ -234,8 +234,9 @@ int kv_gather(Args& a) {
 }
 
 // device, stream, cache, k_gscale, v_gscale, page_size, q, page_table, kv_len, o, max_kv_len, workspace, cu_q,
-// max_q_len, scale (None: 1/sqrt(d)), window, lse
-int kv_attention(Args& a) {
+// max_q_len, scale (None: 1/sqrt(d)), window, lse, and with TREE tree_mask
+template <bool TREE>
+int attention(Args& a) {
   const Cache c = cache_of(a);
   const at::Tensor *tq = a.tensor("q"), *table = a.tensor("page_table"), *kv_len = a.tensor("kv_len"),
                    *to = a.tensor("o");
@@ -258,20 +259,33 @@ int kv_attention(Args& a) {
               lse->size(1) != heads || !lse->is_contiguous()))
     refuse(NVFP4_ERR_INVALID_ARG, "lse must be contiguous float32 [%lld, %lld]", (long long)q.rows, (long long)heads);
   if (ws && !ws->is_contiguous()) refuse(NVFP4_ERR_INVALID_ARG, "workspace must be contiguous");
-  return nvfp4_kv_attention(
-      q.p, dtype, q.ld, q.rows, (int32_t)heads, c.heads, c.d, (int32_t)tab.rows,
-      indices<int32_t>(cu, at::kInt, "int32", tab.rows + 1, "cu_q"), max_q_len,
-      indices<int32_t>(kv_len, at::kInt, "int32", tab.rows, "kv_len"), max_kv_len,
-      static_cast<const int32_t*>(tab.p), tab.cols, tab.ld, c.p, c.pages, c.page_size, c.kg, c.vg,
-      (float)scale, window, o.p, o.ld,
-      lse ? static_cast<float*>(lse->data_ptr()) : nullptr, ws ? ws->data_ptr() : nullptr,
-      ws ? (int64_t)(ws->numel() * ws->element_size()) : 0, a.stream());
+  const int32_t* const cu_q = indices<int32_t>(cu, at::kInt, "int32", tab.rows + 1, "cu_q");
+  const int32_t* const lens = indices<int32_t>(kv_len, at::kInt, "int32", tab.rows, "kv_len");
+  const int32_t* const pages = static_cast<const int32_t*>(tab.p);
+  float* const lse_p = lse ? static_cast<float*>(lse->data_ptr()) : nullptr;
+  void* const ws_p = ws ? ws->data_ptr() : nullptr;
+  const int64_t ws_bytes = ws ? (int64_t)(ws->numel() * ws->element_size()) : 0;
+  if constexpr (TREE) {
+    const at::Tensor* mask = a.tensor("tree_mask");
+    if (mask->scalar_type() != at::kLong) refuse(NVFP4_ERR_UNSUPPORTED, "tree_mask must be int64");
+    const Rows bits = rows_of(mask, "tree_mask");
+    if (bits.rows != q.rows) refuse(NVFP4_ERR_INVALID_ARG, "tree_mask must be [%lld, words]", (long long)q.rows);
+    return nvfp4_kv_tree_attention(q.p, dtype, q.ld, q.rows, (int32_t)heads, c.heads, c.d, (int32_t)tab.rows, cu_q,
+                                   max_q_len, lens, max_kv_len, pages, tab.cols, tab.ld, c.p, c.pages, c.page_size, c.kg,
+                                   c.vg, (float)scale, window, static_cast<const uint64_t*>(bits.p), bits.cols, bits.ld,
+                                   o.p, o.ld, lse_p, ws_p, ws_bytes, a.stream());
+  } else {
+    return nvfp4_kv_attention(q.p, dtype, q.ld, q.rows, (int32_t)heads, c.heads, c.d, (int32_t)tab.rows, cu_q, max_q_len,
+                              lens, max_kv_len, pages, tab.cols, tab.ld, c.p, c.pages, c.page_size, c.kg, c.vg,
+                              (float)scale, window, o.p, o.ld, lse_p, ws_p, ws_bytes, a.stream());
+  }
 }
 
 PyMethodDef methods[] = {
     {"rope_append_kv", reinterpret_cast<PyCFunction>(entry<rope_append_kv, 15>), METH_FASTCALL, nullptr},
     {"kv_gather", reinterpret_cast<PyCFunction>(entry<kv_gather, 9>), METH_FASTCALL, nullptr},
-    {"kv_attention", reinterpret_cast<PyCFunction>(entry<kv_attention, 17>), METH_FASTCALL, nullptr},
+    {"kv_attention", reinterpret_cast<PyCFunction>(entry<attention<false>, 17>), METH_FASTCALL, nullptr},
+    {"kv_tree_attention", reinterpret_cast<PyCFunction>(entry<attention<true>, 18>), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_torch_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

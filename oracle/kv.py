@@ -84,23 +84,41 @@ def gather(cache, slots, Hkv, D, kg, vg, page):
 def attention(q, k, v, scale, window=0):
     """One sequence: q [m, Hq, D], the last m of the n tokens of k, v [n, Hkv, D].
     Returns (o [m, Hq, D], lse [m, Hq], weights [m, Hq, n]) in float64."""
+    m, n = q.shape[0], k.shape[0]
+    rows = []
+    for i in range(m):
+        p = n - m + i
+        rows.append(range(max(0, p - window + 1) if window else 0, p + 1))
+    return _attend(q, k, v, scale, rows)
+
+
+def tree_attention(q, k, v, scale, paths, window=0):
+    """The same for a drafted tree: query token i attends to the tokens before the m query
+    tokens and to those of the query tokens that paths[i] (numbers from 0 to m - 1) holds;
+    with a window, to the last `window` of these."""
+    c = k.shape[0] - q.shape[0]
+    rows = [list(range(c)) + [c + j for j in sorted(p) if c + j >= 0] for p in paths]
+    return _attend(q, k, v, scale, [r[-window:] if window else r for r in rows])
+
+
+def _attend(q, k, v, scale, rows):
+    """Attention of query token i to the tokens rows[i]."""
     m, Hq, D = q.shape
     n, Hkv, _ = k.shape
     q = np.asarray(q, dtype=np.float64)
     o, lse, weights = np.zeros((m, Hq, D)), np.full((m, Hq), -np.inf), np.zeros((m, Hq, n))
-    for i in range(m):
-        p = n - m + i
-        lo = max(0, p - window + 1) if window else 0
-        if p < lo:
+    for i, at in enumerate(rows):
+        if not len(at):
             continue
+        at = slice(at.start, at.stop) if isinstance(at, range) else np.array(at)
         for h in range(Hq):
             kh = h // (Hq // Hkv)
-            s = scale * (k[lo:p + 1, kh] @ q[i, h])
+            s = scale * (k[at, kh] @ q[i, h])
             top = s.max()
             w = np.exp(s - top)
             lse[i, h] = top + np.log(w.sum())
-            weights[i, h, lo:p + 1] = w / w.sum()
-            o[i, h] = weights[i, h, lo:p + 1] @ v[lo:p + 1, kh]
+            weights[i, h, at] = w / w.sum()
+            o[i, h] = weights[i, h, at] @ v[at, kh]
     return o, lse, weights
 
 
