@@ -93,6 +93,9 @@ def _load() -> ctypes.CDLL:
     lib.nvfp4_kv_attention.restype = I32
     lib.nvfp4_kv_attention.argtypes = [P, I32, I64, I64, I32, I32, I32, I32, P, I64, P, I64, P, I64, I64, P, I64, I32, P, P,
                                        ctypes.c_float, I32, P, I64, P, P, I64, P]
+    lib.nvfp4_kv_tree_attention.restype = I32
+    lib.nvfp4_kv_tree_attention.argtypes = (lib.nvfp4_kv_attention.argtypes[:22] + [P, I64, I64]
+                                            + lib.nvfp4_kv_attention.argtypes[22:])
     lib.nvfp4_kv_attention_workspace.restype = I32
     lib.nvfp4_kv_attention_workspace.argtypes = [I32, I64, I32, I32, I32, I32, I64, I64, P]
     return lib
