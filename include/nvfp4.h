@@ -481,6 +481,81 @@ NVFP4_API int32_t nvfp4_kv_attention_workspace(int32_t dtype, int64_t T, int32_t
                                      int32_t head_dim, int64_t max_q_len, int64_t max_kv_len, int64_t* bytes_out);
 
 /*
+ * The accepted path of a drafted tree, after nvfp4_kv_tree_attention: of the m query tokens of
+ * sequence b, the last of its n = kv_len[b] tokens, the count = n_accepted[b] (0 to max_accepted) whose
+ * numbers are accepted[b][0 ..] move to the places n - m, n - m + 1, ..., keys and values of every
+ * head, and the sequence has n - m + count tokens.  All rows are read before any is written: the
+ * numbers, each below m, may stand in any order (and more than once).
+ *   cu_q       device int32 [batch + 1], as for the attention, or NULL: m = 1
+ *   accepted   device int32 [batch][ld_accepted], max_accepted (1 to 256) a row
+ *   n_accepted device int32 [batch]
+ *   kv_len_out device int32 [batch]: the new lengths; may be kv_len itself
+ * The pages that it writes must be the sequence's alone.  Numbers outside their range are
+ * clamped into it; a row whose page is not in the cache is not moved.
+ */
+NVFP4_API int32_t nvfp4_kv_accept(uint8_t* cache, int64_t n_pages, int32_t page_size, int32_t n_kv_heads, int32_t head_dim,
+                        int32_t batch, const int32_t* kv_len, const int32_t* cu_q, const int32_t* page_table,
+                        int64_t max_pages, int64_t ld_table, const int32_t* accepted, int64_t max_accepted,
+                        int64_t ld_accepted, const int32_t* n_accepted, int32_t* kv_len_out, void* stream);
+
+/*
+ * The attention weight that cached tokens receive, by which nvfp4_kv_evict chooses.  Sequences, query
+ * tokens and what each attends to are those of nvfp4_kv_attention, whose log-sums lse are
+ * taken in; for every token t of a sequence with m > 0 query tokens and n cached ones, and every kv head,
+ *   w_t = (t < n - m ? decay * w_t : 0) + sum over query tokens i that attend to t and heads h of the
+ *         kv head's group of e^{scale <q_ih, k_t> - lse_ih}
+ * in fp32 (the tokens that are new in this call begin at 0; a decay of 0 reads no earlier
+ * weights).  A sequence without query tokens keeps its weights.
+ *   lse          device fp32 [T][n_q_heads]; -inf: the row has no weights
+ *   key_weights  device fp32 [n_pages][n_kv_heads][page_size], 16-byte aligned: a weight for each slot
+ *                and kv head.  The pages of a call's sequences must be each sequence's alone.
+ * Products are those of the attention; an exponent is off by up to about 2^-23 of |scale <q, k>| +
+ * |lse|, which the rounding of lse alone may cost.  Sums are in the same order in every call.
+ * A weight whose page is not in the cache is not written.
+ */
+NVFP4_API int32_t nvfp4_kv_attention_weights(const void* q, int32_t dtype, int64_t ldq, int64_t T, int32_t n_q_heads,
+                                   int32_t n_kv_heads, int32_t head_dim, int32_t batch, const int32_t* cu_q,
+                                   int64_t max_q_len, const int32_t* kv_len, int64_t max_kv_len,
+                                   const int32_t* page_table, int64_t max_pages, int64_t ld_table, const uint8_t* cache,
+                                   int64_t n_pages, int32_t page_size, const float* k_gscale, float scale, int32_t window,
+                                   const float* lse, float* key_weights, float decay, void* stream);
+
+/*
+ * Eviction: sequences of more than `budget` tokens are cut to it, each kv head by its own weights.
+ * A head of n > budget tokens keeps the first keep_first, the last keep_last and, of the tokens between,
+ * the budget - keep_first - keep_last of the largest weights (equal ones: the lowest token first; a
+ * NaN counts as -inf).  Rows move within the sequence's pages, as few as can be:
+ *   place j < keep_first                   token j
+ *   places budget - keep_last .. budget-1  the last tokens, in their order
+ *   places between                         kept tokens below budget - keep_last stay; the other kept ones,
+ *                                          in their order, fill the free places, from the lowest on
+ * Attention does not ask for the order of tokens (keys are rotated already), but a window counts
+ * places: it is right over the first evicted cache only as far as keep_last goes.
+ *   key_weights  device fp32 [n_pages][n_kv_heads][page_size]
+ *   weights_out  the same shape, or NULL: the kept tokens' weights at their new places; may be
+ *                key_weights itself
+ *   kept         device int32 [batch][n_kv_heads][budget] or NULL: the earlier place of the token at each new
+ *                place (-1 past the new length)
+ *   max_kv_len   host: bound on the lengths, from which the launch is chosen; longer sequences
+ *                are right too, more slowly
+ *   kv_len_out   device int32 [batch]: min(n, budget); may be kv_len itself
+ *   workspace    device, at least nvfp4_kv_evict_workspace(...) bytes, 16-byte aligned; calls that
+ *                overlap on the GPU need one each, and a recorded graph its own
+ * The pages that it writes must be the sequence's alone.  A row whose page (or place's page) is not in
+ * the cache is not moved.
+ */
+NVFP4_API int32_t nvfp4_kv_evict(uint8_t* cache, int64_t n_pages, int32_t page_size, int32_t n_kv_heads, int32_t head_dim,
+                       const float* key_weights, float* weights_out, int32_t batch, const int32_t* kv_len,
+                       int64_t max_kv_len, const int32_t* page_table, int64_t max_pages, int64_t ld_table, int64_t budget,
+                       int64_t keep_first, int64_t keep_last, int32_t* kept, int32_t* kv_len_out, void* workspace,
+                       int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes of an eviction of these sizes (host only); a call of smaller ones, with the same
+ * budget, needs no more. */
+NVFP4_API int32_t nvfp4_kv_evict_workspace(int32_t batch, int32_t n_kv_heads, int64_t budget, int64_t max_kv_len,
+                                 int64_t* bytes_out);
+
+/*
  * Measurement helper, not part of the layer: a kernel that only issues f16 MFMA
  * 32x32x16 instructions (n_blocks workgroups of 4 waves, each wave 4 x iters of
  * them, 32768 FLOP each), so that a benchmark can report the matrix rate the chip

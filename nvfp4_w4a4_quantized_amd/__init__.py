@@ -32,7 +32,8 @@ EXPORTED = ["nvfp4_abi_version", "nvfp4_last_error", "nvfp4_quantize_act", "nvfp
             "nvfp4_require_single_scale", "nvfp4_rotate_quantize", "nvfp4_w4a4_gemm_rowcol",
             "nvfp4_gdn_gated_delta", "nvfp4_mxfp4_quantize", "nvfp4_mxfp4_gemm", "nvfp4_bench_mfma_peak",
             "nvfp4_kv_page_bytes", "nvfp4_rope_append_kv", "nvfp4_kv_gather", "nvfp4_kv_attention",
-            "nvfp4_kv_attention_workspace", "nvfp4_kv_tree_attention"]
+            "nvfp4_kv_attention_workspace", "nvfp4_kv_tree_attention", "nvfp4_kv_accept", "nvfp4_kv_attention_weights",
+            "nvfp4_kv_evict", "nvfp4_kv_evict_workspace"]
 
 
 class Nvfp4Error(RuntimeError):
@@ -96,6 +97,15 @@ def _load() -> ctypes.CDLL:
     lib.nvfp4_kv_tree_attention.restype = I32
     lib.nvfp4_kv_tree_attention.argtypes = (lib.nvfp4_kv_attention.argtypes[:22] + [P, I64, I64]
                                             + lib.nvfp4_kv_attention.argtypes[22:])
+    lib.nvfp4_kv_accept.restype = I32
+    lib.nvfp4_kv_accept.argtypes = [P, I64, I32, I32, I32, I32, P, P, P, I64, I64, P, I64, I64, P, P, P]
+    lib.nvfp4_kv_attention_weights.restype = I32
+    lib.nvfp4_kv_attention_weights.argtypes = [P, I32, I64, I64, I32, I32, I32, I32, P, I64, P, I64, P, I64, I64, P, I64, I32,
+                                               P, ctypes.c_float, I32, P, P, ctypes.c_float, P]
+    lib.nvfp4_kv_evict.restype = I32
+    lib.nvfp4_kv_evict.argtypes = [P, I64, I32, I32, I32, P, P, I32, P, I64, P, I64, I64, I64, I64, I64, P, P, P, I64, P]
+    lib.nvfp4_kv_evict_workspace.restype = I32
+    lib.nvfp4_kv_evict_workspace.argtypes = [I32, I32, I64, I64, P]
     lib.nvfp4_kv_attention_workspace.restype = I32
     lib.nvfp4_kv_attention_workspace.argtypes = [I32, I64, I32, I32, I32, I32, I64, I64, P]
     return lib
@@ -441,6 +451,44 @@ def nvfp4_kv_tree_attention(q, cache, page_table, kv_len, k_gscale, v_gscale, pa
     nvfp4_kv_attention."""
     _kv_call("kv_tree_attention", stream, cache, k_gscale, v_gscale, page_size, q, page_table, kv_len, o, max_kv_len,
              workspace, cu_q, max_q_len, scale, window, lse, tree_mask)
+
+
+def nvfp4_kv_accept(cache, page_table, kv_len, cu_q, accepted, n_accepted, n_kv_heads, page_size, kv_len_out,
+                    stream=None) -> None:
+    """The accepted path of a drafted tree: of sequence b's query tokens (rows cu_q[b] ..
+    cu_q[b + 1], the last of its kv_len[b] tokens; cu_q None: one each) the n_accepted[b]
+    whose numbers accepted[b] holds (int32 [batch, most], any order) move to the front of
+    the query tokens' places; kv_len_out (may be kv_len) gets the new lengths."""
+    _kv_call("kv_accept", stream, cache, page_table, kv_len, cu_q, accepted, n_accepted, n_kv_heads, page_size,
+             kv_len_out)
+
+
+def nvfp4_kv_attention_weights(q, cache, page_table, kv_len, k_gscale, page_size, lse, key_weights, max_kv_len, cu_q=None,
+                               max_q_len=1, scale=None, window=0, decay=1.0, stream=None) -> None:
+    """Add to key_weights (fp32 [n_pages, n_kv_heads, page_size]) the attention weight that each
+    cached token receives from the query tokens of an nvfp4_kv_attention call, whose lse
+    [T, n_q_heads] goes in; earlier weights are multiplied by decay (0: not read), those of
+    the call's own tokens begin at 0."""
+    _kv_call("kv_attention_weights", stream, cache, page_size, q, page_table, kv_len, k_gscale, lse, key_weights, max_kv_len,
+             cu_q, max_q_len, scale, window, decay)
+
+
+def nvfp4_kv_evict_workspace(batch: int, n_kv_heads: int, budget: int, max_kv_len: int) -> int:
+    """Workspace bytes of an nvfp4_kv_evict call."""
+    n = ctypes.c_int64(0)
+    _check(lib.nvfp4_kv_evict_workspace(batch, n_kv_heads, budget, max_kv_len, ctypes.byref(n)))
+    return n.value
+
+
+def nvfp4_kv_evict(cache, key_weights, page_table, kv_len, page_size, budget, kv_len_out, max_kv_len, workspace,
+                   keep_first=0, keep_last=0, weights_out=None, kept=None, stream=None) -> None:
+    """Cut sequences to `budget` tokens: each kv head keeps the first keep_first, the last
+    keep_last and of the others those of the largest key_weights (fp32 [n_pages, n_kv_heads,
+    page_size]), its rows moved in place; weights_out (may be key_weights; None: not
+    wanted) gets the kept tokens' weights, kept (int32 [batch, n_kv_heads, budget]) their earlier
+    places, kv_len_out (may be kv_len) the new lengths."""
+    _kv_call("kv_evict", stream, cache, page_size, key_weights, page_table, kv_len, budget, kv_len_out, max_kv_len,
+             workspace, keep_first, keep_last, weights_out, kept)
 
 
 def nvfp4_bench_mfma_peak(iters: int, n_blocks: int, out, stream=None) -> None:

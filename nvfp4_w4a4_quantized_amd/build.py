@@ -26,7 +26,7 @@ BINDING = os.path.join(HERE, "_torch_binding.so")
 OBJDIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["abi.cpp", "quant.hip", "gemm.hip", "gemv.hip", "skinny.hip", "requant.hip", "mx.hip", "noalloc.hip", "gdn.hip", "probe.hip", "soloq.hip", "kvcache.hip",
-           "kvattn.hip", "kvprefill.hip"]
+           "kvattn.hip", "kvprefill.hip", "kvweights.hip", "kvevict.hip"]
 
 COMPILE_FLAGS = [
     "--offload-arch=gfx950",

@@ -298,6 +298,48 @@ int32_t check_kv_attn_sizes(int64_t T, int32_t batch, int32_t n_q_heads, int32_t
   return check_kv_rows(T, n_q_heads);
 }
 
+int32_t check_kv_table(int64_t max_pages, int64_t ld_table, int32_t page_size) {
+  if (max_pages <= 0 || max_pages > (1ll << 30) / page_size)
+    return fail(NVFP4_ERR_INVALID_ARG, "max_pages=%lld of %d tokens: 1 to 2^30 tokens are supported",
+                (long long)max_pages, page_size);
+  if (ld_table < max_pages)
+    return fail(NVFP4_ERR_INVALID_ARG, "ld_table=%lld < max_pages=%lld", (long long)ld_table, (long long)max_pages);
+  return NVFP4_OK;
+}
+
+// Whether two buffers share a byte
+bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
+}
+
+// The lengths may be written where they are read, or apart from there
+int32_t check_kv_len_out(const int32_t* kv_len, const int32_t* kv_len_out, int32_t batch) {
+  if (!kv_len || !kv_len_out) return fail(NVFP4_ERR_INVALID_ARG, "kv_len/kv_len_out is NULL");
+  if (kv_len != kv_len_out && overlap(kv_len, 4ll * batch, kv_len_out, 4ll * batch))
+    return fail(NVFP4_ERR_INVALID_ARG, "kv_len_out overlaps kv_len without being it");
+  return NVFP4_OK;
+}
+
+int32_t check_kv_pairs(int32_t batch, int32_t n_kv_heads) {
+  if (batch <= 0) return fail(NVFP4_ERR_INVALID_ARG, "batch=%d must be positive", batch);
+  if ((int64_t)batch * n_kv_heads > nvfp4::kv_most_blocks(nvfp4::kKvMoveThreads))
+    return fail(NVFP4_ERR_UNSUPPORTED, "batch * n_kv_heads = %lld exceeds %lld", (long long)batch * n_kv_heads,
+                (long long)nvfp4::kv_most_blocks(nvfp4::kKvMoveThreads));
+  return NVFP4_OK;
+}
+
+int32_t check_kv_budget(int64_t budget, int64_t keep_first, int64_t keep_last, int64_t max_kv_len) {
+  if (budget < 1 || budget > (1ll << 30))
+    return fail(NVFP4_ERR_INVALID_ARG, "budget=%lld outside [1, 2^30]", (long long)budget);
+  if (keep_first < 0 || keep_last < 0 || keep_first > budget || keep_last > budget - keep_first)
+    return fail(NVFP4_ERR_INVALID_ARG, "keep_first=%lld and keep_last=%lld must fit into budget=%lld",
+                (long long)keep_first, (long long)keep_last, (long long)budget);
+  if (max_kv_len < 0 || max_kv_len > 0x7FFFFFFFll)
+    return fail(NVFP4_ERR_INVALID_ARG, "max_kv_len=%lld must be in [0, 2^31)", (long long)max_kv_len);
+  return NVFP4_OK;
+}
+
 // A drafted tree's bits: rows of `words` words, `ld` apart
 struct TreeMask {
   const uint64_t* mask;
@@ -322,11 +364,8 @@ int32_t kv_attention_call(const void* q, int32_t dtype, int64_t ldq, int64_t T, 
     return fail(NVFP4_ERR_INVALID_ARG, "without cu_q every sequence has one token: T=%lld must equal batch=%d",
                 (long long)T, batch);
   if (!kv_len || !page_table) return fail(NVFP4_ERR_INVALID_ARG, "kv_len/page_table is NULL");
-  if (max_pages <= 0 || max_pages > (1ll << 30) / page_size)
-    return fail(NVFP4_ERR_INVALID_ARG, "max_pages=%lld of %d tokens: 1 to 2^30 tokens are supported",
-                (long long)max_pages, page_size);
-  if (ld_table < max_pages)
-    return fail(NVFP4_ERR_INVALID_ARG, "ld_table=%lld < max_pages=%lld", (long long)ld_table, (long long)max_pages);
+  st = check_kv_table(max_pages, ld_table, page_size);
+  if (st) return st;
   if (!std::isfinite(scale)) return fail(NVFP4_ERR_INVALID_ARG, "scale is not finite");
   if (window < 0) return fail(NVFP4_ERR_INVALID_ARG, "window=%d must not be negative (0 = none)", window);
   if (tree) {
@@ -790,6 +829,146 @@ int32_t nvfp4_kv_tree_attention(const void* q, int32_t dtype, int64_t ldq, int64
   return kv_attention_call(q, dtype, ldq, T, n_q_heads, n_kv_heads, head_dim, batch, cu_q, max_q_len, kv_len, max_kv_len,
                            page_table, max_pages, ld_table, cache, n_pages, page_size, k_gscale, v_gscale, scale, window,
                            &tree, o, ldo, lse, workspace, workspace_bytes, stream);
+}
+
+int32_t nvfp4_kv_accept(uint8_t* cache, int64_t n_pages, int32_t page_size, int32_t n_kv_heads, int32_t head_dim,
+                        int32_t batch, const int32_t* kv_len, const int32_t* cu_q, const int32_t* page_table,
+                        int64_t max_pages, int64_t ld_table, const int32_t* accepted, int64_t max_accepted,
+                        int64_t ld_accepted, const int32_t* n_accepted, int32_t* kv_len_out, void* stream) {
+  nvfp4::KvAcceptArgs a{};
+  int32_t st = check_kv_shape(n_kv_heads, page_size, head_dim, n_pages, &a.pages.geom);
+  if (!st) st = check_kv_pairs(batch, n_kv_heads);
+  if (st) return st;
+  if (!cache || !page_table) return fail(NVFP4_ERR_INVALID_ARG, "cache/page_table is NULL");
+  if (!aligned16(cache)) return fail(NVFP4_ERR_UNSUPPORTED, "cache must be 16-byte aligned");
+  st = check_kv_table(max_pages, ld_table, page_size);
+  if (!st) st = check_kv_len_out(kv_len, kv_len_out, batch);
+  if (st) return st;
+  if (!accepted || !n_accepted) return fail(NVFP4_ERR_INVALID_ARG, "accepted/n_accepted is NULL");
+  if (max_accepted < 1) return fail(NVFP4_ERR_INVALID_ARG, "max_accepted=%lld must be positive", (long long)max_accepted);
+  if (max_accepted > nvfp4::kKvMostAccepted)
+    return fail(NVFP4_ERR_UNSUPPORTED, "max_accepted=%lld exceeds %d", (long long)max_accepted, nvfp4::kKvMostAccepted);
+  if (ld_accepted < max_accepted)
+    return fail(NVFP4_ERR_INVALID_ARG, "ld_accepted=%lld < max_accepted=%lld", (long long)ld_accepted,
+                (long long)max_accepted);
+  st = check_device();
+  if (st) return st;
+  a.cache = cache;
+  a.pages.table = page_table;
+  a.pages.max_pages = max_pages;
+  a.pages.ld_table = ld_table;
+  a.pages.batch = batch;
+  a.kv_len = kv_len;
+  a.cu_q = cu_q;
+  a.accepted = accepted;
+  a.ld_accepted = ld_accepted;
+  a.max_accepted = (int32_t)max_accepted;
+  a.n_accepted = n_accepted;
+  a.kv_len_out = kv_len_out;
+  return hip_status(nvfp4::launch_kv_accept(a, head_dim, static_cast<hipStream_t>(stream)), "nvfp4_kv_accept launch");
+}
+
+int32_t nvfp4_kv_attention_weights(const void* q, int32_t dtype, int64_t ldq, int64_t T, int32_t n_q_heads,
+                                   int32_t n_kv_heads, int32_t head_dim, int32_t batch, const int32_t* cu_q,
+                                   int64_t max_q_len, const int32_t* kv_len, int64_t max_kv_len,
+                                   const int32_t* page_table, int64_t max_pages, int64_t ld_table, const uint8_t* cache,
+                                   int64_t n_pages, int32_t page_size, const float* k_gscale, float scale, int32_t window,
+                                   const float* lse, float* key_weights, float decay, void* stream) {
+  nvfp4::KvWeightsArgs w{};
+  nvfp4::KvAttnArgs& a = w.a;
+  int32_t st = check_kv_attn_sizes(T, batch, n_q_heads, n_kv_heads, head_dim, max_q_len, max_kv_len);
+  if (!st) st = check_kv_shape(n_kv_heads, page_size, head_dim, n_pages, &a.geom);
+  if (!st) st = check_x(q, dtype, T, (int64_t)n_q_heads * head_dim, ldq, "q");
+  if (!st) st = check_kv_cache(cache, k_gscale, k_gscale);
+  if (st) return st;
+  if (!cu_q && T != batch)
+    return fail(NVFP4_ERR_INVALID_ARG, "without cu_q every sequence has one token: T=%lld must equal batch=%d",
+                (long long)T, batch);
+  if (!kv_len || !page_table) return fail(NVFP4_ERR_INVALID_ARG, "kv_len/page_table is NULL");
+  if (!lse || !key_weights) return fail(NVFP4_ERR_INVALID_ARG, "lse/key_weights is NULL");
+  if (!aligned16(key_weights)) return fail(NVFP4_ERR_UNSUPPORTED, "key_weights must be 16-byte aligned");
+  st = check_kv_table(max_pages, ld_table, page_size);
+  if (st) return st;
+  if (!std::isfinite(scale)) return fail(NVFP4_ERR_INVALID_ARG, "scale is not finite");
+  if (!std::isfinite(decay)) return fail(NVFP4_ERR_INVALID_ARG, "decay is not finite");
+  if (window < 0) return fail(NVFP4_ERR_INVALID_ARG, "window=%d must not be negative (0 = none)", window);
+  st = check_device();
+  if (st) return st;
+  a.q = q;
+  a.ldq = ldq;
+  a.T = T;
+  a.n_q_heads = n_q_heads;
+  a.batch = batch;
+  a.cu_q = cu_q;
+  a.kv_len = kv_len;
+  a.table = page_table;
+  a.max_pages = max_pages;
+  a.ld_table = ld_table;
+  a.cache = cache;
+  a.k_gscale = k_gscale;
+  a.scale = scale;
+  a.window = window < (1 << 30) ? window : (1 << 30);   // no sequence is longer
+  w.lse = lse;
+  w.weights = key_weights;
+  w.decay = decay;
+  return hip_status(nvfp4::launch_kv_weights(w, in_type(dtype), head_dim, max_kv_len, static_cast<hipStream_t>(stream)),
+                    "nvfp4_kv_attention_weights launch");
+}
+
+int32_t nvfp4_kv_evict_workspace(int32_t batch, int32_t n_kv_heads, int64_t budget, int64_t max_kv_len,
+                                 int64_t* bytes_out) {
+  if (!bytes_out) return fail(NVFP4_ERR_INVALID_ARG, "bytes_out is NULL");
+  if (n_kv_heads <= 0) return fail(NVFP4_ERR_INVALID_ARG, "n_kv_heads=%d must be positive", n_kv_heads);
+  int32_t st = check_kv_pairs(batch, n_kv_heads);
+  if (!st) st = check_kv_budget(budget, 0, 0, max_kv_len);
+  if (st) return st;
+  *bytes_out = nvfp4::kv_evict_workspace(batch, n_kv_heads, budget);
+  return ok();
+}
+
+int32_t nvfp4_kv_evict(uint8_t* cache, int64_t n_pages, int32_t page_size, int32_t n_kv_heads, int32_t head_dim,
+                       const float* key_weights, float* weights_out, int32_t batch, const int32_t* kv_len,
+                       int64_t max_kv_len, const int32_t* page_table, int64_t max_pages, int64_t ld_table, int64_t budget,
+                       int64_t keep_first, int64_t keep_last, int32_t* kept, int32_t* kv_len_out, void* workspace,
+                       int64_t workspace_bytes, void* stream) {
+  nvfp4::KvEvictArgs a{};
+  int32_t st = check_kv_shape(n_kv_heads, page_size, head_dim, n_pages, &a.pages.geom);
+  if (!st) st = check_kv_pairs(batch, n_kv_heads);
+  if (st) return st;
+  if (!cache || !key_weights || !page_table)
+    return fail(NVFP4_ERR_INVALID_ARG, "cache/key_weights/page_table is NULL");
+  if (!aligned16(cache) || !aligned16(key_weights) || !aligned16(weights_out))
+    return fail(NVFP4_ERR_UNSUPPORTED, "cache, key_weights and weights_out must be 16-byte aligned");
+  const int64_t weights = n_pages * n_kv_heads * page_size * 4;
+  if (weights_out && weights_out != key_weights && overlap(weights_out, weights, key_weights, weights))
+    return fail(NVFP4_ERR_INVALID_ARG, "weights_out overlaps key_weights without being it");
+  st = check_kv_table(max_pages, ld_table, page_size);
+  if (!st) st = check_kv_len_out(kv_len, kv_len_out, batch);
+  if (!st) st = check_kv_budget(budget, keep_first, keep_last, max_kv_len);
+  if (st) return st;
+  const int64_t need = nvfp4::kv_evict_workspace(batch, n_kv_heads, budget);
+  if (!workspace || workspace_bytes < need)
+    return fail(NVFP4_ERR_INVALID_ARG, "workspace of %lld bytes is too small: %lld needed",
+                (long long)(workspace ? workspace_bytes : 0), (long long)need);
+  if (!aligned16(workspace)) return fail(NVFP4_ERR_UNSUPPORTED, "workspace must be 16-byte aligned");
+  st = check_device();
+  if (st) return st;
+  a.cache = cache;
+  a.pages.table = page_table;
+  a.pages.max_pages = max_pages;
+  a.pages.ld_table = ld_table;
+  a.pages.batch = batch;
+  a.kv_len = kv_len;
+  a.weights = key_weights;
+  a.weights_out = weights_out;
+  a.budget = (int32_t)budget;
+  a.first = (int32_t)keep_first;
+  a.last = (int32_t)keep_last;
+  a.kept = kept;
+  a.kv_len_out = kv_len_out;
+  a.lists = static_cast<int32_t*>(workspace);
+  return hip_status(nvfp4::launch_kv_evict(a, head_dim, max_kv_len, static_cast<hipStream_t>(stream)),
+                    "nvfp4_kv_evict launch");
 }
 
 int32_t nvfp4_mxfp4_quantize(const void* x, int32_t x_dtype, int64_t M, int64_t K, int64_t ldx, uint8_t* codes,

@@ -42,6 +42,49 @@ struct KvGatherArgs {
 };
 hipError_t launch_kv_gather(const KvGatherArgs& a, InType t, int32_t D, hipStream_t s);
 
+// kvevict.hip: rows that move within a sequence's pages.
+struct KvPages {
+  const int32_t* table;
+  int64_t max_pages, ld_table; // table row: max_pages entries, ld_table apart
+  KvGeom geom;
+  int32_t batch;
+};
+constexpr int kKvMoveThreads = 1024;
+constexpr int kKvMostAccepted = 256;
+struct KvAcceptArgs {
+  uint8_t* cache;
+  KvPages pages;
+  const int32_t* kv_len;
+  const int32_t* cu_q;         // NULL: one query token per sequence
+  const int32_t* accepted;     // [batch][ld_accepted]
+  int64_t ld_accepted;
+  int32_t max_accepted;
+  const int32_t* n_accepted;
+  int32_t* kv_len_out;
+};
+hipError_t launch_kv_accept(const KvAcceptArgs& a, int32_t D, hipStream_t s);
+
+constexpr int kKvEvictMostKeys = 36864;            // that LDS holds beside the histogram
+struct KvEvictArgs {
+  uint8_t* cache;
+  KvPages pages;
+  const int32_t* kv_len;
+  const float* weights;        // [n_pages][n_kv_heads][page_size]
+  float* weights_out;          // optional; may be weights
+  int32_t budget, first, last;
+  int32_t* kept;               // optional [batch][n_kv_heads][budget]
+  int32_t* kv_len_out;
+  int32_t* lists;              // [batch][n_kv_heads][2][budget] (workspace)
+  // the plan
+  int32_t lds_keys;            // keys that the launch's LDS holds
+  int32_t lengths;             // whether the kernel writes the lengths
+};
+// bytes of its workspace: what moves and where to
+inline int64_t kv_evict_workspace(int32_t batch, int32_t n_kv_heads, int64_t budget) {
+  return (int64_t)batch * n_kv_heads * budget * 2 * (int64_t)sizeof(int32_t);
+}
+hipError_t launch_kv_evict(KvEvictArgs a, int32_t D, int64_t max_kv_len, hipStream_t s);
+
 // kvattn.hip: attention over the cache.
 struct KvAttnArgs {
   const void* q;
@@ -84,6 +127,18 @@ struct KvAttnPlan {
 KvAttnPlan kv_attn_plan(InType t, int64_t T, int32_t batch, int32_t n_q_heads, int32_t n_kv_heads, int32_t D,
                         int64_t max_q_len, int64_t max_kv_len, int64_t window);
 hipError_t launch_kv_attn(KvAttnArgs a, const KvAttnPlan& p, InType t, int32_t D, hipStream_t s);
+
+// kvweights.hip: the attention weight of cached tokens
+struct KvWeightsArgs {
+  KvAttnArgs a;                // its queries, pages and scale; o, lse, plan unused
+  const float* lse;            // [T][n_q_heads]
+  float* weights;              // [n_pages][n_kv_heads][page_size]
+  float decay;
+  // the plan
+  int32_t tiles;               // workgroups per sequence and kv head
+  FastDiv by_tiles;
+};
+hipError_t launch_kv_weights(KvWeightsArgs w, InType t, int32_t D, int64_t max_kv_len, hipStream_t s);
 
 // joins the pieces that either kernel left
 hipError_t launch_kv_join(const KvAttnArgs& a, InType t, int32_t D, hipStream_t s);

@@ -281,11 +281,119 @@ int attention(Args& a) {
   }
 }
 
+// A cache of `heads` kv heads whose scales the call does not take
+Cache plain_cache(const at::Tensor* t, int32_t page_size, int64_t heads) {
+  if (t->scalar_type() != at::kByte || t->dim() != 2 || !t->is_contiguous())
+    refuse(NVFP4_ERR_INVALID_ARG, "cache must be contiguous uint8 [n_pages, page bytes]");
+  const int64_t bytes = t->size(1), per = 9 * heads * page_size;
+  const int64_t d = heads > 0 && heads <= 65536 && page_size > 0 ? bytes * 8 / per : 0;
+  if (d <= 0 || d > 65536 || per * d != bytes * 8)
+    refuse(NVFP4_ERR_INVALID_ARG, "cache pages of %lld bytes do not hold %d tokens of %lld heads", (long long)bytes,
+           page_size, (long long)heads);
+  return {static_cast<uint8_t*>(t->data_ptr()), t->size(0), page_size, (int32_t)heads, (int32_t)d, nullptr, nullptr};
+}
+
+Rows table_of(const at::Tensor* t) {
+  if (t->scalar_type() != at::kInt) refuse(NVFP4_ERR_UNSUPPORTED, "page_table must be int32");
+  const Rows tab = rows_of(t, "page_table");
+  if (tab.rows > INT32_MAX - 1) refuse(NVFP4_ERR_INVALID_ARG, "too many sequences");
+  return tab;
+}
+
+// Weights of the slots of c's pages
+float* slot_weights(const at::Tensor* t, const Cache& c, const char* name) {
+  if (!t) return nullptr;
+  if (t->scalar_type() != at::kFloat || t->dim() != 3 || t->size(0) != c.pages || t->size(1) != c.heads ||
+      t->size(2) != c.page_size || !t->is_contiguous())
+    refuse(NVFP4_ERR_INVALID_ARG, "%s must be contiguous float32 [%lld, %d, %d]", name, (long long)c.pages, c.heads,
+           c.page_size);
+  return static_cast<float*>(t->data_ptr());
+}
+
+// device, stream, cache, page_table, kv_len, cu_q, accepted, n_accepted, n_kv_heads, page_size, kv_len_out
+int kv_accept(Args& a) {
+  const at::Tensor *tc = a.tensor("cache"), *table = a.tensor("page_table"), *kv_len = a.tensor("kv_len"),
+                   *cu = a.tensor("cu_q", true), *acc = a.tensor("accepted"), *n_acc = a.tensor("n_accepted");
+  const int32_t heads = a.small("n_kv_heads"), page = a.small("page_size");
+  const at::Tensor* out = a.tensor("kv_len_out");
+  const Cache c = plain_cache(tc, page, heads);
+  const Rows tab = table_of(table);
+  if (acc->scalar_type() != at::kInt) refuse(NVFP4_ERR_UNSUPPORTED, "accepted must be int32");
+  const Rows paths = rows_of(acc, "accepted");
+  if (paths.rows != tab.rows) refuse(NVFP4_ERR_INVALID_ARG, "accepted must be [%lld, most]", (long long)tab.rows);
+  return nvfp4_kv_accept(c.p, c.pages, c.page_size, c.heads, c.d, (int32_t)tab.rows,
+                         indices<int32_t>(kv_len, at::kInt, "int32", tab.rows, "kv_len"),
+                         indices<int32_t>(cu, at::kInt, "int32", tab.rows + 1, "cu_q"),
+                         static_cast<const int32_t*>(tab.p), tab.cols, tab.ld, static_cast<const int32_t*>(paths.p),
+                         paths.cols, paths.ld, indices<int32_t>(n_acc, at::kInt, "int32", tab.rows, "n_accepted"),
+                         indices<int32_t>(out, at::kInt, "int32", tab.rows, "kv_len_out"), a.stream());
+}
+
+// device, stream, cache, page_size, q, page_table, kv_len, k_gscale, lse, key_weights, max_kv_len, cu_q, max_q_len,
+// scale (None: 1/sqrt(d)), window, decay
+int kv_attention_weights(Args& a) {
+  const at::Tensor* tc = a.tensor("cache");
+  const int32_t page = a.small("page_size");
+  const at::Tensor *tq = a.tensor("q"), *table = a.tensor("page_table"), *kv_len = a.tensor("kv_len"),
+                   *kg = a.tensor("k_gscale"), *lse = a.tensor("lse"), *weights = a.tensor("key_weights");
+  const int64_t max_kv_len = a.number("max_kv_len");
+  const at::Tensor* cu = a.tensor("cu_q", true);
+  const int64_t max_q_len = a.number("max_q_len");
+  const Cache c = plain_cache(tc, page, kg->dim() == 1 ? kg->size(0) : -1);
+  const double scale = a.real("scale", 1.0 / std::sqrt((double)c.d));
+  const int32_t window = a.small("window");
+  const double decay = a.real("decay", 1.0);
+  const Rows q = rows_of(tq, "q"), tab = table_of(table);
+  if (q.cols % c.d || q.cols / c.d > INT32_MAX) refuse(NVFP4_ERR_INVALID_ARG, "q must be [T, n_q_heads * %d]", c.d);
+  const int64_t heads = q.cols / c.d;
+  if (lse->scalar_type() != at::kFloat || lse->dim() != 2 || lse->size(0) != q.rows || lse->size(1) != heads ||
+      !lse->is_contiguous())
+    refuse(NVFP4_ERR_INVALID_ARG, "lse must be contiguous float32 [%lld, %lld]", (long long)q.rows, (long long)heads);
+  return nvfp4_kv_attention_weights(
+      q.p, dtype_of(tq, "q"), q.ld, q.rows, (int32_t)heads, c.heads, c.d, (int32_t)tab.rows,
+      indices<int32_t>(cu, at::kInt, "int32", tab.rows + 1, "cu_q"), max_q_len,
+      indices<int32_t>(kv_len, at::kInt, "int32", tab.rows, "kv_len"), max_kv_len, static_cast<const int32_t*>(tab.p),
+      tab.cols, tab.ld, c.p, c.pages, c.page_size, indices<float>(kg, at::kFloat, "float32", c.heads, "k_gscale"),
+      (float)scale, window, static_cast<const float*>(lse->data_ptr()), slot_weights(weights, c, "key_weights"),
+      (float)decay, a.stream());
+}
+
+// device, stream, cache, page_size, key_weights, page_table, kv_len, budget, kv_len_out, max_kv_len, workspace,
+// keep_first, keep_last, weights_out, kept
+int kv_evict(Args& a) {
+  const at::Tensor* tc = a.tensor("cache");
+  const int32_t page = a.small("page_size");
+  const at::Tensor *weights = a.tensor("key_weights"), *table = a.tensor("page_table"), *kv_len = a.tensor("kv_len");
+  const int64_t budget = a.number("budget");
+  const at::Tensor* out = a.tensor("kv_len_out");
+  const int64_t max_kv_len = a.number("max_kv_len");
+  const at::Tensor* ws = a.tensor("workspace");
+  const int64_t first = a.number("keep_first"), last = a.number("keep_last");
+  const at::Tensor *w_out = a.tensor("weights_out", true), *kept = a.tensor("kept", true);
+  const Cache c = plain_cache(tc, page, weights->dim() == 3 ? weights->size(1) : -1);
+  const Rows tab = table_of(table);
+  if (kept && (kept->scalar_type() != at::kInt || kept->dim() != 3 || kept->size(0) != tab.rows ||
+               kept->size(1) != c.heads || kept->size(2) != budget || !kept->is_contiguous()))
+    refuse(NVFP4_ERR_INVALID_ARG, "kept must be contiguous int32 [%lld, %d, %lld]", (long long)tab.rows, c.heads,
+           (long long)budget);
+  if (!ws->is_contiguous()) refuse(NVFP4_ERR_INVALID_ARG, "workspace must be contiguous");
+  return nvfp4_kv_evict(c.p, c.pages, c.page_size, c.heads, c.d, slot_weights(weights, c, "key_weights"),
+                        slot_weights(w_out, c, "weights_out"), (int32_t)tab.rows,
+                        indices<int32_t>(kv_len, at::kInt, "int32", tab.rows, "kv_len"), max_kv_len,
+                        static_cast<const int32_t*>(tab.p), tab.cols, tab.ld, budget, first, last,
+                        kept ? static_cast<int32_t*>(kept->data_ptr()) : nullptr,
+                        indices<int32_t>(out, at::kInt, "int32", tab.rows, "kv_len_out"), ws->data_ptr(),
+                        (int64_t)(ws->numel() * ws->element_size()), a.stream());
+}
+
 PyMethodDef methods[] = {
     {"rope_append_kv", reinterpret_cast<PyCFunction>(entry<rope_append_kv, 15>), METH_FASTCALL, nullptr},
     {"kv_gather", reinterpret_cast<PyCFunction>(entry<kv_gather, 9>), METH_FASTCALL, nullptr},
     {"kv_attention", reinterpret_cast<PyCFunction>(entry<attention<false>, 17>), METH_FASTCALL, nullptr},
     {"kv_tree_attention", reinterpret_cast<PyCFunction>(entry<attention<true>, 18>), METH_FASTCALL, nullptr},
+    {"kv_accept", reinterpret_cast<PyCFunction>(entry<kv_accept, 11>), METH_FASTCALL, nullptr},
+    {"kv_attention_weights", reinterpret_cast<PyCFunction>(entry<kv_attention_weights, 16>), METH_FASTCALL, nullptr},
+    {"kv_evict", reinterpret_cast<PyCFunction>(entry<kv_evict, 15>), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_torch_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -145,3 +145,47 @@ def attention_bounds(q, k, v, weights, scale, out_dtype):
     most = np.abs(vr).max(0)[None] if n else 0.0
     o = (2 * ds[..., None] + f16 + 2 * (n + 16) * u) * mean * 1.01 + n * 2.0 ** -32 * most
     return o, ds + (n + 16) * u
+
+
+def attention_weights(q, k, lse, scale, window=0, dtype="bf16"):
+    """The attention weight [n, Hkv] that each of the n tokens of k receives from the query
+    tokens q [m, Hq, D], the last m of them, under the log-sums lse [m, Hq] (-inf: a row
+    without weights); and the bound on a kernel's error.
+
+    An exponent scale <q, k> - lse: the fp32 sum of D products (gamma_D of the sum of
+    magnitudes), the fp32 score factor (4 u of the score), lse times log2 e (2 u of lse), the
+    subtraction, exp2 (together 16 u and 2 u of either), fp32 queries as two f16 terms (2^-21).
+    A weight inherits it relatively; the fp32 sum of N weights adds gamma_N, and weights
+    below fp32's normal range may be lost (2^-126 each)."""
+    u = 2.0 ** -24
+    m, Hq, D = q.shape
+    n, Hkv, _ = k.shape
+    group = Hq // Hkv
+    q = np.asarray(q, dtype=np.float64)
+    total, bound = np.zeros((n, Hkv)), np.zeros((n, Hkv))
+    for i in range(m):
+        p = n - m + i
+        lo = max(0, p - window + 1) if window else 0
+        for h in range(Hq if p >= lo else 0):
+            if np.isneginf(lse[i, h]):
+                continue
+            x = k[lo:p + 1, h // group]
+            w = np.exp(scale * (x @ q[i, h]) - lse[i, h])
+            mag = abs(scale) * (np.abs(x) @ np.abs(q[i, h]))
+            total[lo:p + 1, h // group] += w
+            bound[lo:p + 1, h // group] += w * (((D + 16) * u + (2.0 ** -21 if dtype == "f32" else 0)) * mag
+                                                + 4 * u * abs(lse[i, h]) + 16 * u)
+    terms = m * group
+    return total, 1.01 * bound + terms * u / (1 - terms * u) * total + terms * 2.0 ** -126
+
+
+def evicted(weights, n, budget, first, last):
+    """The tokens that a head of n tokens with these weights keeps, by their new places."""
+    if n <= budget:
+        return list(range(n))
+    w = [float("-inf") if np.isnan(x) else float(x) for x in weights]
+    heavy = sorted(range(first, n - last), key=lambda t: (-w[t], t))[:budget - first - last]
+    behind = iter(sorted(t for t in heavy if t >= budget - last))
+    stays = set(heavy)
+    return list(range(first)) + [t if t in stays else next(behind) for t in range(first, budget - last)] \
+        + list(range(n - last, n))
