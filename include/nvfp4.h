@@ -506,6 +506,7 @@ NVFP4_API int32_t nvfp4_kv_accept(uint8_t* cache, int64_t n_pages, int32_t page_
  *         kv head's group of e^{scale <q_ih, k_t> - lse_ih}
  * in fp32 (the tokens that are new in this call begin at 0; a decay of 0 reads no earlier
  * weights).  A sequence without query tokens keeps its weights.
+ *   q            as for nvfp4_kv_attention, ldq at most 2^23 (NVFP4_ERR_UNSUPPORTED otherwise)
  *   lse          device fp32 [T][n_q_heads]; -inf: the row has no weights
  *   key_weights  device fp32 [n_pages][n_kv_heads][page_size], 16-byte aligned: a weight for each slot
  *                and kv head.  The pages of a call's sequences must be each sequence's alone.

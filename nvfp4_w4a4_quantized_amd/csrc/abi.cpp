@@ -885,6 +885,8 @@ int32_t nvfp4_kv_attention_weights(const void* q, int32_t dtype, int64_t ldq, in
     return fail(NVFP4_ERR_INVALID_ARG, "without cu_q every sequence has one token: T=%lld must equal batch=%d",
                 (long long)T, batch);
   if (!kv_len || !page_table) return fail(NVFP4_ERR_INVALID_ARG, "kv_len/page_table is NULL");
+  if (ldq > nvfp4::kKvWeightsMostLd)
+    return fail(NVFP4_ERR_UNSUPPORTED, "ldq=%lld exceeds 2^23", (long long)ldq);
   if (!lse || !key_weights) return fail(NVFP4_ERR_INVALID_ARG, "lse/key_weights is NULL");
   if (!aligned16(key_weights)) return fail(NVFP4_ERR_UNSUPPORTED, "key_weights must be 16-byte aligned");
   st = check_kv_table(max_pages, ld_table, page_size);
@@ -911,7 +913,8 @@ int32_t nvfp4_kv_attention_weights(const void* q, int32_t dtype, int64_t ldq, in
   w.lse = lse;
   w.weights = key_weights;
   w.decay = decay;
-  return hip_status(nvfp4::launch_kv_weights(w, in_type(dtype), head_dim, max_kv_len, static_cast<hipStream_t>(stream)),
+  return hip_status(nvfp4::launch_kv_weights(w, in_type(dtype), head_dim, max_q_len, max_kv_len,
+                                             static_cast<hipStream_t>(stream)),
                     "nvfp4_kv_attention_weights launch");
 }
 

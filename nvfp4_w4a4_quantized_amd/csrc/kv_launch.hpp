@@ -136,9 +136,12 @@ struct KvWeightsArgs {
   float decay;
   // the plan
   int32_t tiles;               // workgroups per sequence and kv head
+  int32_t steps;               // few query columns: 64 tokens each, of a wave's run
+  int32_t split;               // many: log2 of the waves that share tokens; few: -1
   FastDiv by_tiles;
 };
-hipError_t launch_kv_weights(KvWeightsArgs w, InType t, int32_t D, int64_t max_kv_len, hipStream_t s);
+constexpr int64_t kKvWeightsMostLd = 1 << 23;      // elements between query rows: a tile's offsets have 32 bits
+hipError_t launch_kv_weights(KvWeightsArgs w, InType t, int32_t D, int64_t max_q_len, int64_t max_kv_len, hipStream_t s);
 
 // joins the pieces that either kernel left
 hipError_t launch_kv_join(const KvAttnArgs& a, InType t, int32_t D, hipStream_t s);

@@ -2,10 +2,10 @@
 // group, from the queries' log-sums:
 //   W_t <- decay W_t [t < n - m] + sum_{i, h} e^{scale <q_ih, k_t> - lse_ih}  over the i that attend to t
 //
-// S = q K^T on the f16 MFMA 16x16x32: the rows are query columns (query token x head), the columns
-// tokens, so that a lane has four query columns of one token and sums in place; over all query
-// columns the sum stays in one register a token, in an order that does not depend on the grid.
-// Numerics of the product as in kvattn.hip; exponents, weights and sums are fp32.
+// Both kernels take query columns (query token x head) as the rows of a matrix product and tokens as
+// its columns, so that a lane has scores of one token and sums its weights in place; a token's
+// sum is in one wave's registers, or eight waves' that are joined in a fixed order: a call gives
+// the same bits every time.  Exponents, weights and sums are fp32.
 #include "kv_device.hpp"
 
 namespace nvfp4 {
@@ -65,6 +65,10 @@ __device__ __forceinline__ QueryRange queries_of(const SeqInfo& s, int32_t t0, i
   return r;
 }
 
+// Few query columns: one token a sequence as a rule.  Bound by the keys' bytes, so a wave goes through
+// a run of tokens, 64 at a time, with the next 64 tokens' codes in flight; S on the f16 MFMA
+// 16x16x32 with the numerics of kvattn.hip, 16 query columns at a time (more of them, which the
+// bounds did not announce, are prepared again for every step).
 template <int D, bool F32>
 __global__ __launch_bounds__(64 * kWeightWaves) void k_kv_weights(KvWeightsArgs w) {
   constexpr int KC = D / 32, TERMS = F32 ? 2 : 1, NG = kWaveTokens / 16;
@@ -78,124 +82,489 @@ __global__ __launch_bounds__(64 * kWeightWaves) void k_kv_weights(KvWeightsArgs 
   const int b = item / a.by_heads, kh = item - b * hkv;
   const SeqInfo seq = seq_info(a, b);
   if (seq.m == 0) return;
-  const int32_t c0 = seq.n - seq.m;
+  const int32_t c0 = seq.n - seq.m, cols = seq.m * group;
   const float kg = a.k_gscale[kh];
+  const int32_t run = w.steps * kWaveTokens;
 
-  // tokens past the planned ones go with the first tiles
-  for (int64_t tile = (int)blockIdx.x - item * w.tiles; tile * (kWeightWaves * kWaveTokens) < seq.n; tile += w.tiles) {
-    const int32_t t0 = (int32_t)tile * (kWeightWaves * kWaveTokens) + wave * kWaveTokens;
-    if (t0 >= seq.n) break;
-    const QueryRange q = queries_of(seq, t0, kWaveTokens, a.window);
-    const bool any = q.first < q.end;
-    if (!any && w.decay == 1.0f) continue;
-
-    int64_t page[NG];
-    f16x8 kf[NG][KC];
+  // the block of columns in registers: A operand, row r; results' rows 4 g + i
+  f16x8 qf[TERMS][KC];
+  float csc[4], sub[4];
+  int32_t pos[4];
+  auto prepare = [&](int32_t col0) {
+    int32_t col = col0 + r;
+    const bool past = col >= cols;
+    col = past ? cols - 1 : col;
+    const int32_t qi = col / a.by_group, head = kh * group + (col - qi * group);
+    const int64_t off = (seq.q0 + qi) * a.ldq + (int64_t)head * D;
+    const float lse = w.lse[(seq.q0 + qi) * a.n_q_heads + head];
+    float v[KC][8];
+    float amax = 0.0f;
 #pragma unroll
-    for (int u = 0; u < NG; ++u) {
-      int32_t t = t0 + 16 * u;
-      t = t < seq.n ? t : seq.n - 1;                 // past the end: the last granule again
-      const int32_t id = __builtin_amdgcn_readfirstlane(a.table[(int64_t)b * a.ld_table + (t >> a.geom.page_shift)]);
-      page[u] = id;
-      const int32_t read = id < 0 ? 0 : (id >= a.geom.n_pages ? (int32_t)a.geom.n_pages - 1 : id);
-      if (any) {
-        Keys<D> x;
-        load_keys<D>(granule_buffer<D>(a, read, kh * per_head + ((t >> 4) & (per_head - 1))), lane, x);
+    for (int c = 0; c < KC; ++c) load8<F32>(a.q, off + (D == 64 ? 16 * g + 8 * c : 128 * (c / 4) + 32 * g + 8 * (c % 4)), v[c]);
 #pragma unroll
-        for (int c = 0; c < KC; ++c) kf[u][c] = key_frag<D>(x, c);
+    for (int c = 0; c < KC; ++c)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) amax = __builtin_fmaxf(amax, __builtin_fabsf(v[c][e]));
+    amax = max_xor32(max_xor16(amax));
+    const float up = a.scale < 0.0f ? -query_up(amax) : query_up(amax);
+    const float csc_r = score_factor(a.scale, kg, amax);
+    // a row that attends to nothing, or is not there, has no weights
+    const float sub_r = past || lse == -__builtin_inff() ? __builtin_inff() : lse * kLog2e;
+#pragma unroll
+    for (int c = 0; c < KC; ++c)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float x = v[c][e] * up;
+        const _Float16 hi = (_Float16)x;
+        qf[0][c][e] = hi;
+        if constexpr (F32) qf[TERMS - 1][c][e] = (_Float16)(x - (float)hi);
       }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      csc[i] = __shfl(csc_r, 4 * g + i);
+      sub[i] = __shfl(sub_r, 4 * g + i);
+      pos[i] = c0 + __shfl(qi, 4 * g + i);
     }
+  };
 
-    float sum[NG] = {};
-    for (int32_t col0 = q.first * group; any && col0 < q.end * group; col0 += 16) {
-      const int32_t cols = q.end * group;
-      // A operand: row r of the block of columns
-      int32_t col = col0 + r;
-      const bool past = col >= cols;
-      col = past ? cols - 1 : col;
-      const int32_t qi = col / a.by_group, head = kh * group + (col - qi * group);
-      const int64_t off = (seq.q0 + qi) * a.ldq + (int64_t)head * D;
-      float v[KC][8];
-      float amax = 0.0f;
-#pragma unroll
-      for (int c = 0; c < KC; ++c) {
-        load8<F32>(a.q, off + (D == 64 ? 16 * g + 8 * c : 128 * (c / 4) + 32 * g + 8 * (c % 4)), v[c]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) amax = __builtin_fmaxf(amax, __builtin_fabsf(v[c][e]));
-      }
-      amax = max_xor32(max_xor16(amax));
-      const float up = a.scale < 0.0f ? -query_up(amax) : query_up(amax);
-      const float csc_r = score_factor(a.scale, kg, amax);
-      const float lse = w.lse[(seq.q0 + qi) * a.n_q_heads + head];
-      // a row that attends to nothing, or is not there, has no weights
-      const float sub_r = past || lse == -__builtin_inff() ? __builtin_inff() : lse * kLog2e;
-      f16x8 qf[TERMS][KC];
-#pragma unroll
-      for (int c = 0; c < KC; ++c)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float x = v[c][e] * up;
-          const _Float16 hi = (_Float16)x;
-          qf[0][c][e] = hi;
-          if constexpr (F32) qf[TERMS - 1][c][e] = (_Float16)(x - (float)hi);
-        }
-      // the results' rows: 4 g + i
-      float csc[4], sub[4];
-      int32_t pos[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        csc[i] = __shfl(csc_r, 4 * g + i);
-        sub[i] = __shfl(sub_r, 4 * g + i);
-        pos[i] = c0 + __shfl(qi, 4 * g + i);
-      }
+  // runs past the planned ones go with the first ones' waves
+  for (int64_t at = (int64_t)((int)blockIdx.x - item * w.tiles) * kWeightWaves + wave; at * run < seq.n;
+       at += (int64_t)w.tiles * kWeightWaves) {
+    const int32_t begin = (int32_t)(at * run), end = begin + run < seq.n ? begin + run : seq.n;
+    const int32_t last_granule = (seq.n - 1) >> 4;
+    // page of token begin + 16 lane (a run is at most 1024 tokens)
+    int32_t t_page = begin + 16 * lane;
+    t_page = t_page < seq.n ? t_page : seq.n - 1;
+    const int32_t id = a.table[(int64_t)b * a.ld_table + (t_page >> a.geom.page_shift)];
+    const int32_t pages = id < 0 ? 0 : (id >= a.geom.n_pages ? (int32_t)a.geom.n_pages - 1 : id);
+    Keys<D> next[NG];
+    auto issue = [&](int32_t t0) {
 #pragma unroll
       for (int u = 0; u < NG; ++u) {
-        f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+        const int32_t page = __builtin_amdgcn_readlane(pages, (t0 - begin) / 16 + u);
+        int32_t gr = t0 / 16 + u;
+        gr = gr < last_granule ? gr : last_granule;       // past the end: the last granule again
+        load_keys<D>(granule_buffer<D>(a, page, kh * per_head + (gr & (per_head - 1))), lane, next[u]);
+      }
+    };
+    // the lane's own token of a step and its weight
+    float* own = nullptr;
+    float old = 0.0f;
+    float* own_next = nullptr;
+    float old_next = 0.0f;
+    auto issue_old = [&](int32_t t0) {
+      const int32_t t = t0 + lane;
+      const int32_t page = __shfl(id, (t0 - begin) / 16 + g);
+      own_next = nullptr;
+      if (t < seq.n && page >= 0 && page < a.geom.n_pages) {
+        own_next = w.weights + ((((int64_t)page * hkv + kh) << a.geom.page_shift) + (t & ((1 << a.geom.page_shift) - 1)));
+        if (t < c0 && w.decay != 0.0f) old_next = *own_next;
+      }
+    };
+    bool prepared = false;
+    // what of the run any query attends to; nothing needs reading elsewhere, but weights fade
+    const QueryRange all = queries_of(seq, begin, end - begin, a.window);
+    const bool any = all.first < all.end;
+    if (!any && w.decay == 1.0f) continue;
+    if (any) issue(begin);
+    issue_old(begin);
+    for (int32_t t0 = begin; t0 < end; t0 += kWaveTokens) {
+      Keys<D> cur[NG];
 #pragma unroll
-        for (int c = 0; c < KC; ++c)
+      for (int u = 0; u < NG; ++u) cur[u] = next[u];
+      own = own_next;
+      old = old_next;
+      if (!prepared && any && cols <= 16) prepare(0);
+      prepared = true;
+      if (t0 + kWaveTokens < end) {
+        if (any) issue(t0 + kWaveTokens);
+        issue_old(t0 + kWaveTokens);
+      }
+      const QueryRange q = queries_of(seq, t0, kWaveTokens, a.window);
+      float sum[NG] = {};
+      for (int32_t col0 = cols <= 16 ? 0 : q.first * group; q.first < q.end && col0 < q.end * group; col0 += 16) {
+        if (cols > 16) prepare(col0);
 #pragma unroll
-          for (int e = 0; e < TERMS; ++e) s = mfma16(qf[e][c], kf[u][c], s);
-        const int32_t t = t0 + 16 * u + r;
+        for (int u = 0; u < NG; ++u) {
+          f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const bool sees = t <= pos[i] && (!a.window || t > pos[i] - a.window);
-          const float x = sees ? __builtin_fmaf(s[i], csc[i], -sub[i]) : -__builtin_inff();
-          sum[u] += __builtin_amdgcn_exp2f(x);
+          for (int c = 0; c < KC; ++c) {
+            const f16x8 kf = key_frag<D>(cur[u], c);
+#pragma unroll
+            for (int e = 0; e < TERMS; ++e) s = mfma16(qf[e][c], kf, s);
+          }
+          const int32_t t = t0 + 16 * u + r;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bool sees = t <= pos[i] && (!a.window || t > pos[i] - a.window);
+            const float x = sees ? __builtin_fmaf(s[i], csc[i], -sub[i]) : -__builtin_inff();
+            sum[u] += __builtin_amdgcn_exp2f(x);
+          }
         }
       }
-    }
 #pragma unroll
-    for (int u = 0; u < NG; ++u) {
-      const float total = sum_xor32(sum_xor16(sum[u]));
-      const int32_t t = t0 + 16 * u + r;
-      if (g == 0 && t < seq.n && page[u] >= 0 && page[u] < a.geom.n_pages) {
-        float* const at = w.weights + (((page[u] * hkv + kh) << a.geom.page_shift) + (t & ((1 << a.geom.page_shift) - 1)));
-        *at = t < c0 && w.decay != 0.0f ? __builtin_fmaf(w.decay, *at, total) : total;
-      }
+      for (int u = 0; u < NG; ++u) sum[u] = sum_xor32(sum_xor16(sum[u]));
+      // lane (g, r): token 16 g + r
+      const float total = g < 2 ? (g == 0 ? sum[0] : sum[1]) : (g == 2 ? sum[2] : sum[3]);
+      if (own && (q.first < q.end || w.decay != 1.0f))
+        *own = t0 + lane < c0 && w.decay != 0.0f ? __builtin_fmaf(w.decay, old, total) : total;
     }
   }
 }
 
-template <int D>
-hipError_t launch(const KvWeightsArgs& w, InType t, hipStream_t s) {
-  const dim3 blocks((unsigned)((int64_t)w.a.batch * w.a.geom.n_kv_heads * w.tiles)), threads(64 * kWeightWaves);
-  if (t == InType::F32) hipLaunchKernelGGL((k_kv_weights<D, true>), blocks, threads, 0, s, w);
-  else hipLaunchKernelGGL((k_kv_weights<D, false>), blocks, threads, 0, s, w);
+// Many query columns: the matrix product and the exponentials bound it.  A wave keeps TB blocks of 32
+// tokens decoded in registers, as B operands of the bf16 MFMA 32x32x16 (e2m1 * s has 6 significant
+// bits, and bf16 queries go in as they are), and takes tiles of 32 query columns past them; the
+// waves of a workgroup have different tokens, or every qs-th tile of the same ones, whose sums
+// are joined in LDS at the end.  Tiles go from memory to LDS by asynchronous loads, each wave's its own,
+// one ahead: no barrier in the loop.  fp32 queries go as three bf16 terms, which hold all their bits.
+//
+// A tile is whole query tokens, as many as 32 rows hold (heads 32 s .. of one token where the
+// group has more), so that its rows' places are the same in every tile.
+constexpr int kManyWaves = 8;
+constexpr int kTileRows = 32;
+constexpr int kRingBytes = 8192;                   // of each of the two places of a wave's ring
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+template <int D, bool F32>
+struct Many {
+  static constexpr int SIZE = F32 ? 4 : 2;
+  static constexpr int TB = D == 256 || (F32 && D == 128) ? 2 : 4;
+  static constexpr int KS = D / 16;                          // K steps: elements (D / 2) h + 8 k + j
+  static constexpr int CHUNK = F32 ? 64 : (D < 128 ? D : 128);   // elements of a row that are loaded at once
+  static constexpr int NCH = D / CHUNK;
+  static constexpr int KSC = CHUNK / 16;
+  static constexpr int UNITS = CHUNK * SIZE / 16;            // 16-byte units of a row
+  static constexpr int LOADS = kTileRows * UNITS / 64;
+  // a unit's place in its row: 16 lanes that read a unit of 16 rows meet every bank once
+  static __device__ __forceinline__ int swizzle(int row) { return UNITS == 16 ? row & 15 : (row >> 1) & 7; }
+};
+
+__device__ __forceinline__ f32x16 mfma32(bf16x8 a, bf16x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+__device__ __forceinline__ uint32_t high_halves(float lo, float hi) {
+  return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
+}
+
+// 8 codes under their block's scale: exact in bf16
+__device__ __forceinline__ bf16x8 decode8_bf16(uint32_t codes, float s) {
+  u32x4 x;
+  const auto a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 0);
+  const auto b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 1);
+  const auto c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 2);
+  const auto d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 3);
+  x[0] = high_halves(a[0] * s, a[1] * s);
+  x[1] = high_halves(b[0] * s, b[1] * s);
+  x[2] = high_halves(c[0] * s, c[1] * s);
+  x[3] = high_halves(d[0] * s, d[1] * s);
+  return __builtin_bit_cast(bf16x8, x);
+}
+
+__device__ __forceinline__ void to_lds16(__amdgpu_buffer_rsrc_t r, uint8_t* lds, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, off, 0, 0, 0);
+}
+__device__ __forceinline__ void to_lds4(__amdgpu_buffer_rsrc_t r, uint8_t* lds, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 4, off, 0, 0, 0);
+}
+
+// `bytes` from p on as a buffer (what lies past them reads as 0)
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, int64_t bytes) {
+  const int32_t n = bytes < 0 ? 0 : (bytes > 0x7FFFFFFF ? 0x7FFFFFFF : (int32_t)bytes);
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(reinterpret_cast<const void*>(uniform64((int64_t)p))), (short)0,
+                                           __builtin_amdgcn_readfirstlane(n), 0x00020000);
+}
+
+template <int D, bool F32>
+__global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv_weights_many(KvWeightsArgs w) {
+  using M = Many<D, F32>;
+  constexpr int TB = M::TB, KS = M::KS;
+  extern __shared__ __attribute__((aligned(256))) uint8_t shared[];
+  const KvAttnArgs& a = w.a;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int h = lane >> 5, r = lane & 31;
+  uint8_t* const ring = shared + wave * 2 * kRingBytes;
+  float* const s_lse = reinterpret_cast<float*>(shared + kManyWaves * 2 * kRingBytes) + wave * 3 * kTileRows;
+  float* const s_sub = s_lse + 2 * kTileRows;
+  float* const s_sum = reinterpret_cast<float*>(shared + kManyWaves * (2 * kRingBytes + 3 * kTileRows * 4));
+
+  const int hkv = a.geom.n_kv_heads, group = (int)a.by_group.d;
+  const int per_head = 1 << (a.geom.page_shift - 4);
+  // the tiles that the most queries attend to first; workgroups side by side differ in the head
+  const int turn = (int)blockIdx.x / a.by_pairs, item = (int)blockIdx.x - turn * (int)a.by_pairs.d;
+  const int b = item / a.by_heads, kh = item - b * hkv;
+  const SeqInfo seq = seq_info(a, b);
+  if (seq.m == 0) return;
+  const int32_t c0 = seq.n - seq.m;
+  const float csc = (float)((double)a.scale * 1.4426950408889634 * (double)a.k_gscale[kh]);
+  const int qs = 1 << w.split, ql = wave & (qs - 1), tg = wave >> w.split;
+  const int32_t wg_tokens = (kManyWaves >> w.split) * TB * 32;
+
+  const int32_t per_tile = group <= kTileRows ? kTileRows / group : 1;          // query tokens of a tile
+  const int32_t slices = (group + kTileRows - 1) / kTileRows;                   // tiles of a query token
+  const int32_t rows = group <= kTileRows ? per_tile * group : kTileRows;
+
+  // this lane's bytes of a tile's rows
+  uint32_t off[M::LOADS];
+#pragma unroll
+  for (int i = 0; i < M::LOADS; ++i) {
+    const int place = i * (64 / M::UNITS) + lane / M::UNITS;
+    const int row = place < rows ? place : rows - 1;
+    const int unit = (lane % M::UNITS) ^ M::swizzle(place);
+    const int tok = group <= kTileRows ? row / a.by_group : 0, hd = row - tok * group;
+    off[i] = (uint32_t)(((int64_t)tok * a.ldq + hd * D + (unit / (M::UNITS / 2)) * (D / 2)) * M::SIZE +
+                        (unit % (M::UNITS / 2)) * 16);
+  }
+  const int lse_row = r < rows ? r : rows - 1, lse_tok = group <= kTileRows ? lse_row / a.by_group : 0;
+  const uint32_t off_lse = (uint32_t)(lse_tok * a.n_q_heads + lse_row - lse_tok * group) * 4;
+
+  for (int64_t tile = turn; tile * wg_tokens < seq.n; tile += w.tiles) {
+    const int32_t t0 = (int32_t)(tile * wg_tokens) + tg * TB * 32;
+    const QueryRange q = queries_of(seq, t0, TB * 32, a.window);
+    const bool live = t0 < seq.n && q.first < q.end;
+    float sum[TB] = {};
+    if (live) {
+      // keys
+      bf16x8 kf[TB][KS];
+#pragma unroll
+      for (int tb = 0; tb < TB; ++tb) {
+        int32_t t = t0 + 32 * tb + r;
+        t = t < seq.n ? t : seq.n - 1;
+        int32_t id = a.table[(int64_t)b * a.ld_table + (t >> a.geom.page_shift)];
+        id = id < 0 ? 0 : (id >= a.geom.n_pages ? (int32_t)a.geom.n_pages - 1 : id);
+        const uint8_t* p = a.cache + (int64_t)id * a.geom.page_bytes +
+                           (int64_t)(kh * per_head + ((t >> 4) & (per_head - 1))) * kv_granule_bytes(D);
+        const uint8_t* codes = p + (t & 15) * (D / 2) + h * (D / 4);
+        const uint8_t* scales = p + 8 * D + (t & 15) * (D / 16) + h * (D / 32);
+        uint32_t c[KS], sc[D == 256 ? 2 : 1];
+#pragma unroll
+        for (int i = 0; i < KS; i += 4) {
+          const u32x4 x = *reinterpret_cast<const u32x4*>(codes + 4 * i);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) c[i + e] = x[e];
+        }
+        if constexpr (D == 64) sc[0] = *reinterpret_cast<const uint16_t*>(scales);
+        else if constexpr (D == 128) sc[0] = *reinterpret_cast<const uint32_t*>(scales);
+        else {
+          sc[0] = *reinterpret_cast<const uint32_t*>(scales);
+          sc[1] = *reinterpret_cast<const uint32_t*>(scales + 4);
+        }
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+          float s;
+          const int blk = i / 2;
+          if (blk % 4 == 0) s = __builtin_amdgcn_cvt_f32_fp8(sc[blk / 4], 0);
+          else if (blk % 4 == 1) s = __builtin_amdgcn_cvt_f32_fp8(sc[blk / 4], 1);
+          else if (blk % 4 == 2) s = __builtin_amdgcn_cvt_f32_fp8(sc[blk / 4], 2);
+          else s = __builtin_amdgcn_cvt_f32_fp8(sc[blk / 4], 3);
+          kf[tb][i] = decode8_bf16(c[i], s);
+        }
+      }
+
+      // the query tokens' tiles from the last on, every qs-th of them
+      const int32_t first = q.first / per_tile, tiles = ((q.end - 1) / per_tile - first + 1) * slices;
+      const int64_t q_end = ((int64_t)(a.T - 1) * a.ldq + (int64_t)a.n_q_heads * D) * M::SIZE;
+      const int64_t lse_end = a.T * a.n_q_heads * 4;
+      auto issue = [&](int32_t x, int chunk, int place) {
+        const int32_t j = first + x / slices, slice = x - (x / slices) * slices;
+        const int64_t at = ((int64_t)(seq.q0 + j * per_tile) * a.ldq + (int64_t)(kh * group + slice * kTileRows) * D) * M::SIZE +
+                           chunk * (M::CHUNK / 2) * M::SIZE;
+        const auto buf = buffer_of(static_cast<const uint8_t*>(a.q) + at, q_end - at);
+#pragma unroll
+        for (int i = 0; i < M::LOADS; ++i) to_lds16(buf, ring + place * kRingBytes + i * 1024, off[i]);
+        if (chunk == 0) {
+          const int64_t l = ((int64_t)(seq.q0 + j * per_tile) * a.n_q_heads + kh * group + slice * kTileRows) * 4;
+          const auto lbuf = buffer_of(reinterpret_cast<const uint8_t*>(w.lse) + l, lse_end - l);
+          if (h == 0) to_lds4(lbuf, reinterpret_cast<uint8_t*>(s_lse + (x >> w.split & 1) * kTileRows), off_lse);
+        }
+      };
+      int32_t x = tiles - 1 - ql;
+      int place = 0;
+      if (x >= 0) issue(x, 0, 0);
+      for (; x >= 0; x -= qs) {
+        const int32_t j = first + x / slices, slice = x - (x / slices) * slices;
+        // rows from the tile's first query token on that are there
+        const int32_t tok0 = j * per_tile, tok1 = tok0 + per_tile < seq.m ? tok0 + per_tile : seq.m;
+        int32_t have = group <= kTileRows ? (tok1 - tok0) * group : group - slice * kTileRows;
+        have = have < kTileRows ? have : kTileRows;
+        // scores' rows: 8 (i / 4) + 4 h + i % 4
+        float sub[16];
+        // adds the weights of a block's scores
+        auto add = [&](const f32x16& score, int32_t tmin, float& to) {
+          if (have >= rows && tmin + 31 <= c0 + tok0 && (!a.window || tmin > c0 + tok1 - 1 - a.window)) {
+            float part[4] = {};
+#pragma unroll
+            for (int i = 0; i < 16; ++i) part[i % 4] += __builtin_amdgcn_exp2f(__builtin_fmaf(score[i], csc, -sub[i]));
+            to += (part[0] + part[1]) + (part[2] + part[3]);
+            return;
+          }
+          const int32_t t = tmin + r;
+#pragma unroll
+          for (int i4 = 0; i4 < 4; ++i4) {
+            if (8 * i4 >= have) continue;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int row = 8 * i4 + 4 * h + e;
+              const int32_t pos = c0 + tok0 + (group <= kTileRows ? row / a.by_group : 0);
+              const bool sees = row < have && t <= pos && (!a.window || t > pos - a.window);
+              const float y = __builtin_fmaf(score[4 * i4 + e], csc, -sub[4 * i4 + e]);
+              to += sees ? __builtin_amdgcn_exp2f(y) : 0.0f;
+            }
+          }
+        };
+        auto landed = [&](int32_t next_x, int next_chunk) {
+          wait_vmcnt<0>();                         // this chunk (and the log-sums) are there
+          asm volatile("" ::: "memory");           // and nothing is read before
+          if (next_x >= 0) issue(next_x, next_chunk, place ^ 1);
+        };
+        auto log_sums = [&] {
+          if (h == 0) {
+            const float lse = s_lse[(x >> w.split & 1) * kTileRows + r];
+            s_sub[r] = r >= rows || lse == -__builtin_inff() ? __builtin_inff() : lse * kLog2e;
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const f32x4 y = *reinterpret_cast<const f32x4*>(s_sub + 8 * i + 4 * h);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sub[4 * i + e] = y[e];
+          }
+        };
+        // K step `step` of blocks [tb0, tb0 + N)
+        auto products = [&]<int N>(f32x16 (&acc)[N], int tb0, int chunk, int k) {
+          const uint8_t* const row = ring + place * kRingBytes + r * (M::UNITS * 16);
+          const int step = chunk * M::KSC + k;
+          if constexpr (!F32) {
+            const int unit = h * (M::UNITS / 2) + k;
+            const bf16x8 qf = *reinterpret_cast<const bf16x8*>(row + ((unit ^ M::swizzle(r)) * 16));
+#pragma unroll
+            for (int i = 0; i < N; ++i) acc[i] = mfma32(qf, kf[tb0 + i][step], step == 0 ? f32x16{} : acc[i]);
+          } else {
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int unit = h * (M::UNITS / 2) + 2 * k + e;
+              const f32x4 y = *reinterpret_cast<const f32x4*>(row + ((unit ^ M::swizzle(r)) * 16));
+#pragma unroll
+              for (int z = 0; z < 4; ++z) v[4 * e + z] = y[z];
+            }
+            // each term the upper 16 bits of what is left: three hold every bit
+            u32x4 term[3];
+#pragma unroll
+            for (int t = 0; t < 3; ++t)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                term[t][e] = high_halves(v[2 * e], v[2 * e + 1]);
+                v[2 * e] -= __uint_as_float(__float_as_uint(v[2 * e]) & 0xFFFF0000u);
+                v[2 * e + 1] -= __uint_as_float(__float_as_uint(v[2 * e + 1]) & 0xFFFF0000u);
+              }
+#pragma unroll
+            for (int t = 2; t >= 0; --t)
+#pragma unroll
+              for (int i = 0; i < N; ++i)
+                acc[i] = mfma32(__builtin_bit_cast(bf16x8, term[t]), kf[tb0 + i][step], step == 0 && t == 2 ? f32x16{} : acc[i]);
+          }
+        };
+        if constexpr (M::NCH == 1 && TB == 4) {
+          landed(x - qs, 0);
+          log_sums();
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            f32x16 acc[2];
+#pragma unroll
+            for (int k = 0; k < KS; ++k) products(acc, 2 * half, 0, k);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) add(acc[i], t0 + 32 * (2 * half + i), sum[2 * half + i]);
+          }
+          place ^= 1;
+        } else {
+          f32x16 acc[TB];
+#pragma unroll
+          for (int chunk = 0; chunk < M::NCH; ++chunk) {
+            if (chunk + 1 < M::NCH) landed(x, chunk + 1);
+            else landed(x - qs, 0);
+            if (chunk == 0) log_sums();
+#pragma unroll
+            for (int k = 0; k < M::KSC; ++k) products(acc, 0, chunk, k);
+            place ^= 1;
+          }
+#pragma unroll
+          for (int i = 0; i < TB; ++i) add(acc[i], t0 + 32 * i, sum[i]);
+        }
+      }
+    }
+    // the waves' sums: lane (0, r) token r of each block
+    __syncthreads();                               // s_sum of the tile before is read
+#pragma unroll
+    for (int tb = 0; tb < TB; ++tb) {
+      const float y = sum_xor32(sum[tb]);
+      if (h == 0) s_sum[wave * TB * 32 + 32 * tb + r] = y;
+    }
+    __syncthreads();
+    for (int32_t i = threadIdx.x; i < wg_tokens; i += 64 * kManyWaves) {
+      const int32_t t = (int32_t)(tile * wg_tokens) + i;
+      if (t >= seq.n) break;
+      const int32_t of = i / (TB * 32), lane_at = i % (TB * 32);
+      const QueryRange mine = queries_of(seq, (int32_t)(tile * wg_tokens) + of * TB * 32, TB * 32, a.window);
+      if (mine.first >= mine.end && w.decay == 1.0f) continue;
+      const int32_t id = a.table[(int64_t)b * a.ld_table + (t >> a.geom.page_shift)];
+      if (id < 0 || id >= a.geom.n_pages) continue;
+      float total = 0.0f;
+      for (int s = 0; s < qs; ++s) total += s_sum[((of << w.split) + s) * TB * 32 + lane_at];
+      float* const out = w.weights + ((((int64_t)id * hkv + kh) << a.geom.page_shift) + (t & ((1 << a.geom.page_shift) - 1)));
+      *out = t < c0 && w.decay != 0.0f ? __builtin_fmaf(w.decay, *out, total) : total;
+    }
+  }
+}
+
+constexpr int kManyLds = kManyWaves * (2 * kRingBytes + 3 * kTileRows * 4) + kManyWaves * 4 * 32 * 4;
+
+template <int D, bool F32>
+hipError_t launch(const KvWeightsArgs& w, int64_t blocks, hipStream_t s) {
+  if (w.split < 0) {
+    hipLaunchKernelGGL((k_kv_weights<D, F32>), dim3((unsigned)blocks), dim3(64 * kWeightWaves), 0, s, w);
+    return hipGetLastError();
+  }
+  const hipError_t e = lds_limit_once<k_kv_weights_many<D, F32>>(kManyLds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((k_kv_weights_many<D, F32>), dim3((unsigned)blocks), dim3(64 * kManyWaves), kManyLds, s, w);
   return hipGetLastError();
+}
+
+template <int D, bool F32>
+hipError_t plan(KvWeightsArgs w, int64_t max_q_len, int64_t max_kv_len, hipStream_t s) {
+  const int64_t pairs = (int64_t)w.a.batch * w.a.geom.n_kv_heads, group = w.a.by_group.d;
+  const int64_t m = max_q_len < w.a.T ? max_q_len : w.a.T;
+  const int64_t n = max_kv_len < 1 ? 1 : max_kv_len;
+  if (m * group <= 16) {
+    // runs so long that all waves are there at once, five a SIMD
+    const int64_t steps = pairs * ((n + kWaveTokens - 1) / kWaveTokens), each = steps / 5120;
+    w.split = -1;
+    w.steps = (int32_t)(each < 1 ? 1 : (each > 16 ? 16 : each));
+    const int64_t tokens = (int64_t)w.steps * kWaveTokens * kWeightWaves;
+    w.tiles = kv_planned_tiles((n + tokens - 1) / tokens, pairs, 64 * kWeightWaves);
+  } else {
+    const int64_t tiles = group <= kTileRows ? (m + kTileRows / group - 1) / (kTileRows / group) : m * ((group + kTileRows - 1) / kTileRows);
+    w.split = tiles >= 32 ? 3 : (tiles >= 16 ? 2 : (tiles >= 8 ? 1 : 0));
+    const int64_t tokens = (kManyWaves >> w.split) * Many<D, F32>::TB * 32;
+    w.tiles = kv_planned_tiles((n + tokens - 1) / tokens, pairs, 64 * kManyWaves);
+  }
+  w.by_tiles = fast_div((uint32_t)w.tiles);
+  return launch<D, F32>(w, pairs * w.tiles, s);
 }
 
 }  // namespace
 
-hipError_t launch_kv_weights(KvWeightsArgs w, InType t, int32_t D, int64_t max_kv_len, hipStream_t s) {
-  const int64_t tokens = kWeightWaves * kWaveTokens, pairs = (int64_t)w.a.batch * w.a.geom.n_kv_heads;
-  const int64_t tiles = max_kv_len < 1 ? 1 : (max_kv_len + tokens - 1) / tokens;
-  w.tiles = kv_planned_tiles(tiles, pairs, 64 * kWeightWaves);
-  w.by_tiles = fast_div((uint32_t)w.tiles);
+hipError_t launch_kv_weights(KvWeightsArgs w, InType t, int32_t D, int64_t max_q_len, int64_t max_kv_len, hipStream_t s) {
   w.a.by_group = fast_div((uint32_t)(w.a.n_q_heads / w.a.geom.n_kv_heads));
   w.a.by_heads = fast_div((uint32_t)w.a.geom.n_kv_heads);
-  if (D == 64) return launch<64>(w, t, s);
-  if (D == 128) return launch<128>(w, t, s);
-  return launch<256>(w, t, s);
+  w.a.by_pairs = fast_div((uint32_t)w.a.batch * (uint32_t)w.a.geom.n_kv_heads);
+  const bool f32 = t == InType::F32;
+  if (D == 64) return f32 ? plan<64, true>(w, max_q_len, max_kv_len, s) : plan<64, false>(w, max_q_len, max_kv_len, s);
+  if (D == 128) return f32 ? plan<128, true>(w, max_q_len, max_kv_len, s) : plan<128, false>(w, max_q_len, max_kv_len, s);
+  return f32 ? plan<256, true>(w, max_q_len, max_kv_len, s) : plan<256, false>(w, max_q_len, max_kv_len, s);
 }
 
 }  // namespace nvfp4
