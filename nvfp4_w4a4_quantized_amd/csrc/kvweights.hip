@@ -277,7 +277,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, int64
                                            __builtin_amdgcn_readfirstlane(n), 0x00020000);
 }
 
-template <int D, bool F32>
+// SLICED: more heads in a group than a tile has rows
+template <int D, bool F32, bool SLICED>
 __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv_weights_many(KvWeightsArgs w) {
   using M = Many<D, F32>;
   constexpr int TB = M::TB, KS = M::KS;
@@ -290,6 +291,7 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv_weights_many(KvWeight
   float* const s_lse = reinterpret_cast<float*>(shared + kManyWaves * 2 * kRingBytes) + wave * 3 * kTileRows;
   float* const s_sub = s_lse + 2 * kTileRows;
   float* const s_sum = reinterpret_cast<float*>(shared + kManyWaves * (2 * kRingBytes + 3 * kTileRows * 4));
+  uint32_t* const s_off = reinterpret_cast<uint32_t*>(s_sum + kManyWaves * 4 * 32);
 
   const int hkv = a.geom.n_kv_heads, group = (int)a.by_group.d;
   const int per_head = 1 << (a.geom.page_shift - 4);
@@ -303,30 +305,28 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv_weights_many(KvWeight
   const int qs = 1 << w.split, ql = wave & (qs - 1), tg = wave >> w.split;
   const int32_t wg_tokens = (kManyWaves >> w.split) * TB * 32;
 
-  const int32_t per_tile = group <= kTileRows ? kTileRows / group : 1;          // query tokens of a tile
-  const int32_t slices = (group + kTileRows - 1) / kTileRows;                   // tiles of a query token
-  const int32_t rows = group <= kTileRows ? per_tile * group : kTileRows;
+  const int32_t per_tile = SLICED ? 1 : kTileRows / group;                      // query tokens of a tile
+  const int32_t slices = SLICED ? (group + kTileRows - 1) / kTileRows : 1;      // tiles of a query token
+  const int32_t rows = SLICED ? kTileRows : per_tile * group;
 
-  // this lane's bytes of a tile's rows
-  uint32_t off[M::LOADS];
-#pragma unroll
-  for (int i = 0; i < M::LOADS; ++i) {
-    const int place = i * (64 / M::UNITS) + lane / M::UNITS;
+  // a lane's bytes of a tile's rows, the same for every wave: load i of the tile
+  for (int i = wave; i <= M::LOADS; i += kManyWaves) {
+    const int place = i < M::LOADS ? i * (64 / M::UNITS) + lane / M::UNITS : r;
     const int row = place < rows ? place : rows - 1;
     const int unit = (lane % M::UNITS) ^ M::swizzle(place);
-    const int tok = group <= kTileRows ? row / a.by_group : 0, hd = row - tok * group;
-    off[i] = (uint32_t)(((int64_t)tok * a.ldq + hd * D + (unit / (M::UNITS / 2)) * (D / 2)) * M::SIZE +
-                        (unit % (M::UNITS / 2)) * 16);
+    const int tok = SLICED ? 0 : row / a.by_group, hd = row - tok * group;
+    s_off[i * 64 + lane] =
+        i < M::LOADS ? (uint32_t)(((int64_t)tok * a.ldq + hd * D + (unit / (M::UNITS / 2)) * (D / 2)) * M::SIZE +
+                                  (unit % (M::UNITS / 2)) * 16)
+                     : (uint32_t)(tok * a.n_q_heads + hd) * 4;                  // the log-sum of row r
   }
-  const int lse_row = r < rows ? r : rows - 1, lse_tok = group <= kTileRows ? lse_row / a.by_group : 0;
-  const uint32_t off_lse = (uint32_t)(lse_tok * a.n_q_heads + lse_row - lse_tok * group) * 4;
+  __syncthreads();
 
   for (int64_t tile = turn; tile * wg_tokens < seq.n; tile += w.tiles) {
     const int32_t t0 = (int32_t)(tile * wg_tokens) + tg * TB * 32;
     const QueryRange q = queries_of(seq, t0, TB * 32, a.window);
-    const bool live = t0 < seq.n && q.first < q.end;
     float sum[TB] = {};
-    if (live) {
+    if (t0 < seq.n && q.first < q.end) {
       // keys
       bf16x8 kf[TB][KS];
 #pragma unroll
@@ -374,11 +374,11 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv_weights_many(KvWeight
                            chunk * (M::CHUNK / 2) * M::SIZE;
         const auto buf = buffer_of(static_cast<const uint8_t*>(a.q) + at, q_end - at);
 #pragma unroll
-        for (int i = 0; i < M::LOADS; ++i) to_lds16(buf, ring + place * kRingBytes + i * 1024, off[i]);
+        for (int i = 0; i < M::LOADS; ++i) to_lds16(buf, ring + place * kRingBytes + i * 1024, s_off[i * 64 + lane]);
         if (chunk == 0) {
           const int64_t l = ((int64_t)(seq.q0 + j * per_tile) * a.n_q_heads + kh * group + slice * kTileRows) * 4;
           const auto lbuf = buffer_of(reinterpret_cast<const uint8_t*>(w.lse) + l, lse_end - l);
-          if (h == 0) to_lds4(lbuf, reinterpret_cast<uint8_t*>(s_lse + (x >> w.split & 1) * kTileRows), off_lse);
+          if (h == 0) to_lds4(lbuf, reinterpret_cast<uint8_t*>(s_lse + (x >> w.split & 1) * kTileRows), s_off[M::LOADS * 64 + r]);
         }
       };
       int32_t x = tiles - 1 - ql;
@@ -388,27 +388,26 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv_weights_many(KvWeight
         const int32_t j = first + x / slices, slice = x - (x / slices) * slices;
         // rows from the tile's first query token on that are there
         const int32_t tok0 = j * per_tile, tok1 = tok0 + per_tile < seq.m ? tok0 + per_tile : seq.m;
-        int32_t have = group <= kTileRows ? (tok1 - tok0) * group : group - slice * kTileRows;
+        int32_t have = SLICED ? group - slice * kTileRows : (tok1 - tok0) * group;
         have = have < kTileRows ? have : kTileRows;
+        // every row is there and attends to every token
+        const bool full = have >= rows && t0 + TB * 32 - 1 <= c0 + tok0 && (!a.window || t0 > c0 + tok1 - 1 - a.window);
         // scores' rows: 8 (i / 4) + 4 h + i % 4
         float sub[16];
-        // adds the weights of a block's scores
-        auto add = [&](const f32x16& score, int32_t tmin, float& to) {
-          if (have >= rows && tmin + 31 <= c0 + tok0 && (!a.window || tmin > c0 + tok1 - 1 - a.window)) {
-            float part[4] = {};
-#pragma unroll
-            for (int i = 0; i < 16; ++i) part[i % 4] += __builtin_amdgcn_exp2f(__builtin_fmaf(score[i], csc, -sub[i]));
-            to += (part[0] + part[1]) + (part[2] + part[3]);
-            return;
-          }
+        auto weight = [&](const f32x16& score, float (&part)[4], int i) {
+          part[i % 4] += __builtin_amdgcn_exp2f(__builtin_fmaf(score[i], csc, -sub[i]));
+        };
+        auto add_some = [&](const f32x16& score, int32_t tmin, float& to) {
           const int32_t t = tmin + r;
+          int row0 = 4 * h;
+          asm volatile("" : "+v"(row0));           // rare: the rows' tokens are not kept through the loop
 #pragma unroll
           for (int i4 = 0; i4 < 4; ++i4) {
             if (8 * i4 >= have) continue;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int row = 8 * i4 + 4 * h + e;
-              const int32_t pos = c0 + tok0 + (group <= kTileRows ? row / a.by_group : 0);
+              const int row = row0 + 8 * i4 + e;
+              const int32_t pos = c0 + tok0 + (SLICED ? 0 : row / a.by_group);
               const bool sees = row < have && t <= pos && (!a.window || t > pos - a.window);
               const float y = __builtin_fmaf(score[4 * i4 + e], csc, -sub[4 * i4 + e]);
               to += sees ? __builtin_amdgcn_exp2f(y) : 0.0f;
@@ -432,51 +431,42 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv_weights_many(KvWeight
             for (int e = 0; e < 4; ++e) sub[4 * i + e] = y[e];
           }
         };
-        // K step `step` of blocks [tb0, tb0 + N)
-        auto products = [&]<int N>(f32x16 (&acc)[N], int tb0, int chunk, int k) {
-          const uint8_t* const row = ring + place * kRingBytes + r * (M::UNITS * 16);
-          const int step = chunk * M::KSC + k;
-          if constexpr (!F32) {
-            const int unit = h * (M::UNITS / 2) + k;
-            const bf16x8 qf = *reinterpret_cast<const bf16x8*>(row + ((unit ^ M::swizzle(r)) * 16));
-#pragma unroll
-            for (int i = 0; i < N; ++i) acc[i] = mfma32(qf, kf[tb0 + i][step], step == 0 ? f32x16{} : acc[i]);
-          } else {
-            float v[8];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int unit = h * (M::UNITS / 2) + 2 * k + e;
-              const f32x4 y = *reinterpret_cast<const f32x4*>(row + ((unit ^ M::swizzle(r)) * 16));
-#pragma unroll
-              for (int z = 0; z < 4; ++z) v[4 * e + z] = y[z];
-            }
-            // each term the upper 16 bits of what is left: three hold every bit
-            u32x4 term[3];
-#pragma unroll
-            for (int t = 0; t < 3; ++t)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                term[t][e] = high_halves(v[2 * e], v[2 * e + 1]);
-                v[2 * e] -= __uint_as_float(__float_as_uint(v[2 * e]) & 0xFFFF0000u);
-                v[2 * e + 1] -= __uint_as_float(__float_as_uint(v[2 * e + 1]) & 0xFFFF0000u);
-              }
-#pragma unroll
-            for (int t = 2; t >= 0; --t)
-#pragma unroll
-              for (int i = 0; i < N; ++i)
-                acc[i] = mfma32(__builtin_bit_cast(bf16x8, term[t]), kf[tb0 + i][step], step == 0 && t == 2 ? f32x16{} : acc[i]);
-          }
+        auto unit_at = [&](int unit) {
+          return ring + place * kRingBytes + r * (M::UNITS * 16) + ((unit ^ M::swizzle(r)) * 16);
         };
-        if constexpr (M::NCH == 1 && TB == 4) {
+        if constexpr (!F32 && M::NCH == 1) {
+          // scores of block i + 1 on the matrix unit beside the weights of block i
           landed(x - qs, 0);
+          bf16x8 qf[KS];
+#pragma unroll
+          for (int k = 0; k < KS; ++k) qf[k] = *reinterpret_cast<const bf16x8*>(unit_at(h * (M::UNITS / 2) + k));
           log_sums();
+          f32x16 acc[2];
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            f32x16 acc[2];
+          for (int k = 0; k < KS; ++k) acc[0] = mfma32(qf[k], kf[0][k], k == 0 ? f32x16{} : acc[0]);
+          if (full) {
 #pragma unroll
-            for (int k = 0; k < KS; ++k) products(acc, 2 * half, 0, k);
+            for (int tb = 0; tb < TB; ++tb) {
+              float part[4] = {};
 #pragma unroll
-            for (int i = 0; i < 2; ++i) add(acc[i], t0 + 32 * (2 * half + i), sum[2 * half + i]);
+              for (int k = 0; k < KS; ++k) {
+                __builtin_amdgcn_sched_barrier(0);
+                if (tb + 1 < TB) acc[(tb + 1) & 1] = mfma32(qf[k], kf[tb + 1 < TB ? tb + 1 : 0][k], k == 0 ? f32x16{} : acc[(tb + 1) & 1]);
+#pragma unroll
+                for (int i = 0; i < 16 / KS; ++i) weight(acc[tb & 1], part, k * (16 / KS) + i);
+              }
+              sum[tb] += (part[0] + part[1]) + (part[2] + part[3]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+          } else {
+#pragma unroll
+            for (int tb = 0; tb < TB; ++tb) {
+              if (tb) {
+#pragma unroll
+                for (int k = 0; k < KS; ++k) acc[0] = mfma32(qf[k], kf[tb][k], k == 0 ? f32x16{} : acc[0]);
+              }
+              add_some(acc[0], t0 + 32 * tb, sum[tb]);
+            }
           }
           place ^= 1;
         } else {
@@ -487,11 +477,51 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv_weights_many(KvWeight
             else landed(x - qs, 0);
             if (chunk == 0) log_sums();
 #pragma unroll
-            for (int k = 0; k < M::KSC; ++k) products(acc, 0, chunk, k);
+            for (int k = 0; k < M::KSC; ++k) {
+              const int step = chunk * M::KSC + k;
+              if constexpr (!F32) {
+                const bf16x8 qf = *reinterpret_cast<const bf16x8*>(unit_at(h * (M::UNITS / 2) + k));
+#pragma unroll
+                for (int i = 0; i < TB; ++i) acc[i] = mfma32(qf, kf[i][step], step == 0 ? f32x16{} : acc[i]);
+              } else {
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const f32x4 y = *reinterpret_cast<const f32x4*>(unit_at(h * (M::UNITS / 2) + 2 * k + e));
+#pragma unroll
+                  for (int z = 0; z < 4; ++z) v[4 * e + z] = y[z];
+                }
+                // each term the upper 16 bits of what is left: three hold every bit
+                u32x4 term[3];
+#pragma unroll
+                for (int t = 0; t < 3; ++t)
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    term[t][e] = high_halves(v[2 * e], v[2 * e + 1]);
+                    v[2 * e] -= __uint_as_float(__float_as_uint(v[2 * e]) & 0xFFFF0000u);
+                    v[2 * e + 1] -= __uint_as_float(__float_as_uint(v[2 * e + 1]) & 0xFFFF0000u);
+                  }
+#pragma unroll
+                for (int t = 2; t >= 0; --t)
+#pragma unroll
+                  for (int i = 0; i < TB; ++i)
+                    acc[i] = mfma32(__builtin_bit_cast(bf16x8, term[t]), kf[i][step], step == 0 && t == 2 ? f32x16{} : acc[i]);
+              }
+            }
             place ^= 1;
           }
+          if (full) {
 #pragma unroll
-          for (int i = 0; i < TB; ++i) add(acc[i], t0 + 32 * i, sum[i]);
+            for (int tb = 0; tb < TB; ++tb) {
+              float part[4] = {};
+#pragma unroll
+              for (int i = 0; i < 16; ++i) weight(acc[tb], part, i);
+              sum[tb] += (part[0] + part[1]) + (part[2] + part[3]);
+            }
+          } else {
+#pragma unroll
+            for (int tb = 0; tb < TB; ++tb) add_some(acc[tb], t0 + 32 * tb, sum[tb]);
+          }
         }
       }
     }
@@ -519,7 +549,15 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv_weights_many(KvWeight
   }
 }
 
-constexpr int kManyLds = kManyWaves * (2 * kRingBytes + 3 * kTileRows * 4) + kManyWaves * 4 * 32 * 4;
+constexpr int kManyLds = kManyWaves * (2 * kRingBytes + 3 * kTileRows * 4) + kManyWaves * 4 * 32 * 4 + 9 * 64 * 4;
+
+template <int D, bool F32, bool SLICED>
+hipError_t launch_many(const KvWeightsArgs& w, int64_t blocks, hipStream_t s) {
+  const hipError_t e = lds_limit_once<k_kv_weights_many<D, F32, SLICED>>(kManyLds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((k_kv_weights_many<D, F32, SLICED>), dim3((unsigned)blocks), dim3(64 * kManyWaves), kManyLds, s, w);
+  return hipGetLastError();
+}
 
 template <int D, bool F32>
 hipError_t launch(const KvWeightsArgs& w, int64_t blocks, hipStream_t s) {
@@ -527,10 +565,7 @@ hipError_t launch(const KvWeightsArgs& w, int64_t blocks, hipStream_t s) {
     hipLaunchKernelGGL((k_kv_weights<D, F32>), dim3((unsigned)blocks), dim3(64 * kWeightWaves), 0, s, w);
     return hipGetLastError();
   }
-  const hipError_t e = lds_limit_once<k_kv_weights_many<D, F32>>(kManyLds);
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((k_kv_weights_many<D, F32>), dim3((unsigned)blocks), dim3(64 * kManyWaves), kManyLds, s, w);
-  return hipGetLastError();
+  return w.a.by_group.d > kTileRows ? launch_many<D, F32, true>(w, blocks, s) : launch_many<D, F32, false>(w, blocks, s);
 }
 
 template <int D, bool F32>
