@@ -70,7 +70,7 @@ __device__ __forceinline__ QueryRange queries_of(const SeqInfo& s, int32_t t0, i
 // 16x16x32 with the numerics of kvattn.hip, 16 query columns at a time (more of them, which the
 // bounds did not announce, are prepared again for every step).
 template <int D, bool F32>
-__global__ __launch_bounds__(64 * kWeightWaves) void k_kv_weights(KvWeightsArgs w) {
+__global__ __launch_bounds__(64 * kWeightWaves, D == 256 ? (F32 ? 2 : 3) : 4) void k_kv_weights(KvWeightsArgs w) {
   constexpr int KC = D / 32, TERMS = F32 ? 2 : 1, NG = kWaveTokens / 16;
   const KvAttnArgs& a = w.a;
   const int lane = threadIdx.x & 63;
@@ -137,19 +137,14 @@ __global__ __launch_bounds__(64 * kWeightWaves) void k_kv_weights(KvWeightsArgs 
     t_page = t_page < seq.n ? t_page : seq.n - 1;
     const int32_t id = a.table[(int64_t)b * a.ld_table + (t_page >> a.geom.page_shift)];
     const int32_t pages = id < 0 ? 0 : (id >= a.geom.n_pages ? (int32_t)a.geom.n_pages - 1 : id);
-    Keys<D> next[NG];
-    auto issue = [&](int32_t t0) {
-#pragma unroll
-      for (int u = 0; u < NG; ++u) {
-        const int32_t page = __builtin_amdgcn_readlane(pages, (t0 - begin) / 16 + u);
-        int32_t gr = t0 / 16 + u;
-        gr = gr < last_granule ? gr : last_granule;       // past the end: the last granule again
-        load_keys<D>(granule_buffer<D>(a, page, kh * per_head + (gr & (per_head - 1))), lane, next[u]);
-      }
+    Keys<D> key[NG];
+    auto issue = [&](int32_t t0, int u) {
+      const int32_t page = __builtin_amdgcn_readlane(pages, (t0 - begin) / 16 + u);
+      int32_t gr = t0 / 16 + u;
+      gr = gr < last_granule ? gr : last_granule;         // past the end: the last granule again
+      load_keys<D>(granule_buffer<D>(a, page, kh * per_head + (gr & (per_head - 1))), lane, key[u]);
     };
-    // the lane's own token of a step and its weight
-    float* own = nullptr;
-    float old = 0.0f;
+    // the lane's own token of a step, 16 g + r, and its weight
     float* own_next = nullptr;
     float old_next = 0.0f;
     auto issue_old = [&](int32_t t0) {
@@ -161,51 +156,50 @@ __global__ __launch_bounds__(64 * kWeightWaves) void k_kv_weights(KvWeightsArgs 
         if (t < c0 && w.decay != 0.0f) old_next = *own_next;
       }
     };
-    bool prepared = false;
-    // what of the run any query attends to; nothing needs reading elsewhere, but weights fade
+    // where no query attends to anything of the run, nothing is read, but weights fade
     const QueryRange all = queries_of(seq, begin, end - begin, a.window);
     const bool any = all.first < all.end;
     if (!any && w.decay == 1.0f) continue;
-    if (any) issue(begin);
+    if (any) {
+#pragma unroll
+      for (int u = 0; u < NG; ++u) issue(begin, u);
+    }
     issue_old(begin);
+    if (any && cols <= 16) prepare(0);
     for (int32_t t0 = begin; t0 < end; t0 += kWaveTokens) {
-      Keys<D> cur[NG];
-#pragma unroll
-      for (int u = 0; u < NG; ++u) cur[u] = next[u];
-      own = own_next;
-      old = old_next;
-      if (!prepared && any && cols <= 16) prepare(0);
-      prepared = true;
-      if (t0 + kWaveTokens < end) {
-        if (any) issue(t0 + kWaveTokens);
-        issue_old(t0 + kWaveTokens);
-      }
       const QueryRange q = queries_of(seq, t0, kWaveTokens, a.window);
-      float sum[NG] = {};
-      for (int32_t col0 = cols <= 16 ? 0 : q.first * group; q.first < q.end && col0 < q.end * group; col0 += 16) {
-        if (cols > 16) prepare(col0);
+      float total = 0.0f;
 #pragma unroll
-        for (int u = 0; u < NG; ++u) {
-          f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+      for (int u = 0; u < NG; ++u) {
+        float sum = 0.0f;
+        if (q.first < q.end) {
+          f16x8 kf[KC];
 #pragma unroll
-          for (int c = 0; c < KC; ++c) {
-            const f16x8 kf = key_frag<D>(cur[u], c);
-#pragma unroll
-            for (int e = 0; e < TERMS; ++e) s = mfma16(qf[e][c], kf, s);
-          }
+          for (int c = 0; c < KC; ++c) kf[c] = key_frag<D>(key[u], c);
           const int32_t t = t0 + 16 * u + r;
+          for (int32_t col0 = cols <= 16 ? 0 : q.first * group; col0 < q.end * group; col0 += 16) {
+            if (cols > 16) prepare(col0);
+            f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const bool sees = t <= pos[i] && (!a.window || t > pos[i] - a.window);
-            const float x = sees ? __builtin_fmaf(s[i], csc[i], -sub[i]) : -__builtin_inff();
-            sum[u] += __builtin_amdgcn_exp2f(x);
+            for (int c = 0; c < KC; ++c)
+#pragma unroll
+              for (int e = 0; e < TERMS; ++e) s = mfma16(qf[e][c], kf[c], s);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const bool sees = t <= pos[i] && (!a.window || t > pos[i] - a.window);
+              const float x = sees ? __builtin_fmaf(s[i], csc[i], -sub[i]) : -__builtin_inff();
+              sum += __builtin_amdgcn_exp2f(x);
+            }
           }
+          sum = sum_xor32(sum_xor16(sum));
         }
+        // the next step's keys, into the registers that these leave
+        if (any && t0 + kWaveTokens < end) issue(t0 + kWaveTokens, u);
+        if (g == u) total = sum;
       }
-#pragma unroll
-      for (int u = 0; u < NG; ++u) sum[u] = sum_xor32(sum_xor16(sum[u]));
-      // lane (g, r): token 16 g + r
-      const float total = g < 2 ? (g == 0 ? sum[0] : sum[1]) : (g == 2 ? sum[2] : sum[3]);
+      float* const own = own_next;
+      const float old = old_next;
+      if (t0 + kWaveTokens < end) issue_old(t0 + kWaveTokens);
       if (own && (q.first < q.end || w.decay != 1.0f))
         *own = t0 + lane < c0 && w.decay != 0.0f ? __builtin_fmaf(w.decay, old, total) : total;
     }
@@ -574,15 +568,20 @@ hipError_t plan(KvWeightsArgs w, int64_t max_q_len, int64_t max_kv_len, hipStrea
   const int64_t m = max_q_len < w.a.T ? max_q_len : w.a.T;
   const int64_t n = max_kv_len < 1 ? 1 : max_kv_len;
   if (m * group <= 16) {
-    // runs so long that all waves are there at once, five a SIMD
-    const int64_t steps = pairs * ((n + kWaveTokens - 1) / kWaveTokens), each = steps / 5120;
+    // runs so long that about all waves are there at once, four a SIMD
+    const int64_t steps = pairs * ((n + kWaveTokens - 1) / kWaveTokens), each = steps / 8192;
     w.split = -1;
     w.steps = (int32_t)(each < 1 ? 1 : (each > 16 ? 16 : each));
     const int64_t tokens = (int64_t)w.steps * kWaveTokens * kWeightWaves;
     w.tiles = kv_planned_tiles((n + tokens - 1) / tokens, pairs, 64 * kWeightWaves);
   } else {
     const int64_t tiles = group <= kTileRows ? (m + kTileRows / group - 1) / (kTileRows / group) : m * ((group + kTileRows - 1) / kTileRows);
-    w.split = tiles >= 32 ? 3 : (tiles >= 16 ? 2 : (tiles >= 8 ? 1 : 0));
+    // More waves to the same tokens while workgroups are few (two a compute unit) and each wave has two
+    // tiles, or where the tiles are many: the keys are decoded by each of them.
+    w.split = 0;
+    while (w.split < 3 && tiles >= (4 << w.split) &&
+           (tiles >= 32 || pairs * ((n * 2 + kManyWaves * Many<D, F32>::TB * 32 - 1) / (kManyWaves * Many<D, F32>::TB * 32 >> w.split)) < 1024))
+      ++w.split;
     const int64_t tokens = (kManyWaves >> w.split) * Many<D, F32>::TB * 32;
     w.tiles = kv_planned_tiles((n + tokens - 1) / tokens, pairs, 64 * kManyWaves);
   }
