@@ -70,7 +70,7 @@ __device__ __forceinline__ QueryRange queries_of(const SeqInfo& s, int32_t t0, i
 // 16x16x32 with the numerics of kvattn.hip, 16 query columns at a time (more of them, which the
 // bounds did not announce, are prepared again for every step).
 template <int D, bool F32>
-__global__ __launch_bounds__(64 * kWeightWaves, D == 256 ? (F32 ? 2 : 3) : 4) void k_kv_weights(KvWeightsArgs w) {
+__global__ __launch_bounds__(64 * kWeightWaves, D == 256 ? 2 : 4) void k_kv_weights(KvWeightsArgs w) {
   constexpr int KC = D / 32, TERMS = F32 ? 2 : 1, NG = kWaveTokens / 16;
   const KvAttnArgs& a = w.a;
   const int lane = threadIdx.x & 63;
@@ -168,6 +168,8 @@ __global__ __launch_bounds__(64 * kWeightWaves, D == 256 ? (F32 ? 2 : 3) : 4) vo
     if (any && cols <= 16) prepare(0);
     for (int32_t t0 = begin; t0 < end; t0 += kWaveTokens) {
       const QueryRange q = queries_of(seq, t0, kWaveTokens, a.window);
+      // every query token attends to every token of the step
+      const bool full = t0 + kWaveTokens - 1 <= c0 && (!a.window || t0 > seq.n - 1 - a.window);
       float total = 0.0f;
 #pragma unroll
       for (int u = 0; u < NG; ++u) {
@@ -184,11 +186,16 @@ __global__ __launch_bounds__(64 * kWeightWaves, D == 256 ? (F32 ? 2 : 3) : 4) vo
             for (int c = 0; c < KC; ++c)
 #pragma unroll
               for (int e = 0; e < TERMS; ++e) s = mfma16(qf[e][c], kf[c], s);
+            if (full) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const bool sees = t <= pos[i] && (!a.window || t > pos[i] - a.window);
-              const float x = sees ? __builtin_fmaf(s[i], csc[i], -sub[i]) : -__builtin_inff();
-              sum += __builtin_amdgcn_exp2f(x);
+              for (int i = 0; i < 4; ++i) sum += __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], csc[i], -sub[i]));
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const bool sees = t <= pos[i] && (!a.window || t > pos[i] - a.window);
+                const float x = sees ? __builtin_fmaf(s[i], csc[i], -sub[i]) : -__builtin_inff();
+                sum += __builtin_amdgcn_exp2f(x);
+              }
             }
           }
           sum = sum_xor32(sum_xor16(sum));
@@ -569,7 +576,7 @@ hipError_t plan(KvWeightsArgs w, int64_t max_q_len, int64_t max_kv_len, hipStrea
   const int64_t n = max_kv_len < 1 ? 1 : max_kv_len;
   if (m * group <= 16) {
     // runs so long that about all waves are there at once, four a SIMD
-    const int64_t steps = pairs * ((n + kWaveTokens - 1) / kWaveTokens), each = steps / 8192;
+    const int64_t steps = pairs * ((n + kWaveTokens - 1) / kWaveTokens), each = steps / 4096;
     w.split = -1;
     w.steps = (int32_t)(each < 1 ? 1 : (each > 16 ? 16 : each));
     const int64_t tokens = (int64_t)w.steps * kWaveTokens * kWeightWaves;
