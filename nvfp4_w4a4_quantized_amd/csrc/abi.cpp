@@ -925,7 +925,7 @@ int32_t nvfp4_kv_evict_workspace(int32_t batch, int32_t n_kv_heads, int64_t budg
   int32_t st = check_kv_pairs(batch, n_kv_heads);
   if (!st) st = check_kv_budget(budget, 0, 0, max_kv_len);
   if (st) return st;
-  *bytes_out = nvfp4::kv_evict_workspace(batch, n_kv_heads, budget);
+  *bytes_out = nvfp4::kv_evict_plan(batch, n_kv_heads, budget, max_kv_len).workspace;
   return ok();
 }
 
@@ -949,7 +949,8 @@ int32_t nvfp4_kv_evict(uint8_t* cache, int64_t n_pages, int32_t page_size, int32
   if (!st) st = check_kv_len_out(kv_len, kv_len_out, batch);
   if (!st) st = check_kv_budget(budget, keep_first, keep_last, max_kv_len);
   if (st) return st;
-  const int64_t need = nvfp4::kv_evict_workspace(batch, n_kv_heads, budget);
+  const nvfp4::KvEvictPlan plan = nvfp4::kv_evict_plan(batch, n_kv_heads, budget, max_kv_len);
+  const int64_t need = plan.workspace;
   if (!workspace || workspace_bytes < need)
     return fail(NVFP4_ERR_INVALID_ARG, "workspace of %lld bytes is too small: %lld needed",
                 (long long)(workspace ? workspace_bytes : 0), (long long)need);
@@ -969,8 +970,7 @@ int32_t nvfp4_kv_evict(uint8_t* cache, int64_t n_pages, int32_t page_size, int32
   a.last = (int32_t)keep_last;
   a.kept = kept;
   a.kv_len_out = kv_len_out;
-  a.lists = static_cast<int32_t*>(workspace);
-  return hip_status(nvfp4::launch_kv_evict(a, head_dim, max_kv_len, static_cast<hipStream_t>(stream)),
+  return hip_status(nvfp4::launch_kv_evict(a, head_dim, plan, max_kv_len, workspace, static_cast<hipStream_t>(stream)),
                     "nvfp4_kv_evict launch");
 }
 

@@ -74,16 +74,25 @@ struct KvEvictArgs {
   int32_t budget, first, last;
   int32_t* kept;               // optional [batch][n_kv_heads][budget]
   int32_t* kv_len_out;
-  int32_t* lists;              // [batch][n_kv_heads][2][budget] (workspace)
+  int32_t* lists;              // [rows][2][budget]: what moves, and where to (workspace)
+  void* states;                // [2][rows] and, below, what the parts count (workspace)
+  void* counts;
   // the plan
+  int32_t rows;                // batch * n_kv_heads
   int32_t lds_keys;            // keys that the launch's LDS holds
-  int32_t lengths;             // whether the kernel writes the lengths
+  int32_t lengths;             // whether the kernels write the lengths
+  int32_t parts, move_parts;   // of a row, for the keys and for what moves; 0: a workgroup does a whole row
 };
-// bytes of its workspace: what moves and where to
-inline int64_t kv_evict_workspace(int32_t batch, int32_t n_kv_heads, int64_t budget) {
-  return (int64_t)batch * n_kv_heads * budget * 2 * (int64_t)sizeof(int32_t);
-}
-hipError_t launch_kv_evict(KvEvictArgs a, int32_t D, int64_t max_kv_len, hipStream_t s);
+constexpr int kKvEvictParts = 512;                 // of all rows
+constexpr int kKvEvictMostParts = 64;              // of a row
+constexpr int kKvEvictPartBytes = 24832;           // that a part counts
+struct KvEvictPlan {
+  int32_t parts;
+  int64_t states_at, counts_at;   // byte offsets in the workspace
+  int64_t workspace;              // bytes
+};
+KvEvictPlan kv_evict_plan(int32_t batch, int32_t n_kv_heads, int64_t budget, int64_t max_kv_len);
+hipError_t launch_kv_evict(KvEvictArgs a, int32_t D, const KvEvictPlan& p, int64_t max_kv_len, void* workspace, hipStream_t s);
 
 // kvattn.hip: attention over the cache.
 struct KvAttnArgs {

@@ -147,12 +147,14 @@ __global__ __launch_bounds__(kThreads) void k_kv_accept(KvAcceptArgs a) {
   }
 }
 
-// Eviction.  A workgroup per sequence and kv head:
-//   the weights of the tokens [first, n - last) as 32-bit keys of the same order (in LDS where they
-//   fit), the largest kept one by its digits (11, 11 and 10 bits, a histogram each), of the
-//   tokens that equal it the lowest ones;
+// Eviction of a row: one kv head of one sequence.
+//   the weights of the tokens [first, n - last) as 32-bit keys of the same order, the smallest
+//   kept key by its digits (11, 11 and 10 bits, a histogram each), of the tokens that equal it the
+//   lowest ones;
 //   kept tokens behind the places of the kept (movers) and free places, ascending, to two lists;
-//   mover i to free place i, then the last tokens down, 256 at a time.
+//   mover i to free place i, then the last tokens down.
+// A workgroup does a whole row, its keys in LDS; rows that are too long for that, or too few, are
+// cut into parts, and each pass over the keys is a launch.
 constexpr uint32_t kDigits[3] = {21, 10, 0};
 constexpr int kBins = 2048;
 
@@ -185,170 +187,412 @@ __device__ __forceinline__ int32_t sum_before(int32_t x, int32_t* s_waves, int32
   return before + upto - x;
 }
 
+// A row and what of it is kept
+struct Row {
+  Pages pages;
+  int32_t kh, n, budget, first, last;
+  bool over;
+  int32_t left, rated, keep, behind;   // new length; tokens that are rated, and kept of them; places below the last tokens'
+
+  __device__ __forceinline__ Row(const KvEvictArgs& a, int32_t row)
+      : pages(pages_of(a.pages, row / a.pages.geom.n_kv_heads)), kh(row % a.pages.geom.n_kv_heads),
+        n(length_of(a.pages, a.kv_len, row / a.pages.geom.n_kv_heads)), budget(a.budget), first(a.first), last(a.last),
+        over(n > budget), left(over ? budget : n), rated(n - first - last), keep(budget - first - last),
+        behind(budget - last) {}
+
+  __device__ __forceinline__ uint32_t key(const KvEvictArgs& a, int32_t i) const {
+    const int64_t page = pages.of(first + i);
+    return page < 0 ? weight_key(-__builtin_inff()) : weight_key(a.weights[pages.weight_at(page, kh, first + i)]);
+  }
+};
+
+// What does not move: `count` threads of a row share it
+__device__ __forceinline__ void keep_places(const KvEvictArgs& a, const Row& x, int32_t row, int32_t thread, int32_t count) {
+  if (a.kept)
+    for (int32_t j = thread; j < a.budget; j += count) a.kept[(int64_t)row * a.budget + j] = j < x.left ? j : -1;
+  if (a.weights_out && a.weights_out != a.weights)
+    for (int32_t j = thread; j < x.left; j += count) {
+      const int64_t page = x.pages.of(j);
+      if (page >= 0) {
+        const int64_t at = x.pages.weight_at(page, x.kh, j);
+        a.weights_out[at] = a.weights[at];
+      }
+    }
+  if (a.lengths && x.kh == 0 && thread == 0) a.kv_len_out[row / a.pages.geom.n_kv_heads] = x.left;
+}
+
+// The digit in which `wanted` keys, from the largest digit on, are reached; `mine`: this thread's
+// two bins, kBins - 1 - 2 tid and the one below.  Writes {digit, those wanted of its keys, its keys}.
+__device__ __forceinline__ void find_digit(int32_t x, int32_t y, int32_t wanted, int32_t* s_waves, int32_t* s_found) {
+  int32_t all;
+  const int32_t before = sum_before(x + y, s_waves, all);
+  if (before < wanted && wanted <= before + x + y) {
+    const bool upper = wanted <= before + x;
+    s_found[0] = kBins - 1 - 2 * (int)threadIdx.x - (upper ? 0 : 1);
+    s_found[1] = wanted - before - (upper ? 0 : x);
+    s_found[2] = upper ? x : y;
+  }
+  __syncthreads();
+}
+
+// Walks the rated tokens [r0, r1) of a wave in order, `ties` tokens of the border's key before them, and
+// calls f(token, whether it moves, its number among the movers, whether its place is free, its
+// number among those) for 64 at a time
+template <typename K, typename F>
+__device__ __forceinline__ void walk(const Row& x, int32_t r0, int32_t r1, uint32_t border, int32_t wanted, int32_t ties, K key_of,
+                                     int32_t& movers, int32_t& gaps, F f) {
+  const int lane = threadIdx.x & 63;
+  const uint64_t below = (1ull << lane) - 1;
+  for (int32_t i = r0; i < r1; i += 64) {
+    const bool have = i + lane < r1;
+    const uint32_t k = have ? key_of(i + lane) : 0;
+    const bool tie = have && x.keep > 0 && k == border;
+    const uint64_t tie_lanes = __builtin_amdgcn_ballot_w64(tie);
+    const bool stays = have && x.keep > 0 &&
+                       (k > border || (tie && ties + __builtin_popcountll(tie_lanes & below) < wanted));
+    ties += __builtin_popcountll(tie_lanes);
+    const int32_t t = x.first + i + lane;
+    const bool moves = stays && t >= x.behind, gap = have && !stays && t < x.behind;
+    const uint64_t mv = __builtin_amdgcn_ballot_w64(moves), gp = __builtin_amdgcn_ballot_w64(gap);
+    f(t, moves, movers + __builtin_popcountll(mv & below), gap, gaps + __builtin_popcountll(gp & below));
+    movers += __builtin_popcountll(mv);
+    gaps += __builtin_popcountll(gp);
+  }
+}
+
+// A row on its way, in its 16 lanes
+template <int D>
+struct Moving {
+  RowPart<D> x;
+  float w;
+  uint8_t* to;
+  int64_t w_at;
+  int32_t t;
+
+  __device__ __forceinline__ void read(const KvEvictArgs& a, const Row& row, int32_t* kept, int32_t old, int32_t place, int l) {
+    to = nullptr;
+    const int64_t src = row.pages.of(old), dst = row.pages.of(place);
+    if (src < 0 || dst < 0) return;
+    x = load_row<D>(granule_at<D>(a.cache, row.pages, src, row.kh, old), old, l);
+    to = granule_at<D>(a.cache, row.pages, dst, row.kh, place);
+    t = place;
+    if (l == 0) {
+      if (a.weights_out) {
+        w = a.weights[row.pages.weight_at(src, row.kh, old)];
+        w_at = row.pages.weight_at(dst, row.kh, place);
+      }
+      if (kept) kept[place] = old;
+    }
+  }
+  __device__ __forceinline__ void write(const KvEvictArgs& a, int l) const {
+    if (!to) return;
+    store_row<D>(to, t, l, x);
+    if (l == 0 && a.weights_out) a.weights_out[w_at] = w;
+  }
+};
+
+// The last tokens down by n - budget, in order where old and new places overlap: what a chunk overwrites
+// was read by it or by chunks before
+template <int D>
+__device__ __forceinline__ void move_last(const KvEvictArgs& a, const Row& x, int32_t* kept) {
+  const int row = threadIdx.x / kRowLanes, l = threadIdx.x % kRowLanes;
+  for (int32_t j0 = 0; j0 < x.last; j0 += kHeld * kRows) {
+    Moving<D> h[kHeld];
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      const int32_t j = j0 + i * kRows + row;
+      h[i].to = nullptr;
+      if (j < x.last) h[i].read(a, x, kept, x.n - x.last + j, x.behind + j, l);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) h[i].write(a, l);
+  }
+}
+
 template <int D>
 __global__ __launch_bounds__(kThreads) void k_kv_evict(KvEvictArgs a) {
   extern __shared__ uint32_t s_keys[];
   __shared__ int32_t s_hist[kBins];
   __shared__ int32_t s_waves[kWaves];
   __shared__ int32_t s_found[3];
-  const int hkv = a.pages.geom.n_kv_heads;
-  const int b = (int)blockIdx.x / hkv, kh = (int)blockIdx.x - b * hkv;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const Pages pages = pages_of(a.pages, b);
-  const int32_t n = length_of(a.pages, a.kv_len, b), budget = a.budget;
-  const bool over = n > budget;
-  const int32_t left = over ? budget : n;
-  int32_t* const kept = a.kept ? a.kept + (int64_t)blockIdx.x * budget : nullptr;
-  // what does not move
-  if (kept)
-    for (int32_t j = tid; j < budget; j += kThreads) kept[j] = j < left ? j : -1;
-  if (a.weights_out && a.weights_out != a.weights)
-    for (int32_t j = tid; j < left; j += kThreads) {
-      const int64_t page = pages.of(j);
-      if (page >= 0) {
-        const int64_t at = pages.weight_at(page, kh, j);
-        a.weights_out[at] = a.weights[at];
-      }
-    }
-  if (a.lengths && kh == 0 && tid == 0) a.kv_len_out[b] = left;
-  if (!over) return;
-
-  const int32_t first = a.first, last = a.last;
-  const int32_t rated = n - first - last, keep = budget - first - last, behind = budget - last;
-  const bool in_lds = rated <= a.lds_keys;
-  auto load_key = [&](int32_t i) {
-    const int64_t page = pages.of(first + i);
-    return page < 0 ? weight_key(-__builtin_inff()) : weight_key(a.weights[pages.weight_at(page, kh, first + i)]);
-  };
-  auto key_of = [&](int32_t i) { return in_lds ? s_keys[i] : load_key(i); };
+  const Row x(a, blockIdx.x);
+  keep_places(a, x, blockIdx.x, tid, kThreads);
+  if (!x.over) return;
+  int32_t* const kept = a.kept ? a.kept + (int64_t)blockIdx.x * a.budget : nullptr;
+  const bool in_lds = x.rated <= a.lds_keys;
+  auto key_of = [&](int32_t i) { return in_lds ? s_keys[i] : x.key(a, i); };
   if (in_lds)
-    for (int32_t i = tid; i < rated; i += kThreads) s_keys[i] = load_key(i);
+    for (int32_t i = tid; i < x.rated; i += kThreads) s_keys[i] = x.key(a, i);
 
   // the smallest kept key, and how many tokens of it are kept
   uint32_t border = 0, known = 0;
-  int32_t wanted = keep, equal = 0;
-  if (keep > 0) {
-    for (int pass = 0; pass < 3; ++pass) {
-      const uint32_t shift = kDigits[pass], mask = pass < 2 ? kBins - 1 : (kBins >> 1) - 1;
-      for (int i = tid; i < kBins; i += kThreads) s_hist[i] = 0;
-      __syncthreads();
-      for (int32_t i = tid; i < rated; i += kThreads) {
-        const uint32_t k = key_of(i);
-        if ((k & known) == border) atomicAdd(&s_hist[(k >> shift) & mask], 1);
-      }
-      __syncthreads();
-      // bins from the largest digit on, two a thread
-      const int hi = kBins - 1 - 2 * tid;
-      const int32_t x = s_hist[hi], y = s_hist[hi - 1];
-      int32_t all;
-      const int32_t before = sum_before(x + y, s_waves, all);
-      if (before < wanted && wanted <= before + x + y) {
-        const bool upper = wanted <= before + x;
-        s_found[0] = upper ? hi : hi - 1;
-        s_found[1] = wanted - before - (upper ? 0 : x);
-        s_found[2] = upper ? x : y;
-      }
-      __syncthreads();
-      border |= (uint32_t)s_found[0] << shift;
-      known |= mask << shift;
-      wanted = s_found[1];
-      equal = s_found[2];
+  int32_t wanted = x.keep, equal = 0;
+  for (int pass = 0; x.keep > 0 && pass < 3; ++pass) {
+    const uint32_t shift = kDigits[pass], mask = pass < 2 ? kBins - 1 : (kBins >> 1) - 1;
+    for (int i = tid; i < kBins; i += kThreads) s_hist[i] = 0;
+    __syncthreads();
+    for (int32_t i = tid; i < x.rated; i += kThreads) {
+      const uint32_t k = key_of(i);
+      if ((k & known) == border) atomicAdd(&s_hist[(k >> shift) & mask], 1);
     }
+    __syncthreads();
+    find_digit(s_hist[kBins - 1 - 2 * tid], s_hist[kBins - 2 - 2 * tid], wanted, s_waves, s_found);
+    border |= (uint32_t)s_found[0] << shift;
+    known |= mask << shift;
+    wanted = s_found[1];
+    equal = s_found[2];
   }
 
   // each wave a run of tokens, in order
-  const int32_t run = ((rated + kWaves - 1) / kWaves + 63) & ~63;
-  const int32_t r0 = wave * run < rated ? wave * run : rated, r1 = r0 + run < rated ? r0 + run : rated;
-  const uint64_t below = (1ull << lane) - 1;
+  const int32_t run = ((x.rated + kWaves - 1) / kWaves + 63) & ~63;
+  const int32_t r0 = wave * run < x.rated ? wave * run : x.rated, r1 = r0 + run < x.rated ? r0 + run : x.rated;
   int32_t ties0 = 0;                               // tokens of the border's key before this wave's run
-  if (keep > 0 && equal > wanted) {
-    int32_t ties = 0;
-    for (int32_t i = r0; i < r1; i += 64)
-      ties += i + lane < r1 && key_of(i + lane) == border;
-    int32_t all;
-    // of the waves before: what the first lane has before it
-    ties0 = __builtin_amdgcn_readfirstlane(sum_before(ties, s_waves, all));
+  if (x.keep > 0 && equal > wanted) {
+    int32_t ties = 0, all;
+    for (int32_t i = r0 + lane; i < r1; i += 64) ties += key_of(i) == border;
+    ties0 = __builtin_amdgcn_readfirstlane(sum_before(ties, s_waves, all));   // what the first lane has before it
   }
-  // calls f(token, its number among the movers or free places of the run) for each of these
-  auto walk = [&](int32_t& movers, int32_t& free_, auto f) {
-    int32_t ties = ties0;
-    for (int32_t i = r0; i < r1; i += 64) {
-      const bool have = i + lane < r1;
-      const uint32_t k = have ? key_of(i + lane) : 0;
-      const bool tie = have && keep > 0 && k == border;
-      const uint64_t tie_lanes = __builtin_amdgcn_ballot_w64(tie);
-      const bool stays = have && keep > 0 &&
-                         (k > border || (tie && ties + __builtin_popcountll(tie_lanes & below) < wanted));
-      ties += __builtin_popcountll(tie_lanes);
-      const int32_t t = first + i + lane;
-      const bool moves = stays && t >= behind, gap = have && !stays && t < behind;
-      const uint64_t mv = __builtin_amdgcn_ballot_w64(moves), gp = __builtin_amdgcn_ballot_w64(gap);
-      f(t, moves, movers + __builtin_popcountll(mv & below), gap, free_ + __builtin_popcountll(gp & below));
-      movers += __builtin_popcountll(mv);
-      free_ += __builtin_popcountll(gp);
-    }
-  };
-  int32_t movers = 0, free_ = 0, moving, gaps;
-  walk(movers, free_, [](int32_t, bool, int32_t, bool, int32_t) {});
-  const int32_t movers0 = __builtin_amdgcn_readfirstlane(sum_before(lane == 0 ? movers : 0, s_waves, moving));
-  const int32_t free0 = __builtin_amdgcn_readfirstlane(sum_before(lane == 0 ? free_ : 0, s_waves, gaps));
-  int32_t* const from = a.lists + (int64_t)blockIdx.x * 2 * budget;
-  int32_t* const to = from + budget;
-  movers = movers0;
-  free_ = free0;
-  walk(movers, free_, [&](int32_t t, bool moves, int32_t i, bool gap, int32_t j) {
+  int32_t movers = 0, gaps = 0, moving, all;
+  walk(x, r0, r1, border, wanted, ties0, key_of, movers, gaps, [](int32_t, bool, int32_t, bool, int32_t) {});
+  movers = __builtin_amdgcn_readfirstlane(sum_before(lane == 0 ? movers : 0, s_waves, moving));
+  gaps = __builtin_amdgcn_readfirstlane(sum_before(lane == 0 ? gaps : 0, s_waves, all));
+  int32_t* const from = a.lists + (int64_t)blockIdx.x * 2 * a.budget;
+  int32_t* const to = from + a.budget;
+  walk(x, r0, r1, border, wanted, ties0, key_of, movers, gaps, [&](int32_t t, bool moves, int32_t i, bool gap, int32_t j) {
     if (moves) from[i] = t;
     if (gap) to[j] = t;
   });
   __syncthreads();
 
-  const int row = tid / kRowLanes, l = tid % kRowLanes;
-  struct Held {
-    RowPart<D> x;
-    float w;
-    uint8_t* to;
-    int64_t w_at;
-    int32_t t;
-  };
-  auto read = [&](int32_t old, int32_t place, Held& h) {
-    h.to = nullptr;
-    const int64_t src = pages.of(old), dst = pages.of(place);
-    if (src < 0 || dst < 0) return;
-    h.x = load_row<D>(granule_at<D>(a.cache, pages, src, kh, old), old, l);
-    h.to = granule_at<D>(a.cache, pages, dst, kh, place);
-    h.t = place;
-    if (l == 0) {
-      if (a.weights_out) {
-        h.w = a.weights[pages.weight_at(src, kh, old)];
-        h.w_at = pages.weight_at(dst, kh, place);
-      }
-      if (kept) kept[place] = old;
-    }
-  };
-  auto write = [&](const Held& h) {
-    if (!h.to) return;
-    store_row<D>(h.to, h.t, l, h.x);
-    if (l == 0 && a.weights_out) a.weights_out[h.w_at] = h.w;
-  };
   // movers stand behind every free place: nothing that is read here is written
+  const int row = tid / kRowLanes, l = tid % kRowLanes;
   for (int32_t i = row; i < moving; i += kRows) {
-    Held h;
-    read(from[i], to[i], h);
-    write(h);
+    Moving<D> m;
+    m.read(a, x, kept, from[i], to[i], l);
+    m.write(a, l);
   }
-  // Down by n - budget: what a chunk overwrites was read by it, by the movers or by chunks before
-  for (int32_t j0 = 0; j0 < last; j0 += kHeld * kRows) {
-    Held h[kHeld];
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-      const int32_t j = j0 + i * kRows + row;
-      h[i].to = nullptr;
-      if (j < last) read(n - last + j, behind + j, h[i]);
+  move_last<D>(a, x, kept);
+}
+
+// The same in parts: row blockIdx / parts, part blockIdx % parts, of equal runs of the row's rated
+// tokens.  A part leaves its histograms, which the launch after sums up.
+struct Parts {
+  int32_t row, part, r0, r1;
+  __device__ __forceinline__ Parts(const KvEvictArgs& a, int32_t block) : row(block / a.parts), part(block % a.parts) {}
+  __device__ __forceinline__ int32_t size(const KvEvictArgs& a, const Row& x) const {
+    return ((x.rated + a.parts - 1) / a.parts + kThreads - 1) / kThreads * kThreads;
+  }
+  __device__ __forceinline__ int32_t begin(const KvEvictArgs& a, const Row& x, int32_t p) const {
+    const int64_t at = (int64_t)p * size(a, x);
+    return at < x.rated ? (int32_t)at : x.rated;
+  }
+};
+// what a part leaves: two histograms, the third for the tokens whose places are kept ones' and for the
+// others, and how many of either have larger first two digits
+struct PartCounts {
+  int32_t digit[2][kBins];
+  int32_t last[2][kBins / 2];
+  int32_t larger[2];
+};
+struct RowState {
+  uint32_t border;
+  int32_t wanted, moving, pad;
+};
+static_assert(sizeof(PartCounts) <= kKvEvictPartBytes && sizeof(RowState) == 16, "kv_launch.hpp");
+__device__ __forceinline__ PartCounts* counts_of(const KvEvictArgs& a, int32_t row, int32_t part) {
+  return reinterpret_cast<PartCounts*>(static_cast<uint8_t*>(a.counts) + ((int64_t)row * a.parts + part) * kKvEvictPartBytes);
+}
+__device__ __forceinline__ RowState* state_of(const KvEvictArgs& a, int32_t row) {
+  return reinterpret_cast<RowState*>(a.states) + row;
+}
+
+// Histogram PASS of a part's keys, those whose digits before are the border's
+template <int PASS>
+__global__ __launch_bounds__(kThreads) void k_kv_evict_digits(KvEvictArgs a) {
+  __shared__ int32_t s_hist[kBins];
+  __shared__ int32_t s_waves[kWaves];
+  __shared__ int32_t s_found[3];
+  __shared__ int32_t s_larger[2];
+  const int tid = threadIdx.x;
+  const Parts p(a, blockIdx.x);
+  const Row x(a, p.row);
+  if constexpr (PASS == 0) keep_places(a, x, p.row, p.part * kThreads + tid, a.parts * kThreads);
+  if (!x.over || x.keep == 0) return;
+  uint32_t border = 0;
+  if constexpr (PASS > 0) {
+    int32_t wanted = x.keep;
+    if constexpr (PASS == 2) {
+      border = state_of(a, p.row)->border;
+      wanted = state_of(a, p.row)->wanted;
     }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) write(h[i]);
+    int32_t hi = 0, lo = 0;
+    for (int32_t q = 0; q < a.parts; ++q) {
+      const int32_t* const c = counts_of(a, p.row, q)->digit[PASS - 1];
+      hi += c[kBins - 1 - 2 * tid];
+      lo += c[kBins - 2 - 2 * tid];
+    }
+    find_digit(hi, lo, wanted, s_waves, s_found);
+    border |= (uint32_t)s_found[0] << kDigits[PASS - 1];
+    // the part that is last to begin its row's next launch reads what any part writes here
+    if (p.part == 0 && tid == 0) {
+      RowState* const st = PASS == 1 ? state_of(a, p.row) : state_of(a, p.row) + a.rows;
+      st->border = border;
+      st->wanted = s_found[1];
+    }
   }
+  for (int i = tid; i < kBins; i += kThreads) s_hist[i] = 0;
+  if (tid < 2) s_larger[tid] = 0;
+  __syncthreads();
+  const int32_t r0 = p.begin(a, x, p.part), r1 = p.begin(a, x, p.part + 1);
+  int32_t larger[2] = {0, 0};
+  auto count = [&](uint32_t k, int32_t i) {
+    if constexpr (PASS == 0) {
+      atomicAdd(&s_hist[k >> 21], 1);
+    } else if constexpr (PASS == 1) {
+      if (k >> 21 == border >> 21) atomicAdd(&s_hist[(k >> 10) & (kBins - 1)], 1);
+    } else {
+      const int behind = x.first + i >= x.behind;
+      if (k >> 10 == border >> 10) atomicAdd(&s_hist[behind * (kBins / 2) + (k & (kBins / 2 - 1))], 1);
+      else if (k >> 10 > border >> 10) ++larger[behind];
+    }
+  };
+  int32_t i = r0 + tid;
+  for (; i + 3 * kThreads < r1; i += 4 * kThreads) {
+    uint32_t k[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) k[e] = x.key(a, i + e * kThreads);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) count(k[e], i + e * kThreads);
+  }
+  for (; i < r1; i += kThreads) count(x.key(a, i), i);
+  if constexpr (PASS == 2) {
+    if (larger[0]) atomicAdd(&s_larger[0], larger[0]);
+    if (larger[1]) atomicAdd(&s_larger[1], larger[1]);
+  }
+  __syncthreads();
+  PartCounts* const c = counts_of(a, p.row, p.part);
+  int32_t* const out = PASS < 2 ? c->digit[PASS < 2 ? PASS : 0] : c->last[0];
+  for (int j = tid; j < kBins; j += kThreads) out[j] = s_hist[j];
+  if (PASS == 2 && tid < 2) c->larger[tid] = s_larger[tid];
+}
+
+// The lists
+__global__ __launch_bounds__(kThreads) void k_kv_evict_lists(KvEvictArgs a) {
+  __shared__ int32_t s_waves[kWaves];
+  __shared__ int32_t s_found[3];
+  __shared__ int32_t s_part[kKvEvictMostParts][4];     // of each part: larger and equal keys, of kept places' tokens and others
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const Parts p(a, blockIdx.x);
+  const Row x(a, p.row);
+  if (!x.over) return;
+  uint32_t border = 0;
+  int32_t wanted = 0, ties0 = 0, movers = 0, gaps = 0;
+  if (x.keep > 0) {
+    const RowState st = state_of(a, p.row)[a.rows];
+    int32_t hi = 0, lo = 0;
+    if (tid >= kBins / 4)                              // the third digit has half the bins
+      for (int32_t q = 0; q < a.parts; ++q) {
+        const PartCounts* const c = counts_of(a, p.row, q);
+        const int at = kBins - 1 - 2 * tid;
+        hi += c->last[0][at] + c->last[1][at];
+        lo += c->last[0][at - 1] + c->last[1][at - 1];
+      }
+    find_digit(hi, lo, st.wanted, s_waves, s_found);
+    const int32_t digit = s_found[0];
+    border = st.border | (uint32_t)digit;
+    wanted = s_found[1];
+    for (int32_t q = wave; q < a.parts; q += kWaves) {
+      const PartCounts* const c = counts_of(a, p.row, q);
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        int32_t more = 0;
+        for (int j = lane; j < kBins / 2; j += 64) more += j > digit ? c->last[z][j] : 0;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) more += __shfl_xor(more, off);
+        if (lane == 0) {
+          s_part[q][z] = more + c->larger[z];
+          s_part[q][2 + z] = c->last[z][digit];
+        }
+      }
+    }
+  }
+  __syncthreads();
+  // what stands before this part (and, for the last one's use, in all)
+  int32_t moving = 0;
+  for (int32_t q = 0, ties = 0; q < a.parts; ++q) {
+    if (q == p.part) {
+      ties0 = ties;
+      movers = moving;
+    }
+    const int32_t r0 = p.begin(a, x, q), r1 = p.begin(a, x, q + 1);
+    int32_t near = x.behind - x.first - r0;             // its tokens on kept ones' places
+    near = near < 0 ? 0 : (near > r1 - r0 ? r1 - r0 : near);
+    int32_t stay = 0;
+    if (x.keep > 0) {
+      // of its ties, in order, those that are still wanted
+      const int32_t open = wanted - ties < 0 ? 0 : wanted - ties;
+      const int32_t t0 = s_part[q][2] < open ? s_part[q][2] : open;
+      const int32_t t1 = s_part[q][3] < open - t0 ? s_part[q][3] : open - t0;
+      stay = s_part[q][0] + t0;
+      moving += s_part[q][1] + t1;
+      ties += s_part[q][2] + s_part[q][3];
+    }
+    if (q < p.part) gaps += near - stay;
+  }
+  if (p.part == 0 && tid == 0) state_of(a, p.row)->moving = moving;
+
+  const int32_t r0 = p.begin(a, x, p.part), r1 = p.begin(a, x, p.part + 1);
+  const int32_t run = ((r1 - r0 + kWaves - 1) / kWaves + 63) & ~63;
+  const int32_t w0 = r0 + wave * run < r1 ? r0 + wave * run : r1, w1 = w0 + run < r1 ? w0 + run : r1;
+  auto key_of = [&](int32_t i) { return x.key(a, i); };
+  int32_t ties = 0, all;
+  if (x.keep > 0)
+    for (int32_t i = w0 + lane; i < w1; i += 64) ties += key_of(i) == border;
+  ties0 += __builtin_amdgcn_readfirstlane(sum_before(ties, s_waves, all));
+  int32_t m = 0, g = 0;
+  walk(x, w0, w1, border, wanted, ties0, key_of, m, g, [](int32_t, bool, int32_t, bool, int32_t) {});
+  m = movers + __builtin_amdgcn_readfirstlane(sum_before(lane == 0 ? m : 0, s_waves, all));
+  g = gaps + __builtin_amdgcn_readfirstlane(sum_before(lane == 0 ? g : 0, s_waves, all));
+  int32_t* const from = a.lists + (int64_t)p.row * 2 * a.budget;
+  int32_t* const to = from + a.budget;
+  walk(x, w0, w1, border, wanted, ties0, key_of, m, g, [&](int32_t t, bool moves, int32_t i, bool gap, int32_t j) {
+    if (moves) from[i] = t;
+    if (gap) to[j] = t;
+  });
+}
+
+// Movers, and the last tokens where their old and new places do not overlap
+template <int D>
+__global__ __launch_bounds__(256) void k_kv_evict_move(KvEvictArgs a) {
+  const Parts p(a, blockIdx.x);
+  const Row x(a, p.row);
+  if (!x.over) return;
+  int32_t* const kept = a.kept ? a.kept + (int64_t)p.row * a.budget : nullptr;
+  const int32_t* const from = a.lists + (int64_t)p.row * 2 * a.budget;
+  const int32_t* const to = from + a.budget;
+  const int32_t moving = state_of(a, p.row)->moving;
+  const int row = threadIdx.x / kRowLanes, l = threadIdx.x % kRowLanes;
+  constexpr int kSide = 256 / kRowLanes, kDeep = 4;
+  for (int32_t i0 = p.part * kSide * kDeep; i0 < moving; i0 += a.parts * kSide * kDeep) {
+    Moving<D> m[kDeep];
+#pragma unroll
+    for (int e = 0; e < kDeep; ++e) {
+      const int32_t i = i0 + e * kSide + row;
+      m[e].to = nullptr;
+      if (i < moving) m[e].read(a, x, kept, from[i], to[i], l);
+    }
+#pragma unroll
+    for (int e = 0; e < kDeep; ++e) m[e].write(a, l);
+  }
+}
+
+template <int D>
+__global__ __launch_bounds__(kThreads) void k_kv_evict_last(KvEvictArgs a) {
+  const Row x(a, blockIdx.x);
+  if (!x.over) return;
+  move_last<D>(a, x, a.kept ? a.kept + (int64_t)blockIdx.x * a.budget : nullptr);
 }
 
 // The lengths, where they are written over those that the workgroups read
@@ -360,11 +604,27 @@ __global__ __launch_bounds__(256) void k_kv_lengths(KvEvictArgs a) {
 }
 
 template <int D>
-hipError_t evict(const KvEvictArgs& a, hipStream_t s) {
-  const int bytes = a.lds_keys * (int)sizeof(uint32_t);
-  const hipError_t e = lds_limit_once<k_kv_evict<D>>(kKvEvictMostKeys * (int)sizeof(uint32_t));
+hipError_t evict(KvEvictArgs a, hipStream_t s) {
+  const dim3 rows((unsigned)a.rows), threads(kThreads);
+  if (a.parts == 0) {
+    const hipError_t e = lds_limit_once<k_kv_evict<D>>(kKvEvictMostKeys * (int)sizeof(uint32_t));
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((k_kv_evict<D>), rows, threads, a.lds_keys * (int)sizeof(uint32_t), s, a);
+    return hipGetLastError();
+  }
+  const dim3 parts((unsigned)(a.rows * a.parts));
+  hipLaunchKernelGGL((k_kv_evict_digits<0>), parts, threads, 0, s, a);
+  hipLaunchKernelGGL((k_kv_evict_digits<1>), parts, threads, 0, s, a);
+  hipLaunchKernelGGL((k_kv_evict_digits<2>), parts, threads, 0, s, a);
+  hipLaunchKernelGGL(k_kv_evict_lists, parts, threads, 0, s, a);
+  hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((k_kv_evict<D>), dim3((unsigned)(a.pages.batch * a.pages.geom.n_kv_heads)), dim3(kThreads), bytes, s, a);
+  KvEvictArgs m = a;
+  m.parts = a.move_parts;
+  hipLaunchKernelGGL((k_kv_evict_move<D>), dim3((unsigned)(m.rows * m.parts)), dim3(256), 0, s, m);
+  e = hipGetLastError();
+  if (e != hipSuccess || a.last == 0) return e;
+  hipLaunchKernelGGL((k_kv_evict_last<D>), rows, threads, 0, s, a);
   return hipGetLastError();
 }
 
@@ -378,10 +638,35 @@ hipError_t launch_kv_accept(const KvAcceptArgs& a, int32_t D, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_kv_evict(KvEvictArgs a, int32_t D, int64_t max_kv_len, hipStream_t s) {
+KvEvictPlan kv_evict_plan(int32_t batch, int32_t n_kv_heads, int64_t budget, int64_t max_kv_len) {
+  KvEvictPlan p{};
+  const int64_t rows = (int64_t)batch * n_kv_heads;
+  const int64_t lists = (rows * 2 * budget * (int64_t)sizeof(int32_t) + 255) & ~255ll;
+  p.workspace = lists;
+  // Parts of 8192 tokens
+  const int64_t tokens = (max_kv_len + 8191) / 8192, most = kKvEvictParts / rows;
+  const int64_t parts = tokens < most ? tokens : most;
+  if (max_kv_len > kKvEvictMostKeys) {             // fewer rows need no more than more of them
+    if (parts > 1) p.parts = (int32_t)(parts < kKvEvictMostParts ? parts : kKvEvictMostParts);
+    p.states_at = lists;
+    p.counts_at = lists + kKvEvictParts * 2 * 16;
+    p.workspace = p.counts_at + (int64_t)kKvEvictParts * kKvEvictPartBytes;
+  }
+  return p;
+}
+
+hipError_t launch_kv_evict(KvEvictArgs a, int32_t D, const KvEvictPlan& p, int64_t max_kv_len, void* workspace, hipStream_t s) {
   const int64_t rated = max_kv_len - a.first - a.last;
-  a.lds_keys = (int32_t)(rated < 0 ? 0 : (rated > kKvEvictMostKeys ? 0 : rated));
+  a.rows = a.pages.batch * a.pages.geom.n_kv_heads;
+  a.lds_keys = (int32_t)(rated < 0 || rated > kKvEvictMostKeys ? 0 : rated);
   a.lengths = a.kv_len_out != a.kv_len;
+  a.parts = p.parts;
+  a.lists = static_cast<int32_t*>(workspace);
+  a.states = static_cast<uint8_t*>(workspace) + p.states_at;
+  a.counts = static_cast<uint8_t*>(workspace) + p.counts_at;
+  // 64 rows a workgroup and turn
+  const int64_t turns = (a.budget + 63) / 64, most = 2048 / a.rows + 1;
+  a.move_parts = (int32_t)(turns < most ? turns : most);
   const hipError_t e = D == 64 ? evict<64>(a, s) : (D == 128 ? evict<128>(a, s) : evict<256>(a, s));
   if (e != hipSuccess || a.lengths) return e;
   hipLaunchKernelGGL(k_kv_lengths, dim3((unsigned)((a.pages.batch + 255) / 256)), dim3(256), 0, s, a);
