@@ -81,7 +81,8 @@ struct KvEvictArgs {
   int32_t rows;                // batch * n_kv_heads
   int32_t lds_keys;            // keys that the launch's LDS holds
   int32_t lengths;             // whether the kernels write the lengths
-  int32_t parts, move_parts;   // of a row, for the keys and for what moves; 0: a workgroup does a whole row
+  int32_t parts;               // of a row; 0: a workgroup does a whole one
+  int32_t move_parts, last_parts;   // for what moves
 };
 constexpr int kKvEvictParts = 512;                 // of all rows
 constexpr int kKvEvictMostParts = 64;              // of a row

@@ -206,12 +206,42 @@ struct Row {
   }
 };
 
-// What does not move: `count` threads of a row share it
+// Calls f(i, key of rated token i) for i = begin + thread, + count, ... below end, four tokens' loads side
+// by side; COPY: and gives the weights of the tokens that may stay where they are to weights_out
+template <bool COPY, typename F>
+__device__ __forceinline__ void for_keys(const KvEvictArgs& a, const Row& x, int32_t begin, int32_t end, int32_t thread,
+                                         int32_t count, F f) {
+  constexpr int N = 4;
+  const bool copy = COPY && a.weights_out && a.weights_out != a.weights;
+  for (int32_t i0 = begin + thread; i0 < end; i0 += N * count) {
+    int64_t at[N];
+    float w[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const int32_t i = i0 + e * count, t = x.first + (i < end ? i : i0);
+      const int64_t page = x.pages.of(t);
+      at[e] = page < 0 ? -1 : x.pages.weight_at(page, x.kh, t);
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e) w[e] = at[e] < 0 ? -__builtin_inff() : a.weights[at[e]];
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const int32_t i = i0 + e * count;
+      if (i >= end) break;
+      if (copy && x.first + i < x.behind && at[e] >= 0) a.weights_out[at[e]] = w[e];
+      f(i, weight_key(w[e]));
+    }
+  }
+}
+
+// What does not move, but for the rated tokens' weights (for_keys): `count` threads of a row share it
 __device__ __forceinline__ void keep_places(const KvEvictArgs& a, const Row& x, int32_t row, int32_t thread, int32_t count) {
+  const int32_t stay = x.over ? x.behind : x.left;
   if (a.kept)
-    for (int32_t j = thread; j < a.budget; j += count) a.kept[(int64_t)row * a.budget + j] = j < x.left ? j : -1;
+    for (int32_t j = thread; j < (x.over ? x.behind : a.budget); j += count)
+      a.kept[(int64_t)row * a.budget + j] = j < stay ? j : -1;
   if (a.weights_out && a.weights_out != a.weights)
-    for (int32_t j = thread; j < x.left; j += count) {
+    for (int32_t j = thread; j < (x.over ? x.first : x.left); j += count) {
       const int64_t page = x.pages.of(j);
       if (page >= 0) {
         const int64_t at = x.pages.weight_at(page, x.kh, j);
@@ -291,40 +321,43 @@ struct Moving {
   }
 };
 
-// The last tokens down by n - budget, in order where old and new places overlap: what a chunk overwrites
-// was read by it or by chunks before
+// The last tokens down by n - budget, a chunk of kHeld * kRows at a time from j0 on, in order where
+// old and new places overlap: what a chunk overwrites was read by it or by chunks before.
+constexpr int kChunk = kHeld * kRows;
+
 template <int D>
-__device__ __forceinline__ void move_last(const KvEvictArgs& a, const Row& x, int32_t* kept) {
+__device__ __forceinline__ void read_last(const KvEvictArgs& a, const Row& x, int32_t* kept, int32_t j0, Moving<D> (&h)[kHeld]) {
   const int row = threadIdx.x / kRowLanes, l = threadIdx.x % kRowLanes;
-  for (int32_t j0 = 0; j0 < x.last; j0 += kHeld * kRows) {
-    Moving<D> h[kHeld];
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-      const int32_t j = j0 + i * kRows + row;
-      h[i].to = nullptr;
-      if (j < x.last) h[i].read(a, x, kept, x.n - x.last + j, x.behind + j, l);
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) h[i].write(a, l);
+  for (int i = 0; i < kHeld; ++i) {
+    const int32_t j = j0 + i * kRows + row;
+    h[i].to = nullptr;
+    if (j < x.last) h[i].read(a, x, kept, x.n - x.last + j, x.behind + j, l);
   }
 }
 
 template <int D>
 __global__ __launch_bounds__(kThreads) void k_kv_evict(KvEvictArgs a) {
   extern __shared__ uint32_t s_keys[];
-  __shared__ int32_t s_hist[kBins];
+  __shared__ int32_t s_hist[kBins];                // and the lists, where they are short
   __shared__ int32_t s_waves[kWaves];
   __shared__ int32_t s_found[3];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const Row x(a, blockIdx.x);
-  keep_places(a, x, blockIdx.x, tid, kThreads);
-  if (!x.over) return;
+  if (!x.over) {
+    keep_places(a, x, blockIdx.x, tid, kThreads);
+    return;
+  }
   int32_t* const kept = a.kept ? a.kept + (int64_t)blockIdx.x * a.budget : nullptr;
   const bool in_lds = x.rated <= a.lds_keys;
   auto key_of = [&](int32_t i) { return in_lds ? s_keys[i] : x.key(a, i); };
-  if (in_lds)
-    for (int32_t i = tid; i < x.rated; i += kThreads) s_keys[i] = x.key(a, i);
+  for_keys<true>(a, x, 0, x.rated, tid, kThreads, [&](int32_t i, uint32_t k) {
+    if (in_lds) s_keys[i] = k;
+  });
+  // the last tokens' first chunk, on its way while the others are chosen
+  Moving<D> tail[kHeld];
+  read_last<D>(a, x, kept, 0, tail);
+  keep_places(a, x, blockIdx.x, tid, kThreads);
 
   // the smallest kept key, and how many tokens of it are kept
   uint32_t border = 0, known = 0;
@@ -358,22 +391,39 @@ __global__ __launch_bounds__(kThreads) void k_kv_evict(KvEvictArgs a) {
   walk(x, r0, r1, border, wanted, ties0, key_of, movers, gaps, [](int32_t, bool, int32_t, bool, int32_t) {});
   movers = __builtin_amdgcn_readfirstlane(sum_before(lane == 0 ? movers : 0, s_waves, moving));
   gaps = __builtin_amdgcn_readfirstlane(sum_before(lane == 0 ? gaps : 0, s_waves, all));
-  int32_t* const from = a.lists + (int64_t)blockIdx.x * 2 * a.budget;
-  int32_t* const to = from + a.budget;
-  walk(x, r0, r1, border, wanted, ties0, key_of, movers, gaps, [&](int32_t t, bool moves, int32_t i, bool gap, int32_t j) {
-    if (moves) from[i] = t;
-    if (gap) to[j] = t;
-  });
-  __syncthreads();
+  auto lists = [&](int32_t* from, int32_t* to) {
+    walk(x, r0, r1, border, wanted, ties0, key_of, movers, gaps, [&](int32_t t, bool moves, int32_t i, bool gap, int32_t j) {
+      if (moves) from[i] = t;
+      if (gap) to[j] = t;
+    });
+    __syncthreads();
+    // movers stand behind every free place: nothing that is read here is written
+    const int row = tid / kRowLanes, l = tid % kRowLanes;
+    for (int32_t i0 = row; i0 < moving; i0 += 2 * kRows) {
+      Moving<D> m[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int32_t i = i0 + e * kRows;
+        m[e].to = nullptr;
+        if (i < moving) m[e].read(a, x, kept, from[i], to[i], l);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) m[e].write(a, l);
+    }
+  };
+  if (moving <= kBins / 2) lists(s_hist, s_hist + kBins / 2);
+  else lists(a.lists + (int64_t)blockIdx.x * 2 * a.budget, a.lists + (int64_t)blockIdx.x * 2 * a.budget + a.budget);
 
-  // movers stand behind every free place: nothing that is read here is written
-  const int row = tid / kRowLanes, l = tid % kRowLanes;
-  for (int32_t i = row; i < moving; i += kRows) {
-    Moving<D> m;
-    m.read(a, x, kept, from[i], to[i], l);
-    m.write(a, l);
+  const int l = tid % kRowLanes;
+  __syncthreads();                                 // the movers are read
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) tail[i].write(a, l);
+  for (int32_t j0 = kChunk; j0 < x.last; j0 += kChunk) {
+    read_last<D>(a, x, kept, j0, tail);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) tail[i].write(a, l);
   }
-  move_last<D>(a, x, kept);
 }
 
 // The same in parts: row blockIdx / parts, part blockIdx % parts, of equal runs of the row's rated
@@ -408,6 +458,23 @@ __device__ __forceinline__ RowState* state_of(const KvEvictArgs& a, int32_t row)
   return reinterpret_cast<RowState*>(a.states) + row;
 }
 
+// Sums f(counts of a part) over a row's parts, eight loads side by side
+template <typename F>
+__device__ __forceinline__ void sum_parts(const KvEvictArgs& a, int32_t row, F f, int32_t& x, int32_t& y) {
+  constexpr int N = 8;
+  for (int32_t q0 = 0; q0 < a.parts; q0 += N) {
+    int2 v[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) v[e] = f(counts_of(a, row, q0 + e < a.parts ? q0 + e : q0));
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (q0 + e < a.parts) {
+        x += v[e].x;
+        y += v[e].y;
+      }
+  }
+}
+
 // Histogram PASS of a part's keys, those whose digits before are the border's
 template <int PASS>
 __global__ __launch_bounds__(kThreads) void k_kv_evict_digits(KvEvictArgs a) {
@@ -419,7 +486,7 @@ __global__ __launch_bounds__(kThreads) void k_kv_evict_digits(KvEvictArgs a) {
   const Parts p(a, blockIdx.x);
   const Row x(a, p.row);
   if constexpr (PASS == 0) keep_places(a, x, p.row, p.part * kThreads + tid, a.parts * kThreads);
-  if (!x.over || x.keep == 0) return;
+  if (!x.over || (PASS > 0 && x.keep == 0)) return;   // the first one copies weights
   uint32_t border = 0;
   if constexpr (PASS > 0) {
     int32_t wanted = x.keep;
@@ -428,11 +495,9 @@ __global__ __launch_bounds__(kThreads) void k_kv_evict_digits(KvEvictArgs a) {
       wanted = state_of(a, p.row)->wanted;
     }
     int32_t hi = 0, lo = 0;
-    for (int32_t q = 0; q < a.parts; ++q) {
-      const int32_t* const c = counts_of(a, p.row, q)->digit[PASS - 1];
-      hi += c[kBins - 1 - 2 * tid];
-      lo += c[kBins - 2 - 2 * tid];
-    }
+    sum_parts(a, p.row, [&](const PartCounts* c) {
+      return *reinterpret_cast<const int2*>(&c->digit[PASS - 1][kBins - 2 - 2 * tid]);
+    }, lo, hi);
     find_digit(hi, lo, wanted, s_waves, s_found);
     border |= (uint32_t)s_found[0] << kDigits[PASS - 1];
     // the part that is last to begin its row's next launch reads what any part writes here
@@ -458,15 +523,7 @@ __global__ __launch_bounds__(kThreads) void k_kv_evict_digits(KvEvictArgs a) {
       else if (k >> 10 > border >> 10) ++larger[behind];
     }
   };
-  int32_t i = r0 + tid;
-  for (; i + 3 * kThreads < r1; i += 4 * kThreads) {
-    uint32_t k[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) k[e] = x.key(a, i + e * kThreads);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) count(k[e], i + e * kThreads);
-  }
-  for (; i < r1; i += kThreads) count(x.key(a, i), i);
+  for_keys<PASS == 0>(a, x, r0, r1, tid, kThreads, [&](int32_t i, uint32_t k) { count(k, i); });
   if constexpr (PASS == 2) {
     if (larger[0]) atomicAdd(&s_larger[0], larger[0]);
     if (larger[1]) atomicAdd(&s_larger[1], larger[1]);
@@ -479,26 +536,32 @@ __global__ __launch_bounds__(kThreads) void k_kv_evict_digits(KvEvictArgs a) {
 }
 
 // The lists
+constexpr int kPartKeys = 9216;                        // of a part, that LDS holds
+
 __global__ __launch_bounds__(kThreads) void k_kv_evict_lists(KvEvictArgs a) {
   __shared__ int32_t s_waves[kWaves];
   __shared__ int32_t s_found[3];
+  __shared__ uint32_t s_keys[kPartKeys];
   __shared__ int32_t s_part[kKvEvictMostParts][4];     // of each part: larger and equal keys, of kept places' tokens and others
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const Parts p(a, blockIdx.x);
   const Row x(a, p.row);
   if (!x.over) return;
+  const int32_t r0 = p.begin(a, x, p.part), r1 = p.begin(a, x, p.part + 1);
+  const bool in_lds = r1 - r0 <= kPartKeys;
+  if (in_lds) for_keys<false>(a, x, r0, r1, tid, kThreads, [&](int32_t i, uint32_t k) { s_keys[i - r0] = k; });
+  auto key_of = [&](int32_t i) { return in_lds ? s_keys[i - r0] : x.key(a, i); };
   uint32_t border = 0;
   int32_t wanted = 0, ties0 = 0, movers = 0, gaps = 0;
   if (x.keep > 0) {
     const RowState st = state_of(a, p.row)[a.rows];
     int32_t hi = 0, lo = 0;
     if (tid >= kBins / 4)                              // the third digit has half the bins
-      for (int32_t q = 0; q < a.parts; ++q) {
-        const PartCounts* const c = counts_of(a, p.row, q);
-        const int at = kBins - 1 - 2 * tid;
-        hi += c->last[0][at] + c->last[1][at];
-        lo += c->last[0][at - 1] + c->last[1][at - 1];
-      }
+#pragma unroll
+      for (int z = 0; z < 2; ++z)
+        sum_parts(a, p.row, [&](const PartCounts* c) {
+          return *reinterpret_cast<const int2*>(&c->last[z][kBins - 2 - 2 * tid]);
+        }, lo, hi);
     find_digit(hi, lo, st.wanted, s_waves, s_found);
     const int32_t digit = s_found[0];
     border = st.border | (uint32_t)digit;
@@ -508,7 +571,11 @@ __global__ __launch_bounds__(kThreads) void k_kv_evict_lists(KvEvictArgs a) {
 #pragma unroll
       for (int z = 0; z < 2; ++z) {
         int32_t more = 0;
-        for (int j = lane; j < kBins / 2; j += 64) more += j > digit ? c->last[z][j] : 0;
+#pragma unroll
+        for (int j = 0; j < kBins / 2; j += 64) {
+          const int32_t y = c->last[z][j + lane];
+          more += j + lane > digit ? y : 0;
+        }
 #pragma unroll
         for (int off = 1; off < 64; off <<= 1) more += __shfl_xor(more, off);
         if (lane == 0) {
@@ -526,9 +593,9 @@ __global__ __launch_bounds__(kThreads) void k_kv_evict_lists(KvEvictArgs a) {
       ties0 = ties;
       movers = moving;
     }
-    const int32_t r0 = p.begin(a, x, q), r1 = p.begin(a, x, q + 1);
-    int32_t near = x.behind - x.first - r0;             // its tokens on kept ones' places
-    near = near < 0 ? 0 : (near > r1 - r0 ? r1 - r0 : near);
+    const int32_t q0 = p.begin(a, x, q), q1 = p.begin(a, x, q + 1);
+    int32_t near = x.behind - x.first - q0;             // its tokens on kept ones' places
+    near = near < 0 ? 0 : (near > q1 - q0 ? q1 - q0 : near);
     int32_t stay = 0;
     if (x.keep > 0) {
       // of its ties, in order, those that are still wanted
@@ -543,12 +610,10 @@ __global__ __launch_bounds__(kThreads) void k_kv_evict_lists(KvEvictArgs a) {
   }
   if (p.part == 0 && tid == 0) state_of(a, p.row)->moving = moving;
 
-  const int32_t r0 = p.begin(a, x, p.part), r1 = p.begin(a, x, p.part + 1);
   const int32_t run = ((r1 - r0 + kWaves - 1) / kWaves + 63) & ~63;
   const int32_t w0 = r0 + wave * run < r1 ? r0 + wave * run : r1, w1 = w0 + run < r1 ? w0 + run : r1;
-  auto key_of = [&](int32_t i) { return x.key(a, i); };
   int32_t ties = 0, all;
-  if (x.keep > 0)
+  if (x.keep > 0 && s_part[p.part][2] + s_part[p.part][3] > 0)
     for (int32_t i = w0 + lane; i < w1; i += 64) ties += key_of(i) == border;
   ties0 += __builtin_amdgcn_readfirstlane(sum_before(ties, s_waves, all));
   int32_t m = 0, g = 0;
@@ -588,11 +653,23 @@ __global__ __launch_bounds__(256) void k_kv_evict_move(KvEvictArgs a) {
   }
 }
 
+// The last tokens: a part every parts-th chunk where old and new places do not overlap, else the first
+// part all of them, in order
 template <int D>
 __global__ __launch_bounds__(kThreads) void k_kv_evict_last(KvEvictArgs a) {
-  const Row x(a, blockIdx.x);
-  if (!x.over) return;
-  move_last<D>(a, x, a.kept ? a.kept + (int64_t)blockIdx.x * a.budget : nullptr);
+  const Parts p(a, blockIdx.x);
+  const Row x(a, p.row);
+  const bool overlap = x.n - x.budget < x.last;
+  if (!x.over || (overlap && p.part > 0)) return;
+  int32_t* const kept = a.kept ? a.kept + (int64_t)p.row * a.budget : nullptr;
+  const int l = threadIdx.x % kRowLanes;
+  for (int64_t j0 = (int64_t)p.part * kChunk; j0 < x.last; j0 += (int64_t)(overlap ? 1 : a.parts) * kChunk) {
+    Moving<D> h[kHeld];
+    read_last<D>(a, x, kept, (int32_t)j0, h);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) h[i].write(a, l);
+  }
 }
 
 // The lengths, where they are written over those that the workgroups read
@@ -624,7 +701,8 @@ hipError_t evict(KvEvictArgs a, hipStream_t s) {
   hipLaunchKernelGGL((k_kv_evict_move<D>), dim3((unsigned)(m.rows * m.parts)), dim3(256), 0, s, m);
   e = hipGetLastError();
   if (e != hipSuccess || a.last == 0) return e;
-  hipLaunchKernelGGL((k_kv_evict_last<D>), rows, threads, 0, s, a);
+  m.parts = a.last_parts;
+  hipLaunchKernelGGL((k_kv_evict_last<D>), dim3((unsigned)(m.rows * m.parts)), threads, 0, s, m);
   return hipGetLastError();
 }
 
@@ -667,6 +745,8 @@ hipError_t launch_kv_evict(KvEvictArgs a, int32_t D, const KvEvictPlan& p, int64
   // 64 rows a workgroup and turn
   const int64_t turns = (a.budget + 63) / 64, most = 2048 / a.rows + 1;
   a.move_parts = (int32_t)(turns < most ? turns : most);
+  const int64_t chunks = (a.last + kChunk - 1) / kChunk;
+  a.last_parts = (int32_t)(chunks < most ? chunks : most);
   const hipError_t e = D == 64 ? evict<64>(a, s) : (D == 128 ? evict<128>(a, s) : evict<256>(a, s));
   if (e != hipSuccess || a.lengths) return e;
   hipLaunchKernelGGL(k_kv_lengths, dim3((unsigned)((a.pages.batch + 255) / 256)), dim3(256), 0, s, a);
