@@ -164,15 +164,21 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return x & 0x80000000u ? ~x : x | 0x80000000u;
 }
 
+// Sum over the lanes up to this one: within rows of 16, then the rows before
+__device__ __forceinline__ int32_t sum_upto(int32_t x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);   // the lane 1, 2, 4, 8 before in the row
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);   // lane 15 (47) to the row after
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);   // lane 31 to the upper half
+  return x;
+}
+
 // Sum over the threads before this one, and over all (every thread calls it)
 __device__ __forceinline__ int32_t sum_before(int32_t x, int32_t* s_waves, int32_t& all) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int32_t upto = x;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const int32_t y = __shfl_up(upto, off);
-    if (lane >= off) upto += y;
-  }
+  const int32_t upto = sum_upto(x);
   __syncthreads();                                 // s_waves of the call before is read
   if (lane == 63) s_waves[wave] = upto;
   __syncthreads();
@@ -336,20 +342,47 @@ __device__ __forceinline__ void read_last(const KvEvictArgs& a, const Row& x, in
   }
 }
 
+// Movers stand behind every free place: nothing that is read here is written
 template <int D>
-__global__ __launch_bounds__(kThreads) void k_kv_evict(KvEvictArgs a) {
-  extern __shared__ uint32_t s_keys[];
-  __shared__ int32_t s_hist[kBins];                // and the lists, where they are short
-  __shared__ int32_t s_waves[kWaves];
-  __shared__ int32_t s_found[3];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const Row x(a, blockIdx.x);
-  if (!x.over) {
-    keep_places(a, x, blockIdx.x, tid, kThreads);
-    return;
+__device__ __forceinline__ void move_listed(const KvEvictArgs& a, const Row& x, int32_t* kept, const int32_t* from,
+                                            const int32_t* to, int32_t moving) {
+  const int row = threadIdx.x / kRowLanes, l = threadIdx.x % kRowLanes;
+  for (int32_t i0 = row; i0 < moving; i0 += 2 * kRows) {
+    Moving<D> m[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int32_t i = i0 + e * kRows;
+      m[e].to = nullptr;
+      if (i < moving) m[e].read(a, x, kept, from[i], to[i], l);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) m[e].write(a, l);
   }
+}
+
+// The last tokens, their first chunk read already
+template <int D>
+__device__ __forceinline__ void move_last(const KvEvictArgs& a, const Row& x, int32_t* kept, Moving<D> (&tail)[kHeld]) {
+  const int l = threadIdx.x % kRowLanes;
+  __syncthreads();                                 // the movers are read
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) tail[i].write(a, l);
+  for (int32_t j0 = kChunk; j0 < x.last; j0 += kChunk) {
+    read_last<D>(a, x, kept, j0, tail);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) tail[i].write(a, l);
+  }
+}
+
+// A whole row of any length: its keys in LDS if there are at most lds_keys, else read again and again.
+// s_hist [kBins]: the histograms, and the lists, where they are short
+template <int D>
+__device__ __forceinline__ void evict_row(const KvEvictArgs& a, const Row& x, uint32_t* s_keys, int32_t lds_keys, int32_t* s_hist,
+                                          int32_t* s_waves, int32_t* s_found) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   int32_t* const kept = a.kept ? a.kept + (int64_t)blockIdx.x * a.budget : nullptr;
-  const bool in_lds = x.rated <= a.lds_keys;
+  const bool in_lds = x.rated <= lds_keys;
   auto key_of = [&](int32_t i) { return in_lds ? s_keys[i] : x.key(a, i); };
   for_keys<true>(a, x, 0, x.rated, tid, kThreads, [&](int32_t i, uint32_t k) {
     if (in_lds) s_keys[i] = k;
@@ -397,33 +430,160 @@ __global__ __launch_bounds__(kThreads) void k_kv_evict(KvEvictArgs a) {
       if (gap) to[j] = t;
     });
     __syncthreads();
-    // movers stand behind every free place: nothing that is read here is written
-    const int row = tid / kRowLanes, l = tid % kRowLanes;
-    for (int32_t i0 = row; i0 < moving; i0 += 2 * kRows) {
-      Moving<D> m[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int32_t i = i0 + e * kRows;
-        m[e].to = nullptr;
-        if (i < moving) m[e].read(a, x, kept, from[i], to[i], l);
-      }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) m[e].write(a, l);
-    }
+    move_listed<D>(a, x, kept, from, to, moving);
   };
   if (moving <= kBins / 2) lists(s_hist, s_hist + kBins / 2);
   else lists(a.lists + (int64_t)blockIdx.x * 2 * a.budget, a.lists + (int64_t)blockIdx.x * 2 * a.budget + a.budget);
+  move_last<D>(a, x, kept, tail);
+}
 
-  const int l = tid % kRowLanes;
-  __syncthreads();                                 // the movers are read
+// A whole row of up to kThreads * KEYS rated tokens, whose keys stay in registers: each wave has a run of
+// tokens, 64 at a time.  (Rows that the bound did not announce are longer: evict_row.)
+template <int D, int KEYS>
+__global__ __launch_bounds__(kThreads) void k_kv_evict_held(KvEvictArgs a) {
+  __shared__ int32_t s_hist[3][kBins];             // and the lists, where they are short
+  __shared__ int32_t s_waves[2][kWaves], s_scan[3][kWaves];
+  __shared__ int32_t s_found[3][3];
+  constexpr int kListed = 3 * kBins / 2;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const Row x(a, blockIdx.x);
+  if (!x.over) {
+    keep_places(a, x, blockIdx.x, tid, kThreads);
+    return;
+  }
+  if (x.rated > KEYS * kThreads) {
+    evict_row<D>(a, x, nullptr, 0, s_hist[0], s_waves[0], s_found[0]);
+    return;
+  }
+  int32_t* const kept = a.kept ? a.kept + (int64_t)blockIdx.x * a.budget : nullptr;
+  const int32_t run = ((x.rated + kWaves - 1) / kWaves + 63) & ~63;
+  const int32_t r0 = wave * run + lane, end = wave * run + run < x.rated ? wave * run + run : x.rated;
+  auto have = [&](int e) { return r0 + 64 * e < end; };
+  uint32_t key[KEYS];
+  const bool copy = a.weights_out && a.weights_out != a.weights;
+  constexpr int N = KEYS < 8 ? KEYS : 8;           // tokens whose loads are side by side
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i) tail[i].write(a, l);
-  for (int32_t j0 = kChunk; j0 < x.last; j0 += kChunk) {
-    read_last<D>(a, x, kept, j0, tail);
+  for (int e0 = 0; e0 < KEYS; e0 += N) {
+    int64_t at[N];
+    float w[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const int32_t t = x.first + r0 + 64 * (e0 + e);
+      const int64_t page = have(e0 + e) ? x.pages.of(t) : -1;
+      at[e] = page < 0 ? -1 : x.pages.weight_at(page, x.kh, t);
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e) w[e] = at[e] < 0 ? -__builtin_inff() : a.weights[at[e]];
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      if (copy && at[e] >= 0 && x.first + r0 + 64 * (e0 + e) < x.behind) a.weights_out[at[e]] = w[e];
+      key[e0 + e] = weight_key(w[e]);
+    }
+  }
+  // the last tokens' first chunk, on its way while the others are chosen
+  Moving<D> tail[kHeld];
+  read_last<D>(a, x, kept, 0, tail);
+  keep_places(a, x, blockIdx.x, tid, kThreads);
+  for (int i = tid; i < 3 * kBins; i += kThreads) s_hist[0][i] = 0;
+  __syncthreads();
+
+  // the smallest kept key, and how many tokens of it are kept
+  uint32_t border = 0;
+  int32_t wanted = x.keep, equal = 0;
+  if (x.keep > 0) {
+#pragma unroll
+    for (int pass = 0; pass < 3; ++pass) {
+      const uint32_t shift = kDigits[pass], mask = pass < 2 ? kBins - 1 : (kBins >> 1) - 1, above = shift + (pass < 2 ? 11 : 10);
+#pragma unroll
+      for (int e = 0; e < KEYS; ++e)
+        if (have(e) && (pass == 0 || key[e] >> above == border >> above)) atomicAdd(&s_hist[pass][(key[e] >> shift) & mask], 1);
+      __syncthreads();
+      // bins from the largest digit on, two a thread
+      const int32_t lo = s_hist[pass][kBins - 2 - 2 * tid], hi = s_hist[pass][kBins - 1 - 2 * tid];
+      const int32_t upto = sum_upto(hi + lo);
+      if (lane == 63) s_scan[pass][wave] = upto;
+      __syncthreads();
+      int32_t before = upto - hi - lo;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) before += w < wave ? s_scan[pass][w] : 0;
+      if (before < wanted && wanted <= before + hi + lo) {
+        const bool upper = wanted <= before + hi;
+        s_found[pass][0] = kBins - 1 - 2 * tid - (upper ? 0 : 1);
+        s_found[pass][1] = wanted - before - (upper ? 0 : hi);
+        s_found[pass][2] = upper ? hi : lo;
+      }
+      __syncthreads();
+      border |= (uint32_t)s_found[pass][0] << shift;
+      wanted = s_found[pass][1];
+      equal = s_found[pass][2];
+    }
+  }
+
+  // tokens of the border's key before this wave's run
+  int32_t ties = 0;
+  if (x.keep > 0 && equal > wanted) {
+    int32_t own = 0;
+#pragma unroll
+    for (int e = 0; e < KEYS; ++e) own += __builtin_popcountll(__builtin_amdgcn_ballot_w64(have(e) && key[e] == border));
+    if (lane == 0) s_waves[0][wave] = own;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) tail[i].write(a, l);
+    for (int w = 0; w < kWaves; ++w) ties += w < wave ? s_waves[0][w] : 0;
   }
+  const uint64_t below = (1ull << lane) - 1;
+  uint64_t mv[KEYS], gp[KEYS];                     // lanes whose token moves, or whose place is free
+  int32_t movers = 0, gaps = 0;
+#pragma unroll
+  for (int e = 0; e < KEYS; ++e) {
+    const bool tie = have(e) && x.keep > 0 && key[e] == border;
+    const uint64_t tie_lanes = __builtin_amdgcn_ballot_w64(tie);
+    const bool stays = have(e) && x.keep > 0 &&
+                       (key[e] > border || (tie && ties + __builtin_popcountll(tie_lanes & below) < wanted));
+    ties += __builtin_popcountll(tie_lanes);
+    const int32_t t = x.first + r0 + 64 * e;
+    mv[e] = __builtin_amdgcn_ballot_w64(stays && t >= x.behind);
+    gp[e] = __builtin_amdgcn_ballot_w64(have(e) && !stays && t < x.behind);
+    movers += __builtin_popcountll(mv[e]);
+    gaps += __builtin_popcountll(gp[e]);
+  }
+  // both are at most kThreads KEYS < 2^16
+  if (lane == 0) s_waves[1][wave] = movers << 16 | gaps;
+  __syncthreads();
+  uint32_t before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    before += w < wave ? (uint32_t)s_waves[1][w] : 0;
+    all += (uint32_t)s_waves[1][w];
+  }
+  movers = (int32_t)(before >> 16);
+  gaps = (int32_t)(before & 0xFFFF);
+  const int32_t moving = (int32_t)(all >> 16);
+  auto lists = [&](int32_t* from, int32_t* to) {
+#pragma unroll
+    for (int e = 0; e < KEYS; ++e) {
+      const int32_t t = x.first + r0 + 64 * e;
+      if (mv[e] >> lane & 1) from[movers + __builtin_popcountll(mv[e] & below)] = t;
+      if (gp[e] >> lane & 1) to[gaps + __builtin_popcountll(gp[e] & below)] = t;
+      movers += __builtin_popcountll(mv[e]);
+      gaps += __builtin_popcountll(gp[e]);
+    }
+    __syncthreads();
+    move_listed<D>(a, x, kept, from, to, moving);
+  };
+  if (moving <= kListed) lists(s_hist[0], s_hist[0] + kListed);
+  else lists(a.lists + (int64_t)blockIdx.x * 2 * a.budget, a.lists + (int64_t)blockIdx.x * 2 * a.budget + a.budget);
+  move_last<D>(a, x, kept, tail);
+}
+
+template <int D>
+__global__ __launch_bounds__(kThreads) void k_kv_evict(KvEvictArgs a) {
+  extern __shared__ uint32_t s_keys[];
+  __shared__ int32_t s_hist[kBins];
+  __shared__ int32_t s_waves[kWaves];
+  __shared__ int32_t s_found[3];
+  const Row x(a, blockIdx.x);
+  if (x.over) evict_row<D>(a, x, s_keys, a.lds_keys, s_hist, s_waves, s_found);
+  else keep_places(a, x, blockIdx.x, threadIdx.x, kThreads);
 }
 
 // The same in parts: row blockIdx / parts, part blockIdx % parts, of equal runs of the row's rated
@@ -683,6 +843,11 @@ __global__ __launch_bounds__(256) void k_kv_lengths(KvEvictArgs a) {
 template <int D>
 hipError_t evict(KvEvictArgs a, hipStream_t s) {
   const dim3 rows((unsigned)a.rows), threads(kThreads);
+  if (a.parts == 0 && a.lds_keys > 0 && a.lds_keys <= 16 * kThreads) {
+    if (a.lds_keys <= 4 * kThreads) hipLaunchKernelGGL((k_kv_evict_held<D, 4>), rows, threads, 0, s, a);
+    else hipLaunchKernelGGL((k_kv_evict_held<D, 16>), rows, threads, 0, s, a);
+    return hipGetLastError();
+  }
   if (a.parts == 0) {
     const hipError_t e = lds_limit_once<k_kv_evict<D>>(kKvEvictMostKeys * (int)sizeof(uint32_t));
     if (e != hipSuccess) return e;
