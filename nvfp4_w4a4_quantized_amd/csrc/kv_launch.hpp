@@ -64,7 +64,6 @@ struct KvAcceptArgs {
 };
 hipError_t launch_kv_accept(const KvAcceptArgs& a, int32_t D, hipStream_t s);
 
-constexpr int kKvEvictMostKeys = 36864;            // that LDS holds beside the histogram
 struct KvEvictArgs {
   uint8_t* cache;
   KvPages pages;
@@ -75,22 +74,20 @@ struct KvEvictArgs {
   int32_t* kept;               // optional [batch][n_kv_heads][budget]
   int32_t* kv_len_out;
   int32_t* lists;              // [rows][2][budget]: what moves, and where to (workspace)
-  void* states;                // [2][rows] and, below, what the parts count (workspace)
-  void* counts;
+  void* counts;                // of the rows, and of their parts (workspace)
   // the plan
   int32_t rows;                // batch * n_kv_heads
-  int32_t lds_keys;            // keys that the launch's LDS holds
   int32_t lengths;             // whether the kernels write the lengths
   int32_t parts;               // of a row; 0: a workgroup does a whole one
   int32_t move_parts, last_parts;   // for what moves
 };
-constexpr int kKvEvictParts = 512;                 // of all rows
 constexpr int kKvEvictMostParts = 64;              // of a row
-constexpr int kKvEvictPartBytes = 24832;           // that a part counts
+constexpr int kKvEvictRowBytes = 20736;            // that a row's parts count
+constexpr int kKvEvictPartBytes = 8448;            // and each of them
 struct KvEvictPlan {
   int32_t parts;
-  int64_t states_at, counts_at;   // byte offsets in the workspace
-  int64_t workspace;              // bytes
+  int64_t counts_at;           // byte offset in the workspace
+  int64_t workspace;           // bytes
 };
 KvEvictPlan kv_evict_plan(int32_t batch, int32_t n_kv_heads, int64_t budget, int64_t max_kv_len);
 hipError_t launch_kv_evict(KvEvictArgs a, int32_t D, const KvEvictPlan& p, int64_t max_kv_len, void* workspace, hipStream_t s);

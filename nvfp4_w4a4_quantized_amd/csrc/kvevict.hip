@@ -212,12 +212,12 @@ struct Row {
   }
 };
 
-// Calls f(i, key of rated token i) for i = begin + thread, + count, ... below end, four tokens' loads side
+// Calls f(i, key of rated token i) for i = begin + thread, + count, ... below end, eight tokens' loads side
 // by side; COPY: and gives the weights of the tokens that may stay where they are to weights_out
 template <bool COPY, typename F>
 __device__ __forceinline__ void for_keys(const KvEvictArgs& a, const Row& x, int32_t begin, int32_t end, int32_t thread,
                                          int32_t count, F f) {
-  constexpr int N = 4;
+  constexpr int N = 8;
   const bool copy = COPY && a.weights_out && a.weights_out != a.weights;
   for (int32_t i0 = begin + thread; i0 < end; i0 += N * count) {
     int64_t at[N];
@@ -347,16 +347,16 @@ template <int D>
 __device__ __forceinline__ void move_listed(const KvEvictArgs& a, const Row& x, int32_t* kept, const int32_t* from,
                                             const int32_t* to, int32_t moving) {
   const int row = threadIdx.x / kRowLanes, l = threadIdx.x % kRowLanes;
-  for (int32_t i0 = row; i0 < moving; i0 += 2 * kRows) {
-    Moving<D> m[2];
+  for (int32_t i0 = row; i0 < moving; i0 += 3 * kRows) {
+    Moving<D> m[3];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+    for (int e = 0; e < 3; ++e) {
       const int32_t i = i0 + e * kRows;
       m[e].to = nullptr;
       if (i < moving) m[e].read(a, x, kept, from[i], to[i], l);
     }
 #pragma unroll
-    for (int e = 0; e < 2; ++e) m[e].write(a, l);
+    for (int e = 0; e < 3; ++e) m[e].write(a, l);
   }
 }
 
@@ -375,18 +375,14 @@ __device__ __forceinline__ void move_last(const KvEvictArgs& a, const Row& x, in
   }
 }
 
-// A whole row of any length: its keys in LDS if there are at most lds_keys, else read again and again.
-// s_hist [kBins]: the histograms, and the lists, where they are short
+// A whole row of any length, longer than the bound announced: its keys are read again and again.
+// s_hist [kBins]: the histograms
 template <int D>
-__device__ __forceinline__ void evict_row(const KvEvictArgs& a, const Row& x, uint32_t* s_keys, int32_t lds_keys, int32_t* s_hist,
-                                          int32_t* s_waves, int32_t* s_found) {
+__device__ __forceinline__ void evict_row(const KvEvictArgs& a, const Row& x, int32_t* s_hist, int32_t* s_waves, int32_t* s_found) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   int32_t* const kept = a.kept ? a.kept + (int64_t)blockIdx.x * a.budget : nullptr;
-  const bool in_lds = x.rated <= lds_keys;
-  auto key_of = [&](int32_t i) { return in_lds ? s_keys[i] : x.key(a, i); };
-  for_keys<true>(a, x, 0, x.rated, tid, kThreads, [&](int32_t i, uint32_t k) {
-    if (in_lds) s_keys[i] = k;
-  });
+  auto key_of = [&](int32_t i) { return x.key(a, i); };
+  for_keys<true>(a, x, 0, x.rated, tid, kThreads, [](int32_t, uint32_t) {});
   // the last tokens' first chunk, on its way while the others are chosen
   Moving<D> tail[kHeld];
   read_last<D>(a, x, kept, 0, tail);
@@ -424,16 +420,14 @@ __device__ __forceinline__ void evict_row(const KvEvictArgs& a, const Row& x, ui
   walk(x, r0, r1, border, wanted, ties0, key_of, movers, gaps, [](int32_t, bool, int32_t, bool, int32_t) {});
   movers = __builtin_amdgcn_readfirstlane(sum_before(lane == 0 ? movers : 0, s_waves, moving));
   gaps = __builtin_amdgcn_readfirstlane(sum_before(lane == 0 ? gaps : 0, s_waves, all));
-  auto lists = [&](int32_t* from, int32_t* to) {
-    walk(x, r0, r1, border, wanted, ties0, key_of, movers, gaps, [&](int32_t t, bool moves, int32_t i, bool gap, int32_t j) {
-      if (moves) from[i] = t;
-      if (gap) to[j] = t;
-    });
-    __syncthreads();
-    move_listed<D>(a, x, kept, from, to, moving);
-  };
-  if (moving <= kBins / 2) lists(s_hist, s_hist + kBins / 2);
-  else lists(a.lists + (int64_t)blockIdx.x * 2 * a.budget, a.lists + (int64_t)blockIdx.x * 2 * a.budget + a.budget);
+  int32_t* const from = a.lists + (int64_t)blockIdx.x * 2 * a.budget;
+  int32_t* const to = from + a.budget;
+  walk(x, r0, r1, border, wanted, ties0, key_of, movers, gaps, [&](int32_t t, bool moves, int32_t i, bool gap, int32_t j) {
+    if (moves) from[i] = t;
+    if (gap) to[j] = t;
+  });
+  __syncthreads();
+  move_listed<D>(a, x, kept, from, to, moving);
   move_last<D>(a, x, kept, tail);
 }
 
@@ -452,7 +446,7 @@ __global__ __launch_bounds__(kThreads) void k_kv_evict_held(KvEvictArgs a) {
     return;
   }
   if (x.rated > KEYS * kThreads) {
-    evict_row<D>(a, x, nullptr, 0, s_hist[0], s_waves[0], s_found[0]);
+    evict_row<D>(a, x, s_hist[0], s_waves[0], s_found[0]);
     return;
   }
   int32_t* const kept = a.kept ? a.kept + (int64_t)blockIdx.x * a.budget : nullptr;
@@ -575,64 +569,43 @@ __global__ __launch_bounds__(kThreads) void k_kv_evict_held(KvEvictArgs a) {
   move_last<D>(a, x, kept, tail);
 }
 
-template <int D>
-__global__ __launch_bounds__(kThreads) void k_kv_evict(KvEvictArgs a) {
-  extern __shared__ uint32_t s_keys[];
-  __shared__ int32_t s_hist[kBins];
-  __shared__ int32_t s_waves[kWaves];
-  __shared__ int32_t s_found[3];
-  const Row x(a, blockIdx.x);
-  if (x.over) evict_row<D>(a, x, s_keys, a.lds_keys, s_hist, s_waves, s_found);
-  else keep_places(a, x, blockIdx.x, threadIdx.x, kThreads);
-}
-
-// The same in parts: row blockIdx / parts, part blockIdx % parts, of equal runs of the row's rated
-// tokens.  A part leaves its histograms, which the launch after sums up.
+// Longer rows in parts: row blockIdx / parts, part blockIdx % parts, of equal runs of the row's rated
+// tokens.  Parts add their histograms up; each pass over the keys is a launch.
 struct Parts {
-  int32_t row, part, r0, r1;
+  int32_t row, part;
   __device__ __forceinline__ Parts(const KvEvictArgs& a, int32_t block) : row(block / a.parts), part(block % a.parts) {}
-  __device__ __forceinline__ int32_t size(const KvEvictArgs& a, const Row& x) const {
-    return ((x.rated + a.parts - 1) / a.parts + kThreads - 1) / kThreads * kThreads;
-  }
   __device__ __forceinline__ int32_t begin(const KvEvictArgs& a, const Row& x, int32_t p) const {
-    const int64_t at = (int64_t)p * size(a, x);
+    const int32_t size = ((x.rated + a.parts - 1) / a.parts + kThreads - 1) / kThreads * kThreads;
+    const int64_t at = (int64_t)p * size;
     return at < x.rated ? (int32_t)at : x.rated;
   }
 };
-// what a part leaves: two histograms, the third for the tokens whose places are kept ones' and for the
-// others, and how many of either have larger first two digits
+struct RowCounts {
+  int32_t digit[2][kBins], last[kBins / 2];        // the histograms
+  // after each launch: the border's digits so far, the tokens wanted of those that have them
+  struct {
+    uint32_t border;
+    int32_t wanted;
+  } found[2];
+  int32_t moving, pad[3];
+};
+// of a part's tokens on kept places (0) and behind them (1): those whose key is at least the border's first two
+// digits and third digit i
 struct PartCounts {
-  int32_t digit[2][kBins];
-  int32_t last[2][kBins / 2];
-  int32_t larger[2];
+  int32_t least[2][kBins / 2 + 4];
 };
-struct RowState {
-  uint32_t border;
-  int32_t wanted, moving, pad;
-};
-static_assert(sizeof(PartCounts) <= kKvEvictPartBytes && sizeof(RowState) == 16, "kv_launch.hpp");
-__device__ __forceinline__ PartCounts* counts_of(const KvEvictArgs& a, int32_t row, int32_t part) {
-  return reinterpret_cast<PartCounts*>(static_cast<uint8_t*>(a.counts) + ((int64_t)row * a.parts + part) * kKvEvictPartBytes);
+static_assert(sizeof(RowCounts) <= kKvEvictRowBytes && sizeof(PartCounts) <= kKvEvictPartBytes, "kv_launch.hpp");
+__device__ __forceinline__ RowCounts* row_counts(const KvEvictArgs& a, int32_t row) {
+  return reinterpret_cast<RowCounts*>(static_cast<uint8_t*>(a.counts) + (int64_t)row * kKvEvictRowBytes);
 }
-__device__ __forceinline__ RowState* state_of(const KvEvictArgs& a, int32_t row) {
-  return reinterpret_cast<RowState*>(a.states) + row;
+__device__ __forceinline__ PartCounts* part_counts(const KvEvictArgs& a, int32_t row, int32_t part) {
+  return reinterpret_cast<PartCounts*>(static_cast<uint8_t*>(a.counts) + (int64_t)a.rows * kKvEvictRowBytes +
+                                       ((int64_t)row * a.parts + part) * kKvEvictPartBytes);
 }
 
-// Sums f(counts of a part) over a row's parts, eight loads side by side
-template <typename F>
-__device__ __forceinline__ void sum_parts(const KvEvictArgs& a, int32_t row, F f, int32_t& x, int32_t& y) {
-  constexpr int N = 8;
-  for (int32_t q0 = 0; q0 < a.parts; q0 += N) {
-    int2 v[N];
-#pragma unroll
-    for (int e = 0; e < N; ++e) v[e] = f(counts_of(a, row, q0 + e < a.parts ? q0 + e : q0));
-#pragma unroll
-    for (int e = 0; e < N; ++e)
-      if (q0 + e < a.parts) {
-        x += v[e].x;
-        y += v[e].y;
-      }
-  }
+__global__ __launch_bounds__(256) void k_kv_evict_clear(KvEvictArgs a) {
+  u32x4* const p = reinterpret_cast<u32x4*>(row_counts(a, blockIdx.x));
+  for (int i = threadIdx.x; i < kKvEvictRowBytes / 16; i += 256) p[i] = u32x4{0, 0, 0, 0};
 }
 
 // Histogram PASS of a part's keys, those whose digits before are the border's
@@ -641,38 +614,34 @@ __global__ __launch_bounds__(kThreads) void k_kv_evict_digits(KvEvictArgs a) {
   __shared__ int32_t s_hist[kBins];
   __shared__ int32_t s_waves[kWaves];
   __shared__ int32_t s_found[3];
-  __shared__ int32_t s_larger[2];
+  __shared__ int32_t s_larger[2], s_near;
   const int tid = threadIdx.x;
   const Parts p(a, blockIdx.x);
   const Row x(a, p.row);
   if constexpr (PASS == 0) keep_places(a, x, p.row, p.part * kThreads + tid, a.parts * kThreads);
   if (!x.over || (PASS > 0 && x.keep == 0)) return;   // the first one copies weights
+  RowCounts* const c = row_counts(a, p.row);
+  for (int i = tid; i < kBins; i += kThreads) s_hist[i] = 0;
+  if (tid < 2) s_larger[tid] = 0;
   uint32_t border = 0;
   if constexpr (PASS > 0) {
     int32_t wanted = x.keep;
     if constexpr (PASS == 2) {
-      border = state_of(a, p.row)->border;
-      wanted = state_of(a, p.row)->wanted;
+      border = c->found[0].border;
+      wanted = c->found[0].wanted;
     }
-    int32_t hi = 0, lo = 0;
-    sum_parts(a, p.row, [&](const PartCounts* c) {
-      return *reinterpret_cast<const int2*>(&c->digit[PASS - 1][kBins - 2 - 2 * tid]);
-    }, lo, hi);
-    find_digit(hi, lo, wanted, s_waves, s_found);
+    const int2 bins = *reinterpret_cast<const int2*>(&c->digit[PASS - 1][kBins - 2 - 2 * tid]);
+    find_digit(bins.y, bins.x, wanted, s_waves, s_found);
     border |= (uint32_t)s_found[0] << kDigits[PASS - 1];
-    // the part that is last to begin its row's next launch reads what any part writes here
     if (p.part == 0 && tid == 0) {
-      RowState* const st = PASS == 1 ? state_of(a, p.row) : state_of(a, p.row) + a.rows;
-      st->border = border;
-      st->wanted = s_found[1];
+      c->found[PASS - 1].border = border;
+      c->found[PASS - 1].wanted = s_found[1];
     }
   }
-  for (int i = tid; i < kBins; i += kThreads) s_hist[i] = 0;
-  if (tid < 2) s_larger[tid] = 0;
   __syncthreads();
   const int32_t r0 = p.begin(a, x, p.part), r1 = p.begin(a, x, p.part + 1);
   int32_t larger[2] = {0, 0};
-  auto count = [&](uint32_t k, int32_t i) {
+  for_keys<PASS == 0>(a, x, r0, r1, tid, kThreads, [&](int32_t i, uint32_t k) {
     if constexpr (PASS == 0) {
       atomicAdd(&s_hist[k >> 21], 1);
     } else if constexpr (PASS == 1) {
@@ -682,17 +651,31 @@ __global__ __launch_bounds__(kThreads) void k_kv_evict_digits(KvEvictArgs a) {
       if (k >> 10 == border >> 10) atomicAdd(&s_hist[behind * (kBins / 2) + (k & (kBins / 2 - 1))], 1);
       else if (k >> 10 > border >> 10) ++larger[behind];
     }
-  };
-  for_keys<PASS == 0>(a, x, r0, r1, tid, kThreads, [&](int32_t i, uint32_t k) { count(k, i); });
+  });
   if constexpr (PASS == 2) {
     if (larger[0]) atomicAdd(&s_larger[0], larger[0]);
     if (larger[1]) atomicAdd(&s_larger[1], larger[1]);
   }
   __syncthreads();
-  PartCounts* const c = counts_of(a, p.row, p.part);
-  int32_t* const out = PASS < 2 ? c->digit[PASS < 2 ? PASS : 0] : c->last[0];
-  for (int j = tid; j < kBins; j += kThreads) out[j] = s_hist[j];
-  if (PASS == 2 && tid < 2) c->larger[tid] = s_larger[tid];
+  if constexpr (PASS < 2) {
+    for (int i = tid; i < kBins; i += kThreads)
+      if (s_hist[i]) atomicAdd(&c->digit[PASS][i], s_hist[i]);
+  } else {
+    static_assert(kThreads == kBins / 2, "a thread per digit, and two digits of one half a thread");
+    const int32_t both = s_hist[tid] + s_hist[kBins / 2 + tid];
+    if (both) atomicAdd(&c->last[tid], both);
+    const int z = tid >> 9, at = kBins / 2 - 2 - 2 * (tid & 511);
+    const int32_t lo = s_hist[z * (kBins / 2) + at], hi = s_hist[z * (kBins / 2) + at + 1];
+    int32_t all;
+    int32_t before = sum_before(lo + hi, s_waves, all);
+    if (tid == kThreads / 2) s_near = before;
+    __syncthreads();
+    before += s_larger[z] - (z ? s_near : 0);
+    PartCounts* const out = part_counts(a, p.row, p.part);
+    out->least[z][at + 1] = before + hi;
+    out->least[z][at] = before + hi + lo;
+    if (at + 2 == kBins / 2) out->least[z][kBins / 2] = before;
+  }
 }
 
 // The lists
@@ -702,7 +685,7 @@ __global__ __launch_bounds__(kThreads) void k_kv_evict_lists(KvEvictArgs a) {
   __shared__ int32_t s_waves[kWaves];
   __shared__ int32_t s_found[3];
   __shared__ uint32_t s_keys[kPartKeys];
-  __shared__ int32_t s_part[kKvEvictMostParts][4];     // of each part: larger and equal keys, of kept places' tokens and others
+  __shared__ int32_t s_part[kKvEvictMostParts][4];     // of each part: larger and equal keys, on kept places and behind
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const Parts p(a, blockIdx.x);
   const Row x(a, p.row);
@@ -711,42 +694,27 @@ __global__ __launch_bounds__(kThreads) void k_kv_evict_lists(KvEvictArgs a) {
   const bool in_lds = r1 - r0 <= kPartKeys;
   if (in_lds) for_keys<false>(a, x, r0, r1, tid, kThreads, [&](int32_t i, uint32_t k) { s_keys[i - r0] = k; });
   auto key_of = [&](int32_t i) { return in_lds ? s_keys[i - r0] : x.key(a, i); };
+  RowCounts* const c = row_counts(a, p.row);
   uint32_t border = 0;
   int32_t wanted = 0, ties0 = 0, movers = 0, gaps = 0;
   if (x.keep > 0) {
-    const RowState st = state_of(a, p.row)[a.rows];
-    int32_t hi = 0, lo = 0;
-    if (tid >= kBins / 4)                              // the third digit has half the bins
-#pragma unroll
-      for (int z = 0; z < 2; ++z)
-        sum_parts(a, p.row, [&](const PartCounts* c) {
-          return *reinterpret_cast<const int2*>(&c->last[z][kBins - 2 - 2 * tid]);
-        }, lo, hi);
-    find_digit(hi, lo, st.wanted, s_waves, s_found);
+    // the third digit has half the bins: threads from kBins / 4 on
+    int2 bins = {0, 0};
+    if (tid >= kBins / 4) bins = *reinterpret_cast<const int2*>(&c->last[kBins - 2 - 2 * tid]);
+    find_digit(bins.y, bins.x, c->found[1].wanted, s_waves, s_found);
     const int32_t digit = s_found[0];
-    border = st.border | (uint32_t)digit;
+    border = c->found[1].border | (uint32_t)digit;
     wanted = s_found[1];
-    for (int32_t q = wave; q < a.parts; q += kWaves) {
-      const PartCounts* const c = counts_of(a, p.row, q);
-#pragma unroll
-      for (int z = 0; z < 2; ++z) {
-        int32_t more = 0;
-#pragma unroll
-        for (int j = 0; j < kBins / 2; j += 64) {
-          const int32_t y = c->last[z][j + lane];
-          more += j + lane > digit ? y : 0;
-        }
-#pragma unroll
-        for (int off = 1; off < 64; off <<= 1) more += __shfl_xor(more, off);
-        if (lane == 0) {
-          s_part[q][z] = more + c->larger[z];
-          s_part[q][2 + z] = c->last[z][digit];
-        }
-      }
+    for (int32_t q = tid >> 1; q < a.parts; q += kThreads / 2) {
+      const int z = tid & 1;
+      const int32_t* const least = part_counts(a, p.row, q)->least[z];
+      const int32_t larger = least[digit + 1], from = least[digit];
+      s_part[q][z] = larger;
+      s_part[q][2 + z] = from - larger;
     }
   }
   __syncthreads();
-  // what stands before this part (and, for the last one's use, in all)
+  // what stands before this part, and in all
   int32_t moving = 0;
   for (int32_t q = 0, ties = 0; q < a.parts; ++q) {
     if (q == p.part) {
@@ -768,7 +736,7 @@ __global__ __launch_bounds__(kThreads) void k_kv_evict_lists(KvEvictArgs a) {
     }
     if (q < p.part) gaps += near - stay;
   }
-  if (p.part == 0 && tid == 0) state_of(a, p.row)->moving = moving;
+  if (p.part == 0 && tid == 0) c->moving = moving;
 
   const int32_t run = ((r1 - r0 + kWaves - 1) / kWaves + 63) & ~63;
   const int32_t w0 = r0 + wave * run < r1 ? r0 + wave * run : r1, w1 = w0 + run < r1 ? w0 + run : r1;
@@ -797,7 +765,7 @@ __global__ __launch_bounds__(256) void k_kv_evict_move(KvEvictArgs a) {
   int32_t* const kept = a.kept ? a.kept + (int64_t)p.row * a.budget : nullptr;
   const int32_t* const from = a.lists + (int64_t)p.row * 2 * a.budget;
   const int32_t* const to = from + a.budget;
-  const int32_t moving = state_of(a, p.row)->moving;
+  const int32_t moving = row_counts(a, p.row)->moving;
   const int row = threadIdx.x / kRowLanes, l = threadIdx.x % kRowLanes;
   constexpr int kSide = 256 / kRowLanes, kDeep = 4;
   for (int32_t i0 = p.part * kSide * kDeep; i0 < moving; i0 += a.parts * kSide * kDeep) {
@@ -841,20 +809,15 @@ __global__ __launch_bounds__(256) void k_kv_lengths(KvEvictArgs a) {
 }
 
 template <int D>
-hipError_t evict(KvEvictArgs a, hipStream_t s) {
+hipError_t evict(KvEvictArgs a, bool short_rows, hipStream_t s) {
   const dim3 rows((unsigned)a.rows), threads(kThreads);
-  if (a.parts == 0 && a.lds_keys > 0 && a.lds_keys <= 16 * kThreads) {
-    if (a.lds_keys <= 4 * kThreads) hipLaunchKernelGGL((k_kv_evict_held<D, 4>), rows, threads, 0, s, a);
+  if (a.parts == 0) {
+    if (short_rows) hipLaunchKernelGGL((k_kv_evict_held<D, 4>), rows, threads, 0, s, a);
     else hipLaunchKernelGGL((k_kv_evict_held<D, 16>), rows, threads, 0, s, a);
     return hipGetLastError();
   }
-  if (a.parts == 0) {
-    const hipError_t e = lds_limit_once<k_kv_evict<D>>(kKvEvictMostKeys * (int)sizeof(uint32_t));
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_kv_evict<D>), rows, threads, a.lds_keys * (int)sizeof(uint32_t), s, a);
-    return hipGetLastError();
-  }
   const dim3 parts((unsigned)(a.rows * a.parts));
+  hipLaunchKernelGGL(k_kv_evict_clear, rows, dim3(256), 0, s, a);
   hipLaunchKernelGGL((k_kv_evict_digits<0>), parts, threads, 0, s, a);
   hipLaunchKernelGGL((k_kv_evict_digits<1>), parts, threads, 0, s, a);
   hipLaunchKernelGGL((k_kv_evict_digits<2>), parts, threads, 0, s, a);
@@ -884,35 +847,29 @@ hipError_t launch_kv_accept(const KvAcceptArgs& a, int32_t D, hipStream_t s) {
 KvEvictPlan kv_evict_plan(int32_t batch, int32_t n_kv_heads, int64_t budget, int64_t max_kv_len) {
   KvEvictPlan p{};
   const int64_t rows = (int64_t)batch * n_kv_heads;
-  const int64_t lists = (rows * 2 * budget * (int64_t)sizeof(int32_t) + 255) & ~255ll;
-  p.workspace = lists;
-  // Parts of 8192 tokens
-  const int64_t tokens = (max_kv_len + 8191) / 8192, most = kKvEvictParts / rows;
-  const int64_t parts = tokens < most ? tokens : most;
-  if (max_kv_len > kKvEvictMostKeys) {             // fewer rows need no more than more of them
-    if (parts > 1) p.parts = (int32_t)(parts < kKvEvictMostParts ? parts : kKvEvictMostParts);
-    p.states_at = lists;
-    p.counts_at = lists + kKvEvictParts * 2 * 16;
-    p.workspace = p.counts_at + (int64_t)kKvEvictParts * kKvEvictPartBytes;
-  }
+  p.counts_at = (rows * 2 * budget * (int64_t)sizeof(int32_t) + 255) & ~255ll;
+  p.workspace = p.counts_at;
+  // Parts of 8192 tokens, where a workgroup's registers do not hold a row's keys, and a launch takes them
+  const int64_t parts = (max_kv_len + 8191) / 8192;
+  p.parts = (int32_t)(parts < kKvEvictMostParts ? parts : kKvEvictMostParts);
+  if (max_kv_len <= 16 * kThreads || rows * p.parts > kv_most_blocks(kThreads)) p.parts = 0;
+  if (p.parts) p.workspace += rows * (kKvEvictRowBytes + (int64_t)p.parts * kKvEvictPartBytes);
   return p;
 }
 
 hipError_t launch_kv_evict(KvEvictArgs a, int32_t D, const KvEvictPlan& p, int64_t max_kv_len, void* workspace, hipStream_t s) {
-  const int64_t rated = max_kv_len - a.first - a.last;
   a.rows = a.pages.batch * a.pages.geom.n_kv_heads;
-  a.lds_keys = (int32_t)(rated < 0 || rated > kKvEvictMostKeys ? 0 : rated);
   a.lengths = a.kv_len_out != a.kv_len;
   a.parts = p.parts;
   a.lists = static_cast<int32_t*>(workspace);
-  a.states = static_cast<uint8_t*>(workspace) + p.states_at;
   a.counts = static_cast<uint8_t*>(workspace) + p.counts_at;
   // 64 rows a workgroup and turn
   const int64_t turns = (a.budget + 63) / 64, most = 2048 / a.rows + 1;
   a.move_parts = (int32_t)(turns < most ? turns : most);
   const int64_t chunks = (a.last + kChunk - 1) / kChunk;
   a.last_parts = (int32_t)(chunks < most ? chunks : most);
-  const hipError_t e = D == 64 ? evict<64>(a, s) : (D == 128 ? evict<128>(a, s) : evict<256>(a, s));
+  const bool short_rows = max_kv_len - a.first - a.last <= 4 * kThreads;
+  const hipError_t e = D == 64 ? evict<64>(a, short_rows, s) : (D == 128 ? evict<128>(a, short_rows, s) : evict<256>(a, short_rows, s));
   if (e != hipSuccess || a.lengths) return e;
   hipLaunchKernelGGL(k_kv_lengths, dim3((unsigned)((a.pages.batch + 255) / 256)), dim3(256), 0, s, a);
   return hipGetLastError();
