@@ -385,7 +385,8 @@ int32_t kv_attention_call(const void* q, int32_t dtype, int64_t ldq, int64_t T, 
     a.tree_words = (int32_t)tree->words;
   }
   const nvfp4::KvAttnPlan plan =
-      nvfp4::kv_attn_plan(in_type(dtype), T, batch, n_q_heads, n_kv_heads, head_dim, max_q_len, max_kv_len, window);
+      nvfp4::kv_attn_plan(in_type(dtype), T, batch, n_q_heads, n_kv_heads, head_dim, max_q_len, max_kv_len, window,
+                          tree != nullptr);
   if (plan.workspace > 0) {
     if (!workspace || workspace_bytes < plan.workspace)
       return fail(NVFP4_ERR_INVALID_ARG, "workspace of %lld bytes is too small: %lld needed",
@@ -802,8 +803,13 @@ int32_t nvfp4_kv_attention_workspace(int32_t dtype, int64_t T, int32_t batch, in
   const int32_t st = check_kv_attn_sizes(T, batch, n_q_heads, n_kv_heads, head_dim, max_q_len, max_kv_len);
   if (st) return st;
   // a window never needs more
-  *bytes_out = nvfp4::kv_attn_plan(in_type(dtype), T, batch, n_q_heads, n_kv_heads, head_dim, max_q_len, max_kv_len, 0)
-                   .workspace;
+  int64_t need = 0;
+  for (const bool tree : {false, true}) {
+    const int64_t w = nvfp4::kv_attn_plan(in_type(dtype), T, batch, n_q_heads, n_kv_heads, head_dim, max_q_len, max_kv_len, 0, tree)
+                          .workspace;
+    need = w > need ? w : need;
+  }
+  *bytes_out = need;
   return ok();
 }
 

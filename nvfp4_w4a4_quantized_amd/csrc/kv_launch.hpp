@@ -132,7 +132,7 @@ struct KvAttnPlan {
   int64_t workspace;           // bytes
 };
 KvAttnPlan kv_attn_plan(InType t, int64_t T, int32_t batch, int32_t n_q_heads, int32_t n_kv_heads, int32_t D,
-                        int64_t max_q_len, int64_t max_kv_len, int64_t window);
+                        int64_t max_q_len, int64_t max_kv_len, int64_t window, bool tree);
 hipError_t launch_kv_attn(KvAttnArgs a, const KvAttnPlan& p, InType t, int32_t D, hipStream_t s);
 
 // kvweights.hip: the attention weight of cached tokens
@@ -156,6 +156,7 @@ hipError_t launch_kv_join(const KvAttnArgs& a, InType t, int32_t D, hipStream_t 
 // kvprefill.hip: bf16, items of kv_prefill_cols() query columns, a workgroup of
 // kv_prefill_threads() each.
 int32_t kv_prefill_cols();
+int32_t kv_tree_cols(int32_t D);   // columns from which drafted trees go there, 128 at a time up to 128
 int32_t kv_prefill_threads();
 hipError_t launch_kv_prefill(const KvAttnArgs& a, int32_t D, hipStream_t s);
 

@@ -718,16 +718,17 @@ hipError_t launch_kv_join(const KvAttnArgs& a, InType t, int32_t D, hipStream_t 
 }
 
 KvAttnPlan kv_attn_plan(InType t, int64_t T, int32_t batch, int32_t n_q_heads, int32_t n_kv_heads, int32_t D,
-                        int64_t max_q_len, int64_t max_kv_len, int64_t window) {
+                        int64_t max_q_len, int64_t max_kv_len, int64_t window, bool tree) {
   KvAttnPlan p{};
   const int64_t cols = (max_q_len < T ? max_q_len : T) * (n_q_heads / n_kv_heads);
+  const int32_t least = tree ? kv_tree_cols(D) : kv_prefill_cols();
   // From one full tile of query columns on, decoding a key once for all of them pays.  This
   // kernel / kvprefill.hip, us: 1 x 16384 keys and 256 columns 64 / 53, 1024 columns 123 / 93; 8 x
   // 4096 and 256 columns 81 / 66, but 128 columns 56 / 58; 32 x 4096 and 256 columns 245 / 175, but 128
   // columns 127 / 146; head dimension 256, 1 x 16384, 512 columns 81 / 61; 64, 2 x 4096, 512 columns 44 / 35.
-  if (t == InType::BF16 && cols >= kv_prefill_cols()) {
+  if (t == InType::BF16 && cols >= least) {
     p.prefill = true;
-    p.tile_cols = kv_prefill_cols();
+    p.tile_cols = tree && cols <= 128 ? 128 : kv_prefill_cols();
     const int64_t pairs = (int64_t)batch * n_kv_heads, tiles = (cols + p.tile_cols - 1) / p.tile_cols;
     p.col_tiles = kv_planned_tiles(tiles, pairs, kv_prefill_threads());
     const int64_t items = pairs * p.col_tiles;

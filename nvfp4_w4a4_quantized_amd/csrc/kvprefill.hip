@@ -109,29 +109,35 @@ __device__ __forceinline__ void read_dwords(const uint8_t* p, uint32_t* d) {
 struct TileSpan {
   int32_t lo, begin, steps;
 };
-template <int D, bool TREE>
+template <int D, int COLS, bool TREE>
 __device__ __forceinline__ TileSpan tile_span(const KvAttnArgs& a, const SeqInfo& seq, int32_t tile, int group) {
-  const int32_t cols = seq.m * group, first = tile * kPrefillCols;
-  const Span s = span_of<TREE>(seq, first, first + kPrefillCols < cols ? first + kPrefillCols : cols, a.by_group, a.window);
+  const int32_t cols = seq.m * group, first = tile * COLS;
+  const Span s = span_of<TREE>(seq, first, first + COLS < cols ? first + COLS : cols, a.by_group, a.window);
   TileSpan t;
   t.lo = s.lo;
   t.begin = s.lo & ~15;
   t.steps = seq.n > 0 ? (s.hi - t.begin + kTok<D> - 1) / kTok<D> : 0;
   return t;
 }
+template <int COLS>
 __device__ __forceinline__ int32_t tiles_of(const SeqInfo& seq, int group) {
-  return (seq.m * group + kPrefillCols - 1) / kPrefillCols;
+  return (seq.m * group + COLS - 1) / COLS;
 }
+template <int COLS>
 __device__ __forceinline__ int32_t planned_tiles(const KvAttnArgs& a, const SeqInfo& seq, int group) {
-  const int32_t t = tiles_of(seq, group);
+  const int32_t t = tiles_of<COLS>(seq, group);
   return t < a.col_tiles ? t : a.col_tiles;
 }
 
 // SPLIT: workgroups have pieces of items instead of items (a template parameter: its
 // registers cost the other form 2 to 5 %)
-template <int D, bool SPLIT, bool TREE>
+// TG: groups of waves that have the same 256 / TG query columns and share the blocks of every tile, for
+// items of 128 columns (TG 2), whose results are joined in LDS.
+template <int D, bool SPLIT, bool TREE, int TG>
 __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs a) {
   constexpr bool PIPE = D <= 128;
+  static_assert(TG == 1 || (TG == 2 && PIPE), "a group has two blocks of a tile");
+  constexpr int COLS = kPrefillCols / TG, CW = kPrefillWaves / TG;
   constexpr int TOK = kTok<D>;
   constexpr int KD = D / 32;                       // dwords of codes a lane decodes, keys and values each
   constexpr int NB = D / 32;                       // 32-row blocks of O^T
@@ -153,7 +159,7 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
     b = pair / a.by_heads;
     kh = pair - b * hkv;
     seq = seq_info(a, b);
-    const int32_t tiles = tiles_of(seq, group);
+    const int32_t tiles = tiles_of<COLS>(seq, group);
     tile0 = (tiles < a.col_tiles ? tiles : a.col_tiles) - 1 - turn;
     if (tile0 < 0) return;
   } else {
@@ -163,8 +169,8 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
     float total = 0.0f;
     for (b = 0; b < a.batch; ++b) {
       seq = seqs.at(a, b);
-      const int32_t tiles = planned_tiles(a, seq, group);
-      for (int32_t t = lane; t < tiles; t += 64) total += (float)tile_span<D, TREE>(a, seq, t, group).steps;
+      const int32_t tiles = planned_tiles<COLS>(a, seq, group);
+      for (int32_t t = lane; t < tiles; t += 64) total += (float)tile_span<D, COLS, TREE>(a, seq, t, group).steps;
     }
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) total += __shfl_xor(total, off);
@@ -176,9 +182,9 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
     int32_t rest = (int32_t)blockIdx.x, tiles = 0, of_head = 0;
     for (b = 0; b < a.batch; ++b) {
       seq = seqs.at(a, b);
-      tiles = planned_tiles(a, seq, group);
+      tiles = planned_tiles<COLS>(a, seq, group);
       of_head = 0;
-      for (int32_t t = lane; t < tiles; t += 64) of_head += pieces_of(tile_span<D, TREE>(a, seq, t, group).steps);
+      for (int32_t t = lane; t < tiles; t += 64) of_head += pieces_of(tile_span<D, COLS, TREE>(a, seq, t, group).steps);
 #pragma unroll
       for (int off = 1; off < 64; off <<= 1) of_head += __shfl_xor(of_head, off);
       of_head = __builtin_amdgcn_readfirstlane(of_head);
@@ -193,7 +199,7 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
     rest -= kh * of_head;
     int32_t pieces = 1;
     for (int32_t t0 = 0;; t0 += 64) {
-      const int32_t own = t0 + lane < tiles ? pieces_of(tile_span<D, TREE>(a, seq, t0 + lane, group).steps) : 0;
+      const int32_t own = t0 + lane < tiles ? pieces_of(tile_span<D, COLS, TREE>(a, seq, t0 + lane, group).steps) : 0;
       int32_t upto = own;
 #pragma unroll
       for (int off = 1; off < 64; off <<= 1) {
@@ -210,16 +216,16 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
       }
       rest -= __builtin_amdgcn_readlane(upto, 63);
     }
-    const int32_t steps = tile_span<D, TREE>(a, seq, tile0, group).steps;
+    const int32_t steps = tile_span<D, COLS, TREE>(a, seq, tile0, group).steps;
     if (pieces > 1) {
       const int32_t q = (int32_t)((uint32_t)steps / (uint32_t)pieces), more = steps - q * pieces;
       s_first = rest * q + (rest < more ? rest : more);
       s_last = s_first + q + (rest < more);
     }
     if (threadIdx.x == 0) {
-      const int32_t fc = tile0 * kPrefillCols, left = seq.m * group - fc;
+      const int32_t fc = tile0 * COLS, left = seq.m * group - fc;
       ItemPieces* const p = static_cast<ItemPieces*>(a.pieces) + blockIdx.x;
-      p->cols = pieces > 1 && rest == 0 ? (left < kPrefillCols ? left : kPrefillCols) : 0;
+      p->cols = pieces > 1 && rest == 0 ? (left < COLS ? left : COLS) : 0;
       p->pieces = pieces;
       p->q0 = seq.q0;
       p->first_col = fc;
@@ -234,17 +240,18 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
   const int gran = D == 256 ? wave & 3 : wave;      // this wave's granule of a tile
 
   // tiles past the planned ones are done whole, with the first piece of one of those
-  for (int32_t tile = tile0; (int64_t)tile * kPrefillCols < cols; tile += a.col_tiles) {
+  for (int32_t tile = tile0; (int64_t)tile * COLS < cols; tile += a.col_tiles) {
     const bool whole = !SPLIT || s_last < 0 || tile != tile0;
     if (SPLIT && tile != tile0 && s_first > 0) break;
-    const int32_t col_first = tile * kPrefillCols;
-    const int32_t col_end = col_first + kPrefillCols < cols ? col_first + kPrefillCols : cols;
-    const TileSpan span = tile_span<D, TREE>(a, seq, tile, group);
+    const int32_t col_first = tile * COLS;
+    const int32_t col_end = col_first + COLS < cols ? col_first + COLS : cols;
+    const TileSpan span = tile_span<D, COLS, TREE>(a, seq, tile, group);
     const int32_t begin = whole ? span.begin : span.begin + s_first * TOK;
     const int32_t steps = whole ? span.steps : s_last - s_first;
 
     // this wave's columns (past the tile's end: its last one again, never written)
-    const int32_t col0 = col_first + 32 * wave;
+    const int cw = wave % CW, tg = wave / CW;
+    const int32_t col0 = col_first + 32 * cw;
     const int32_t w0 = col0 < col_end ? col0 : col_end - 1;
     const int32_t w1 = col0 + 32 < col_end ? col0 + 32 : col_end;
     const Span sp = span_of<TREE>(seq, w0, w1, a.by_group, a.window);
@@ -540,36 +547,65 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
           for (int e = 0; e < 8; ++e) pb[k][e] = (_Float16)0.0f;
 #pragma unroll
         for (int i = 0; i < KS; ++i) {
-          read_k(k_tile(0) + kbase, 0, i);
+          read_k(k_tile(0) + kbase, TG == 1 ? 0 : 2 * tg, i);
           score_piece(sa, i);
         }
-        // Past the last tile the decoder writes, from stale registers, what nothing reads unmasked.
-        // The next keys are written after the reads of the tile before them and are due after the
-        // second barrier, the next values after the second and due after the first.
-        for (int32_t s = 0; s < steps; ++s) {
-          const int32_t t0 = begin + s * TOK;
-          stage(k_tile(s), 1, v_tile(s + 1), 3, t0, sb, sa, pa, pb, nothing);
-          __syncthreads();
-          const uint32_t kw = fresh(k_tile(s + 1) + kwbase);
-          stage(k_tile(s), 2, v_tile(s), 0, t0 + 32, sa, sb, pb, pa, [&](int i) {
-            if (i < KD) decode_k(kw, i);
-          });
-          if (s + 2 < steps) load_k(s + 2, id_next);
-          stage(k_tile(s), 3, v_tile(s), 1, t0 + 64, sb, sa, pa, pb, nothing);
-          __syncthreads();
-          const uint32_t vw = fresh(v_tile(s + 1) + vwbase);
-          stage(k_tile(s + 1), 0, v_tile(s), 2, t0 + 96, sa, sb, pb, pa, [&](int i) {
-            if (i < KS / 2) decode_v(vw, i);
-          });
-          if (s + 2 < steps) {
-            load_v(s + 2, id_next);
-            id_next = page_of(s + 3);
+        if constexpr (TG == 1) {
+          // Past the last tile the decoder writes, from stale registers, what nothing reads unmasked.
+          // The next keys are written after the reads of the tile before them and are due after the
+          // second barrier, the next values after the second and due after the first.
+          for (int32_t s = 0; s < steps; ++s) {
+            const int32_t t0 = begin + s * TOK;
+            stage(k_tile(s), 1, v_tile(s + 1), 3, t0, sb, sa, pa, pb, nothing);
+            __syncthreads();
+            const uint32_t kw = fresh(k_tile(s + 1) + kwbase);
+            stage(k_tile(s), 2, v_tile(s), 0, t0 + 32, sa, sb, pb, pa, [&](int i) {
+              if (i < KD) decode_k(kw, i);
+            });
+            if (s + 2 < steps) load_k(s + 2, id_next);
+            stage(k_tile(s), 3, v_tile(s), 1, t0 + 64, sb, sa, pa, pb, nothing);
+            __syncthreads();
+            const uint32_t vw = fresh(v_tile(s + 1) + vwbase);
+            stage(k_tile(s + 1), 0, v_tile(s), 2, t0 + 96, sa, sb, pb, pa, [&](int i) {
+              if (i < KS / 2) decode_v(vw, i);
+            });
+            if (s + 2 < steps) {
+              load_v(s + 2, id_next);
+              id_next = page_of(s + 3);
+            }
           }
-        }
+  #pragma unroll
+          for (int i = 0; i < KS; ++i) {
+            read_v(v_tile(steps - 1) + vbase, 3, i);
+            output_piece(pb, i);
+          }
+        } else {
+          // Blocks 2 tg and 2 tg + 1 of a tile.  The next keys are written before the barrier and due after it,
+          // into the place of the tile before this one, whose keys were read before the last barrier; the
+          // next values after the barrier and due after the next one, over those that were read before it.
+          const int b0 = 2 * tg, b1 = b0 + 1;
+          for (int32_t s = 0; s < steps; ++s) {
+            const int32_t t0 = begin + s * TOK + 32 * b0;
+            const uint32_t kw = fresh(k_tile(s + 1) + kwbase);
+            stage(k_tile(s), b1, v_tile(s + 1), b1, t0, sb, sa, pa, pb, [&](int i) {
+              if (i < KD) decode_k(kw, i);
+            });
+            if (s + 2 < steps) load_k(s + 2, id_next);
+            __syncthreads();
+            const uint32_t vw = fresh(v_tile(s + 1) + vwbase);
+            stage(k_tile(s + 1), b0, v_tile(s), b0, t0 + 32, sa, sb, pb, pa, [&](int i) {
+              if (i < KS / 2) decode_v(vw, i);
+            });
+            if (s + 2 < steps) {
+              load_v(s + 2, id_next);
+              id_next = page_of(s + 3);
+            }
+          }
 #pragma unroll
-        for (int i = 0; i < KS; ++i) {
-          read_v(v_tile(steps - 1) + vbase, 3, i);
-          output_piece(pb, i);
+          for (int i = 0; i < KS; ++i) {
+            read_v(v_tile(steps - 1) + vbase, b1, i);
+            output_piece(pb, i);
+          }
         }
       } else {
         for (int32_t s = 0; s < steps; ++s) {
@@ -621,9 +657,34 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
       }
     }
 
-    // elements g and g + 8 of the blocks: consecutive dimensions, those of a part of the granule
     l = sum_xor32(l);
-    if (col0 + c32 < col_end) {
+    if constexpr (TG == 2) {
+      // the second group's results to the first one's: a lane's registers to the lane that has the same
+      // column and elements
+      const uint32_t slot = lds + (uint32_t)(cw * (16 * NB + 2)) * 256 + 4 * lane;
+      __syncthreads();                             // the tiles are read
+      if (tg == 1) {
+        lds_at<float>(slot) = m;
+        lds_at<float>(slot + 256) = l;
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) lds_at<float>(slot + 256 * (2 + 16 * i + e)) = acc[i][e];
+      }
+      __syncthreads();
+      if (tg == 0) {
+        const float m1 = lds_at<float>(slot), top = __builtin_fmaxf(m, m1);
+        const float f = __builtin_amdgcn_exp2f(m - top), f1 = __builtin_amdgcn_exp2f(m1 - top);
+        l = l * f + lds_at<float>(slot + 256) * f1;
+        m = top;
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) acc[i][e] = acc[i][e] * f + lds_at<float>(slot + 256 * (2 + 16 * i + e)) * f1;
+      }
+    }
+    // elements g and g + 8 of the blocks: consecutive dimensions, those of a part of the granule
+    if (tg == 0 && col0 + c32 < col_end) {
       auto first_of = [&](int g) { return ((g & 4) * 2 + 4 * h + (g & 3)) * (D / 16); };
       if (whole) {
         const float f = l == 0.0f ? 0.0f : vg / l;
@@ -653,25 +714,36 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
   }
 }
 
-template <int D, bool SPLIT, bool TREE>
+template <int D, bool SPLIT, bool TREE, int TG>
 hipError_t launch(const KvAttnArgs& a, hipStream_t s) {
   constexpr int bytes = kLdsBytes<D, TREE>;
-  const hipError_t e = lds_limit_once<k_kv_prefill<D, SPLIT, TREE>>(bytes);
+  const hipError_t e = lds_limit_once<k_kv_prefill<D, SPLIT, TREE, TG>>(bytes);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((k_kv_prefill<D, SPLIT, TREE>), dim3((unsigned)a.blocks), dim3(64 * kPrefillWaves), bytes, s, a);
+  hipLaunchKernelGGL((k_kv_prefill<D, SPLIT, TREE, TG>), dim3((unsigned)a.blocks), dim3(64 * kPrefillWaves), bytes, s, a);
   const hipError_t launched = hipGetLastError();
   return SPLIT && launched == hipSuccess ? launch_kv_join(a, InType::BF16, D, s) : launched;
 }
 
+template <int D, bool TREE, int TG>
+hipError_t launch(const KvAttnArgs& a, hipStream_t s) {
+  return a.n_workers ? launch<D, true, TREE, TG>(a, s) : launch<D, false, TREE, TG>(a, s);
+}
+
 template <int D>
 hipError_t launch(const KvAttnArgs& a, hipStream_t s) {
-  if (a.tree) return a.n_workers ? launch<D, true, true>(a, s) : launch<D, false, true>(a, s);
-  return a.n_workers ? launch<D, true, false>(a, s) : launch<D, false, false>(a, s);
+  if (!a.tree) return launch<D, false, 1>(a, s);
+  if (a.tile_cols == kPrefillCols) return launch<D, true, 1>(a, s);
+  if constexpr (D == 256) return launch<D, true, 1>(a, s);
+  else return launch<D, true, 2>(a, s);
 }
 
 }  // namespace
 
 int32_t kv_prefill_cols() { return kPrefillCols; }
+// kvattn.hip / here, us: 8 x 4096, 32 / 8 heads, 16 nodes (64 columns) 40 / 42, 32 nodes 56 / 50; 32 x 2048, 16 nodes 42 / 41,
+// 32 nodes 83 / 53, 60 nodes 128 / 86; head dimension 64, 32 nodes 43 / 41; 256 (16 / 2 heads, 8 x 8192), 16 nodes 66 / 67, 30
+// nodes 97 / 95.
+int32_t kv_tree_cols(int32_t D) { return D == 256 ? kPrefillCols / 2 + 1 : kPrefillCols / 4 + 1; }
 int32_t kv_prefill_threads() { return 64 * kPrefillWaves; }
 
 hipError_t launch_kv_prefill(const KvAttnArgs& a, int32_t D, hipStream_t s) {
