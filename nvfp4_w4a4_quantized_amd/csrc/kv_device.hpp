@@ -143,17 +143,22 @@ __device__ __forceinline__ uint64_t tree_word(const KvAttnArgs& a, const SeqInfo
   return x;
 }
 
+__device__ __forceinline__ int32_t tree_words(const KvAttnArgs& a, const SeqInfo& s) {
+  const int32_t words = (s.m + 63) >> 6;
+  return words < a.tree_words ? words : a.tree_words;
+}
+
 // First token of a row's window: it attends to the last `window` of the tokens before c0 and its
-// own ones behind them, in order.
-__device__ __forceinline__ int32_t tree_floor(const KvAttnArgs& a, const SeqInfo& s, int64_t row) {
-  if (!a.window) return 0;
-  const int32_t c0 = s.n - s.m, words = (s.m + 63) >> 6 < a.tree_words ? (s.m + 63) >> 6 : a.tree_words;
+// own ones behind them, in order.  word(w): word w of the row
+template <typename W>
+__device__ __forceinline__ int32_t tree_floor(const KvAttnArgs& a, const SeqInfo& s, W word) {
+  const int32_t c0 = s.n - s.m, words = tree_words(a, s);
   int32_t own = 0;
-  for (int32_t w = 0; w < words; ++w) own += __builtin_popcountll(tree_word(a, s, row, w));
+  for (int32_t w = 0; w < words; ++w) own += __builtin_popcountll(word(w));
   int32_t skip = own - a.window;
   if (skip <= 0) return c0 + skip;                         // -skip tokens before c0
   for (int32_t w = 0; w < words; ++w) {
-    uint64_t x = tree_word(a, s, row, w);
+    uint64_t x = word(w);
     const int32_t bits = __builtin_popcountll(x);
     if (skip >= bits) {
       skip -= bits;
@@ -166,13 +171,14 @@ __device__ __forceinline__ int32_t tree_floor(const KvAttnArgs& a, const SeqInfo
 }
 
 // Which of the 64 tokens from t0 on a row whose window begins at token `from` attends to
-__device__ __forceinline__ uint64_t tree_sees(const KvAttnArgs& a, const SeqInfo& s, int64_t row, int32_t from, int32_t t0) {
+template <typename W>
+__device__ __forceinline__ uint64_t tree_sees(const SeqInfo& s, int32_t from, int32_t t0, W word) {
   const int32_t j0 = t0 - (s.n - s.m);
   uint64_t x = 0;
   if (j0 > -64) {
     const int32_t w = j0 >> 6, shift = j0 & 63;
-    x = tree_word(a, s, row, w) >> shift;
-    if (shift) x |= tree_word(a, s, row, w + 1) << (64 - shift);
+    x = word(w) >> shift;
+    if (shift) x |= word(w + 1) << (64 - shift);
   }
   if (j0 < 0) x |= j0 <= -64 ? ~0ull : (1ull << -j0) - 1;  // tokens before the tree
   const int32_t skip = from - t0;

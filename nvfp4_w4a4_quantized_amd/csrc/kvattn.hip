@@ -319,7 +319,8 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
           if constexpr (F32) qf[TERMS - 1][n][c][i] = (_Float16)(x - (float)hi);
         }
       limit[n] = TREE ? seq.q0 + qi : pos + 1;
-      floor_[n] = TREE ? tree_floor(a, seq, seq.q0 + qi) : (a.window ? pos - a.window + 1 : 0);
+      floor_[n] = a.window ? (TREE ? tree_floor(a, seq, [&](int32_t w) { return tree_word(a, seq, seq.q0 + qi, w); })
+                                   : pos - a.window + 1) : 0;
       m[n] = kNegBig;
       l[n] = 0.0f;
 #pragma unroll
@@ -371,7 +372,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, 2) void k_kv_attn(KvAttnArgs a) {
         for (int n = 0; n < NQ; ++n) {
           if (edge) {
             if constexpr (TREE) {
-              uint64_t sees = tree_sees(a, seq, limit[n], floor_[n], t0);
+              uint64_t sees = tree_sees(seq, floor_[n], t0, [&](int32_t w) { return tree_word(a, seq, limit[n], w); });
               seen |= sees;
               sees >>= 4 * g;
 #pragma unroll
@@ -754,13 +755,16 @@ KvAttnPlan kv_attn_plan(InType t, int64_t T, int32_t batch, int32_t n_q_heads, i
   // two column blocks share a decoded granule where their registers fit, or nearly (head dimension
   // 128: 9 to 14 spill)
   p.nq = cols > 16 && (D == 64 || (D == 128 && t == InType::BF16)) ? 2 : 1;
-  const int64_t blk = 16 * p.nq;
-  p.tile_cols = (int32_t)(cols < blk * kAttnWaves ? cols : blk * kAttnWaves);
   const int64_t pairs = (int64_t)batch * n_kv_heads;
+  // few trees: a workgroup for every 16 columns, each of whose waves has a fourth of the tokens
+  const bool thin = tree && pairs * ((cols + 15) / 16) <= 256;
+  if (thin) p.nq = 1;
+  const int64_t blk = 16 * p.nq, most_cols = thin ? blk : blk * kAttnWaves;
+  p.tile_cols = (int32_t)(cols < most_cols ? cols : most_cols);
   p.col_tiles = kv_planned_tiles((cols + p.tile_cols - 1) / p.tile_cols, pairs, 64 * kAttnWaves);
   const int64_t items = pairs * p.col_tiles;
   p.blocks = (int32_t)items;
-  const int64_t tok = D == 256 ? 32 : 64, waves = cols <= blk ? 4 : (cols <= 2 * blk ? 2 : 1);
+  const int64_t tok = D == 256 ? 32 : 64, waves = thin || cols <= blk ? 4 : (cols <= 2 * blk ? 2 : 1);
   // keys that a tile attends to, at most
   const int64_t span = window > 0 && window + max_q_len < max_kv_len ? window + max_q_len : max_kv_len;
   const int64_t steps = (span + tok - 1) / tok;

@@ -71,8 +71,14 @@ template <int D>
 constexpr int kTreeFirst = kFactors<D> + 4 * kPrefillCols;
 template <int D>
 constexpr int kTreeAny = kTreeFirst<D> + 16;
+// and its rows' windows' first tokens and, where they are not too many, their words
+template <int D>
+constexpr int kTreeFloor = kTreeAny<D> + 8 * kMaxTreeWords;
+template <int D>
+constexpr int kTreeBits = kTreeFloor<D> + 4 * kPrefillCols;
+constexpr int kTreeStaged = 2048;
 template <int D, bool TREE>
-constexpr int kLdsBytes = TREE ? kTreeAny<D> + 8 * kMaxTreeWords : kTreeFirst<D>;
+constexpr int kLdsBytes = TREE ? kTreeBits<D> + 8 * kTreeStaged : kTreeFirst<D>;
 
 template <typename T>
 __device__ __forceinline__ __attribute__((address_space(3))) T& lds_at(uint32_t at) {
@@ -167,6 +173,10 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
     // steps of the call by n_workers, as in kvattn.hip; a lane counts every 64th tile.
     const SeqTable seqs(a, lane);
     float total = 0.0f;
+    if constexpr (TREE) {
+      // every tile of a sequence has the same keys: a lane counts a sequence
+      total = (float)planned_tiles<COLS>(a, seqs.mine, group) * (float)tile_span<D, COLS, TREE>(a, seqs.mine, 0, group).steps;
+    } else
     for (b = 0; b < a.batch; ++b) {
       seq = seqs.at(a, b);
       const int32_t tiles = planned_tiles<COLS>(a, seq, group);
@@ -179,7 +189,25 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
     auto pieces_of = [&](int32_t steps) {
       return steps <= S ? 1 : (int32_t)((uint32_t)(steps + S - 1) / (uint32_t)S);
     };
-    int32_t rest = (int32_t)blockIdx.x, tiles = 0, of_head = 0;
+    int32_t rest = (int32_t)blockIdx.x, tiles = 0, of_head = 0, pieces = 1;
+    if constexpr (TREE) {
+      const int32_t each = pieces_of(tile_span<D, COLS, TREE>(a, seqs.mine, 0, group).steps);
+      const int32_t own = planned_tiles<COLS>(a, seqs.mine, group) * each;
+      int32_t upto = own * hkv;
+#pragma unroll
+      for (int off = 1; off < 64; off <<= 1) {
+        const int32_t x = __shfl_up(upto, off);
+        if (lane >= off) upto += x;
+      }
+      const uint64_t past = __builtin_amdgcn_ballot_w64(upto > rest);
+      b = past ? __builtin_ctzll(past) : a.batch;
+      if (past) {
+        seq = seqs.at(a, b);
+        of_head = __builtin_amdgcn_readlane(own, b);
+        pieces = __builtin_amdgcn_readlane(each, b);
+        rest -= __builtin_amdgcn_readlane(upto, b) - of_head * hkv;
+      }
+    } else
     for (b = 0; b < a.batch; ++b) {
       seq = seqs.at(a, b);
       tiles = planned_tiles<COLS>(a, seq, group);
@@ -197,7 +225,10 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
     }
     kh = (int32_t)((uint32_t)rest / (uint32_t)of_head);
     rest -= kh * of_head;
-    int32_t pieces = 1;
+    if constexpr (TREE) {
+      tile0 = (int32_t)((uint32_t)rest / (uint32_t)pieces);
+      rest -= tile0 * pieces;
+    } else
     for (int32_t t0 = 0;; t0 += 64) {
       const int32_t own = t0 + lane < tiles ? pieces_of(tile_span<D, COLS, TREE>(a, seq, t0 + lane, group).steps) : 0;
       int32_t upto = own;
@@ -292,7 +323,12 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
       read_dwords<KD>(p + 9 * D + (16 * quad + part) * (D / 8), rv);
       vsc = *reinterpret_cast<const uint32_t*>(p + 17 * D + (quad * (D / 16) + part * D / 256) * 4);
       const int32_t first = begin + s * TOK + 16 * gran;
+      if (!TREE && (first < span.lo || first + 16 > seq.n)) vsc = live_scales(vsc, first + 4 * quad, span.lo, seq.n);
+    };
+    // (TREE: when they are decoded, so that the load is not waited for)
+    auto mask_v = [&](int32_t s) {
       if constexpr (TREE) {
+        const int32_t first = begin + s * TOK + 16 * gran;
         const int32_t c0 = seq.n - seq.m, from = lds_at<int32_t>(lds + kTreeFirst<D>);
         if (first < from || first + 16 > c0) {
           uint32_t any = 0;
@@ -305,7 +341,7 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
           }
           vsc &= bytes_of_bits(any);
         }
-      } else if (first < span.lo || first + 16 > seq.n) vsc = live_scales(vsc, first + 4 * quad, span.lo, seq.n);
+      }
     };
     // decode dword i of the loaded keys: a 16-byte chunk of a token's row
     auto decode_k = [&](uint32_t kb, int i) {               // kb: the lane's first chunk in the tile
@@ -339,26 +375,6 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
 
     int32_t id_next = 0;
     __syncthreads();                               // the tile before is done with LDS
-    if constexpr (TREE) {
-      const int32_t rows = (col_end - 1) / a.by_group - col_first / a.by_group + 1;
-      const int32_t words = (seq.m + 63) >> 6 < a.tree_words ? (seq.m + 63) >> 6 : a.tree_words;
-      if (threadIdx.x < 2 * kMaxTreeWords) lds_at<uint32_t>(lds + kTreeAny<D> + 4 * threadIdx.x) = 0;
-      if (threadIdx.x == 0) lds_at<int32_t>(lds + kTreeFirst<D>) = INT32_MAX;
-      __syncthreads();
-      for (int32_t i = threadIdx.x; i < rows; i += 64 * kPrefillWaves) {
-        const int64_t row = seq.q0 + col_first / a.by_group + i;
-        const int32_t from = tree_floor(a, seq, row);
-        atomicMin((int32_t*)(shared + kTreeFirst<D>), from);
-        for (int32_t w = 0; w < words; ++w) {
-          uint64_t x = tree_word(a, seq, row, w);
-          const int32_t skip = from - (seq.n - seq.m) - 64 * w;
-          if (skip > 0) x &= skip >= 64 ? 0 : ~0ull << skip;
-          atomicOr((uint32_t*)(shared + kTreeAny<D>) + 2 * w, (uint32_t)x);
-          atomicOr((uint32_t*)(shared + kTreeAny<D>) + 2 * w + 1, (uint32_t)(x >> 32));
-        }
-      }
-      __syncthreads();
-    }
     if (steps > 0) {
       const int32_t id = page_of(0);
       if (D != 256 || wave < 4) load_k(0, id);
@@ -366,6 +382,38 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
       id_next = page_of(1);
     }
 
+    // TREE: the rows' words and windows, and what of the tree any of them attends to
+    const int32_t row_first = col_first / a.by_group, words = TREE ? tree_words(a, seq) : 0;
+    const int32_t rows = (col_end - 1) / a.by_group - row_first + 1;
+    const bool staged = TREE && rows * words <= kTreeStaged;
+    auto bits_of = [&](int32_t row, int32_t w) -> uint64_t {
+      if (staged) return w >= 0 && w < words ? lds_at<uint64_t>(lds + kTreeBits<D> + 8 * (row * words + w)) : 0;
+      return tree_word(a, seq, seq.q0 + row_first + row, w);
+    };
+    auto stage_tree = [&] {
+      if constexpr (!TREE) return;
+      if (threadIdx.x < 2 * kMaxTreeWords) lds_at<uint32_t>(lds + kTreeAny<D> + 4 * threadIdx.x) = 0;
+      if (threadIdx.x == 0) lds_at<int32_t>(lds + kTreeFirst<D>) = INT32_MAX;
+      if (staged)
+        for (int32_t i = threadIdx.x; i < rows * words; i += 64 * kPrefillWaves) {
+          const int32_t row = words == 1 ? i : (int32_t)((uint32_t)i / (uint32_t)words);
+          lds_at<uint64_t>(lds + kTreeBits<D> + 8 * i) = tree_word(a, seq, seq.q0 + row_first + row, i - row * words);
+        }
+      lds_sync();                                  // (loads of keys and queries stay on their way)
+      for (int32_t i = threadIdx.x; i < rows; i += 64 * kPrefillWaves) {
+        const int32_t from = a.window ? tree_floor(a, seq, [&](int32_t w) { return bits_of(i, w); }) : 0;
+        lds_at<int32_t>(lds + kTreeFloor<D> + 4 * i) = from;
+        atomicMin((int32_t*)(shared + kTreeFirst<D>), from);
+        for (int32_t w = 0; w < words; ++w) {
+          uint64_t x = bits_of(i, w);
+          const int32_t skip = from - (seq.n - seq.m) - 64 * w;
+          if (skip > 0) x &= skip >= 64 ? 0 : ~0ull << skip;
+          if ((uint32_t)x) atomicOr((uint32_t*)(shared + kTreeAny<D>) + 2 * w, (uint32_t)x);
+          if ((uint32_t)(x >> 32)) atomicOr((uint32_t*)(shared + kTreeAny<D>) + 2 * w + 1, (uint32_t)(x >> 32));
+        }
+      }
+      lds_sync();
+    };
     // query columns: B operand of K step k: elements 16 k + 8 h + j of column c32
     f16x8 qf[KS];
     int32_t col = col0 + c32;
@@ -378,6 +426,7 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
       const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + (seq.q0 + qi) * a.ldq + (int64_t)head * D + 8 * h;
 #pragma unroll
       for (int k = 0; k < KS; ++k) raw[k] = *reinterpret_cast<const u32x4*>(src + 16 * k);
+      stage_tree();
 #pragma unroll
       for (int k = 0; k < KS; ++k)
 #pragma unroll
@@ -405,7 +454,7 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
     const int32_t all_lo = wide ? INT32_MAX : sp.all_lo;   // wide: every block takes the slower way
     const int32_t pos = seq.n - seq.m + qi;
     const int32_t limit = pos + 1;
-    const int32_t floor_ = TREE ? tree_floor(a, seq, seq.q0 + qi) : (a.window ? pos - a.window + 1 : 0);
+    const int32_t floor_ = TREE ? lds_at<int32_t>(lds + kTreeFloor<D> + 4 * (qi - row_first)) : (a.window ? pos - a.window + 1 : 0);
     float m = kNegBig, l = 0.0f;
     f32x16 acc[NB];
 #pragma unroll
@@ -431,7 +480,7 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
     auto reference = [&](int32_t t0, f32x16& sc) {
       if (t0 < all_lo || t0 + 32 > sp.all_hi) {
         if constexpr (TREE) {
-          const uint32_t sees = (uint32_t)tree_sees(a, seq, seq.q0 + qi, floor_, t0) >> (4 * h);
+          const uint32_t sees = (uint32_t)tree_sees(seq, floor_, t0, [&](int32_t w) { return bits_of(qi - row_first, w); }) >> (4 * h);
 #pragma unroll
           for (int e = 0; e < 16; ++e)
             if (!((sees >> (8 * (e / 4) + e % 4)) & 1)) sc[e] = -__builtin_inff();
@@ -488,6 +537,7 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
         for (int i = 0; i < KD; ++i) decode_k(k_tile(0) + kwbase, i);
       }
       if (D != 256 || wave >= 4) {
+        mask_v(0);
 #pragma unroll
         for (int i = 0; i < KS / 2; ++i) decode_v(v_tile(0) + vwbase, i);
       }
@@ -565,7 +615,8 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
             if (s + 2 < steps) load_k(s + 2, id_next);
             stage(k_tile(s), 3, v_tile(s), 1, t0 + 64, sb, sa, pa, pb, nothing);
             __syncthreads();
-            const uint32_t vw = fresh(v_tile(s + 1) + vwbase);
+            mask_v(s + 1);
+          const uint32_t vw = fresh(v_tile(s + 1) + vwbase);
             stage(k_tile(s + 1), 0, v_tile(s), 2, t0 + 96, sa, sb, pb, pa, [&](int i) {
               if (i < KS / 2) decode_v(vw, i);
             });
@@ -592,7 +643,8 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
             });
             if (s + 2 < steps) load_k(s + 2, id_next);
             __syncthreads();
-            const uint32_t vw = fresh(v_tile(s + 1) + vwbase);
+            mask_v(s + 1);
+          const uint32_t vw = fresh(v_tile(s + 1) + vwbase);
             stage(k_tile(s + 1), b0, v_tile(s), b0, t0 + 32, sa, sb, pb, pa, [&](int i) {
               if (i < KS / 2) decode_v(vw, i);
             });
@@ -614,6 +666,7 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
 #pragma unroll
             for (int i = 0; i < KD; ++i) decode_k(kw, i);
           } else {
+            mask_v(s + 1);
 #pragma unroll
             for (int i = 0; i < KS / 2; ++i) decode_v(vw, i);
           }
