@@ -802,14 +802,7 @@ int32_t nvfp4_kv_attention_workspace(int32_t dtype, int64_t T, int32_t batch, in
   if (!valid_dtype(dtype)) return fail(NVFP4_ERR_UNSUPPORTED, "dtype %d is not F32 or BF16", dtype);
   const int32_t st = check_kv_attn_sizes(T, batch, n_q_heads, n_kv_heads, head_dim, max_q_len, max_kv_len);
   if (st) return st;
-  // a window never needs more
-  int64_t need = 0;
-  for (const bool tree : {false, true}) {
-    const int64_t w = nvfp4::kv_attn_plan(in_type(dtype), T, batch, n_q_heads, n_kv_heads, head_dim, max_q_len, max_kv_len, 0, tree)
-                          .workspace;
-    need = w > need ? w : need;
-  }
-  *bytes_out = need;
+  *bytes_out = nvfp4::kv_attn_workspace(in_type(dtype), T, batch, n_q_heads, n_kv_heads, head_dim, max_q_len, max_kv_len);
   return ok();
 }
 

@@ -133,6 +133,9 @@ struct KvAttnPlan {
 };
 KvAttnPlan kv_attn_plan(InType t, int64_t T, int32_t batch, int32_t n_q_heads, int32_t n_kv_heads, int32_t D,
                         int64_t max_q_len, int64_t max_kv_len, int64_t window, bool tree);
+// bytes for a call of these sizes, of a tree or not, with any window
+int64_t kv_attn_workspace(InType t, int64_t T, int32_t batch, int32_t n_q_heads, int32_t n_kv_heads, int32_t D,
+                          int64_t max_q_len, int64_t max_kv_len);
 hipError_t launch_kv_attn(KvAttnArgs a, const KvAttnPlan& p, InType t, int32_t D, hipStream_t s);
 
 // kvweights.hip: the attention weight of cached tokens

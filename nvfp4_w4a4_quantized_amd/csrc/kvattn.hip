@@ -718,8 +718,31 @@ hipError_t launch_kv_join(const KvAttnArgs& a, InType t, int32_t D, hipStream_t 
   return f32 ? join<256, true>(a, s) : join<256, false>(a, s);
 }
 
-KvAttnPlan kv_attn_plan(InType t, int64_t T, int32_t batch, int32_t n_q_heads, int32_t n_kv_heads, int32_t D,
-                        int64_t max_q_len, int64_t max_kv_len, int64_t window, bool tree) {
+// Drafted trees: whether a workgroup takes every 16 columns of a sequence and kv head (each of its waves a
+// fourth of the tokens, or of a piece of them), whose keys it decodes for itself, or more of them that share
+// the decoding but need the time of a prompt's kernel (shared) to begin and end, or two blocks of
+// columns a wave.  By the times of both sides in us, head dimension 128, 32 / 8 heads, thin / other:
+//   shared     1 x 300, 32 nodes 7 / 27; 1 x 4096, 60 nodes 22 / 45; 4 x 4096, 32 nodes 30 / 35, 60 nodes 46 / 50; 8 x
+//              4096, 24 nodes 48 / 42, 60 nodes 93 / 67; 2 x 131072, 32 nodes 323 / 190
+//   two blocks 1 x 300, 8 nodes 7 / 11; 8 x 4096, 16 nodes 30 / 40; 16 x 1024, 16 nodes 19 / 25; 16 x 4096, 16 nodes
+//              54 / 53; 32 x 2048, 16 nodes 59 / 42; 2 x 131072, 16 nodes 165 / 132
+// (64: 8 x 4096, 32 nodes 36 / 35; 256: 8 x 8192, 16 / 2 heads, 16 nodes 58 / 66, 30 nodes 104 / 91, 4 x 8192 53 / 70).
+// The shared kernel's time is taken as a beginning and its tiles by the compute units, thin items' as
+// rounds of one a compute unit, or, few ones, which are cut, as all their steps.
+static bool thin_items(int64_t pairs, int64_t cols, int32_t D, int64_t span, bool shared) {
+  const int64_t items = pairs * ((cols + 15) / 16), steps = (span + 63) / 64;
+  const double width = D == 64 ? 0.55 : (D == 128 ? 1.0 : 2.0);
+  if (!shared) return items <= 256 ? (double)items * (double)steps * width <= 40960 : (items <= 512 && steps <= 16);
+  const double own = items >= 160 ? 10 + 0.36 * width * (double)steps * (double)((items + 255) / 256)
+                                  : 12 + 0.00125 * width * (double)items * (double)steps;
+  const bool wide = cols > kv_prefill_cols() / 2;
+  const double tile = (wide ? 4.2 : 2.7) * (D == 256 ? 2.6 : width), begin = D == 256 ? 45 : (wide ? 33 : 23);
+  const int64_t tiles = pairs * ((span + 127) / 128) * (wide ? (cols + kv_prefill_cols() - 1) / kv_prefill_cols() : 1);
+  return own < begin + tile * (double)tiles / 256;
+}
+
+static KvAttnPlan plan_of(InType t, int64_t T, int32_t batch, int32_t n_q_heads, int32_t n_kv_heads, int32_t D,
+                          int64_t max_q_len, int64_t max_kv_len, int64_t window, bool tree, bool thin) {
   KvAttnPlan p{};
   const int64_t cols = (max_q_len < T ? max_q_len : T) * (n_q_heads / n_kv_heads);
   const int32_t least = tree ? kv_tree_cols(D) : kv_prefill_cols();
@@ -727,7 +750,7 @@ KvAttnPlan kv_attn_plan(InType t, int64_t T, int32_t batch, int32_t n_q_heads, i
   // kernel / kvprefill.hip, us: 1 x 16384 keys and 256 columns 64 / 53, 1024 columns 123 / 93; 8 x
   // 4096 and 256 columns 81 / 66, but 128 columns 56 / 58; 32 x 4096 and 256 columns 245 / 175, but 128
   // columns 127 / 146; head dimension 256, 1 x 16384, 512 columns 81 / 61; 64, 2 x 4096, 512 columns 44 / 35.
-  if (t == InType::BF16 && cols >= least) {
+  if (t == InType::BF16 && cols >= least && !thin) {
     p.prefill = true;
     p.tile_cols = tree && cols <= 128 ? 128 : kv_prefill_cols();
     const int64_t pairs = (int64_t)batch * n_kv_heads, tiles = (cols + p.tile_cols - 1) / p.tile_cols;
@@ -756,8 +779,6 @@ KvAttnPlan kv_attn_plan(InType t, int64_t T, int32_t batch, int32_t n_q_heads, i
   // 128: 9 to 14 spill)
   p.nq = cols > 16 && (D == 64 || (D == 128 && t == InType::BF16)) ? 2 : 1;
   const int64_t pairs = (int64_t)batch * n_kv_heads;
-  // few trees: a workgroup for every 16 columns, each of whose waves has a fourth of the tokens
-  const bool thin = tree && pairs * ((cols + 15) / 16) <= 256;
   if (thin) p.nq = 1;
   const int64_t blk = 16 * p.nq, most_cols = thin ? blk : blk * kAttnWaves;
   p.tile_cols = (int32_t)(cols < most_cols ? cols : most_cols);
@@ -772,7 +793,7 @@ KvAttnPlan kv_attn_plan(InType t, int64_t T, int32_t batch, int32_t n_q_heads, i
   // latency (4.5 us) and pays where it brings idle compute units to work.  Measured, whole
   // / cut: 256 items of up to 64 steps 29.7 / 32.8 us, 128 of 32 15.8 / 20.2 and of 64 26.7 / 22.0,
   // 64 of 32 15.1 / 18.8, 32 of 32 15.5 / 11.3.
-  const int64_t alone = items >= 256 ? 16 : (items >= 64 ? 8 : 4);
+  const int64_t alone = items >= (thin ? 160 : 256) ? 16 : (items >= 64 ? 8 : 4);
   if (items >= 1024 || steps <= alone * waves) return p;
   p.min_steps = (int32_t)waves;                           // a step for each wave
   // about as many pieces as run at once: rounding up adds half a piece to an item
@@ -781,6 +802,26 @@ KvAttnPlan kv_attn_plan(InType t, int64_t T, int32_t batch, int32_t n_q_heads, i
   p.pieces_at = (int64_t)p.blocks * p.tile_cols * (D + 4) * (int64_t)sizeof(float);
   p.workspace = p.pieces_at + (int64_t)p.blocks * kItemPiecesBytes;
   return p;
+}
+
+KvAttnPlan kv_attn_plan(InType t, int64_t T, int32_t batch, int32_t n_q_heads, int32_t n_kv_heads, int32_t D,
+                        int64_t max_q_len, int64_t max_kv_len, int64_t window, bool tree) {
+  const int64_t cols = (max_q_len < T ? max_q_len : T) * (n_q_heads / n_kv_heads);
+  const int64_t span = window > 0 && window + max_q_len < max_kv_len ? window + max_q_len : max_kv_len;
+  const bool thin = tree && thin_items((int64_t)batch * n_kv_heads, cols, D, span, t == InType::BF16 && cols >= kv_tree_cols(D));
+  return plan_of(t, T, batch, n_q_heads, n_kv_heads, D, max_q_len, max_kv_len, window, tree, thin);
+}
+
+// A window shortens the keys, by which trees' items are thin or not: enough for either.  For one or the other,
+// it never needs more.
+int64_t kv_attn_workspace(InType t, int64_t T, int32_t batch, int32_t n_q_heads, int32_t n_kv_heads, int32_t D,
+                          int64_t max_q_len, int64_t max_kv_len) {
+  int64_t need = 0;
+  for (int i = 0; i < 3; ++i) {
+    const int64_t w = plan_of(t, T, batch, n_q_heads, n_kv_heads, D, max_q_len, max_kv_len, 0, i > 0, i > 1).workspace;
+    need = w > need ? w : need;
+  }
+  return need;
 }
 
 hipError_t launch_kv_attn(KvAttnArgs a, const KvAttnPlan& p, InType t, int32_t D, hipStream_t s) {

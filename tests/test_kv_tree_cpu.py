@@ -5,6 +5,7 @@ import ctypes
 
 import numpy as np
 import pytest
+import torch
 
 from oracle import kv as KV
 from tests.test_kv_abi_cpu import FAKE, ODD, nv  # noqa: F401  (the fixture)
@@ -59,3 +60,19 @@ def test_oracle_empty_rows():
     q, k, v = _case(np.random.default_rng(0), 2, 2, 2, 1, 8)
     o, lse, w = KV.tree_attention(q, k, v, 1.0, [set(), {0, 1}])
     assert np.all(o[0] == 0) and np.all(np.isneginf(lse[0])) and np.all(w[0] == 0) and np.all(np.isfinite(lse[1]))
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="its buffers are not real: where there is a GPU the calls would be launched")
+def test_workspace_covers_every_window(nv):  # noqa: F811
+    """A window may change how a tree's call is planned: the workspace that is asked for without
+    one is enough (the call is not refused for it: without a GPU it goes on to look for the
+    device)."""
+    for T, batch, hq, hkv, d, mq, mk in ((480, 8, 32, 8, 128, 60, 4096), (64, 2, 32, 8, 128, 32, 131072), (256, 8, 16, 2, 256, 32, 8192),
+                                         (40, 5, 15, 5, 64, 8, 100000), (960, 16, 32, 8, 128, 60, 8192)):
+        for dt, dtype in ((1, torch.bfloat16), (0, torch.float32)):
+            need = nv.nvfp4_kv_attention_workspace(T, batch, hq, hkv, d, mq, mk, dtype)
+            for window in (0, 1, 17, 300, 2000, 20000):
+                st = nv.lib.nvfp4_kv_tree_attention(FAKE, dt, hq * d, T, hq, hkv, d, batch, FAKE, mq, FAKE, mk, FAKE, mk // 16 + 1,
+                                                    mk // 16 + 1, FAKE, 1 << 20, 16, FAKE, FAKE, ctypes.c_float(0.1), window, FAKE, 1, 1,
+                                                    FAKE, hq * d, None, FAKE, need, None)
+                assert st in (nv.NVFP4_ERR_HIP, nv.NVFP4_ERR_DEVICE), (T, window, nv.nvfp4_last_error())
