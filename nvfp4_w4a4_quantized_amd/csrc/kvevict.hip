@@ -3,8 +3,10 @@
 //
 // A row (one token of one kv head) is 9/8 D bytes in places that its neighbours' lie between:
 // D/2 bytes of key codes and D/16 of their scales in one piece each, 16 parts of D/32 bytes of
-// value codes, D/16 single bytes of value scales.  16 lanes move a row: a part of the key codes
-// and of the value codes each, and a byte of both scales.
+// value codes, D/16 single bytes of value scales.  A wave moves 16 rows: four lanes a row its keys, in a load
+// of both (16 bytes a lane at D = 128), then 16 lanes a row the parts of the values, in four, and D/16
+// lanes a row their scales.  What counts is the number of such loads and stores, not their bytes (with
+// 16 lanes a row for everything, twice as many: evict_step 19 us, not 17).
 #include "kernel_common.hpp"
 #include "kv_launch.hpp"
 
@@ -14,34 +16,20 @@ namespace {
 
 constexpr int kThreads = kKvMoveThreads;
 constexpr int kWaves = kThreads / 64;
-constexpr int kRowLanes = 16;
-constexpr int kRows = kThreads / kRowLanes;        // rows that a workgroup moves side by side
-
-template <int D>
-struct PartOf { using type = uint32_t; };
-template <>
-struct PartOf<64> { using type = uint16_t; };
-template <>
-struct PartOf<256> { using type = uint64_t; };
-
-// What one of its 16 lanes holds of a row
-template <int D>
-struct RowPart {
-  typename PartOf<D>::type k, v;
-  uint8_t ks, vs;
-};
+constexpr int kWaveRows = 16;                      // rows of a wave
+constexpr int kRows = kWaves * kWaveRows;          // and of a workgroup
 
 // A sequence's pages
 struct Pages {
   const int32_t* table;
   KvGeom geom;
   int32_t last;                // of the table's entries
-  // the page of token t, or -1: an entry outside the cache is never followed
-  __device__ __forceinline__ int64_t of(int32_t t) const {
-    const int32_t at = t >> geom.page_shift;
-    if (t < 0 || at > last) return -1;
-    const int32_t id = table[at];
-    return id >= 0 && id < geom.n_pages ? id : -1;
+  // the page of token t, or -1: an entry outside the cache is never followed.  (No branches here and in what
+  // follows: loads are counted in order, and a load that waits for another one, or for a branch, holds up all
+  // those behind it.)
+  __device__ __forceinline__ int32_t of(int32_t t) const {
+    const int32_t at = t >> geom.page_shift, id = table[at < 0 ? 0 : (at > last ? last : at)];
+    return at >= 0 && at <= last && id >= 0 && id < geom.n_pages ? id : -1;
   }
   __device__ __forceinline__ int32_t place(int32_t t) const { return t & ((1 << geom.page_shift) - 1); }
   // token t's weight (page: of(t))
@@ -60,43 +48,108 @@ __device__ __forceinline__ int32_t length_of(const KvPages& p, const int32_t* kv
   return (int32_t)(n < 0 ? 0 : (n > most ? most : n));
 }
 
+// Where a row is: 16 times the place of its granule in the cache, and its place in the granule
 template <int D>
-__device__ __forceinline__ uint8_t* granule_at(uint8_t* cache, const Pages& p, int64_t page, int32_t kh, int32_t t) {
-  return cache + page * p.geom.page_bytes +
-         ((int64_t)(kh << (p.geom.page_shift - 4)) + (p.place(t) >> 4)) * kv_granule_bytes(D);
+__device__ __forceinline__ int64_t row_at(const Pages& p, int64_t page, int32_t kh, int32_t t) {
+  return (page * p.geom.page_bytes + ((int64_t)(kh << (p.geom.page_shift - 4)) + (p.place(t) >> 4)) * kv_granule_bytes(D)) * 16 +
+         (t & 15);
 }
 
-template <int D>
-__device__ __forceinline__ RowPart<D> load_row(const uint8_t* granule, int32_t t, int l) {
-  using P = typename PartOf<D>::type;
-  const int r = t & 15;
-  RowPart<D> x;
-  x.k = *reinterpret_cast<const P*>(granule + r * (D / 2) + l * (D / 32));
-  x.v = *reinterpret_cast<const P*>(granule + 9 * D + (r >> 2) * (2 * D) + l * (D / 8) + (r & 3) * (D / 32));
-  x.ks = x.vs = 0;
-  if (l < D / 16) {
-    x.ks = granule[8 * D + r * (D / 16) + l];
-    x.vs = granule[17 * D + (r >> 2) * (D / 4) + 4 * l + (r & 3)];
-  }
-  return x;
+__device__ __forceinline__ int64_t of_lane(int64_t x, int lane) {
+  const uint32_t lo = (uint32_t)__shfl((int)x, lane), hi = (uint32_t)__shfl((int)(x >> 32), lane);
+  return (int64_t)((uint64_t)hi << 32 | lo);
 }
 
+// What a lane holds of its wave's 16 rows.  Rows are given by four lanes each, lanes 4 i to 4 i + 3 row i;
+// every lane of the wave takes part.
 template <int D>
-__device__ __forceinline__ void store_row(uint8_t* granule, int32_t t, int l, const RowPart<D>& x) {
-  using P = typename PartOf<D>::type;
-  const int r = t & 15;
-  *reinterpret_cast<P*>(granule + r * (D / 2) + l * (D / 32)) = x.k;
-  *reinterpret_cast<P*>(granule + 9 * D + (r >> 2) * (2 * D) + l * (D / 8) + (r & 3) * (D / 32)) = x.v;
-  if (l < D / 16) {
-    granule[8 * D + r * (D / 16) + l] = x.ks;
-    granule[17 * D + (r >> 2) * (D / 4) + 4 * l + (r & 3)] = x.vs;
+struct Rows {
+  static constexpr int VS = D / 64, PER = D / 16;  // loads of value scales; lanes a row in them
+  uint32_t k[D / 32], ks;
+  uint64_t v[4];
+  uint8_t vs[VS];
+
+  template <typename F>
+  static __device__ __forceinline__ void parts(int64_t row, F f) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t x = of_lane(row, (4 * i + (lane >> 4)) * 4);
+      const int r = (int)(x & 15);
+      f(i, x, 9 * D + (r >> 2) * (2 * D) + (lane & 15) * (D / 8) + (r & 3) * (D / 32));
+    }
   }
-}
+  template <typename F>
+  static __device__ __forceinline__ void scales(int64_t row, F f) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < VS; ++i) {
+      const int64_t x = of_lane(row, (i * (64 / PER) + lane / PER) * 4);
+      const int r = (int)(x & 15);
+      f(i, x, 17 * D + (r >> 2) * (D / 4) + (lane % PER) * 4 + (r & 3));
+    }
+  }
+
+  // rows `from` (all of them in the cache)
+  __device__ __forceinline__ void load(const uint8_t* cache, int64_t from) {
+    const int q = threadIdx.x & 3, r = (int)(from & 15);
+    const uint8_t* const p = cache + (from >> 4);
+    const uint8_t *kp = p + r * (D / 2) + q * (D / 8), *sp = p + 8 * D + r * (D / 16) + q * (D / 64);
+    if constexpr (D == 64) {
+      const u32x2 x = *reinterpret_cast<const u32x2*>(kp);
+      k[0] = x[0];
+      k[1] = x[1];
+      ks = *sp;
+    } else {
+#pragma unroll
+      for (int i = 0; i < D / 32; i += 4) {
+        const u32x4 x = *reinterpret_cast<const u32x4*>(kp + 4 * i);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) k[i + e] = x[e];
+      }
+      ks = D == 128 ? *reinterpret_cast<const uint16_t*>(sp) : *reinterpret_cast<const uint32_t*>(sp);
+    }
+    parts(from, [&](int i, int64_t x, int at) {
+      const uint8_t* const vp = cache + (x >> 4) + at;
+      if constexpr (D == 64) v[i] = *reinterpret_cast<const uint16_t*>(vp);
+      else if constexpr (D == 128) v[i] = *reinterpret_cast<const uint32_t*>(vp);
+      else v[i] = *reinterpret_cast<const uint64_t*>(vp);
+    });
+    scales(from, [&](int i, int64_t x, int at) { vs[i] = cache[(x >> 4) + at]; });
+  }
+  // to the rows `to` (-1: nowhere)
+  __device__ __forceinline__ void store(uint8_t* cache, int64_t to) const {
+    const int q = threadIdx.x & 3, r = (int)(to & 15);
+    if (to >= 0) {
+      uint8_t* const p = cache + (to >> 4);
+      uint8_t *kp = p + r * (D / 2) + q * (D / 8), *sp = p + 8 * D + r * (D / 16) + q * (D / 64);
+      if constexpr (D == 64) {
+        *reinterpret_cast<u32x2*>(kp) = u32x2{k[0], k[1]};
+        *sp = (uint8_t)ks;
+      } else {
+#pragma unroll
+        for (int i = 0; i < D / 32; i += 4) *reinterpret_cast<u32x4*>(kp + 4 * i) = u32x4{k[i], k[i + 1], k[i + 2], k[i + 3]};
+        if constexpr (D == 128) *reinterpret_cast<uint16_t*>(sp) = (uint16_t)ks;
+        else *reinterpret_cast<uint32_t*>(sp) = ks;
+      }
+    }
+    parts(to, [&](int i, int64_t x, int at) {
+      if (x < 0) return;
+      uint8_t* const vp = cache + (x >> 4) + at;
+      if constexpr (D == 64) *reinterpret_cast<uint16_t*>(vp) = (uint16_t)v[i];
+      else if constexpr (D == 128) *reinterpret_cast<uint32_t*>(vp) = (uint32_t)v[i];
+      else *reinterpret_cast<uint64_t*>(vp) = v[i];
+    });
+    scales(to, [&](int i, int64_t x, int at) {
+      if (x >= 0) cache[(x >> 4) + at] = vs[i];
+    });
+  }
+};
 
 // Accepted path: a workgroup per sequence, so that the sequence's length may be written where it was
-// read.  The rows of whole heads, up to kRows times kHeld at a time, are all read before any is
-// written: a path's numbers need not increase.
-constexpr int kHeld = kKvMostAccepted / kRows;
+// read.  The rows of whole heads, up to kRows at a time, are all read before any is written: a path's
+// numbers need not increase.
+static_assert(kKvMostAccepted <= kRows, "a head's rows at a time");
 
 template <int D>
 __global__ __launch_bounds__(kThreads) void k_kv_accept(KvAcceptArgs a) {
@@ -112,33 +165,24 @@ __global__ __launch_bounds__(kThreads) void k_kv_accept(KvAcceptArgs a) {
   const int32_t most = m < a.max_accepted ? m : a.max_accepted;
   count = count < 0 ? 0 : (count > most ? most : count);
   const int32_t c0 = n - m;
-  const int row = threadIdx.x / kRowLanes, l = threadIdx.x % kRowLanes;
-  const int32_t heads = count > 0 ? kHeld * kRows / count : hkv;      // at a time
+  const int row = threadIdx.x / 4;
+  const int32_t heads = count > 0 ? kRows / count : hkv;              // at a time
   for (int32_t h0 = 0; count > 0 && h0 < hkv; h0 += heads) {
-    const int32_t rows = (hkv - h0 < heads ? hkv - h0 : heads) * count;
-    RowPart<D> x[kHeld];
-    uint8_t* to[kHeld];
-    int32_t at[kHeld];
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-      const int32_t j = row + i * kRows;
-      to[i] = nullptr;
-      if (j >= rows) continue;
-      const int32_t h = j / count, p = j - h * count;
-      int32_t node = a.accepted[(int64_t)b * a.ld_accepted + p];
-      node = node < 0 ? 0 : (node >= m ? m - 1 : node);
-      const int32_t from = c0 + node;
-      at[i] = c0 + p;
-      if (from == at[i] || from < 0 || at[i] < 0) continue;
-      const int64_t src = pages.of(from), dst = pages.of(at[i]);
-      if (src < 0 || dst < 0) continue;
-      x[i] = load_row<D>(granule_at<D>(a.cache, pages, src, h0 + h, from), from, l);
-      to[i] = granule_at<D>(a.cache, pages, dst, h0 + h, at[i]);
+    const int32_t rows = (hkv - h0 < heads ? hkv - h0 : heads) * count, j = row < rows ? row : rows - 1;
+    const bool busy = (row & ~(kWaveRows - 1)) < rows;                // the wave has rows
+    Rows<D> x;
+    int64_t to = -1;
+    if (busy) {
+      const int32_t h = j / count, p = j - h * count, at = c0 + p;
+      const int32_t node = a.accepted[(int64_t)b * a.ld_accepted + p];
+      const int32_t from = c0 + (node < 0 ? 0 : (node >= m ? m - 1 : node));
+      const int32_t src = pages.of(from), dst = pages.of(at);
+      const bool moves = row < rows && from != at && from >= 0 && at >= 0 && src >= 0 && dst >= 0;
+      x.load(a.cache, row_at<D>(pages, src < 0 ? 0 : src, h0 + h, from));
+      if (moves) to = row_at<D>(pages, dst, h0 + h, at);
     }
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i)
-      if (to[i]) store_row<D>(to[i], at[i], l, x[i]);
+    if (busy) x.store(a.cache, to);
   }
   __syncthreads();                                 // every thread has read the length
   if (threadIdx.x == 0) {
@@ -207,7 +251,7 @@ struct Row {
         behind(budget - last) {}
 
   __device__ __forceinline__ uint32_t key(const KvEvictArgs& a, int32_t i) const {
-    const int64_t page = pages.of(first + i);
+    const int32_t page = pages.of(first + i);
     return page < 0 ? weight_key(-__builtin_inff()) : weight_key(a.weights[pages.weight_at(page, kh, first + i)]);
   }
 };
@@ -225,11 +269,13 @@ __device__ __forceinline__ void for_keys(const KvEvictArgs& a, const Row& x, int
 #pragma unroll
     for (int e = 0; e < N; ++e) {
       const int32_t i = i0 + e * count, t = x.first + (i < end ? i : i0);
-      const int64_t page = x.pages.of(t);
+      const int32_t page = x.pages.of(t);
       at[e] = page < 0 ? -1 : x.pages.weight_at(page, x.kh, t);
     }
 #pragma unroll
-    for (int e = 0; e < N; ++e) w[e] = at[e] < 0 ? -__builtin_inff() : a.weights[at[e]];
+    for (int e = 0; e < N; ++e) w[e] = a.weights[at[e] < 0 ? 0 : at[e]];
+#pragma unroll
+    for (int e = 0; e < N; ++e) w[e] = at[e] < 0 ? -__builtin_inff() : w[e];
 #pragma unroll
     for (int e = 0; e < N; ++e) {
       const int32_t i = i0 + e * count;
@@ -248,7 +294,7 @@ __device__ __forceinline__ void keep_places(const KvEvictArgs& a, const Row& x, 
       a.kept[(int64_t)row * a.budget + j] = j < stay ? j : -1;
   if (a.weights_out && a.weights_out != a.weights)
     for (int32_t j = thread; j < (x.over ? x.first : x.left); j += count) {
-      const int64_t page = x.pages.of(j);
+      const int32_t page = x.pages.of(j);
       if (page >= 0) {
         const int64_t at = x.pages.weight_at(page, x.kh, j);
         a.weights_out[at] = a.weights[at];
@@ -296,82 +342,103 @@ __device__ __forceinline__ void walk(const Row& x, int32_t r0, int32_t r1, uint3
   }
 }
 
-// A row on its way, in its 16 lanes
-template <int D>
+// 16 N rows of a wave on their way
+template <int D, int N>
 struct Moving {
-  RowPart<D> x;
-  float w;
-  uint8_t* to;
-  int64_t w_at;
-  int32_t t;
+  Rows<D> x[N];
+  int64_t to[N], w_at[N];
+  float w[N];
 
-  __device__ __forceinline__ void read(const KvEvictArgs& a, const Row& row, int32_t* kept, int32_t old, int32_t place, int l) {
-    to = nullptr;
-    const int64_t src = row.pages.of(old), dst = row.pages.of(place);
-    if (src < 0 || dst < 0) return;
-    x = load_row<D>(granule_at<D>(a.cache, row.pages, src, row.kh, old), old, l);
-    to = granule_at<D>(a.cache, row.pages, dst, row.kh, place);
-    t = place;
-    if (l == 0) {
-      if (a.weights_out) {
-        w = a.weights[row.pages.weight_at(src, row.kh, old)];
-        w_at = row.pages.weight_at(dst, row.kh, place);
+  // rows e: token old[e] to place[e], where live[e]; none from rows `some` on is (the same number for the wave)
+  __device__ __forceinline__ void read(const KvEvictArgs& a, const Row& row, int32_t* kept, const int32_t (&old)[N],
+                                       const int32_t (&place)[N], const bool (&live)[N], int some) {
+    int32_t src[N], dst[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      src[e] = dst[e] = 0;
+      to[e] = -1;
+      if (e >= some) continue;
+      src[e] = row.pages.of(old[e]);
+      dst[e] = row.pages.of(place[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      if (e >= some) continue;
+      const bool moves = live[e] && src[e] >= 0 && dst[e] >= 0;
+      const int32_t from = src[e] < 0 ? 0 : src[e];
+      x[e].load(a.cache, row_at<D>(row.pages, from, row.kh, old[e]));
+      w[e] = a.weights[row.pages.weight_at(from, row.kh, old[e])];
+      if (moves) {
+        to[e] = row_at<D>(row.pages, dst[e], row.kh, place[e]);
+        w_at[e] = row.pages.weight_at(dst[e], row.kh, place[e]);
+        if (kept && (threadIdx.x & 3) == 0) kept[place[e]] = old[e];
       }
-      if (kept) kept[place] = old;
     }
   }
-  __device__ __forceinline__ void write(const KvEvictArgs& a, int l) const {
-    if (!to) return;
-    store_row<D>(to, t, l, x);
-    if (l == 0 && a.weights_out) a.weights_out[w_at] = w;
+  __device__ __forceinline__ void write(const KvEvictArgs& a) const {
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (__builtin_amdgcn_ballot_w64(to[e] >= 0)) {
+        x[e].store(a.cache, to[e]);
+        if (a.weights_out && to[e] >= 0 && (threadIdx.x & 3) == 0) a.weights_out[w_at[e]] = w[e];
+      }
   }
 };
 
-// The last tokens down by n - budget, a chunk of kHeld * kRows at a time from j0 on, in order where
-// old and new places overlap: what a chunk overwrites was read by it or by chunks before.
-constexpr int kChunk = kHeld * kRows;
+// The last tokens down by n - budget, kRows at a time from j0 on, in order where old and new places
+// overlap: what they overwrite was read with them or before.
+constexpr int kChunk = kRows;
+
+// how many of N groups of rows, `side` apart, a wave has where `left` rows are left for its workgroup
+__device__ __forceinline__ int groups_of(int32_t left, int side) {
+  const int32_t own = left - (int32_t)(threadIdx.x >> 6) * kWaveRows;
+  return __builtin_amdgcn_readfirstlane(own <= 0 ? 0 : (own + side - 1) / side);
+}
 
 template <int D>
-__device__ __forceinline__ void read_last(const KvEvictArgs& a, const Row& x, int32_t* kept, int32_t j0, Moving<D> (&h)[kHeld]) {
-  const int row = threadIdx.x / kRowLanes, l = threadIdx.x % kRowLanes;
+__device__ __forceinline__ void read_last(const KvEvictArgs& a, const Row& x, int32_t* kept, int32_t j0, Moving<D, 1>& h) {
+  const int32_t j = j0 + (int32_t)threadIdx.x / 4;
+  const bool live[1] = {j < x.last};
+  const int32_t old[1] = {live[0] ? x.n - x.last + j : x.n - 1}, place[1] = {live[0] ? x.behind + j : 0};
+  h.read(a, x, kept, old, place, live, groups_of(x.last - j0, kRows));
+}
+
+// Rows i0 + thread / 4, + side, ... of the lists (N of them, those below `moving`)
+template <int D, int N>
+__device__ __forceinline__ void read_listed(const KvEvictArgs& a, const Row& x, int32_t* kept, const int32_t* from, const int32_t* to,
+                                            int32_t i0, int side, int32_t moving, Moving<D, N>& m) {
+  int32_t old[N], place[N];
+  bool live[N];
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i) {
-    const int32_t j = j0 + i * kRows + row;
-    h[i].to = nullptr;
-    if (j < x.last) h[i].read(a, x, kept, x.n - x.last + j, x.behind + j, l);
+  for (int e = 0; e < N; ++e) {
+    const int32_t i = i0 + e * side + (int32_t)threadIdx.x / 4;
+    live[e] = i < moving;
+    old[e] = from[live[e] ? i : i0];
+    place[e] = to[live[e] ? i : i0];
   }
+  m.read(a, x, kept, old, place, live, groups_of(moving - i0, side));
 }
 
 // Movers stand behind every free place: nothing that is read here is written
 template <int D>
 __device__ __forceinline__ void move_listed(const KvEvictArgs& a, const Row& x, int32_t* kept, const int32_t* from,
                                             const int32_t* to, int32_t moving) {
-  const int row = threadIdx.x / kRowLanes, l = threadIdx.x % kRowLanes;
-  for (int32_t i0 = row; i0 < moving; i0 += 3 * kRows) {
-    Moving<D> m[3];
-#pragma unroll
-    for (int e = 0; e < 3; ++e) {
-      const int32_t i = i0 + e * kRows;
-      m[e].to = nullptr;
-      if (i < moving) m[e].read(a, x, kept, from[i], to[i], l);
-    }
-#pragma unroll
-    for (int e = 0; e < 3; ++e) m[e].write(a, l);
+  for (int32_t i0 = 0; i0 < moving; i0 += kRows) {
+    Moving<D, 1> m;
+    read_listed<D, 1>(a, x, kept, from, to, i0, kRows, moving, m);
+    m.write(a);
   }
 }
 
 // The last tokens, their first chunk read already
 template <int D>
-__device__ __forceinline__ void move_last(const KvEvictArgs& a, const Row& x, int32_t* kept, Moving<D> (&tail)[kHeld]) {
-  const int l = threadIdx.x % kRowLanes;
+__device__ __forceinline__ void move_last(const KvEvictArgs& a, const Row& x, int32_t* kept, Moving<D, 1>& tail) {
   __syncthreads();                                 // the movers are read
-#pragma unroll
-  for (int i = 0; i < kHeld; ++i) tail[i].write(a, l);
+  tail.write(a);
   for (int32_t j0 = kChunk; j0 < x.last; j0 += kChunk) {
     read_last<D>(a, x, kept, j0, tail);
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) tail[i].write(a, l);
+    tail.write(a);
   }
 }
 
@@ -384,7 +451,7 @@ __device__ __forceinline__ void evict_row(const KvEvictArgs& a, const Row& x, in
   auto key_of = [&](int32_t i) { return x.key(a, i); };
   for_keys<true>(a, x, 0, x.rated, tid, kThreads, [](int32_t, uint32_t) {});
   // the last tokens' first chunk, on its way while the others are chosen
-  Moving<D> tail[kHeld];
+  Moving<D, 1> tail;
   read_last<D>(a, x, kept, 0, tail);
   keep_places(a, x, blockIdx.x, tid, kThreads);
 
@@ -462,20 +529,22 @@ __global__ __launch_bounds__(kThreads) void k_kv_evict_held(KvEvictArgs a) {
     float w[N];
 #pragma unroll
     for (int e = 0; e < N; ++e) {
-      const int32_t t = x.first + r0 + 64 * (e0 + e);
-      const int64_t page = have(e0 + e) ? x.pages.of(t) : -1;
+      const int32_t t = have(e0 + e) ? x.first + r0 + 64 * (e0 + e) : x.first;
+      const int32_t page = x.pages.of(t);
       at[e] = page < 0 ? -1 : x.pages.weight_at(page, x.kh, t);
     }
 #pragma unroll
-    for (int e = 0; e < N; ++e) w[e] = at[e] < 0 ? -__builtin_inff() : a.weights[at[e]];
+    for (int e = 0; e < N; ++e) w[e] = a.weights[at[e] < 0 ? 0 : at[e]];
+#pragma unroll
+    for (int e = 0; e < N; ++e) w[e] = at[e] < 0 ? -__builtin_inff() : w[e];
 #pragma unroll
     for (int e = 0; e < N; ++e) {
-      if (copy && at[e] >= 0 && x.first + r0 + 64 * (e0 + e) < x.behind) a.weights_out[at[e]] = w[e];
+      if (copy && have(e0 + e) && at[e] >= 0 && x.first + r0 + 64 * (e0 + e) < x.behind) a.weights_out[at[e]] = w[e];
       key[e0 + e] = weight_key(w[e]);
     }
   }
   // the last tokens' first chunk, on its way while the others are chosen
-  Moving<D> tail[kHeld];
+  Moving<D, 1> tail;
   read_last<D>(a, x, kept, 0, tail);
   keep_places(a, x, blockIdx.x, tid, kThreads);
   for (int i = tid; i < 3 * kBins; i += kThreads) s_hist[0][i] = 0;
@@ -766,18 +835,11 @@ __global__ __launch_bounds__(256) void k_kv_evict_move(KvEvictArgs a) {
   const int32_t* const from = a.lists + (int64_t)p.row * 2 * a.budget;
   const int32_t* const to = from + a.budget;
   const int32_t moving = row_counts(a, p.row)->moving;
-  const int row = threadIdx.x / kRowLanes, l = threadIdx.x % kRowLanes;
-  constexpr int kSide = 256 / kRowLanes, kDeep = 4;
+  constexpr int kSide = 256 / 4, kDeep = 2;
   for (int32_t i0 = p.part * kSide * kDeep; i0 < moving; i0 += a.parts * kSide * kDeep) {
-    Moving<D> m[kDeep];
-#pragma unroll
-    for (int e = 0; e < kDeep; ++e) {
-      const int32_t i = i0 + e * kSide + row;
-      m[e].to = nullptr;
-      if (i < moving) m[e].read(a, x, kept, from[i], to[i], l);
-    }
-#pragma unroll
-    for (int e = 0; e < kDeep; ++e) m[e].write(a, l);
+    Moving<D, kDeep> m;
+    read_listed<D, kDeep>(a, x, kept, from, to, i0, kSide, moving, m);
+    m.write(a);
   }
 }
 
@@ -790,13 +852,11 @@ __global__ __launch_bounds__(kThreads) void k_kv_evict_last(KvEvictArgs a) {
   const bool overlap = x.n - x.budget < x.last;
   if (!x.over || (overlap && p.part > 0)) return;
   int32_t* const kept = a.kept ? a.kept + (int64_t)p.row * a.budget : nullptr;
-  const int l = threadIdx.x % kRowLanes;
   for (int64_t j0 = (int64_t)p.part * kChunk; j0 < x.last; j0 += (int64_t)(overlap ? 1 : a.parts) * kChunk) {
-    Moving<D> h[kHeld];
+    Moving<D, 1> h;
     read_last<D>(a, x, kept, (int32_t)j0, h);
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) h[i].write(a, l);
+    h.write(a);
   }
 }
 
@@ -863,8 +923,8 @@ hipError_t launch_kv_evict(KvEvictArgs a, int32_t D, const KvEvictPlan& p, int64
   a.parts = p.parts;
   a.lists = static_cast<int32_t*>(workspace);
   a.counts = static_cast<uint8_t*>(workspace) + p.counts_at;
-  // 64 rows a workgroup and turn
-  const int64_t turns = (a.budget + 63) / 64, most = 2048 / a.rows + 1;
+  // 128 rows a workgroup and turn
+  const int64_t turns = (a.budget + 127) / 128, most = 2048 / a.rows + 1;
   a.move_parts = (int32_t)(turns < most ? turns : most);
   const int64_t chunks = (a.last + kChunk - 1) / kChunk;
   a.last_parts = (int32_t)(chunks < most ? chunks : most);
