@@ -79,7 +79,7 @@ struct KvEvictArgs {
   int32_t rows;                // batch * n_kv_heads
   int32_t lengths;             // whether the kernels write the lengths
   int32_t parts;               // of a row; 0: a workgroup does a whole one
-  int32_t move_parts, last_parts;   // for what moves
+  int32_t move_parts;          // for what moves
 };
 constexpr int kKvEvictMostParts = 64;              // of a row
 constexpr int kKvEvictRowBytes = 20736;            // that a row's parts count

@@ -387,7 +387,6 @@ struct Moving {
 
 // The last tokens down by n - budget, kRows at a time from j0 on, in order where old and new places
 // overlap: what they overwrite was read with them or before.
-constexpr int kChunk = kRows;
 
 // how many of N groups of rows, `side` apart, a wave has where `left` rows are left for its workgroup
 __device__ __forceinline__ int groups_of(int32_t left, int side) {
@@ -396,11 +395,12 @@ __device__ __forceinline__ int groups_of(int32_t left, int side) {
 }
 
 template <int D>
-__device__ __forceinline__ void read_last(const KvEvictArgs& a, const Row& x, int32_t* kept, int32_t j0, Moving<D, 1>& h) {
+__device__ __forceinline__ void read_last(const KvEvictArgs& a, const Row& x, int32_t* kept, int32_t j0, int32_t rows,
+                                          Moving<D, 1>& h) {
   const int32_t j = j0 + (int32_t)threadIdx.x / 4;
   const bool live[1] = {j < x.last};
   const int32_t old[1] = {live[0] ? x.n - x.last + j : x.n - 1}, place[1] = {live[0] ? x.behind + j : 0};
-  h.read(a, x, kept, old, place, live, groups_of(x.last - j0, kRows));
+  h.read(a, x, kept, old, place, live, groups_of(x.last - j0, rows));
 }
 
 // Rows i0 + thread / 4, + side, ... of the lists (N of them, those below `moving`)
@@ -435,8 +435,8 @@ template <int D>
 __device__ __forceinline__ void move_last(const KvEvictArgs& a, const Row& x, int32_t* kept, Moving<D, 1>& tail) {
   __syncthreads();                                 // the movers are read
   tail.write(a);
-  for (int32_t j0 = kChunk; j0 < x.last; j0 += kChunk) {
-    read_last<D>(a, x, kept, j0, tail);
+  for (int32_t j0 = kRows; j0 < x.last; j0 += kRows) {
+    read_last<D>(a, x, kept, j0, kRows, tail);
     __syncthreads();
     tail.write(a);
   }
@@ -452,7 +452,7 @@ __device__ __forceinline__ void evict_row(const KvEvictArgs& a, const Row& x, in
   for_keys<true>(a, x, 0, x.rated, tid, kThreads, [](int32_t, uint32_t) {});
   // the last tokens' first chunk, on its way while the others are chosen
   Moving<D, 1> tail;
-  read_last<D>(a, x, kept, 0, tail);
+  read_last<D>(a, x, kept, 0, kRows, tail);
   keep_places(a, x, blockIdx.x, tid, kThreads);
 
   // the smallest kept key, and how many tokens of it are kept
@@ -498,6 +498,101 @@ __device__ __forceinline__ void evict_row(const KvEvictArgs& a, const Row& x, in
   move_last<D>(a, x, kept, tail);
 }
 
+// A run of rated tokens whose keys a wave holds, token r0 + 64 e + lane in key[e] (below `end`)
+template <int KEYS>
+struct Run {
+  int32_t r0, end;             // r0: the lane's
+  uint32_t key[KEYS];
+  uint64_t moves[KEYS], gaps[KEYS];   // lanes whose token moves, or whose place is free
+
+  __device__ __forceinline__ Run(int32_t begin, int32_t upto) {
+    const int32_t wave = (int32_t)(threadIdx.x >> 6), run = ((upto - begin + kWaves - 1) / kWaves + 63) & ~63;
+    const int32_t first = begin + wave * run;
+    r0 = first + (int32_t)(threadIdx.x & 63);
+    end = first + run < upto ? first + run : upto;
+  }
+  __device__ __forceinline__ bool have(int e) const { return r0 + 64 * e < end; }
+
+  // COPY: weights of tokens that may stay where they are go to weights_out
+  template <bool COPY>
+  __device__ __forceinline__ void load(const KvEvictArgs& a, const Row& x) {
+    const bool copy = COPY && a.weights_out && a.weights_out != a.weights;
+    constexpr int N = KEYS < 8 ? KEYS : 8;         // tokens whose loads are side by side
+#pragma unroll
+    for (int e0 = 0; e0 < KEYS; e0 += N) {
+      int64_t at[N];
+      float w[N];
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const int32_t t = have(e0 + e) ? x.first + r0 + 64 * (e0 + e) : x.first;
+        const int32_t page = x.pages.of(t);
+        at[e] = page < 0 ? -1 : x.pages.weight_at(page, x.kh, t);
+      }
+#pragma unroll
+      for (int e = 0; e < N; ++e) w[e] = a.weights[at[e] < 0 ? 0 : at[e]];
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        w[e] = at[e] < 0 ? -__builtin_inff() : w[e];
+        if (copy && have(e0 + e) && at[e] >= 0 && x.first + r0 + 64 * (e0 + e) < x.behind) a.weights_out[at[e]] = w[e];
+        key[e0 + e] = weight_key(w[e]);
+      }
+    }
+  }
+  // the wave's tokens of this key
+  __device__ __forceinline__ int32_t equal(uint32_t border) const {
+    int32_t n = 0;
+#pragma unroll
+    for (int e = 0; e < KEYS; ++e) n += __builtin_popcountll(__builtin_amdgcn_ballot_w64(have(e) && key[e] == border));
+    return n;
+  }
+  // which tokens move and whose places are free, `ties` tokens of the border's key before the run; how many
+  __device__ __forceinline__ void choose(const Row& x, uint32_t border, int32_t wanted, int32_t ties, int32_t& n_moves, int32_t& n_gaps) {
+    const uint64_t below = (1ull << (threadIdx.x & 63)) - 1;
+    n_moves = n_gaps = 0;
+#pragma unroll
+    for (int e = 0; e < KEYS; ++e) {
+      const bool tie = have(e) && x.keep > 0 && key[e] == border;
+      const uint64_t tie_lanes = __builtin_amdgcn_ballot_w64(tie);
+      const bool stays = have(e) && x.keep > 0 &&
+                         (key[e] > border || (tie && ties + __builtin_popcountll(tie_lanes & below) < wanted));
+      ties += __builtin_popcountll(tie_lanes);
+      const int32_t t = x.first + r0 + 64 * e;
+      moves[e] = __builtin_amdgcn_ballot_w64(stays && t >= x.behind);
+      gaps[e] = __builtin_amdgcn_ballot_w64(have(e) && !stays && t < x.behind);
+      n_moves += __builtin_popcountll(moves[e]);
+      n_gaps += __builtin_popcountll(gaps[e]);
+    }
+  }
+  // to the lists, the wave's from numbers i and j on
+  __device__ __forceinline__ void list(const Row& x, int32_t* from, int32_t* to, int32_t i, int32_t j) const {
+    const int lane = threadIdx.x & 63;
+    const uint64_t below = (1ull << lane) - 1;
+#pragma unroll
+    for (int e = 0; e < KEYS; ++e) {
+      const int32_t t = x.first + r0 + 64 * e;
+      if (moves[e] >> lane & 1) from[i + __builtin_popcountll(moves[e] & below)] = t;
+      if (gaps[e] >> lane & 1) to[j + __builtin_popcountll(gaps[e] & below)] = t;
+      i += __builtin_popcountll(moves[e]);
+      j += __builtin_popcountll(gaps[e]);
+    }
+  }
+};
+
+// Of a number that each wave has, those of the waves before this one, and of all (every thread calls it)
+__device__ __forceinline__ uint32_t waves_before(uint32_t x, int32_t* s_waves, uint32_t& all) {
+  const int wave = threadIdx.x >> 6;
+  if ((threadIdx.x & 63) == 0) s_waves[wave] = (int32_t)x;
+  __syncthreads();
+  uint32_t before = 0;
+  all = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    before += w < wave ? (uint32_t)s_waves[w] : 0;
+    all += (uint32_t)s_waves[w];
+  }
+  return before;
+}
+
 // A whole row of up to kThreads * KEYS rated tokens, whose keys stay in registers: each wave has a run of
 // tokens, 64 at a time.  (Rows that the bound did not announce are longer: evict_row.)
 template <int D, int KEYS>
@@ -517,35 +612,11 @@ __global__ __launch_bounds__(kThreads) void k_kv_evict_held(KvEvictArgs a) {
     return;
   }
   int32_t* const kept = a.kept ? a.kept + (int64_t)blockIdx.x * a.budget : nullptr;
-  const int32_t run = ((x.rated + kWaves - 1) / kWaves + 63) & ~63;
-  const int32_t r0 = wave * run + lane, end = wave * run + run < x.rated ? wave * run + run : x.rated;
-  auto have = [&](int e) { return r0 + 64 * e < end; };
-  uint32_t key[KEYS];
-  const bool copy = a.weights_out && a.weights_out != a.weights;
-  constexpr int N = KEYS < 8 ? KEYS : 8;           // tokens whose loads are side by side
-#pragma unroll
-  for (int e0 = 0; e0 < KEYS; e0 += N) {
-    int64_t at[N];
-    float w[N];
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-      const int32_t t = have(e0 + e) ? x.first + r0 + 64 * (e0 + e) : x.first;
-      const int32_t page = x.pages.of(t);
-      at[e] = page < 0 ? -1 : x.pages.weight_at(page, x.kh, t);
-    }
-#pragma unroll
-    for (int e = 0; e < N; ++e) w[e] = a.weights[at[e] < 0 ? 0 : at[e]];
-#pragma unroll
-    for (int e = 0; e < N; ++e) w[e] = at[e] < 0 ? -__builtin_inff() : w[e];
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-      if (copy && have(e0 + e) && at[e] >= 0 && x.first + r0 + 64 * (e0 + e) < x.behind) a.weights_out[at[e]] = w[e];
-      key[e0 + e] = weight_key(w[e]);
-    }
-  }
+  Run<KEYS> run(0, x.rated);
+  run.template load<true>(a, x);
   // the last tokens' first chunk, on its way while the others are chosen
   Moving<D, 1> tail;
-  read_last<D>(a, x, kept, 0, tail);
+  read_last<D>(a, x, kept, 0, kRows, tail);
   keep_places(a, x, blockIdx.x, tid, kThreads);
   for (int i = tid; i < 3 * kBins; i += kThreads) s_hist[0][i] = 0;
   __syncthreads();
@@ -559,7 +630,8 @@ __global__ __launch_bounds__(kThreads) void k_kv_evict_held(KvEvictArgs a) {
       const uint32_t shift = kDigits[pass], mask = pass < 2 ? kBins - 1 : (kBins >> 1) - 1, above = shift + (pass < 2 ? 11 : 10);
 #pragma unroll
       for (int e = 0; e < KEYS; ++e)
-        if (have(e) && (pass == 0 || key[e] >> above == border >> above)) atomicAdd(&s_hist[pass][(key[e] >> shift) & mask], 1);
+        if (run.have(e) && (pass == 0 || run.key[e] >> above == border >> above))
+          atomicAdd(&s_hist[pass][(run.key[e] >> shift) & mask], 1);
       __syncthreads();
       // bins from the largest digit on, two a thread
       const int32_t lo = s_hist[pass][kBins - 2 - 2 * tid], hi = s_hist[pass][kBins - 1 - 2 * tid];
@@ -583,58 +655,19 @@ __global__ __launch_bounds__(kThreads) void k_kv_evict_held(KvEvictArgs a) {
   }
 
   // tokens of the border's key before this wave's run
-  int32_t ties = 0;
-  if (x.keep > 0 && equal > wanted) {
-    int32_t own = 0;
-#pragma unroll
-    for (int e = 0; e < KEYS; ++e) own += __builtin_popcountll(__builtin_amdgcn_ballot_w64(have(e) && key[e] == border));
-    if (lane == 0) s_waves[0][wave] = own;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) ties += w < wave ? s_waves[0][w] : 0;
-  }
-  const uint64_t below = (1ull << lane) - 1;
-  uint64_t mv[KEYS], gp[KEYS];                     // lanes whose token moves, or whose place is free
-  int32_t movers = 0, gaps = 0;
-#pragma unroll
-  for (int e = 0; e < KEYS; ++e) {
-    const bool tie = have(e) && x.keep > 0 && key[e] == border;
-    const uint64_t tie_lanes = __builtin_amdgcn_ballot_w64(tie);
-    const bool stays = have(e) && x.keep > 0 &&
-                       (key[e] > border || (tie && ties + __builtin_popcountll(tie_lanes & below) < wanted));
-    ties += __builtin_popcountll(tie_lanes);
-    const int32_t t = x.first + r0 + 64 * e;
-    mv[e] = __builtin_amdgcn_ballot_w64(stays && t >= x.behind);
-    gp[e] = __builtin_amdgcn_ballot_w64(have(e) && !stays && t < x.behind);
-    movers += __builtin_popcountll(mv[e]);
-    gaps += __builtin_popcountll(gp[e]);
-  }
+  uint32_t ties = 0, all;
+  if (x.keep > 0 && equal > wanted) ties = waves_before((uint32_t)run.equal(border), s_waves[0], all);
+  int32_t movers, gaps;
+  run.choose(x, border, wanted, (int32_t)ties, movers, gaps);
   // both are at most kThreads KEYS < 2^16
-  if (lane == 0) s_waves[1][wave] = movers << 16 | gaps;
-  __syncthreads();
-  uint32_t before = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    before += w < wave ? (uint32_t)s_waves[1][w] : 0;
-    all += (uint32_t)s_waves[1][w];
-  }
-  movers = (int32_t)(before >> 16);
-  gaps = (int32_t)(before & 0xFFFF);
+  const uint32_t before = waves_before((uint32_t)movers << 16 | (uint32_t)gaps, s_waves[1], all);
   const int32_t moving = (int32_t)(all >> 16);
-  auto lists = [&](int32_t* from, int32_t* to) {
-#pragma unroll
-    for (int e = 0; e < KEYS; ++e) {
-      const int32_t t = x.first + r0 + 64 * e;
-      if (mv[e] >> lane & 1) from[movers + __builtin_popcountll(mv[e] & below)] = t;
-      if (gp[e] >> lane & 1) to[gaps + __builtin_popcountll(gp[e] & below)] = t;
-      movers += __builtin_popcountll(mv[e]);
-      gaps += __builtin_popcountll(gp[e]);
-    }
-    __syncthreads();
-    move_listed<D>(a, x, kept, from, to, moving);
-  };
-  if (moving <= kListed) lists(s_hist[0], s_hist[0] + kListed);
-  else lists(a.lists + (int64_t)blockIdx.x * 2 * a.budget, a.lists + (int64_t)blockIdx.x * 2 * a.budget + a.budget);
+  const bool listed = moving <= kListed;
+  int32_t* const from = listed ? s_hist[0] : a.lists + (int64_t)blockIdx.x * 2 * a.budget;
+  int32_t* const to = from + (listed ? kListed : a.budget);
+  run.list(x, from, to, (int32_t)(before >> 16), (int32_t)(before & 0xFFFF));
+  __syncthreads();
+  move_listed<D>(a, x, kept, from, to, moving);
   move_last<D>(a, x, kept, tail);
 }
 
@@ -748,86 +781,100 @@ __global__ __launch_bounds__(kThreads) void k_kv_evict_digits(KvEvictArgs a) {
 }
 
 // The lists
-constexpr int kPartKeys = 9216;                        // of a part, that LDS holds
-
 __global__ __launch_bounds__(kThreads) void k_kv_evict_lists(KvEvictArgs a) {
-  __shared__ int32_t s_waves[kWaves];
+  constexpr int KEYS = 8;                              // of a thread, where a part is as long as was announced
+  __shared__ int32_t s_waves[3][kWaves];
   __shared__ int32_t s_found[3];
-  __shared__ uint32_t s_keys[kPartKeys];
-  __shared__ int32_t s_part[kKvEvictMostParts][4];     // of each part: larger and equal keys, on kept places and behind
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const Parts p(a, blockIdx.x);
   const Row x(a, p.row);
   if (!x.over) return;
   const int32_t r0 = p.begin(a, x, p.part), r1 = p.begin(a, x, p.part + 1);
-  const bool in_lds = r1 - r0 <= kPartKeys;
-  if (in_lds) for_keys<false>(a, x, r0, r1, tid, kThreads, [&](int32_t i, uint32_t k) { s_keys[i - r0] = k; });
-  auto key_of = [&](int32_t i) { return in_lds ? s_keys[i - r0] : x.key(a, i); };
+  const bool held = r1 - r0 <= KEYS * kThreads;
+  Run<KEYS> run(r0, r1);
+  if (held) run.template load<false>(a, x);
   RowCounts* const c = row_counts(a, p.row);
   uint32_t border = 0;
-  int32_t wanted = 0, ties0 = 0, movers = 0, gaps = 0;
+  int32_t wanted = 0, larger[2] = {0, 0}, equal[2] = {0, 0};
+  static_assert(kKvEvictMostParts <= 64, "a lane counts a part");
   if (x.keep > 0) {
     // the third digit has half the bins: threads from kBins / 4 on
     int2 bins = {0, 0};
     if (tid >= kBins / 4) bins = *reinterpret_cast<const int2*>(&c->last[kBins - 2 - 2 * tid]);
-    find_digit(bins.y, bins.x, c->found[1].wanted, s_waves, s_found);
+    find_digit(bins.y, bins.x, c->found[1].wanted, s_waves[0], s_found);
     const int32_t digit = s_found[0];
     border = c->found[1].border | (uint32_t)digit;
     wanted = s_found[1];
-    for (int32_t q = tid >> 1; q < a.parts; q += kThreads / 2) {
-      const int z = tid & 1;
-      const int32_t* const least = part_counts(a, p.row, q)->least[z];
-      const int32_t larger = least[digit + 1], from = least[digit];
-      s_part[q][z] = larger;
-      s_part[q][2 + z] = from - larger;
+    const PartCounts* const q = part_counts(a, p.row, lane < a.parts ? lane : 0);
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      const int32_t from = q->least[z][digit], more = q->least[z][digit + 1];
+      larger[z] = lane < a.parts ? more : 0;
+      equal[z] = lane < a.parts ? from - more : 0;
     }
   }
-  __syncthreads();
-  // what stands before this part, and in all
-  int32_t moving = 0;
-  for (int32_t q = 0, ties = 0; q < a.parts; ++q) {
-    if (q == p.part) {
-      ties0 = ties;
-      movers = moving;
-    }
-    const int32_t q0 = p.begin(a, x, q), q1 = p.begin(a, x, q + 1);
-    int32_t near = x.behind - x.first - q0;             // its tokens on kept ones' places
-    near = near < 0 ? 0 : (near > q1 - q0 ? q1 - q0 : near);
-    int32_t stay = 0;
-    if (x.keep > 0) {
-      // of its ties, in order, those that are still wanted
-      const int32_t open = wanted - ties < 0 ? 0 : wanted - ties;
-      const int32_t t0 = s_part[q][2] < open ? s_part[q][2] : open;
-      const int32_t t1 = s_part[q][3] < open - t0 ? s_part[q][3] : open - t0;
-      stay = s_part[q][0] + t0;
-      moving += s_part[q][1] + t1;
-      ties += s_part[q][2] + s_part[q][3];
-    }
-    if (q < p.part) gaps += near - stay;
-  }
-  if (p.part == 0 && tid == 0) c->moving = moving;
+  // What stands before this part, and in all: lane q counts part q.  Of its ties, in order, those that are
+  // still wanted stay.
+  const int32_t q0 = p.begin(a, x, lane < a.parts ? lane : a.parts), q1 = p.begin(a, x, lane < a.parts ? lane + 1 : a.parts);
+  int32_t near = x.behind - x.first - q0;              // its tokens on kept ones' places
+  near = near < 0 ? 0 : (near > q1 - q0 ? q1 - q0 : near);
+  const int32_t ties_before = sum_upto(equal[0] + equal[1]) - equal[0] - equal[1];
+  const int32_t open = wanted - ties_before < 0 ? 0 : wanted - ties_before;
+  const int32_t stay0 = equal[0] < open ? equal[0] : open, stay1 = equal[1] < open - stay0 ? equal[1] : open - stay0;
+  const int32_t moves = larger[1] + stay1, free_ = near - larger[0] - stay0;
+  const int32_t moves_upto = sum_upto(moves), free_upto = sum_upto(free_);
+  if (p.part == 0 && tid == 63) c->moving = moves_upto;
+  const int32_t movers = __builtin_amdgcn_readlane(moves_upto - moves, p.part);
+  const int32_t gaps = __builtin_amdgcn_readlane(free_upto - free_, p.part);
+  int32_t ties = __builtin_amdgcn_readlane(ties_before, p.part);
+  const bool tied = __builtin_amdgcn_readlane(equal[0] + equal[1], p.part) > 0;
 
-  const int32_t run = ((r1 - r0 + kWaves - 1) / kWaves + 63) & ~63;
-  const int32_t w0 = r0 + wave * run < r1 ? r0 + wave * run : r1, w1 = w0 + run < r1 ? w0 + run : r1;
-  int32_t ties = 0, all;
-  if (x.keep > 0 && s_part[p.part][2] + s_part[p.part][3] > 0)
-    for (int32_t i = w0 + lane; i < w1; i += 64) ties += key_of(i) == border;
-  ties0 += __builtin_amdgcn_readfirstlane(sum_before(ties, s_waves, all));
-  int32_t m = 0, g = 0;
-  walk(x, w0, w1, border, wanted, ties0, key_of, m, g, [](int32_t, bool, int32_t, bool, int32_t) {});
-  m = movers + __builtin_amdgcn_readfirstlane(sum_before(lane == 0 ? m : 0, s_waves, all));
-  g = gaps + __builtin_amdgcn_readfirstlane(sum_before(lane == 0 ? g : 0, s_waves, all));
   int32_t* const from = a.lists + (int64_t)p.row * 2 * a.budget;
   int32_t* const to = from + a.budget;
-  walk(x, w0, w1, border, wanted, ties0, key_of, m, g, [&](int32_t t, bool moves, int32_t i, bool gap, int32_t j) {
-    if (moves) from[i] = t;
+  uint32_t all;
+  if (held) {
+    if (tied) ties += (int32_t)waves_before((uint32_t)run.equal(border), s_waves[1], all);
+    int32_t m, g;
+    run.choose(x, border, wanted, ties, m, g);
+    const uint32_t before = waves_before((uint32_t)m << 16 | (uint32_t)g, s_waves[2], all);
+    run.list(x, from, to, movers + (int32_t)(before >> 16), gaps + (int32_t)(before & 0xFFFF));
+    return;
+  }
+  auto key_of = [&](int32_t i) { return x.key(a, i); };
+  const int32_t size = ((r1 - r0 + kWaves - 1) / kWaves + 63) & ~63;
+  const int32_t w0 = r0 + wave * size < r1 ? r0 + wave * size : r1, w1 = w0 + size < r1 ? w0 + size : r1;
+  int32_t own = 0, m = 0, g = 0;
+  for (int32_t i = w0 + lane; i < w1; i += 64) own += x.keep > 0 && key_of(i) == border;
+  ties += __builtin_amdgcn_readfirstlane(sum_before(own, s_waves[0], own));
+  walk(x, w0, w1, border, wanted, ties, key_of, m, g, [](int32_t, bool, int32_t, bool, int32_t) {});
+  int32_t sum;
+  m = movers + __builtin_amdgcn_readfirstlane(sum_before(lane == 0 ? m : 0, s_waves[0], sum));
+  g = gaps + __builtin_amdgcn_readfirstlane(sum_before(lane == 0 ? g : 0, s_waves[0], sum));
+  walk(x, w0, w1, border, wanted, ties, key_of, m, g, [&](int32_t t, bool mv, int32_t i, bool gap, int32_t j) {
+    if (mv) from[i] = t;
     if (gap) to[j] = t;
   });
 }
 
-// Movers, and the last tokens where their old and new places do not overlap
+// Movers, and the last tokens.  The last tokens' new places may hold movers, those below the budget: first
+// in the list.  Where old and new places of the last tokens do not overlap, they go in chunks of 64, and the
+// workgroup of a chunk moves the movers of its new places before; else the first workgroup moves all of
+// these in order.
+constexpr int kMoveThreads = 256, kMoveRows = kMoveThreads / 4, kMoveDeep = 2;
+
+// How many of the movers are below token t
+__device__ __forceinline__ int32_t movers_below(const int32_t* from, int32_t moving, int32_t t) {
+  int32_t lo = 0, hi = moving;
+  while (lo < hi) {
+    const int32_t mid = (lo + hi) >> 1;
+    if (from[mid] < t) lo = mid + 1;
+    else hi = mid;
+  }
+  return lo;
+}
+
 template <int D>
-__global__ __launch_bounds__(256) void k_kv_evict_move(KvEvictArgs a) {
+__global__ __launch_bounds__(kMoveThreads) void k_kv_evict_move(KvEvictArgs a) {
   const Parts p(a, blockIdx.x);
   const Row x(a, p.row);
   if (!x.over) return;
@@ -835,29 +882,26 @@ __global__ __launch_bounds__(256) void k_kv_evict_move(KvEvictArgs a) {
   const int32_t* const from = a.lists + (int64_t)p.row * 2 * a.budget;
   const int32_t* const to = from + a.budget;
   const int32_t moving = row_counts(a, p.row)->moving;
-  constexpr int kSide = 256 / 4, kDeep = 2;
-  for (int32_t i0 = p.part * kSide * kDeep; i0 < moving; i0 += a.parts * kSide * kDeep) {
-    Moving<D, kDeep> m;
-    read_listed<D, kDeep>(a, x, kept, from, to, i0, kSide, moving, m);
+  const bool overlap = x.n - x.budget < x.last;
+  const int32_t chunks = (x.last + kMoveRows - 1) / kMoveRows;
+  auto movers = [&](int32_t i0, int32_t i1, int32_t step) {
+    for (; i0 < i1; i0 += step) {
+      Moving<D, kMoveDeep> m;
+      read_listed<D, kMoveDeep>(a, x, kept, from, to, i0, kMoveRows, i1, m);
+      m.write(a);
+    }
+  };
+  for (int32_t c = p.part; c < chunks && (!overlap || p.part == 0); c += overlap ? 1 : a.parts) {
+    const int32_t place = x.behind + c * kMoveRows;
+    movers(movers_below(from, moving, place), movers_below(from, moving, place + kMoveRows < x.budget ? place + kMoveRows : x.budget),
+           kMoveRows * kMoveDeep);
+    Moving<D, 1> m;
+    read_last<D>(a, x, kept, c * kMoveRows, kMoveRows, m);
+    __syncthreads();                               // these movers and tokens are read
     m.write(a);
   }
-}
-
-// The last tokens: a part every parts-th chunk where old and new places do not overlap, else the first
-// part all of them, in order
-template <int D>
-__global__ __launch_bounds__(kThreads) void k_kv_evict_last(KvEvictArgs a) {
-  const Parts p(a, blockIdx.x);
-  const Row x(a, p.row);
-  const bool overlap = x.n - x.budget < x.last;
-  if (!x.over || (overlap && p.part > 0)) return;
-  int32_t* const kept = a.kept ? a.kept + (int64_t)p.row * a.budget : nullptr;
-  for (int64_t j0 = (int64_t)p.part * kChunk; j0 < x.last; j0 += (int64_t)(overlap ? 1 : a.parts) * kChunk) {
-    Moving<D, 1> h;
-    read_last<D>(a, x, kept, (int32_t)j0, h);
-    __syncthreads();
-    h.write(a);
-  }
+  const int32_t rest = movers_below(from, moving, x.budget);
+  movers(rest + p.part * kMoveRows * kMoveDeep, moving, a.parts * kMoveRows * kMoveDeep);
 }
 
 // The lengths, where they are written over those that the workgroups read
@@ -886,11 +930,7 @@ hipError_t evict(KvEvictArgs a, bool short_rows, hipStream_t s) {
   if (e != hipSuccess) return e;
   KvEvictArgs m = a;
   m.parts = a.move_parts;
-  hipLaunchKernelGGL((k_kv_evict_move<D>), dim3((unsigned)(m.rows * m.parts)), dim3(256), 0, s, m);
-  e = hipGetLastError();
-  if (e != hipSuccess || a.last == 0) return e;
-  m.parts = a.last_parts;
-  hipLaunchKernelGGL((k_kv_evict_last<D>), dim3((unsigned)(m.rows * m.parts)), threads, 0, s, m);
+  hipLaunchKernelGGL((k_kv_evict_move<D>), dim3((unsigned)(m.rows * m.parts)), dim3(kMoveThreads), 0, s, m);
   return hipGetLastError();
 }
 
@@ -923,11 +963,8 @@ hipError_t launch_kv_evict(KvEvictArgs a, int32_t D, const KvEvictPlan& p, int64
   a.parts = p.parts;
   a.lists = static_cast<int32_t*>(workspace);
   a.counts = static_cast<uint8_t*>(workspace) + p.counts_at;
-  // 128 rows a workgroup and turn
-  const int64_t turns = (a.budget + 127) / 128, most = 2048 / a.rows + 1;
+  const int64_t turns = (a.budget + kMoveRows * kMoveDeep - 1) / (kMoveRows * kMoveDeep), most = 2048 / a.rows + 1;
   a.move_parts = (int32_t)(turns < most ? turns : most);
-  const int64_t chunks = (a.last + kChunk - 1) / kChunk;
-  a.last_parts = (int32_t)(chunks < most ? chunks : most);
   const bool short_rows = max_kv_len - a.first - a.last <= 4 * kThreads;
   const hipError_t e = D == 64 ? evict<64>(a, short_rows, s) : (D == 128 ? evict<128>(a, short_rows, s) : evict<256>(a, short_rows, s));
   if (e != hipSuccess || a.lengths) return e;
