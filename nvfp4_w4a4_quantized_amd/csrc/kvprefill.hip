@@ -29,12 +29,13 @@
 // instead of 452.
 //
 // What bounds it: matrix and vector instructions of two waves per SIMD that only partly overlap.  8192
-// tokens, 32 / 8 heads of 128: 527 to 617 us by card, 890 to 1043 TFLOP/s (a large f16 matrix product
-// reaches 1095 to 1193 there, at the clock that its power leaves); the matrix unit is busy 47 % of the
+// tokens, 32 / 8 heads of 128: 519 us, 1060 TFLOP/s, on a fast card, 17 % more on a slow one (a large f16
+// matrix product reaches 1095 to 1193 there, at the clock that its power leaves); the matrix unit is busy 47 % of the
 // cycles, the vector unit 54 %, LDS 36 %, and waves wait 32 %.  Head dimension 256, whose accumulators leave no
-// registers for the pipeline (20 or 26 spill, four or five accesses of them in the loop over the
-// tiles): 3 sequences of 300 to 2048 new tokens of up to 16384 862 to 952 us, 879 to 971 TFLOP/s, the
-// matrix unit 42 % busy, waves waiting 45 %.  64 columns a wave at one wave per SIMD (512 registers)
+// registers for the pipeline (11 or 16 spill, outside of the products): 3 sequences of 300 to 2048 new
+// tokens of up to 16384 764 us, 1096 TFLOP/s.  What a tile's loads return is looked at only when the
+// tile is decoded: the check of a page id and the halves of a row of scales, put together right after
+// their loads, made every wave wait for these (826 us).  64 columns a wave at one wave per SIMD (512 registers)
 // took 845 us where this took 606.
 #include <type_traits>
 
@@ -65,10 +66,17 @@ constexpr int kVTile = D * kVRow<D>;
 // after the tiles: the columns' score factors where a wave's are wide
 template <int D>
 constexpr int kFactors = 2 * (kKTile<D> + kVTile<D>);
+// of trees with D = 256, then the last of each lane's query operands: the masks' code leaves no registers
+// for it, and read back from scratch memory it waited for the loads of the next tile (8 trees of 64 to 128
+// nodes over up to 16384 tokens 243 / 229 us)
+template <int D>
+constexpr int kLdsQ = D == 256 ? 1 : 0;
+template <int D>
+constexpr int kQueries = kFactors<D> + 4 * kPrefillCols;
 // after those, of a tree's tile: the first token that any column attends to, and the bits of the
 // tree's tokens that any column attends to
 template <int D>
-constexpr int kTreeFirst = kFactors<D> + 4 * kPrefillCols;
+constexpr int kTreeFirst = kQueries<D> + kLdsQ<D> * 16 * 64 * kPrefillWaves;
 template <int D>
 constexpr int kTreeAny = kTreeFirst<D> + 16;
 // and its rows' windows' first tokens and, where they are not too many, their words
@@ -76,9 +84,10 @@ template <int D>
 constexpr int kTreeFloor = kTreeAny<D> + 8 * kMaxTreeWords;
 template <int D>
 constexpr int kTreeBits = kTreeFloor<D> + 4 * kPrefillCols;
-constexpr int kTreeStaged = 2048;
+template <int D>
+constexpr int kTreeStaged = D == 256 ? 1024 : 2048;
 template <int D, bool TREE>
-constexpr int kLdsBytes = TREE ? kTreeBits<D> + 8 * kTreeStaged : kTreeFirst<D>;
+constexpr int kLdsBytes = TREE ? kTreeBits<D> + 8 * kTreeStaged<D> : kQueries<D>;
 
 template <typename T>
 __device__ __forceinline__ __attribute__((address_space(3))) T& lds_at(uint32_t at) {
@@ -287,14 +296,23 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
     const int32_t w1 = col0 + 32 < col_end ? col0 + 32 : col_end;
     const Span sp = span_of<TREE>(seq, w0, w1, a.by_group, a.window);
 
-    // loads of tile s: this wave's granule, its page id known one tile ahead
+    // an address that the compiler does not take out of the loop: with every chunk's address
+    // in a register of its own the kernel spills
+    auto fresh = [](uint32_t x) {
+      asm volatile("" : "+v"(x));
+      return x;
+    };
+
+    // loads of tile s: this wave's granule, its page id known one tile ahead (as the table has it: looked
+    // at only when it is used, it is not waited for here, and with it the loads before it)
     auto page_of = [&](int32_t s) -> int32_t {
       int32_t pg = (begin + s * TOK + 16 * gran) >> a.geom.page_shift;
       pg = pg < last_page ? pg : last_page;
-      const int32_t id = a.table[(int64_t)b * a.ld_table + pg];
-      return id < 0 ? 0 : (id >= a.geom.n_pages ? (int32_t)a.geom.n_pages - 1 : id);
+      return a.table[(int64_t)b * a.ld_table + pg];
     };
     auto granule = [&](int32_t s, int32_t id) {
+      id = __builtin_amdgcn_readfirstlane(id);
+      id = id < 0 ? 0 : (id >= a.geom.n_pages ? (int32_t)a.geom.n_pages - 1 : id);
       int32_t gr = (begin + s * TOK) / 16 + gran;
       gr = gr < last_granule ? gr : last_granule;
       return a.cache + (int64_t)id * a.geom.page_bytes +
@@ -303,16 +321,18 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
     // the quad of tokens and part of a granule's values that this lane decodes
     const int quad = lane >> 4, part = lane & 15;
     // (D = 256: a wave holds either)
-    uint32_t rk[KD] = {}, rv_[D == 256 ? 1 : KD] = {}, ksc = 0, vsc_ = 0;
+    uint32_t rk[KD] = {}, rv_[D == 256 ? 1 : KD] = {}, ksc = 0, ksc_far = 0, vsc_ = 0;
     uint32_t* const rv = D == 256 ? rk : rv_;
     uint32_t& vsc = D == 256 ? ksc : vsc_;
     auto load_k = [&](int32_t s, int32_t id) {
       const uint8_t* p = granule(s, id);
       if constexpr (D == 256) {          // a quarter of either half of a token's row
-        const uint8_t *c = p + (lane >> 2) * 128 + (lane & 3) * 16, *f = p + 8 * D + (lane >> 2) * 16 + (lane & 3) * 2;
+        const uint32_t i = fresh(lane);
+        const uint8_t *c = p + ((i >> 2) * 128 + (i & 3) * 16), *f = p + 8 * D + ((i >> 2) * 16 + (i & 3) * 2);
         read_dwords<4>(c, rk);
         read_dwords<4>(c + 64, rk + 4);
-        ksc = *reinterpret_cast<const uint16_t*>(f) | (uint32_t)*reinterpret_cast<const uint16_t*>(f + 8) << 16;
+        ksc = *reinterpret_cast<const uint16_t*>(f);
+        ksc_far = *reinterpret_cast<const uint16_t*>(f + 8);   // (put together here, they were waited for)
       } else {                           // a quarter of a token's row
         read_dwords<KD>(p + lane * (D / 8), rk);
         ksc = D == 64 ? p[8 * D + lane] : *reinterpret_cast<const uint16_t*>(p + 8 * D + 2 * lane);
@@ -320,8 +340,9 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
     };
     auto load_v = [&](int32_t s, int32_t id) {
       const uint8_t* p = granule(s, id);
-      read_dwords<KD>(p + 9 * D + (16 * quad + part) * (D / 8), rv);
-      vsc = *reinterpret_cast<const uint32_t*>(p + 17 * D + (quad * (D / 16) + part * D / 256) * 4);
+      const uint32_t i = D == 256 ? fresh(lane) : lane;
+      read_dwords<KD>(p + 9 * D + i * (D / 8), rv);
+      vsc = *reinterpret_cast<const uint32_t*>(p + 17 * D + ((i >> 4) * (D / 16) + (i & 15) * D / 256) * 4);
       const int32_t first = begin + s * TOK + 16 * gran;
       if (!TREE && (first < span.lo || first + 16 > seq.n)) vsc = live_scales(vsc, first + 4 * quad, span.lo, seq.n);
     };
@@ -345,7 +366,7 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
     };
     // decode dword i of the loaded keys: a 16-byte chunk of a token's row
     auto decode_k = [&](uint32_t kb, int i) {               // kb: the lane's first chunk in the tile
-      const f16x2 sc = bcast(scale_pair_f16(D == 256 ? ksc >> (16 * (i / 4)) : ksc), D == 64 ? 0 : (i >> 1) & 1);
+      const f16x2 sc = bcast(scale_pair_f16(D == 256 && i >= 4 ? ksc_far : ksc), D == 64 ? 0 : (i >> 1) & 1);
       lds_at<f16x8>(kb + 16 * i + (i < 4 ? 0 : 192)) = decode8_f16(rk[i], sc);
     };
     // decode byte i of the four tokens' words of the loaded values: elements 2 i and 2 i + 1
@@ -385,7 +406,7 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
     // TREE: the rows' words and windows, and what of the tree any of them attends to
     const int32_t row_first = col_first / a.by_group, words = TREE ? tree_words(a, seq) : 0;
     const int32_t rows = (col_end - 1) / a.by_group - row_first + 1;
-    const bool staged = TREE && rows * words <= kTreeStaged;
+    const bool staged = TREE && rows * words <= kTreeStaged<D>;
     auto bits_of = [&](int32_t row, int32_t w) -> uint64_t {
       if (staged) return w >= 0 && w < words ? lds_at<uint64_t>(lds + kTreeBits<D> + 8 * (row * words + w)) : 0;
       return tree_word(a, seq, seq.q0 + row_first + row, w);
@@ -473,7 +494,15 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
     auto read_v = [&](uint32_t vb, int b, int i) {
       vf[i % (PF + 1)] = lds_at<f16x8>(vb + 32 * kVRow<D> * (i % NB) + 32 * (2 * b + i / NB));
     };
-    auto score_piece = [&](f32x16& sc, int i) { sc = mfma32(kf[i % (PF + 1)], qf[i], sc); };
+    auto query = [&](int i) { return lds + kQueries<D> + 16 * (threadIdx.x + 64 * kPrefillWaves * (KS - 1 - i)); };
+    constexpr int QL = TREE ? kLdsQ<D> : 0;
+    if constexpr (QL > 0) {
+#pragma unroll
+      for (int i = KS - QL; i < KS; ++i) lds_at<f16x8>(query(i)) = qf[i];   // each lane reads what it wrote
+    }
+    auto score_piece = [&](f32x16& sc, int i) {
+      sc = mfma32(kf[i % (PF + 1)], i < KS - QL ? qf[i] : lds_at<f16x8>(query(i)), sc);
+    };
     auto output_piece = [&](const f16x8 p[2], int i) { acc[i % NB] = mfma32(vf[i % (PF + 1)], p[i / NB], acc[i % NB]); };
     // moves the reference M for the block from token t0 on; returns what the earlier sums are
     // scaled by
@@ -524,12 +553,6 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
     };
     auto k_tile = [&](int32_t s) { return lds + (uint32_t)((s & 1) * kKTile<D>); };
     auto v_tile = [&](int32_t s) { return lds + (uint32_t)(2 * kKTile<D> + (s & 1) * kVTile<D>); };
-    // an address that the compiler does not take out of the loop: with every chunk's address
-    // in a register of its own the kernel spills
-    auto fresh = [](uint32_t x) {
-      asm volatile("" : "+v"(x));
-      return x;
-    };
 
     if (steps > 0) {
       if (D != 256 || wave < 4) {
@@ -616,7 +639,7 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
             stage(k_tile(s), 3, v_tile(s), 1, t0 + 64, sb, sa, pa, pb, nothing);
             __syncthreads();
             mask_v(s + 1);
-          const uint32_t vw = fresh(v_tile(s + 1) + vwbase);
+            const uint32_t vw = fresh(v_tile(s + 1) + vwbase);
             stage(k_tile(s + 1), 0, v_tile(s), 2, t0 + 96, sa, sb, pb, pa, [&](int i) {
               if (i < KS / 2) decode_v(vw, i);
             });
@@ -625,7 +648,7 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
               id_next = page_of(s + 3);
             }
           }
-  #pragma unroll
+#pragma unroll
           for (int i = 0; i < KS; ++i) {
             read_v(v_tile(steps - 1) + vbase, 3, i);
             output_piece(pb, i);
@@ -644,7 +667,7 @@ __global__ __launch_bounds__(64 * kPrefillWaves, 2) void k_kv_prefill(KvAttnArgs
             if (s + 2 < steps) load_k(s + 2, id_next);
             __syncthreads();
             mask_v(s + 1);
-          const uint32_t vw = fresh(v_tile(s + 1) + vwbase);
+            const uint32_t vw = fresh(v_tile(s + 1) + vwbase);
             stage(k_tile(s + 1), b0, v_tile(s), b0, t0 + 32, sa, sb, pb, pa, [&](int i) {
               if (i < KS / 2) decode_v(vw, i);
             });
