@@ -6,6 +6,8 @@
 // its columns, so that a lane has scores of one token and sums its weights in place; a token's
 // sum is in one wave's registers, or eight waves' that are joined in a fixed order: a call gives
 // the same bits every time.  Exponents, weights and sums are fp32.
+#include <type_traits>
+
 #include "kv_device.hpp"
 
 namespace nvfp4 {
@@ -23,7 +25,8 @@ __device__ __forceinline__ f32x4 mfma16(f16x8 a, f16x8 b, f32x4 c) {
 // 128 c + 32 g + 8 m + j (D = 256), 16 g + 8 m + j (D = 64)
 template <int D>
 struct Keys {
-  uint32_t k[D / 32], ks[D == 256 ? 2 : 1];
+  uint32_t k[D / 32];
+  uint16_t ks[D == 256 ? 2 : 1];         // (widened where it is loaded, it was waited for)
 };
 
 template <int D>
@@ -131,84 +134,99 @@ __global__ __launch_bounds__(64 * kWeightWaves, D == 256 ? 2 : 4) void k_kv_weig
   for (int64_t at = (int64_t)((int)blockIdx.x - item * w.tiles) * kWeightWaves + wave; at * run < seq.n;
        at += (int64_t)w.tiles * kWeightWaves) {
     const int32_t begin = (int32_t)(at * run), end = begin + run < seq.n ? begin + run : seq.n;
-    const int32_t last_granule = (seq.n - 1) >> 4;
+    const int32_t last_granule = (end - 1) >> 4;
     // page of token begin + 16 lane (a run is at most 1024 tokens)
     int32_t t_page = begin + 16 * lane;
     t_page = t_page < seq.n ? t_page : seq.n - 1;
     const int32_t id = a.table[(int64_t)b * a.ld_table + (t_page >> a.geom.page_shift)];
     const int32_t pages = id < 0 ? 0 : (id >= a.geom.n_pages ? (int32_t)a.geom.n_pages - 1 : id);
+    // the lane's own token of a step, 16 g + r, and its weight
+    float* own = nullptr;
+    float old = 0.0f;
+    auto issue_old = [&](int32_t t0) {
+      const int32_t t = t0 + lane, i = ((t0 - begin) >> 4) + g;
+      const int32_t page = __shfl(id, i < 63 ? i : 63);
+      const bool there = t < end && page >= 0 && page < a.geom.n_pages;
+      const uint32_t slot = (uint32_t)t & ((1u << a.geom.page_shift) - 1);
+      own = w.weights + (there ? (((int64_t)page * hkv + kh) << a.geom.page_shift) + slot : 0);
+      old = *own;
+      own = there ? own : nullptr;
+    };
+    auto put = [&](int32_t t0, float total) {
+      if (own) *own = t0 + lane < c0 && w.decay != 0.0f ? __builtin_fmaf(w.decay, old, total) : total;
+    };
+    // where no query attends to anything of the run, no key is read, but weights fade
+    const QueryRange all = queries_of(seq, begin, end - begin, a.window);
+    if (all.first >= all.end) {
+      if (w.decay != 1.0f)
+        for (int32_t t0 = begin; t0 < end; t0 += kWaveTokens) {
+          issue_old(t0);
+          put(t0, 0.0f);
+        }
+      continue;
+    }
     Keys<D> key[NG];
     auto issue = [&](int32_t t0, int u) {
-      const int32_t page = __builtin_amdgcn_readlane(pages, (t0 - begin) / 16 + u);
-      int32_t gr = t0 / 16 + u;
+      int32_t gr = (t0 >> 4) + u;
       gr = gr < last_granule ? gr : last_granule;         // past the end: the last granule again
+      const int32_t page = __builtin_amdgcn_readlane(pages, gr - (begin >> 4));
       load_keys<D>(granule_buffer<D>(a, page, kh * per_head + (gr & (per_head - 1))), lane, key[u]);
     };
-    // the lane's own token of a step, 16 g + r, and its weight
-    float* own_next = nullptr;
-    float old_next = 0.0f;
-    auto issue_old = [&](int32_t t0) {
-      const int32_t t = t0 + lane;
-      const int32_t page = __shfl(id, (t0 - begin) / 16 + g);
-      own_next = nullptr;
-      if (t < seq.n && page >= 0 && page < a.geom.n_pages) {
-        own_next = w.weights + ((((int64_t)page * hkv + kh) << a.geom.page_shift) + (t & ((1 << a.geom.page_shift) - 1)));
-        if (t < c0 && w.decay != 0.0f) old_next = *own_next;
-      }
-    };
-    // where no query attends to anything of the run, nothing is read, but weights fade
-    const QueryRange all = queries_of(seq, begin, end - begin, a.window);
-    const bool any = all.first < all.end;
-    if (!any && w.decay == 1.0f) continue;
-    if (any) {
+    auto go = [&](auto once) {
+      for (int32_t t0 = begin; t0 < end; t0 += kWaveTokens) {
+        const QueryRange q = queries_of(seq, t0, kWaveTokens, a.window);
+        // every query token attends to every token of the step
+        const bool full = t0 + kWaveTokens - 1 <= c0 && (!a.window || t0 > seq.n - 1 - a.window);
+        float total = 0.0f;
 #pragma unroll
-      for (int u = 0; u < NG; ++u) issue(begin, u);
-    }
-    issue_old(begin);
-    if (any && cols <= 16) prepare(0);
-    for (int32_t t0 = begin; t0 < end; t0 += kWaveTokens) {
-      const QueryRange q = queries_of(seq, t0, kWaveTokens, a.window);
-      // every query token attends to every token of the step
-      const bool full = t0 + kWaveTokens - 1 <= c0 && (!a.window || t0 > seq.n - 1 - a.window);
-      float total = 0.0f;
-#pragma unroll
-      for (int u = 0; u < NG; ++u) {
-        float sum = 0.0f;
-        if (q.first < q.end) {
+        for (int u = 0; u < NG; ++u) {
           f16x8 kf[KC];
+          if (!decltype(once)::value) issue(t0, u);
 #pragma unroll
           for (int c = 0; c < KC; ++c) kf[c] = key_frag<D>(key[u], c);
+          // decoded here, so that the next step's keys come into the registers that these leave: with a copy of
+          // them at the step's end, that waits for them
+#pragma unroll
+          for (int c = 0; c < KC; ++c) asm volatile("" : "+v"(kf[c]));
+          __builtin_amdgcn_sched_barrier(0);
+          if (decltype(once)::value) issue(t0 + kWaveTokens, u);
           const int32_t t = t0 + 16 * u + r;
-          for (int32_t col0 = cols <= 16 ? 0 : q.first * group; col0 < q.end * group; col0 += 16) {
-            if (cols > 16) prepare(col0);
+          float sum = 0.0f;
+          auto add = [&] {
             f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int c = 0; c < KC; ++c)
 #pragma unroll
               for (int e = 0; e < TERMS; ++e) s = mfma16(qf[e][c], kf[c], s);
-            if (full) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) sum += __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], csc[i], -sub[i]));
-            } else {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const bool sees = t <= pos[i] && (!a.window || t > pos[i] - a.window);
-                const float x = sees ? __builtin_fmaf(s[i], csc[i], -sub[i]) : -__builtin_inff();
-                sum += __builtin_amdgcn_exp2f(x);
-              }
+            for (int i = 0; i < 4; ++i) {
+              float x = __builtin_fmaf(s[i], csc[i], -sub[i]);
+              if (!full) x = t <= pos[i] && (!a.window || t > pos[i] - a.window) ? x : -__builtin_inff();
+              sum += __builtin_amdgcn_exp2f(x);
             }
-          }
+          };
+          if constexpr (decltype(once)::value) add();
+          else
+            for (int32_t col0 = q.first * group; col0 < q.end * group; col0 += 16) {
+              prepare(col0);
+              add();
+            }
           sum = sum_xor32(sum_xor16(sum));
+          if (g == u) total = sum;
         }
-        // the next step's keys, into the registers that these leave
-        if (any && t0 + kWaveTokens < end) issue(t0 + kWaveTokens, u);
-        if (g == u) total = sum;
+        if (q.first < q.end || w.decay != 1.0f) put(t0, total);
+        issue_old(t0 + kWaveTokens);
       }
-      float* const own = own_next;
-      const float old = old_next;
-      if (t0 + kWaveTokens < end) issue_old(t0 + kWaveTokens);
-      if (own && (q.first < q.end || w.decay != 1.0f))
-        *own = t0 + lane < c0 && w.decay != 0.0f ? __builtin_fmaf(w.decay, old, total) : total;
+    };
+    if (cols <= 16) {
+#pragma unroll
+      for (int u = 0; u < NG; ++u) issue(begin, u);
+      issue_old(begin);
+      prepare(0);
+      go(std::true_type{});
+    } else {
+      issue_old(begin);
+      go(std::false_type{});
     }
   }
 }
