@@ -4,8 +4,8 @@
 //
 // Both kernels take query columns (query token x head) as the rows of a matrix product and tokens as
 // its columns, so that a lane has scores of one token and sums its weights in place; a token's
-// sum is in one wave's registers, or eight waves' that are joined in a fixed order: a call gives
-// the same bits every time.  Exponents, weights and sums are fp32.
+// sum is in one wave's registers, or eight waves' that are joined in a fixed order: a call of
+// the same sizes and bounds gives the same bits every time.  Exponents, weights and sums are fp32.
 #include <type_traits>
 
 #include "kv_device.hpp"
@@ -71,7 +71,9 @@ __device__ __forceinline__ QueryRange queries_of(const SeqInfo& s, int32_t t0, i
 // Few query columns: one token a sequence as a rule.  Bound by the keys' bytes, so a wave goes through
 // a run of tokens, 64 at a time, with the next 64 tokens' codes in flight; S on the f16 MFMA
 // 16x16x32 with the numerics of kvattn.hip, 16 query columns at a time (more of them, which the
-// bounds did not announce, are prepared again for every step).
+// bounds did not announce, are prepared again for every step).  32 sequences of up to 8192 tokens, 32 / 8
+// heads of 128: 27 us, 3.6 TB/s (unlike lengths: the longest runs last); of 32768 124 us, 5.2 TB/s, as fast as
+// a copy.
 template <int D, bool F32>
 __global__ __launch_bounds__(64 * kWeightWaves, D == 256 ? 2 : 4) void k_kv_weights(KvWeightsArgs w) {
   constexpr int KC = D / 32, TERMS = F32 ? 2 : 1, NG = kWaveTokens / 16;
@@ -237,6 +239,10 @@ __global__ __launch_bounds__(64 * kWeightWaves, D == 256 ? 2 : 4) void k_kv_weig
 // waves of a workgroup have different tokens, or every qs-th tile of the same ones, whose sums
 // are joined in LDS at the end.  Tiles go from memory to LDS by asynchronous loads, each wave's its own,
 // one ahead: no barrier in the loop.  fp32 queries go as three bf16 terms, which hold all their bits.
+//
+// 8192 tokens, 32 / 8 heads of 128: 288 us, 956 TFLOP/s (a large bf16 matrix product reaches 1188); 256, 3
+// sequences of 300 to 2048 new tokens of up to 16384 495 us, 846; fp32, 4096 tokens 228 us, 302, a third of the
+// products' terms.
 //
 // A tile is whole query tokens, as many as 32 rows hold (heads 32 s .. of one token where the
 // group has more), so that its rows' places are the same in every tile.
@@ -593,8 +599,10 @@ hipError_t plan(KvWeightsArgs w, int64_t max_q_len, int64_t max_kv_len, hipStrea
   const int64_t m = max_q_len < w.a.T ? max_q_len : w.a.T;
   const int64_t n = max_kv_len < 1 ? 1 : max_kv_len;
   if (m * group <= 16) {
-    // runs so long that about all waves are there at once, four a SIMD
-    const int64_t steps = pairs * ((n + kWaveTokens - 1) / kWaveTokens), each = steps / 4096;
+    // Runs so long that about all waves are there at once, four a SIMD; one, where a wave's columns are long.  By
+    // 4096 / 2048 / 1024 waves, us: head dimension 128, 32 x up to 8192 27 / 29 / 30, fp32 8 x up to 8192 11 / 11 /
+    // 13; 64, 32 x up to 8192 13 / 14 / 19; 256, 16 x up to 32768 36 / 32 / 32, fp32 4 x up to 32768 22 / 14 / 13.
+    const int64_t steps = pairs * ((n + kWaveTokens - 1) / kWaveTokens), each = steps / (D == 256 ? 1024 : 4096);
     w.split = -1;
     w.steps = (int32_t)(each < 1 ? 1 : (each > 16 ? 16 : each));
     const int64_t tokens = (int64_t)w.steps * kWaveTokens * kWeightWaves;

@@ -196,6 +196,35 @@ def test_weights_match_oracle(nv, dtype, kv, m, Hq, Hkv, D, page, window, decay)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kv,m,Hq,Hkv,D,window", [
+    ([70, 33], [20, 5], 40, 1, 64, 0),                               # more heads of a group than a tile's rows
+    ([150], [9], 66, 2, 128, 12),
+    ([300, 2], [40, 2], 36, 1, 256, 0),
+    ([2100], [17], 1, 1, 128, 0),                                    # one head
+])
+def test_weights_of_wide_groups(nv, dtype, kv, m, Hq, Hkv, D, window):
+    p = WeightProblem(nv, kv, m, Hq, Hkv, D, 32, dtype, seed=Hq + D)
+    lse = p.lse_of(nv, window)
+    p.check_weights(p.run_weights(nv, lse, window, 0.75), lse, window, 0.75)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D,batch", [(64, 40), (128, 40), (256, 20)])
+@pytest.mark.parametrize("window", [0, 100])
+def test_weights_of_runs(nv, dtype, D, batch, window):
+    """Sequences so many that a wave has several steps of 64 tokens, of any length."""
+    rng = np.random.default_rng(D)
+    kv = rng.integers(1, 600, batch).tolist()
+    kv[0], kv[1] = 128, 129
+    p = WeightProblem(nv, kv, [1] * batch, 4, 4, D, 16, dtype, seed=D)
+    lse = p.lse_of(nv, window)
+    # as announced, and as for lengths of 20000 (a run of 3 to 16 steps)
+    for most in (None, 20000, 150000):
+        got = p.run_weights(nv, lse, window, 0.5, hints=most and (1, most))
+        p.check_weights(got, lse, window, 0.5)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("hints", [(1, 1), (500, 100000), (2, 3)])
 def test_weights_with_other_bounds(nv, dtype, hints):
     p = WeightProblem(nv, [1200, 77], [40, 60], 6, 2, 64, 16, dtype, seed=8)
@@ -371,6 +400,69 @@ def test_evict_long(nv, kv, budget, first, last, kind):
     s = Eviction(nv, kv, 1, 64, 128, kind, seed=budget)
     s.run(nv, budget, first, last)
     s.check(budget, first, last)
+
+
+@pytest.mark.parametrize("n,budget,first,last,most", [
+    (45000, 700, 3, 64, 100),                            # one workgroup a row, its keys not in registers
+    (45000, 44000, 3, 1200, 16384),
+    (70001, 3000, 0, 100, 17000),                        # parts far longer than announced
+    (70001, 69000, 10, 2000, 20000),
+    (30000, 29999, 0, 3000, 40000),                      # parts, the last tokens move by one
+    (30000, 4000, 3000, 1000, 30000),                    # nothing but the first and the last ones
+    (17000, 16400, 0, 16400, 17000),
+])
+@pytest.mark.parametrize("kind", ["ties", "equal", "odd", "signed"])
+def test_evict_long_beside_its_bounds(nv, n, budget, first, last, most, kind):
+    s = Eviction(nv, [n, 200], 1, 64, 128, kind, seed=budget)
+    s.run(nv, budget, first, last, most=most)
+    s.check(budget, first, last)
+
+
+@pytest.mark.parametrize("out", ["none", "other"])
+@pytest.mark.parametrize("D,Hkv", [(128, 2), (256, 1)])
+def test_evict_long_outputs(nv, out, D, Hkv):
+    s = Eviction(nv, [20000, 5000, 0], Hkv, D, 64, "ties", seed=D)
+    s.run(nv, 6000, 2, 333, out, kept=out != "none", in_place=True)
+    s.check(6000, 2, 333, out)
+
+
+def test_evict_in_parts_replayed(nv):
+    """The launches of a long eviction in a graph, replayed with eager calls between."""
+    kv = [20000, 700]
+    s = Eviction(nv, kv, 1, 64, 64, "ties", seed=12)
+    s.run(nv, 2000, 2, 100, in_place=True)
+    ws = torch.empty(nv.nvfp4_kv_evict_workspace(2, 1, 2000, 20000), dtype=torch.uint8, device="cuda")
+    kept = torch.zeros(2, 1, 2000, dtype=torch.int32, device="cuda")
+
+    def call():
+        nv.nvfp4_kv_evict(s.cache, s.dweights, s.dtable, s.kv_len, 64, 2000, s.kv_len, 20000, ws, keep_first=2, keep_last=100,
+                          weights_out=s.dweights, kept=kept)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for i, seed in enumerate((1, 2, 3, 4)):
+        e = Eviction(nv, kv, 1, 64, 64, "ties", seed=12)
+        e.weights = draw_weights(np.random.default_rng(seed), e.weights.shape, ("ties", "signed")[i % 2])
+        for name, x in (("cache", e.bytes), ("dweights", e.weights), ("kv_len", np.array(e.kv, dtype=np.int32))):
+            getattr(s, name).copy_(dev(x))
+        torch.cuda.synchronize()
+        call() if i == 2 else graph.replay()
+        torch.cuda.synchronize()
+        e.cache, e.dweights, e.w_out, e.kept, e.len_out = s.cache, s.dweights, s.dweights, kept, s.kv_len
+        e.check(2000, 2, 100)
+
+
+def test_two_evictions_at_once(nv):
+    """Calls of different caches on two streams, each with its own workspace."""
+    a, b = (Eviction(nv, [20000, 3000], 1, 64, 64, kind, seed=i) for i, kind in enumerate(("plain", "ties")))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    a.run(nv, 1500, 1, 50)
+    with torch.cuda.stream(side):
+        b.run(nv, 1500, 1, 50)
+    torch.cuda.synchronize()
+    a.check(1500, 1, 50)
+    b.check(1500, 1, 50)
 
 
 def test_evict_many_short_sequences(nv):

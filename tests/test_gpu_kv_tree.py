@@ -192,6 +192,32 @@ def test_widest_masks(nv, Hq, words):
     p.check_tree(p.run_tree(nv, hints=(300, 700), mask=wide[:, :words]), rows=[0, 6, 63, 64, 150, 255, 256, 299])
 
 
+@pytest.mark.parametrize("D,Hq,m", [(64, 2, 600), (128, 1, 700), (256, 2, 330)])
+@pytest.mark.parametrize("window", [0, 50])
+def test_words_that_are_not_kept(nv, D, Hq, m, window):
+    """Trees of so many words that a tile's are read where they are used."""
+    p = TreeProblem(nv, [m + 100], [m], Hq, 1, D, 16, "bf16", seed=D + m, kinds=("any",))
+    p.check_tree(p.run_tree(nv, window), window, rows=[0, 63, 64, 128, 255, 256, m // 2, m - 1])
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,m", [(64, 4, 2, 3), (128, 8, 1, 11), (128, 16, 1, 12), (256, 8, 1, 20)])
+@pytest.mark.parametrize("window", [0, 19])
+def test_more_sequences_than_lanes(nv, D, Hq, Hkv, m, window):
+    """66 to 70 trees, of up to 24, 88, 192 and 160 columns a kv head."""
+    rng = np.random.default_rng(m)
+    kv = rng.integers(m, 200, 66 + D % 5).tolist()
+    p = TreeProblem(nv, kv, rng.integers(0, m + 1, len(kv)).tolist(), Hq, Hkv, D, 16, "bf16", seed=m, kinds=("tree", "any"))
+    p.check_tree(p.run_tree(nv, window, hints=(m, 200)), window, rows=[0, 1, m // 2, m - 1])
+
+
+@pytest.mark.parametrize("Hq,Hkv,m", [(8, 1, 9), (8, 1, 16), (8, 1, 17), (4, 1, 32), (4, 1, 33), (3, 1, 41), (9, 1, 14), (5, 1, 26)])
+@pytest.mark.parametrize("kv", [[190], [900, 60, 400] * 24])
+def test_columns_about_a_tile(nv, Hq, Hkv, m, kv):
+    """Just below and above the columns where another kernel or form of it takes over, whole and cut."""
+    p = TreeProblem(nv, kv, [m] * len(kv), Hq, Hkv, 64, 16, "bf16", seed=Hq * m)
+    p.check_tree(p.run_tree(nv), rows=[0, m // 2, m - 1])
+
+
 @pytest.mark.parametrize("Hq,m", [(4, 9), (16, 40)])
 @pytest.mark.parametrize("window", [0, 30])
 def test_nodes_that_no_row_sees_may_be_unwritten(nv, Hq, m, window):
@@ -259,6 +285,28 @@ def test_graph_replays(nv, Hq, m):
         p.mask = mask
         p.check_tree((o.float().cpu().numpy().reshape(p.T, Hq, 128).astype(np.float64), lse.cpu().numpy().astype(np.float64)),
                      rows=[0, 2, 8, 19, 63])
+
+
+def test_two_calls_at_once(nv):
+    """Two trees on two streams, each call with its own workspace."""
+    a, b = (TreeProblem(nv, [5000, 300], [m, 9], 8, 2, 128, 32, "bf16", seed=m) for m in (40, 12))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    outs = []
+    for p, stream in ((a, None), (b, side)):
+        q = p.q.reshape(p.T, -1).cuda()
+        torch.cuda.synchronize()
+        o, lse = torch.empty_like(q), torch.empty(p.T, 8, device="cuda")
+        ws = torch.empty(nv.nvfp4_kv_attention_workspace(p.T, 2, 8, 2, 128, 40, 5000), dtype=torch.uint8, device="cuda")
+        outs.append((p, stream, q, o, lse, ws))
+    torch.cuda.synchronize()
+    for p, stream, q, o, lse, ws in outs:
+        nv.nvfp4_kv_tree_attention(q, p.cache, p.table, p.kv_len, p.dkg, p.dvg, 32, o, 5000, p.mask, ws, cu_q=p.cu, max_q_len=40,
+                                   lse=lse, stream=stream)
+    torch.cuda.synchronize()
+    for p, _, _, o, lse, _ in outs:
+        p.check_tree((o.float().cpu().numpy().reshape(p.T, 8, 128).astype(np.float64), lse.cpu().numpy().astype(np.float64)),
+                     rows=[0, 5, 39])
 
 
 def test_on_another_stream(nv):
