@@ -6,7 +6,7 @@
 // value codes, D/16 single bytes of value scales.  A wave moves 16 rows: four lanes a row its keys, in a load
 // of both (16 bytes a lane at D = 128), then 16 lanes a row the parts of the values, in four, and D/16
 // lanes a row their scales.  What counts is the number of such loads and stores, not their bytes (with
-// 16 lanes a row for everything, twice as many: evict_step 19 us, not 17).
+// 16 lanes a row for everything, twice as many: 32 x 8 heads of about 4130 tokens to 4096 19 us, not 17).
 #include "kernel_common.hpp"
 #include "kv_launch.hpp"
 
@@ -197,8 +197,12 @@ __global__ __launch_bounds__(kThreads) void k_kv_accept(KvAcceptArgs a) {
 //   lowest ones;
 //   kept tokens behind the places of the kept (movers) and free places, ascending, to two lists;
 //   mover i to free place i, then the last tokens down.
-// A workgroup does a whole row, its keys in LDS; rows that are too long for that, or too few, are
-// cut into parts, and each pass over the keys is a launch.
+// A workgroup does a whole row of up to 16384 rated tokens, their keys in registers; rows for which longer ones are announced
+// are cut into parts, and each pass over the keys is a launch.  What bounds it: short rows by the latency of
+// their steps, each of which waits for the one before (weights, three histograms, lists, rows: 32 x 8 heads
+// of about 4130 tokens to 4096 17 us, of which reading the weights and moving 34 rows a head take 6 at a
+// copy's rate); long ones by that of six launches (2 x 8 heads of up to 131072 tokens to 16384 83 us) and by the sectors of
+// what moves: a row's bytes lie in 27 pieces at D = 128, and about 2.5 times as many are moved.
 constexpr uint32_t kDigits[3] = {21, 10, 0};
 constexpr int kBins = 2048;
 
@@ -862,13 +866,19 @@ __global__ __launch_bounds__(kThreads) void k_kv_evict_lists(KvEvictArgs a) {
 // these in order.
 constexpr int kMoveThreads = 256, kMoveRows = kMoveThreads / 4, kMoveDeep = 2;
 
-// How many of the movers are below token t
+// How many of the movers, which ascend, are below token t: a lane looks at every 64th part of what is left, as
+// each look waits for memory (one lane's search, of 14 looks: 2 x 8 heads of up to 131072 87 us, not 83)
 __device__ __forceinline__ int32_t movers_below(const int32_t* from, int32_t moving, int32_t t) {
-  int32_t lo = 0, hi = moving;
-  while (lo < hi) {
-    const int32_t mid = (lo + hi) >> 1;
-    if (from[mid] < t) lo = mid + 1;
-    else hi = mid;
+  int32_t lo = 0, left = moving;                     // `lo` of them are, and of the `left` next ones some
+  while (left > 0) {
+    const int32_t part = (left + 63) >> 6, i = (int32_t)(threadIdx.x & 63) * part;
+    // the first of each part
+    const bool below = i < left && from[lo + (i < left ? i : 0)] < t;
+    const int32_t parts = __builtin_popcountll(__builtin_amdgcn_ballot_w64(below));
+    if (parts == 0) break;
+    const int32_t skip = (parts - 1) * part + 1;     // the last such one, too
+    lo += skip;
+    left = part - 1 < left - skip ? part - 1 : left - skip;
   }
   return lo;
 }
@@ -949,7 +959,9 @@ KvEvictPlan kv_evict_plan(int32_t batch, int32_t n_kv_heads, int64_t budget, int
   const int64_t rows = (int64_t)batch * n_kv_heads;
   p.counts_at = (rows * 2 * budget * (int64_t)sizeof(int32_t) + 255) & ~255ll;
   p.workspace = p.counts_at;
-  // Parts of 8192 tokens, where a workgroup's registers do not hold a row's keys, and a launch takes them
+  // Parts of 8192 tokens, where a workgroup's registers do not hold a row's keys, and a launch takes them.  By
+  // 4096 / 8192 / 16384, us: 2 x 8 heads of up to 131072 106 / 87 / 104, 1 x 8 of 32768 47 / 50 / 67, 48 x 8 of 20000
+  // 324 / 264 / 261.
   const int64_t parts = (max_kv_len + 8191) / 8192;
   p.parts = (int32_t)(parts < kKvEvictMostParts ? parts : kKvEvictMostParts);
   if (max_kv_len <= 16 * kThreads || rows * p.parts > kv_most_blocks(kThreads)) p.parts = 0;
