@@ -511,7 +511,7 @@ NVFP4_API int32_t nvfp4_kv_accept(uint8_t* cache, int64_t n_pages, int32_t page_
  *   key_weights  device fp32 [n_pages][n_kv_heads][page_size], 16-byte aligned: a weight for each slot
  *                and kv head.  The pages of a call's sequences must be each sequence's alone.
  * Products are those of the attention; an exponent is off by up to about 2^-23 of |scale <q, k>| +
- * |lse|, which the rounding of lse alone may cost.  Sums are in the same order in every call.
+ * |lse|, which the rounding of lse alone may cost.  A call of the same sizes and bounds gives the same bits.
  * A weight whose page is not in the cache is not written.
  */
 NVFP4_API int32_t nvfp4_kv_attention_weights(const void* q, int32_t dtype, int64_t ldq, int64_t T, int32_t n_q_heads,

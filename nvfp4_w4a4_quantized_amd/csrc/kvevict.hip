@@ -197,12 +197,12 @@ __global__ __launch_bounds__(kThreads) void k_kv_accept(KvAcceptArgs a) {
 //   lowest ones;
 //   kept tokens behind the places of the kept (movers) and free places, ascending, to two lists;
 //   mover i to free place i, then the last tokens down.
-// A workgroup does a whole row of up to 16384 rated tokens, their keys in registers; rows for which longer ones are announced
-// are cut into parts, and each pass over the keys is a launch.  What bounds it: short rows by the latency of
+// A workgroup does a whole row of up to 16384 rated tokens, their keys in registers; where longer rows are
+// announced, they are cut into parts, and each pass over the keys is a launch.  What bounds it: short rows by the latency of
 // their steps, each of which waits for the one before (weights, three histograms, lists, rows: 32 x 8 heads
-// of about 4130 tokens to 4096 17 us, of which reading the weights and moving 34 rows a head take 6 at a
+// of about 4130 tokens to 4096 17 us, of which reading the weights and moving about 290 rows a head take 6 at a
 // copy's rate); long ones by that of six launches (2 x 8 heads of up to 131072 tokens to 16384 83 us) and by the sectors of
-// what moves: a row's bytes lie in 27 pieces at D = 128, and about 2.5 times as many are moved.
+// what moves: a row's bytes lie in 26 pieces at D = 128, and about 2.5 times as many are moved.
 constexpr uint32_t kDigits[3] = {21, 10, 0};
 constexpr int kBins = 2048;
 
@@ -964,8 +964,9 @@ KvEvictPlan kv_evict_plan(int32_t batch, int32_t n_kv_heads, int64_t budget, int
   // 324 / 264 / 261.
   const int64_t parts = (max_kv_len + 8191) / 8192;
   p.parts = (int32_t)(parts < kKvEvictMostParts ? parts : kKvEvictMostParts);
-  if (max_kv_len <= 16 * kThreads || rows * p.parts > kv_most_blocks(kThreads)) p.parts = 0;
+  if (max_kv_len <= 16 * kThreads) p.parts = 0;
   if (p.parts) p.workspace += rows * (kKvEvictRowBytes + (int64_t)p.parts * kKvEvictPartBytes);
+  if (rows * p.parts > kv_most_blocks(kThreads)) p.parts = 0;
   return p;
 }
 
