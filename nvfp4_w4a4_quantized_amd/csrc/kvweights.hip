@@ -422,20 +422,24 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv_weights_many(KvWeight
         auto weight = [&](const f32x16& score, float (&part)[4], int i) {
           part[i % 4] += __builtin_amdgcn_exp2f(__builtin_fmaf(score[i], csc, -sub[i]));
         };
+        // rows that attend to a lane's token are neighbours: those of the query tokens from its own place on, before
+        // the window leaves it behind
         auto add_some = [&](const f32x16& score, int32_t tmin, float& to) {
-          const int32_t t = tmin + r;
-          int row0 = 4 * h;
-          asm volatile("" : "+v"(row0));           // rare: the rows' tokens are not kept through the loop
+          int32_t d = tmin + r - c0 - tok0;        // the tile's query tokens before the token
+          d = d < kTileRows ? d : kTileRows;
+          int32_t gone = a.window ? d + a.window : kTileRows;
+          gone = gone < 0 ? 0 : (gone < kTileRows ? gone : kTileRows);
+          d = d < 0 ? 0 : d;
+          const int32_t lo = SLICED ? (d ? kTileRows : 0) : d * group, upto = SLICED ? (gone ? kTileRows : 0) : gone * group;
+          const int32_t hi = upto < have ? upto : have, row0 = 4 * h - lo;
+          const uint32_t count = hi > lo ? hi - lo : 0;
 #pragma unroll
           for (int i4 = 0; i4 < 4; ++i4) {
             if (8 * i4 >= have) continue;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int row = row0 + 8 * i4 + e;
-              const int32_t pos = c0 + tok0 + (SLICED ? 0 : row / a.by_group);
-              const bool sees = row < have && t <= pos && (!a.window || t > pos - a.window);
               const float y = __builtin_fmaf(score[4 * i4 + e], csc, -sub[4 * i4 + e]);
-              to += sees ? __builtin_amdgcn_exp2f(y) : 0.0f;
+              to += __builtin_amdgcn_exp2f((uint32_t)(row0 + 8 * i4 + e) < count ? y : -__builtin_inff());
             }
           }
         };
