@@ -147,7 +147,8 @@ struct KvWeightsArgs {
   // the plan
   int32_t tiles;               // workgroups per sequence and kv head
   int32_t steps;               // few query columns: 64 tokens each, of a wave's run
-  int32_t split;               // many: log2 of the waves that share tokens; few: -1
+  int32_t split;               // many: log2 of the waves that share tokens; few: minus the
+                               // blocks of 16 columns that a wave holds
   FastDiv by_tiles;
 };
 constexpr int64_t kKvWeightsMostLd = 1 << 23;      // elements between query rows: a tile's offsets have 32 bits

@@ -68,14 +68,14 @@ __device__ __forceinline__ QueryRange queries_of(const SeqInfo& s, int32_t t0, i
   return r;
 }
 
-// Few query columns: one token a sequence as a rule.  Bound by the keys' bytes, so a wave goes through
+// Few query columns: one token a sequence, or a path of a few.  Bound by the keys' bytes, so a wave goes through
 // a run of tokens, 64 at a time, with the next 64 tokens' codes in flight; S on the f16 MFMA
-// 16x16x32 with the numerics of kvattn.hip, 16 query columns at a time (more of them, which the
-// bounds did not announce, are prepared again for every step).  32 sequences of up to 8192 tokens, 32 / 8
+// 16x16x32 with the numerics of kvattn.hip, up to NB blocks of 16 query columns, which stay in registers (more of
+// them, which the bounds did not announce, are prepared again for every step).  32 sequences of up to 8192 tokens, 32 / 8
 // heads of 128: 27 us, 3.6 TB/s (unlike lengths: the longest runs last); of 32768 124 us, 5.2 TB/s, as fast as
 // a copy.
-template <int D, bool F32>
-__global__ __launch_bounds__(64 * kWeightWaves, D == 256 ? 2 : 4) void k_kv_weights(KvWeightsArgs w) {
+template <int D, bool F32, int NB>
+__global__ __launch_bounds__(64 * kWeightWaves, D == 256 || NB == 4 ? 2 : (NB == 2 ? 3 : 4)) void k_kv_weights(KvWeightsArgs w) {
   constexpr int KC = D / 32, TERMS = F32 ? 2 : 1, NG = kWaveTokens / 16;
   const KvAttnArgs& a = w.a;
   const int lane = threadIdx.x & 63;
@@ -91,11 +91,11 @@ __global__ __launch_bounds__(64 * kWeightWaves, D == 256 ? 2 : 4) void k_kv_weig
   const float kg = a.k_gscale[kh];
   const int32_t run = w.steps * kWaveTokens;
 
-  // the block of columns in registers: A operand, row r; results' rows 4 g + i
-  f16x8 qf[TERMS][KC];
-  float csc[4], sub[4];
-  int32_t pos[4];
-  auto prepare = [&](int32_t col0) {
+  // the blocks of columns in registers: A operand, row r; results' rows 4 g + i
+  f16x8 qf[NB][TERMS][KC];
+  float csc[NB][4], sub[NB][4];
+  int32_t pos[NB][4];
+  auto prepare = [&](int32_t col0, int nb) {
     int32_t col = col0 + r;
     const bool past = col >= cols;
     col = past ? cols - 1 : col;
@@ -121,14 +121,14 @@ __global__ __launch_bounds__(64 * kWeightWaves, D == 256 ? 2 : 4) void k_kv_weig
       for (int e = 0; e < 8; ++e) {
         const float x = v[c][e] * up;
         const _Float16 hi = (_Float16)x;
-        qf[0][c][e] = hi;
-        if constexpr (F32) qf[TERMS - 1][c][e] = (_Float16)(x - (float)hi);
+        qf[nb][0][c][e] = hi;
+        if constexpr (F32) qf[nb][TERMS - 1][c][e] = (_Float16)(x - (float)hi);
       }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      csc[i] = __shfl(csc_r, 4 * g + i);
-      sub[i] = __shfl(sub_r, 4 * g + i);
-      pos[i] = c0 + __shfl(qi, 4 * g + i);
+      csc[nb][i] = __shfl(csc_r, 4 * g + i);
+      sub[nb][i] = __shfl(sub_r, 4 * g + i);
+      pos[nb][i] = c0 + __shfl(qi, 4 * g + i);
     }
   };
 
@@ -194,25 +194,29 @@ __global__ __launch_bounds__(64 * kWeightWaves, D == 256 ? 2 : 4) void k_kv_weig
           if (decltype(once)::value) issue(t0 + kWaveTokens, u);
           const int32_t t = t0 + 16 * u + r;
           float sum = 0.0f;
-          auto add = [&] {
+          auto add = [&](int nb) {
             f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int c = 0; c < KC; ++c)
 #pragma unroll
-              for (int e = 0; e < TERMS; ++e) s = mfma16(qf[e][c], kf[c], s);
+              for (int e = 0; e < TERMS; ++e) s = mfma16(qf[nb][e][c], kf[c], s);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              float x = __builtin_fmaf(s[i], csc[i], -sub[i]);
-              if (!full) x = t <= pos[i] && (!a.window || t > pos[i] - a.window) ? x : -__builtin_inff();
+              float x = __builtin_fmaf(s[i], csc[nb][i], -sub[nb][i]);
+              if (!full) x = t <= pos[nb][i] && (!a.window || t > pos[nb][i] - a.window) ? x : -__builtin_inff();
               sum += __builtin_amdgcn_exp2f(x);
             }
           };
-          if constexpr (decltype(once)::value) add();
-          else
+          if constexpr (decltype(once)::value) {
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+              if (nb == 0 || 16 * nb < cols) add(nb);
+          } else {
             for (int32_t col0 = q.first * group; col0 < q.end * group; col0 += 16) {
-              prepare(col0);
-              add();
+              prepare(col0, 0);
+              add(0);
             }
+          }
           sum = sum_xor32(sum_xor16(sum));
           if (g == u) total = sum;
         }
@@ -220,11 +224,12 @@ __global__ __launch_bounds__(64 * kWeightWaves, D == 256 ? 2 : 4) void k_kv_weig
         issue_old(t0 + kWaveTokens);
       }
     };
-    if (cols <= 16) {
+    if (cols <= 16 * NB) {
 #pragma unroll
       for (int u = 0; u < NG; ++u) issue(begin, u);
       issue_old(begin);
-      prepare(0);
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) prepare(16 * nb, nb);
       go(std::true_type{});
     } else {
       issue_old(begin);
@@ -240,8 +245,8 @@ __global__ __launch_bounds__(64 * kWeightWaves, D == 256 ? 2 : 4) void k_kv_weig
 // are joined in LDS at the end.  Tiles go from memory to LDS by asynchronous loads, each wave's its own,
 // one ahead: no barrier in the loop.  fp32 queries go as three bf16 terms, which hold all their bits.
 //
-// 8192 tokens, 32 / 8 heads of 128: 288 us, 956 TFLOP/s (a large bf16 matrix product reaches 1188); 256, 3
-// sequences of 300 to 2048 new tokens of up to 16384 495 us, 846; fp32, 4096 tokens 228 us, 302, a third of the
+// 8192 tokens, 32 / 8 heads of 128: 274 us, 1002 TFLOP/s (a large bf16 matrix product reaches 1188); 256, 3
+// sequences of 300 to 2048 new tokens of up to 16384 478 us, 875; fp32, 4096 tokens 220 us, 312, a third of the
 // products' terms.
 //
 // A tile is whole query tokens, as many as 32 rows hold (heads 32 s .. of one token where the
@@ -588,10 +593,20 @@ hipError_t launch_many(const KvWeightsArgs& w, int64_t blocks, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Blocks of 16 columns of the kernel for few, as far as registers hold them.  Many / few, us, 32 / 8 heads of
+// 128: 32 columns, 8 x 4096 11.4 / 10.4, 32 x up to 8192 57 / 39, 1 x 300 7.3 / 5.9; 64 columns, 8 x 4096 14.6 / 16.4,
+// 32 x up to 8192 70 / 56; 36 (48 / 8 heads, 24 x up to 6001) 39 / 28; fp32, 32 columns 16.9 / 16.1, head dimension
+// 64, 64 columns 13.3 / 11.8; 256, 32 columns 8 x 8192 10.4 / 10.9.
+constexpr int few_blocks(int D, bool F32) { return D == 64 || (D == 128 && !F32) ? 4 : (D == 256 && F32 ? 1 : 2); }
+
 template <int D, bool F32>
 hipError_t launch(const KvWeightsArgs& w, int64_t blocks, hipStream_t s) {
   if (w.split < 0) {
-    hipLaunchKernelGGL((k_kv_weights<D, F32>), dim3((unsigned)blocks), dim3(64 * kWeightWaves), 0, s, w);
+    const dim3 grid((unsigned)blocks), threads(64 * kWeightWaves);
+    constexpr int MOST = few_blocks(D, F32);
+    if (w.split == -1) hipLaunchKernelGGL((k_kv_weights<D, F32, 1>), grid, threads, 0, s, w);
+    else if (w.split == -2) hipLaunchKernelGGL((k_kv_weights<D, F32, MOST < 2 ? 1 : 2>), grid, threads, 0, s, w);
+    else hipLaunchKernelGGL((k_kv_weights<D, F32, MOST>), grid, threads, 0, s, w);
     return hipGetLastError();
   }
   return w.a.by_group.d > kTileRows ? launch_many<D, F32, true>(w, blocks, s) : launch_many<D, F32, false>(w, blocks, s);
@@ -602,12 +617,15 @@ hipError_t plan(KvWeightsArgs w, int64_t max_q_len, int64_t max_kv_len, hipStrea
   const int64_t pairs = (int64_t)w.a.batch * w.a.geom.n_kv_heads, group = w.a.by_group.d;
   const int64_t m = max_q_len < w.a.T ? max_q_len : w.a.T;
   const int64_t n = max_kv_len < 1 ? 1 : max_kv_len;
-  if (m * group <= 16) {
-    // Runs so long that about all waves are there at once, four a SIMD; one, where a wave's columns are long.  By
-    // 4096 / 2048 / 1024 waves, us: head dimension 128, 32 x up to 8192 27 / 29 / 30, fp32 8 x up to 8192 11 / 11 /
-    // 13; 64, 32 x up to 8192 13 / 14 / 19; 256, 16 x up to 32768 36 / 32 / 32, fp32 4 x up to 32768 22 / 14 / 13.
-    const int64_t steps = pairs * ((n + kWaveTokens - 1) / kWaveTokens), each = steps / (D == 256 ? 1024 : 4096);
-    w.split = -1;
+  if (m * group <= 16 * few_blocks(D, F32)) {
+    // Runs so long that about all waves are there at once, four a SIMD; two or one, where a wave's columns are more or
+    // longer and it takes longer to bring them.  By 4096 / 2048 / 1024 waves, us: head dimension 128, 32 x up to 8192 27 / 29 / 30,
+    // fp32 8 x up to 8192 11 / 11 / 13; 64, 32 x up to 8192 13 / 14 / 19; 256, 16 x up to 32768 36 / 32 / 32, fp32 4 x up
+    // to 32768 22 / 14 / 13; 128 with 32 columns 8 x 4096 13 / 10 / 11, with 64 24 / 16 / 17, 24 x up to 6001 with 36
+    // 31 / 28 / 45.
+    const int64_t steps = pairs * ((n + kWaveTokens - 1) / kWaveTokens);
+    const int64_t each = steps / (D == 256 ? 1024 : (m * group > 16 ? 2048 : 4096));
+    w.split = m * group <= 16 ? -1 : (m * group <= 32 ? -2 : -4);
     w.steps = (int32_t)(each < 1 ? 1 : (each > 16 ? 16 : each));
     const int64_t tokens = (int64_t)w.steps * kWaveTokens * kWeightWaves;
     w.tiles = kv_planned_tiles((n + tokens - 1) / tokens, pairs, 64 * kWeightWaves);

@@ -225,6 +225,17 @@ def test_weights_of_runs(nv, dtype, D, batch, window):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("Hq,m", [(4, 4), (4, 5), (4, 8), (3, 11), (4, 16), (1, 17), (1, 33), (1, 64), (5, 13)])
+def test_weights_of_paths(nv, dtype, D, Hq, m):
+    """Up to one, two and four blocks of 16 query columns, and just past them; some sequences have fewer."""
+    p = WeightProblem(nv, [300, 70, 64, 1000], [m, m - 1, 1, m], Hq, 1, D, 16, dtype, seed=D + m)
+    for window, hints in ((0, None), (20, None), (0, (m, 200000))):
+        lse = p.lse_of(nv, window)
+        p.check_weights(p.run_weights(nv, lse, window, 0.5, hints=hints), lse, window, 0.5)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("hints", [(1, 1), (500, 100000), (2, 3)])
 def test_weights_with_other_bounds(nv, dtype, hints):
     p = WeightProblem(nv, [1200, 77], [40, 60], 6, 2, 64, 16, dtype, seed=8)
