@@ -74,19 +74,20 @@ struct KvEvictArgs {
   int32_t* kept;               // optional [batch][n_kv_heads][budget]
   int32_t* kv_len_out;
   int32_t* lists;              // [rows][2][budget]: what moves, and where to (workspace)
+  int32_t* moving;             // [rows]: entries of the lists (workspace)
   void* counts;                // of the rows, and of their parts (workspace)
   // the plan
   int32_t rows;                // batch * n_kv_heads
   int32_t lengths;             // whether the kernels write the lengths
   int32_t parts;               // of a row; 0: a workgroup does a whole one
-  int32_t move_parts;          // for what moves
+  int32_t move_parts;          // for what moves; 0: the same workgroup moves it
 };
 constexpr int kKvEvictMostParts = 64;              // of a row
 constexpr int kKvEvictRowBytes = 20736;            // that a row's parts count
 constexpr int kKvEvictPartBytes = 8448;            // and each of them
 struct KvEvictPlan {
   int32_t parts;
-  int64_t counts_at;           // byte offset in the workspace
+  int64_t moving_at, counts_at;   // byte offsets in the workspace
   int64_t workspace;           // bytes
 };
 KvEvictPlan kv_evict_plan(int32_t batch, int32_t n_kv_heads, int64_t budget, int64_t max_kv_len);

@@ -197,7 +197,8 @@ __global__ __launch_bounds__(kThreads) void k_kv_accept(KvAcceptArgs a) {
 //   lowest ones;
 //   kept tokens behind the places of the kept (movers) and free places, ascending, to two lists;
 //   mover i to free place i, then the last tokens down.
-// A workgroup does a whole row of up to 16384 rated tokens, their keys in registers; where longer rows are
+// A workgroup does a whole row of up to 16384 rated tokens, their keys in registers (and moves what moves, or another
+// launch does where workgroups are few and that is much); where longer rows are
 // announced, they are cut into parts, and each pass over the keys is a launch.  What bounds it: short rows by the latency of
 // their steps, each of which waits for the one before (weights, three histograms, lists, rows: 32 x 8 heads
 // of about 4130 tokens to 4096 17 us, of which reading the weights and moving about 290 rows a head take 6 at a
@@ -448,8 +449,8 @@ __device__ __forceinline__ void move_last(const KvEvictArgs& a, const Row& x, in
 }
 
 // A whole row of any length, longer than the bound announced: its keys are read again and again.
-// s_hist [kBins]: the histograms
-template <int D>
+// s_hist [kBins]: the histograms.  APART: what moves is listed, and moved by k_kv_evict_move
+template <int D, bool APART>
 __device__ __forceinline__ void evict_row(const KvEvictArgs& a, const Row& x, int32_t* s_hist, int32_t* s_waves, int32_t* s_found) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   int32_t* const kept = a.kept ? a.kept + (int64_t)blockIdx.x * a.budget : nullptr;
@@ -457,7 +458,7 @@ __device__ __forceinline__ void evict_row(const KvEvictArgs& a, const Row& x, in
   for_keys<true>(a, x, 0, x.rated, tid, kThreads, [](int32_t, uint32_t) {});
   // the last tokens' first chunk, on its way while the others are chosen
   Moving<D, 1> tail;
-  read_last<D>(a, x, kept, 0, kRows, tail);
+  if constexpr (!APART) read_last<D>(a, x, kept, 0, kRows, tail);
   keep_places(a, x, blockIdx.x, tid, kThreads);
 
   // the smallest kept key, and how many tokens of it are kept
@@ -498,9 +499,13 @@ __device__ __forceinline__ void evict_row(const KvEvictArgs& a, const Row& x, in
     if (moves) from[i] = t;
     if (gap) to[j] = t;
   });
-  __syncthreads();
-  move_listed<D>(a, x, kept, from, to, moving);
-  move_last<D>(a, x, kept, tail);
+  if constexpr (APART) {
+    if (tid == 0) a.moving[blockIdx.x] = moving;
+  } else {
+    __syncthreads();
+    move_listed<D>(a, x, kept, from, to, moving);
+    move_last<D>(a, x, kept, tail);
+  }
 }
 
 // A run of rated tokens whose keys a wave holds, token r0 + 64 e + lane in key[e] (below `end`)
@@ -599,8 +604,8 @@ __device__ __forceinline__ uint32_t waves_before(uint32_t x, int32_t* s_waves, u
 }
 
 // A whole row of up to kThreads * KEYS rated tokens, whose keys stay in registers: each wave has a run of
-// tokens, 64 at a time.  (Rows that the bound did not announce are longer: evict_row.)
-template <int D, int KEYS>
+// tokens, 64 at a time.  (Rows that the bound did not announce are longer: evict_row.)  APART: as there
+template <int D, int KEYS, bool APART>
 __global__ __launch_bounds__(kThreads) void k_kv_evict_held(KvEvictArgs a) {
   __shared__ int32_t s_hist[3][kBins];             // and the lists, where they are short
   __shared__ int32_t s_waves[2][kWaves], s_scan[3][kWaves];
@@ -613,7 +618,7 @@ __global__ __launch_bounds__(kThreads) void k_kv_evict_held(KvEvictArgs a) {
     return;
   }
   if (x.rated > KEYS * kThreads) {
-    evict_row<D>(a, x, s_hist[0], s_waves[0], s_found[0]);
+    evict_row<D, APART>(a, x, s_hist[0], s_waves[0], s_found[0]);
     return;
   }
   int32_t* const kept = a.kept ? a.kept + (int64_t)blockIdx.x * a.budget : nullptr;
@@ -621,7 +626,7 @@ __global__ __launch_bounds__(kThreads) void k_kv_evict_held(KvEvictArgs a) {
   run.template load<true>(a, x);
   // the last tokens' first chunk, on its way while the others are chosen
   Moving<D, 1> tail;
-  read_last<D>(a, x, kept, 0, kRows, tail);
+  if constexpr (!APART) read_last<D>(a, x, kept, 0, kRows, tail);
   keep_places(a, x, blockIdx.x, tid, kThreads);
   for (int i = tid; i < 3 * kBins; i += kThreads) s_hist[0][i] = 0;
   __syncthreads();
@@ -667,13 +672,17 @@ __global__ __launch_bounds__(kThreads) void k_kv_evict_held(KvEvictArgs a) {
   // both are at most kThreads KEYS < 2^16
   const uint32_t before = waves_before((uint32_t)movers << 16 | (uint32_t)gaps, s_waves[1], all);
   const int32_t moving = (int32_t)(all >> 16);
-  const bool listed = moving <= kListed;
+  const bool listed = !APART && moving <= kListed;
   int32_t* const from = listed ? s_hist[0] : a.lists + (int64_t)blockIdx.x * 2 * a.budget;
   int32_t* const to = from + (listed ? kListed : a.budget);
   run.list(x, from, to, (int32_t)(before >> 16), (int32_t)(before & 0xFFFF));
-  __syncthreads();
-  move_listed<D>(a, x, kept, from, to, moving);
-  move_last<D>(a, x, kept, tail);
+  if constexpr (APART) {
+    if (tid == 0) a.moving[blockIdx.x] = moving;
+  } else {
+    __syncthreads();
+    move_listed<D>(a, x, kept, from, to, moving);
+    move_last<D>(a, x, kept, tail);
+  }
 }
 
 // Longer rows in parts: row blockIdx / parts, part blockIdx % parts, of equal runs of the row's rated
@@ -694,7 +703,6 @@ struct RowCounts {
     uint32_t border;
     int32_t wanted;
   } found[2];
-  int32_t moving, pad[3];
 };
 // of a part's tokens on kept places (0) and behind them (1): those whose key is at least the border's first two
 // digits and third digit i
@@ -828,7 +836,7 @@ __global__ __launch_bounds__(kThreads) void k_kv_evict_lists(KvEvictArgs a) {
   const int32_t stay0 = equal[0] < open ? equal[0] : open, stay1 = equal[1] < open - stay0 ? equal[1] : open - stay0;
   const int32_t moves = larger[1] + stay1, free_ = near - larger[0] - stay0;
   const int32_t moves_upto = sum_upto(moves), free_upto = sum_upto(free_);
-  if (p.part == 0 && tid == 63) c->moving = moves_upto;
+  if (p.part == 0 && tid == 63) a.moving[p.row] = moves_upto;
   const int32_t movers = __builtin_amdgcn_readlane(moves_upto - moves, p.part);
   const int32_t gaps = __builtin_amdgcn_readlane(free_upto - free_, p.part);
   int32_t ties = __builtin_amdgcn_readlane(ties_before, p.part);
@@ -892,7 +900,7 @@ __global__ __launch_bounds__(kMoveThreads) void k_kv_evict_move(KvEvictArgs a) {
   int32_t* const kept = a.kept ? a.kept + (int64_t)p.row * a.budget : nullptr;
   const int32_t* const from = a.lists + (int64_t)p.row * 2 * a.budget;
   const int32_t* const to = from + a.budget;
-  const int32_t moving = row_counts(a, p.row)->moving;
+  const int32_t moving = a.moving[p.row];
   const bool overlap = x.n - x.budget < x.last;
   const int32_t chunks = (x.last + kMoveRows - 1) / kMoveRows;
   auto movers = [&](int32_t i0, int32_t i1, int32_t step) {
@@ -923,21 +931,30 @@ __global__ __launch_bounds__(256) void k_kv_lengths(KvEvictArgs a) {
   a.kv_len_out[b] = n < a.budget ? n : a.budget;
 }
 
+template <int D, bool APART>
+void evict_held(const KvEvictArgs& a, bool short_rows, hipStream_t s) {
+  const dim3 rows((unsigned)a.rows), threads(kThreads);
+  if (short_rows) hipLaunchKernelGGL((k_kv_evict_held<D, 4, APART>), rows, threads, 0, s, a);
+  else hipLaunchKernelGGL((k_kv_evict_held<D, 16, APART>), rows, threads, 0, s, a);
+}
+
 template <int D>
 hipError_t evict(KvEvictArgs a, bool short_rows, hipStream_t s) {
-  const dim3 rows((unsigned)a.rows), threads(kThreads);
-  if (a.parts == 0) {
-    if (short_rows) hipLaunchKernelGGL((k_kv_evict_held<D, 4>), rows, threads, 0, s, a);
-    else hipLaunchKernelGGL((k_kv_evict_held<D, 16>), rows, threads, 0, s, a);
+  if (a.parts == 0 && a.move_parts == 0) {
+    evict_held<D, false>(a, short_rows, s);
     return hipGetLastError();
   }
-  const dim3 parts((unsigned)(a.rows * a.parts));
-  hipLaunchKernelGGL(k_kv_evict_clear, rows, dim3(256), 0, s, a);
-  hipLaunchKernelGGL((k_kv_evict_digits<0>), parts, threads, 0, s, a);
-  hipLaunchKernelGGL((k_kv_evict_digits<1>), parts, threads, 0, s, a);
-  hipLaunchKernelGGL((k_kv_evict_digits<2>), parts, threads, 0, s, a);
-  hipLaunchKernelGGL(k_kv_evict_lists, parts, threads, 0, s, a);
-  hipError_t e = hipGetLastError();
+  if (a.parts == 0) {
+    evict_held<D, true>(a, short_rows, s);
+  } else {
+    const dim3 rows((unsigned)a.rows), parts((unsigned)(a.rows * a.parts)), threads(kThreads);
+    hipLaunchKernelGGL(k_kv_evict_clear, rows, dim3(256), 0, s, a);
+    hipLaunchKernelGGL((k_kv_evict_digits<0>), parts, threads, 0, s, a);
+    hipLaunchKernelGGL((k_kv_evict_digits<1>), parts, threads, 0, s, a);
+    hipLaunchKernelGGL((k_kv_evict_digits<2>), parts, threads, 0, s, a);
+    hipLaunchKernelGGL(k_kv_evict_lists, parts, threads, 0, s, a);
+  }
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   KvEvictArgs m = a;
   m.parts = a.move_parts;
@@ -958,7 +975,8 @@ hipError_t launch_kv_accept(const KvAcceptArgs& a, int32_t D, hipStream_t s) {
 KvEvictPlan kv_evict_plan(int32_t batch, int32_t n_kv_heads, int64_t budget, int64_t max_kv_len) {
   KvEvictPlan p{};
   const int64_t rows = (int64_t)batch * n_kv_heads;
-  p.counts_at = (rows * 2 * budget * (int64_t)sizeof(int32_t) + 255) & ~255ll;
+  p.moving_at = (rows * 2 * budget * (int64_t)sizeof(int32_t) + 255) & ~255ll;
+  p.counts_at = (p.moving_at + rows * (int64_t)sizeof(int32_t) + 255) & ~255ll;
   p.workspace = p.counts_at;
   // Parts of 8192 tokens, where a workgroup's registers do not hold a row's keys, and a launch takes them.  By
   // 4096 / 8192 / 16384, us: 2 x 8 heads of up to 131072 106 / 87 / 104, 1 x 8 of 32768 47 / 50 / 67, 48 x 8 of 20000
@@ -976,9 +994,16 @@ hipError_t launch_kv_evict(KvEvictArgs a, int32_t D, const KvEvictPlan& p, int64
   a.lengths = a.kv_len_out != a.kv_len;
   a.parts = p.parts;
   a.lists = static_cast<int32_t*>(workspace);
+  a.moving = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + p.moving_at);
   a.counts = static_cast<uint8_t*>(workspace) + p.counts_at;
   const int64_t turns = (a.budget + kMoveRows * kMoveDeep - 1) / (kMoveRows * kMoveDeep), most = 2048 / a.rows + 1;
   a.move_parts = (int32_t)(turns < most ? turns : most);
+  // What moves is a launch of its own also where whole rows are done by few workgroups and much can move (not
+  // where the last tokens' places would overlap: these go in turn).  One workgroup a row / two launches, us, 8 rows:
+  // 4100 tokens to 3500 17 / 18, to 2000 22 / 18, 8200 to 2000 36 / 27, 16000 to 6000 73 / 31; 64 rows: 25 / 26
+  // (4100 to 2000), 39 / 36, 95 / 61; 128 rows: 27 / 41, 52 / 62, 106 / 103; 8 rows, 4100 to 4000, the last 300: 15 / 27.
+  const int64_t keep = a.budget - a.first - a.last, behind = max_kv_len - a.budget;
+  if (p.parts == 0 && !(a.rows <= 64 && (keep < behind ? keep : behind) > 768 && behind >= a.last)) a.move_parts = 0;
   const bool short_rows = max_kv_len - a.first - a.last <= 4 * kThreads;
   const hipError_t e = D == 64 ? evict<64>(a, short_rows, s) : (D == 128 ? evict<128>(a, short_rows, s) : evict<256>(a, short_rows, s));
   if (e != hipSuccess || a.lengths) return e;

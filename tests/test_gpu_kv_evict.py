@@ -476,6 +476,22 @@ def test_two_evictions_at_once(nv):
     b.check(1500, 1, 50)
 
 
+@pytest.mark.parametrize("kv,budget,first,last,most", [
+    ([4000, 3100, 700], 2000, 4, 64, None),
+    ([9000, 2100], 1500, 0, 1000, None),
+    ([2600, 2590], 1300, 5, 1290, None),                 # the last tokens' places meet or overlap their old ones
+    ([30000, 5000], 2000, 1, 50, 4000),                  # longer than announced
+    ([1999, 5000, 2001], 2000, 2000, 0, None),
+])
+@pytest.mark.parametrize("kind", ["ties", "odd"])
+@pytest.mark.parametrize("out", ["same", "other"])
+def test_evict_much_of_few(nv, kv, budget, first, last, most, kind, out):
+    """Few rows of which much moves: chosen and moved in two launches."""
+    s = Eviction(nv, kv, 2, 64, 64, kind, seed=budget)
+    s.run(nv, budget, first, last, out, most=most)
+    s.check(budget, first, last, out)
+
+
 def test_evict_many_short_sequences(nv):
     rng = np.random.default_rng(0)
     kv = rng.integers(0, 60, 400).tolist()
