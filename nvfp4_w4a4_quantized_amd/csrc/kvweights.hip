@@ -617,13 +617,15 @@ hipError_t plan(KvWeightsArgs w, int64_t max_q_len, int64_t max_kv_len, hipStrea
   const int64_t pairs = (int64_t)w.a.batch * w.a.geom.n_kv_heads, group = w.a.by_group.d;
   const int64_t m = max_q_len < w.a.T ? max_q_len : w.a.T;
   const int64_t n = max_kv_len < 1 ? 1 : max_kv_len;
+  // keys that a sequence's queries attend to, at most
+  const int64_t span = w.a.window && w.a.window + m < n ? w.a.window + m : n;
   if (m * group <= 16 * few_blocks(D, F32)) {
     // Runs so long that about all waves are there at once, four a SIMD; two or one, where a wave's columns are more or
     // longer and it takes longer to bring them.  By 4096 / 2048 / 1024 waves, us: head dimension 128, 32 x up to 8192 27 / 29 / 30,
     // fp32 8 x up to 8192 11 / 11 / 13; 64, 32 x up to 8192 13 / 14 / 19; 256, 16 x up to 32768 36 / 32 / 32, fp32 4 x up
     // to 32768 22 / 14 / 13; 128 with 32 columns 8 x 4096 13 / 10 / 11, with 64 24 / 16 / 17, 24 x up to 6001 with 36
     // 31 / 28 / 45.
-    const int64_t steps = pairs * ((n + kWaveTokens - 1) / kWaveTokens);
+    const int64_t steps = pairs * ((span + kWaveTokens - 1) / kWaveTokens);
     const int64_t each = steps / (D == 256 ? 1024 : (m * group > 16 ? 2048 : 4096));
     w.split = m * group <= 16 ? -1 : (m * group <= 32 ? -2 : -4);
     w.steps = (int32_t)(each < 1 ? 1 : (each > 16 ? 16 : each));
@@ -632,10 +634,13 @@ hipError_t plan(KvWeightsArgs w, int64_t max_q_len, int64_t max_kv_len, hipStrea
   } else {
     const int64_t tiles = group <= kTileRows ? (m + kTileRows / group - 1) / (kTileRows / group) : m * ((group + kTileRows - 1) / kTileRows);
     // More waves to the same tokens while workgroups are few (two a compute unit) and each wave has two
-    // tiles, or where the tiles are many: the keys are decoded by each of them.
+    // tiles, or where the tiles are many: the keys are decoded by each of them.  While they are fewer than half the
+    // compute units, each wave one: without / with, us, 1 x 300, 40 new, 32 / 8 heads of 128 14.9 / 9.3, 1 x 2000, 100 new, 8 / 2
+    // heads 14.9 / 10.8, fp32 1 x 100, 40 new, 4 / 2 heads of 256 17.7 / 11.7.
     w.split = 0;
-    while (w.split < 3 && tiles >= (4 << w.split) &&
-           (tiles >= 32 || pairs * ((n * 2 + kManyWaves * Many<D, F32>::TB * 32 - 1) / (kManyWaves * Many<D, F32>::TB * 32 >> w.split)) < 1024))
+    constexpr int64_t WG = kManyWaves * Many<D, F32>::TB * 32;
+    while (w.split < 3 && ((tiles >= (4 << w.split) && (tiles >= 32 || pairs * ((span * 2 + WG - 1) / (WG >> w.split)) < 1024)) ||
+                           (tiles > (1 << w.split) && pairs * ((span + (WG >> w.split) - 1) / (WG >> w.split)) < 128)))
       ++w.split;
     const int64_t tokens = (kManyWaves >> w.split) * Many<D, F32>::TB * 32;
     w.tiles = kv_planned_tiles((n + tokens - 1) / tokens, pairs, 64 * kManyWaves);
