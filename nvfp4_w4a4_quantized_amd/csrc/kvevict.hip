@@ -7,6 +7,8 @@
 // of both (16 bytes a lane at D = 128), then 16 lanes a row the parts of the values, in four, and D/16
 // lanes a row their scales.  What counts is the number of such loads and stores, not their bytes (with
 // 16 lanes a row for everything, twice as many: 32 x 8 heads of about 4130 tokens to 4096 19 us, not 17).
+#include <type_traits>
+
 #include "kernel_common.hpp"
 #include "kv_launch.hpp"
 
@@ -400,12 +402,18 @@ __device__ __forceinline__ int groups_of(int32_t left, int side) {
   return __builtin_amdgcn_readfirstlane(own <= 0 ? 0 : (own + side - 1) / side);
 }
 
-template <int D>
+template <int D, int N>
 __device__ __forceinline__ void read_last(const KvEvictArgs& a, const Row& x, int32_t* kept, int32_t j0, int32_t rows,
-                                          Moving<D, 1>& h) {
-  const int32_t j = j0 + (int32_t)threadIdx.x / 4;
-  const bool live[1] = {j < x.last};
-  const int32_t old[1] = {live[0] ? x.n - x.last + j : x.n - 1}, place[1] = {live[0] ? x.behind + j : 0};
+                                          Moving<D, N>& h) {
+  int32_t old[N], place[N];
+  bool live[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    const int32_t j = j0 + e * rows + (int32_t)threadIdx.x / 4;
+    live[e] = j < x.last;
+    old[e] = live[e] ? x.n - x.last + j : x.n - 1;
+    place[e] = live[e] ? x.behind + j : 0;
+  }
   h.read(a, x, kept, old, place, live, groups_of(x.last - j0, rows));
 }
 
@@ -442,7 +450,7 @@ __device__ __forceinline__ void move_last(const KvEvictArgs& a, const Row& x, in
   __syncthreads();                                 // the movers are read
   tail.write(a);
   for (int32_t j0 = kRows; j0 < x.last; j0 += kRows) {
-    read_last<D>(a, x, kept, j0, kRows, tail);
+    read_last<D, 1>(a, x, kept, j0, kRows, tail);
     __syncthreads();
     tail.write(a);
   }
@@ -458,7 +466,7 @@ __device__ __forceinline__ void evict_row(const KvEvictArgs& a, const Row& x, in
   for_keys<true>(a, x, 0, x.rated, tid, kThreads, [](int32_t, uint32_t) {});
   // the last tokens' first chunk, on its way while the others are chosen
   Moving<D, 1> tail;
-  if constexpr (!APART) read_last<D>(a, x, kept, 0, kRows, tail);
+  if constexpr (!APART) read_last<D, 1>(a, x, kept, 0, kRows, tail);
   keep_places(a, x, blockIdx.x, tid, kThreads);
 
   // the smallest kept key, and how many tokens of it are kept
@@ -626,7 +634,7 @@ __global__ __launch_bounds__(kThreads) void k_kv_evict_held(KvEvictArgs a) {
   run.template load<true>(a, x);
   // the last tokens' first chunk, on its way while the others are chosen
   Moving<D, 1> tail;
-  if constexpr (!APART) read_last<D>(a, x, kept, 0, kRows, tail);
+  if constexpr (!APART) read_last<D, 1>(a, x, kept, 0, kRows, tail);
   keep_places(a, x, blockIdx.x, tid, kThreads);
   for (int i = tid; i < 3 * kBins; i += kThreads) s_hist[0][i] = 0;
   __syncthreads();
@@ -872,7 +880,7 @@ __global__ __launch_bounds__(kThreads) void k_kv_evict_lists(KvEvictArgs a) {
 // Movers, and the last tokens.  The last tokens' new places may hold movers, those below the budget: first
 // in the list.  Where old and new places of the last tokens do not overlap, they go in chunks of 64, and the
 // workgroup of a chunk moves the movers of its new places before; else the first workgroup moves all of
-// these in order.
+// these in order, 128 at a time (8 heads of 50000 to 49900, the last 1024: 64 at a time 81 us, 128 71).
 constexpr int kMoveThreads = 256, kMoveRows = kMoveThreads / 4, kMoveDeep = 2;
 
 // How many of the movers, which ascend, are below token t: a lane looks at every 64th part of what is left, as
@@ -902,23 +910,26 @@ __global__ __launch_bounds__(kMoveThreads) void k_kv_evict_move(KvEvictArgs a) {
   const int32_t* const to = from + a.budget;
   const int32_t moving = a.moving[p.row];
   const bool overlap = x.n - x.budget < x.last;
-  const int32_t chunks = (x.last + kMoveRows - 1) / kMoveRows;
-  auto movers = [&](int32_t i0, int32_t i1, int32_t step) {
+  auto movers = [&](int32_t i0, int32_t i1, int32_t step) __attribute__((always_inline)) {
     for (; i0 < i1; i0 += step) {
       Moving<D, kMoveDeep> m;
       read_listed<D, kMoveDeep>(a, x, kept, from, to, i0, kMoveRows, i1, m);
       m.write(a);
     }
   };
-  for (int32_t c = p.part; c < chunks && (!overlap || p.part == 0); c += overlap ? 1 : a.parts) {
-    const int32_t place = x.behind + c * kMoveRows;
-    movers(movers_below(from, moving, place), movers_below(from, moving, place + kMoveRows < x.budget ? place + kMoveRows : x.budget),
-           kMoveRows * kMoveDeep);
-    Moving<D, 1> m;
-    read_last<D>(a, x, kept, c * kMoveRows, kMoveRows, m);
-    __syncthreads();                               // these movers and tokens are read
-    m.write(a);
-  }
+  auto last = [&](auto deep, int32_t j0, int32_t step) __attribute__((always_inline)) {
+    constexpr int N = decltype(deep)::value;
+    for (; j0 < x.last; j0 += step) {
+      const int32_t place = x.behind + j0, end = place + kMoveRows * N < x.budget ? place + kMoveRows * N : x.budget;
+      movers(movers_below(from, moving, place), movers_below(from, moving, end), kMoveRows * kMoveDeep);
+      Moving<D, N> m;
+      read_last<D, N>(a, x, kept, j0, kMoveRows, m);
+      __syncthreads();                             // these movers and tokens are read
+      m.write(a);
+    }
+  };
+  if (!overlap) last(std::integral_constant<int, 1>{}, p.part * kMoveRows, a.parts * kMoveRows);
+  else if (p.part == 0) last(std::integral_constant<int, kMoveDeep>{}, 0, kMoveRows * kMoveDeep);
   const int32_t rest = movers_below(from, moving, x.budget);
   movers(rest + p.part * kMoveRows * kMoveDeep, moving, a.parts * kMoveRows * kMoveDeep);
 }
