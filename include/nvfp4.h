@@ -507,7 +507,8 @@ NVFP4_API int32_t nvfp4_kv_accept(uint8_t* cache, int64_t n_pages, int32_t page_
  * in fp32 (the tokens that are new in this call begin at 0; a decay of 0 reads no earlier
  * weights).  A sequence without query tokens keeps its weights.
  *   q            as for nvfp4_kv_attention, ldq at most 2^23 (NVFP4_ERR_UNSUPPORTED otherwise)
- *   lse          device fp32 [T][n_q_heads]; -inf: the row has no weights
+ *   lse          device fp32 [T][n_q_heads]; -inf: the row has no weights, whatever its query holds (a
+ *                row that a batch is padded with)
  *   key_weights  device fp32 [n_pages][n_kv_heads][page_size], 16-byte aligned: a weight for each slot
  *                and kv head.  The pages of a call's sequences must be each sequence's alone.
  * Products are those of the attention; an exponent is off by up to about 2^-23 of |scale <q, k>| +

@@ -106,15 +106,20 @@ __global__ __launch_bounds__(64 * kWeightWaves, D == 256 || NB == 4 ? 2 : (NB ==
     float amax = 0.0f;
 #pragma unroll
     for (int c = 0; c < KC; ++c) load8<F32>(a.q, off + (D == 64 ? 16 * g + 8 * c : 128 * (c / 4) + 32 * g + 8 * (c % 4)), v[c]);
+    // A row that attends to nothing, is taken out or is not there has no weights: e^(0 - inf).  Its query may hold anything,
+    // and a NaN or an infinity would stay a NaN.
+    const bool none = past || lse == -__builtin_inff();
 #pragma unroll
     for (int c = 0; c < KC; ++c)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) amax = __builtin_fmaxf(amax, __builtin_fabsf(v[c][e]));
+      for (int e = 0; e < 8; ++e) {
+        v[c][e] = none ? 0.0f : v[c][e];
+        amax = __builtin_fmaxf(amax, __builtin_fabsf(v[c][e]));
+      }
     amax = max_xor32(max_xor16(amax));
     const float up = a.scale < 0.0f ? -query_up(amax) : query_up(amax);
     const float csc_r = score_factor(a.scale, kg, amax);
-    // a row that attends to nothing, or is not there, has no weights
-    const float sub_r = past || lse == -__builtin_inff() ? __builtin_inff() : lse * kLog2e;
+    const float sub_r = none ? __builtin_inff() : lse * kLog2e;
 #pragma unroll
     for (int c = 0; c < KC; ++c)
 #pragma unroll
@@ -453,11 +458,14 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv_weights_many(KvWeight
           asm volatile("" ::: "memory");           // and nothing is read before
           if (next_x >= 0) issue(next_x, next_chunk, place ^ 1);
         };
+        // Rows of log-sum -inf have no weights, e^(0 - inf): their queries are taken as 0, since a NaN or an
+        // infinity in one would stay a NaN.  none: whether the lane's row is one; any_none: whether any is (rare).
+        bool none = false, any_none = false;
         auto log_sums = [&] {
-          if (h == 0) {
-            const float lse = s_lse[(x >> w.split & 1) * kTileRows + r];
-            s_sub[r] = r >= rows || lse == -__builtin_inff() ? __builtin_inff() : lse * kLog2e;
-          }
+          const float lse = s_lse[(x >> w.split & 1) * kTileRows + r];
+          none = lse == -__builtin_inff();
+          any_none = __builtin_amdgcn_ballot_w64(none) != 0;
+          if (h == 0) s_sub[r] = r >= rows || none ? __builtin_inff() : lse * kLog2e;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const f32x4 y = *reinterpret_cast<const f32x4*>(s_sub + 8 * i + 4 * h);
@@ -475,6 +483,10 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv_weights_many(KvWeight
 #pragma unroll
           for (int k = 0; k < KS; ++k) qf[k] = *reinterpret_cast<const bf16x8*>(unit_at(h * (M::UNITS / 2) + k));
           log_sums();
+          if (any_none) {
+#pragma unroll
+            for (int k = 0; k < KS; ++k) qf[k] = none ? bf16x8{} : qf[k];
+          }
           f32x16 acc[2];
 #pragma unroll
           for (int k = 0; k < KS; ++k) acc[0] = mfma32(qf[k], kf[0][k], k == 0 ? f32x16{} : acc[0]);
@@ -510,6 +522,15 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void k_kv_weights_many(KvWeight
             if (chunk + 1 < M::NCH) landed(x, chunk + 1);
             else landed(x - qs, 0);
             if (chunk == 0) log_sums();
+            if (any_none) {
+              // the row in LDS, half of it a lane, before any lane reads it
+              if (none) {
+#pragma unroll
+                for (int u = 0; u < M::UNITS / 2; ++u)
+                  *reinterpret_cast<u32x4*>(unit_at(h * (M::UNITS / 2) + u)) = u32x4{0, 0, 0, 0};
+              }
+              asm volatile("" ::: "memory");
+            }
 #pragma unroll
             for (int k = 0; k < M::KSC; ++k) {
               const int step = chunk * M::KSC + k;

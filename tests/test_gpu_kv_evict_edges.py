@@ -1,0 +1,50 @@
+"""Edges of the attention weights and of eviction over the paged NVFP4 key/value cache, against the
+CPU oracle: rows that are taken out, bounds below the lengths, pages that are not there."""
+
+import numpy as np
+import pytest
+import torch
+
+from tests.test_gpu_kv_evict import WeightProblem
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def nv():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import nvfp4_w4a4_quantized_amd as nvmod
+    return nvmod
+
+
+# ----------------------------------------------------------------------------- attention weights
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("kv,m,Hq,Hkv,window,hints", [
+    ([400, 70], [1, 1], 8, 2, 0, None),                  # a generated token each
+    ([400, 70], [3, 2], 8, 2, 90, None),
+    ([400, 70], [5, 4], 9, 1, 0, None),                  # blocks of 16 columns whose last is not full
+    ([400, 70], [30, 9], 4, 2, 0, (1, 400)),             # more columns than announced
+    ([900, 40], [70, 40], 8, 2, 0, None),                # many columns
+    ([900, 40], [70, 40], 5, 1, 300, None),              # tiles of less than 32 rows
+    ([600], [11], 40, 1, 0, None),                       # more heads of a group than a tile's rows
+])
+def test_queries_of_rows_of_no_weight(nv, dtype, D, kv, m, Hq, Hkv, window, hints):
+    """Rows whose log-sum is -inf have no weights whatever their queries hold, as the rows of a batch that
+    is padded to a fixed size do: NaN, infinities, values whose products overflow."""
+    p = WeightProblem(nv, kv, m, Hq, Hkv, D, 16, dtype, seed=D + Hq)
+    lse = p.lse_of(nv, window)
+    rng = np.random.default_rng(Hq)
+    gone = rng.random((p.T, Hq)) < 0.3
+    gone[0] = True                                       # a whole query token
+    gone[-1, 0] = True
+    lse[torch.from_numpy(gone)] = -np.inf
+    for i, h in np.argwhere(gone):
+        kind = (i + h) % 4
+        p.q[i, h] = (float("nan"), float("inf"), 3e38, -float("inf"))[kind]
+        if kind == 3:
+            p.q[i, h, ::2] = 1.0                         # products of both signs, and ordinary ones
+    got = p.run_weights(nv, lse, window, 0.5, hints=hints)
+    p.check_weights(got, lse, window, 0.5)
