@@ -537,7 +537,7 @@ NVFP4_API int32_t nvfp4_kv_attention_weights(const void* q, int32_t dtype, int64
  *   weights_out  the same shape, or NULL: the kept tokens' weights at their new places; may be
  *                key_weights itself
  *   kept         device int32 [batch][n_kv_heads][budget] or NULL: the earlier place of the token at each new
- *                place (-1 past the new length)
+ *                place (-1 past the new length; where a row was not moved, the place itself)
  *   max_kv_len   host: bound on the lengths, from which the launch is chosen; longer sequences
  *                are right too, more slowly
  *   kv_len_out   device int32 [batch]: min(n, budget); may be kv_len itself

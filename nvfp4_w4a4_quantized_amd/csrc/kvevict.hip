@@ -379,8 +379,9 @@ struct Moving {
       if (moves) {
         to[e] = row_at<D>(row.pages, dst[e], row.kh, place[e]);
         w_at[e] = row.pages.weight_at(dst[e], row.kh, place[e]);
-        if (kept && (threadIdx.x & 3) == 0) kept[place[e]] = old[e];
       }
+      // a row that does not move leaves the place as it is
+      if (kept && live[e] && (threadIdx.x & 3) == 0) kept[place[e]] = moves ? old[e] : place[e];
     }
   }
   __device__ __forceinline__ void write(const KvEvictArgs& a) const {

@@ -5,7 +5,8 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_kv_evict import WeightProblem
+from oracle import kv as KV
+from tests.test_gpu_kv_evict import Eviction, WeightProblem
 
 pytestmark = pytest.mark.gpu
 
@@ -48,3 +49,39 @@ def test_queries_of_rows_of_no_weight(nv, dtype, D, kv, m, Hq, Hkv, window, hint
             p.q[i, h, ::2] = 1.0                         # products of both signs, and ordinary ones
     got = p.run_weights(nv, lse, window, 0.5, hints=hints)
     p.check_weights(got, lse, window, 0.5)
+
+
+# ----------------------------------------------------------------------------- eviction
+
+def ranked(s, b, t, h, missing):
+    """A token whose page is not there ranks last."""
+    return -np.inf if b == 0 and t // s.page == missing else s.weight(s.weights, b, t, h)
+
+
+@pytest.mark.parametrize("kv,budget,first,last,page", [
+    ([100, 60], 50, 2, 10, 16),                          # a workgroup a row
+    ([4000, 3100], 2000, 4, 200, 64),                    # chosen and moved in two launches
+    ([20000, 700], 2000, 2, 300, 64),                    # in parts
+    ([20000, 700], 19900, 2, 300, 64),                   # and places that overlap
+])
+@pytest.mark.parametrize("gone", ["source", "place"])
+def test_every_place_of_kept_is_written(nv, kv, budget, first, last, page, gone):
+    """A row whose page, or whose place's page, is not in the cache does not move: kept has the place itself
+    there, and no place of kept is left as it was."""
+    s = Eviction(nv, kv, 2, 64, page, "plain", seed=budget)
+    n = kv[0]
+    token = n - last // 2 if gone == "source" else budget - last // 2      # among the last ones
+    missing = token // page
+    s.dtable[0, missing] = -1 if gone == "source" else 10 ** 6
+    s.run(nv, budget, first, last, out="none")
+    for b, n in enumerate(kv):
+        for h in range(2):
+            w = np.array([ranked(s, b, t, h, missing) for t in range(n)])
+            want = np.array(KV.evicted(w, n, budget, first, last))
+            if b == 0 and n > budget:
+                place = np.arange(budget)
+                still = (want // page == missing) | (place // page == missing)
+                assert still[budget - last:].any()
+                want = np.where(still, place, want)
+            got = s.kept[b, h].cpu().numpy()
+            assert np.array_equal(got[:len(want)], want) and np.all(got[len(want):] == -1), (b, h)
