@@ -51,6 +51,23 @@ def test_queries_of_rows_of_no_weight(nv, dtype, D, kv, m, Hq, Hkv, window, hint
     p.check_weights(got, lse, window, 0.5)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("most", [1, 700])
+@pytest.mark.parametrize("kv,m,Hq,Hkv,window", [
+    ([2500, 310], [90, 310], 8, 2, 0),
+    ([2500, 310], [90, 310], 8, 2, 400),                 # a window that leaves whole turns of tokens out
+    ([2500, 310], [40, 17], 40, 1, 0),                   # more heads of a group than a tile's rows
+    ([1200, 300] + [20] * 6, [9] * 8, 128, 16, 0),       # waves that have tokens each, of many heads
+])
+def test_many_columns_of_more_tokens_than_announced(nv, dtype, D, most, kv, m, Hq, Hkv, window):
+    """A workgroup takes tokens again and again where the lengths are above their bound."""
+    p = WeightProblem(nv, kv, m, Hq, Hkv, D, 32, dtype, seed=D + Hq)
+    lse = p.lse_of(nv, window)
+    got = p.run_weights(nv, lse, window, 0.5, hints=(max(m), most))
+    p.check_weights(got, lse, window, 0.5)
+
+
 # ----------------------------------------------------------------------------- eviction
 
 def ranked(s, b, t, h, missing):
