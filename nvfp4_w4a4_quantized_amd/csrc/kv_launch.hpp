@@ -1,6 +1,8 @@
 // Launch entries of the key/value cache and its attention.
 #pragma once
 
+#include <cstddef>
+
 #include "kv_layout.hpp"
 #include "launch.hpp"
 
@@ -108,9 +110,6 @@ struct KvAttnArgs {
   const float* v_gscale;
   float scale;
   int32_t window;              // 0 = none
-  const uint64_t* tree;        // NULL: causal; else the query rows' bits over their sequence's query tokens
-  int64_t ld_tree;             // words from row to row
-  int32_t tree_words;
   void* o;
   int64_t ldo;
   float* lse;                  // optional
@@ -123,7 +122,13 @@ struct KvAttnArgs {
   int32_t tile_cols;           // query columns of an item
   int32_t col_tiles;           // items per sequence and kv head
   FastDiv by_group, by_heads, by_tile_cols, by_col_tiles, by_pairs;   // pairs: sequence, kv head
+  // Last, so that what causal calls read lies in 256 bytes, four lines of the kernel's arguments (with a fifth,
+  // 1 x 257 keys 6.7 us, not 6.5)
+  const uint64_t* tree;        // NULL: causal; else the query rows' bits over their sequence's query tokens
+  int64_t ld_tree;             // words from row to row
+  int32_t tree_words;
 };
+static_assert(offsetof(KvAttnArgs, tree) <= 256, "causal calls' arguments: four lines");
 constexpr int kItemPiecesBytes = 32;
 constexpr int kMaxTreeWords = 64;
 struct KvAttnPlan {
@@ -141,7 +146,6 @@ hipError_t launch_kv_attn(KvAttnArgs a, const KvAttnPlan& p, InType t, int32_t D
 
 // kvweights.hip: the attention weight of cached tokens
 struct KvWeightsArgs {
-  KvAttnArgs a;                // its queries, pages and scale; o, lse, plan unused
   const float* lse;            // [T][n_q_heads]
   float* weights;              // [n_pages][n_kv_heads][page_size]
   float decay;
@@ -151,6 +155,8 @@ struct KvWeightsArgs {
   int32_t split;               // many: log2 of the waves that share tokens; few: minus the
                                // blocks of 16 columns that a wave holds
   FastDiv by_tiles;
+  // last, so that the tree's fields are behind all that is read (3 x 37 to 300 new fp32 tokens 17.9 us, 17.5)
+  KvAttnArgs a;                // its queries, pages and scale; o, lse, plan unused
 };
 constexpr int64_t kKvWeightsMostLd = 1 << 23;      // elements between query rows: a tile's offsets have 32 bits
 hipError_t launch_kv_weights(KvWeightsArgs w, InType t, int32_t D, int64_t max_q_len, int64_t max_kv_len, hipStream_t s);
