@@ -511,8 +511,9 @@ NVFP4_API int32_t nvfp4_kv_accept(uint8_t* cache, int64_t n_pages, int32_t page_
  *                row that a batch is padded with)
  *   key_weights  device fp32 [n_pages][n_kv_heads][page_size], 16-byte aligned: a weight for each slot
  *                and kv head.  The pages of a call's sequences must be each sequence's alone.
- * Products are those of the attention; an exponent is off by up to about 2^-23 of |scale <q, k>| +
- * |lse|, which the rounding of lse alone may cost.  A call of the same sizes and bounds gives the same bits.
+ * Products are those of the attention (with many query columns of queries as they are: sums of
+ * q times the stored key, k / k_gscale, must be in fp32's range); an exponent is off by up to about
+ * 2^-23 of |scale <q, k>| + |lse|, which the rounding of lse alone may cost.  A call of the same sizes and bounds gives the same bits.
  * A weight whose page is not in the cache is not written.
  */
 NVFP4_API int32_t nvfp4_kv_attention_weights(const void* q, int32_t dtype, int64_t ldq, int64_t T, int32_t n_q_heads,
@@ -539,7 +540,10 @@ NVFP4_API int32_t nvfp4_kv_attention_weights(const void* q, int32_t dtype, int64
  *   kept         device int32 [batch][n_kv_heads][budget] or NULL: the earlier place of the token at each new
  *                place (-1 past the new length; where a row was not moved, the place itself)
  *   max_kv_len   host: bound on the lengths, from which the launch is chosen; longer sequences
- *                are right too, more slowly
+ *                are right too, more slowly.  So are bounds far above the lengths: above 16384 a row is
+ *                announced as so many parts, in six launches, whatever it has (32 x 8 heads of about
+ *                4130 tokens cut to 4096, us: 17 as announced, 25 at a bound of 16384, 97 at 16400, 312 at
+ *                131072; 5, 5, 21 and 47 where none is over its budget)
  *   kv_len_out   device int32 [batch]: min(n, budget); may be kv_len itself
  *   workspace    device, at least nvfp4_kv_evict_workspace(...) bytes, 16-byte aligned; calls that
  *                overlap on the GPU need one each, and a recorded graph its own

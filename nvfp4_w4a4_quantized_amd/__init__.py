@@ -467,8 +467,8 @@ def nvfp4_kv_attention_weights(q, cache, page_table, kv_len, k_gscale, page_size
                                max_q_len=1, scale=None, window=0, decay=1.0, stream=None) -> None:
     """Add to key_weights (fp32 [n_pages, n_kv_heads, page_size]) the attention weight that each
     cached token receives from the query tokens of an nvfp4_kv_attention call, whose lse
-    [T, n_q_heads] goes in; earlier weights are multiplied by decay (0: not read), those of
-    the call's own tokens begin at 0."""
+    [T, n_q_heads] goes in (-inf: a row that has no weights, such as one that pads the batch);
+    earlier weights are multiplied by decay (0: not read), those of the call's own tokens begin at 0."""
     _kv_call("kv_attention_weights", stream, cache, page_size, q, page_table, kv_len, k_gscale, lse, key_weights, max_kv_len,
              cu_q, max_q_len, scale, window, decay)
 
@@ -486,7 +486,8 @@ def nvfp4_kv_evict(cache, key_weights, page_table, kv_len, page_size, budget, kv
     keep_last and of the others those of the largest key_weights (fp32 [n_pages, n_kv_heads,
     page_size]), its rows moved in place; weights_out (may be key_weights; None: not
     wanted) gets the kept tokens' weights, kept (int32 [batch, n_kv_heads, budget]) their earlier
-    places, kv_len_out (may be kv_len) the new lengths."""
+    places, kv_len_out (may be kv_len) the new lengths.  max_kv_len chooses the launch: announced
+    above 16384, short sequences take several times as long."""
     _kv_call("kv_evict", stream, cache, page_size, key_weights, page_table, kv_len, budget, kv_len_out, max_kv_len,
              workspace, keep_first, keep_last, weights_out, kept)
 

@@ -36,7 +36,7 @@
 // about five steps of 450 (64 tokens each, most of it decoding), and 36 columns take a second column
 // group that decodes every key again.  Two blocks of 16 columns share a decoded granule (9 or 14
 // registers spilled, one access of them in the loop over the steps; fp32 at head dimension 256
-// spills 20 or 23); three spilled 180.  Granules two steps ahead (62 us instead of 49 then) and two
+// spills 20 or 23; drafted trees 34 or 35, and 29 or 32); three spilled 180.  Granules two steps ahead (62 us instead of 49 then) and two
 // steps a turn without the register copies between them (no change; drafts 57 us instead of 47) did
 // not pay.
 #include "kv_device.hpp"
@@ -728,7 +728,9 @@ hipError_t launch_kv_join(const KvAttnArgs& a, InType t, int32_t D, hipStream_t 
 //              54 / 53; 32 x 2048, 16 nodes 59 / 42; 2 x 131072, 16 nodes 165 / 132
 // (64: 8 x 4096, 32 nodes 36 / 35; 256: 8 x 8192, 16 / 2 heads, 16 nodes 58 / 66, 30 nodes 104 / 91, 4 x 8192 53 / 70).
 // The shared kernel's time is taken as a beginning and its tiles by the compute units, thin items' as
-// rounds of one a compute unit, or, few ones, which are cut, as all their steps.
+// rounds of one a compute unit, or, few ones, which are cut, as all their steps.  Every point above goes to its
+// faster side by this but one: 4 x 4096 with 60 nodes are taken as 56 / 50 and go to the shared kernel.  (fp32 has
+// no shared kernel: trees of many columns decode a key again for each 16 or 32 of them.)
 static bool thin_items(int64_t pairs, int64_t cols, int32_t D, int64_t span, bool shared) {
   const int64_t items = pairs * ((cols + 15) / 16), steps = (span + 63) / 64;
   const double width = D == 64 ? 0.55 : (D == 128 ? 1.0 : 2.0);
@@ -776,7 +778,7 @@ static KvAttnPlan plan_of(InType t, int64_t T, int32_t batch, int32_t n_q_heads,
     return p;
   }
   // two column blocks share a decoded granule where their registers fit, or nearly (head dimension
-  // 128: 9 to 14 spill)
+  // 128: 9 to 14 spill, of trees 34 or 35)
   p.nq = cols > 16 && (D == 64 || (D == 128 && t == InType::BF16)) ? 2 : 1;
   const int64_t pairs = (int64_t)batch * n_kv_heads;
   if (thin) p.nq = 1;

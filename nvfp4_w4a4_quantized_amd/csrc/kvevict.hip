@@ -992,7 +992,8 @@ KvEvictPlan kv_evict_plan(int32_t batch, int32_t n_kv_heads, int64_t budget, int
   p.workspace = p.counts_at;
   // Parts of 8192 tokens, where a workgroup's registers do not hold a row's keys, and a launch takes them.  By
   // 4096 / 8192 / 16384, us: 2 x 8 heads of up to 131072 106 / 87 / 104, 1 x 8 of 32768 47 / 50 / 67, 48 x 8 of 20000
-  // 324 / 264 / 261.
+  // 324 / 264 / 261.  The lengths are the device's: rows that turn out short are taken in as many parts (32 x 8 heads of
+  // about 4130 tokens to 4096, us by bound: 4201 16, 16384 25, 16400 97, 131072 312).
   const int64_t parts = (max_kv_len + 8191) / 8192;
   p.parts = (int32_t)(parts < kKvEvictMostParts ? parts : kKvEvictMostParts);
   if (max_kv_len <= 16 * kThreads) p.parts = 0;

@@ -29,13 +29,16 @@
 // instead of 452.
 //
 // What bounds it: matrix and vector instructions of two waves per SIMD that only partly overlap.  8192
-// tokens, 32 / 8 heads of 128: 519 us, 1060 TFLOP/s, on a fast card, 17 % more on a slow one (a large f16
-// matrix product reaches 1095 to 1193 there, at the clock that its power leaves); the matrix unit is busy 47 % of the
-// cycles, the vector unit 54 %, LDS 36 %, and waves wait 32 %.  Head dimension 256, whose accumulators leave no
+// tokens, 32 / 8 heads of 128: 519 to 551 us by card, 998 to 1060 TFLOP/s (a large f16
+// matrix product reaches 1095 to 1193, at the clock that its power leaves); the matrix unit is busy 49 % of the
+// cycles, the vector unit 56 %, LDS 37 %, and waves wait 29 %.  Head dimension 256, whose accumulators leave no
 // registers for the pipeline (11 or 16 spill, outside of the products): 3 sequences of 300 to 2048 new
-// tokens of up to 16384 764 us, 1096 TFLOP/s.  What a tile's loads return is looked at only when the
-// tile is decoded: the check of a page id and the halves of a row of scales, put together right after
-// their loads, made every wave wait for these (826 us).  64 columns a wave at one wave per SIMD (512 registers)
+// tokens of up to 16384 764 to 811 us, 1032 to 1096 TFLOP/s, the matrix unit 51 % busy, waves waiting 39 %.  What a
+// tile's loads return is looked at only when the tile is decoded: the check of a page id and the halves of a row
+// of scales, put together right after their loads, made every wave wait for these (826 us where it takes 764, 894 / 811
+// on another card).  Drafted trees spill 28 or 32 registers at head dimension 256, and 39 to 67 scalar ones at
+// every head dimension (causal items 0 to 11): 8 trees of 64 to 128 nodes over up to 16384 tokens 206 to 208 us, 769
+// TFLOP/s, the matrix unit 42 % busy.  64 columns a wave at one wave per SIMD (512 registers)
 // took 845 us where this took 606.
 #include <type_traits>
 

@@ -72,8 +72,8 @@ __device__ __forceinline__ QueryRange queries_of(const SeqInfo& s, int32_t t0, i
 // a run of tokens, 64 at a time, with the next 64 tokens' codes in flight; S on the f16 MFMA
 // 16x16x32 with the numerics of kvattn.hip, up to NB blocks of 16 query columns, which stay in registers (more of
 // them, which the bounds did not announce, are prepared again for every step).  32 sequences of up to 8192 tokens, 32 / 8
-// heads of 128: 27 us, 3.6 TB/s (unlike lengths: the longest runs last); of 32768 124 us, 5.2 TB/s, as fast as
-// a copy.
+// heads of 128: 27 us, 3.6 TB/s (unlike lengths: the longest runs last); of 32768 124 to 128 us, 5.2 TB/s, as fast
+// as a copy.
 template <int D, bool F32, int NB>
 __global__ __launch_bounds__(64 * kWeightWaves, D == 256 || NB == 4 ? 2 : (NB == 2 ? 3 : 4)) void k_kv_weights(KvWeightsArgs w) {
   constexpr int KC = D / 32, TERMS = F32 ? 2 : 1, NG = kWaveTokens / 16;
@@ -250,9 +250,9 @@ __global__ __launch_bounds__(64 * kWeightWaves, D == 256 || NB == 4 ? 2 : (NB ==
 // are joined in LDS at the end.  Tiles go from memory to LDS by asynchronous loads, each wave's its own,
 // one ahead: no barrier in the loop.  fp32 queries go as three bf16 terms, which hold all their bits.
 //
-// 8192 tokens, 32 / 8 heads of 128: 274 us, 1002 TFLOP/s (a large bf16 matrix product reaches 1188); 256, 3
-// sequences of 300 to 2048 new tokens of up to 16384 478 us, 875; fp32, 4096 tokens 220 us, 312, a third of the
-// products' terms.
+// 8192 tokens, 32 / 8 heads of 128: 274 to 291 us by card, 945 to 1002 TFLOP/s (a large bf16 matrix product reaches
+// 1188); 256, 3 sequences of 300 to 2048 new tokens of up to 16384 478 to 494 us, 847 to 875; fp32, 4096 tokens 220 to
+// 228 us, 302 to 312, a third of the products' terms.
 //
 // A tile is whole query tokens, as many as 32 rows hold (heads 32 s .. of one token where the
 // group has more), so that its rows' places are the same in every tile.
@@ -617,7 +617,8 @@ hipError_t launch_many(const KvWeightsArgs& w, int64_t blocks, hipStream_t s) {
 // Blocks of 16 columns of the kernel for few, as far as registers hold them.  Many / few, us, 32 / 8 heads of
 // 128: 32 columns, 8 x 4096 11.4 / 10.4, 32 x up to 8192 57 / 39, 1 x 300 7.3 / 5.9; 64 columns, 8 x 4096 14.6 / 16.4,
 // 32 x up to 8192 70 / 56; 36 (48 / 8 heads, 24 x up to 6001) 39 / 28; fp32, 32 columns 16.9 / 16.1, head dimension
-// 64, 64 columns 13.3 / 11.8; 256, 32 columns 8 x 8192 10.4 / 10.9.
+// 64, 64 columns 13.3 / 11.8; 256, 32 columns 8 x 8192 10.4 / 10.9.  The rule looks at the columns alone, and loses
+// 0.5 to 2 us where they are many for the head dimension and the tokens not many (8 x 4096 with 64, the last one).
 constexpr int few_blocks(int D, bool F32) { return D == 64 || (D == 128 && !F32) ? 4 : (D == 256 && F32 ? 1 : 2); }
 
 template <int D, bool F32>
